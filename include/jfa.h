@@ -404,6 +404,121 @@ jfa_status jfa_plan_kernel_times(jfa_plan plan, double* total_ms, int64_t* launc
 /* Static description of a status code. */
 const char* jfa_status_string(int32_t status);
 
+/*
+ * Paged key/value cache: serving a jagged model token by token.
+ *
+ * A cache holds keys and values of many sequences in pages of `page_size` positions.
+ * Sequence b's position p lies in page page_table[b * max_pages + p / page_size], slot
+ * p % page_size.  Element (page, slot, head, d) of the keys is at
+ *   K[page * k_strides[0] + slot * k_strides[1] + head * k_strides[2] + d]
+ * (strides in elements), and likewise of the values, so token-major pages
+ * [n_pages, page_size, Hkv, D], head-major pages [n_pages, Hkv, page_size, D] and keys
+ * and values interleaved in one array are all served without a copy.
+ *
+ * A step of a served batch is two calls on the same arrays:
+ *   jfa_cache_append  writes the new tokens' keys and values to their slots, with the
+ *                     position rotation applied to keys and queries on the way;
+ *   jfa_cache_fwd     attends from the new tokens to the cached positions.
+ * Both take, as int32 DEVICE arrays read when the kernels run (so a captured graph can be
+ * replayed on new contents):
+ *   q_offsets [B+1]  the new tokens of sequence b are rows q_offsets[b] .. q_offsets[b+1]
+ *                    of Q, K and V (non-decreasing; rows from q_offsets[B] to T belong to
+ *                    no sequence and are left alone);
+ *   kv_lens [B]      positions of sequence b in the cache, its new tokens included: they are
+ *                    its last q_len_b positions;
+ *   page_table [B, max_pages]  only the first ceil(kv_len / page_size) entries of a row are
+ *                    read, with a window only those that hold a position some new token sees.
+ * The kernels check them: a sequence whose offsets leave [0, T], whose length leaves
+ * [0, max_pages * page_size], or a page outside [0, n_pages) sets the status that
+ * jfa_cache_device_status reports as JFA_ERR_DEVICE_BOUNDS.  Nothing outside the arrays is
+ * read or written then; a bad sequence's rows stay as they were, and rows that needed a bad
+ * page are wrong.
+ */
+typedef struct jfa_cache_t* jfa_cache;
+
+/* Rotation layouts: which elements of a head's first rot_dim form a pair (x_a, x_b).
+ * HALF: (x_k, x_{k + rot_dim/2});  PAIRS: (x_{2k}, x_{2k+1}). */
+typedef enum { JFA_ROT_HALF = 0, JFA_ROT_PAIRS = 1 } jfa_rot_kind;
+
+/*
+ * A handle on a cache whose K and V arrays the caller owns (they must outlive it).
+ *   dtype JFA_BF16 (D 64 or 128) or JFA_F32 (D 32 or 64); Hkv >= 1 key/value heads;
+ *   page_size a power of two from 8 to 1024; n_pages >= 1.
+ *   K, V: DEVICE pointers of the current device, 16-byte aligned; k_strides, v_strides:
+ *   host int64[3] (page, slot, head), each at least D and a multiple of 16 bytes.
+ *   The handle allocates a status word on the current device (synchronises `stream`).
+ *   It keeps no state between calls: calls on one handle may run at once on different
+ *   streams, with a workspace each.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype / D / page_size), NO_DEVICE, CUDA.
+ */
+jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_size, int64_t n_pages,
+                            void* K, void* V, const int64_t* k_strides, const int64_t* v_strides,
+                            void* stream, jfa_cache* out);
+
+/* Frees the handle (not K and V).  cudaFree synchronises the device.  NULL is accepted. */
+jfa_status jfa_cache_destroy(jfa_cache cache);
+
+/* As jfa_plan_device_status: synchronises `stream`, reads and clears the status word. */
+jfa_status jfa_cache_device_status(jfa_cache cache, void* stream);
+
+/*
+ * Appends the new tokens' keys and values, rotating keys (and queries) by their position.
+ *   K, V [T, Hkv, D] and, with a rotation, Q, Q_out [T, H, D] in the cache's dtype: heads
+ *   dense, tokens *_stride elements apart (at least the row, a multiple of 16 bytes), so that
+ *   slices of one fused projection are taken as they are.  Q_out may be Q itself.
+ *   rot: NULL (keys stored as given, Q and Q_out must be NULL), or an fp32 table
+ *   [rot_len, rot_dim], 16-byte aligned, whose row p holds the rot_dim / 2 cosines and then
+ *   the sines of position p.  Of each pair of the first rot_dim elements of a head
+ *     y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin,
+ *   in fp32, rounded once; the other elements are copied.  rot_dim is a multiple of 16, at
+ *   most D.  A position at or past rot_len sets JFA_ERR_DEVICE_BOUNDS and its token is
+ *   skipped.
+ *   Q may be NULL with a rotation (keys alone); H is then ignored.
+ *   Two tokens must not share a slot (pages shared by sequences are for reading).
+ * Errors: INVALID_ARG, PLAN_MISMATCH (another device is current), CUDA.
+ */
+jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets,
+                            const int32_t* kv_lens, const int32_t* page_table, int32_t max_pages,
+                            const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                            const void* Q, int64_t q_stride, int32_t H, void* Q_out, int64_t qo_stride,
+                            const float* rot, int32_t rot_dim, int64_t rot_len, int32_t rot_kind,
+                            void* stream);
+
+/* Bytes of device workspace jfa_cache_fwd needs, for any batch with H query heads (0: bad
+ * arguments). */
+size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
+
+/*
+ * Attention of the new tokens over the cache: with i' = i + kv_len - q_len for row i of
+ * sequence b and key head h / (H / Hkv) of query head h (H a multiple of Hkv),
+ *   s_ij = scale * <q_i, k_j> + bias[h, bucket(|i' - j|)],  o_i = sum_j softmax_j(s_ij) v_j
+ * over the keys j < kv_len allowed as in jfa_plan_create_ex: causal (0/1) j <= i', window
+ * W >= 0 (with causal) j >= i' - W, -1: none.  A row with no allowed key gets o = 0 and
+ * lse = -inf.
+ *   Q [T, H, D] in the cache's dtype, tokens q_stride elements apart (a multiple of 16
+ *   bytes); O [T, H, D] dense, in o_dtype (JFA_F32, or JFA_BF16 with a bf16 cache);
+ *   lse fp32 [T, H], or NULL.  bias_kind JFA_BIAS_NONE or JFA_BIAS_RELPOS32 (fp32 [H, 32]).
+ *   scale must be finite and positive.
+ *   max_q_len: an upper bound of the batch's q_len, or 0 if unknown (T is taken).  It only
+ *   chooses among kernels: results do not depend on it beyond rounding, and a longer
+ *   sequence is still computed in full.
+ *   Keys that no new token of a sequence may see -- slots at or past kv_len, positions
+ *   before every row's window -- may hold anything, NaN included, and pages that hold only
+ *   such positions may be unset in the table; the other values must be finite.
+ *   workspace: at least jfa_cache_workspace_size bytes, 256-byte aligned.  Its first
+ *   JFA_CACHE_ZERO_BYTES must be zero before its first use and are zero again after every
+ *   call (zero them again after JFA_ERR_TIMEOUT); the rest needs no initialisation.  Calls
+ *   that may overlap on the GPU need a workspace each: order those that share one.
+ *   The result is the same bit for bit on every run of the same call.
+ * Errors: INVALID_ARG, UNSUPPORTED, PLAN_MISMATCH (another device is current), CUDA.
+ */
+#define JFA_CACHE_ZERO_BYTES ((size_t)8192)
+jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
+                         const int32_t* kv_lens, const int32_t* page_table, int32_t max_pages,
+                         const void* Q, int64_t q_stride, int32_t H, int32_t causal, int32_t window,
+                         int32_t bias_kind, const float* bias_table, float scale, void* O, int32_t o_dtype,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

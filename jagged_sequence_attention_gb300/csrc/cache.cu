@@ -1,0 +1,236 @@
+// C-ABI of the paged key/value cache: argument checks, the handle, and kernel launches.
+// Semantics of every entry point are documented in include/jfa.h.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include "cache_common.cuh"
+
+using namespace jfa;
+
+struct jfa_cache_t {
+    int32_t dtype, Hkv, D, page_log2, n_pages;
+    void* K;
+    void* V;
+    int64_t ks[3], vs[3];
+    int device, num_sms;
+    int* d_status;
+};
+
+namespace {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline size_t elem(int dtype) { return dtype == JFA_F32 ? 4 : 2; }
+
+// Whether the cache's device is the current one.
+bool on_device(jfa_cache c) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
+}
+
+// Checks of the arrays both calls take; max_kv: the longest sequence they can address.
+jfa_status check_batch(jfa_cache c, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
+                       const int32_t* page_table, int32_t max_pages, int32_t* max_kv) {
+    if (!c || B < 0 || B > (1 << 16) || T < 0 || T > (1 << 30) || max_pages < 0) return JFA_ERR_INVALID_ARG;
+    if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4)) return JFA_ERR_INVALID_ARG;
+    if (B > 0 && (!q_offsets || !kv_lens || (max_pages > 0 && !page_table))) return JFA_ERR_INVALID_ARG;
+    *max_kv = int32_t(std::min<int64_t>(int64_t(max_pages) << c->page_log2, INT32_MAX - T - 1024));
+    return JFA_OK;
+}
+
+// [T, heads, D] rows `stride` elements apart.
+bool row_ok(jfa_cache c, const void* p, int64_t stride, int32_t heads) {
+    return p && aligned(p, 16) && stride >= int64_t(heads) * c->D && (size_t(stride) * elem(c->dtype)) % 16 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_size, int64_t n_pages, void* K, void* V,
+                            const int64_t* k_strides, const int64_t* v_strides, void* stream, jfa_cache* out) {
+    if (!out) return JFA_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (dtype != JFA_BF16 && dtype != JFA_F32) return JFA_ERR_INVALID_ARG;
+    if (Hkv < 1 || Hkv > 65535 || n_pages < 1 || n_pages > INT32_MAX || !K || !V || !k_strides || !v_strides ||
+        !aligned(K, 16) || !aligned(V, 16))
+        return JFA_ERR_INVALID_ARG;
+    if (!supported(dtype, D) || page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)))
+        return JFA_ERR_UNSUPPORTED;
+    for (int i = 0; i < 3; ++i)
+        for (const int64_t s : {k_strides[i], v_strides[i]})
+            if (s < D || s > (int64_t(1) << 38) || (size_t(s) * elem(dtype)) % 16 != 0) return JFA_ERR_INVALID_ARG;
+    int dev = 0;
+    cudaDeviceProp prop;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaGetDeviceProperties(&prop, dev) != cudaSuccess || prop.major != 10)
+        return JFA_ERR_NO_DEVICE;
+    jfa_cache_t* c = new (std::nothrow) jfa_cache_t();
+    if (!c) return JFA_ERR_CUDA;
+    c->dtype = dtype;
+    c->Hkv = Hkv;
+    c->D = D;
+    c->page_log2 = 0;
+    while ((1 << c->page_log2) < page_size) ++c->page_log2;
+    c->n_pages = int32_t(n_pages);
+    c->K = K;
+    c->V = V;
+    for (int i = 0; i < 3; ++i) {
+        c->ks[i] = k_strides[i];
+        c->vs[i] = v_strides[i];
+    }
+    c->device = dev;
+    c->num_sms = prop.multiProcessorCount;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cudaMalloc(reinterpret_cast<void**>(&c->d_status), 256) != cudaSuccess) {
+        delete c;
+        return JFA_ERR_CUDA;
+    }
+    if (cudaMemsetAsync(c->d_status, 0, 256, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) {
+        cudaFree(c->d_status);
+        delete c;
+        return JFA_ERR_CUDA;
+    }
+    *out = c;
+    return JFA_OK;
+}
+
+jfa_status jfa_cache_destroy(jfa_cache cache) {
+    if (!cache) return JFA_OK;
+    const cudaError_t e = cudaFree(cache->d_status);
+    delete cache;
+    return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+}
+
+jfa_status jfa_cache_device_status(jfa_cache cache, void* stream) {
+    if (!cache) return JFA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int h = 0;
+    if (cudaMemcpyAsync(&h, cache->d_status, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaMemsetAsync(cache->d_status, 0, 4, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+        return JFA_ERR_CUDA;
+    if (h & kStatusTimeout) return JFA_ERR_TIMEOUT;
+    if (h & kStatusBounds) return JFA_ERR_DEVICE_BOUNDS;
+    return JFA_OK;
+}
+
+jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
+                            const int32_t* page_table, int32_t max_pages, const void* K, int64_t k_stride, const void* V,
+                            int64_t v_stride, const void* Q, int64_t q_stride, int32_t H, void* Q_out, int64_t qo_stride,
+                            const float* rot, int32_t rot_dim, int64_t rot_len, int32_t rot_kind, void* stream) {
+    int32_t max_kv = 0;
+    const jfa_status s = check_batch(cache, B, T, q_offsets, kv_lens, page_table, max_pages, &max_kv);
+    if (s != JFA_OK) return s;
+    if ((Q == nullptr) != (Q_out == nullptr) || (Q && (H < 1 || H > 65535)) || (Q && !rot)) return JFA_ERR_INVALID_ARG;
+    if (rot && (rot_dim < 16 || rot_dim > cache->D || rot_dim % 16 != 0 || rot_len < 1 || !aligned(rot, 16) ||
+                (rot_kind != JFA_ROT_HALF && rot_kind != JFA_ROT_PAIRS)))
+        return JFA_ERR_INVALID_ARG;
+    if (T > 0 && (!row_ok(cache, K, k_stride, cache->Hkv) || !row_ok(cache, V, v_stride, cache->Hkv)))
+        return JFA_ERR_INVALID_ARG;
+    if (T > 0 && Q && (!row_ok(cache, Q, q_stride, H) || !row_ok(cache, Q_out, qo_stride, H)))
+        return JFA_ERR_INVALID_ARG;
+    if (T > 0 && Q == Q_out && q_stride != qo_stride) return JFA_ERR_INVALID_ARG;
+    if (!on_device(cache)) return JFA_ERR_PLAN_MISMATCH;
+    if (B == 0 || T == 0) return JFA_OK;
+    CacheAppendParams p;
+    p.q_off = q_offsets;
+    p.kv_lens = kv_lens;
+    p.table = page_table;
+    p.B = B;
+    p.max_pages = max_pages;
+    p.T = int(T);
+    p.max_kv = max_kv;
+    p.H = Q ? H : 0;
+    p.Hkv = cache->Hkv;
+    p.D = cache->D;
+    p.page_log2 = cache->page_log2;
+    p.n_pages = cache->n_pages;
+    p.K = K;
+    p.V = V;
+    p.Q = Q;
+    p.Q_out = Q_out;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_stride = q_stride;
+    p.qo_stride = qo_stride;
+    p.Kc = cache->K;
+    p.Vc = cache->V;
+    for (int i = 0; i < 3; ++i) {
+        p.ks[i] = cache->ks[i];
+        p.vs[i] = cache->vs[i];
+    }
+    p.rot = rot;
+    p.rot_dim = rot_dim;
+    p.rot_len = int(std::min<int64_t>(rot_len, INT32_MAX));
+    p.pairs = rot_kind == JFA_ROT_PAIRS;
+    p.status = cache->d_status;
+    return launch_cache_append(cache->dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+}
+
+size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
+    if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
+    return JFA_CACHE_ZERO_BYTES + cache_simt_part_bytes(cache->D, cache->num_sms);
+}
+
+jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
+                         const int32_t* kv_lens, const int32_t* page_table, int32_t max_pages, const void* Q,
+                         int64_t q_stride, int32_t H, int32_t causal, int32_t window, int32_t bias_kind,
+                         const float* bias_table, float scale, void* O, int32_t o_dtype, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    int32_t max_kv = 0;
+    const jfa_status s = check_batch(cache, B, T, q_offsets, kv_lens, page_table, max_pages, &max_kv);
+    if (s != JFA_OK) return s;
+    if (H < 1 || H > 65535 || H % cache->Hkv != 0 || T * H > INT32_MAX || max_q_len < 0) return JFA_ERR_INVALID_ARG;
+    if ((causal != 0 && causal != 1) || window < -1 || (window >= 0 && causal != 1)) return JFA_ERR_INVALID_ARG;
+    if (bias_kind != JFA_BIAS_NONE && bias_kind != JFA_BIAS_RELPOS32)
+        return bias_kind == JFA_BIAS_DENSE ? JFA_ERR_UNSUPPORTED : JFA_ERR_INVALID_ARG;
+    if (bias_kind == JFA_BIAS_RELPOS32 && (!bias_table || !aligned(bias_table, 4))) return JFA_ERR_INVALID_ARG;
+    if (!(scale > 0.f && scale < INFINITY)) return JFA_ERR_INVALID_ARG;
+    if (o_dtype != JFA_BF16 && o_dtype != JFA_F32) return JFA_ERR_INVALID_ARG;
+    if (cache->dtype == JFA_F32 && o_dtype != JFA_F32) return JFA_ERR_UNSUPPORTED;
+    if (T > 0 && (!row_ok(cache, Q, q_stride, H) || !O || !aligned(O, 16) || !aligned(lse, 4))) return JFA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < jfa_cache_workspace_size(cache, H))
+        return JFA_ERR_INVALID_ARG;
+    if (!on_device(cache)) return JFA_ERR_PLAN_MISMATCH;
+    if (B == 0 || T == 0) return JFA_OK;
+    CacheFwdParams p;
+    p.q_off = q_offsets;
+    p.kv_lens = kv_lens;
+    p.table = page_table;
+    p.B = B;
+    p.max_pages = max_pages;
+    p.T = int(T);
+    p.max_kv = max_kv;
+    p.H = H;
+    p.Hkv = cache->Hkv;
+    p.g = H / cache->Hkv;
+    p.page_log2 = cache->page_log2;
+    p.n_pages = cache->n_pages;
+    p.causal = causal;
+    p.window = window < max_kv ? window : -1;  // a window of every position is none
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.bias = bias_kind == JFA_BIAS_RELPOS32 ? bias_table : nullptr;
+    p.Q = Q;
+    p.q_stride = q_stride;
+    p.O = O;
+    p.o_f32 = o_dtype == JFA_F32;
+    p.lse = lse;
+    p.K = cache->K;
+    p.V = cache->V;
+    for (int i = 0; i < 3; ++i) {
+        p.ks[i] = cache->ks[i];
+        p.vs[i] = cache->vs[i];
+    }
+    p.counters = static_cast<uint32_t*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES);
+    p.status = cache->d_status;
+    p.min_units = 1;
+    p.row_lo = 0;
+    p.row_hi = INT32_MAX;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launch_cache_simt(cache->dtype, cache->D, p, cache->num_sms, st) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+}
+
+}  // extern "C"

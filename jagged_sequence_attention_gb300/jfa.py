@@ -24,15 +24,20 @@ JFA_STATIC_SCRATCH_BYTES = 64 << 20
 JFA_SOFTMAX, JFA_GDPA_GELU_TANH, JFA_GDPA_SILU = 0, 1, 2
 JFA_BF16, JFA_F32 = 0, 1
 JFA_BIAS_NONE, JFA_BIAS_RELPOS32, JFA_BIAS_DENSE = 0, 1, 2
+JFA_ROT_HALF, JFA_ROT_PAIRS = 0, 1
+JFA_CACHE_ZERO_BYTES = 8192
 
 MODES = {"softmax": JFA_SOFTMAX, "gelu_tanh": JFA_GDPA_GELU_TANH, "silu": JFA_GDPA_SILU}
 DTYPES = {torch.bfloat16: JFA_BF16, torch.float32: JFA_F32}
+ROT_KINDS = {"half": JFA_ROT_HALF, "pairs": JFA_ROT_PAIRS}
 
 EXPORTED = ["jfa_plan_create", "jfa_plan_create_ex", "jfa_plan_destroy", "jfa_plan_info", "jfa_fwd", "jfa_bwd_workspace_size",
             "jfa_bwd", "jfa_plan_device_status", "jfa_worklist_size", "jfa_worklist_build",
             "jfa_status_string", "jfa_plan_set_timing", "jfa_plan_kernel_times", "jfa_bwd_static_scratch",
             "jfa_partition_sequences", "jfa_bwd_ex_workspace_size", "jfa_bwd_ex", "jfa_plan_create_shared_kv",
-            "jfa_partition_users", "jfa_plan_set_deterministic", "jfa_plan_set_work_item"]
+            "jfa_partition_users", "jfa_plan_set_deterministic", "jfa_plan_set_work_item",
+            "jfa_cache_create", "jfa_cache_destroy", "jfa_cache_device_status", "jfa_cache_append",
+            "jfa_cache_workspace_size", "jfa_cache_fwd"]
 
 
 class JFAError(RuntimeError):
@@ -82,13 +87,23 @@ def load_library(path):
     L.jfa_plan_set_deterministic.argtypes = [vp, i32]
     L.jfa_plan_set_work_item.argtypes = [vp, i32, i64, vp]
     L.jfa_plan_kernel_times.argtypes = [vp, vp, vp]
+    L.jfa_cache_create.argtypes = [i32, i32, i32, i32, i64, vp, vp, P(i64), P(i64), vp, P(vp)]
+    L.jfa_cache_destroy.argtypes = [vp]
+    L.jfa_cache_device_status.argtypes = [vp, vp]
+    L.jfa_cache_append.argtypes = [vp, i32, i64, vp, vp, vp, i32, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i32,
+                                   i64, i32, vp]
+    L.jfa_cache_workspace_size.argtypes = [vp, i32]
+    L.jfa_cache_workspace_size.restype = sz
+    L.jfa_cache_fwd.argtypes = [vp, i32, i64, i32, vp, vp, vp, i32, vp, i64, i32, i32, i32, i32, vp, f32, vp, i32, vp,
+                                vp, sz, vp]
     L.jfa_status_string.argtypes = [i32]
     L.jfa_status_string.restype = ctypes.c_char_p
     for name in ("jfa_plan_create", "jfa_plan_create_ex", "jfa_plan_destroy", "jfa_plan_info", "jfa_fwd", "jfa_bwd",
                  "jfa_plan_device_status", "jfa_worklist_size", "jfa_worklist_build", "jfa_plan_set_timing",
                  "jfa_plan_kernel_times", "jfa_bwd_static_scratch", "jfa_partition_sequences", "jfa_bwd_ex",
                  "jfa_plan_create_shared_kv", "jfa_partition_users", "jfa_plan_set_deterministic",
-                 "jfa_plan_set_work_item"):
+                 "jfa_plan_set_work_item", "jfa_cache_create", "jfa_cache_destroy", "jfa_cache_device_status",
+                 "jfa_cache_append", "jfa_cache_fwd"):
         getattr(L, name).restype = i32
     return L
 
@@ -412,6 +427,168 @@ def jfa_worklist_build(q_offsets, kv_offsets, H: int, causal: bool, pass_: int, 
         int(bool(causal)), _win(window), int(pass_), int(n_ctas), items.ctypes.data_as(ctypes.c_void_p),
         offs.ctypes.data_as(ctypes.c_void_p), cost.ctypes.data_as(ctypes.c_void_p)))
     return items[:n], offs, cost
+
+
+# --------------------------------------------------------------------------- paged cache
+
+
+class Cache:
+    """Owns a jfa_cache handle and keeps the cache's arrays alive."""
+
+    def __init__(self, handle, K, V):
+        self.handle, self.K, self.V = handle, K, V
+        self.n_pages, self.page_size, self.Hkv, self.D = K.shape
+        self.dtype, self.device = K.dtype, K.device
+
+    def __del__(self):
+        try:
+            if self.handle is not None and _lib is not None:
+                _lib.jfa_cache_destroy(self.handle)
+        finally:
+            self.handle = None
+
+
+def _bad(fn: str, what: str):
+    raise JFAError(f"{fn} ({what})", JFA_ERR_INVALID_ARG)
+
+
+def jfa_cache_create(K: torch.Tensor, V: torch.Tensor, stream=None) -> Cache:
+    """A handle on caches K, V [n_pages, page_size, Hkv, D] (bf16 or fp32, on the current CUDA
+    device; any strides that are multiples of 16 bytes with a dense last dimension, so
+    head-major pages are given as a permuted view)."""
+    fn = "jfa_cache_create"
+    if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or K.device != V.device or not K.is_cuda:
+        _bad(fn, "K and V must be CUDA tensors of one shape [n_pages, page_size, Hkv, D] and type")
+    if K.stride(3) != 1 or V.stride(3) != 1:
+        _bad(fn, "the head dimension must be dense")
+    n, ps, Hkv, D = K.shape
+    ks, vs = (ctypes.c_int64 * 3)(*K.stride()[:3]), (ctypes.c_int64 * 3)(*V.stride()[:3])
+    h = ctypes.c_void_p()
+    _check(fn, lib().jfa_cache_create(_dtype_code(K), Hkv, D, ps, n, K.data_ptr(), V.data_ptr(), ks, vs,
+                                      _stream(stream), ctypes.byref(h)))
+    return Cache(h, K, V)
+
+
+def jfa_cache_destroy(cache: Cache):
+    if cache.handle is not None:
+        _check("jfa_cache_destroy", lib().jfa_cache_destroy(cache.handle))
+        cache.handle = None
+
+
+def jfa_cache_device_status(cache: Cache, stream=None) -> int:
+    return int(lib().jfa_cache_device_status(cache.handle, _stream(stream)))
+
+
+def _cache_batch(fn: str, cache: Cache, q_offsets, kv_lens, page_table):
+    """(B, max_pages) of a batch's device arrays."""
+    for t in (q_offsets, kv_lens, page_table):
+        if t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous():
+            _bad(fn, "q_offsets, kv_lens and page_table must be contiguous int32 tensors on the cache's device")
+    B = kv_lens.numel()
+    if q_offsets.numel() != B + 1 or page_table.dim() != 2 or page_table.shape[0] != B:
+        _bad(fn, "q_offsets [B + 1], kv_lens [B] and page_table [B, max_pages] disagree")
+    return B, page_table.shape[1]
+
+
+def _cache_rows(fn: str, cache: Cache, t: torch.Tensor, heads, T=None):
+    """The token stride of [T, heads, D] rows whose heads are dense."""
+    D = cache.D
+    if t.dtype != cache.dtype or t.device != cache.device or t.dim() != 3 or t.shape[2] != D or \
+            (heads is not None and t.shape[1] != heads) or (T is not None and t.shape[0] != T):
+        _bad(fn, "rows must be [T, heads, D] in the cache's type, on its device")
+    s = t.stride()
+    if t.numel() and (s[2] != 1 or (t.shape[1] > 1 and s[1] != D)):
+        _bad(fn, "the heads of a row must be dense")
+    # one token (or none): torch leaves its stride free
+    return s[0] if t.shape[0] > 1 else t.shape[1] * D
+
+
+def jfa_cache_append(cache: Cache, K, V, q_offsets, kv_lens, page_table, Q=None, Q_out=None, rot=None,
+                     rot_kind="half", stream=None):
+    """Appends the new tokens' K, V [T, Hkv, D] to their slots.  rot: the rotation's table
+    [rot_len, rot_dim] (cosines, then sines, fp32), applied to the keys and to Q [T, H, D]
+    (into Q_out, which may be Q; allocated if None).  Returns Q_out (None without Q)."""
+    fn = "jfa_cache_append"
+    B, max_pages = _cache_batch(fn, cache, q_offsets, kv_lens, page_table)
+    T = K.shape[0]
+    ks = _cache_rows(fn, cache, K, cache.Hkv)
+    vs = _cache_rows(fn, cache, V, cache.Hkv, T)
+    H, qs, qos, qp, qop = 1, 0, 0, None, None
+    if Q is not None:
+        H = Q.shape[1] if Q.dim() == 3 else 0
+        if Q_out is None:
+            Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        qs, qos = _cache_rows(fn, cache, Q, None, T), _cache_rows(fn, cache, Q_out, H, T)
+        qp, qop = Q.data_ptr(), Q_out.data_ptr()
+    elif Q_out is not None:
+        _bad(fn, "Q_out without Q")
+    rp, rot_dim, rot_len = None, 0, 0
+    if rot is not None:
+        if rot.dtype != torch.float32 or rot.device != cache.device or rot.dim() != 2 or not rot.is_contiguous():
+            _bad(fn, "rot must be a contiguous fp32 tensor [rot_len, rot_dim] on the cache's device")
+        rot_len, rot_dim = rot.shape
+        rp = rot.data_ptr()
+    kind = ROT_KINDS.get(rot_kind, -1) if isinstance(rot_kind, str) else int(rot_kind)
+    _check(fn, lib().jfa_cache_append(cache.handle, B, T, q_offsets.data_ptr(), kv_lens.data_ptr(),
+                                      page_table.data_ptr(), max_pages, K.data_ptr(), ks, V.data_ptr(), vs, qp, qs, H,
+                                      qop, qos, rp, rot_dim, rot_len, kind, _stream(stream)))
+    return Q_out
+
+
+def jfa_cache_workspace_size(cache: Cache, H: int) -> int:
+    return int(lib().jfa_cache_workspace_size(cache.handle, int(H)))
+
+
+def jfa_cache_workspace(cache: Cache, H: int) -> torch.Tensor:
+    """A workspace for jfa_cache_fwd, with the part that must start zero cleared on the
+    current stream.  Calls that may overlap need one each."""
+    n = jfa_cache_workspace_size(cache, H)
+    if n == 0:
+        _bad("jfa_cache_workspace", "H must be a multiple of the cache's heads")
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    ws[:JFA_CACHE_ZERO_BYTES].zero_()
+    return ws
+
+
+def jfa_cache_fwd(cache: Cache, Q, q_offsets, kv_lens, page_table, bias=None, scale=None, causal=True, window=None,
+                  max_q_len=None, O=None, lse=None, out_dtype=None, workspace=None, stream=None):
+    """Attention of the new tokens Q [T, H, D] over the cache.  Returns (O, lse).  bias: the
+    bucket table [H, 32]; max_q_len: an upper bound of the batch's query lengths (it chooses
+    the kernel); workspace: jfa_cache_workspace's, kept by the caller (one is made if None)."""
+    fn = "jfa_cache_fwd"
+    B, max_pages = _cache_batch(fn, cache, q_offsets, kv_lens, page_table)
+    qs = _cache_rows(fn, cache, Q, None)
+    T, H, D = Q.shape
+    scale = 1.0 / float(D) ** 0.5 if scale is None else float(scale)
+    if O is None:
+        O = torch.empty((T, H, D), dtype=out_dtype or Q.dtype, device=Q.device)
+    elif O.shape != Q.shape or not O.is_contiguous() or O.device != cache.device:
+        _bad(fn, "O must be a contiguous tensor of Q's shape")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=Q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.device != cache.device:
+        _bad(fn, "lse must be a contiguous fp32 tensor [T, H]")
+    bp = None
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.shape != (H, 32) or not bias.is_contiguous() or \
+                bias.device != cache.device:
+            _bad(fn, "bias must be a contiguous fp32 tensor [H, 32]")
+        bp = bias.data_ptr()
+    if workspace is None:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                workspace = jfa_cache_workspace(cache, H)
+        else:
+            workspace = jfa_cache_workspace(cache, H)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        _bad(fn, "workspace must be a contiguous tensor on the cache's device")
+    _check(fn, lib().jfa_cache_fwd(cache.handle, B, T, 0 if max_q_len is None else int(max_q_len),
+                                   q_offsets.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), max_pages,
+                                   Q.data_ptr(), qs, H, int(bool(causal)), _win(window),
+                                   JFA_BIAS_NONE if bp is None else JFA_BIAS_RELPOS32, bp, scale, O.data_ptr(),
+                                   _dtype_code(O), lse.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    return O, lse
 
 
 # --------------------------------------------------------------------------- convenience
