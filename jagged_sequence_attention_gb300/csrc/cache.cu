@@ -1,6 +1,7 @@
 // C-ABI of the paged key/value cache: argument checks, the handle, and kernel launches.
 // Semantics of every entry point are documented in include/jfa.h.
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
@@ -18,12 +19,33 @@ struct jfa_cache_t {
     int64_t ks[3], vs[3];
     int device, num_sms;
     int* d_status;
+    CUtensorMap mk, mv;  // bf16: the pages as (D, slot, head, page), boxes of one page's keys (at most 64)
 };
 
 namespace {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t elem(int dtype) { return dtype == JFA_F32 ? 4 : 2; }
+
+// The pages [n_pages][Hkv][page_size][D] by their strides, boxes of 128 bytes x `rows` slots.
+jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* c, const int64_t* s, int rows) {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f
+                                                                                                             : nullptr);
+    }();
+    if (!enc) return JFA_ERR_CUDA;
+    const cuuint64_t dims[4] = {cuuint64_t(c->D), cuuint64_t(1) << c->page_log2, cuuint64_t(c->Hkv), cuuint64_t(c->n_pages)};
+    const cuuint64_t strides[3] = {cuuint64_t(s[1]) * 2, cuuint64_t(s[2]) * 2, cuuint64_t(s[0]) * 2};
+    const cuuint32_t box[4] = {64u, cuuint32_t(rows), 1u, 1u}, one[4] = {1u, 1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? JFA_OK
+               : JFA_ERR_CUDA;
+}
 
 // Whether the cache's device is the current one.
 bool on_device(jfa_cache c) {
@@ -83,6 +105,13 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
     }
     c->device = dev;
     c->num_sms = prop.multiProcessorCount;
+    if (dtype == JFA_BF16) {
+        const int rows = std::min(64, page_size);
+        if (make_page_map(&c->mk, K, c, c->ks, rows) != JFA_OK || make_page_map(&c->mv, V, c, c->vs, rows) != JFA_OK) {
+            delete c;
+            return JFA_ERR_CUDA;
+        }
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cudaMalloc(reinterpret_cast<void**>(&c->d_status), 256) != cudaSuccess) {
         delete c;
@@ -171,7 +200,8 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
 
 size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
     if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
-    return JFA_CACHE_ZERO_BYTES + cache_simt_part_bytes(cache->D, cache->num_sms);
+    return JFA_CACHE_ZERO_BYTES + std::max(cache_simt_part_bytes(cache->D, cache->num_sms),
+                                           cache_decode_part_bytes(cache->D, cache->num_sms));
 }
 
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
@@ -230,7 +260,10 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.row_lo = 0;
     p.row_hi = INT32_MAX;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return launch_cache_simt(cache->dtype, cache->D, p, cache->num_sms, st) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+    const cudaError_t e = cache->dtype == JFA_BF16
+                              ? launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st)
+                              : launch_cache_simt(cache->dtype, cache->D, p, cache->num_sms, st);
+    return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -258,6 +258,10 @@ __device__ __forceinline__ int cache_slot(int cta, int first_cta) { return 2 * c
 
 cudaError_t launch_cache_simt(int dtype, int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_simt_part_bytes(int D, int num_sms);
+// bf16, row tiles of 16 packed rows: bound by the stream of K and V.
+cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                                cudaStream_t st);
+size_t cache_decode_part_bytes(int D, int num_sms);
 
 struct CacheAppendParams {
     const int32_t* q_off;

@@ -1,0 +1,485 @@
+// Paged-cache attention for few rows: single tokens and short query sets (bf16).
+//
+// A row tile holds at most 16 packed rows (tokens x grouped heads), so every key byte meets
+// at most 16 multiply-adds: the kernel is a stream of K and V at memory speed, and everything
+// else has to hide under it.  64-key stages (K and V, one TMA box per page and 128-byte
+// column block) pass through a ring of 96 KB per CTA, two CTAs per SM; one warp issues the
+// loads, four warps take 16 keys of each stage.  The products are m16n8k16 tensor-core
+// instructions on operands read by ldmatrix: at 16 rows a 128-row accumulator tile would be
+// seven-eighths padding, and the arithmetic is a small part of the time either way.
+//   S = Q K^T (Q in registers), online softmax per warp with a lazily moved maximum, O += P V.
+// P is rounded to bf16 for the product (its sum is taken before, in fp32).  The warps work on
+// separate keys with separate (m, l, O) and merge at the end of the item, so no step of the
+// stream waits for another warp.  The work split, and the merge of an item split over CTAs,
+// are those of cache_common.cuh.
+#include "cache_common.cuh"
+#include "tilemath.cuh"
+
+namespace jfa {
+
+namespace {
+
+constexpr int kDecBM = 16, kDecBN = 64, kDecWarps = 4, kDecThreads = 32 * (kDecWarps + 1), kDecCtasPerSm = 2;
+
+template <int D>
+struct DecCfg {
+    static constexpr int kCB = D / 64;                       // 128-byte column blocks of a row
+    static constexpr int kBlock = kDecBN * 128;              // one column block of a stage's keys
+    static constexpr int kStage = 2 * kCB * kBlock;          // K blocks, then V blocks
+    static constexpr int kStages = 98304 / kStage;
+    static constexpr int kOffSlots = kStages * kStage;       // two 16 x 64 fp32 tiles of the merge
+    static constexpr int kOffML = kOffSlots + 2 * 16 * 64 * 4;   // [2 buffers][m, l][warp][row]
+    static constexpr int kOffBar = kOffML + 2 * 2 * kDecWarps * 16 * 4;
+    static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
+    static constexpr int kBytes = kOffMisc + 16 + int(sizeof(CacheStart)) + 1024;
+    static constexpr int kPart = kDecBM * (D + 2);           // floats of a partial result: O, m, l
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// c += a b, m16n8k16, bf16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecWarps) : "memory"); }
+
+template <int D, bool BIAS>
+__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
+    jfa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const CacheFwdParams p) {
+    using C = DecCfg<D>;
+    constexpr int BM = kDecBM, BN = kDecBN, NT = D / 8;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto full = [&](uint32_t s) -> uint32_t { return sbase + C::kOffBar + 8u * s; };
+    auto empty = [&](uint32_t s) -> uint32_t { return sbase + C::kOffBar + 8u * (C::kStages + s); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    CacheStart* start = reinterpret_cast<CacheStart*>(smem + C::kOffMisc + 16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < uint32_t(C::kStages); ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kDecWarps);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    cache_start<BM, BN>(p, start, reinterpret_cast<long long*>(smem));  // (the ring's memory as scratch)
+    CacheCursor<BM, BN> cur(*start);
+    CacheSeg g;
+
+    if (warp == kDecWarps) {
+        // ---------------------------------------------------------------- producer
+        // A lane loads one box of each stage: K or V, column block, page.
+        fence_proxy_async_smem();  // the scratch's writes before the first loads into it
+        const int rows = min(1 << p.page_log2, BN);          // keys of a box
+        const int per = BN / rows;                           // pages (or parts of one) in a stage
+        const bool mine = lane < 2 * C::kCB * per;
+        const int pg = lane % per, cb = (lane / per) % C::kCB, isv = lane / (per * C::kCB);
+        const uint32_t box = uint32_t(isv * C::kCB * C::kBlock + cb * C::kBlock + pg * rows * 128);
+        const CUtensorMap* map = isv ? &tmV : &tmK;
+        uint32_t it = 0;
+        bool ok = true, have = cur.next(p, g);
+        int kt = g.k0;
+        // A stage's page: -1 outside the item's keys (not loaded); past the cache (read as
+        // zeros) for a bad entry.
+        auto page_of = [&](const CacheSeg& s, int k) -> int {
+            const int j = (s.r.f + k) * BN + pg * rows;
+            if (!mine || j >= s.r.hi || j + rows <= s.r.lo) return -1;
+            const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+            if (page >= 0 && page < p.n_pages) return page;
+            atomicOr(p.status, kStatusBounds);
+            return p.n_pages;
+        };
+        while (have && (g.r.n == 0)) have = cur.next(p, g), kt = g.k0;
+        int page = have ? page_of(g, kt) : -1;
+        while (have) {
+            const int at = page, j0 = (g.r.f + kt) * BN + pg * rows, hk = g.hk;
+            if (++kt >= g.k1) {
+                do {
+                    have = cur.next(p, g);
+                    kt = g.k0;
+                } while (have && g.r.n == 0);
+            }
+            if (have) page = page_of(g, kt);
+            const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(st), ph ^ 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            const int n = __popc(__ballot_sync(0xffffffffu, at >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(full(st), uint32_t(n * rows * 128));
+            __syncwarp();
+            if (at >= 0)
+                tma_load_4d(sbase + st * C::kStage + box, map, full(st), cb * 64, j0 & ((1 << p.page_log2) - 1), hk, at);
+            ++it;
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0) atomicOr(p.status, kStatusTimeout);
+        }
+        drain_ring(full(0), it, C::kStages);
+        return;
+    }
+
+    // -------------------------------------------------------------------- consumers
+    float* slots = reinterpret_cast<float*>(smem + C::kOffSlots);
+    float* ml = reinterpret_cast<float*>(smem + C::kOffML);
+    const int quad = lane & 3, qrow = lane >> 2;
+    uint32_t it = 0, seg_no = 0;
+    bool ok = true;
+    // ldmatrix source: row of this warp's 16 keys and 16-byte piece, for K and (transposed) V
+    const int krow = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kpc = (lane >> 3) & 1;
+    const int vrow = 16 * warp + (lane & 7) + (((lane >> 3) & 1) << 3), vpc = lane >> 4;
+    while (cur.next(p, g)) {
+        const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * BM;
+        const int nr = min(BM, R - r0);
+        const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.Q);
+        // this lane's rows qrow and qrow + 8: queries, limits, heads
+        uint32_t qa[D / 16][4];
+        int lim[2], low[2], rel[2];
+        const float* brow[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int rr = qrow + 8 * i;
+            const bool in = rr < nr;
+            const int r = r0 + (in ? rr : 0), tok = r / p.g, head = g.hk * p.g + r - tok * p.g;
+            rel[i] = tok + diag;
+            lim[i] = p.causal ? min(g.s.kv_len, rel[i] + 1) : g.s.kv_len;
+            low[i] = p.window >= 0 ? rel[i] - p.window : 0;
+            brow[i] = BIAS ? p.bias + head * 32 : nullptr;
+            const __nv_bfloat16* src = Q + (g.s.q0 + tok) * p.q_stride + int64_t(head) * D + 2 * quad;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                qa[s][i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s) : 0u;
+                qa[s][2 + i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8) : 0u;
+            }
+        }
+        // keys that every row of the tile sees: no mask in [all_lo, all_hi)
+        const int t_first = r0 / p.g, t_last = (r0 + nr - 1) / p.g;
+        const int all_hi = p.causal ? min(g.s.kv_len, t_first + diag + 1) : g.s.kv_len;
+        const int all_lo = p.window >= 0 ? max(0, t_last + diag - p.window) : 0;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+        int bucket = -1;
+        float bcur[2] = {0.f, 0.f};
+        const int k_end = g.r.n > 0 ? g.k1 : g.k0;
+        for (int kt = g.k0; kt < k_end; ++kt, ++it) {
+            const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1;
+            if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(full(st), ph, abort_flag))) {
+                ok = false;
+                *abort_flag = 1;
+                if (lane == 0) atomicOr(p.status, kStatusTimeout);
+            }
+            if (!ok) continue;
+            const int c0 = (g.r.f + kt) * BN, w0 = c0 + 16 * warp;  // this warp's keys [w0, w0 + 16)
+            const uint32_t sK = sbase + st * C::kStage, sV = sK + C::kCB * C::kBlock;
+            // Values that no row may see are undefined, and 0 * NaN is not 0: clear them.
+            const bool edge = w0 < g.r.lo || w0 + 16 > g.r.hi;
+            if (edge) {
+                for (int e = lane; e < 16 * C::kCB * 8; e += 32) {
+                    const int row = e & 15, j = w0 + row;
+                    if (j < g.r.lo || j >= g.r.hi)
+                        st_shared_v4(sV + uint32_t((e >> 7) * C::kBlock + (16 * warp + row) * 128 + ((e >> 4) & 7) * 16), 0, 0, 0, 0);
+                }
+                __syncwarp();
+            }
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                ldsm4(b, sK + uint32_t((k >> 2) * C::kBlock + krow * 128 + (((((k & 3) << 1) + kpc) ^ (krow & 7)) << 4)));
+                mma16816(s[0], qa[k], b[0], b[1]);
+                mma16816(s[1], qa[k], b[2], b[3]);
+            }
+            // scores of rows qrow (i = 0) and qrow + 8 (i = 1) at keys w0 + 8 n + 2 quad + e
+            if (BIAS) {
+                const int far = t_last + diag - w0, near = t_first + diag - (w0 + 15);
+                const int bk = relpos_bucket(far);
+                if ((near >= 0 || far <= 0) && bk == relpos_bucket(near)) {
+                    if (bk != bucket) {
+                        bucket = bk;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) bcur[i] = __ldg(brow[i] + bk) * 1.4426950408889634f;
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[n][i] = fmaf(s[n][i], p.scale_log2, bcur[i >> 1]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = w0 + 8 * n + 2 * quad + (i & 1);
+                            const float bv = __ldg(brow[i >> 1] + relpos_bucket(rel[i >> 1] - j));
+                            s[n][i] = fmaf(s[n][i], p.scale_log2, bv * 1.4426950408889634f);
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
+            }
+            if (w0 < all_lo || w0 + 16 > all_hi) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = w0 + 8 * n + 2 * quad + (i & 1);
+                        if (j >= lim[i >> 1] || j < low[i >> 1]) s[n][i] = -INFINITY;
+                    }
+            }
+            float mx[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            }
+            // The maximum moves only when it would grow by more than 2^8: sums and O stay in
+            // its units, and P stays below 2^8.
+            const bool grow0 = mx[0] > m[0] + 8.f, grow1 = mx[1] > m[1] + 8.f;
+            if (__any_sync(0xffffffffu, grow0 || grow1)) {
+                const float n0 = grow0 ? mx[0] : m[0], n1 = grow1 ? mx[1] : m[1];
+                const float a0 = m[0] == -INFINITY ? 0.f : ex2_approx(m[0] - n0);
+                const float a1 = m[1] == -INFINITY ? 0.f : ex2_approx(m[1] - n1);
+                m[0] = n0;
+                m[1] = n1;
+                l[0] *= a0;
+                l[1] *= a1;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    o[n][0] *= a0;
+                    o[n][1] *= a0;
+                    o[n][2] *= a1;
+                    o[n][3] *= a1;
+                }
+            }
+            const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
+            uint32_t pa[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float e0 = ex2_approx(s[n][0] - u0), e1 = ex2_approx(s[n][1] - u0);
+                const float e2 = ex2_approx(s[n][2] - u1), e3 = ex2_approx(s[n][3] - u1);
+                l[0] += e0 + e1;
+                l[1] += e2 + e3;
+                pa[2 * n] = pack_bf16x2(e0, e1);
+                pa[2 * n + 1] = pack_bf16x2(e2, e3);
+            }
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                uint32_t b[4];
+                ldsm4_t(b, sV + uint32_t((n >> 2) * C::kBlock + vrow * 128 + (((((n & 3) << 1) + vpc) ^ (vrow & 7)) << 4)));
+                mma16816(o[2 * n], pa, b[0], b[1]);
+                mma16816(o[2 * n + 1], pa, b[2], b[3]);
+            }
+            if (edge) fence_proxy_async_smem();  // the cleared rows before the ring's next load
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(st));
+        }
+        // ------------------------------------------------------------ end of the item's part
+        // Merge the four warps: m and l of every row, then O, 64 columns at a time, warps 2
+        // and 3 into the slots, warps 0 and 1 onto them, and the two slots' sum out.
+        float* mw = ml + (seg_no & 1) * (2 * kDecWarps * 16);
+        float* lw = mw + kDecWarps * 16;
+        ++seg_no;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            if (quad == 0) {
+                mw[warp * 16 + qrow + 8 * i] = m[i];
+                lw[warp * 16 + qrow + 8 * i] = l[i];
+            }
+        }
+        consumer_sync();
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = qrow + 8 * i;
+            const float mm = fmaxf(fmaxf(mw[r], mw[16 + r]), fmaxf(mw[32 + r], mw[48 + r]));
+            f[i] = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - mm);
+        }
+        // this thread's output: row orow, columns 8 (tid & 7) + of each 64
+        const int orow = threadIdx.x >> 3, ocol = threadIdx.x & 7;
+        float om = -INFINITY, ol = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) om = fmaxf(om, mw[16 * w + orow]);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            const float mm = mw[16 * w + orow];
+            ol = fmaf(mm == -INFINITY ? 0.f : ex2_approx(mm - om), lw[16 * w + orow], ol);
+        }
+        const bool whole = g.whole();
+        int first = 0, last = 0;
+        if (!whole) {
+            first = cache_cta_of(*start, g.first);
+            last = cache_cta_of(*start, g.first + g.units - 1);
+        }
+        float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
+        const int r = r0 + orow, tok = r / p.g;
+        const size_t grow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
+        const bool out = orow < nr && ok;
+        const float inv = ol > 0.f ? 1.f / ol : 0.f;
+        auto put = [&](int col, const float (&v)[8], float mul) {
+            if (p.o_f32) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + grow * D + col);
+                dst[0] = make_float4(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul);
+                dst[1] = make_float4(v[4] * mul, v[5] * mul, v[6] * mul, v[7] * mul);
+            } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + grow * D + col) =
+                    make_uint4(pack_bf16x2(v[0] * mul, v[1] * mul), pack_bf16x2(v[2] * mul, v[3] * mul),
+                               pack_bf16x2(v[4] * mul, v[5] * mul), pack_bf16x2(v[6] * mul, v[7] * mul));
+            }
+        };
+#pragma unroll
+        for (int hc = 0; hc < D / 64; ++hc) {
+            float2* slot = reinterpret_cast<float2*>(slots) + (warp & 1) * 512 + lane;  // [8 n][2 halves][32 lanes]
+            if (warp >= 2) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float* v = o[8 * hc + n];
+                    slot[n * 64] = make_float2(v[0] * f[0], v[1] * f[0]);
+                    slot[n * 64 + 32] = make_float2(v[2] * f[1], v[3] * f[1]);
+                }
+            }
+            consumer_sync();
+            if (warp < 2) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float* v = o[8 * hc + n];
+                    const float2 x = slot[n * 64], y = slot[n * 64 + 32];
+                    slot[n * 64] = make_float2(fmaf(v[0], f[0], x.x), fmaf(v[1], f[0], x.y));
+                    slot[n * 64 + 32] = make_float2(fmaf(v[2], f[1], y.x), fmaf(v[3], f[1], y.y));
+                }
+            }
+            consumer_sync();
+            const float4* a = reinterpret_cast<const float4*>(slots) + (ocol * 2 + (orow >> 3)) * 16 + (orow & 7) * 2;
+            const float4 a0 = a[0], a1 = a[1], b0 = a[256], b1 = a[257];
+            const float v[8] = {a0.x + b0.x, a0.y + b0.y, a0.z + b0.z, a0.w + b0.w,
+                                a1.x + b1.x, a1.y + b1.y, a1.z + b1.z, a1.w + b1.w};
+            if (out) {
+                if (whole) {
+                    put(64 * hc + 8 * ocol, v, inv);
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(part + orow * D + 64 * hc + 8 * ocol);
+                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+            if (hc + 1 < D / 64) consumer_sync();
+        }
+        if (whole) {
+            if (out && ocol == 0 && p.lse)
+                p.lse[grow] = ol > 0.f ? (om + __log2f(ol)) * 0.6931471805599453f : -INFINITY;
+            continue;
+        }
+        if (out && ocol == 0) {
+            part[BM * D + orow] = om;
+            part[BM * D + BM + orow] = ol;
+        }
+        __threadfence();
+        consumer_sync();
+        if (threadIdx.x == 0) {
+            int done = 0;
+            if (ok) {
+                done = atomicAdd(p.counters + first, 1u) == uint32_t(last - first);
+                if (done) p.counters[first] = 0u;  // every part has arrived: ready for the next call
+                __threadfence();
+            }
+            *last_flag = done;
+        }
+        consumer_sync();
+        if (!*last_flag) continue;
+        // The last part to arrive adds them all up, in the order of the keys.
+        if (orow < nr) {
+            float mm = -INFINITY;
+#pragma unroll 8
+            for (int c = first; c <= last; ++c)
+                mm = fmaxf(mm, __ldcg(p.part + size_t(cache_slot(c, first)) * C::kPart + BM * D + orow));
+            const float mu = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f, acc[D / 64][8];
+#pragma unroll
+            for (int hc = 0; hc < D / 64; ++hc)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[hc][i] = 0.f;
+#pragma unroll 2
+            for (int c = first; c <= last; ++c) {
+                const float* src = p.part + size_t(cache_slot(c, first)) * C::kPart;
+                const float w = ex2_approx(__ldcg(src + BM * D + orow) - mu);
+                ll = fmaf(__ldcg(src + BM * D + BM + orow), w, ll);
+#pragma unroll
+                for (int hc = 0; hc < D / 64; ++hc) {
+                    const float4* q = reinterpret_cast<const float4*>(src + orow * D + 64 * hc + 8 * ocol);
+                    const float4 x = __ldcg(q), y = __ldcg(q + 1);
+                    acc[hc][0] = fmaf(x.x, w, acc[hc][0]);
+                    acc[hc][1] = fmaf(x.y, w, acc[hc][1]);
+                    acc[hc][2] = fmaf(x.z, w, acc[hc][2]);
+                    acc[hc][3] = fmaf(x.w, w, acc[hc][3]);
+                    acc[hc][4] = fmaf(y.x, w, acc[hc][4]);
+                    acc[hc][5] = fmaf(y.y, w, acc[hc][5]);
+                    acc[hc][6] = fmaf(y.z, w, acc[hc][6]);
+                    acc[hc][7] = fmaf(y.w, w, acc[hc][7]);
+                }
+            }
+            const float li = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+            for (int hc = 0; hc < D / 64; ++hc) put(64 * hc + 8 * ocol, acc[hc], li);
+            if (ocol == 0 && p.lse)
+                p.lse[grow] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        }
+    }
+}
+
+template <int D, bool BIAS>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(jfa_cache_decode_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         DecCfg<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    jfa_cache_decode_kernel<D, BIAS><<<num_sms * kDecCtasPerSm, kDecThreads, DecCfg<D>::kBytes, st>>>(mk, mv, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_decode_part_bytes(int D, int num_sms) {
+    return size_t(num_sms) * kDecCtasPerSm * 2 * kDecBM * size_t(D + 2) * 4;
+}
+
+cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                                cudaStream_t st) {
+    if (D == 128) return p.bias ? launch<128, true>(mk, mv, p, num_sms, st) : launch<128, false>(mk, mv, p, num_sms, st);
+    return p.bias ? launch<64, true>(mk, mv, p, num_sms, st) : launch<64, false>(mk, mv, p, num_sms, st);
+}
+
+}  // namespace jfa
