@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libjfa.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "plan.cpp", "fwd.cu", "fwd_short.cu", "fwd_pack.cu", "bwd.cu", "bwd_dq.cu", "bwd_fused.cu", "bwd_short.cu", "f32.cu", "static_scratch.cu",
-           "cache.cu", "cache_append.cu", "cache_simt.cu", "cache_decode.cu"]
+           "cache.cu", "cache_append.cu", "cache_simt.cu", "cache_decode.cu", "cache_chunk.cu"]
 
 
 def _nvcc() -> str:

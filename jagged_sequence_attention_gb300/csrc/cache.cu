@@ -47,6 +47,8 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
                : JFA_ERR_CUDA;
 }
 
+constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
+
 // Whether the cache's device is the current one.
 bool on_device(jfa_cache c) {
     int dev = -1;
@@ -200,8 +202,9 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
 
 size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
     if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
-    return JFA_CACHE_ZERO_BYTES + std::max(cache_simt_part_bytes(cache->D, cache->num_sms),
-                                           cache_decode_part_bytes(cache->D, cache->num_sms));
+    const int D = cache->D, n = cache->num_sms;
+    return JFA_CACHE_ZERO_BYTES + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n)
+                                                           : std::max(cache_decode_part_bytes(D, n), cache_chunk_part_bytes(D, n)));
 }
 
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
@@ -260,9 +263,21 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.row_lo = 0;
     p.row_hi = INT32_MAX;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->dtype == JFA_BF16
-                              ? launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st)
-                              : launch_cache_simt(cache->dtype, cache->D, p, cache->num_sms, st);
+    cudaError_t e = cudaSuccess;
+    if (cache->dtype == JFA_F32) {
+        e = launch_cache_simt(cache->dtype, cache->D, p, cache->num_sms, st);
+    } else {
+        // Sequences of at most kDecodeRows packed rows run in the decode kernel, the others in
+        // the chunk kernel; which there are is known on the device only, beyond max_q_len.
+        const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
+        if (rows > kDecodeRows) {
+            p.row_lo = kDecodeRows;
+            e = launch_cache_chunk(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
+            p.row_lo = 0;
+            p.row_hi = kDecodeRows;
+        }
+        if (e == cudaSuccess) e = launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
+    }
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 

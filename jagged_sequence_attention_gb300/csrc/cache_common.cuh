@@ -256,12 +256,26 @@ __device__ __forceinline__ int cache_cta_of(const CacheStart& st, long long u) {
 // first part in slot 1 of `first`, the others in slot 0.
 __device__ __forceinline__ int cache_slot(int cta, int first_cta) { return 2 * cta + (cta == first_cta ? 1 : 0); }
 
+// One box of the pages: elements x .., slots y .., head z, page w.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 cudaError_t launch_cache_simt(int dtype, int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_simt_part_bytes(int D, int num_sms);
 // bf16, row tiles of 16 packed rows: bound by the stream of K and V.
 cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
                                 cudaStream_t st);
 size_t cache_decode_part_bytes(int D, int num_sms);
+// bf16, items of 256 packed rows: bound by the tensor cores and the exponentials.
+cudaError_t launch_cache_chunk(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                               cudaStream_t st);
+size_t cache_chunk_part_bytes(int D, int num_sms);
 
 struct CacheAppendParams {
     const int32_t* q_off;
