@@ -438,7 +438,7 @@ class Cache:
     def __init__(self, handle, K, V):
         self.handle, self.K, self.V = handle, K, V
         self.n_pages, self.page_size, self.Hkv, self.D = K.shape
-        self.dtype, self.device = K.dtype, K.device
+        self.dtype, self.device, self.device_index = K.dtype, K.device, K.get_device()
 
     def __del__(self):
         try:
@@ -462,7 +462,8 @@ def jfa_cache_create(K: torch.Tensor, V: torch.Tensor, stream=None) -> Cache:
     if K.stride(3) != 1 or V.stride(3) != 1:
         _bad(fn, "the head dimension must be dense")
     n, ps, Hkv, D = K.shape
-    ks, vs = (ctypes.c_int64 * 3)(*K.stride()[:3]), (ctypes.c_int64 * 3)(*V.stride()[:3])
+    # (a dimension of one element leaves its stride free)
+    ks, vs = ((ctypes.c_int64 * 3)(*[t.stride(i) if t.shape[i] > 1 else D for i in range(3)]) for t in (K, V))
     h = ctypes.c_void_p()
     _check(fn, lib().jfa_cache_create(_dtype_code(K), Hkv, D, ps, n, K.data_ptr(), V.data_ptr(), ks, vs,
                                       _stream(stream), ctypes.byref(h)))
@@ -479,28 +480,39 @@ def jfa_cache_device_status(cache: Cache, stream=None) -> int:
     return int(lib().jfa_cache_device_status(cache.handle, _stream(stream)))
 
 
+# The two calls of a served step run once per layer and token, and a small one takes a few
+# microseconds on the GPU: the checks below read each tensor's attributes once.
+
 def _cache_batch(fn: str, cache: Cache, q_offsets, kv_lens, page_table):
     """(B, max_pages) of a batch's device arrays."""
-    for t in (q_offsets, kv_lens, page_table):
-        if t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous():
-            _bad(fn, "q_offsets, kv_lens and page_table must be contiguous int32 tensors on the cache's device")
-    B = kv_lens.numel()
-    if q_offsets.numel() != B + 1 or page_table.dim() != 2 or page_table.shape[0] != B:
+    dev, i32 = cache.device_index, torch.int32
+    shape = page_table.shape
+    if len(shape) != 2 or (kv_lens.numel(),) != shape[:1] or q_offsets.numel() != shape[0] + 1:
         _bad(fn, "q_offsets [B + 1], kv_lens [B] and page_table [B, max_pages] disagree")
-    return B, page_table.shape[1]
+    if not (q_offsets.dtype is kv_lens.dtype is page_table.dtype is i32
+            and q_offsets.get_device() == kv_lens.get_device() == page_table.get_device() == dev
+            and q_offsets.is_contiguous() and kv_lens.is_contiguous() and page_table.is_contiguous()):
+        _bad(fn, "q_offsets, kv_lens and page_table must be contiguous int32 tensors on the cache's device")
+    return shape
 
 
 def _cache_rows(fn: str, cache: Cache, t: torch.Tensor, heads, T=None):
     """The token stride of [T, heads, D] rows whose heads are dense."""
-    D = cache.D
-    if t.dtype != cache.dtype or t.device != cache.device or t.dim() != 3 or t.shape[2] != D or \
-            (heads is not None and t.shape[1] != heads) or (T is not None and t.shape[0] != T):
+    shape, D = t.shape, cache.D
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads) or \
+            (T is not None and shape[0] != T) or t.dtype is not cache.dtype or t.get_device() != cache.device_index:
         _bad(fn, "rows must be [T, heads, D] in the cache's type, on its device")
-    s = t.stride()
-    if t.numel() and (s[2] != 1 or (t.shape[1] > 1 and s[1] != D)):
+    n, h, _ = shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (h > 1 and s1 != D)) and n * h:
         _bad(fn, "the heads of a row must be dense")
     # one token (or none): torch leaves its stride free
-    return s[0] if t.shape[0] > 1 else t.shape[1] * D
+    return s0 if n > 1 else h * D
+
+
+def _cache_stream(cache: Cache, stream):
+    """The stream's handle: the given one's, or the current one of the cache's device."""
+    return torch.cuda.current_stream(cache.device).cuda_stream if stream is None else stream.cuda_stream
 
 
 def jfa_cache_append(cache: Cache, K, V, q_offsets, kv_lens, page_table, Q=None, Q_out=None, rot=None,
@@ -510,28 +522,33 @@ def jfa_cache_append(cache: Cache, K, V, q_offsets, kv_lens, page_table, Q=None,
     (into Q_out, which may be Q; allocated if None).  Returns Q_out (None without Q)."""
     fn = "jfa_cache_append"
     B, max_pages = _cache_batch(fn, cache, q_offsets, kv_lens, page_table)
-    T = K.shape[0]
     ks = _cache_rows(fn, cache, K, cache.Hkv)
+    T = K.shape[0]
     vs = _cache_rows(fn, cache, V, cache.Hkv, T)
     H, qs, qos, qp, qop = 1, 0, 0, None, None
     if Q is not None:
-        H = Q.shape[1] if Q.dim() == 3 else 0
+        qs = _cache_rows(fn, cache, Q, None, T)
+        H = Q.shape[1]
         if Q_out is None:
-            Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-        qs, qos = _cache_rows(fn, cache, Q, None, T), _cache_rows(fn, cache, Q_out, H, T)
+            Q_out = torch.empty((T, H, cache.D), dtype=Q.dtype, device=Q.device)
+        qos = _cache_rows(fn, cache, Q_out, H, T)
         qp, qop = Q.data_ptr(), Q_out.data_ptr()
     elif Q_out is not None:
         _bad(fn, "Q_out without Q")
     rp, rot_dim, rot_len = None, 0, 0
     if rot is not None:
-        if rot.dtype != torch.float32 or rot.device != cache.device or rot.dim() != 2 or not rot.is_contiguous():
+        shape = rot.shape
+        if len(shape) != 2 or rot.dtype is not torch.float32 or rot.get_device() != cache.device_index or \
+                not rot.is_contiguous():
             _bad(fn, "rot must be a contiguous fp32 tensor [rot_len, rot_dim] on the cache's device")
-        rot_len, rot_dim = rot.shape
+        rot_len, rot_dim = shape
         rp = rot.data_ptr()
     kind = ROT_KINDS.get(rot_kind, -1) if isinstance(rot_kind, str) else int(rot_kind)
-    _check(fn, lib().jfa_cache_append(cache.handle, B, T, q_offsets.data_ptr(), kv_lens.data_ptr(),
-                                      page_table.data_ptr(), max_pages, K.data_ptr(), ks, V.data_ptr(), vs, qp, qs, H,
-                                      qop, qos, rp, rot_dim, rot_len, kind, _stream(stream)))
+    status = lib().jfa_cache_append(cache.handle, B, T, q_offsets.data_ptr(), kv_lens.data_ptr(),
+                                    page_table.data_ptr(), max_pages, K.data_ptr(), ks, V.data_ptr(), vs, qp, qs, H,
+                                    qop, qos, rp, rot_dim, rot_len, kind, _cache_stream(cache, stream))
+    if status != JFA_OK:
+        raise JFAError(fn, status)
     return Q_out
 
 
@@ -558,36 +575,38 @@ def jfa_cache_fwd(cache: Cache, Q, q_offsets, kv_lens, page_table, bias=None, sc
     fn = "jfa_cache_fwd"
     B, max_pages = _cache_batch(fn, cache, q_offsets, kv_lens, page_table)
     qs = _cache_rows(fn, cache, Q, None)
-    T, H, D = Q.shape
-    scale = 1.0 / float(D) ** 0.5 if scale is None else float(scale)
+    shape, dev = Q.shape, cache.device_index
+    T, H, D = shape
     if O is None:
-        O = torch.empty((T, H, D), dtype=out_dtype or Q.dtype, device=Q.device)
-    elif O.shape != Q.shape or not O.is_contiguous() or O.device != cache.device:
+        O = torch.empty(shape, dtype=out_dtype or Q.dtype, device=Q.device)
+    elif O.shape != shape or not O.is_contiguous() or O.get_device() != dev:
         _bad(fn, "O must be a contiguous tensor of Q's shape")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=Q.device)
-    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.device != cache.device:
+    elif lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous() or \
+            lse.get_device() != dev:
         _bad(fn, "lse must be a contiguous fp32 tensor [T, H]")
-    bp = None
+    bp, kind = None, JFA_BIAS_NONE
     if bias is not None:
-        if bias.dtype != torch.float32 or bias.shape != (H, 32) or not bias.is_contiguous() or \
-                bias.device != cache.device:
+        if bias.dtype is not torch.float32 or bias.shape != (H, 32) or not bias.is_contiguous() or \
+                bias.get_device() != dev:
             _bad(fn, "bias must be a contiguous fp32 tensor [H, 32]")
-        bp = bias.data_ptr()
+        bp, kind = bias.data_ptr(), JFA_BIAS_RELPOS32
     if workspace is None:
         if stream is not None:
             with torch.cuda.stream(stream):
                 workspace = jfa_cache_workspace(cache, H)
         else:
             workspace = jfa_cache_workspace(cache, H)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         _bad(fn, "workspace must be a contiguous tensor on the cache's device")
-    _check(fn, lib().jfa_cache_fwd(cache.handle, B, T, 0 if max_q_len is None else int(max_q_len),
-                                   q_offsets.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), max_pages,
-                                   Q.data_ptr(), qs, H, int(bool(causal)), _win(window),
-                                   JFA_BIAS_NONE if bp is None else JFA_BIAS_RELPOS32, bp, scale, O.data_ptr(),
-                                   _dtype_code(O), lse.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    status = lib().jfa_cache_fwd(cache.handle, B, T, 0 if max_q_len is None else int(max_q_len), q_offsets.data_ptr(),
+                                 kv_lens.data_ptr(), page_table.data_ptr(), max_pages, Q.data_ptr(), qs, H,
+                                 1 if causal else 0, -1 if window is None else int(window), kind, bp,
+                                 D ** -0.5 if scale is None else float(scale), O.data_ptr(), _dtype_code(O),
+                                 lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _cache_stream(cache, stream))
+    if status != JFA_OK:
+        raise JFAError(fn, status)
     return O, lse
 
 
