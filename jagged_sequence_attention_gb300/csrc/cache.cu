@@ -263,21 +263,22 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.row_lo = 0;
     p.row_hi = INT32_MAX;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Sequences of at most kDecodeRows packed rows run in the decode kernel, the others in the
+    // chunk kernel; which there are is known on the device only, beyond max_q_len.
+    auto launch = [&](bool chunk) {
+        if (cache->dtype == JFA_F32) return launch_cache_simt(cache->D, chunk, p, cache->num_sms, st);
+        return chunk ? launch_cache_chunk(cache->D, cache->mk, cache->mv, p, cache->num_sms, st)
+                     : launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
+    };
+    const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
     cudaError_t e = cudaSuccess;
-    if (cache->dtype == JFA_F32) {
-        e = launch_cache_simt(cache->dtype, cache->D, p, cache->num_sms, st);
-    } else {
-        // Sequences of at most kDecodeRows packed rows run in the decode kernel, the others in
-        // the chunk kernel; which there are is known on the device only, beyond max_q_len.
-        const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
-        if (rows > kDecodeRows) {
-            p.row_lo = kDecodeRows;
-            e = launch_cache_chunk(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
-            p.row_lo = 0;
-            p.row_hi = kDecodeRows;
-        }
-        if (e == cudaSuccess) e = launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
+    if (rows > kDecodeRows) {
+        p.row_lo = kDecodeRows;
+        e = launch(true);
+        p.row_lo = 0;
+        p.row_hi = kDecodeRows;
     }
+    if (e == cudaSuccess) e = launch(false);
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 

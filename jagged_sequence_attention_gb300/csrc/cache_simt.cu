@@ -1,200 +1,315 @@
-// Paged-cache attention on the CUDA cores (plain fp32 arithmetic on float inputs).
+// Paged-cache attention for fp32: plain fp32 arithmetic on the CUDA cores (the tensor cores'
+// fp32-input format would drop 13 mantissa bits), in two row-tile sizes.
 //
-// A CTA of four warps takes 16 packed rows of an item and streams its keys 64 at a time
-// through shared memory; warp w owns rows 4w .. 4w+3 from scores to output, so the softmax
-// needs no exchange between warps.  Scores: a lane takes two keys and four rows; P V: a lane
-// takes D / 32 columns and four rows.
+// A CTA of four warps streams an item's keys 64 at a time through shared memory, copied
+// there 16 bytes at a time (cp.async) by pages.  A warp owns its rows from scores to output,
+// so the softmax needs no exchange between warps; a thread takes RT rows x KT keys of the
+// scores and RT rows x CT columns of P V.
+//   128 rows (chunks): bound by the FMA units and, nearly as much, by shared-memory reads --
+//     a thread's 8 x 8 tile reads 16 16-byte words per 256 products, as many cycles of the
+//     128 B/clk return path as of the FMA units.  K is loaded again during P V and V during
+//     the next scores, so one buffer of each is enough and two CTAs fit an SM.
+//   16 rows (single tokens, short sets): 4 x 2 scores per thread, two buffers of K and V,
+//     three CTAs per SM: bound by the stream of K and V up to a few rows per key head.
 #include "cache_common.cuh"
+#include "tilemath.cuh"
 
 namespace jfa {
 
 namespace {
 
-constexpr int kSimtBM = 16, kSimtBN = 64, kSimtThreads = 128, kSimtCtasPerSm = 2;
+constexpr int kSimtBN = 64, kSimtThreads = 128;
 
-template <int D>
+template <int D, int BM>
 struct SimtCfg {
-    static constexpr int kStride = D + 4;  // floats per staged key row: 16-byte reads of 8 rows cover all banks
-    static constexpr int kQ = 0, kK = kQ + kSimtBM * D, kV = kK + kSimtBN * kStride, kP = kV + kSimtBN * D;
-    static constexpr int kFloats = kP + kSimtBM * kSimtBN;
+    static constexpr bool kBig = BM == 128;
+    static constexpr int kRows = BM / 4;                  // rows of a warp
+    static constexpr int LY = 4, LX = 8;                  // big: lanes 4 (rows) x 8 (keys); small: 1 x 32
+    static constexpr int RT = kBig ? kRows / LY : kRows;  // rows of a thread
+    static constexpr int KT = kBig ? kSimtBN / LX : 2;    // keys of a thread
+    static constexpr int kCtasPerSm = kBig ? 2 : 3;
+    static constexpr int kBufs = kBig ? 1 : 2;
+    // floats per staged row: 16-byte reads of 8 consecutive key rows cover all banks
+    static constexpr int kStrideK = D + 4, kStrideQ = D + 4, kStrideP = kBig ? kSimtBN + 8 : kSimtBN;
+    static constexpr int kQ = 0, kK = kQ + BM * kStrideQ, kV = kK + kBufs * kSimtBN * kStrideK;
+    static constexpr int kP = kV + kBufs * kSimtBN * D, kFloats = kP + BM * kStrideP;
     static constexpr int kBytes = kFloats * 4;
-    static constexpr int kPart = kSimtBM * (D + 2);  // floats of a partial result: O, m, l
+    static constexpr int kPart = BM * (D + 2);  // floats of a partial result: O, m, l
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-__device__ __forceinline__ int rel_bucket(int r) {
-    r = abs(r);
-    const int rc = min(r, 46339);
-    return r >= 46340 ? 31 : 31 - __clz(int(uint32_t(rc + 1) * uint32_t(rc + 1)));
+__device__ __forceinline__ void cp16(float* dst, const float* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kSimtThreads) jfa_cache_simt_kernel(const CacheFwdParams p) {
-    using C = SimtCfg<D>;
-    constexpr int BM = kSimtBM, BN = kSimtBN, NC = D / 32;
+template <int D, int BM, bool BIAS>
+__global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_cache_simt_kernel(const CacheFwdParams p) {
+    using C = SimtCfg<D, BM>;
+    constexpr int BN = kSimtBN, RT = C::RT, KT = C::KT;
+    // columns of a thread in P V: big: groups of four at 4 kx + 32 j; small: lane + 32 j
+    constexpr int NC = C::kBig ? D / C::LX : D / 32;
     extern __shared__ __align__(16) float sm[];
     __shared__ CacheStart start;
     __shared__ int last_flag;
     float* sQ = sm + C::kQ;
-    float* sK = sm + C::kK;
-    float* sV = sm + C::kV;
     float* sP = sm + C::kP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ry = C::kBig ? lane / C::LX : 0, kx = C::kBig ? lane % C::LX : lane;
+    // tile row of this thread's row i, tile key of its key j, output column of its column c
+    auto row_of = [&](int i) { return warp * C::kRows + (C::kBig ? C::LY * i + ry : i); };
+    auto key_of = [&](int j) { return kx + (C::kBig ? C::LX : 32) * j; };
     cache_start<BM, BN>(p, &start, reinterpret_cast<long long*>(sm));
     CacheCursor<BM, BN> cur(start);
     CacheSeg g;
     const int page_mask = (1 << p.page_log2) - 1;
     while (cur.next(p, g)) {
-        const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len;
-        __syncthreads();
-        for (int e = threadIdx.x; e < BM * D; e += kSimtThreads) {
-            const int r = g.tile * BM + e / D;
-            float v = 0.f;
-            if (r < R)
-                v = to_f<T>(static_cast<const T*>(p.Q)[(g.s.q0 + r / p.g) * p.q_stride +
-                                                       int64_t(g.hk * p.g + r % p.g) * D + e % D]);
-            sQ[e] = v;
+        const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * BM;
+        // 64 rows of K or V from position c0 on, zeros where no row of the item may look
+        auto load = [&](float* dst, int stride, const void* base, const int64_t* s, int c0) {
+            constexpr int kPieces = D / 4, kStep = kSimtThreads / kPieces;
+            const int c = threadIdx.x % kPieces;
+#pragma unroll 4
+            for (int r = threadIdx.x / kPieces; r < BN; r += kStep) {
+                const int j = c0 + r;
+                const float* src = static_cast<const float*>(base);
+                bool in = j >= g.r.lo && j < g.r.hi;
+                if (in) {
+                    const int page = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                    in = page >= 0 && page < p.n_pages;
+                    if (in)
+                        src += page * s[0] + (j & page_mask) * s[1] + g.hk * s[2] + 4 * c;
+                    else if (c == 0)
+                        atomicOr(p.status, kStatusBounds);
+                }
+                cp16(dst + r * stride + 4 * c, src, in);
+            }
+            cp_commit();
+        };
+        auto load_k = [&](int kt) { load(sm + C::kK + (C::kBufs > 1 ? (kt & 1) * BN * C::kStrideK : 0), C::kStrideK, p.K, p.ks, (g.r.f + kt) * BN); };
+        auto load_v = [&](int kt) { load(sm + C::kV + (C::kBufs > 1 ? (kt & 1) * BN * D : 0), D, p.V, p.vs, (g.r.f + kt) * BN); };
+        const int k_end = g.r.n > 0 ? g.k1 : g.k0;
+        __syncthreads();  // the previous item's last reads
+        if (g.k0 < k_end) {
+            load_k(g.k0);
+            load_v(g.k0);
         }
-        // rows 4 warp + i: their limits and heads
-        int lim[4], low[4], head[4], tok[4];
-        float m[4], l[4], o[4][NC];
+        for (int e = threadIdx.x; e < BM * D / 4; e += kSimtThreads) {
+            const int tr = e / (D / 4), c = e % (D / 4), r = r0 + tr;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < R) {
+                const int tok = r / p.g;
+                v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
+                                                     int64_t(g.hk * p.g + r - tok * p.g) * D + 4 * c);
+            }
+            *reinterpret_cast<float4*>(sQ + tr * C::kStrideQ + 4 * c) = v;
+        }
+        float m[RT], l[RT], o[RT][NC];
+        int rel[RT];                 // position of each row (rows past the end repeat the last one's)
+        const float* brow[RT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = g.tile * BM + 4 * warp + i;
-            tok[i] = r / p.g;
-            head[i] = r < R ? g.hk * p.g + r % p.g : 0;
-            const int at = tok[i] + diag;
-            lim[i] = r < R ? (p.causal ? min(g.s.kv_len, at + 1) : g.s.kv_len) : 0;
-            low[i] = p.window >= 0 ? at - p.window : 0;
+        for (int i = 0; i < RT; ++i) {
+            const int r = min(r0 + row_of(i), R - 1), tok = r / p.g;
+            rel[i] = tok + diag;
+            brow[i] = BIAS ? p.bias + (g.hk * p.g + r - tok * p.g) * 32 : nullptr;
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
         }
-        const int k_end = g.r.n > 0 ? g.k1 : g.k0;
+        const int t_first = r0 / p.g + diag, t_last = (min(R, r0 + BM) - 1) / p.g + diag;
+        const int all_hi = p.causal ? min(g.s.kv_len, t_first + 1) : g.s.kv_len;
+        const int all_lo = p.window >= 0 ? max(0, t_last - p.window) : 0;
         for (int kt = g.k0; kt < k_end; ++kt) {
             const int c0 = (g.r.f + kt) * BN;
-            __syncthreads();
-            for (int e = threadIdx.x; e < BN * D; e += kSimtThreads) {
-                const int j = c0 + e / D, d = e % D;
-                float kx = 0.f, vx = 0.f;
-                if (j >= g.r.lo && j < g.r.hi) {
-                    const int page = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
-                    if (page >= 0 && page < p.n_pages) {
-                        const int slot = j & page_mask;
-                        kx = to_f<T>(static_cast<const T*>(p.K)[page * p.ks[0] + slot * p.ks[1] + g.hk * p.ks[2] + d]);
-                        vx = to_f<T>(static_cast<const T*>(p.V)[page * p.vs[0] + slot * p.vs[1] + g.hk * p.vs[2] + d]);
-                    } else if (d == 0) {
-                        atomicOr(p.status, kStatusBounds);
-                    }
+            const float* sK = sm + C::kK + (C::kBufs > 1 ? (kt & 1) * BN * C::kStrideK : 0);
+            const float* sV = sm + C::kV + (C::kBufs > 1 ? (kt & 1) * BN * D : 0);
+            if (C::kBufs > 1) {
+                // both of the next tile's loads go out before this tile is waited for
+                if (kt > g.k0) __syncthreads();  // the other buffers have been read
+                if (kt + 1 < k_end) {
+                    load_k(kt + 1);
+                    load_v(kt + 1);
+                    cp_wait<2>();
+                } else {
+                    cp_wait<0>();
                 }
-                sK[(e / D) * C::kStride + d] = kx;
-                sV[e] = vx;
+            } else {
+                cp_wait<1>();  // K of this tile (V may still be on its way)
             }
             __syncthreads();
-            float x[4][2];
+            float x[RT][KT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = 0.f;
-#pragma unroll 4
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < KT; ++j) x[i][j] = 0.f;
+#pragma unroll 1
             for (int d = 0; d < D; d += 4) {
-                float4 kk[2];
+                float4 kk[KT];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) kk[c] = *reinterpret_cast<const float4*>(sK + (lane + 32 * c) * C::kStride + d);
+                for (int j = 0; j < KT; ++j) kk[j] = *reinterpret_cast<const float4*>(sK + key_of(j) * C::kStrideK + d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 q = *reinterpret_cast<const float4*>(sQ + (4 * warp + i) * D + d);
+                for (int i = 0; i < RT; ++i) {
+                    const float4 q = *reinterpret_cast<const float4*>(sQ + row_of(i) * C::kStrideQ + d);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        x[i][c] = fmaf(q.x, kk[c].x, x[i][c]);
-                        x[i][c] = fmaf(q.y, kk[c].y, x[i][c]);
-                        x[i][c] = fmaf(q.z, kk[c].z, x[i][c]);
-                        x[i][c] = fmaf(q.w, kk[c].w, x[i][c]);
+                    for (int j = 0; j < KT; ++j) {
+                        x[i][j] = fmaf(q.x, kk[j].x, x[i][j]);
+                        x[i][j] = fmaf(q.y, kk[j].y, x[i][j]);
+                        x[i][j] = fmaf(q.z, kk[j].z, x[i][j]);
+                        x[i][j] = fmaf(q.w, kk[j].w, x[i][j]);
                     }
                 }
             }
+            if (C::kBufs == 1) {
+                __syncthreads();  // K has been read: the next tile's loads overlap P V
+                if (kt + 1 < k_end) load_k(kt + 1);
+            }
+            const bool masked = c0 < all_lo || c0 + BN > all_hi;
+            const int bk = BIAS ? relpos_bucket(t_last - c0) : 0;
+            const int near = t_first - c0 - (BN - 1);
+            const bool one = BIAS && (near >= 0 || t_last <= c0) && bk == relpos_bucket(near);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RT; ++i) {
+                const float b1 = BIAS && one ? __ldg(brow[i] + bk) * 1.4426950408889634f : 0.f;
                 float mx = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int j = c0 + lane + 32 * c;
-                    float y = x[i][c] * p.scale_log2;
-                    if (p.bias) y += p.bias[head[i] * 32 + rel_bucket(tok[i] + diag - j)] * 1.4426950408889634f;
-                    x[i][c] = j < lim[i] && j >= low[i] ? y : -INFINITY;
-                    mx = fmaxf(mx, x[i][c]);
+                for (int j = 0; j < KT; ++j) {
+                    const int key = c0 + key_of(j);
+                    float add = b1;
+                    if (BIAS && !one) add = __ldg(brow[i] + relpos_bucket(rel[i] - key)) * 1.4426950408889634f;
+                    float y = BIAS ? fmaf(x[i][j], p.scale_log2, add) : x[i][j] * p.scale_log2;
+                    if (masked) {
+                        const bool in = key < g.s.kv_len && (!p.causal || key <= rel[i]) &&
+                                        (p.window < 0 || key >= rel[i] - p.window);
+                        y = in ? y : -INFINITY;
+                    }
+                    x[i][j] = y;
+                    mx = fmaxf(mx, y);
                 }
 #pragma unroll
-                for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+                for (int s = (C::kBig ? C::LX : 32) / 2; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
                 const float m_new = fmaxf(m[i], mx);
                 const float m_use = m_new == -INFINITY ? 0.f : m_new;
                 const float alpha = exp2f(m[i] - m_use);
                 m[i] = m_new;
                 float sum = 0.f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float e = exp2f(x[i][c] - m_use);
-                    sP[(4 * warp + i) * BN + lane + 32 * c] = e;
+                for (int j = 0; j < KT; ++j) {
+                    const float e = exp2f(x[i][j] - m_use);
+                    sP[row_of(i) * C::kStrideP + key_of(j)] = e;
                     sum += e;
                 }
-#pragma unroll
-                for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-                l[i] = l[i] * alpha + sum;
+                l[i] = fmaf(l[i], alpha, sum);  // this thread's keys; summed over the lanes at the end
 #pragma unroll
                 for (int c = 0; c < NC; ++c) o[i][c] *= alpha;
             }
             __syncwarp();
+            if (C::kBufs == 1) {
+                if (kt + 1 < k_end)
+                    cp_wait<1>();  // V of this tile
+                else
+                    cp_wait<0>();
+                __syncthreads();
+            }
+            if constexpr (C::kBig) {
+#pragma unroll 1
+                for (int j = 0; j < BN; j += 4) {
+                    float4 e[RT];
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sP + row_of(i) * C::kStrideP + j);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int c4 = 0; c4 < NC / 4; ++c4) {
+                            const float4 v = *reinterpret_cast<const float4*>(sV + (j + q) * D + 4 * kx + 32 * c4);
+#pragma unroll
+                            for (int i = 0; i < RT; ++i) {
+                                const float w = q == 0 ? e[i].x : q == 1 ? e[i].y : q == 2 ? e[i].z : e[i].w;
+                                o[i][4 * c4] = fmaf(w, v.x, o[i][4 * c4]);
+                                o[i][4 * c4 + 1] = fmaf(w, v.y, o[i][4 * c4 + 1]);
+                                o[i][4 * c4 + 2] = fmaf(w, v.z, o[i][4 * c4 + 2]);
+                                o[i][4 * c4 + 3] = fmaf(w, v.w, o[i][4 * c4 + 3]);
+                            }
+                        }
+                }
+                __syncthreads();  // V has been read: the next tile's loads overlap its scores
+                if (kt + 1 < k_end) load_v(kt + 1);
+            } else {
 #pragma unroll 2
-            for (int j = 0; j < BN; j += 4) {
-                float4 e[4];
+                for (int j = 0; j < BN; j += 4) {
+                    float4 e[RT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const float4*>(sP + (4 * warp + i) * BN + j);
+                    for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sP + row_of(i) * C::kStrideP + j);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float v = sV[(j + q) * D + lane + 32 * c];
+                        for (int c = 0; c < NC; ++c) {
+                            const float v = sV[(j + q) * D + lane + 32 * c];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[i][c] = fmaf(q == 0 ? e[i].x : q == 1 ? e[i].y : q == 2 ? e[i].z : e[i].w, v, o[i][c]);
-                    }
+                            for (int i = 0; i < RT; ++i)
+                                o[i][c] = fmaf(q == 0 ? e[i].x : q == 1 ? e[i].y : q == 2 ? e[i].z : e[i].w, v, o[i][c]);
+                        }
+                }
+                __syncwarp();
             }
         }
-        // Row i of this warp, written out: O / l and lse.
-        auto finish = [&](int i, float mm, float ll, const float (&v)[NC]) {
-            const int r = g.tile * BM + 4 * warp + i;
-            if (r >= R) return;
-            const size_t row = size_t(g.s.q0 + r / p.g) * size_t(p.H) + size_t(g.hk * p.g + r % p.g);
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                if (p.o_f32)
-                    static_cast<float*>(p.O)[row * D + lane + 32 * c] = v[c] * inv;
-                else
-                    static_cast<__nv_bfloat16*>(p.O)[row * D + lane + 32 * c] = __float2bfloat16(v[c] * inv);
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int s = (C::kBig ? C::LX : 32) / 2; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
+        // a row's columns as this thread holds them, to dst (times mul) or out of src (added, times w)
+        auto put = [&](float* dst, const float (&v)[NC], float mul) {
+            if constexpr (C::kBig) {
+#pragma unroll
+                for (int c = 0; c < NC; c += 4)
+                    *reinterpret_cast<float4*>(dst + 4 * kx + 8 * c) =
+                        make_float4(v[c] * mul, v[c + 1] * mul, v[c + 2] * mul, v[c + 3] * mul);
+            } else {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) dst[lane + 32 * c] = v[c] * mul;
             }
-            if (p.lse && lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        };
+        auto take = [&](const float* src, float (&v)[NC], float w) {
+            if constexpr (C::kBig) {
+#pragma unroll
+                for (int c = 0; c < NC; c += 4) {
+                    const float4 u = __ldcg(reinterpret_cast<const float4*>(src + 4 * kx + 8 * c));
+                    v[c] = fmaf(u.x, w, v[c]);
+                    v[c + 1] = fmaf(u.y, w, v[c + 1]);
+                    v[c + 2] = fmaf(u.z, w, v[c + 2]);
+                    v[c + 3] = fmaf(u.w, w, v[c + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) v[c] = fmaf(__ldcg(src + lane + 32 * c), w, v[c]);
+            }
+        };
+        auto finish = [&](int i, float mm, float ll, const float (&v)[NC]) {
+            const int r = r0 + row_of(i);
+            if (r >= R) return;
+            const int tok = r / p.g;
+            const size_t row = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
+            put(static_cast<float*>(p.O) + row * D, v, ll > 0.f ? 1.f / ll : 0.f);
+            if (p.lse && kx == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
         };
         if (g.whole()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) finish(i, m[i], l[i], o[i]);
+            for (int i = 0; i < RT; ++i) finish(i, m[i], l[i], o[i]);
             continue;
         }
         const int first = cache_cta_of(start, g.first), last = cache_cta_of(start, g.first + g.units - 1);
         float* mine = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 4 * warp + i;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) mine[r * D + lane + 32 * c] = o[i][c];
-            if (lane == 0) {
-                mine[BM * D + r] = m[i];
-                mine[BM * D + BM + r] = l[i];
+        for (int i = 0; i < RT; ++i) {
+            const int tr = row_of(i);
+            if (r0 + tr >= R) continue;
+            put(mine + tr * D, o[i], 1.f);
+            if (kx == 0) {
+                mine[BM * D + tr] = m[i];
+                mine[BM * D + BM + tr] = l[i];
             }
         }
         __threadfence();
@@ -206,49 +321,52 @@ __global__ void __launch_bounds__(kSimtThreads) jfa_cache_simt_kernel(const Cach
         }
         __syncthreads();
         if (!last_flag) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 4 * warp + i;
+#pragma unroll 1
+        for (int i = 0; i < RT; ++i) {
+            const int tr = row_of(i);
+            if (r0 + tr >= R) continue;
+            const float* pm = p.part + BM * D + tr;
             float mm = -INFINITY;
-            for (int c = first; c <= last; ++c)
-                mm = fmaxf(mm, __ldcg(p.part + size_t(cache_slot(c, first)) * C::kPart + BM * D + r));
+#pragma unroll 4
+            for (int c = first; c <= last; ++c) mm = fmaxf(mm, __ldcg(pm + size_t(cache_slot(c, first)) * C::kPart));
             const float mu = mm == -INFINITY ? 0.f : mm;
             float ll = 0.f, v[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) v[c] = 0.f;
+#pragma unroll 2
             for (int c = first; c <= last; ++c) {
                 const float* part = p.part + size_t(cache_slot(c, first)) * C::kPart;
-                const float w = exp2f(__ldcg(part + BM * D + r) - mu);
-                ll = fmaf(__ldcg(part + BM * D + BM + r), w, ll);
-#pragma unroll
-                for (int k = 0; k < NC; ++k) v[k] = fmaf(__ldcg(part + r * D + lane + 32 * k), w, v[k]);
+                const float w = exp2f(__ldcg(part + BM * D + tr) - mu);
+                ll = fmaf(__ldcg(part + BM * D + BM + tr), w, ll);
+                take(part + tr * D, v, w);
             }
             finish(i, mm, ll, v);
         }
     }
 }
 
-template <int D, typename T>
+template <int D, int BM, bool BIAS>
 cudaError_t launch(const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(jfa_cache_simt_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SimtCfg<D>::kBytes);
+    using C = SimtCfg<D, BM>;
+    cudaError_t e = cudaFuncSetAttribute(jfa_cache_simt_kernel<D, BM, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::kBytes);
     if (e != cudaSuccess) return e;
-    jfa_cache_simt_kernel<D, T><<<num_sms * kSimtCtasPerSm, kSimtThreads, SimtCfg<D>::kBytes, st>>>(p);
+    jfa_cache_simt_kernel<D, BM, BIAS><<<num_sms * C::kCtasPerSm, kSimtThreads, C::kBytes, st>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, int BM>
+cudaError_t launch_b(const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    return p.bias ? launch<D, BM, true>(p, num_sms, st) : launch<D, BM, false>(p, num_sms, st);
 }
 
 }  // namespace
 
-size_t cache_simt_part_bytes(int D, int num_sms) {
-    return size_t(num_sms) * kSimtCtasPerSm * 2 * kSimtBM * size_t(D + 2) * 4;
-}
+size_t cache_simt_part_bytes(int D, int num_sms) { return size_t(num_sms) * 2 * 2 * 128 * size_t(D + 2) * 4; }
 
-cudaError_t launch_cache_simt(int dtype, int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    if (dtype == JFA_F32 && D == 32) return launch<32, float>(p, num_sms, st);
-    if (dtype == JFA_F32 && D == 64) return launch<64, float>(p, num_sms, st);
-    if (dtype == JFA_BF16 && D == 64) return launch<64, __nv_bfloat16>(p, num_sms, st);
-    if (dtype == JFA_BF16 && D == 128) return launch<128, __nv_bfloat16>(p, num_sms, st);
-    return cudaErrorInvalidValue;
+cudaError_t launch_cache_simt(int D, bool chunk, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    if (D == 32) return chunk ? launch_b<32, 128>(p, num_sms, st) : launch_b<32, 16>(p, num_sms, st);
+    return chunk ? launch_b<64, 128>(p, num_sms, st) : launch_b<64, 16>(p, num_sms, st);
 }
 
 }  // namespace jfa
