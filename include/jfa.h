@@ -420,8 +420,8 @@ const char* jfa_status_string(int32_t status);
  *                     position rotation applied to keys and queries on the way;
  *   jfa_cache_fwd     attends from the new tokens to the cached positions.
  * Both take, as int32 DEVICE arrays read when the kernels run (so a captured graph can be
- * replayed on new contents):
- *   q_offsets [B+1]  the new tokens of sequence b are rows q_offsets[b] .. q_offsets[b+1]
+ * replayed on new contents), for B of at most 16384 sequences and T below 2^30 rows:
+ * *   q_offsets [B+1]  the new tokens of sequence b are rows q_offsets[b] .. q_offsets[b+1]
  *                    of Q, K and V (non-decreasing; rows from q_offsets[B] to T belong to
  *                    no sequence and are left alone);
  *   kv_lens [B]      positions of sequence b in the cache, its new tokens included: they are
@@ -490,7 +490,7 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
 
 /*
  * Attention of the new tokens over the cache: with i' = i + kv_len - q_len for row i of
- * sequence b and key head h / (H / Hkv) of query head h (H a multiple of Hkv),
+ * sequence b and key head h / (H / Hkv) of query head h (H a multiple of Hkv, with bf16 at most 128 Hkv),
  *   s_ij = scale * <q_i, k_j> + bias[h, bucket(|i' - j|)],  o_i = sum_j softmax_j(s_ij) v_j
  * over the keys j < kv_len allowed as in jfa_plan_create_ex: causal (0/1) j <= i', window
  * W >= 0 (with causal) j >= i' - W, -1: none.  A row with no allowed key gets o = 0 and
@@ -512,7 +512,7 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  *   The result is the same bit for bit on every run of the same call.
  * Errors: INVALID_ARG, UNSUPPORTED, PLAN_MISMATCH (another device is current), CUDA.
  */
-#define JFA_CACHE_ZERO_BYTES ((size_t)8192)
+#define JFA_CACHE_ZERO_BYTES ((size_t)32768)
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
                          const int32_t* kv_lens, const int32_t* page_table, int32_t max_pages,
                          const void* Q, int64_t q_stride, int32_t H, int32_t causal, int32_t window,

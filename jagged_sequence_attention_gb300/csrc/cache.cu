@@ -27,8 +27,7 @@ namespace {
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t elem(int dtype) { return dtype == JFA_F32 ? 4 : 2; }
 
-// The pages [n_pages][Hkv][page_size][D] by their strides, boxes of 128 bytes x `rows` slots.
-jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* c, const int64_t* s, int rows) {
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
     static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -36,17 +35,34 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f
                                                                                                              : nullptr);
     }();
+    return enc;
+}
+
+// A bf16 tensor of `rank` dimensions (the first dense, strides of the others in elements), its
+// boxes 128 bytes of the first, with 128-byte swizzle.
+jfa_status make_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const int64_t* strides,
+                         const cuuint32_t* box) {
+    const auto enc = encode_tiled();
     if (!enc) return JFA_ERR_CUDA;
-    const cuuint64_t dims[4] = {cuuint64_t(c->D), cuuint64_t(1) << c->page_log2, cuuint64_t(c->Hkv), cuuint64_t(c->n_pages)};
-    const cuuint64_t strides[3] = {cuuint64_t(s[1]) * 2, cuuint64_t(s[2]) * 2, cuuint64_t(s[0]) * 2};
-    const cuuint32_t box[4] = {64u, cuuint32_t(rows), 1u, 1u}, one[4] = {1u, 1u, 1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+    cuuint64_t bytes[3];
+    for (int i = 0; i + 1 < rank; ++i) bytes[i] = cuuint64_t(strides[i]) * 2;
+    const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, bytes, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? JFA_OK
                : JFA_ERR_CUDA;
 }
 
+// The pages by their strides, as (D, slot, head, page), boxes of `rows` slots.
+jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* c, const int64_t* s, int rows) {
+    const cuuint64_t dims[4] = {cuuint64_t(c->D), cuuint64_t(1) << c->page_log2, cuuint64_t(c->Hkv), cuuint64_t(c->n_pages)};
+    const int64_t strides[3] = {s[1], s[2], s[0]};
+    const cuuint32_t box[4] = {64u, cuuint32_t(rows), 1u, 1u};
+    return make_bf16_map(map, base, 4, dims, strides, box);
+}
+
+constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 
 // Whether the cache's device is the current one.
@@ -58,7 +74,7 @@ bool on_device(jfa_cache c) {
 // Checks of the arrays both calls take; max_kv: the longest sequence they can address.
 jfa_status check_batch(jfa_cache c, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
                        const int32_t* page_table, int32_t max_pages, int32_t* max_kv) {
-    if (!c || B < 0 || B > (1 << 16) || T < 0 || T > (1 << 30) || max_pages < 0) return JFA_ERR_INVALID_ARG;
+    if (!c || B < 0 || B > kCacheMaxB || T < 0 || T > (1 << 30) || max_pages < 0) return JFA_ERR_INVALID_ARG;
     if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4)) return JFA_ERR_INVALID_ARG;
     if (B > 0 && (!q_offsets || !kv_lens || (max_pages > 0 && !page_table))) return JFA_ERR_INVALID_ARG;
     *max_kv = int32_t(std::min<int64_t>(int64_t(max_pages) << c->page_log2, INT32_MAX - T - 1024));
@@ -89,7 +105,8 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
             if (s < D || s > (int64_t(1) << 38) || (size_t(s) * elem(dtype)) % 16 != 0) return JFA_ERR_INVALID_ARG;
     int dev = 0;
     cudaDeviceProp prop;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaGetDeviceProperties(&prop, dev) != cudaSuccess || prop.major != 10)
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaGetDeviceProperties(&prop, dev) != cudaSuccess || prop.major != 10 ||
+        prop.multiProcessorCount > kMaxSms)
         return JFA_ERR_NO_DEVICE;
     jfa_cache_t* c = new (std::nothrow) jfa_cache_t();
     if (!c) return JFA_ERR_CUDA;
@@ -203,7 +220,7 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
 size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
     if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
     const int D = cache->D, n = cache->num_sms;
-    return JFA_CACHE_ZERO_BYTES + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n)
+    return JFA_CACHE_ZERO_BYTES + kCutBytes + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n)
                                                            : std::max(cache_decode_part_bytes(D, n), cache_chunk_part_bytes(D, n)));
 }
 
@@ -216,6 +233,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const jfa_status s = check_batch(cache, B, T, q_offsets, kv_lens, page_table, max_pages, &max_kv);
     if (s != JFA_OK) return s;
     if (H < 1 || H > 65535 || H % cache->Hkv != 0 || T * H > INT32_MAX || max_q_len < 0) return JFA_ERR_INVALID_ARG;
+    if (cache->dtype == JFA_BF16 && H / cache->Hkv > 128) return JFA_ERR_UNSUPPORTED;  // a token's rows fill one tile
     if ((causal != 0 && causal != 1) || window < -1 || (window >= 0 && causal != 1)) return JFA_ERR_INVALID_ARG;
     if (bias_kind != JFA_BIAS_NONE && bias_kind != JFA_BIAS_RELPOS32)
         return bias_kind == JFA_BIAS_DENSE ? JFA_ERR_UNSUPPORTED : JFA_ERR_INVALID_ARG;
@@ -239,6 +257,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.H = H;
     p.Hkv = cache->Hkv;
     p.g = H / cache->Hkv;
+    set_div_g(p);
     p.page_log2 = cache->page_log2;
     p.n_pages = cache->n_pages;
     p.causal = causal;
@@ -257,7 +276,9 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.vs[i] = cache->vs[i];
     }
     p.counters = static_cast<uint32_t*>(workspace);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES);
+    p.cut_flags = p.counters + kCtrCuts;
+    p.cuts = reinterpret_cast<CacheCut*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES + kCutBytes);
     p.status = cache->d_status;
     p.min_units = 1;
     p.row_lo = 0;
@@ -265,14 +286,27 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Sequences of at most kDecodeRows packed rows run in the decode kernel, the others in the
     // chunk kernel; which there are is known on the device only, beyond max_q_len.
+    CUtensorMap mq;
     auto launch = [&](bool chunk) {
+        // a 128-key step of the chunk kernel is short against an item's start and end
+        p.min_units = chunk && cache->dtype == JFA_BF16 ? 4 : 1;
+        p.bm = chunk ? 128 : 16;
         if (cache->dtype == JFA_F32) return launch_cache_simt(cache->D, chunk, p, cache->num_sms, st);
-        return chunk ? launch_cache_chunk(cache->D, cache->mk, cache->mv, p, cache->num_sms, st)
+        p.tile_tokens = 128 / p.g;
+        if (chunk) p.bm = 2 * p.tile_tokens * p.g;
+        return chunk ? launch_cache_chunk(cache->D, mq, cache->mk, cache->mv, p, cache->num_sms, st)
                      : launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
     };
     const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
     cudaError_t e = cudaSuccess;
     if (rows > kDecodeRows) {
+        if (cache->dtype == JFA_BF16) {  // the queries as (D, head, token), boxes of one tile's rows
+            const cuuint64_t dims[3] = {cuuint64_t(cache->D), cuuint64_t(H), cuuint64_t(T)};
+            const int64_t strides[2] = {cache->D, q_stride};
+            const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(128 / p.g)};
+            const jfa_status ms = make_bf16_map(&mq, Q, 3, dims, strides, box);
+            if (ms != JFA_OK) return ms;
+        }
         p.row_lo = kDecodeRows;
         e = launch(true);
         p.row_lo = 0;

@@ -1,30 +1,48 @@
 // Paged-cache attention for chunks of new tokens (bf16): tcgen05 products, TMEM accumulators.
 //
 // An item is up to 256 packed rows (tokens x grouped heads) of one (sequence, key head): two
-// 128-row tiles that share every key and value tile, so that one tile's softmax runs while
+// tiles of floor(128 / g) tokens' rows (so that a tile is one box of Q) that share every key and value tile, so that one tile's softmax runs while
 // the tensor core works on the other.  Key tiles of 128 positions are gathered by TMA, one
 // box per page and 128-byte column block; a box of a short page lands at its rows of the
 // tile, whose swizzle repeats every 8 rows (the smallest page).
-// CTA = 18 warps, one CTA per SM, each on an equal share of the batch's key-tile steps
-// (cache_common.cuh).  Two warps share each row (thread = row = TMEM lane): one takes score
-// columns [0, 64) and O columns [0, D/2), the other the rest; they exchange row maxima and
-// sums through shared memory.
+// CTA = 19 warps, one CTA per SM; the CTAs draw their work from a counter (cache_common.cuh).
+// Two warps share each row (thread = row = TMEM lane): one takes score columns [0, 64) and O
+// columns [0, D/2), the other the rest; they exchange row maxima and sums through shared
+// memory.
 //   warps 0-3, 8-11    tile A, columns [0, 64) and [64, 128): softmax, rescaling, epilogue
 //   warps 4-7, 12-15   tile B
-//   warp 16            loads: Q rows (cp.async, swizzled by hand: packed rows of grouped
-//                      heads are not a box), K and V boxes through 2-stage rings
+//   warp 16            TMA loads: Q once per item, K and V boxes through 2-stage rings
 //   warp 17            tcgen05.mma issuer and TMEM owner; clears V rows no query may see
+//   warp 18            draws pieces of work ahead of the others and hands out their items
 // TMEM (512 columns): S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P
 // overwrites its own S columns as packed bf16 and is read from TMEM by O += P V.
 // An item with a single row tile runs its steps alternately as tile A and tile B (both on
 // the same query rows, each with its own maximum, sum and O), so it keeps the overlap; the
 // two are merged at the end.
+// The parts of an item cut between blocks go to the workspace in fp32, and a second kernel
+// adds them up: the last part's CTA alone would read them at one SM's rate (about 2 us a
+// part of 132 KB), and a long history under one chunk has tens of parts.
 #include "cache_common.cuh"
 #include "tilemath.cuh"
 
 namespace jfa {
 
 namespace {
+
+// A part of an item, as handed to the other warps (b < 0: the end).
+struct alignas(16) SegRec {
+    int b, hk, tile, k0, k1;
+    int q0, q_len, kv_len;
+    int first, last, slot;  // split item: blocks of its first and last part, this part's slot
+    int pad;
+};
+
+// From this many positions back on, 32 consecutive positions lie in three buckets at most:
+// r in [62, ..) and r - 31 differ by a factor of at most 2 in 1 + r, two buckets' width.
+// (and r <= -31 likewise, from the other side).  Chunks between the two touch |r| <= 93 and
+// read the bias from a table by position; a stride of 4 mod 32 spreads the heads of a warp's
+// rows over the banks.
+constexpr int kThreeBuckets = 62, kNear = 96, kNearStride = 100, kNearHeads = 48;
 
 template <int D>
 struct ChkCfg {
@@ -35,13 +53,17 @@ struct ChkCfg {
     static constexpr int kOffBar = kOffV + 2 * kKVBytes;
     static constexpr int kNumBars = 32;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag, merge flag
-    static constexpr int kOffStart = kOffMisc + 16;
-    static constexpr int kOffComb = kOffStart + 64;           // tile B's m and l halves of a split item, two buffers
+    static constexpr int kOffSeg = kOffMisc + 16;             // the part of an item handed out next
+    static constexpr int kOffStarts = kOffSeg + int(sizeof(SegRec));  // first position of each bias bucket
+    static constexpr int kOffComb = kOffStarts + 32 * 4;      // tile B's m and l of a split item, two buffers
     static constexpr int kOffXch = kOffComb + 2 * 3 * BM * 4; // pair exchanges [2][2][8][32]
-    static constexpr int kSmemNeed = kOffXch + 2 * 2 * 8 * 32 * 4 + 1024;
+    static constexpr int kOffGroups = kOffXch + 2 * 2 * 8 * 32 * 4;
+    // bias by relative position |r| < kNear, log2 units, of the first kNearHeads heads
+    static constexpr int kOffNear = kOffGroups + (int(sizeof(CacheGroups)) + 15) / 16 * 16;
+    static constexpr int kSmemNeed = kOffNear + kNearHeads * kNearStride * 4 + 1024;
     // at least 120 KB: one CTA per SM, as the CTA allocates all 512 TMEM columns
     static constexpr int kSmemBytes = kSmemNeed > 120 * 1024 ? kSmemNeed : 120 * 1024;
-    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 17, kThreads = 18 * 32;
+    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 17, kDrawWarp = 18, kThreads = 19 * 32;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, BM, BN, false, false);
     static constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, BM, D, false, true);
@@ -64,17 +86,12 @@ enum {
     B_DRAIN = 18,
     B_COMBINE = 19,  // split item: tile B's last P V done and its m and l written
     B_XCH = 20,      // +pair of warps
-    B_PART = 28,     // partial result written by every softmax warp
-    B_FLAG = 29,     // and its arrival counted
+    B_SEG_FULL = 28,   // the next part of an item handed out
+    B_SEG_EMPTY = 29,  // and read by every other warp
 };
 
 // TMEM column (within a tile's S/P columns) of the 16 P values of P V step s.
 __device__ __forceinline__ uint32_t p_col(int s) { return uint32_t(32 * (s >> 1) + 8 * (s & 1)); }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // What every role derives from an item's part: the steps [k0, k1) of the pair's key tiles,
 // and those of them that each tile takes.
@@ -91,11 +108,12 @@ __device__ __forceinline__ Steps steps_of(const CacheFwdParams& p, const CacheSe
     Steps s;
     s.k0 = g.k0;
     s.k1 = g.r.n > 0 ? g.k1 : g.k0;
-    s.split = (2 * g.tile + 1) * 128 >= g.s.q_len * p.g;
+    const int rt = p.tile_tokens * p.g;  // packed rows of a tile
+    s.split = (2 * g.tile + 1) * rt >= g.s.q_len * p.g;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         CacheRange r{0, 0, 0, 0};
-        if ((2 * g.tile + x) * 128 < g.s.q_len * p.g) r = cache_range<128, 128>(p, g.s, 2 * g.tile + x);
+        if ((2 * g.tile + x) * rt < g.s.q_len * p.g) r = cache_range<128>(p, g.s, 2 * g.tile + x, rt);
         s.a[x] = max(s.k0, r.f - g.r.f);
         s.b[x] = r.n > 0 ? min(s.k1, r.f - g.r.f + r.n) : s.a[x];
     }
@@ -103,9 +121,8 @@ __device__ __forceinline__ Steps steps_of(const CacheFwdParams& p, const CacheSe
 }
 
 template <int D, bool BIAS>
-__global__ void __launch_bounds__(576, 1)
-    jfa_cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                           const CacheFwdParams p) {
+__global__ void __launch_bounds__(608, 1)
+    jfa_cache_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const CacheFwdParams p) {
     using C = ChkCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -114,9 +131,10 @@ __global__ void __launch_bounds__(576, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * uint32_t(i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-    CacheStart* start = reinterpret_cast<CacheStart*>(smem + C::kOffStart);
-    static_assert(sizeof(CacheStart) <= 64, "start record");
+    SegRec* handed = reinterpret_cast<SegRec*>(smem + C::kOffSeg);
+    int* starts = reinterpret_cast<int*>(smem + C::kOffStarts);
+    CacheGroups* groups = reinterpret_cast<CacheGroups*>(smem + C::kOffGroups);
+    static_assert(C::kSmemNeed <= 227 * 1024, "shared memory of a CTA");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -135,22 +153,56 @@ __global__ void __launch_bounds__(576, 1)
         mbar_init(bar(B_DRAIN), 1);
         mbar_init(bar(B_COMBINE), 8);
         for (int q = 0; q < 8; ++q) mbar_init(bar(B_XCH + q), 2);
-        mbar_init(bar(B_PART), C::kSoftWarps);
-        mbar_init(bar(B_FLAG), 1);
+        mbar_init(bar(B_SEG_FULL), 1);
+        mbar_init(bar(B_SEG_EMPTY), C::kSoftWarps + 2);
         *abort_flag = 0;
         fence_barrier_init();
+    }
+    if (threadIdx.x >= 64 && threadIdx.x < 96) {
+        // the smallest r with (1 + r)^2 >= 2^b: the root's integer part is within one of it
+        int r = int(sqrtf(exp2f(float(lane))));
+        r = max(r - 2, 0);
+        while ((long long)(1 + r) * (1 + r) < (1LL << lane)) ++r;
+        starts[lane] = r;
     }
     if (warp == C::kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
-    cache_start<C::kPair, C::BN>(p, start, reinterpret_cast<long long*>(smem));  // (Q's memory as scratch)
+    float* near_tab = reinterpret_cast<float*>(smem + C::kOffNear);
+    const bool near_ok = BIAS && p.H <= kNearHeads;
+    if (near_ok)
+        for (int e = threadIdx.x; e < p.H * kNear; e += C::kThreads)
+            near_tab[(e / kNear) * kNearStride + e % kNear] = p.bias[(e / kNear) * 32 + relpos_bucket(e % kNear)] * 1.4426950408889634f;
+    cache_pieces<C::BN>(p, groups);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    CacheCursor<C::kPair, C::BN> cur(*start);
     CacheSeg g;
+    int first = 0, last = 0, part_slot = 0;
+    uint32_t seg_no = 0;
+    // The next part of an item (false: no more, or the CTA gave up).
+    auto next = [&]() -> bool {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_SEG_FULL), seg_no & 1, abort_flag))) return false;
+        const SegRec r = *handed;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_SEG_EMPTY));
+        ++seg_no;
+        if (r.b < 0) return false;
+        g.b = r.b;
+        g.hk = r.hk;
+        g.tile = r.tile;
+        g.s = CacheSeq{r.q0, r.q_len, r.kv_len};
+        g.r = cache_range<C::BN>(p, g.s, g.tile);
+        g.units = max(1, g.r.n);
+        g.k0 = r.k0;
+        g.k1 = r.k1;
+        first = r.first;
+        last = r.last;
+        part_slot = r.slot;
+        return true;
+    };
 
     auto fail = [&]() {
         *abort_flag = 1;
@@ -177,30 +229,18 @@ __global__ void __launch_bounds__(576, 1)
         auto wwait = [&](int b, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag));
         };
-        while (ok && cur.next(p, g)) {
+        while (ok && next()) {
             if (g.r.n == 0) continue;
             if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
             {
-                // Q: row r of the pair (token r / g, head r % g) to row r % 128 of its tile
-                constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte pieces of a row; rows per pass
-                const int c = lane % kChunks, R = g.s.q_len * p.g, r0 = g.tile * C::kPair;
-                const int n = min(C::kPair, (min(R - r0, C::kPair) + C::BM - 1) / C::BM * C::BM);
-                int r = lane / kChunks, tok = (r0 + r) / p.g, h = r0 + r - tok * p.g;
-                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q);
-                for (; r < n; r += kStep) {
-                    const bool in = r0 + r < R;
-                    const __nv_bfloat16* src =
-                        in ? q + (g.s.q0 + tok) * p.q_stride + int64_t(g.hk * p.g + h) * D + 8 * c : q;
-                    const int row = r & (C::BM - 1);
-                    cp_async16(sQ + uint32_t((r / C::BM) * C::kQBytes + (c >> 3) * C::BM * 128 + row * 128 +
-                                             (((c & 7) ^ (row & 7)) << 4)),
-                               src, in);
-                    h += kStep;
-                    while (h >= p.g) {
-                        h -= p.g;
-                        ++tok;
-                    }
-                }
+                // a box per tile and column block; tokens past the sequence's are not stored
+                const int tiles = (2 * g.tile + 1) * p.tile_tokens < g.s.q_len ? 2 : 1;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar(B_Q_FULL), uint32_t(tiles * C::kCB * p.tile_tokens * p.g * 128));
+                __syncwarp();
+                if (lane < tiles * C::kCB)
+                    tma_load_3d(sQ + (lane / C::kCB) * C::kQBytes + (lane % C::kCB) * C::BM * 128, &tmQ, bar(B_Q_FULL),
+                                (lane % C::kCB) * 64, g.hk * p.g, g.s.q0 + (2 * g.tile + lane / C::kCB) * p.tile_tokens);
             }
             ++item_it;
             int page = page_of(g, g.k0);
@@ -217,19 +257,64 @@ __global__ void __launch_bounds__(576, 1)
                 if (lane == 0) mbar_arrive_expect_tx(bar(B_V_FULL + st), bytes);
                 __syncwarp();
                 if (at >= 0) tma_load_4d(sV + st * C::kKVBytes + box, &tmV, bar(B_V_FULL + st), cb * 64, slot, g.hk, at);
-                if (k == g.k0) {  // Q has arrived by now, or nearly
-                    cp_async_wait_all();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_Q_FULL));
-                }
             }
         }
         if (!ok && lane == 0) fail();
-        cp_async_wait_all();
-        __syncwarp();
+        if (item_it > 0) mbar_wait_bounded(bar(B_Q_FULL), (item_it - 1) & 1, nullptr);
         drain_ring(bar(B_K_FULL), kv_it + k_extra, 2);
         drain_ring(bar(B_V_FULL), kv_it, 2);
+    } else if (warp == C::kDrawWarp) {
+        // ------------------------------------------------------------ work
+        const int ng = (p.B + 31) >> 5, pieces = groups->pieces, whole = groups->items_whole, blk = groups->blk;
+        const long long cut = groups->cut;
+        bool ok = true;
+        // Waits until the part handed out last has been taken by every warp, so that a CTA
+        // holds one part beside the one it works on, and draws no more than it can work off.
+        auto taken = [&]() {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(B_SEG_EMPTY), (seg_no & 1) ^ 1, abort_flag));
+            return ok;
+        };
+        auto hand_out = [&](const SegRec& r) {
+            if (lane == 0) {
+                *handed = r;
+                mbar_arrive(bar(B_SEG_FULL));
+            }
+            __syncwarp();
+            ++seg_no;
+        };
+        int w = blockIdx.x;
+        while (w < pieces) {
+            CacheStart st;
+            if (w < whole) {
+                st = cache_find_item<C::BN>(p, *groups, ng, w, lane);
+                st.u_end = st.u + (1LL << 40);  // (one item, all of its units)
+            } else {
+                const long long u = cut + (long long)(w - whole) * blk;
+                st = cache_find_unit<C::BN>(p, *groups, ng, u, lane);
+                st.u_end = min(groups->total, u + blk);
+            }
+            CacheCursor<C::BN> cur(st);
+            while (cur.next(p, g) && taken()) {
+                SegRec r{g.b, g.hk, g.tile, g.k0, g.k1, g.s.q0, g.s.q_len, g.s.kv_len, 0, 0, 0, 0};
+                if (w >= whole) {
+                    r.first = int(div_ll(g.first - cut, blk));
+                    r.last = int(div_ll(g.first + g.units - 1 - cut, blk));
+                    r.slot = cache_slot(w - whole, r.first);
+                }
+                hand_out(r);
+                if (w < whole) break;
+            }
+            if (!taken()) break;
+            if (lane == 0) w = int(gridDim.x + atomicAdd(p.counters + kCtrDrawn, 1u));
+            w = __shfl_sync(0xffffffffu, w, 0);
+        }
+        if (taken()) hand_out(SegRec{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
+        if (!ok && lane == 0) fail();
+        // the last CTA to have drawn its last piece leaves the counters zero
+        if (lane == 0 && atomicAdd(p.counters + kCtrDone, 1u) == gridDim.x - 1) {
+            p.counters[kCtrDrawn] = 0u;
+            p.counters[kCtrDone] = 0u;
+        }
     } else if (warp == C::kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         auto wwait = [&](int b, uint32_t parity) -> bool {
@@ -292,7 +377,7 @@ __global__ void __launch_bounds__(576, 1)
             fence_proxy_async_smem();
             __syncwarp();
         };
-        while (ok && cur.next(p, g)) {
+        while (ok && next()) {
             if (g.r.n == 0) continue;
             const Steps s = steps_of(p, g);
             const int n = s.k1 - s.k0;
@@ -364,7 +449,7 @@ __global__ void __launch_bounds__(576, 1)
         const uint32_t tSt = tmem + lane_base + C::tmem_s(x);
         const uint32_t tS = tSt + uint32_t(HC * hf);
         const uint32_t tO = tmem + lane_base + C::tmem_o(x) + uint32_t(OC * hf);
-        uint32_t s_cnt = 0, split_cnt = 0, x_cnt = 0, part_cnt = 0;
+        uint32_t s_cnt = 0, split_cnt = 0, x_cnt = 0;
         float* comb_s = reinterpret_cast<float*>(smem + C::kOffComb);
         float* xch_s = reinterpret_cast<float*>(smem + C::kOffXch);
         auto wwait = [&](int b, uint32_t parity) -> bool {
@@ -389,25 +474,19 @@ __global__ void __launch_bounds__(576, 1)
         };
         const float xs = p.scale_log2;
         bool ok = true;
-        while (ok && cur.next(p, g)) {
+        while (ok && next()) {
             const Steps sp = steps_of(p, g);
             const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len;
             const int n = sp.count(x);
             const int first_k = sp.split ? sp.k0 + x : sp.a[x], stride_k = sp.split ? 2 : 1;
-            const int row = (2 * g.tile + (sp.split ? 0 : x)) * C::BM + t;  // packed row
-            const bool row_valid = row < R;
-            const int rc = min(row, R - 1), tok = rc / p.g, head = g.hk * p.g + rc - tok * p.g;
+            const int rt = p.tile_tokens * p.g;                      // packed rows of a tile
+            const int row = (2 * g.tile + (sp.split ? 0 : x)) * rt + t;  // packed row
+            const bool row_valid = t < rt && row < R;
+            const int rc = min(row, R - 1), tok = div_g(p, rc), head = g.hk * p.g + rc - tok * p.g;
             const int rel = tok + diag;  // position of the row: rows past the end repeat the last one's masks
             const int t0 = __shfl_sync(0xffffffffu, tok, 0), t31 = __shfl_sync(0xffffffffu, tok, 31);
             const float* brow = BIAS ? p.bias + head * 32 : nullptr;
             const size_t orow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(head);
-            float bmax = 0.f;
-            if (BIAS) {
-                bmax = -INFINITY;
-#pragma unroll 8
-                for (int i = 0; i < 32; ++i) bmax = fmaxf(bmax, __ldg(brow + i));
-                bmax *= 1.4426950408889634f;
-            }
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i) {
                 const int col0 = (g.r.f + first_k + i * stride_k) * C::BN;
@@ -416,7 +495,8 @@ __global__ void __launch_bounds__(576, 1)
                 const int lo = p.window >= 0 ? rel - p.window - col0 : 0;
                 const bool full = __all_sync(0xffffffffu, lim >= C::BN && lo <= 0);
                 // Bias per 32-column chunk: one value per row when every row's positions of
-                // the chunk share a bucket, else looked up per element.
+                // the chunk share a bucket, else three values a row, or near the row's own
+                // position a table's.
                 uint32_t hmask = 3u;
                 float cb[2] = {0.f, 0.f};
                 if (BIAS) {
@@ -447,11 +527,31 @@ __global__ void __launch_bounds__(576, 1)
                             r[e + 1] = __float_as_uint(t2.y);
                         }
                     } else {
-                        const int rk = rel - col0 - 32 * kk;
+                        const int rk = rel - col0 - 32 * kk;  // relative position of the chunk's first column
+                        const bool back = __all_sync(0xffffffffu, rk >= kThreeBuckets);
+                        if (back || __all_sync(0xffffffffu, rk <= -31)) {
+                            const int b0 = relpos_bucket(rk), s = back ? -1 : 1;
+                            const int b1 = min(b0 + s, 31), b2 = min(b0 + 2 * s, 31);
+                            // columns before e1 lie in b0, before e2 in b1
+                            const int e1 = back ? rk - starts[b0] + 1 : starts[b1] + rk;
+                            const int e2 = back ? rk - starts[b1] + 1 : (b1 == b0 ? 32 : starts[b2] + rk);
+                            const float v0 = fmaf(__ldg(brow + b0), 1.4426950408889634f, -shift);
+                            const float v1 = fmaf(__ldg(brow + b1), 1.4426950408889634f, -shift);
+                            const float v2 = fmaf(__ldg(brow + b2), 1.4426950408889634f, -shift);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float bv = __ldg(brow + relpos_bucket(rk - e));
-                            r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), xs, fmaf(bv, 1.4426950408889634f, -shift)));
+                            for (int e = 0; e < 32; ++e)
+                                r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), xs, e < e1 ? v0 : e < e2 ? v1 : v2));
+                        } else if (near_ok) {
+                            const float* tab = near_tab + head * kNearStride;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), xs, tab[abs(rk - e)] - shift));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float bv = __ldg(brow + relpos_bucket(rk - e));
+                                r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), xs, fmaf(bv, 1.4426950408889634f, -shift)));
+                            }
                         }
                     }
                     if (!full) {
@@ -462,13 +562,19 @@ __global__ void __launch_bounds__(576, 1)
                 };
                 tmem_ld_wait(sr[0]);
                 tmem_ld_wait(sr[1]);
-                // pass 1: an upper bound of this half's row maximum from the raw scores
+                // pass 1: this half's row maximum, from the raw scores where the bias is one value
                 float mx = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int kk = 2 * hf + k;
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if (full) {
+                    const bool vary = BIAS && !(hmask & (1u << k));
+                    if (vary) {
+                        to_x(sr[k], k, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1]));
+                    } else if (full) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
                             m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1]));
@@ -479,7 +585,7 @@ __global__ void __launch_bounds__(576, 1)
                             m4[e & 3] = fmaxf(m4[e & 3], (e >= lok && e < lk) ? __uint_as_float(sr[k][e]) : -INFINITY);
                     }
                     const float mk = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    mx = fmaxf(mx, fmaf(mk, xs, (hmask & (1u << k)) ? cb[k] : bmax));
+                    mx = fmaxf(mx, vary ? mk : fmaf(mk, xs, cb[k]));
                 }
                 float mo;
                 if (!exchange(mx, mo)) { ok = false; break; }
@@ -632,84 +738,36 @@ __global__ void __launch_bounds__(576, 1)
                     p.lse[orow] = lt > 0.f ? (m + __log2f(lt)) * 0.6931471805599453f : -INFINITY;
                 continue;
             }
-            // An item split over CTAs: leave this part, count it, and the last one to arrive
-            // adds them all up in the order of the keys.
-            const int first = cache_cta_of(*start, g.first), last = cache_cta_of(*start, g.first + g.units - 1);
-            const int prow = sp.split ? t : x * C::BM + t;  // row of the pair
+            // An item cut between blocks: leave this part, and with the first one the record
+            // by which the merge kernel finds the item.
+            const int prow = sp.split ? t : x * rt + t;  // row of the item
             if (owner) {
-                float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
+                float* part = p.part + size_t(part_slot) * C::kPart;
                 float4* po = reinterpret_cast<float4*>(part);
                 if (n > 0) {
 #pragma unroll
                     for (int c = 0; c < OC / 32; ++c) {
                         float v[32];
                         load_o(c, 1.f, v);
+                        if (row_valid) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            po[((OC * hf + 32 * c) / 4 + e) * C::kPair + prow] =
-                                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            for (int e = 0; e < 8; ++e)
+                                po[((OC * hf + 32 * c) / 4 + e) * C::kPair + prow] =
+                                    make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        }
                     }
                     release();
                 }
-                if (hf == 0) {
+                if (hf == 0 && row_valid) {
                     part[C::kPair * D + prow] = m;
                     part[C::kPair * D + C::kPair + prow] = n > 0 ? lt : 0.f;
                 }
-                __threadfence();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_PART));
-            if (threadIdx.x == 0) {
-                int done = 0;
-                if (mbar_wait_bounded(bar(B_PART), part_cnt & 1, abort_flag)) {
-                    __threadfence();
-                    done = atomicAdd(p.counters + first, 1u) == uint32_t(last - first);
-                    if (done) p.counters[first] = 0u;  // every part has arrived: ready for the next call
-                    __threadfence();
-                }
-                *last_flag = done;
-                mbar_arrive(bar(B_FLAG));
+            if (threadIdx.x < kMergeCtas && g.k0 == 0) {
+                if (threadIdx.x == 0)
+                    p.cuts[first] = CacheCut{g.s.q0, min(2 * rt, R - 2 * g.tile * rt), 2 * g.tile * rt, g.hk * p.g, first, last, {0, 0}};
+                p.cut_flags[first * kMergeCtas + threadIdx.x] = 1u;
             }
-            __syncwarp();
-            if (!wwait(B_FLAG, part_cnt & 1)) { ok = false; break; }
-            ++part_cnt;
-            if (!*last_flag || !owner) continue;
-            const float* pm = p.part + C::kPair * D + prow;
-            float mm = -INFINITY, ll = 0.f;
-#pragma unroll 4
-            for (int c = first; c <= last; ++c) mm = fmaxf(mm, __ldcg(pm + size_t(cache_slot(c, first)) * C::kPart));
-#pragma unroll 4
-            for (int c = first; c <= last; ++c) {
-                const float* q = pm + size_t(cache_slot(c, first)) * C::kPart;
-                const float mc = __ldcg(q);
-                ll = fmaf(__ldcg(q + C::kPair), mc == -INFINITY ? 0.f : ex2_approx(mc - mm), ll);
-            }
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
-#pragma unroll 1
-            for (int c8 = 0; c8 < OC / 16; ++c8) {
-                float v[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = 0.f;
-#pragma unroll 2
-                for (int c = first; c <= last; ++c) {
-                    const float* q = p.part + size_t(cache_slot(c, first)) * C::kPart;
-                    const float mc = __ldcg(q + C::kPair * D + prow);
-                    if (mc == -INFINITY) continue;  // no key of this part: its O is not set
-                    const float w = ex2_approx(mc - mm) * inv;
-                    const float4* q4 = reinterpret_cast<const float4*>(q) + ((OC * hf) / 4 + 4 * c8) * C::kPair + prow;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 u = __ldcg(q4 + e * C::kPair);
-                        v[4 * e] = fmaf(u.x, w, v[4 * e]);
-                        v[4 * e + 1] = fmaf(u.y, w, v[4 * e + 1]);
-                        v[4 * e + 2] = fmaf(u.z, w, v[4 * e + 2]);
-                        v[4 * e + 3] = fmaf(u.w, w, v[4 * e + 3]);
-                    }
-                }
-                put(OC * hf + 16 * c8, v, 16);
-            }
-            if (row_valid && p.lse && hf == 0)
-                p.lse[orow] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
         }
         if (!ok && lane == 0) fail();
     }
@@ -720,23 +778,88 @@ __global__ void __launch_bounds__(576, 1)
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// Adds up the parts of the items cut between blocks: CTA (i, j) takes rows 64 j .. 64 j + 63
+// of the item that starts in block i and goes on past it, if there is one (its flag, which
+// the CTA clears for the next call).  A thread takes one row and a quarter of the columns;
+// a warp's loads are whole lines, since parts are stored four columns of all rows at a time.
+template <int D>
+__global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdParams p) {
+    using C = ChkCfg<D>;
+    __shared__ uint32_t there;
+    if (threadIdx.x == 0) {
+        uint32_t* flag = p.cut_flags + blockIdx.x * kMergeCtas + blockIdx.y;
+        there = *flag;
+        if (there) *flag = 0u;
+    }
+    __syncthreads();
+    if (!there) return;
+    const CacheCut cut = p.cuts[blockIdx.x];
+    const int row = 64 * blockIdx.y + (threadIdx.x & 63), quarter = threadIdx.x >> 6;
+    if (row >= cut.rows) return;
+    const int first = cut.first, last = cut.last;
+    const float* pm = p.part + C::kPair * D + row;
+    float mm = -INFINITY;
+#pragma unroll 8
+    for (int c = first; c <= last; ++c) mm = fmaxf(mm, pm[size_t(cache_slot(c, first)) * C::kPart]);
+    constexpr int NV = D / 16;  // float4s of a thread
+    float ll = 0.f;
+    float4 v[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = first; c <= last; ++c) {
+        const float* q = p.part + size_t(cache_slot(c, first)) * C::kPart;
+        const float mc = q[C::kPair * D + row], lc = q[C::kPair * D + C::kPair + row];
+        const float w = mc == -INFINITY ? 0.f : ex2_approx(mc - mm);
+        const float4* q4 = reinterpret_cast<const float4*>(q) + quarter * NV * C::kPair + row;
+        ll = fmaf(lc, w, ll);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            float4 u = q4[e * C::kPair];
+            if (mc == -INFINITY) u = make_float4(0.f, 0.f, 0.f, 0.f);  // no key of this part: its O is not set
+            v[e].x = fmaf(u.x, w, v[e].x);
+            v[e].y = fmaf(u.y, w, v[e].y);
+            v[e].z = fmaf(u.z, w, v[e].z);
+            v[e].w = fmaf(u.w, w, v[e].w);
+        }
+    }
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const int r = cut.row0 + row, tok = div_g(p, r);
+    const size_t orow = size_t(cut.q0 + tok) * size_t(p.H) + size_t(cut.head0 + r - tok * p.g);
+    if (p.o_f32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + quarter * (D / 4));
+#pragma unroll
+        for (int e = 0; e < NV; ++e) dst[e] = make_float4(v[e].x * inv, v[e].y * inv, v[e].z * inv, v[e].w * inv);
+    } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + orow * D + quarter * (D / 4));
+#pragma unroll
+        for (int e = 0; e < NV; e += 2)
+            dst[e / 2] = make_uint4(pack_bf16x2(v[e].x * inv, v[e].y * inv), pack_bf16x2(v[e].z * inv, v[e].w * inv),
+                                    pack_bf16x2(v[e + 1].x * inv, v[e + 1].y * inv),
+                                    pack_bf16x2(v[e + 1].z * inv, v[e + 1].w * inv));
+    }
+    if (p.lse && quarter == 0) p.lse[orow] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+}
+
 template <int D, bool BIAS>
-cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(jfa_cache_chunk_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          ChkCfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    jfa_cache_chunk_kernel<D, BIAS><<<num_sms, ChkCfg<D>::kThreads, ChkCfg<D>::kSmemBytes, st>>>(mk, mv, p);
+    jfa_cache_chunk_kernel<D, BIAS><<<num_sms, ChkCfg<D>::kThreads, ChkCfg<D>::kSmemBytes, st>>>(mq, mk, mv, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    jfa_cache_merge_kernel<D><<<dim3(num_sms * kBlocksPerCta, kMergeCtas), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t cache_chunk_part_bytes(int D, int num_sms) { return size_t(num_sms) * 2 * 256 * size_t(D + 2) * 4; }
+size_t cache_chunk_part_bytes(int D, int num_sms) { return size_t(num_sms) * kBlocksPerCta * 2 * 256 * size_t(D + 2) * 4; }
 
-cudaError_t launch_cache_chunk(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
-                               cudaStream_t st) {
-    if (D == 128) return p.bias ? launch<128, true>(mk, mv, p, num_sms, st) : launch<128, false>(mk, mv, p, num_sms, st);
-    return p.bias ? launch<64, true>(mk, mv, p, num_sms, st) : launch<64, false>(mk, mv, p, num_sms, st);
+cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    if (D == 128) return p.bias ? launch<128, true>(mq, mk, mv, p, num_sms, st) : launch<128, false>(mq, mk, mv, p, num_sms, st);
+    return p.bias ? launch<64, true>(mq, mk, mv, p, num_sms, st) : launch<64, false>(mq, mk, mv, p, num_sms, st);
 }
 
 }  // namespace jfa

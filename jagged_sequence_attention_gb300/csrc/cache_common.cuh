@@ -2,7 +2,7 @@
 //
 // The new tokens of sequence b and the g = H / Hkv query heads of one key head hk form
 // R_b = q_len_b * g packed rows (row r: token r / g, head hk * g + r % g), so grouped heads
-// share every key and value read.  Rows are cut into tiles of BM, keys into tiles of BN; an
+// share every key and value read.  Rows are cut into tiles of p.bm, keys into tiles of BN; an
 // item is a (sequence, key head, row tile) and its units are the key tiles it visits (at
 // least one, so that rows without a key still get their zeros).
 //
@@ -19,12 +19,30 @@
 
 namespace jfa {
 
+constexpr int kCacheMaxB = 1 << 14, kCacheMaxGroups = kCacheMaxB / 32;
+constexpr int kBlocksPerCta = 4;  // chunk kernel: blocks of the last part of the work, per CTA
+constexpr int kMergeCtas = 4;     // CTAs that merge a cut item of it
+constexpr int kMaxSms = 320;
+// Words of the workspace's zeroed part: pieces drawn and CTAs done (chunk kernel), arrivals of
+// split items (the other kernels, at most 3 CTAs an SM), flags of cut items (chunk kernel).
+constexpr int kCtrDrawn = 0, kCtrDone = 1, kCtrSplit = 64, kCtrCuts = kCtrSplit + 3 * kMaxSms,
+              kCtrEnd = kCtrCuts + kMaxSms * kBlocksPerCta * kMergeCtas;
+static_assert(kCtrEnd * 4 <= JFA_CACHE_ZERO_BYTES, "counters fit the zeroed part");
+
+// An item cut between blocks: `rows` packed rows from row0 on of the sequence at q0, heads
+// from head0 on, blocks first .. last.
+struct CacheCut {
+    int q0, rows, row0, head0, first, last;
+    int pad[2];
+};
+
 struct CacheFwdParams {
     const int32_t* q_off;    // [B+1]
     const int32_t* kv_lens;  // [B]
     const int32_t* table;    // [B, max_pages]
     int B, max_pages, T, max_kv;
     int H, Hkv, g;
+    uint32_t g_mul, g_shift; // division by g (div_g)
     int page_log2, n_pages;
     int causal, window;      // window: -1 none
     float scale_log2;        // scale * log2(e)
@@ -37,16 +55,37 @@ struct CacheFwdParams {
     const void* K;
     const void* V;
     int64_t ks[3], vs[3];    // page, slot, head strides (elements)
-    uint32_t* counters;      // workspace: arrivals per split item (zero between calls)
-    float* part;             // workspace: partial results, two slots per CTA
+    uint32_t* counters;      // workspace: arrivals per split item, pieces drawn (zero between calls)
+    uint32_t* cut_flags;     // workspace (zero between calls): [block][kMergeCtas]
+    CacheCut* cuts;          // workspace: [block]
+    float* part;             // workspace: partial results, two slots per CTA or block
     int* status;
     int min_units;           // units a CTA takes at least
     int row_lo, row_hi;      // sequences this launch works on: row_lo < q_len * g <= row_hi
+    int bm;                  // packed rows of an item
+    int tile_tokens;         // chunk kernel: tokens of one of an item's two tiles
 };
 
 struct CacheSeq {
     int q0, q_len, kv_len;
 };
+
+// r / g for 0 <= r < 2^31, by a multiplication: with l = ceil(log2 g) and
+// g_mul = floor(2^32 (2^l - g) / g) + 1, floor(r / g) = (hi32(r g_mul) + r) >> l exactly
+// (Granlund and Montgomery 1994; the sum fits 32 bits since r < 2^31).
+__host__ inline void set_div_g(CacheFwdParams& p) {
+    uint32_t l = 0;
+    while ((1u << l) < uint32_t(p.g)) ++l;
+    p.g_shift = l;
+    p.g_mul = uint32_t((uint64_t(1) << 32) * ((uint64_t(1) << l) - uint64_t(p.g)) / uint64_t(p.g)) + 1u;
+}
+__device__ __forceinline__ int div_g(const CacheFwdParams& p, int r) {
+    return int((__umulhi(uint32_t(r), p.g_mul) + uint32_t(r)) >> p.g_shift);
+}
+// a / b for non-negative values, in 32 bits where they fit (as they nearly always do).
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)(uint32_t(a) / uint32_t(b));
+}
 
 // Sequence b's lengths; a bad sequence reads as empty.  In bad: whether it is one.
 __device__ __forceinline__ CacheSeq cache_seq(const CacheFwdParams& p, int b, bool& bad) {
@@ -61,21 +100,25 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheFwdParams& p, int b, bo
 struct CacheRange {
     int lo, hi, f, n;
 };
-template <int BM, int BN>
-__device__ __forceinline__ CacheRange cache_range(const CacheFwdParams& p, const CacheSeq& s, int tile) {
-    const int r0 = tile * BM, r1 = min(s.q_len * p.g, r0 + BM) - 1;
+template <int BN>
+__device__ __forceinline__ CacheRange cache_range(const CacheFwdParams& p, const CacheSeq& s, int tile, int bm) {
+    const int r0 = tile * bm, r1 = min(s.q_len * p.g, r0 + bm) - 1;
     const int diag = s.kv_len - s.q_len;
     CacheRange k;
-    k.hi = p.causal ? max(0, min(s.kv_len, r1 / p.g + diag + 1)) : s.kv_len;
-    k.lo = p.window >= 0 ? max(0, r0 / p.g + diag - p.window) : 0;
+    k.hi = p.causal ? max(0, min(s.kv_len, div_g(p, r1) + diag + 1)) : s.kv_len;
+    k.lo = p.window >= 0 ? max(0, div_g(p, r0) + diag - p.window) : 0;
     k.f = k.lo / BN;
     k.n = k.hi > k.lo ? (k.hi - 1) / BN + 1 - k.f : 0;
     return k;
 }
 
-template <int BM>
+template <int BN>
+__device__ __forceinline__ CacheRange cache_range(const CacheFwdParams& p, const CacheSeq& s, int tile) {
+    return cache_range<BN>(p, s, tile, p.bm);
+}
+
 __device__ __forceinline__ int cache_tiles(const CacheFwdParams& p, const CacheSeq& s) {
-    return (s.q_len * p.g + BM - 1) / BM;
+    return int(uint32_t(s.q_len * p.g + p.bm - 1) / uint32_t(p.bm));
 }
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
@@ -94,26 +137,26 @@ __device__ __forceinline__ long long warp_scan_ll(long long v, int lane) {  // i
 
 // Units of one key head of sequence 32 c + lane, by the whole warp: a lane counts the tiles
 // of its own short sequence, and the warp together those of a long one.
-template <int BM, int BN>
+template <int BN>
 __device__ long long cache_seq_units(const CacheFwdParams& p, int c, int lane, bool report) {
     const int b = 32 * c + lane;
     CacheSeq s{0, 0, 0};
     bool bad = false;
     if (b < p.B) s = cache_seq(p, b, bad);
     if (bad && report) atomicOr(p.status, kStatusBounds);
-    const int nt = cache_tiles<BM>(p, s);
+    const int nt = cache_tiles(p, s);
     long long u = 0;
-    const bool heavy = nt > 4;
+    const bool heavy = nt > 32;
     if (!heavy)
-        for (int t = 0; t < nt; ++t) u += max(1, cache_range<BM, BN>(p, s, t).n);
+        for (int t = 0; t < nt; ++t) u += max(1, cache_range<BN>(p, s, t).n);
     uint32_t todo = __ballot_sync(0xffffffffu, heavy);
     while (todo) {
         const int l = __ffs(todo) - 1;
         todo &= todo - 1;
         const CacheSeq h{0, __shfl_sync(0xffffffffu, s.q_len, l), __shfl_sync(0xffffffffu, s.kv_len, l)};
-        const int hn = cache_tiles<BM>(p, h);
+        const int hn = cache_tiles(p, h);
         long long v = 0;
-        for (int t = lane; t < hn; t += 32) v += max(1, cache_range<BM, BN>(p, h, t).n);
+        for (int t = lane; t < hn; t += 32) v += max(1, cache_range<BN>(p, h, t).n);
         v = warp_sum_ll(v);
         if (lane == l) u = v;
     }
@@ -130,12 +173,12 @@ struct CacheStart {
 
 // By every thread of the CTA (blockDim.x a multiple of 32).  sums: shared scratch of
 // ceil(B / 32) values.
-template <int BM, int BN>
+template <int BN>
 __device__ void cache_start(const CacheFwdParams& p, CacheStart* out, long long* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int chunks = (p.B + 31) >> 5;
     for (int c = warp; c < chunks; c += warps) {
-        const long long v = warp_sum_ll(cache_seq_units<BM, BN>(p, c, lane, blockIdx.x == 0));
+        const long long v = warp_sum_ll(cache_seq_units<BN>(p, c, lane, blockIdx.x == 0));
         if (lane == 0) sums[c] = v * p.Hkv;
     }
     __syncthreads();
@@ -144,11 +187,11 @@ __device__ void cache_start(const CacheFwdParams& p, CacheStart* out, long long*
         for (int c = lane; c < chunks; c += 32) total += sums[c];
         total = warp_sum_ll(total);
         CacheStart st{0, 0, 0, 0, 0, 0, 0, 0};
-        const long long want = (total + p.min_units - 1) / p.min_units;
+        const long long want = div_ll(total + p.min_units - 1, p.min_units);
         const int G = int(min((long long)(gridDim.x), max(want, 1LL)));
         const int cta = blockIdx.x;
         if (cta < G && total > 0) {
-            st.base = total / G;
+            st.base = div_ll(total, G);
             st.rem = int(total - st.base * G);
             st.u = cta * st.base + min(cta, st.rem);
             st.u_end = st.u + st.base + (cta < st.rem ? 1 : 0);
@@ -168,19 +211,19 @@ __device__ void cache_start(const CacheFwdParams& p, CacheStart* out, long long*
                 }
                 left -= __shfl_sync(0xffffffffu, inc, 31);
             }
-            const long long one = cache_seq_units<BM, BN>(p, c, lane, false);
+            const long long one = cache_seq_units<BN>(p, c, lane, false);
             const long long inc = warp_scan_ll(one * p.Hkv, lane);
             const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
             left -= __shfl_sync(0xffffffffu, inc - one * p.Hkv, l);
             st.b = 32 * c + l;
             const long long per = __shfl_sync(0xffffffffu, one, l);
-            st.hk = int(left / per);
+            st.hk = int(div_ll(left, per));
             left -= st.hk * per;
             bool bad;
             const CacheSeq s = cache_seq(p, st.b, bad);
-            const int nt = cache_tiles<BM>(p, s);
+            const int nt = cache_tiles(p, s);
             for (int t0 = 0; t0 < nt; t0 += 32) {
-                const long long n = t0 + lane < nt ? max(1, cache_range<BM, BN>(p, s, t0 + lane).n) : 0;
+                const long long n = t0 + lane < nt ? max(1, cache_range<BN>(p, s, t0 + lane).n) : 0;
                 const long long in = warp_scan_ll(n, lane);
                 const uint32_t m = __ballot_sync(0xffffffffu, in > left);
                 if (m) {
@@ -208,7 +251,7 @@ struct CacheSeg {
 };
 
 // Walks a CTA's range.  Every role of a CTA walks its own copy.
-template <int BM, int BN>
+template <int BN>
 struct CacheCursor {
     CacheStart st;
     CacheSeq s;
@@ -221,13 +264,13 @@ struct CacheCursor {
             if (st.b >= p.B) return false;
             bool bad;
             s = cache_seq(p, st.b, bad);
-            nt = cache_tiles<BM>(p, s);
+            nt = cache_tiles(p, s);
         }
         g.b = st.b;
         g.hk = st.hk;
         g.tile = st.tile;
         g.s = s;
-        g.r = cache_range<BM, BN>(p, s, st.tile);
+        g.r = cache_range<BN>(p, s, st.tile);
         g.units = max(1, g.r.n);
         g.k0 = st.kt;
         g.k1 = int(min((long long)(g.units), st.kt + (st.u_end - st.u)));
@@ -248,7 +291,164 @@ struct CacheCursor {
 // The CTA that holds unit u.
 __device__ __forceinline__ int cache_cta_of(const CacheStart& st, long long u) {
     const long long head = st.rem * (st.base + 1);
-    return u < head ? int(u / (st.base + 1)) : st.rem + int((u - head) / st.base);
+    return u < head ? int(div_ll(u, st.base + 1)) : st.rem + int(div_ll(u - head, st.base));
+}
+
+// ------------------------------------------------------------------ work drawn in order
+//
+// The chunk kernel's CTAs draw their work one piece at a time from a counter, so that the
+// pieces in flight are neighbours (row tiles of one key head, reading the same keys out of
+// L2) and no CTA is left with more than its share.  The pieces are whole items, in order,
+// while much work remains, and near the end blocks of `blk` units, which may cut items; the
+// cut items' parts, numbered by block, are merged by a second kernel.  Which units form a piece
+// depends on the lengths alone, so results do not depend on who draws what.
+struct CacheGroups {      // shared memory
+    long long units[kCacheMaxGroups];  // units before the group of 32 sequences
+    int32_t items[kCacheMaxGroups];    // items before it
+    long long total, cut;  // units; the first `items_whole` items are units [0, cut)
+    int32_t items_whole, blk, pieces;
+    int32_t longest;       // units of the longest item
+};
+
+// Lanes' exclusive prefix of the 32 sequences of group c: units and items of each.
+template <int BN>
+__device__ __forceinline__ void cache_group_lane(const CacheFwdParams& p, int c, int lane, bool report, long long& units,
+                                                 int& tiles) {
+    units = cache_seq_units<BN>(p, c, lane, report);
+    tiles = 0;
+    bool bad;
+    if (32 * c + lane < p.B) tiles = cache_tiles(p, cache_seq(p, 32 * c + lane, bad));
+}
+
+// The group of unit u (or item u): the last one starting at or before it.
+template <typename T>
+__device__ __forceinline__ int cache_find_group(const T* before, int groups, T u, int lane) {
+    int c = 0;
+    for (int c0 = 0; c0 < groups; c0 += 32) {
+        const uint32_t m = __ballot_sync(0xffffffffu, c0 + lane < groups && before[c0 + lane] <= u);
+        if (!m) break;
+        c = c0 + 31 - __clz(int(m));
+    }
+    return c;
+}
+
+// Unit u of the batch, by a whole warp: its item and the key tile within it; the item's
+// number in `item`.
+template <int BN>
+__device__ CacheStart cache_find_unit(const CacheFwdParams& p, const CacheGroups& G, int groups, long long u, int lane,
+                                      int* item = nullptr) {
+    CacheStart st{0, 0, 0, 0, u, u, 0, 0};
+    // (a group without units shares its successor's start, which the search prefers)
+    const int c = cache_find_group(G.units, groups, u, lane);
+    long long left = u - G.units[c], one;
+    int tiles;
+    cache_group_lane<BN>(p, c, lane, false, one, tiles);
+    const long long inc = warp_scan_ll(one * p.Hkv, lane);
+    const long long tinc = warp_scan_ll((long long)(tiles)*p.Hkv, lane);
+    const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
+    left -= __shfl_sync(0xffffffffu, inc - one * p.Hkv, l);
+    const long long before = __shfl_sync(0xffffffffu, tinc - (long long)(tiles)*p.Hkv, l);
+    const long long per = __shfl_sync(0xffffffffu, one, l);
+    st.b = 32 * c + l;
+    st.hk = int(div_ll(left, per));
+    left -= st.hk * per;
+    bool bad;
+    const CacheSeq s = cache_seq(p, st.b, bad);
+    const int nt = cache_tiles(p, s);
+    for (int t0 = 0; t0 < nt; t0 += 32) {
+        const long long n = t0 + lane < nt ? max(1, cache_range<BN>(p, s, t0 + lane).n) : 0;
+        const long long in = warp_scan_ll(n, lane);
+        const uint32_t m = __ballot_sync(0xffffffffu, in > left);
+        if (m) {
+            const int t = __ffs(m) - 1;
+            st.tile = t0 + t;
+            st.kt = int(left - __shfl_sync(0xffffffffu, in - n, t));
+            break;
+        }
+        left -= __shfl_sync(0xffffffffu, in, 31);
+    }
+    if (item) *item = G.items[c] + int(before) + st.hk * nt + st.tile;
+    return st;
+}
+
+// Item i of the batch, by a whole warp.
+template <int BN>
+__device__ CacheStart cache_find_item(const CacheFwdParams& p, const CacheGroups& G, int groups, int i, int lane) {
+    CacheStart st{0, 0, 0, 0, 0, 0, 0, 0};
+    const int c = cache_find_group(G.items, groups, i, lane);
+    long long left = i - G.items[c];
+    bool bad;
+    const int tiles = 32 * c + lane < p.B ? cache_tiles(p, cache_seq(p, 32 * c + lane, bad)) : 0;
+    const long long inc = warp_scan_ll((long long)(tiles)*p.Hkv, lane);
+    const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
+    left -= __shfl_sync(0xffffffffu, inc - (long long)(tiles)*p.Hkv, l);
+    const int nt = __shfl_sync(0xffffffffu, tiles, l);
+    st.b = 32 * c + l;
+    st.hk = int(div_ll(left, nt));
+    st.tile = int(left - (long long)(st.hk) * nt);
+    return st;
+}
+
+// The batch's pieces, by every thread of the CTA.  G.pieces is 0 for a batch without rows.
+template <int BN>
+__device__ void cache_pieces(const CacheFwdParams& p, CacheGroups* G) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int groups = (p.B + 31) >> 5;
+    if (threadIdx.x == 0) G->longest = 1;
+    __syncthreads();
+    for (int c = warp; c < groups; c += warps) {
+        long long u;
+        int tiles;
+        cache_group_lane<BN>(p, c, lane, blockIdx.x == 0, u, tiles);
+        if (tiles > 0) {  // a sequence's last item sees the most keys, but for a window's odd tile
+            bool bad;
+            const int n = cache_range<BN>(p, cache_seq(p, 32 * c + lane, bad), tiles - 1).n;
+            if (n > 1) atomicMax(&G->longest, n);
+        }
+        u = warp_sum_ll(u);
+        const long long t = warp_sum_ll(tiles);
+        if (lane == 0) {
+            G->units[c] = u * p.Hkv;
+            G->items[c] = int32_t(t * p.Hkv);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long u = 0, items = 0;
+        for (int c0 = 0; c0 < groups; c0 += 32) {  // sums to exclusive prefixes
+            const bool in = c0 + lane < groups;
+            const long long v = in ? G->units[c0 + lane] : 0, w = in ? G->items[c0 + lane] : 0;
+            const long long vi = warp_scan_ll(v, lane), wi = warp_scan_ll(w, lane);
+            if (in) {
+                G->units[c0 + lane] = u + vi - v;
+                G->items[c0 + lane] = int32_t(items + wi - w);
+            }
+            u += __shfl_sync(0xffffffffu, vi, 31);
+            items += __shfl_sync(0xffffffffu, wi, 31);
+        }
+        __syncwarp();
+        const long long grid = gridDim.x;
+        // The last part, cut in blocks, covers the spread with which the CTAs come out of the
+        // whole items: half an item each.
+        const long long rest = min(u, grid * (G->longest + 1) / 2);
+        long long cut = 0;
+        int whole = 0;
+        if (u > rest) {
+            const CacheStart st = cache_find_unit<BN>(p, *G, groups, u - rest, lane, &whole);
+            cut = u - rest - st.kt;
+        }
+        const long long left = u - cut;
+        const long long blk = left <= grid * 8 ? max(div_ll(left + grid - 1, grid), (long long)(p.min_units))
+                                               : max(8LL, div_ll(left + kBlocksPerCta * grid - 1, kBlocksPerCta * grid));
+        if (lane == 0) {
+            G->total = u;
+            G->cut = cut;
+            G->items_whole = whole;
+            G->blk = int32_t(blk);
+            G->pieces = whole + int32_t(left > 0 ? div_ll(left + blk - 1, blk) : 0);
+        }
+    }
+    __syncthreads();
 }
 
 // Partial results of split items: slot 0 of a CTA for the item that started in an earlier
@@ -256,6 +456,13 @@ __device__ __forceinline__ int cache_cta_of(const CacheStart& st, long long u) {
 // first part in slot 1 of `first`, the others in slot 0.
 __device__ __forceinline__ int cache_slot(int cta, int first_cta) { return 2 * cta + (cta == first_cta ? 1 : 0); }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
 // One box of the pages: elements x .., slots y .., head z, page w.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             int w) {
@@ -274,8 +481,9 @@ cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap&
                                 cudaStream_t st);
 size_t cache_decode_part_bytes(int D, int num_sms);
 // bf16, items of 256 packed rows: bound by the tensor cores and the exponentials.
-cudaError_t launch_cache_chunk(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
-                               cudaStream_t st);
+// mq: the queries as (D, head, token), boxes of 128 bytes x g heads x tile_tokens.
+cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_chunk_part_bytes(int D, int num_sms);
 
 struct CacheAppendParams {

@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         *abort_flag = 0;
         fence_barrier_init();
     }
-    cache_start<BM, BN>(p, start, reinterpret_cast<long long*>(smem));  // (the ring's memory as scratch)
-    CacheCursor<BM, BN> cur(*start);
+    cache_start<BN>(p, start, reinterpret_cast<long long*>(smem));  // (the ring's memory as scratch)
+    CacheCursor<BN> cur(*start);
     CacheSeg g;
 
     if (warp == kDecWarps) {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         for (int i = 0; i < 2; ++i) {
             const int rr = qrow + 8 * i;
             const bool in = rr < nr;
-            const int r = r0 + (in ? rr : 0), tok = r / p.g, head = g.hk * p.g + r - tok * p.g;
+            const int r = r0 + (in ? rr : 0), tok = div_g(p, r), head = g.hk * p.g + r - tok * p.g;
             rel[i] = tok + diag;
             lim[i] = p.causal ? min(g.s.kv_len, rel[i] + 1) : g.s.kv_len;
             low[i] = p.window >= 0 ? rel[i] - p.window : 0;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             }
         }
         // keys that every row of the tile sees: no mask in [all_lo, all_hi)
-        const int t_first = r0 / p.g, t_last = (r0 + nr - 1) / p.g;
+        const int t_first = div_g(p, r0), t_last = div_g(p, r0 + nr - 1);
         const int all_hi = p.causal ? min(g.s.kv_len, t_first + diag + 1) : g.s.kv_len;
         const int all_lo = p.window >= 0 ? max(0, t_last + diag - p.window) : 0;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[NT][4];
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             last = cache_cta_of(*start, g.first + g.units - 1);
         }
         float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
-        const int r = r0 + orow, tok = r / p.g;
+        const int r = r0 + orow, tok = div_g(p, r);
         const size_t grow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
         const bool out = orow < nr && ok;
         const float inv = ol > 0.f ? 1.f / ol : 0.f;
@@ -404,50 +404,106 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         if (threadIdx.x == 0) {
             int done = 0;
             if (ok) {
-                done = atomicAdd(p.counters + first, 1u) == uint32_t(last - first);
-                if (done) p.counters[first] = 0u;  // every part has arrived: ready for the next call
+                done = atomicAdd(p.counters + kCtrSplit + first, 1u) == uint32_t(last - first);
+                if (done) p.counters[kCtrSplit + first] = 0u;  // every part has arrived: ready for the next call
                 __threadfence();
             }
             *last_flag = done;
         }
         consumer_sync();
         if (!*last_flag) continue;
-        // The last part to arrive adds them all up, in the order of the keys.
-        if (orow < nr) {
+        // The last part to arrive adds them all up, in the order of the keys.  A warp takes a
+        // row's maxima and sums, its lanes the parts; the weights go to the slots' memory, at
+        // most kBatch parts at a time, and then a thread takes four columns of a row over the
+        // parts, with the parts dealt to several threads where there are few columns.
+        const int parts = last - first + 1, cols = nr * (D / 4);
+        constexpr int kBatch = 96;           // parts x 16 rows of weights: 6 of the slots' 8 KB
+        constexpr int kCols = BM * (D / 4) / (32 * kDecWarps);
+        float* wts = slots;                  // [part][16]
+        float* row_m = slots + kBatch * 16;  // [16], and the sums [16]
+        float* row_l = row_m + 16;
+        auto part_of = [&](int c) { return p.part + size_t(cache_slot(first + c, first)) * C::kPart; };
+        for (int rr = warp; rr < nr; rr += kDecWarps) {
             float mm = -INFINITY;
+            for (int c = lane; c < parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + BM * D + rr));
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+            float ll = 0.f;
+            for (int c = lane; c < parts; c += 32) {
+                const float mc = __ldcg(part_of(c) + BM * D + rr);
+                ll = fmaf(mc == -INFINITY ? 0.f : ex2_approx(mc - mm), __ldcg(part_of(c) + BM * D + BM + rr), ll);
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);
+            if (lane == 0) {
+                row_m[rr] = mm;
+                row_l[rr] = ll;
+            }
+        }
+        consumer_sync();
+        // columns: up to 4 per thread (nr = 16); threads per column: as many as fit
+        const int share = cols > 64 ? 1 : 32 * kDecWarps / cols, who = share > 1 ? threadIdx.x / cols : 0;
+        const int col0 = share > 1 ? threadIdx.x % cols : threadIdx.x;
+        float4 acc[kCols];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < parts; c0 += kBatch) {
+            const int n = min(kBatch, parts - c0);
+            for (int e = threadIdx.x; e < n * 16; e += 32 * kDecWarps) {
+                const int rr = e & 15;
+                const float mc = rr < nr ? __ldcg(part_of(c0 + (e >> 4)) + BM * D + rr) : -INFINITY;
+                wts[e] = mc == -INFINITY ? 0.f : ex2_approx(mc - row_m[rr]);
+            }
+            consumer_sync();
+            if (who < share) {
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) {
+                    const int col = col0 + k * 32 * kDecWarps, rr = col / (D / 4);
+                    if (col >= cols) break;
+                    const float* w = wts + rr;
 #pragma unroll 8
-            for (int c = first; c <= last; ++c)
-                mm = fmaxf(mm, __ldcg(p.part + size_t(cache_slot(c, first)) * C::kPart + BM * D + orow));
-            const float mu = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f, acc[D / 64][8];
-#pragma unroll
-            for (int hc = 0; hc < D / 64; ++hc)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[hc][i] = 0.f;
-#pragma unroll 2
-            for (int c = first; c <= last; ++c) {
-                const float* src = p.part + size_t(cache_slot(c, first)) * C::kPart;
-                const float w = ex2_approx(__ldcg(src + BM * D + orow) - mu);
-                ll = fmaf(__ldcg(src + BM * D + BM + orow), w, ll);
-#pragma unroll
-                for (int hc = 0; hc < D / 64; ++hc) {
-                    const float4* q = reinterpret_cast<const float4*>(src + orow * D + 64 * hc + 8 * ocol);
-                    const float4 x = __ldcg(q), y = __ldcg(q + 1);
-                    acc[hc][0] = fmaf(x.x, w, acc[hc][0]);
-                    acc[hc][1] = fmaf(x.y, w, acc[hc][1]);
-                    acc[hc][2] = fmaf(x.z, w, acc[hc][2]);
-                    acc[hc][3] = fmaf(x.w, w, acc[hc][3]);
-                    acc[hc][4] = fmaf(y.x, w, acc[hc][4]);
-                    acc[hc][5] = fmaf(y.y, w, acc[hc][5]);
-                    acc[hc][6] = fmaf(y.z, w, acc[hc][6]);
-                    acc[hc][7] = fmaf(y.w, w, acc[hc][7]);
+                    for (int c = who; c < n; c += share) {
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c)) + col);
+                        const float f0 = w[c * 16];
+                        acc[k].x = fmaf(u.x, f0, acc[k].x);
+                        acc[k].y = fmaf(u.y, f0, acc[k].y);
+                        acc[k].z = fmaf(u.z, f0, acc[k].z);
+                        acc[k].w = fmaf(u.w, f0, acc[k].w);
+                    }
                 }
             }
-            const float li = ll > 0.f ? 1.f / ll : 0.f;
+            consumer_sync();
+        }
+        if (share > 1) {  // the threads of a column, added in their order
+            float4* sums = reinterpret_cast<float4*>(slots);  // (over the weights, read by now; row_l lies behind)
+            if (who < share) sums[threadIdx.x] = acc[0];
+            consumer_sync();
+            if (who == 0)
+                for (int k = 1; k < share; ++k) {
+                    const float4 u = sums[k * cols + col0];
+                    acc[0].x += u.x;
+                    acc[0].y += u.y;
+                    acc[0].z += u.z;
+                    acc[0].w += u.w;
+                }
+        }
+        if (who == 0) {
 #pragma unroll
-            for (int hc = 0; hc < D / 64; ++hc) put(64 * hc + 8 * ocol, acc[hc], li);
-            if (ocol == 0 && p.lse)
-                p.lse[grow] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            for (int k = 0; k < kCols; ++k) {
+                const int col = col0 + k * 32 * kDecWarps, rr = col / (D / 4), c = 4 * (col % (D / 4));
+                if (col >= cols) break;
+                const int r2 = r0 + rr, t2 = div_g(p, r2);
+                const size_t orow2 = size_t(g.s.q0 + t2) * size_t(p.H) + size_t(g.hk * p.g + r2 - t2 * p.g);
+                const float ll = row_l[rr], li = ll > 0.f ? 1.f / ll : 0.f;
+                if (p.o_f32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow2 * D + c) =
+                        make_float4(acc[k].x * li, acc[k].y * li, acc[k].z * li, acc[k].w * li);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + orow2 * D + c) =
+                        make_uint2(pack_bf16x2(acc[k].x * li, acc[k].y * li), pack_bf16x2(acc[k].z * li, acc[k].w * li));
+                if (p.lse && c == 0)
+                    p.lse[orow2] = ll > 0.f ? (row_m[rr] + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            }
         }
     }
 }

@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
     // tile row of this thread's row i, tile key of its key j, output column of its column c
     auto row_of = [&](int i) { return warp * C::kRows + (C::kBig ? C::LY * i + ry : i); };
     auto key_of = [&](int j) { return kx + (C::kBig ? C::LX : 32) * j; };
-    cache_start<BM, BN>(p, &start, reinterpret_cast<long long*>(sm));
-    CacheCursor<BM, BN> cur(start);
+    cache_start<BN>(p, &start, reinterpret_cast<long long*>(sm));
+    CacheCursor<BN> cur(start);
     CacheSeg g;
     const int page_mask = (1 << p.page_log2) - 1;
     while (cur.next(p, g)) {
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
             const int tr = e / (D / 4), c = e % (D / 4), r = r0 + tr;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < R) {
-                const int tok = r / p.g;
+                const int tok = div_g(p, r);
                 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
                                                      int64_t(g.hk * p.g + r - tok * p.g) * D + 4 * c);
             }
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
         const float* brow[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            const int r = min(r0 + row_of(i), R - 1), tok = r / p.g;
+            const int r = min(r0 + row_of(i), R - 1), tok = div_g(p, r);
             rel[i] = tok + diag;
             brow[i] = BIAS ? p.bias + (g.hk * p.g + r - tok * p.g) * 32 : nullptr;
             m[i] = -INFINITY;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
         }
-        const int t_first = r0 / p.g + diag, t_last = (min(R, r0 + BM) - 1) / p.g + diag;
+        const int t_first = div_g(p, r0) + diag, t_last = div_g(p, min(R, r0 + BM) - 1) + diag;
         const int all_hi = p.causal ? min(g.s.kv_len, t_first + 1) : g.s.kv_len;
         const int all_lo = p.window >= 0 ? max(0, t_last - p.window) : 0;
         for (int kt = g.k0; kt < k_end; ++kt) {
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
         auto finish = [&](int i, float mm, float ll, const float (&v)[NC]) {
             const int r = r0 + row_of(i);
             if (r >= R) return;
-            const int tok = r / p.g;
+            const int tok = div_g(p, r);
             const size_t row = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
             put(static_cast<float*>(p.O) + row * D, v, ll > 0.f ? 1.f / ll : 0.f);
             if (p.lse && kx == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
-            last_flag = atomicAdd(p.counters + first, 1u) == uint32_t(last - first);
-            if (last_flag) p.counters[first] = 0u;  // every part has arrived: ready for the next call
+            last_flag = atomicAdd(p.counters + kCtrSplit + first, 1u) == uint32_t(last - first);
+            if (last_flag) p.counters[kCtrSplit + first] = 0u;  // every part has arrived: ready for the next call
             __threadfence();
         }
         __syncthreads();

@@ -25,7 +25,7 @@ JFA_SOFTMAX, JFA_GDPA_GELU_TANH, JFA_GDPA_SILU = 0, 1, 2
 JFA_BF16, JFA_F32 = 0, 1
 JFA_BIAS_NONE, JFA_BIAS_RELPOS32, JFA_BIAS_DENSE = 0, 1, 2
 JFA_ROT_HALF, JFA_ROT_PAIRS = 0, 1
-JFA_CACHE_ZERO_BYTES = 8192
+JFA_CACHE_ZERO_BYTES = 32768
 
 MODES = {"softmax": JFA_SOFTMAX, "gelu_tanh": JFA_GDPA_GELU_TANH, "silu": JFA_GDPA_SILU}
 DTYPES = {torch.bfloat16: JFA_BF16, torch.float32: JFA_F32}
