@@ -64,6 +64,9 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
 
 constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
+// What an item's start and end cost the decode kernel, as bytes of keys and values streamed:
+// about 4 us of a CTA, at its share of the memory's rate.
+constexpr int kDecodeItemBytes = 98304;
 
 // Whether the cache's device is the current one.
 bool on_device(jfa_cache c) {
@@ -221,7 +224,7 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
     if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
     const int D = cache->D, n = cache->num_sms;
     return JFA_CACHE_ZERO_BYTES + kCutBytes + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n)
-                                                           : std::max(cache_decode_part_bytes(D, n), cache_chunk_part_bytes(D, n)));
+                                                           : cache_decode_part_bytes(D, n) + cache_chunk_part_bytes(D, n));
 }
 
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
@@ -280,39 +283,53 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.cuts = reinterpret_cast<CacheCut*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES + kCutBytes);
     p.status = cache->d_status;
-    p.min_units = 1;
     p.row_lo = 0;
     p.row_hi = INT32_MAX;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Sequences of at most kDecodeRows packed rows run in the decode kernel, the others in the
     // chunk kernel; which there are is known on the device only, beyond max_q_len.
-    CUtensorMap mq;
-    auto launch = [&](bool chunk) {
-        // a 128-key step of the chunk kernel is short against an item's start and end
-        p.min_units = chunk && cache->dtype == JFA_BF16 ? 4 : 1;
-        p.bm = chunk ? 128 : 16;
-        if (cache->dtype == JFA_F32) return launch_cache_simt(cache->D, chunk, p, cache->num_sms, st);
-        p.tile_tokens = 128 / p.g;
-        if (chunk) p.bm = 2 * p.tile_tokens * p.g;
-        return chunk ? launch_cache_chunk(cache->D, mq, cache->mk, cache->mv, p, cache->num_sms, st)
-                     : launch_cache_decode(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);
+    const int n = cache->num_sms, D = cache->D;
+    const bool bf16 = cache->dtype == JFA_BF16;
+    const bool chunks = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g > kDecodeRows;
+    // the kernels count units in 31 bits
+    auto fits = [&](int64_t rows, int bm, int bn) {
+        return double(rows / bm + B) * p.Hkv * (double(max_kv) / bn + 16.0) < double(INT32_MAX);
     };
-    const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
     cudaError_t e = cudaSuccess;
-    if (rows > kDecodeRows) {
-        if (cache->dtype == JFA_BF16) {  // the queries as (D, head, token), boxes of one tile's rows
-            const cuuint64_t dims[3] = {cuuint64_t(cache->D), cuuint64_t(H), cuuint64_t(T)};
-            const int64_t strides[2] = {cache->D, q_stride};
-            const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(128 / p.g)};
+    if (chunks) {
+        p.row_lo = kDecodeRows;
+        p.bm = 128;
+        p.item_cost = 0;
+        p.min_units = 1;
+        if (!bf16) {
+            if (!fits(T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
+            e = launch_cache_simt(D, true, p, n, st);
+        } else {
+            // the queries as (D, head, token), boxes of one tile's rows
+            p.tile_tokens = 128 / p.g;
+            p.bm = 2 * p.tile_tokens * p.g;
+            p.min_units = 4;  // a 128-key step is short against an item's start and end
+            if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
+            CUtensorMap mq;
+            const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
+            const int64_t strides[2] = {D, q_stride};
+            const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(p.tile_tokens)};
             const jfa_status ms = make_bf16_map(&mq, Q, 3, dims, strides, box);
             if (ms != JFA_OK) return ms;
+            e = launch_cache_chunk(D, mq, cache->mk, cache->mv, p, n, st);
         }
-        p.row_lo = kDecodeRows;
-        e = launch(true);
         p.row_lo = 0;
         p.row_hi = kDecodeRows;
     }
-    if (e == cudaSuccess) e = launch(false);
+    const CacheFwdParams pc = p;  // the merge's parameters
+    p.bm = 16;
+    p.min_units = 1;
+    p.item_cost = bf16 ? kDecodeItemBytes / (D * 256) : 0;
+    if (!fits(chunks ? 0 : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
+    if (bf16) p.part += cache_chunk_part_bytes(D, n) / sizeof(float);  // the two kernels may run at once
+    if (e == cudaSuccess)
+        e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, false, p, n, st);
+    if (e == cudaSuccess && chunks && bf16) e = launch_cache_merge(D, pc, n, st);
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 

@@ -25,6 +25,8 @@
 #include "cache_common.cuh"
 #include "tilemath.cuh"
 
+#include <limits.h>
+
 namespace jfa {
 
 namespace {
@@ -158,6 +160,11 @@ __global__ void __launch_bounds__(608, 1)
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if (warp == C::kProdWarp && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
     if (threadIdx.x >= 64 && threadIdx.x < 96) {
         // the smallest r with (1 + r)^2 >= 2^b: the root's integer part is within one of it
         int r = int(sqrtf(exp2f(float(lane))));
@@ -179,6 +186,7 @@ __global__ void __launch_bounds__(608, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    launch_dependents();  // the decode kernel may fill SMs as they come free
     CacheSeg g;
     int first = 0, last = 0, part_slot = 0;
     uint32_t seg_no = 0;
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(608, 1)
         g.tile = r.tile;
         g.s = CacheSeq{r.q0, r.q_len, r.kv_len};
         g.r = cache_range<C::BN>(p, g.s, g.tile);
-        g.units = max(1, g.r.n);
+        g.n = max(1, g.r.n);
         g.k0 = r.k0;
         g.k1 = r.k1;
         first = r.first;
@@ -265,8 +273,8 @@ __global__ void __launch_bounds__(608, 1)
         drain_ring(bar(B_V_FULL), kv_it, 2);
     } else if (warp == C::kDrawWarp) {
         // ------------------------------------------------------------ work
-        const int ng = (p.B + 31) >> 5, pieces = groups->pieces, whole = groups->items_whole, blk = groups->blk;
-        const long long cut = groups->cut;
+        const int ng = (p.B + 31) >> 5, pieces = groups->pieces, whole = groups->whole, blk = groups->blk;
+        const int cut = groups->cut;
         bool ok = true;
         // Waits until the part handed out last has been taken by every warp, so that a CTA
         // holds one part beside the one it works on, and draws no more than it can work off.
@@ -286,10 +294,10 @@ __global__ void __launch_bounds__(608, 1)
         while (w < pieces) {
             CacheStart st;
             if (w < whole) {
-                st = cache_find_item<C::BN>(p, *groups, ng, w, lane);
-                st.u_end = st.u + (1LL << 40);  // (one item, all of its units)
+                st = cache_find_item(p, *groups, ng, w, lane);
+                st.u_end = INT_MAX;  // (one item, all of its units)
             } else {
-                const long long u = cut + (long long)(w - whole) * blk;
+                const int u = cut + (w - whole) * blk;
                 st = cache_find_unit<C::BN>(p, *groups, ng, u, lane);
                 st.u_end = min(groups->total, u + blk);
             }
@@ -297,8 +305,8 @@ __global__ void __launch_bounds__(608, 1)
             while (cur.next(p, g) && taken()) {
                 SegRec r{g.b, g.hk, g.tile, g.k0, g.k1, g.s.q0, g.s.q_len, g.s.kv_len, 0, 0, 0, 0};
                 if (w >= whole) {
-                    r.first = int(div_ll(g.first - cut, blk));
-                    r.last = int(div_ll(g.first + g.units - 1 - cut, blk));
+                    r.first = int(uint32_t(g.first + p.item_cost - cut) / uint32_t(blk));
+                    r.last = int(uint32_t(g.first + p.item_cost + g.n - 1 - cut) / uint32_t(blk));
                     r.slot = cache_slot(w - whole, r.first);
                 }
                 hand_out(r);
@@ -847,8 +855,6 @@ cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorM
                                          ChkCfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
     jfa_cache_chunk_kernel<D, BIAS><<<num_sms, ChkCfg<D>::kThreads, ChkCfg<D>::kSmemBytes, st>>>(mq, mk, mv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    jfa_cache_merge_kernel<D><<<dim3(num_sms * kBlocksPerCta, kMergeCtas), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -860,6 +866,15 @@ cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& 
                                const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     if (D == 128) return p.bias ? launch<128, true>(mq, mk, mv, p, num_sms, st) : launch<128, false>(mq, mk, mv, p, num_sms, st);
     return p.bias ? launch<64, true>(mq, mk, mv, p, num_sms, st) : launch<64, false>(mq, mk, mv, p, num_sms, st);
+}
+
+cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    const dim3 grid(num_sms * kBlocksPerCta, kMergeCtas);
+    if (D == 128)
+        jfa_cache_merge_kernel<128><<<grid, 256, 0, st>>>(p);
+    else
+        jfa_cache_merge_kernel<64><<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace jfa

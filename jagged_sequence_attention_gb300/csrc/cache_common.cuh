@@ -61,6 +61,7 @@ struct CacheFwdParams {
     float* part;             // workspace: partial results, two slots per CTA or block
     int* status;
     int min_units;           // units a CTA takes at least
+    int item_cost;           // units that stand for an item's start and end (cache_units)
     int row_lo, row_hi;      // sequences this launch works on: row_lo < q_len * g <= row_hi
     int bm;                  // packed rows of an item
     int tile_tokens;         // chunk kernel: tokens of one of an item's two tiles
@@ -82,11 +83,6 @@ __host__ inline void set_div_g(CacheFwdParams& p) {
 __device__ __forceinline__ int div_g(const CacheFwdParams& p, int r) {
     return int((__umulhi(uint32_t(r), p.g_mul) + uint32_t(r)) >> p.g_shift);
 }
-// a / b for non-negative values, in 32 bits where they fit (as they nearly always do).
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-    return (a | b) >> 32 ? a / b : (long long)(uint32_t(a) / uint32_t(b));
-}
-
 // Sequence b's lengths; a bad sequence reads as empty.  In bad: whether it is one.
 __device__ __forceinline__ CacheSeq cache_seq(const CacheFwdParams& p, int b, bool& bad) {
     const int q0 = p.q_off[b], q1 = p.q_off[b + 1], kv = p.kv_lens[b];
@@ -121,136 +117,162 @@ __device__ __forceinline__ int cache_tiles(const CacheFwdParams& p, const CacheS
     return int(uint32_t(s.q_len * p.g + p.bm - 1) / uint32_t(p.bm));
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// Units of an item: its key tiles, and p.item_cost more that stand for its start and end, so
+// that equal ranges of units take equal times.  (Unit counts fit 31 bits: cache.cu checks.)
+template <int BN>
+__device__ __forceinline__ int cache_units(const CacheFwdParams& p, const CacheSeq& s, int tile) {
+    return max(1, cache_range<BN>(p, s, tile).n) + p.item_cost;
 }
-__device__ __forceinline__ long long warp_scan_ll(long long v, int lane) {  // inclusive
+
+__device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, v, o);
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += x;
     }
     return v;
 }
 
-// Units of one key head of sequence 32 c + lane, by the whole warp: a lane counts the tiles
-// of its own short sequence, and the warp together those of a long one.
+// Units of one key head of a lane's sequence, by the whole warp: a lane counts the tiles of
+// its own short sequence, and the warp together those of a long one.
 template <int BN>
-__device__ long long cache_seq_units(const CacheFwdParams& p, int c, int lane, bool report) {
-    const int b = 32 * c + lane;
-    CacheSeq s{0, 0, 0};
-    bool bad = false;
-    if (b < p.B) s = cache_seq(p, b, bad);
-    if (bad && report) atomicOr(p.status, kStatusBounds);
+__device__ __forceinline__ int cache_seq_units(const CacheFwdParams& p, const CacheSeq& s, int lane) {
     const int nt = cache_tiles(p, s);
-    long long u = 0;
+    int u = 0;
     const bool heavy = nt > 32;
     if (!heavy)
-        for (int t = 0; t < nt; ++t) u += max(1, cache_range<BN>(p, s, t).n);
+        for (int t = 0; t < nt; ++t) u += cache_units<BN>(p, s, t);
     uint32_t todo = __ballot_sync(0xffffffffu, heavy);
     while (todo) {
         const int l = __ffs(todo) - 1;
         todo &= todo - 1;
         const CacheSeq h{0, __shfl_sync(0xffffffffu, s.q_len, l), __shfl_sync(0xffffffffu, s.kv_len, l)};
         const int hn = cache_tiles(p, h);
-        long long v = 0;
-        for (int t = lane; t < hn; t += 32) v += max(1, cache_range<BN>(p, h, t).n);
-        v = warp_sum_ll(v);
+        int v = 0;
+        for (int t = lane; t < hn; t += 32) v += cache_units<BN>(p, h, t);
+        v = __reduce_add_sync(0xffffffffu, v);
         if (lane == l) u = v;
     }
     return u;
 }
 
+// The sequence of a lane in group c (32 sequences); the first CTA reports bad ones.
+__device__ __forceinline__ CacheSeq cache_lane_seq(const CacheFwdParams& p, int c, int lane, bool report) {
+    const int b = 32 * c + lane;
+    bool bad = false;
+    CacheSeq s{0, 0, 0};
+    if (b < p.B) s = cache_seq(p, b, bad);
+    if (bad && report) atomicOr(p.status, kStatusBounds);
+    return s;
+}
+
 // Where a CTA's range of units starts, and how the ranges are cut.
 struct CacheStart {
     int b, hk, tile, kt;
-    long long u, u_end;       // this CTA's units [u, u_end)
-    long long base;           // units per CTA, the first `rem` CTAs one more
-    int rem;
+    int u, u_end;       // this CTA's units [u, u_end)
+    int base, rem;      // units per CTA, the first `rem` CTAs one more
 };
 
-// By every thread of the CTA (blockDim.x a multiple of 32).  sums: shared scratch of
-// ceil(B / 32) values.
+// The item of the `left`-th unit of the sequences that a warp's lanes hold (s: a lane's
+// sequence 32 c + lane, one: its units per key head), into b, hk, tile and kt of `st`.
 template <int BN>
-__device__ void cache_start(const CacheFwdParams& p, CacheStart* out, long long* sums) {
+__device__ __forceinline__ void cache_locate(const CacheFwdParams& p, int c, const CacheSeq& s, int one, int left, int lane,
+                                             CacheStart& st) {
+    const int inc = warp_scan(one * p.Hkv, lane);
+    const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
+    left -= __shfl_sync(0xffffffffu, inc - one * p.Hkv, l);
+    const int per = __shfl_sync(0xffffffffu, one, l);
+    const CacheSeq q{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
+                     __shfl_sync(0xffffffffu, s.kv_len, l)};
+    st.b = 32 * c + l;
+    st.hk = int(uint32_t(left) / uint32_t(per));
+    left -= st.hk * per;
+    const int nt = cache_tiles(p, q);
+    st.tile = 0;
+    st.kt = left;
+    if (nt == 1) return;
+    for (int t0 = 0; t0 < nt; t0 += 32) {
+        const int n = t0 + lane < nt ? cache_units<BN>(p, q, t0 + lane) : 0;
+        const int in = warp_scan(n, lane);
+        const uint32_t m = __ballot_sync(0xffffffffu, in > left);
+        if (m) {
+            const int t = __ffs(m) - 1;
+            st.tile = t0 + t;
+            st.kt = left - __shfl_sync(0xffffffffu, in - n, t);
+            break;
+        }
+        left -= __shfl_sync(0xffffffffu, in, 31);
+    }
+}
+
+__device__ __forceinline__ void cache_cut(const CacheFwdParams& p, int total, CacheStart& st) {
+    const int want = int((uint32_t(total) + uint32_t(p.min_units) - 1u) / uint32_t(p.min_units));
+    const int G = min(int(gridDim.x), max(want, 1)), cta = blockIdx.x;
+    st = CacheStart{0, 0, 0, 0, 0, 0, 0, 0};
+    if (cta < G && total > 0) {
+        st.base = int(uint32_t(total) / uint32_t(G));
+        st.rem = total - st.base * G;
+        st.u = cta * st.base + min(cta, st.rem);
+        st.u_end = st.u + st.base + (cta < st.rem ? 1 : 0);
+    }
+}
+
+// This CTA's range, by every thread of the CTA; each warp gets it in registers.  sums: shared
+// scratch of ceil(B / 32) values (unused up to 32 sequences, which every warp looks over
+// itself); the caller synchronises before it is used for anything else.
+template <int BN>
+__device__ __forceinline__ CacheStart cache_start(const CacheFwdParams& p, int* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int chunks = (p.B + 31) >> 5;
-    for (int c = warp; c < chunks; c += warps) {
-        const long long v = warp_sum_ll(cache_seq_units<BN>(p, c, lane, blockIdx.x == 0));
+    const int groups = (p.B + 31) >> 5;
+    CacheStart st;
+    if (groups <= 1) {
+        const CacheSeq s = cache_lane_seq(p, 0, lane, blockIdx.x == 0 && warp == 0);
+        const int one = cache_seq_units<BN>(p, s, lane);
+        cache_cut(p, __reduce_add_sync(0xffffffffu, one) * p.Hkv, st);
+        if (st.u < st.u_end) cache_locate<BN>(p, 0, s, one, st.u, lane, st);
+        return st;
+    }
+    for (int c = warp; c < groups; c += warps) {
+        const CacheSeq s = cache_lane_seq(p, c, lane, blockIdx.x == 0);
+        const int v = __reduce_add_sync(0xffffffffu, cache_seq_units<BN>(p, s, lane));
         if (lane == 0) sums[c] = v * p.Hkv;
     }
     __syncthreads();
-    if (warp == 0) {
-        long long total = 0;
-        for (int c = lane; c < chunks; c += 32) total += sums[c];
-        total = warp_sum_ll(total);
-        CacheStart st{0, 0, 0, 0, 0, 0, 0, 0};
-        const long long want = div_ll(total + p.min_units - 1, p.min_units);
-        const int G = int(min((long long)(gridDim.x), max(want, 1LL)));
-        const int cta = blockIdx.x;
-        if (cta < G && total > 0) {
-            st.base = div_ll(total, G);
-            st.rem = int(total - st.base * G);
-            st.u = cta * st.base + min(cta, st.rem);
-            st.u_end = st.u + st.base + (cta < st.rem ? 1 : 0);
-        }
-        if (st.u < st.u_end) {
-            long long left = st.u;  // units before the range, from the search's position on
-            int c = 0;
-            for (int c0 = 0; c0 < chunks; c0 += 32) {
-                const long long v = c0 + lane < chunks ? sums[c0 + lane] : 0;
-                const long long inc = warp_scan_ll(v, lane);
-                const uint32_t m = __ballot_sync(0xffffffffu, inc > left);
-                if (m) {
-                    const int l = __ffs(m) - 1;
-                    c = c0 + l;
-                    left -= __shfl_sync(0xffffffffu, inc - v, l);
-                    break;
-                }
-                left -= __shfl_sync(0xffffffffu, inc, 31);
+    int total = 0;
+    for (int c = lane; c < groups; c += 32) total += sums[c];
+    cache_cut(p, __reduce_add_sync(0xffffffffu, total), st);
+    if (st.u < st.u_end) {
+        int left = st.u, c = 0;
+        for (int c0 = 0; c0 < groups; c0 += 32) {
+            const int v = c0 + lane < groups ? sums[c0 + lane] : 0;
+            const int inc = warp_scan(v, lane);
+            const uint32_t m = __ballot_sync(0xffffffffu, inc > left);
+            if (m) {
+                const int l = __ffs(m) - 1;
+                c = c0 + l;
+                left -= __shfl_sync(0xffffffffu, inc - v, l);
+                break;
             }
-            const long long one = cache_seq_units<BN>(p, c, lane, false);
-            const long long inc = warp_scan_ll(one * p.Hkv, lane);
-            const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
-            left -= __shfl_sync(0xffffffffu, inc - one * p.Hkv, l);
-            st.b = 32 * c + l;
-            const long long per = __shfl_sync(0xffffffffu, one, l);
-            st.hk = int(div_ll(left, per));
-            left -= st.hk * per;
-            bool bad;
-            const CacheSeq s = cache_seq(p, st.b, bad);
-            const int nt = cache_tiles(p, s);
-            for (int t0 = 0; t0 < nt; t0 += 32) {
-                const long long n = t0 + lane < nt ? max(1, cache_range<BN>(p, s, t0 + lane).n) : 0;
-                const long long in = warp_scan_ll(n, lane);
-                const uint32_t m = __ballot_sync(0xffffffffu, in > left);
-                if (m) {
-                    const int t = __ffs(m) - 1;
-                    st.tile = t0 + t;
-                    st.kt = int(left - __shfl_sync(0xffffffffu, in - n, t));
-                    break;
-                }
-                left -= __shfl_sync(0xffffffffu, in, 31);
-            }
+            left -= __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) *out = st;
+        const CacheSeq s = cache_lane_seq(p, c, lane, false);
+        cache_locate<BN>(p, c, s, cache_seq_units<BN>(p, s, lane), left, lane, st);
     }
-    __syncthreads();
+    return st;
 }
 
-// A CTA's part of one item: units [k0, k1) of its `units`, from unit number `first` of the batch.
+// A CTA's part of one item: key tiles [k0, k1) of its n (at least one), the item's units from
+// number `first` of the batch on.
 struct CacheSeg {
     int b, hk, tile;
     CacheSeq s;
     CacheRange r;
-    int k0, k1, units;
-    long long first;
-    __device__ bool whole() const { return k0 == 0 && k1 == units; }
+    int k0, k1, n;
+    int first;
+    __device__ bool whole() const { return k0 == 0 && k1 == n; }
 };
 
-// Walks a CTA's range.  Every role of a CTA walks its own copy.
+// Walks a range of units.  Every role of a CTA walks its own copy.
 template <int BN>
 struct CacheCursor {
     CacheStart st;
@@ -258,40 +280,50 @@ struct CacheCursor {
     int nt;
     __device__ explicit CacheCursor(const CacheStart& start) : st(start), s{0, 0, 0}, nt(-1) {}
     __device__ bool next(const CacheFwdParams& p, CacheSeg& g) {
-        if (st.u >= st.u_end) return false;
-        while (nt <= 0) {
-            if (nt == 0) ++st.b;
-            if (st.b >= p.B) return false;
-            bool bad;
-            s = cache_seq(p, st.b, bad);
-            nt = cache_tiles(p, s);
-        }
-        g.b = st.b;
-        g.hk = st.hk;
-        g.tile = st.tile;
-        g.s = s;
-        g.r = cache_range<BN>(p, s, st.tile);
-        g.units = max(1, g.r.n);
-        g.k0 = st.kt;
-        g.k1 = int(min((long long)(g.units), st.kt + (st.u_end - st.u)));
-        g.first = st.u - st.kt;
-        st.u += g.k1 - g.k0;
-        st.kt = 0;
-        if (++st.tile == nt) {
-            st.tile = 0;
-            if (++st.hk == p.Hkv) {
-                st.hk = 0;
-                nt = 0;
+        while (st.u < st.u_end) {
+            while (nt <= 0) {
+                if (nt == 0) ++st.b;
+                if (st.b >= p.B) return false;
+                bool bad;
+                s = cache_seq(p, st.b, bad);
+                nt = cache_tiles(p, s);
             }
+            g.b = st.b;
+            g.hk = st.hk;
+            g.tile = st.tile;
+            g.s = s;
+            g.r = cache_range<BN>(p, s, st.tile);
+            g.n = max(1, g.r.n);
+            // the units before the first key tile are the item's cost
+            const int v1 = min(g.n + p.item_cost, st.kt + (st.u_end - st.u));
+            g.k0 = max(0, st.kt - p.item_cost);
+            g.k1 = max(0, v1 - p.item_cost);
+            g.first = st.u - st.kt;
+            st.u += v1 - st.kt;
+            st.kt = 0;
+            if (++st.tile == nt) {
+                st.tile = 0;
+                if (++st.hk == p.Hkv) {
+                    st.hk = 0;
+                    nt = 0;
+                }
+            }
+            if (g.k1 > g.k0) return true;
         }
-        return true;
+        return false;
     }
 };
 
-// The CTA that holds unit u.
-__device__ __forceinline__ int cache_cta_of(const CacheStart& st, long long u) {
-    const long long head = st.rem * (st.base + 1);
-    return u < head ? int(div_ll(u, st.base + 1)) : st.rem + int(div_ll(u - head, st.base));
+// The CTA that holds unit u, and the first and last CTA with a part of an item.
+__device__ __forceinline__ int cache_cta_of(const CacheStart& st, int u) {
+    const int head = st.rem * (st.base + 1);
+    return u < head ? int(uint32_t(u) / uint32_t(st.base + 1)) : st.rem + int(uint32_t(u - head) / uint32_t(st.base));
+}
+__device__ __forceinline__ int cache_first_cta(const CacheFwdParams& p, const CacheStart& st, const CacheSeg& g) {
+    return cache_cta_of(st, g.first + p.item_cost);
+}
+__device__ __forceinline__ int cache_last_cta(const CacheFwdParams& p, const CacheStart& st, const CacheSeg& g) {
+    return cache_cta_of(st, g.first + p.item_cost + g.n - 1);
 }
 
 // ------------------------------------------------------------------ work drawn in order
@@ -303,26 +335,16 @@ __device__ __forceinline__ int cache_cta_of(const CacheStart& st, long long u) {
 // cut items' parts, numbered by block, are merged by a second kernel.  Which units form a piece
 // depends on the lengths alone, so results do not depend on who draws what.
 struct CacheGroups {      // shared memory
-    long long units[kCacheMaxGroups];  // units before the group of 32 sequences
-    int32_t items[kCacheMaxGroups];    // items before it
-    long long total, cut;  // units; the first `items_whole` items are units [0, cut)
-    int32_t items_whole, blk, pieces;
-    int32_t longest;       // units of the longest item
+    int units[kCacheMaxGroups];  // units before the group of 32 sequences
+    int items[kCacheMaxGroups];  // items before it
+    int total, cut;        // units; the first `whole` items are units [0, cut)
+    int whole, blk, pieces;
+    int longest;           // units of the longest item
 };
 
-// Lanes' exclusive prefix of the 32 sequences of group c: units and items of each.
-template <int BN>
-__device__ __forceinline__ void cache_group_lane(const CacheFwdParams& p, int c, int lane, bool report, long long& units,
-                                                 int& tiles) {
-    units = cache_seq_units<BN>(p, c, lane, report);
-    tiles = 0;
-    bool bad;
-    if (32 * c + lane < p.B) tiles = cache_tiles(p, cache_seq(p, 32 * c + lane, bad));
-}
-
-// The group of unit u (or item u): the last one starting at or before it.
-template <typename T>
-__device__ __forceinline__ int cache_find_group(const T* before, int groups, T u, int lane) {
+// The group of unit u (or item u): the last one starting at or before it.  (A group without
+// any shares its start with the next one that has some, which comes later.)
+__device__ __forceinline__ int cache_find_group(const int* before, int groups, int u, int lane) {
     int c = 0;
     for (int c0 = 0; c0 < groups; c0 += 32) {
         const uint32_t m = __ballot_sync(0xffffffffu, c0 + lane < groups && before[c0 + lane] <= u);
@@ -332,120 +354,92 @@ __device__ __forceinline__ int cache_find_group(const T* before, int groups, T u
     return c;
 }
 
-// Unit u of the batch, by a whole warp: its item and the key tile within it; the item's
-// number in `item`.
+// Unit u of the batch, by a whole warp: its item and unit within it.
 template <int BN>
-__device__ CacheStart cache_find_unit(const CacheFwdParams& p, const CacheGroups& G, int groups, long long u, int lane,
-                                      int* item = nullptr) {
+__device__ __forceinline__ CacheStart cache_find_unit(const CacheFwdParams& p, const CacheGroups& G, int groups, int u,
+                                                      int lane) {
     CacheStart st{0, 0, 0, 0, u, u, 0, 0};
-    // (a group without units shares its successor's start, which the search prefers)
     const int c = cache_find_group(G.units, groups, u, lane);
-    long long left = u - G.units[c], one;
-    int tiles;
-    cache_group_lane<BN>(p, c, lane, false, one, tiles);
-    const long long inc = warp_scan_ll(one * p.Hkv, lane);
-    const long long tinc = warp_scan_ll((long long)(tiles)*p.Hkv, lane);
-    const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
-    left -= __shfl_sync(0xffffffffu, inc - one * p.Hkv, l);
-    const long long before = __shfl_sync(0xffffffffu, tinc - (long long)(tiles)*p.Hkv, l);
-    const long long per = __shfl_sync(0xffffffffu, one, l);
-    st.b = 32 * c + l;
-    st.hk = int(div_ll(left, per));
-    left -= st.hk * per;
-    bool bad;
-    const CacheSeq s = cache_seq(p, st.b, bad);
-    const int nt = cache_tiles(p, s);
-    for (int t0 = 0; t0 < nt; t0 += 32) {
-        const long long n = t0 + lane < nt ? max(1, cache_range<BN>(p, s, t0 + lane).n) : 0;
-        const long long in = warp_scan_ll(n, lane);
-        const uint32_t m = __ballot_sync(0xffffffffu, in > left);
-        if (m) {
-            const int t = __ffs(m) - 1;
-            st.tile = t0 + t;
-            st.kt = int(left - __shfl_sync(0xffffffffu, in - n, t));
-            break;
-        }
-        left -= __shfl_sync(0xffffffffu, in, 31);
-    }
-    if (item) *item = G.items[c] + int(before) + st.hk * nt + st.tile;
+    const CacheSeq s = cache_lane_seq(p, c, lane, false);
+    cache_locate<BN>(p, c, s, cache_seq_units<BN>(p, s, lane), u - G.units[c], lane, st);
     return st;
 }
 
 // Item i of the batch, by a whole warp.
-template <int BN>
-__device__ CacheStart cache_find_item(const CacheFwdParams& p, const CacheGroups& G, int groups, int i, int lane) {
+__device__ __forceinline__ CacheStart cache_find_item(const CacheFwdParams& p, const CacheGroups& G, int groups, int i,
+                                                      int lane) {
     CacheStart st{0, 0, 0, 0, 0, 0, 0, 0};
     const int c = cache_find_group(G.items, groups, i, lane);
-    long long left = i - G.items[c];
-    bool bad;
-    const int tiles = 32 * c + lane < p.B ? cache_tiles(p, cache_seq(p, 32 * c + lane, bad)) : 0;
-    const long long inc = warp_scan_ll((long long)(tiles)*p.Hkv, lane);
+    const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false));
+    const int inc = warp_scan(tiles * p.Hkv, lane);
+    int left = i - G.items[c];
     const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
-    left -= __shfl_sync(0xffffffffu, inc - (long long)(tiles)*p.Hkv, l);
+    left -= __shfl_sync(0xffffffffu, inc - tiles * p.Hkv, l);
     const int nt = __shfl_sync(0xffffffffu, tiles, l);
     st.b = 32 * c + l;
-    st.hk = int(div_ll(left, nt));
-    st.tile = int(left - (long long)(st.hk) * nt);
+    st.hk = int(uint32_t(left) / uint32_t(nt));
+    st.tile = left - st.hk * nt;
     return st;
 }
 
 // The batch's pieces, by every thread of the CTA.  G.pieces is 0 for a batch without rows.
 template <int BN>
-__device__ void cache_pieces(const CacheFwdParams& p, CacheGroups* G) {
+__device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroups* G) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int groups = (p.B + 31) >> 5;
     if (threadIdx.x == 0) G->longest = 1;
     __syncthreads();
     for (int c = warp; c < groups; c += warps) {
-        long long u;
-        int tiles;
-        cache_group_lane<BN>(p, c, lane, blockIdx.x == 0, u, tiles);
-        if (tiles > 0) {  // a sequence's last item sees the most keys, but for a window's odd tile
-            bool bad;
-            const int n = cache_range<BN>(p, cache_seq(p, 32 * c + lane, bad), tiles - 1).n;
-            if (n > 1) atomicMax(&G->longest, n);
-        }
-        u = warp_sum_ll(u);
-        const long long t = warp_sum_ll(tiles);
+        const CacheSeq s = cache_lane_seq(p, c, lane, blockIdx.x == 0);
+        const int tiles = cache_tiles(p, s);
+        // a sequence's last item sees the most keys (but for a window's odd tile)
+        const int n = __reduce_max_sync(0xffffffffu, tiles > 0 ? cache_units<BN>(p, s, tiles - 1) : 0);
+        const int u = __reduce_add_sync(0xffffffffu, cache_seq_units<BN>(p, s, lane));
+        const int t = __reduce_add_sync(0xffffffffu, tiles);
         if (lane == 0) {
             G->units[c] = u * p.Hkv;
-            G->items[c] = int32_t(t * p.Hkv);
+            G->items[c] = t * p.Hkv;
+            atomicMax(&G->longest, n);
         }
     }
     __syncthreads();
     if (warp == 0) {
-        long long u = 0, items = 0;
+        int u = 0, items = 0;
         for (int c0 = 0; c0 < groups; c0 += 32) {  // sums to exclusive prefixes
             const bool in = c0 + lane < groups;
-            const long long v = in ? G->units[c0 + lane] : 0, w = in ? G->items[c0 + lane] : 0;
-            const long long vi = warp_scan_ll(v, lane), wi = warp_scan_ll(w, lane);
+            const int v = in ? G->units[c0 + lane] : 0, w = in ? G->items[c0 + lane] : 0;
+            const int vi = warp_scan(v, lane), wi = warp_scan(w, lane);
             if (in) {
                 G->units[c0 + lane] = u + vi - v;
-                G->items[c0 + lane] = int32_t(items + wi - w);
+                G->items[c0 + lane] = items + wi - w;
             }
             u += __shfl_sync(0xffffffffu, vi, 31);
             items += __shfl_sync(0xffffffffu, wi, 31);
         }
         __syncwarp();
-        const long long grid = gridDim.x;
+        const int grid = gridDim.x, longest = G->longest;
         // The last part, cut in blocks, covers the spread with which the CTAs come out of the
         // whole items: half an item each.
-        const long long rest = min(u, grid * (G->longest + 1) / 2);
-        long long cut = 0;
-        int whole = 0;
+        const int rest = int(min((long long)(u), (long long)(grid) * (longest + 1) / 2));
+        int cut = 0, whole = 0;
         if (u > rest) {
-            const CacheStart st = cache_find_unit<BN>(p, *G, groups, u - rest, lane, &whole);
+            const CacheStart st = cache_find_unit<BN>(p, *G, groups, u - rest, lane);
             cut = u - rest - st.kt;
+            const int c = st.b >> 5;
+            const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false));
+            const int before = __reduce_add_sync(0xffffffffu, 32 * c + lane < st.b ? tiles : 0);
+            whole = G->items[c] + before * p.Hkv + st.hk * __shfl_sync(0xffffffffu, tiles, st.b & 31) + st.tile;
         }
-        const long long left = u - cut;
-        const long long blk = left <= grid * 8 ? max(div_ll(left + grid - 1, grid), (long long)(p.min_units))
-                                               : max(8LL, div_ll(left + kBlocksPerCta * grid - 1, kBlocksPerCta * grid));
+        const int left = u - cut;
+        // few units: one block a CTA, of at least min_units (or an item); else several
+        const int blk = left <= grid * 8 ? max((left + grid - 1) / grid, min(p.min_units, longest))
+                                         : max(8, (left + kBlocksPerCta * grid - 1) / (kBlocksPerCta * grid));
         if (lane == 0) {
             G->total = u;
             G->cut = cut;
-            G->items_whole = whole;
-            G->blk = int32_t(blk);
-            G->pieces = whole + int32_t(left > 0 ? div_ll(left + blk - 1, blk) : 0);
+            G->whole = whole;
+            G->blk = blk;
+            G->pieces = whole + (left + blk - 1) / blk;
         }
     }
     __syncthreads();
@@ -455,6 +449,11 @@ __device__ void cache_pieces(const CacheFwdParams& p, CacheGroups* G) {
 // CTA, slot 1 for one that goes on in the next.  An item split over CTAs first..last has its
 // first part in slot 1 of `first`, the others in slot 0.
 __device__ __forceinline__ int cache_slot(int cta, int first_cta) { return 2 * cta + (cta == first_cta ? 1 : 0); }
+
+// Programmatic launch: let the next kernel of the stream start (when it was launched so), and
+// wait for the previous one to have finished.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
     asm volatile(
@@ -477,14 +476,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 cudaError_t launch_cache_simt(int D, bool chunk, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_simt_part_bytes(int D, int num_sms);
 // bf16, row tiles of 16 packed rows: bound by the stream of K and V.
-cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
-                                cudaStream_t st);
+// early: start while the chunk kernel before it in the stream still runs (they share no
+// memory that either writes), and end after it.
+cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early,
+                                int num_sms, cudaStream_t st);
 size_t cache_decode_part_bytes(int D, int num_sms);
 // bf16, items of 256 packed rows: bound by the tensor cores and the exponentials.
 // mq: the queries as (D, head, token), boxes of 128 bytes x g heads x tile_tokens.
 cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_chunk_part_bytes(int D, int num_sms);
+cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 
 struct CacheAppendParams {
     const int32_t* q_off;

@@ -29,9 +29,11 @@ struct DecCfg {
     static constexpr int kStages = 98304 / kStage;
     static constexpr int kOffSlots = kStages * kStage;       // two 16 x 64 fp32 tiles of the merge
     static constexpr int kOffML = kOffSlots + 2 * 16 * 64 * 4;   // [2 buffers][m, l][warp][row]
-    static constexpr int kOffBar = kOffML + 2 * 2 * kDecWarps * 16 * 4;
+    static constexpr int kOffBias = kOffML + 2 * 2 * kDecWarps * 16 * 4;  // [row][32 buckets + 1], log2 units
+    static constexpr int kOffBar = kOffBias + 16 * 33 * 4;
     static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
     static constexpr int kBytes = kOffMisc + 16 + int(sizeof(CacheStart)) + 1024;
+    static_assert(kDecCtasPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
     static constexpr int kPart = kDecBM * (D + 2);           // floats of a partial result: O, m, l
 };
 
@@ -69,7 +71,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     auto empty = [&](uint32_t s) -> uint32_t { return sbase + C::kOffBar + 8u * (C::kStages + s); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-    CacheStart* start = reinterpret_cast<CacheStart*>(smem + C::kOffMisc + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -79,9 +80,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         }
         *abort_flag = 0;
         fence_barrier_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
     }
-    cache_start<BN>(p, start, reinterpret_cast<long long*>(smem));  // (the ring's memory as scratch)
-    CacheCursor<BN> cur(*start);
+    CacheStart* start = reinterpret_cast<CacheStart*>(smem + C::kOffMisc + 16);
+    CacheCursor<BN> cur(cache_start<BN>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
+    if (threadIdx.x == 0) *start = cur.st;
+    __syncthreads();
     CacheSeg g;
 
     if (warp == kDecWarps) {
@@ -135,12 +140,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             if (lane == 0) atomicOr(p.status, kStatusTimeout);
         }
         drain_ring(full(0), it, C::kStages);
+        wait_previous();
         return;
     }
 
     // -------------------------------------------------------------------- consumers
     float* slots = reinterpret_cast<float*>(smem + C::kOffSlots);
     float* ml = reinterpret_cast<float*>(smem + C::kOffML);
+    float* btab = reinterpret_cast<float*>(smem + C::kOffBias);
     const int quad = lane & 3, qrow = lane >> 2;
     uint32_t it = 0, seg_no = 0;
     bool ok = true;
@@ -154,7 +161,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         // this lane's rows qrow and qrow + 8: queries, limits, heads
         uint32_t qa[D / 16][4];
         int lim[2], low[2], rel[2];
-        const float* brow[2];
+        if (BIAS) {  // the rows' bias, for this item's heads
+            for (int e = threadIdx.x; e < nr * 32; e += 32 * kDecWarps) {
+                const int r = r0 + (e >> 5);
+                btab[(e >> 5) * 33 + (e & 31)] =
+                    p.bias[(g.hk * p.g + r - div_g(p, r) * p.g) * 32 + (e & 31)] * 1.4426950408889634f;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int rr = qrow + 8 * i;
@@ -163,7 +176,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             rel[i] = tok + diag;
             lim[i] = p.causal ? min(g.s.kv_len, rel[i] + 1) : g.s.kv_len;
             low[i] = p.window >= 0 ? rel[i] - p.window : 0;
-            brow[i] = BIAS ? p.bias + head * 32 : nullptr;
             const __nv_bfloat16* src = Q + (g.s.q0 + tok) * p.q_stride + int64_t(head) * D + 2 * quad;
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
@@ -171,6 +183,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 qa[s][2 + i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8) : 0u;
             }
         }
+        if (BIAS) consumer_sync();
+        const float* brow[2] = {btab + qrow * 33, btab + (qrow + 8 < nr ? qrow + 8 : 0) * 33};
         // keys that every row of the tile sees: no mask in [all_lo, all_hi)
         const int t_first = div_g(p, r0), t_last = div_g(p, r0 + nr - 1);
         const int all_hi = p.causal ? min(g.s.kv_len, t_first + diag + 1) : g.s.kv_len;
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                     if (bk != bucket) {
                         bucket = bk;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) bcur[i] = __ldg(brow[i] + bk) * 1.4426950408889634f;
+                        for (int i = 0; i < 2; ++i) bcur[i] = brow[i][bk];
                     }
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
@@ -231,8 +245,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int j = w0 + 8 * n + 2 * quad + (i & 1);
-                            const float bv = __ldg(brow[i >> 1] + relpos_bucket(rel[i >> 1] - j));
-                            s[n][i] = fmaf(s[n][i], p.scale_log2, bv * 1.4426950408889634f);
+                            s[n][i] = fmaf(s[n][i], p.scale_log2, brow[i >> 1][relpos_bucket(rel[i >> 1] - j)]);
                         }
                 }
             } else {
@@ -334,8 +347,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         const bool whole = g.whole();
         int first = 0, last = 0;
         if (!whole) {
-            first = cache_cta_of(*start, g.first);
-            last = cache_cta_of(*start, g.first + g.units - 1);
+            first = cache_first_cta(p, *start, g);
+            last = cache_last_cta(p, *start, g);
         }
         float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
         const int r = r0 + orow, tok = div_g(p, r);
@@ -423,15 +436,47 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         float* row_m = slots + kBatch * 16;  // [16], and the sums [16]
         float* row_l = row_m + 16;
         auto part_of = [&](int c) { return p.part + size_t(cache_slot(first + c, first)) * C::kPart; };
-        for (int rr = warp; rr < nr; rr += kDecWarps) {
-            float mm = -INFINITY;
-            for (int c = lane; c < parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + BM * D + rr));
+        // columns: up to 4 per thread (nr = 16); threads per column: as many as fit
+        const int share = cols > 64 ? 1 : 32 * kDecWarps / cols, who = share > 1 ? threadIdx.x / cols : 0;
+        const int col0 = share > 1 ? threadIdx.x % cols : threadIdx.x;
+        constexpr int kAhead = 8;            // parts of the first column loaded before the weights are known
+        float4 ahead[kAhead];
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
-            float ll = 0.f;
-            for (int c = lane; c < parts; c += 32) {
-                const float mc = __ldcg(part_of(c) + BM * D + rr);
-                ll = fmaf(mc == -INFINITY ? 0.f : ex2_approx(mc - mm), __ldcg(part_of(c) + BM * D + BM + rr), ll);
+        for (int k = 0; k < kAhead; ++k)
+            if (who + k * share < parts && col0 < cols && who < share)
+                ahead[k] = __ldcg(reinterpret_cast<const float4*>(part_of(who + k * share)) + col0);
+        const bool few = parts <= 64;        // a row's m and l in two registers of a lane
+        for (int rr = warp; rr < nr; rr += kDecWarps) {
+            float mm, ll;
+            if (few) {
+                float mc[2], lc[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int c = lane + 32 * k;
+                    mc[k] = c < parts ? __ldcg(part_of(c) + BM * D + rr) : -INFINITY;
+                    lc[k] = c < parts ? __ldcg(part_of(c) + BM * D + BM + rr) : 0.f;
+                }
+                mm = fmaxf(mc[0], mc[1]);
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+                ll = 0.f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int c = lane + 32 * k;
+                    const float w = mc[k] == -INFINITY ? 0.f : ex2_approx(mc[k] - mm);
+                    ll = fmaf(w, lc[k], ll);
+                    if (c < parts) wts[c * 16 + rr] = w;
+                }
+            } else {
+                mm = -INFINITY;
+                for (int c = lane; c < parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + BM * D + rr));
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+                ll = 0.f;
+                for (int c = lane; c < parts; c += 32) {
+                    const float mc = __ldcg(part_of(c) + BM * D + rr);
+                    ll = fmaf(mc == -INFINITY ? 0.f : ex2_approx(mc - mm), __ldcg(part_of(c) + BM * D + BM + rr), ll);
+                }
             }
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);
@@ -441,35 +486,39 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             }
         }
         consumer_sync();
-        // columns: up to 4 per thread (nr = 16); threads per column: as many as fit
-        const int share = cols > 64 ? 1 : 32 * kDecWarps / cols, who = share > 1 ? threadIdx.x / cols : 0;
-        const int col0 = share > 1 ? threadIdx.x % cols : threadIdx.x;
         float4 acc[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c0 = 0; c0 < parts; c0 += kBatch) {
             const int n = min(kBatch, parts - c0);
-            for (int e = threadIdx.x; e < n * 16; e += 32 * kDecWarps) {
+            for (int e = threadIdx.x; !few && e < n * 16; e += 32 * kDecWarps) {
                 const int rr = e & 15;
                 const float mc = rr < nr ? __ldcg(part_of(c0 + (e >> 4)) + BM * D + rr) : -INFINITY;
                 wts[e] = mc == -INFINITY ? 0.f : ex2_approx(mc - row_m[rr]);
             }
-            consumer_sync();
+            if (!few) consumer_sync();
             if (who < share) {
 #pragma unroll
                 for (int k = 0; k < kCols; ++k) {
                     const int col = col0 + k * 32 * kDecWarps, rr = col / (D / 4);
                     if (col >= cols) break;
                     const float* w = wts + rr;
-#pragma unroll 8
-                    for (int c = who; c < n; c += share) {
-                        const float4 u = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c)) + col);
+                    auto add = [&](const float4 u, int c) {
                         const float f0 = w[c * 16];
                         acc[k].x = fmaf(u.x, f0, acc[k].x);
                         acc[k].y = fmaf(u.y, f0, acc[k].y);
                         acc[k].z = fmaf(u.z, f0, acc[k].z);
                         acc[k].w = fmaf(u.w, f0, acc[k].w);
+                    };
+                    int c = who;
+                    if (k == 0 && c0 == 0) {
+#pragma unroll
+                        for (int a = 0; a < kAhead; ++a)
+                            if (who + a * share < n) add(ahead[a], who + a * share);
+                        c = who + kAhead * share;
                     }
+#pragma unroll 8
+                    for (; c < n; c += share) add(__ldcg(reinterpret_cast<const float4*>(part_of(c0 + c)) + col), c);
                 }
             }
             consumer_sync();
@@ -509,12 +558,22 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 }
 
 template <int D, bool BIAS>
-cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early, int num_sms,
+                   cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(jfa_cache_decode_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          DecCfg<D>::kBytes);
     if (e != cudaSuccess) return e;
-    jfa_cache_decode_kernel<D, BIAS><<<num_sms * kDecCtasPerSm, kDecThreads, DecCfg<D>::kBytes, st>>>(mk, mv, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms * kDecCtasPerSm);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = DecCfg<D>::kBytes;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, jfa_cache_decode_kernel<D, BIAS>, mk, mv, p);
 }
 
 }  // namespace
@@ -523,10 +582,11 @@ size_t cache_decode_part_bytes(int D, int num_sms) {
     return size_t(num_sms) * kDecCtasPerSm * 2 * kDecBM * size_t(D + 2) * 4;
 }
 
-cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
-                                cudaStream_t st) {
-    if (D == 128) return p.bias ? launch<128, true>(mk, mv, p, num_sms, st) : launch<128, false>(mk, mv, p, num_sms, st);
-    return p.bias ? launch<64, true>(mk, mv, p, num_sms, st) : launch<64, false>(mk, mv, p, num_sms, st);
+cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early,
+                                int num_sms, cudaStream_t st) {
+    if (D == 128)
+        return p.bias ? launch<128, true>(mk, mv, p, early, num_sms, st) : launch<128, false>(mk, mv, p, early, num_sms, st);
+    return p.bias ? launch<64, true>(mk, mv, p, early, num_sms, st) : launch<64, false>(mk, mv, p, early, num_sms, st);
 }
 
 }  // namespace jfa

@@ -53,7 +53,6 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
     // columns of a thread in P V: big: groups of four at 4 kx + 32 j; small: lane + 32 j
     constexpr int NC = C::kBig ? D / C::LX : D / 32;
     extern __shared__ __align__(16) float sm[];
-    __shared__ CacheStart start;
     __shared__ int last_flag;
     float* sQ = sm + C::kQ;
     float* sP = sm + C::kP;
@@ -62,7 +61,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
     // tile row of this thread's row i, tile key of its key j, output column of its column c
     auto row_of = [&](int i) { return warp * C::kRows + (C::kBig ? C::LY * i + ry : i); };
     auto key_of = [&](int j) { return kx + (C::kBig ? C::LX : 32) * j; };
-    cache_start<BN>(p, &start, reinterpret_cast<long long*>(sm));
+    const CacheStart start = cache_start<BN>(p, reinterpret_cast<int*>(sm));
     CacheCursor<BN> cur(start);
     CacheSeg g;
     const int page_mask = (1 << p.page_log2) - 1;
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
             for (int i = 0; i < RT; ++i) finish(i, m[i], l[i], o[i]);
             continue;
         }
-        const int first = cache_cta_of(start, g.first), last = cache_cta_of(start, g.first + g.units - 1);
+        const int first = cache_first_cta(p, start, g), last = cache_last_cta(p, start, g);
         float* mine = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
