@@ -420,7 +420,7 @@ const char* jfa_status_string(int32_t status);
  *                     position rotation applied to keys and queries on the way;
  *   jfa_cache_fwd     attends from the new tokens to the cached positions.
  * Both take, as int32 DEVICE arrays read when the kernels run (so a captured graph can be
- * replayed on new contents), for B of at most 16384 sequences and T below 2^30 rows:
+ * replayed on new contents), for B of at most 8192 sequences and T below 2^30 rows:
  * *   q_offsets [B+1]  the new tokens of sequence b are rows q_offsets[b] .. q_offsets[b+1]
  *                    of Q, K and V (non-decreasing; rows from q_offsets[B] to T belong to
  *                    no sequence and are left alone);

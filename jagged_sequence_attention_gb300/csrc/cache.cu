@@ -66,6 +66,8 @@ constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 // What an item's start and end cost the decode kernel, as bytes of keys and values streamed:
 // about 4 us of a CTA, at its share of the memory's rate.
+// The same for the chunk kernel, in its steps of 128 keys (about 2 us each).
+constexpr int kChunkItemUnits = 3;
 constexpr int kDecodeItemBytes = 98304;
 
 // Whether the cache's device is the current one.
@@ -308,7 +310,8 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
             // the queries as (D, head, token), boxes of one tile's rows
             p.tile_tokens = 128 / p.g;
             p.bm = 2 * p.tile_tokens * p.g;
-            p.min_units = 4;  // a 128-key step is short against an item's start and end
+            p.item_cost = kChunkItemUnits;
+            p.min_units = kChunkItemUnits + 4;
             if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
             CUtensorMap mq;
             const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};

@@ -44,7 +44,7 @@ struct alignas(16) SegRec {
 // (and r <= -31 likewise, from the other side).  Chunks between the two touch |r| <= 93 and
 // read the bias from a table by position; a stride of 4 mod 32 spreads the heads of a warp's
 // rows over the banks.
-constexpr int kThreeBuckets = 62, kNear = 96, kNearStride = 100, kNearHeads = 48;
+constexpr int kThreeBuckets = 62, kNear = 96, kNearStride = 100, kNearHeads = 32;
 
 template <int D>
 struct ChkCfg {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(608, 1)
                 st = cache_find_unit<C::BN>(p, *groups, ng, u, lane);
                 st.u_end = min(groups->total, u + blk);
             }
-            CacheCursor<C::BN> cur(st);
+            CacheCursor<C::BN> cur(st, groups->order);
             while (cur.next(p, g) && taken()) {
                 SegRec r{g.b, g.hk, g.tile, g.k0, g.k1, g.s.q0, g.s.q_len, g.s.kv_len, 0, 0, 0, 0};
                 if (w >= whole) {
@@ -520,14 +520,21 @@ __global__ void __launch_bounds__(608, 1)
                 }
                 if (!wwait(B_S_FULL + x, s_cnt & 1)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t sr[2][32];
-                tmem_ld32(tS, sr[0]);
-                tmem_ld32(tS + 32u, sr[1]);
+                // With a bias one chunk's scores are held at a time, in rolled loops: the three
+                // ways of its lookup would otherwise be laid out four times, and a short item
+                // pays for every line of code it fetches.
+                constexpr int kLive = BIAS ? 1 : 2;
+                uint32_t sr[kLive][32];
+                if (!BIAS) {
+                    tmem_ld32(tS, sr[0]);
+                    tmem_ld32(tS + 32u, sr[kLive - 1]);
+                }
                 // in place: scaled, biased and masked scores of chunk k, minus `shift`
                 auto to_x = [&](uint32_t (&r)[32], int k, float shift) {
                     const int kk = 2 * hf + k;
                     if (!BIAS || (hmask & (1u << k))) {
-                        const float2 sc = make_float2(xs, xs), add = make_float2(cb[k] - shift, cb[k] - shift);
+                        const float c1k = k ? cb[1] : cb[0];
+                        const float2 sc = make_float2(xs, xs), add = make_float2(c1k - shift, c1k - shift);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const float2 t2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc, add);
@@ -568,32 +575,39 @@ __global__ void __launch_bounds__(608, 1)
                         for (int e = 0; e < 32; ++e) r[e] = (e >= lok && e < lk) ? r[e] : __float_as_uint(-INFINITY);
                     }
                 };
-                tmem_ld_wait(sr[0]);
-                tmem_ld_wait(sr[1]);
+                if (!BIAS) {
+                    tmem_ld_wait(sr[0]);
+                    tmem_ld_wait(sr[kLive - 1]);
+                }
                 // pass 1: this half's row maximum, from the raw scores where the bias is one value
                 float mx = -INFINITY;
-#pragma unroll
+#pragma unroll kLive
                 for (int k = 0; k < 2; ++k) {
                     const int kk = 2 * hf + k;
+                    uint32_t(&r)[32] = sr[BIAS ? 0 : k];
+                    if (BIAS) {
+                        tmem_ld32(tS + 32u * k, r);
+                        tmem_ld_wait(r);
+                    }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     const bool vary = BIAS && !(hmask & (1u << k));
                     if (vary) {
-                        to_x(sr[k], k, 0.f);
+                        to_x(r, k, 0.f);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
-                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1]));
+                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
                     } else if (full) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
-                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1]));
+                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
                     } else {
                         const int lk = lim - 32 * kk, lok = lo - 32 * kk;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            m4[e & 3] = fmaxf(m4[e & 3], (e >= lok && e < lk) ? __uint_as_float(sr[k][e]) : -INFINITY);
+                            m4[e & 3] = fmaxf(m4[e & 3], (e >= lok && e < lk) ? __uint_as_float(r[e]) : -INFINITY);
                     }
                     const float mk = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    mx = fmaxf(mx, vary ? mk : fmaf(mk, xs, cb[k]));
+                    mx = fmaxf(mx, vary ? mk : fmaf(mk, xs, (k ? cb[1] : cb[0])));
                 }
                 float mo;
                 if (!exchange(mx, mo)) { ok = false; break; }
@@ -618,28 +632,36 @@ __global__ void __launch_bounds__(608, 1)
                 }
                 // pass 2: P = exp2(x - m), its sum in fp32, and bf16 P over the scores
                 float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                tmem_ld32(tS, sr[0]);  // the raw scores again: cheaper than 64 live registers
-                tmem_ld32(tS + 32u, sr[1]);
-                tmem_ld_wait(sr[0]);
-                tmem_ld_wait(sr[1]);
-#pragma unroll
+                if (!BIAS) {
+                    tmem_ld32(tS, sr[0]);  // the raw scores again: cheaper than 64 live registers
+                    tmem_ld32(tS + 32u, sr[kLive - 1]);
+                    tmem_ld_wait(sr[0]);
+                    tmem_ld_wait(sr[kLive - 1]);
+                }
+#pragma unroll kLive
                 for (int k = 0; k < 2; ++k) {
                     const int kk = 2 * hf + k;
+                    uint32_t(&r)[32] = sr[BIAS ? 0 : k];
+                    const float cbk = k ? cb[1] : cb[0];
+                    if (BIAS) {
+                        tmem_ld32(tS + 32u * k, r);
+                        tmem_ld_wait(r);
+                    }
                     uint32_t pk[16];
                     if (full && (!BIAS || (hmask & (1u << k)))) {
-                        const float2 xs2 = make_float2(xs, xs), add = make_float2(cb[k] - m_use, cb[k] - m_use);
+                        const float2 xs2 = make_float2(xs, xs), add = make_float2(cbk - m_use, cbk - m_use);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float2 t2 = fma2(make_float2(__uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1])), xs2, add);
+                            const float2 t2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), xs2, add);
                             const float2 e2 = make_float2(ex2_approx(t2.x), ex2_approx(t2.y));
                             rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], e2);
                             pk[e >> 1] = pack_bf16x2(e2.x, e2.y);
                         }
                     } else {
-                        to_x(sr[k], k, m_use);
+                        to_x(r, k, m_use);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float2 e2 = make_float2(ex2_approx(__uint_as_float(sr[k][e])), ex2_approx(__uint_as_float(sr[k][e + 1])));
+                            const float2 e2 = make_float2(ex2_approx(__uint_as_float(r[e])), ex2_approx(__uint_as_float(r[e + 1])));
                             rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], e2);
                             pk[e >> 1] = pack_bf16x2(e2.x, e2.y);
                         }

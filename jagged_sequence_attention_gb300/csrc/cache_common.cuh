@@ -19,7 +19,7 @@
 
 namespace jfa {
 
-constexpr int kCacheMaxB = 1 << 14, kCacheMaxGroups = kCacheMaxB / 32;
+constexpr int kCacheMaxB = 1 << 13, kCacheMaxGroups = kCacheMaxB / 32;
 constexpr int kBlocksPerCta = 4;  // chunk kernel: blocks of the last part of the work, per CTA
 constexpr int kMergeCtas = 4;     // CTAs that merge a cut item of it
 constexpr int kMaxSms = 320;
@@ -156,12 +156,17 @@ __device__ __forceinline__ int cache_seq_units(const CacheFwdParams& p, const Ca
     return u;
 }
 
-// The sequence of a lane in group c (32 sequences); the first CTA reports bad ones.
-__device__ __forceinline__ CacheSeq cache_lane_seq(const CacheFwdParams& p, int c, int lane, bool report) {
+// The sequence at place b of an order (a lane number within each group of 32).
+__device__ __forceinline__ int cache_ordered(const uint8_t* order, int b) { return order ? (b & ~31) + order[b] : b; }
+
+// The sequence of a lane in group c (32 sequences, in the batch's order or a given one); the
+// first CTA reports bad ones.
+__device__ __forceinline__ CacheSeq cache_lane_seq(const CacheFwdParams& p, int c, int lane, bool report,
+                                                   const uint8_t* order = nullptr) {
     const int b = 32 * c + lane;
     bool bad = false;
     CacheSeq s{0, 0, 0};
-    if (b < p.B) s = cache_seq(p, b, bad);
+    if (b < p.B) s = cache_seq(p, cache_ordered(order, b), bad);
     if (bad && report) atomicOr(p.status, kStatusBounds);
     return s;
 }
@@ -272,23 +277,26 @@ struct CacheSeg {
     __device__ bool whole() const { return k0 == 0 && k1 == n; }
 };
 
-// Walks a range of units.  Every role of a CTA walks its own copy.
+// Walks a range of units, sequences in the batch's order or a given one (st.b then counts
+// places in that order).  Every role of a CTA walks its own copy.
 template <int BN>
 struct CacheCursor {
     CacheStart st;
     CacheSeq s;
     int nt;
-    __device__ explicit CacheCursor(const CacheStart& start) : st(start), s{0, 0, 0}, nt(-1) {}
+    const uint8_t* order;
+    __device__ explicit CacheCursor(const CacheStart& start, const uint8_t* ord = nullptr)
+        : st(start), s{0, 0, 0}, nt(-1), order(ord) {}
     __device__ bool next(const CacheFwdParams& p, CacheSeg& g) {
         while (st.u < st.u_end) {
             while (nt <= 0) {
                 if (nt == 0) ++st.b;
                 if (st.b >= p.B) return false;
                 bool bad;
-                s = cache_seq(p, st.b, bad);
+                s = cache_seq(p, cache_ordered(order, st.b), bad);
                 nt = cache_tiles(p, s);
             }
-            g.b = st.b;
+            g.b = cache_ordered(order, st.b);
             g.hk = st.hk;
             g.tile = st.tile;
             g.s = s;
@@ -334,7 +342,9 @@ __device__ __forceinline__ int cache_last_cta(const CacheFwdParams& p, const Cac
 // while much work remains, and near the end blocks of `blk` units, which may cut items; the
 // cut items' parts, numbered by block, are merged by a second kernel.  Which units form a piece
 // depends on the lengths alone, so results do not depend on who draws what.
+// The sequences of a group of 32 are taken longest first, so that what is drawn late is short.
 struct CacheGroups {      // shared memory
+    uint8_t order[kCacheMaxB];   // sequences in the order they are worked on, within their group
     int units[kCacheMaxGroups];  // units before the group of 32 sequences
     int items[kCacheMaxGroups];  // items before it
     int total, cut;        // units; the first `whole` items are units [0, cut)
@@ -360,7 +370,7 @@ __device__ __forceinline__ CacheStart cache_find_unit(const CacheFwdParams& p, c
                                                       int lane) {
     CacheStart st{0, 0, 0, 0, u, u, 0, 0};
     const int c = cache_find_group(G.units, groups, u, lane);
-    const CacheSeq s = cache_lane_seq(p, c, lane, false);
+    const CacheSeq s = cache_lane_seq(p, c, lane, false, G.order);
     cache_locate<BN>(p, c, s, cache_seq_units<BN>(p, s, lane), u - G.units[c], lane, st);
     return st;
 }
@@ -370,7 +380,7 @@ __device__ __forceinline__ CacheStart cache_find_item(const CacheFwdParams& p, c
                                                       int lane) {
     CacheStart st{0, 0, 0, 0, 0, 0, 0, 0};
     const int c = cache_find_group(G.items, groups, i, lane);
-    const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false));
+    const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false, G.order));
     const int inc = warp_scan(tiles * p.Hkv, lane);
     int left = i - G.items[c];
     const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
@@ -392,6 +402,14 @@ __device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroup
     for (int c = warp; c < groups; c += warps) {
         const CacheSeq s = cache_lane_seq(p, c, lane, blockIdx.x == 0);
         const int tiles = cache_tiles(p, s);
+        int rank = 0;
+#pragma unroll 8
+        for (int l = 0; l < 32; ++l) {
+            const int kv = __shfl_sync(0xffffffffu, s.kv_len, l);
+            rank += kv > s.kv_len || (kv == s.kv_len && l < lane);
+        }
+        // (lanes past the last sequence hold length 0 and come after every other's tie)
+        if (32 * c + lane < p.B) G->order[32 * c + rank] = uint8_t(lane);
         // a sequence's last item sees the most keys (but for a window's odd tile)
         const int n = __reduce_max_sync(0xffffffffu, tiles > 0 ? cache_units<BN>(p, s, tiles - 1) : 0);
         const int u = __reduce_add_sync(0xffffffffu, cache_seq_units<BN>(p, s, lane));
@@ -419,21 +437,24 @@ __device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroup
         __syncwarp();
         const int grid = gridDim.x, longest = G->longest;
         // The last part, cut in blocks, covers the spread with which the CTAs come out of the
-        // whole items: half an item each.
-        const int rest = int(min((long long)(u), (long long)(grid) * (longest + 1) / 2));
+        // whole items: half an item each, the last ones being of average length or less.  Where
+        // the longest item is over half a CTA's share, everything is cut.
+        const int mean = int(uint32_t(u) / uint32_t(max(items, 1)));
+        const int rest = (long long)(longest) * 2 * grid > u ? u : min(u, grid * ((mean + 1) / 2));
         int cut = 0, whole = 0;
         if (u > rest) {
             const CacheStart st = cache_find_unit<BN>(p, *G, groups, u - rest, lane);
             cut = u - rest - st.kt;
             const int c = st.b >> 5;
-            const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false));
+            const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false, G->order));
             const int before = __reduce_add_sync(0xffffffffu, 32 * c + lane < st.b ? tiles : 0);
             whole = G->items[c] + before * p.Hkv + st.hk * __shfl_sync(0xffffffffu, tiles, st.b & 31) + st.tile;
         }
         const int left = u - cut;
-        // few units: one block a CTA, of at least min_units (or an item); else several
-        const int blk = left <= grid * 8 ? max((left + grid - 1) / grid, min(p.min_units, longest))
-                                         : max(8, (left + kBlocksPerCta * grid - 1) / (kBlocksPerCta * grid));
+        // few units: one block a CTA, of at least min_units (or an item); else up to
+        // kBlocksPerCta of at least eight units
+        const int per = max(1, min(kBlocksPerCta, left / (8 * grid))) * grid;
+        const int blk = max((left + per - 1) / per, min(p.min_units, longest));
         if (lane == 0) {
             G->total = u;
             G->cut = cut;
