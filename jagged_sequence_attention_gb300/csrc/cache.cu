@@ -304,6 +304,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.item_cost = 0;
         p.min_units = 1;
         if (!bf16) {
+            p.item_cost = 1;
             if (!fits(T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
             e = launch_cache_simt(D, true, p, n, st);
         } else {
@@ -327,7 +328,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const CacheFwdParams pc = p;  // the merge's parameters
     p.bm = 16;
     p.min_units = 1;
-    p.item_cost = bf16 ? kDecodeItemBytes / (D * 256) : 0;
+    p.item_cost = bf16 ? kDecodeItemBytes / (D * 256) : 2;
     if (!fits(chunks ? 0 : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
     if (bf16) p.part += cache_chunk_part_bytes(D, n) / sizeof(float);  // the two kernels may run at once
     if (e == cudaSuccess)

@@ -18,12 +18,13 @@ namespace jfa {
 
 namespace {
 
-constexpr int kSimtBN = 64, kSimtThreads = 128;
+constexpr int kSimtBN = 64;
 
 template <int D, int BM>
 struct SimtCfg {
     static constexpr bool kBig = BM == 128;
-    static constexpr int kRows = BM / 4;                  // rows of a warp
+    static constexpr int kWarps = kBig ? 8 : 4, kThreads = 32 * kWarps;
+    static constexpr int kRows = BM / kWarps;             // rows of a warp
     static constexpr int LY = 4, LX = 8;                  // big: lanes 4 (rows) x 8 (keys); small: 1 x 32
     static constexpr int RT = kBig ? kRows / LY : kRows;  // rows of a thread
     static constexpr int KT = kBig ? kSimtBN / LX : 2;    // keys of a thread
@@ -47,10 +48,10 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 template <int D, int BM, bool BIAS>
-__global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_cache_simt_kernel(const CacheFwdParams p) {
+__global__ void __launch_bounds__(SimtCfg<D, BM>::kThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_cache_simt_kernel(const CacheFwdParams p) {
     using C = SimtCfg<D, BM>;
     constexpr int BN = kSimtBN, RT = C::RT, KT = C::KT;
-    // columns of a thread in P V: big: groups of four at 4 kx + 32 j; small: lane + 32 j
+    // columns of a thread in P V: big: groups of four at 4 kx + 32 j; small: NC lane and on
     constexpr int NC = C::kBig ? D / C::LX : D / 32;
     extern __shared__ __align__(16) float sm[];
     __shared__ int last_flag;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
         const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * BM;
         // 64 rows of K or V from position c0 on, zeros where no row of the item may look
         auto load = [&](float* dst, int stride, const void* base, const int64_t* s, int c0) {
-            constexpr int kPieces = D / 4, kStep = kSimtThreads / kPieces;
+            constexpr int kPieces = D / 4, kStep = C::kThreads / kPieces;
             const int c = threadIdx.x % kPieces;
 #pragma unroll 4
             for (int r = threadIdx.x / kPieces; r < BN; r += kStep) {
@@ -96,17 +97,19 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
             load_k(g.k0);
             load_v(g.k0);
         }
-        for (int e = threadIdx.x; e < BM * D / 4; e += kSimtThreads) {
+        for (int e = threadIdx.x; e < BM * D / 4; e += C::kThreads) {
             const int tr = e / (D / 4), c = e % (D / 4), r = r0 + tr;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < R) {
                 const int tok = div_g(p, r);
                 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
                                                      int64_t(g.hk * p.g + r - tok * p.g) * D + 4 * c);
+                v = make_float4(v.x * p.scale_log2, v.y * p.scale_log2, v.z * p.scale_log2, v.w * p.scale_log2);
             }
             *reinterpret_cast<float4*>(sQ + tr * C::kStrideQ + 4 * c) = v;
         }
-        float m[RT], l[RT], o[RT][NC];
+        float m[RT], l[RT];
+        float2 o[RT][(NC + 1) / 2];  // columns in pairs: two products an instruction
         int rel[RT];                 // position of each row (rows past the end repeat the last one's)
         const float* brow[RT];
 #pragma unroll
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+            for (int c = 0; c < (NC + 1) / 2; ++c) o[i][c] = make_float2(0.f, 0.f);
         }
         const int t_first = div_g(p, r0) + diag, t_last = div_g(p, min(R, r0 + BM) - 1) + diag;
         const int all_hi = p.causal ? min(g.s.kv_len, t_first + 1) : g.s.kv_len;
@@ -153,13 +156,15 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
                     const float4 q = *reinterpret_cast<const float4*>(sQ + row_of(i) * C::kStrideQ + d);
+                    // (the keys innermost: consecutive instructions are independent)
 #pragma unroll
-                    for (int j = 0; j < KT; ++j) {
-                        x[i][j] = fmaf(q.x, kk[j].x, x[i][j]);
-                        x[i][j] = fmaf(q.y, kk[j].y, x[i][j]);
-                        x[i][j] = fmaf(q.z, kk[j].z, x[i][j]);
-                        x[i][j] = fmaf(q.w, kk[j].w, x[i][j]);
-                    }
+                    for (int j = 0; j < KT; ++j) x[i][j] = fmaf(q.x, kk[j].x, x[i][j]);
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) x[i][j] = fmaf(q.y, kk[j].y, x[i][j]);
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) x[i][j] = fmaf(q.z, kk[j].z, x[i][j]);
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) x[i][j] = fmaf(q.w, kk[j].w, x[i][j]);
                 }
             }
             if (C::kBufs == 1) {
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
                     const int key = c0 + key_of(j);
                     float add = b1;
                     if (BIAS && !one) add = __ldg(brow[i] + relpos_bucket(rel[i] - key)) * 1.4426950408889634f;
-                    float y = BIAS ? fmaf(x[i][j], p.scale_log2, add) : x[i][j] * p.scale_log2;
+                    float y = BIAS ? x[i][j] + add : x[i][j];
                     if (masked) {
                         const bool in = key < g.s.kv_len && (!p.causal || key <= rel[i]) &&
                                         (p.window < 0 || key >= rel[i] - p.window);
@@ -192,18 +197,18 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
                 for (int s = (C::kBig ? C::LX : 32) / 2; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
                 const float m_new = fmaxf(m[i], mx);
                 const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = exp2f(m[i] - m_use);
+                const float alpha = ex2_approx(m[i] - m_use);
                 m[i] = m_new;
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < KT; ++j) {
-                    const float e = exp2f(x[i][j] - m_use);
+                    const float e = ex2_approx(x[i][j] - m_use);
                     sP[row_of(i) * C::kStrideP + key_of(j)] = e;
                     sum += e;
                 }
                 l[i] = fmaf(l[i], alpha, sum);  // this thread's keys; summed over the lanes at the end
 #pragma unroll
-                for (int c = 0; c < NC; ++c) o[i][c] *= alpha;
+                for (int c = 0; c < (NC + 1) / 2; ++c) o[i][c] = mul2(o[i][c], make_float2(alpha, alpha));
             }
             __syncwarp();
             if (C::kBufs == 1) {
@@ -227,10 +232,8 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
 #pragma unroll
                             for (int i = 0; i < RT; ++i) {
                                 const float w = q == 0 ? e[i].x : q == 1 ? e[i].y : q == 2 ? e[i].z : e[i].w;
-                                o[i][4 * c4] = fmaf(w, v.x, o[i][4 * c4]);
-                                o[i][4 * c4 + 1] = fmaf(w, v.y, o[i][4 * c4 + 1]);
-                                o[i][4 * c4 + 2] = fmaf(w, v.z, o[i][4 * c4 + 2]);
-                                o[i][4 * c4 + 3] = fmaf(w, v.w, o[i][4 * c4 + 3]);
+                                o[i][2 * c4] = fma2(make_float2(w, w), make_float2(v.x, v.y), o[i][2 * c4]);
+                                o[i][2 * c4 + 1] = fma2(make_float2(w, w), make_float2(v.z, v.w), o[i][2 * c4 + 1]);
                             }
                         }
                 }
@@ -243,14 +246,18 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
 #pragma unroll
                     for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sP + row_of(i) * C::kStrideP + j);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q) {
+                        float2 v;  // columns NC lane, NC lane + 1
+                        if constexpr (NC == 2)
+                            v = *reinterpret_cast<const float2*>(sV + (j + q) * D + 2 * lane);
+                        else
+                            v = make_float2(sV[(j + q) * D + lane], 0.f);
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            const float v = sV[(j + q) * D + lane + 32 * c];
-#pragma unroll
-                            for (int i = 0; i < RT; ++i)
-                                o[i][c] = fmaf(q == 0 ? e[i].x : q == 1 ? e[i].y : q == 2 ? e[i].z : e[i].w, v, o[i][c]);
+                        for (int i = 0; i < RT; ++i) {
+                            const float w = q == 0 ? e[i].x : q == 1 ? e[i].y : q == 2 ? e[i].z : e[i].w;
+                            o[i][0] = fma2(make_float2(w, w), v, o[i][0]);
                         }
+                    }
                 }
                 __syncwarp();
             }
@@ -259,38 +266,27 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
         for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int s = (C::kBig ? C::LX : 32) / 2; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
-        // a row's columns as this thread holds them, to dst (times mul) or out of src (added, times w)
-        auto put = [&](float* dst, const float (&v)[NC], float mul) {
+        // a row's columns as this thread holds them, to dst (times mul)
+        auto put = [&](float* dst, const float2 (&v)[(NC + 1) / 2], float mul) {
             if constexpr (C::kBig) {
 #pragma unroll
-                for (int c = 0; c < NC; c += 4)
-                    *reinterpret_cast<float4*>(dst + 4 * kx + 8 * c) =
-                        make_float4(v[c] * mul, v[c + 1] * mul, v[c + 2] * mul, v[c + 3] * mul);
+                for (int c = 0; c < NC / 2; c += 2)
+                    *reinterpret_cast<float4*>(dst + 4 * kx + 16 * c) =
+                        make_float4(v[c].x * mul, v[c].y * mul, v[c + 1].x * mul, v[c + 1].y * mul);
+            } else if constexpr (NC == 2) {
+                *reinterpret_cast<float2*>(dst + 2 * lane) = make_float2(v[0].x * mul, v[0].y * mul);
             } else {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) dst[lane + 32 * c] = v[c] * mul;
+                dst[lane] = v[0].x * mul;
             }
         };
-        auto take = [&](const float* src, float (&v)[NC], float w) {
-            if constexpr (C::kBig) {
-#pragma unroll
-                for (int c = 0; c < NC; c += 4) {
-                    const float4 u = __ldcg(reinterpret_cast<const float4*>(src + 4 * kx + 8 * c));
-                    v[c] = fmaf(u.x, w, v[c]);
-                    v[c + 1] = fmaf(u.y, w, v[c + 1]);
-                    v[c + 2] = fmaf(u.z, w, v[c + 2]);
-                    v[c + 3] = fmaf(u.w, w, v[c + 3]);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) v[c] = fmaf(__ldcg(src + lane + 32 * c), w, v[c]);
-            }
+        auto row_at = [&](int r) {
+            const int tok = div_g(p, r);
+            return size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
         };
-        auto finish = [&](int i, float mm, float ll, const float (&v)[NC]) {
+        auto finish = [&](int i, float mm, float ll, const float2 (&v)[(NC + 1) / 2]) {
             const int r = r0 + row_of(i);
             if (r >= R) return;
-            const int tok = div_g(p, r);
-            const size_t row = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
+            const size_t row = row_at(r);
             put(static_cast<float*>(p.O) + row * D, v, ll > 0.f ? 1.f / ll : 0.f);
             if (p.lse && kx == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
         };
@@ -320,26 +316,61 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<D, BM>::kCtasPerSm) jfa_
         }
         __syncthreads();
         if (!last_flag) continue;
-#pragma unroll 1
-        for (int i = 0; i < RT; ++i) {
-            const int tr = row_of(i);
-            if (r0 + tr >= R) continue;
-            const float* pm = p.part + BM * D + tr;
-            float mm = -INFINITY;
-#pragma unroll 4
-            for (int c = first; c <= last; ++c) mm = fmaxf(mm, __ldcg(pm + size_t(cache_slot(c, first)) * C::kPart));
-            const float mu = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f, v[NC];
+        // The last part to arrive adds them up, in the order of the keys: a warp takes a row, its
+        // lanes the parts' maxima and sums and then D / 32 columns each.
+        constexpr int LC = D / 32, kRowsAtOnce = C::kBig ? 4 : 1;
+        const int parts = last - first + 1, nr = min(BM, R - r0);
+        auto part_of = [&](int c) { return p.part + size_t(cache_slot(first + c, first)) * C::kPart; };
+        for (int t0 = warp * kRowsAtOnce; t0 < nr; t0 += C::kWarps * kRowsAtOnce) {
+            float mm[kRowsAtOnce], ll[kRowsAtOnce], v[kRowsAtOnce][LC];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) v[c] = 0.f;
-#pragma unroll 2
-            for (int c = first; c <= last; ++c) {
-                const float* part = p.part + size_t(cache_slot(c, first)) * C::kPart;
-                const float w = exp2f(__ldcg(part + BM * D + tr) - mu);
-                ll = fmaf(__ldcg(part + BM * D + BM + tr), w, ll);
-                take(part + tr * D, v, w);
+            for (int k = 0; k < kRowsAtOnce; ++k) {
+                const int tr = min(t0 + k, nr - 1);
+                mm[k] = -INFINITY;
+                ll[k] = 0.f;
+                for (int c = lane; c < parts; c += 32) mm[k] = fmaxf(mm[k], __ldcg(part_of(c) + BM * D + tr));
+#pragma unroll
+                for (int c = 0; c < LC; ++c) v[k][c] = 0.f;
             }
-            finish(i, mm, ll, v);
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k)
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) mm[k] = fmaxf(mm[k], __shfl_xor_sync(0xffffffffu, mm[k], s));
+            for (int c0 = 0; c0 < parts; c0 += 32) {
+                float w[kRowsAtOnce];
+#pragma unroll
+                for (int k = 0; k < kRowsAtOnce; ++k) {
+                    const int tr = min(t0 + k, nr - 1);
+                    const float mc = c0 + lane < parts ? __ldcg(part_of(c0 + lane) + BM * D + tr) : -INFINITY;
+                    w[k] = mc == -INFINITY ? 0.f : ex2_approx(mc - mm[k]);
+                    if (c0 + lane < parts) ll[k] = fmaf(__ldcg(part_of(c0 + lane) + BM * D + BM + tr), w[k], ll[k]);
+                }
+#pragma unroll 4
+                for (int c = 0; c < min(32, parts - c0); ++c)
+#pragma unroll
+                    for (int k = 0; k < kRowsAtOnce; ++k) {
+                        const float wc = __shfl_sync(0xffffffffu, w[k], c);
+                        const float* src = part_of(c0 + c) + min(t0 + k, nr - 1) * D + LC * lane;
+                        if constexpr (LC == 2) {
+                            const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
+                            v[k][0] = fmaf(u.x, wc, v[k][0]);
+                            v[k][LC - 1] = fmaf(u.y, wc, v[k][LC - 1]);
+                        } else {
+                            v[k][0] = fmaf(__ldcg(src), wc, v[k][0]);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k) {
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) ll[k] += __shfl_xor_sync(0xffffffffu, ll[k], s);
+                if (t0 + k >= nr) continue;
+                const size_t row = row_at(r0 + t0 + k);
+                const float inv = ll[k] > 0.f ? 1.f / ll[k] : 0.f;
+#pragma unroll
+                for (int c = 0; c < LC; ++c) static_cast<float*>(p.O)[row * D + LC * lane + c] = v[k][c] * inv;
+                if (p.lse && lane == 0) p.lse[row] = ll[k] > 0.f ? (mm[k] + log2f(ll[k])) * 0.6931471805599453f : -INFINITY;
+            }
         }
     }
 }
@@ -350,7 +381,7 @@ cudaError_t launch(const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(jfa_cache_simt_kernel<D, BM, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kBytes);
     if (e != cudaSuccess) return e;
-    jfa_cache_simt_kernel<D, BM, BIAS><<<num_sms * C::kCtasPerSm, kSimtThreads, C::kBytes, st>>>(p);
+    jfa_cache_simt_kernel<D, BM, BIAS><<<num_sms * C::kCtasPerSm, C::kThreads, C::kBytes, st>>>(p);
     return cudaGetLastError();
 }
 
