@@ -3,7 +3,9 @@
 Each translation unit compiles in its own process; the objects link into
 ``jagged_sequence_attention_gb300/libjfa.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU driver (tests that
-only need the host planner) and only needs the driver when a CUDA call runs.
+only need the host planner) and only needs the driver when a CUDA call runs.  The
+paged cache's compiled Python calls are built beside it (``_cache_calls.so``, host code
+against torch's headers).
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libjfa.so")
+CALLS = os.path.join(PKG, "_cache_calls.so")  # compiled Python calls of the paged cache
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "plan.cpp", "fwd.cu", "fwd_short.cu", "fwd_pack.cu", "bwd.cu", "bwd_dq.cu", "bwd_fused.cu", "bwd_short.cu", "f32.cu", "static_scratch.cu",
@@ -49,12 +52,34 @@ def _digest(extra) -> str:
     return h.hexdigest()
 
 
+def _calls_command(out: str):
+    """The compile command of the Python extension (host code only, against torch's headers)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], INCLUDE, "/usr/local/cuda/include", os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{i}" for i in inc]
+            + [os.path.join(CSRC, "cache_calls.cpp"), "-o", out, "-L" + os.path.join(root, "lib"), "-lc10",
+               "-lc10_cuda", "-ltorch_python", "-ltorch_cpu", "-ltorch"])
+
+
+def _build_calls():
+    tmp = CALLS + f".tmp{os.getpid()}"
+    r = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: cache_calls.cpp\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
     """Compile (if sources changed) and return the path of libjfa.so."""
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "libjfa.stamp")
-    dig = _digest(extra_flags)
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    dig = _digest(extra_flags) + " ".join(_calls_command(CALLS))
+    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == dig:
                 return LIB
@@ -72,8 +97,10 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
             raise RuntimeError(f"compile failed: {src}\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(compile_one, SOURCES))
+        calls.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, err in results:

@@ -47,6 +47,7 @@ class JFAError(RuntimeError):
 
 
 _lib = None
+_calls = None  # the compiled paged-cache calls (csrc/cache_calls.cpp)
 
 
 def lib():
@@ -57,6 +58,17 @@ def lib():
             raise RuntimeError(f"libjfa.so is not built ({_LIB_PATH}); run __graft_entry__.build()")
         _lib = load_library(_LIB_PATH)
     return _lib
+
+
+def _cache_calls():
+    """Load the compiled paged-cache calls; raises if they have not been built."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        from . import _cache_calls as m
+        m.set_calls(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.jfa_cache_append, L.jfa_cache_fwd)))
+        _calls = m
+    return _calls
 
 
 def load_library(path):
@@ -438,7 +450,8 @@ class Cache:
     def __init__(self, handle, K, V):
         self.handle, self.K, self.V = handle, K, V
         self.n_pages, self.page_size, self.Hkv, self.D = K.shape
-        self.dtype, self.device, self.device_index = K.dtype, K.device, K.get_device()
+        self.dtype, self.device = K.dtype, K.device
+        self.info = _cache_calls().describe(handle.value or 0, K)  # what the compiled calls check against
 
     def __del__(self):
         try:
@@ -473,46 +486,11 @@ def jfa_cache_create(K: torch.Tensor, V: torch.Tensor, stream=None) -> Cache:
 def jfa_cache_destroy(cache: Cache):
     if cache.handle is not None:
         _check("jfa_cache_destroy", lib().jfa_cache_destroy(cache.handle))
-        cache.handle = None
+        cache.handle = cache.info = None
 
 
 def jfa_cache_device_status(cache: Cache, stream=None) -> int:
     return int(lib().jfa_cache_device_status(cache.handle, _stream(stream)))
-
-
-# The two calls of a served step run once per layer and token, and a small one takes a few
-# microseconds on the GPU: the checks below read each tensor's attributes once.
-
-def _cache_batch(fn: str, cache: Cache, q_offsets, kv_lens, page_table):
-    """(B, max_pages) of a batch's device arrays."""
-    dev, i32 = cache.device_index, torch.int32
-    shape = page_table.shape
-    if len(shape) != 2 or (kv_lens.numel(),) != shape[:1] or q_offsets.numel() != shape[0] + 1:
-        _bad(fn, "q_offsets [B + 1], kv_lens [B] and page_table [B, max_pages] disagree")
-    if not (q_offsets.dtype is kv_lens.dtype is page_table.dtype is i32
-            and q_offsets.get_device() == kv_lens.get_device() == page_table.get_device() == dev
-            and q_offsets.is_contiguous() and kv_lens.is_contiguous() and page_table.is_contiguous()):
-        _bad(fn, "q_offsets, kv_lens and page_table must be contiguous int32 tensors on the cache's device")
-    return shape
-
-
-def _cache_rows(fn: str, cache: Cache, t: torch.Tensor, heads, T=None):
-    """The token stride of [T, heads, D] rows whose heads are dense."""
-    shape, D = t.shape, cache.D
-    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads) or \
-            (T is not None and shape[0] != T) or t.dtype is not cache.dtype or t.get_device() != cache.device_index:
-        _bad(fn, "rows must be [T, heads, D] in the cache's type, on its device")
-    n, h, _ = shape
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 or (h > 1 and s1 != D)) and n * h:
-        _bad(fn, "the heads of a row must be dense")
-    # one token (or none): torch leaves its stride free
-    return s0 if n > 1 else h * D
-
-
-def _cache_stream(cache: Cache, stream):
-    """The stream's handle: the given one's, or the current one of the cache's device."""
-    return torch.cuda.current_stream(cache.device).cuda_stream if stream is None else stream.cuda_stream
 
 
 def jfa_cache_append(cache: Cache, K, V, q_offsets, kv_lens, page_table, Q=None, Q_out=None, rot=None,
@@ -520,35 +498,16 @@ def jfa_cache_append(cache: Cache, K, V, q_offsets, kv_lens, page_table, Q=None,
     """Appends the new tokens' K, V [T, Hkv, D] to their slots.  rot: the rotation's table
     [rot_len, rot_dim] (cosines, then sines, fp32), applied to the keys and to Q [T, H, D]
     (into Q_out, which may be Q; allocated if None).  Returns Q_out (None without Q)."""
-    fn = "jfa_cache_append"
-    B, max_pages = _cache_batch(fn, cache, q_offsets, kv_lens, page_table)
-    ks = _cache_rows(fn, cache, K, cache.Hkv)
-    T = K.shape[0]
-    vs = _cache_rows(fn, cache, V, cache.Hkv, T)
-    H, qs, qos, qp, qop = 1, 0, 0, None, None
-    if Q is not None:
-        qs = _cache_rows(fn, cache, Q, None, T)
-        H = Q.shape[1]
-        if Q_out is None:
-            Q_out = torch.empty((T, H, cache.D), dtype=Q.dtype, device=Q.device)
-        qos = _cache_rows(fn, cache, Q_out, H, T)
-        qp, qop = Q.data_ptr(), Q_out.data_ptr()
-    elif Q_out is not None:
-        _bad(fn, "Q_out without Q")
-    rp, rot_dim, rot_len = None, 0, 0
-    if rot is not None:
-        shape = rot.shape
-        if len(shape) != 2 or rot.dtype is not torch.float32 or rot.get_device() != cache.device_index or \
-                not rot.is_contiguous():
-            _bad(fn, "rot must be a contiguous fp32 tensor [rot_len, rot_dim] on the cache's device")
-        rot_len, rot_dim = shape
-        rp = rot.data_ptr()
-    kind = ROT_KINDS.get(rot_kind, -1) if isinstance(rot_kind, str) else int(rot_kind)
-    status = lib().jfa_cache_append(cache.handle, B, T, q_offsets.data_ptr(), kv_lens.data_ptr(),
-                                    page_table.data_ptr(), max_pages, K.data_ptr(), ks, V.data_ptr(), vs, qp, qs, H,
-                                    qop, qos, rp, rot_dim, rot_len, kind, _cache_stream(cache, stream))
+    if Q is not None and Q_out is None:
+        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    try:
+        status = _calls.append(cache.info, K, V, q_offsets, kv_lens, page_table, Q, Q_out, rot,
+                               ROT_KINDS.get(rot_kind, -1) if isinstance(rot_kind, str) else rot_kind,
+                               None if stream is None else stream.cuda_stream)
+    except (ValueError, TypeError) as e:
+        raise JFAError(f"jfa_cache_append ({e})", JFA_ERR_INVALID_ARG) from None
     if status != JFA_OK:
-        raise JFAError(fn, status)
+        raise JFAError("jfa_cache_append", status)
     return Q_out
 
 
@@ -572,41 +531,25 @@ def jfa_cache_fwd(cache: Cache, Q, q_offsets, kv_lens, page_table, bias=None, sc
     """Attention of the new tokens Q [T, H, D] over the cache.  Returns (O, lse).  bias: the
     bucket table [H, 32]; max_q_len: an upper bound of the batch's query lengths (it chooses
     the kernel); workspace: jfa_cache_workspace's, kept by the caller (one is made if None)."""
-    fn = "jfa_cache_fwd"
-    B, max_pages = _cache_batch(fn, cache, q_offsets, kv_lens, page_table)
-    qs = _cache_rows(fn, cache, Q, None)
-    shape, dev = Q.shape, cache.device_index
-    T, H, D = shape
     if O is None:
-        O = torch.empty(shape, dtype=out_dtype or Q.dtype, device=Q.device)
-    elif O.shape != shape or not O.is_contiguous() or O.get_device() != dev:
-        _bad(fn, "O must be a contiguous tensor of Q's shape")
+        O = torch.empty(Q.shape, dtype=out_dtype or Q.dtype, device=Q.device)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=Q.device)
-    elif lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous() or \
-            lse.get_device() != dev:
-        _bad(fn, "lse must be a contiguous fp32 tensor [T, H]")
-    bp, kind = None, JFA_BIAS_NONE
-    if bias is not None:
-        if bias.dtype is not torch.float32 or bias.shape != (H, 32) or not bias.is_contiguous() or \
-                bias.get_device() != dev:
-            _bad(fn, "bias must be a contiguous fp32 tensor [H, 32]")
-        bp, kind = bias.data_ptr(), JFA_BIAS_RELPOS32
+        lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
     if workspace is None:
+        H = Q.shape[1] if Q.dim() == 3 else 0
         if stream is not None:
             with torch.cuda.stream(stream):
                 workspace = jfa_cache_workspace(cache, H)
         else:
             workspace = jfa_cache_workspace(cache, H)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        _bad(fn, "workspace must be a contiguous tensor on the cache's device")
-    status = lib().jfa_cache_fwd(cache.handle, B, T, 0 if max_q_len is None else int(max_q_len), q_offsets.data_ptr(),
-                                 kv_lens.data_ptr(), page_table.data_ptr(), max_pages, Q.data_ptr(), qs, H,
-                                 1 if causal else 0, -1 if window is None else int(window), kind, bp,
-                                 D ** -0.5 if scale is None else float(scale), O.data_ptr(), _dtype_code(O),
-                                 lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _cache_stream(cache, stream))
+    try:
+        status = _calls.fwd(cache.info, Q, q_offsets, kv_lens, page_table, bias,
+                            cache.D ** -0.5 if scale is None else scale, causal, window, max_q_len, O, lse, workspace,
+                            None if stream is None else stream.cuda_stream)
+    except (ValueError, TypeError) as e:
+        raise JFAError(f"jfa_cache_fwd ({e})", JFA_ERR_INVALID_ARG) from None
     if status != JFA_OK:
-        raise JFAError(fn, status)
+        raise JFAError("jfa_cache_fwd", status)
     return O, lse
 
 

@@ -56,19 +56,47 @@ def test_binding_refuses_what_it_would_misread(jfa):
     with pytest.raises(jfa.JFAError) as e:  # host tensors
         jfa.jfa_cache_create(K, K)
     assert e.value.status == jfa.JFA_ERR_INVALID_ARG
-    cache = jfa.Cache(None, K, K)
+    # on host tensors every check of the compiled calls passes or fails as it would on a GPU; a
+    # call that passes them reaches the library, which refuses the null handle
+    cache = jfa.Cache(ctypes.c_void_p(), K, K)
+    calls = jfa._cache_calls()
     off, kv, table = (torch.zeros(n, dtype=torch.int32) for n in (3, 2, 10))
     table = table.view(2, 5)
-    assert jfa._cache_batch("f", cache, off, kv, table) == (2, 5)
-    for a in ((off.long(), kv, table), (off[:2], kv, table), (off, kv, table.view(-1)), (off, kv, table.t()),
-              (off, kv, table[:1]), (off, kv, torch.zeros(2, 10, dtype=torch.int32)[:, ::2])):
-        with pytest.raises(jfa.JFAError):
-            jfa._cache_batch("f", cache, *a)
     wide = torch.zeros(7, 8, 64, dtype=torch.bfloat16)
-    assert jfa._cache_rows("f", cache, wide, 8) == 512
-    assert jfa._cache_rows("f", cache, wide[:, 2:4], 2) == 512     # a slice of a fused projection
-    assert jfa._cache_rows("f", cache, wide[:1, 2:4], 2) == 128    # one token: its stride says nothing
-    for t, heads in ((wide, 4), (wide.float(), 8), (wide[..., :32], 8), (wide[:, ::2], 4), (wide.transpose(0, 1), 7),
-                     (wide[:, :, ::2], 8)):
-        with pytest.raises(jfa.JFAError):
-            jfa._cache_rows("f", cache, t, heads)
+    k, v, q, rot = wide[:, 2:4], wide[:, 4:6], wide[:, :2], torch.zeros(9, 32)
+    good = dict(K=k, V=v, off=off, kv=kv, table=table, Q=q, Qo=q.clone(), rot=rot, kind=0, stream=0)
+
+    def append(**kw):
+        a = dict(good, **kw)
+        return calls.append(cache.info, *(a[n] for n in good))
+
+    bad = jfa.JFA_ERR_INVALID_ARG
+    assert append() == bad and append(Q=None, Qo=None) == bad and append(K=k[:1], V=v[:1], Q=q[:1], Qo=q[:1]) == bad
+    for kw in (dict(off=off.long()), dict(off=off[:2]), dict(table=table.view(-1)), dict(table=table.t()),
+               dict(table=table[:1]), dict(table=torch.zeros(2, 10, dtype=torch.int32)[:, ::2]), dict(K=wide),
+               dict(K=k.float()), dict(K=k[..., :32]), dict(K=wide[:, ::4]), dict(V=v[:3]), dict(Q=q.transpose(0, 1)),
+               dict(Qo=q[:, :1]), dict(Qo=None), dict(Q=None), dict(rot=rot.double()), dict(rot=rot.t()),
+               dict(K=None), dict(kind=None)):
+        with pytest.raises((ValueError, TypeError)):
+            append(**kw)
+    fgood = dict(Q=q, off=off, kv=kv, table=table, bias=torch.zeros(2, 32), scale=0.1, causal=True, window=None, n=None,
+                 O=torch.zeros(7, 2, 64), lse=torch.zeros(7, 2), ws=torch.zeros(8, dtype=torch.uint8), stream=0)
+
+    def fwd(**kw):
+        a = dict(fgood, **kw)
+        return calls.fwd(cache.info, *(a[n] for n in fgood))
+
+    assert fwd() == bad and fwd(bias=None, window=3, n=7) == bad
+    assert fwd(O=torch.zeros(7, 2, 64, dtype=torch.float16)) == jfa.JFA_ERR_UNSUPPORTED
+    for kw in (dict(kv=kv.long()), dict(Q=q.double()), dict(Q=wide[0]), dict(bias=torch.zeros(2, 31)),
+               dict(bias=torch.zeros(3, 32)), dict(O=torch.zeros(7, 3, 64)), dict(O=torch.zeros(2, 7, 64).transpose(0, 1)),
+               dict(lse=torch.zeros(7)), dict(lse=torch.zeros(7, 2).double()), dict(ws=torch.zeros(8, 2).t()),
+               dict(scale=None), dict(window=1.5), dict(O=None)):
+        with pytest.raises((ValueError, TypeError)):
+            fwd(**kw)
+    with pytest.raises(jfa.JFAError) as e:  # the public call, with the binding's own error
+        jfa.jfa_cache_append(cache, wide, v, off, kv, table)
+    assert e.value.status == bad
+    cache.handle = cache.info = None        # as after jfa_cache_destroy
+    with pytest.raises(jfa.JFAError):
+        jfa.jfa_cache_append(cache, k, v, off, kv, table)
