@@ -44,7 +44,7 @@ class Case:
         self.n_pages = n_pages
 
         def normal(*s):
-            return (torch.randn(*s, generator=g, device=device) * std).to(dtype)
+            return (torch.randn(*s, generator=g, device=device, dtype=torch.float32) * std).to(dtype)
 
         if layout == "tokens":
             self.Kc, self.Vc = normal(n_pages, page, Hkv, D), normal(n_pages, page, Hkv, D)
@@ -79,7 +79,7 @@ class Case:
         T = int(q.sum())
         self.T = T
         self.Q = normal(T + pad_rows, H, D)
-        self.bias = torch.randn(H, 32, generator=g, device=device) * 0.5 if bias else None
+        self.bias = torch.randn(H, 32, generator=g, device=device, dtype=torch.float32) * 0.5 if bias else None
         self.q_off = torch.tensor(np.concatenate([[0], np.cumsum(q)]), dtype=torch.int32, device=device)
         self.kv_lens = torch.tensor(kv, dtype=torch.int32, device=device)
         self.table = torch.from_numpy(table).to(device)

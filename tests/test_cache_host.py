@@ -6,6 +6,8 @@ import ctypes
 import pytest
 import torch
 
+F32 = torch.float32
+
 from jagged_sequence_attention_gb300 import _build
 
 
@@ -63,7 +65,7 @@ def test_binding_refuses_what_it_would_misread(jfa):
     off, kv, table = (torch.zeros(n, dtype=torch.int32) for n in (3, 2, 10))
     table = table.view(2, 5)
     wide = torch.zeros(7, 8, 64, dtype=torch.bfloat16)
-    k, v, q, rot = wide[:, 2:4], wide[:, 4:6], wide[:, :2], torch.zeros(9, 32)
+    k, v, q, rot = wide[:, 2:4], wide[:, 4:6], wide[:, :2], torch.zeros(9, 32, dtype=F32)
     good = dict(K=k, V=v, off=off, kv=kv, table=table, Q=q, Qo=q.clone(), rot=rot, kind=0, stream=0)
 
     def append(**kw):
@@ -79,8 +81,8 @@ def test_binding_refuses_what_it_would_misread(jfa):
                dict(K=None), dict(kind=None)):
         with pytest.raises((ValueError, TypeError)):
             append(**kw)
-    fgood = dict(Q=q, off=off, kv=kv, table=table, bias=torch.zeros(2, 32), scale=0.1, causal=True, window=None, n=None,
-                 O=torch.zeros(7, 2, 64), lse=torch.zeros(7, 2), ws=torch.zeros(8, dtype=torch.uint8), stream=0)
+    fgood = dict(Q=q, off=off, kv=kv, table=table, bias=torch.zeros(2, 32, dtype=F32), scale=0.1, causal=True, window=None, n=None,
+                 O=torch.zeros(7, 2, 64, dtype=F32), lse=torch.zeros(7, 2, dtype=F32), ws=torch.zeros(8, dtype=torch.uint8), stream=0)
 
     def fwd(**kw):
         a = dict(fgood, **kw)
@@ -88,9 +90,9 @@ def test_binding_refuses_what_it_would_misread(jfa):
 
     assert fwd() == bad and fwd(bias=None, window=3, n=7) == bad
     assert fwd(O=torch.zeros(7, 2, 64, dtype=torch.float16)) == jfa.JFA_ERR_UNSUPPORTED
-    for kw in (dict(kv=kv.long()), dict(Q=q.double()), dict(Q=wide[0]), dict(bias=torch.zeros(2, 31)),
-               dict(bias=torch.zeros(3, 32)), dict(O=torch.zeros(7, 3, 64)), dict(O=torch.zeros(2, 7, 64).transpose(0, 1)),
-               dict(lse=torch.zeros(7)), dict(lse=torch.zeros(7, 2).double()), dict(ws=torch.zeros(8, 2).t()),
+    for kw in (dict(kv=kv.long()), dict(Q=q.double()), dict(Q=wide[0]), dict(bias=torch.zeros(2, 31, dtype=F32)),
+               dict(bias=torch.zeros(3, 32, dtype=F32)), dict(O=torch.zeros(7, 3, 64, dtype=F32)), dict(O=torch.zeros(2, 7, 64, dtype=F32).transpose(0, 1)),
+               dict(lse=torch.zeros(7, dtype=F32)), dict(lse=torch.zeros(7, 2, dtype=F32).double()), dict(ws=torch.zeros(8, 2, dtype=F32).t()),
                dict(scale=None), dict(window=1.5), dict(O=None)):
         with pytest.raises((ValueError, TypeError)):
             fwd(**kw)

@@ -126,7 +126,7 @@ def test_rows_behind_the_last_sequence_are_left(jfa):
         for lens in (SINGLE, CHUNKS):
             c = Case(*lens, H=4, Hkv=2, D=D, page=16, dtype=dtype, pad_rows=19, seed=11)
             O = torch.full_like(c.Q, 7.0)
-            lse = torch.full((c.T + 19, 4), 9.0, device="cuda")
+            lse = torch.full((c.T + 19, 4), 9.0, device="cuda", dtype=F32)
             c.run(jfa, O=O, lse=lse)
             assert bool((O[c.T:] == 7.0).all()) and bool((lse[c.T:] == 9.0).all())
             c.check(O, lse)
@@ -217,8 +217,8 @@ def append_case(q, kv, *, H, Hkv, D, page, dtype, R, kind, layout="tokens", seed
     c = Case(q, kv, H=H, Hkv=Hkv, D=D, page=page, dtype=dtype, layout=layout, unset=False, seed=seed,
              pad_rows=pad_rows)
     g = torch.Generator(device="cuda").manual_seed(seed)
-    c.K = torch.randn(c.T + pad_rows, Hkv, D, generator=g, device="cuda").to(dtype)
-    c.V = torch.randn(c.T + pad_rows, Hkv, D, generator=g, device="cuda").to(dtype)
+    c.K = torch.randn(c.T + pad_rows, Hkv, D, generator=g, device="cuda", dtype=F32).to(dtype)
+    c.V = torch.randn(c.T + pad_rows, Hkv, D, generator=g, device="cuda", dtype=F32).to(dtype)
     c.rot = make_table(max(1, int(max(kv))), R) if R else None
     c.kind = kind
     return c
@@ -334,8 +334,8 @@ def test_served_steps_equal_the_whole_sequence(jfa, dtype, D):
     lens = [150, 71, 5]
     B, T = len(lens), sum(lens)
     off = np.concatenate([[0], np.cumsum(lens)])
-    X = {n: torch.randn(T, h, D, generator=g, device="cuda").to(dtype) for n, h in (("Q", H), ("K", Hkv), ("V", Hkv))}
-    rot, bias = make_table(max(lens), R), torch.randn(H, 32, generator=g, device="cuda")
+    X = {n: torch.randn(T, h, D, generator=g, device="cuda", dtype=F32).to(dtype) for n, h in (("Q", H), ("K", Hkv), ("V", Hkv))}
+    rot, bias = make_table(max(lens), R), torch.randn(H, 32, generator=g, device="cuda", dtype=F32)
     n_pages = sum(-(-n // page) for n in lens)
     Kc = torch.full((n_pages, page, Hkv, D), float("nan"), dtype=dtype, device="cuda")
     Vc = torch.full_like(Kc, float("nan"))
@@ -378,7 +378,7 @@ def test_a_captured_step_is_replayed_on_new_contents(jfa):
     table = torch.randperm(n * B, device="cuda").int().view(B, n).contiguous()
     cache = jfa.jfa_cache_create(Kc, Vc)
     ws = jfa.jfa_cache_workspace(cache, H)
-    O, lse, q = torch.empty_like(c.Q), torch.empty(B, H, device="cuda"), torch.empty_like(c.Q)
+    O, lse, q = torch.empty_like(c.Q), torch.empty(B, H, device="cuda", dtype=F32), torch.empty_like(c.Q)
 
     def step():
         jfa.jfa_cache_append(cache, c.K, c.V, c.q_off, c.kv_lens, table, Q=c.Q, Q_out=q, rot=c.rot)
@@ -457,10 +457,10 @@ def test_refusals(jfa):
     assert fwd(q_offsets=c.q_off.long()) == bad and fwd(page_table=c.table[:1]) == bad
     assert fwd(kv_lens=c.kv_lens.cpu()) == bad
     assert fwd(workspace=ws[:-256]) == bad and fwd(workspace=ws[16:]) == bad
-    assert fwd(bias=torch.zeros(4, 31, device="cuda")) == bad
+    assert fwd(bias=torch.zeros(4, 31, device="cuda", dtype=F32)) == bad
     assert fwd(O=torch.empty(6, 4, 64, dtype=torch.float16, device="cuda")) == uns
     assert app(Q=None) == jfa.JFA_OK and app(rot=None) == bad and app(Q=None, rot=None) == jfa.JFA_OK
-    assert app(rot=torch.zeros(60, 24, device="cuda")) == bad and app(rot=torch.zeros(60, 80, device="cuda")) == bad
+    assert app(rot=torch.zeros(60, 24, device="cuda", dtype=F32)) == bad and app(rot=torch.zeros(60, 80, device="cuda", dtype=F32)) == bad
     assert app(rot_kind="other") == bad and app(V=c.V[:3]) == bad and app(Q_out=c.Q[:3]) == bad
     L = jfa.lib()
     # a dense bias is not read through a page table
