@@ -64,11 +64,11 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
 
 constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
-// What an item's start and end cost the decode kernel, as bytes of keys and values streamed:
-// about 4 us of a CTA, at its share of the memory's rate.
+// What an item's start and end cost the decode kernel, in its stages of 32 KB: about 4 us of a
+// CTA, at its share of the memory's rate.
 // The same for the chunk kernel, in its steps of 128 keys (about 2 us each).
 constexpr int kChunkItemUnits = 3;
-constexpr int kDecodeItemBytes = 98304;
+constexpr int kDecodeItemUnits = 3;
 
 // Whether the cache's device is the current one.
 bool on_device(jfa_cache c) {
@@ -328,7 +328,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const CacheFwdParams pc = p;  // the merge's parameters
     p.bm = 16;
     p.min_units = 1;
-    p.item_cost = bf16 ? kDecodeItemBytes / (D * 256) : 2;
+    p.item_cost = bf16 ? kDecodeItemUnits : 2;
     if (!fits(chunks ? 0 : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
     if (bf16) p.part += cache_chunk_part_bytes(D, n) / sizeof(float);  // the two kernels may run at once
     if (e == cudaSuccess)

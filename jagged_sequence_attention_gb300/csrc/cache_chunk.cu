@@ -11,7 +11,7 @@
 // memory.
 //   warps 0-3, 8-11    tile A, columns [0, 64) and [64, 128): softmax, rescaling, epilogue
 //   warps 4-7, 12-15   tile B
-//   warp 16            TMA loads: Q once per item, K and V boxes through 2-stage rings
+//   warp 16            TMA loads: Q once per item, K and V boxes through rings
 //   warp 17            tcgen05.mma issuer and TMEM owner; clears V rows no query may see
 //   warp 18            draws pieces of work ahead of the others and hands out their items
 // TMEM (512 columns): S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P
@@ -51,9 +51,12 @@ struct ChkCfg {
     static constexpr int BM = 128, BN = 128, kPair = 2 * BM;
     static constexpr int kCB = D / 64;
     static constexpr int kQBytes = BM * D * 2, kKVBytes = BN * D * 2;
-    static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + 2 * kKVBytes;
-    static constexpr int kOffBar = kOffV + 2 * kKVBytes;
-    static constexpr int kNumBars = 32;
+    // K and V rings: what shared memory holds (a short item's keys come from DRAM, and two
+    // stages of 16 KB in flight would not keep up with it)
+    static constexpr int kStages = D == 128 ? 2 : 5;
+    static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + kStages * kKVBytes;
+    static constexpr int kOffBar = kOffV + kStages * kKVBytes;
+    static constexpr int kNumBars = 48;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag, merge flag
     static constexpr int kOffSeg = kOffMisc + 16;             // the part of an item handed out next
     static constexpr int kOffStarts = kOffSeg + int(sizeof(SegRec));  // first position of each bias bucket
@@ -77,19 +80,19 @@ struct ChkCfg {
 enum {
     B_Q_FULL = 0,
     B_Q_EMPTY = 1,
-    B_K_FULL = 2,   // +stage
-    B_K_EMPTY = 4,
-    B_V_FULL = 6,
-    B_V_EMPTY = 8,
-    B_S_FULL = 10,  // +tile
-    B_P_FULL = 12,
-    B_O_DONE = 14,
-    B_O_EMPTY = 16,
-    B_DRAIN = 18,
-    B_COMBINE = 19,  // split item: tile B's last P V done and its m and l written
-    B_XCH = 20,      // +pair of warps
-    B_SEG_FULL = 28,   // the next part of an item handed out
-    B_SEG_EMPTY = 29,  // and read by every other warp
+    B_S_FULL = 2,    // +tile
+    B_P_FULL = 4,
+    B_O_DONE = 6,
+    B_O_EMPTY = 8,
+    B_DRAIN = 10,
+    B_COMBINE = 11,  // split item: tile B's last P V done and its m and l written
+    B_SEG_FULL = 12,   // the next part of an item handed out
+    B_SEG_EMPTY = 13,  // and read by every other warp
+    B_XCH = 14,      // +pair of warps
+    B_K_FULL = 22,   // +stage (up to 6)
+    B_K_EMPTY = 28,
+    B_V_FULL = 34,
+    B_V_EMPTY = 40,
 };
 
 // TMEM column (within a tile's S/P columns) of the 16 P values of P V step s.
@@ -142,11 +145,13 @@ __global__ void __launch_bounds__(608, 1)
     if (threadIdx.x == 0) {
         mbar_init(bar(B_Q_FULL), 1);
         mbar_init(bar(B_Q_EMPTY), 1);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(B_K_FULL + s), 1);
             mbar_init(bar(B_K_EMPTY + s), 1);
             mbar_init(bar(B_V_FULL + s), 1);
             mbar_init(bar(B_V_EMPTY + s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(bar(B_S_FULL + s), 1);
             mbar_init(bar(B_P_FULL + s), 8);
             mbar_init(bar(B_O_DONE + s), 1);
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(608, 1)
             ++item_it;
             int page = page_of(g, g.k0);
             for (int k = g.k0; k < g.k1; ++k, ++kv_it) {
-                const uint32_t st = kv_it & 1, ph = (kv_it >> 1) & 1;
+                const uint32_t st = kv_it % C::kStages, ph = (kv_it / C::kStages) & 1;
                 const int at = page, slot = ((g.r.f + k) * C::BN + pg * rows) & ((1 << p.page_log2) - 1);
                 const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, at >= 0)) * rows * 128);
                 if (k + 1 < g.k1) page = page_of(g, k + 1);
@@ -269,8 +274,8 @@ __global__ void __launch_bounds__(608, 1)
         }
         if (!ok && lane == 0) fail();
         if (item_it > 0) mbar_wait_bounded(bar(B_Q_FULL), (item_it - 1) & 1, nullptr);
-        drain_ring(bar(B_K_FULL), kv_it + k_extra, 2);
-        drain_ring(bar(B_V_FULL), kv_it, 2);
+        drain_ring(bar(B_K_FULL), kv_it + k_extra, C::kStages);
+        drain_ring(bar(B_V_FULL), kv_it, C::kStages);
     } else if (warp == C::kDrawWarp) {
         // ------------------------------------------------------------ work
         const int ng = (p.B + 31) >> 5, pieces = groups->pieces, whole = groups->whole, blk = groups->blk;
@@ -331,14 +336,14 @@ __global__ void __launch_bounds__(608, 1)
         uint32_t kv_it = 0, item_it = 0, pv_cnt0 = 0, pv_cnt1 = 0, items_x0 = 0, items_x1 = 0;
         bool ok = true;
         const SDesc dQ0 = sdesc_sw128(sQ, 16, 1024), dQ1 = sdesc_sw128(sQ + C::kQBytes, 16, 1024);
-        const SDesc dK0 = sdesc_sw128(sK, 16, 1024), dK1 = sdesc_sw128(sK + C::kKVBytes, 16, 1024);
-        const SDesc dV0 = sdesc_sw128(sV, C::BN * 128, 1024), dV1 = sdesc_sw128(sV + C::kKVBytes, C::BN * 128, 1024);
+        const SDesc dK0 = sdesc_sw128(sK, 16, 1024), dV0 = sdesc_sw128(sV, C::BN * 128, 1024);
+        auto stage = [&](const SDesc& d, uint32_t st) { return SDesc{d.lo + st * (C::kKVBytes >> 4), d.hi}; };
         // S_x = Q K^T, after the tile's previous P V product, which reads P from those columns
         auto issue_s = [&](int x, uint32_t st, int qx) -> bool {
             const uint32_t pc = x ? pv_cnt1 : pv_cnt0;
             if (pc > 0 && !wwait(B_O_DONE + x, (pc - 1) & 1)) return false;
             tc_fence_after();
-            const SDesc dq = qx ? dQ1 : dQ0, dk = st ? dK1 : dK0;
+            const SDesc dq = qx ? dQ1 : dQ0, dk = stage(dK0, st);
             if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(608, 1)
             if (!wwait(B_P_FULL + x, pc & 1)) return false;
             if (first && !wwait(B_O_EMPTY + x, (ix & 1) ^ 1)) return false;
             tc_fence_after();
-            const SDesc dv = st ? dV1 : dV0;
+            const SDesc dv = stage(dV0, st);
             if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < C::BN / 16; ++s)
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(608, 1)
             if (!s.split) {
                 auto act = [&](int x, int j) { return j >= s.a[x] && j < s.b[x]; };
                 {
-                    const uint32_t st = kv_it & 1, ph = (kv_it >> 1) & 1;
+                    const uint32_t st = kv_it % C::kStages, ph = (kv_it / C::kStages) & 1;
                     if (!wwait(B_K_FULL + st, ph)) { ok = false; break; }
                     if (act(0, s.k0) && !issue_s(0, st, 0)) { ok = false; break; }
                     if (act(1, s.k0) && !issue_s(1, st, 1)) { ok = false; break; }
@@ -402,8 +407,8 @@ __global__ void __launch_bounds__(608, 1)
                 }
                 for (int i = 0; i < n && ok; ++i) {
                     const int j = s.k0 + i;
-                    const uint32_t t = kv_it + i, st = t & 1, ph = (t >> 1) & 1;
-                    const uint32_t t1 = t + 1, st1 = t1 & 1, ph1 = (t1 >> 1) & 1;
+                    const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
+                    const uint32_t t1 = t + 1, st1 = t1 % C::kStages, ph1 = (t1 / C::kStages) & 1;
                     if (!wwait(B_V_FULL + st, ph)) { ok = false; break; }
                     clear_v(st, j);
                     if (act(0, j) && !issue_pv(0, st, j == s.a[0])) { ok = false; break; }
@@ -420,15 +425,15 @@ __global__ void __launch_bounds__(608, 1)
             } else {
                 // step i: tile x = i & 1 computes P V of step i, then S of step i + 2
                 for (int i = 0; i < 2 && i < n && ok; ++i) {
-                    const uint32_t t = kv_it + i, st = t & 1, ph = (t >> 1) & 1;
+                    const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
                     if (!wwait(B_K_FULL + st, ph) || !issue_s(i, st, 0)) { ok = false; break; }
                     commit(B_K_EMPTY + st);
                     if (i + 1 == n) commit(B_Q_EMPTY);
                 }
                 for (int i = 0; i < n && ok; ++i) {
                     const int x = i & 1;
-                    const uint32_t t = kv_it + i, st = t & 1, ph = (t >> 1) & 1;
-                    const uint32_t t2 = t + 2, st2 = t2 & 1, ph2 = (t2 >> 1) & 1;
+                    const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
+                    const uint32_t t2 = t + 2, st2 = t2 % C::kStages, ph2 = (t2 / C::kStages) & 1;
                     if (!wwait(B_V_FULL + st, ph)) { ok = false; break; }
                     clear_v(st, s.k0 + i);
                     if (!issue_pv(x, st, i < 2)) { ok = false; break; }

@@ -2,9 +2,9 @@
 //
 // A row tile holds at most 16 packed rows (tokens x grouped heads), so every key byte meets
 // at most 16 multiply-adds: the kernel is a stream of K and V at memory speed, and everything
-// else has to hide under it.  64-key stages (K and V, one TMA box per page and 128-byte
-// column block) pass through a ring of 96 KB per CTA, two CTAs per SM; one warp issues the
-// loads, four warps take 16 keys of each stage.  The products are m16n8k16 tensor-core
+// else has to hide under it.  Stages of 32 KB (K and V of 64 keys, or of 128 at head_dim 64;
+// one TMA box per page and 128-byte column block) pass through a ring of 96 KB per CTA, two
+// CTAs per SM; one warp issues the loads, four warps take a quarter of each stage's keys.  The products are m16n8k16 tensor-core
 // instructions on operands read by ldmatrix: at 16 rows a 128-row accumulator tile would be
 // seven-eighths padding, and the arithmetic is a small part of the time either way.
 //   S = Q K^T (Q in registers), online softmax per warp with a lazily moved maximum, O += P V.
@@ -19,12 +19,14 @@ namespace jfa {
 
 namespace {
 
-constexpr int kDecBM = 16, kDecBN = 64, kDecWarps = 4, kDecThreads = 32 * (kDecWarps + 1), kDecCtasPerSm = 2;
+constexpr int kDecBM = 16, kDecWarps = 4, kDecThreads = 32 * (kDecWarps + 1), kDecCtasPerSm = 2;
 
 template <int D>
 struct DecCfg {
+    static constexpr int BN = 8192 / D;                      // keys of a stage: 32 KB of K and V
+    static constexpr int KG = BN / 64;                       // groups of 16 keys that a warp takes of it
     static constexpr int kCB = D / 64;                       // 128-byte column blocks of a row
-    static constexpr int kBlock = kDecBN * 128;              // one column block of a stage's keys
+    static constexpr int kBlock = BN * 128;                  // one column block of a stage's keys
     static constexpr int kStage = 2 * kCB * kBlock;          // K blocks, then V blocks
     static constexpr int kStages = 98304 / kStage;
     static constexpr int kOffSlots = kStages * kStage;       // two 16 x 64 fp32 tiles of the merge
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     jfa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const CacheFwdParams p) {
     using C = DecCfg<D>;
-    constexpr int BM = kDecBM, BN = kDecBN, NT = D / 8;
+    constexpr int BM = kDecBM, BN = C::BN, KG = C::KG, NS = 2 * KG, NT = D / 8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         // ---------------------------------------------------------------- producer
         // A lane loads one box of each stage: K or V, column block, page.
         fence_proxy_async_smem();  // the scratch's writes before the first loads into it
-        const int rows = min(1 << p.page_log2, BN);          // keys of a box
+        const int rows = min(1 << p.page_log2, 64);          // keys of a box
         const int per = BN / rows;                           // pages (or parts of one) in a stage
         const bool mine = lane < 2 * C::kCB * per;
         const int pg = lane % per, cb = (lane / per) % C::kCB, isv = lane / (per * C::kCB);
@@ -152,8 +154,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     uint32_t it = 0, seg_no = 0;
     bool ok = true;
     // ldmatrix source: row of this warp's 16 keys and 16-byte piece, for K and (transposed) V
-    const int krow = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kpc = (lane >> 3) & 1;
-    const int vrow = 16 * warp + (lane & 7) + (((lane >> 3) & 1) << 3), vpc = lane >> 4;
+    const int krow = 16 * KG * warp + (lane & 7) + ((lane >> 4) << 3), kpc = (lane >> 3) & 1;
+    const int vrow = 16 * KG * warp + (lane & 7) + (((lane >> 3) & 1) << 3), vpc = lane >> 4;
     while (cur.next(p, g)) {
         const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * BM;
         const int nr = min(BM, R - r0);
@@ -205,29 +207,35 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 if (lane == 0) atomicOr(p.status, kStatusTimeout);
             }
             if (!ok) continue;
-            const int c0 = (g.r.f + kt) * BN, w0 = c0 + 16 * warp;  // this warp's keys [w0, w0 + 16)
+            const int w0 = (g.r.f + kt) * BN + 16 * KG * warp;  // this warp's keys [w0, w0 + 16 KG)
             const uint32_t sK = sbase + st * C::kStage, sV = sK + C::kCB * C::kBlock;
             // Values that no row may see are undefined, and 0 * NaN is not 0: clear them.
-            const bool edge = w0 < g.r.lo || w0 + 16 > g.r.hi;
+            const bool edge = w0 < g.r.lo || w0 + 16 * KG > g.r.hi;
             if (edge) {
-                for (int e = lane; e < 16 * C::kCB * 8; e += 32) {
-                    const int row = e & 15, j = w0 + row;
+                for (int e = lane; e < 16 * KG * C::kCB * 8; e += 32) {
+                    const int row = e / (C::kCB * 8), c = e % (C::kCB * 8), j = w0 + row;
                     if (j < g.r.lo || j >= g.r.hi)
-                        st_shared_v4(sV + uint32_t((e >> 7) * C::kBlock + (16 * warp + row) * 128 + ((e >> 4) & 7) * 16), 0, 0, 0, 0);
+                        st_shared_v4(sV + uint32_t((c >> 3) * C::kBlock + (16 * KG * warp + row) * 128 + (c & 7) * 16), 0, 0, 0, 0);
                 }
                 __syncwarp();
             }
-            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float s[NS][4];
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t b[4];
-                ldsm4(b, sK + uint32_t((k >> 2) * C::kBlock + krow * 128 + (((((k & 3) << 1) + kpc) ^ (krow & 7)) << 4)));
-                mma16816(s[0], qa[k], b[0], b[1]);
-                mma16816(s[1], qa[k], b[2], b[3]);
-            }
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int q = 0; q < KG; ++q) {
+                    uint32_t b[4];
+                    ldsm4(b, sK + uint32_t((k >> 2) * C::kBlock + (16 * q + krow) * 128 + (((((k & 3) << 1) + kpc) ^ (krow & 7)) << 4)));
+                    mma16816(s[2 * q], qa[k], b[0], b[1]);
+                    mma16816(s[2 * q + 1], qa[k], b[2], b[3]);
+                }
             // scores of rows qrow (i = 0) and qrow + 8 (i = 1) at keys w0 + 8 n + 2 quad + e
             if (BIAS) {
-                const int far = t_last + diag - w0, near = t_first + diag - (w0 + 15);
+                const int far = t_last + diag - w0, near = t_first + diag - (w0 + 16 * KG - 1);
                 const int bk = relpos_bucket(far);
                 if ((near >= 0 || far <= 0) && bk == relpos_bucket(near)) {
                     if (bk != bucket) {
@@ -236,12 +244,12 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                         for (int i = 0; i < 2; ++i) bcur[i] = brow[i][bk];
                     }
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NS; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) s[n][i] = fmaf(s[n][i], p.scale_log2, bcur[i >> 1]);
                 } else {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NS; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int j = w0 + 8 * n + 2 * quad + (i & 1);
@@ -250,13 +258,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 }
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NS; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
             }
-            if (w0 < all_lo || w0 + 16 > all_hi) {
+            if (w0 < all_lo || w0 + 16 * KG > all_hi) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NS; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = w0 + 8 * n + 2 * quad + (i & 1);
@@ -266,7 +274,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             float mx[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                mx[i] = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+                for (int n = 1; n < NS; ++n) mx[i] = fmax3(mx[i], s[n][2 * i], s[n][2 * i + 1]);
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
             }
@@ -290,23 +300,25 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 }
             }
             const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
-            uint32_t pa[4];
+            uint32_t pa[KG][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < NS; ++n) {
                 const float e0 = ex2_approx(s[n][0] - u0), e1 = ex2_approx(s[n][1] - u0);
                 const float e2 = ex2_approx(s[n][2] - u1), e3 = ex2_approx(s[n][3] - u1);
                 l[0] += e0 + e1;
                 l[1] += e2 + e3;
-                pa[2 * n] = pack_bf16x2(e0, e1);
-                pa[2 * n + 1] = pack_bf16x2(e2, e3);
+                pa[n >> 1][2 * (n & 1)] = pack_bf16x2(e0, e1);
+                pa[n >> 1][2 * (n & 1) + 1] = pack_bf16x2(e2, e3);
             }
 #pragma unroll
-            for (int n = 0; n < NT / 2; ++n) {
-                uint32_t b[4];
-                ldsm4_t(b, sV + uint32_t((n >> 2) * C::kBlock + vrow * 128 + (((((n & 3) << 1) + vpc) ^ (vrow & 7)) << 4)));
-                mma16816(o[2 * n], pa, b[0], b[1]);
-                mma16816(o[2 * n + 1], pa, b[2], b[3]);
-            }
+            for (int q = 0; q < KG; ++q)
+#pragma unroll
+                for (int n = 0; n < NT / 2; ++n) {
+                    uint32_t b[4];
+                    ldsm4_t(b, sV + uint32_t((n >> 2) * C::kBlock + (16 * q + vrow) * 128 + (((((n & 3) << 1) + vpc) ^ (vrow & 7)) << 4)));
+                    mma16816(o[2 * n], pa[q], b[0], b[1]);
+                    mma16816(o[2 * n + 1], pa[q], b[2], b[3]);
+                }
             if (edge) fence_proxy_async_smem();  // the cleared rows before the ring's next load
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(st));
