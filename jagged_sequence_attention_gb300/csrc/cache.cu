@@ -226,7 +226,7 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
 size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
     if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
     const int D = cache->D, n = cache->num_sms;
-    return JFA_CACHE_ZERO_BYTES + kCutBytes + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n)
+    return JFA_CACHE_ZERO_BYTES + kCutBytes + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n) + cache_split_part_bytes(D, n)
                                                            : cache_decode_part_bytes(D, n) + cache_chunk_part_bytes(D, n));
 }
 
@@ -305,9 +305,9 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.item_cost = 0;
         p.min_units = 1;
         if (!bf16) {
-            p.item_cost = 1;
-            if (!fits(T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
-            e = launch_cache_simt(D, true, p, n, st);
+            p.item_cost = kChunkItemUnits;
+            if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
+            e = launch_cache_split(D, p, n, st);
         } else {
             // the queries as (D, head, token), boxes of one tile's rows
             p.tile_tokens = 128 / p.g;
@@ -331,10 +331,11 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.min_units = 1;
     p.item_cost = bf16 ? kDecodeItemUnits : 2;
     if (!fits(chunks ? 0 : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
-    if (bf16) p.part += cache_chunk_part_bytes(D, n) / sizeof(float);  // the two kernels may run at once
+    // (the two kernels may run at once, and the merge comes last)
+    p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
     if (e == cudaSuccess)
         e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, false, p, n, st);
-    if (e == cudaSuccess && chunks && bf16) e = launch_cache_merge(D, pc, n, st);
+    if (e == cudaSuccess && chunks) e = launch_cache_merge(D, pc, n, st);
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 

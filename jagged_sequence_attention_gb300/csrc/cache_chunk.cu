@@ -48,7 +48,7 @@ constexpr int kThreeBuckets = 62, kNear = 96, kNearStride = 100, kNearHeads = 32
 
 template <int D>
 struct ChkCfg {
-    static constexpr int BM = 128, BN = 128, kPair = 2 * BM;
+    static constexpr int BM = 128, BN = 128, kPair = kMergeRows;
     static constexpr int kCB = D / 64;
     static constexpr int kQBytes = BM * D * 2, kKVBytes = BN * D * 2;
     // K and V rings: what shared memory holds (a short item's keys come from DRAM, and two
@@ -72,7 +72,7 @@ struct ChkCfg {
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, BM, BN, false, false);
     static constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, BM, D, false, true);
-    static constexpr int kPart = kPair * (D + 2);  // floats of a partial result: O (four columns of all rows at a time), m, l
+    static constexpr int kPart = cache_merge_part(D);  // floats of a partial result: O (four columns of all rows at a time), m, l
     __host__ __device__ static constexpr uint32_t tmem_s(int x) { return x ? 128u : 0u; }
     __host__ __device__ static constexpr uint32_t tmem_o(int x) { return x ? 384u : 256u; }
 };
@@ -819,7 +819,7 @@ __global__ void __launch_bounds__(608, 1)
 // a warp's loads are whole lines, since parts are stored four columns of all rows at a time.
 template <int D>
 __global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdParams p) {
-    using C = ChkCfg<D>;
+    constexpr int kPart = cache_merge_part(D);
     __shared__ uint32_t there;
     if (threadIdx.x == 0) {
         uint32_t* flag = p.cut_flags + blockIdx.x * kMergeCtas + blockIdx.y;
@@ -832,10 +832,10 @@ __global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdPara
     const int row = 64 * blockIdx.y + (threadIdx.x & 63), quarter = threadIdx.x >> 6;
     if (row >= cut.rows) return;
     const int first = cut.first, last = cut.last;
-    const float* pm = p.part + C::kPair * D + row;
+    const float* pm = p.part + kMergeRows * D + row;
     float mm = -INFINITY;
 #pragma unroll 8
-    for (int c = first; c <= last; ++c) mm = fmaxf(mm, pm[size_t(cache_slot(c, first)) * C::kPart]);
+    for (int c = first; c <= last; ++c) mm = fmaxf(mm, pm[size_t(cache_slot(c, first)) * kPart]);
     constexpr int NV = D / 16;  // float4s of a thread
     float ll = 0.f;
     float4 v[NV];
@@ -843,14 +843,14 @@ __global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdPara
     for (int e = 0; e < NV; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
     for (int c = first; c <= last; ++c) {
-        const float* q = p.part + size_t(cache_slot(c, first)) * C::kPart;
-        const float mc = q[C::kPair * D + row], lc = q[C::kPair * D + C::kPair + row];
+        const float* q = p.part + size_t(cache_slot(c, first)) * kPart;
+        const float mc = q[kMergeRows * D + row], lc = q[kMergeRows * D + kMergeRows + row];
         const float w = mc == -INFINITY ? 0.f : ex2_approx(mc - mm);
-        const float4* q4 = reinterpret_cast<const float4*>(q) + quarter * NV * C::kPair + row;
+        const float4* q4 = reinterpret_cast<const float4*>(q) + quarter * NV * kMergeRows + row;
         ll = fmaf(lc, w, ll);
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
-            float4 u = q4[e * C::kPair];
+            float4 u = q4[e * kMergeRows];
             if (mc == -INFINITY) u = make_float4(0.f, 0.f, 0.f, 0.f);  // no key of this part: its O is not set
             v[e].x = fmaf(u.x, w, v[e].x);
             v[e].y = fmaf(u.y, w, v[e].y);
@@ -899,6 +899,8 @@ cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cuda
     const dim3 grid(num_sms * kBlocksPerCta, kMergeCtas);
     if (D == 128)
         jfa_cache_merge_kernel<128><<<grid, 256, 0, st>>>(p);
+    else if (D == 32)
+        jfa_cache_merge_kernel<32><<<grid, 256, 0, st>>>(p);
     else
         jfa_cache_merge_kernel<64><<<grid, 256, 0, st>>>(p);
     return cudaGetLastError();

@@ -493,6 +493,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// fp32, items of 128 packed rows: tensor-core products of operands in three bf16 parts each.
+cudaError_t launch_cache_split(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
+size_t cache_split_part_bytes(int D, int num_sms);
 // fp32, row tiles of 128 (chunk) or 16 packed rows.
 cudaError_t launch_cache_simt(int D, bool chunk, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_simt_part_bytes(int D, int num_sms);
@@ -507,6 +510,10 @@ size_t cache_decode_part_bytes(int D, int num_sms);
 cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                const CacheFwdParams& p, int num_sms, cudaStream_t st);
 size_t cache_chunk_part_bytes(int D, int num_sms);
+// Parts of cut items as the merge kernel reads them: O four columns of kMergeRows rows at a
+// time, then the rows' m and l.
+constexpr int kMergeRows = 256;
+__host__ __device__ constexpr int cache_merge_part(int D) { return kMergeRows * (D + 2); }  // floats
 cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 
 struct CacheAppendParams {

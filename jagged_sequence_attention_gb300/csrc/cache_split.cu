@@ -1,0 +1,434 @@
+// Paged-cache attention for chunks of new tokens, fp32: tensor-core products of operands split
+// into three bf16 parts each.
+//
+// x = x0 + x1 + x2 with x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1): both
+// differences are exact in fp32, so the parts hold x to 2^-27 of it.  A product of two split
+// values keeps
+//   x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0),
+// leaving out terms of 2^-26 and less: each product is as exact as fp32's own rounding.  The
+// tensor core accumulates in fp32, but not with rounding to nearest, so two things keep its
+// sums at fp32's level: the small terms go first, while the accumulator is small, and leave
+// only the x0 y0 steps (4 for a score, 8 for an output) to the full-size accumulator; and the
+// output of each key tile starts from zero and is added to the running one in registers.
+// Six bf16 products at 16 times and more the rate of the FMA units: the split, the softmax and
+// the loads bound the kernel, not the products.
+//
+// An item is 128 packed rows of one (sequence, key head); a step is 128 keys.  Head dimension
+// 32 runs as 64 with zeros.  CTA = 13 warps, one CTA per SM:
+//   warps 0-7   softmax: two warps share a row, 64 score columns and 32 output columns each
+//   warps 8-11  load Q, K, V (16-byte loads by page, the next tile's ahead in registers), split
+//               them, and write the parts' swizzled tiles
+//   warp 12     tcgen05.mma issuer and TMEM owner
+// TMEM (512 columns): scores twice [0,128), [128,256), so that a tile's scores form during the
+// previous one's softmax; P's parts [256,448); the tile's output [448,512).
+#include "cache_common.cuh"
+#include "tilemath.cuh"
+
+namespace jfa {
+
+namespace {
+
+constexpr int kSpBM = 128, kSpBN = 128, kSpD = 64;
+
+struct SpCfg {
+    static constexpr int kPlane = 128 * 128;        // one part of a tile: 128 rows of 64 bf16
+    static constexpr int kTile = 3 * kPlane;
+    static constexpr int kOffQ = 0, kOffK = kTile, kOffV = kOffK + kTile;
+    static constexpr int kOffBar = kOffV + kTile;
+    static constexpr int kOffMisc = kOffBar + 32 * 8;
+    static constexpr int kOffXch = kOffMisc + 16;   // pair exchanges [2][2][4][32]
+    static constexpr int kOffSums = kOffXch + 2 * 2 * 4 * 32 * 4;  // scratch of the work split
+    static constexpr int kBytes = kOffSums + kCacheMaxGroups * 4 + 1024;
+    static constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kThreads = 13 * 32;
+    static constexpr uint32_t kTmemCols = 512, kP = 256, kO = 448;
+    static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, 128, 128, false, false);
+    static constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, 128, kSpD, false, true);
+};
+
+enum {
+    P_Q_FULL = 0,
+    P_Q_EMPTY,
+    P_K_FULL,
+    P_K_EMPTY,
+    P_V_FULL,
+    P_V_EMPTY,
+    P_P_FULL,
+    P_O_DONE,
+    P_DRAIN,
+    P_S_FULL,                // +buffer
+    P_S_EMPTY = P_S_FULL + 2,
+    P_XCH = P_S_EMPTY + 2,   // +pair of warps
+};
+
+// The six products of split operands, the small ones first: (part of A, part of B).
+__device__ __forceinline__ constexpr int term_a(int t) { return t == 0 ? 1 : t == 1 ? 0 : t == 2 ? 2 : t == 3 ? 0 : t == 4 ? 1 : 0; }
+__device__ __forceinline__ constexpr int term_b(int t) { return t == 0 ? 1 : t == 1 ? 2 : t == 2 ? 0 : t == 3 ? 1 : 0; }
+
+// Two values' three parts, each pair packed.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+    p0 = pack_bf16x2(x, y);
+    const float rx = x - __uint_as_float(p0 << 16), ry = y - __uint_as_float(p0 & 0xffff0000u);
+    p1 = pack_bf16x2(rx, ry);
+    p2 = pack_bf16x2(rx - __uint_as_float(p1 << 16), ry - __uint_as_float(p1 & 0xffff0000u));
+}
+
+template <int D, bool BIAS>
+__global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(const CacheFwdParams p) {
+    using C = SpCfg;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * uint32_t(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(P_Q_FULL), C::kLoadWarps);
+        mbar_init(bar(P_Q_EMPTY), 1);
+        mbar_init(bar(P_K_FULL), C::kLoadWarps);
+        mbar_init(bar(P_K_EMPTY), 1);
+        mbar_init(bar(P_V_FULL), C::kLoadWarps);
+        mbar_init(bar(P_V_EMPTY), 1);
+        mbar_init(bar(P_P_FULL), C::kSoftWarps);
+        mbar_init(bar(P_O_DONE), 1);
+        mbar_init(bar(P_DRAIN), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(P_S_FULL + s), 1);
+            mbar_init(bar(P_S_EMPTY + s), C::kSoftWarps);
+        }
+        for (int q = 0; q < 4; ++q) mbar_init(bar(P_XCH + q), 2);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == C::kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    CacheCursor<kSpBN> cur(cache_start<kSpBN>(p, reinterpret_cast<int*>(smem + C::kOffSums)));
+    const CacheStart start = cur.st;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    CacheSeg g;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(p.status, kStatusTimeout);
+    };
+    auto wwait = [&](int b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag));
+    };
+    bool ok = true;
+
+    if (warp == C::kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        uint32_t it = 0, item_it = 0;  // steps and items so far
+        const SDesc dQ = sdesc_sw128(sbase + C::kOffQ, 16, 1024), dK = sdesc_sw128(sbase + C::kOffK, 16, 1024);
+        const SDesc dV = sdesc_sw128(sbase + C::kOffV, 128 * 128, 1024);
+        auto commit = [&](int b) {
+            if (elect_one()) tc_commit(bar(b));
+            __syncwarp();
+        };
+        auto issue_s = [&](uint32_t i) -> bool {  // scores of step i into buffer i & 1
+            const uint32_t x = i & 1, use = i >> 1;
+            if (!wwait(P_K_FULL, i & 1) || !wwait(P_S_EMPTY + x, (use & 1) ^ 1)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int t = 0; t < 6; ++t)
+#pragma unroll
+                    for (int s = 0; s < kSpD / 16; ++s)
+                        mma_ss(tmem + 128u * x, dQ, term_a(t) * C::kPlane + s * 32, dK, term_b(t) * C::kPlane + s * 32,
+                               C::kIdescQK, t > 0 || s > 0);
+                tc_commit(bar(P_S_FULL + x));
+            }
+            __syncwarp();
+            commit(P_K_EMPTY);
+            return true;
+        };
+        while (ok && cur.next(p, g)) {
+            const int n = g.r.n > 0 ? g.k1 - g.k0 : 0;
+            if (n == 0) continue;
+            if (!wwait(P_Q_FULL, item_it & 1) || !issue_s(it)) { ok = false; break; }
+            if (n == 1) commit(P_Q_EMPTY);
+            for (int j = 0; j < n && ok; ++j) {
+                const uint32_t i = it + j;
+                if (j + 1 < n) {
+                    if (!issue_s(i + 1)) { ok = false; break; }
+                    if (j + 2 == n) commit(P_Q_EMPTY);
+                }
+                if (!wwait(P_V_FULL, i & 1) || !wwait(P_P_FULL, i & 1)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int t = 0; t < 6; ++t)
+#pragma unroll
+                        for (int s = 0; s < kSpBN / 16; ++s)
+                            mma_ts(tmem + C::kO, tmem + C::kP + 64u * term_a(t) + 8u * s, dV,
+                                   term_b(t) * C::kPlane + s * 16 * 128, C::kIdescPV, t > 0 || s > 0);
+                    tc_commit(bar(P_O_DONE));
+                }
+                __syncwarp();
+                commit(P_V_EMPTY);
+            }
+            it += n;
+            ++item_it;
+        }
+        if (!ok && lane == 0) fail();
+        commit(P_DRAIN);  // every issued product, before TMEM is released
+        mbar_wait_bounded(bar(P_DRAIN), 0, nullptr);
+    } else if (warp >= C::kSoftWarps) {
+        // ------------------------------------------------------------ loads and splits
+        const int tid = threadIdx.x - 32 * C::kSoftWarps;
+        const int c = tid & 7, row0 = tid >> 3;  // eight elements of rows row0 + 16 i
+        uint32_t it = 0, item_it = 0;
+        const int page_mask = (1 << p.page_log2) - 1;
+        float4 a[8], b[8];
+        auto put = [&](int off, int full) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = row0 + 16 * i;
+                uint32_t w[3][4];
+                split2(a[i].x, a[i].y, w[0][0], w[1][0], w[2][0]);
+                split2(a[i].z, a[i].w, w[0][1], w[1][1], w[2][1]);
+                split2(b[i].x, b[i].y, w[0][2], w[1][2], w[2][2]);
+                split2(b[i].z, b[i].w, w[0][3], w[1][3], w[2][3]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    st_shared_v4(sbase + uint32_t(off + q * C::kPlane + r * 128 + ((c ^ (r & 7)) << 4)), w[q][0], w[q][1],
+                                 w[q][2], w[q][3]);
+            }
+            fence_proxy_async_smem();  // before the products read them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(full));
+        };
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        // the tile's rows of K or V from position c0 on; zeros where no row of the item may look
+        auto fetch = [&](const void* base, const int64_t* s, int c0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = c0 + row0 + 16 * i;
+                a[i] = b[i] = zero;
+                if (j < g.r.lo || j >= g.r.hi || 8 * c >= D) continue;
+                const int page = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                if (page < 0 || page >= p.n_pages) {
+                    if (c == 0) atomicOr(p.status, kStatusBounds);
+                    continue;
+                }
+                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(base) + page * s[0] +
+                                                                    (j & page_mask) * s[1] + g.hk * s[2] + 8 * c);
+                a[i] = src[0];
+                b[i] = src[1];
+            }
+        };
+        while (ok && cur.next(p, g)) {
+            if (g.r.n == 0) continue;
+            const int R = g.s.q_len * p.g, r0 = g.tile * kSpBM;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + row0 + 16 * i;
+                a[i] = b[i] = zero;
+                if (r >= R || 8 * c >= D) continue;
+                const int tok = div_g(p, r);
+                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
+                                                                    int64_t(g.hk * p.g + r - tok * p.g) * D + 8 * c);
+                a[i] = src[0];
+                b[i] = src[1];
+            }
+            if (!wwait(P_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+            put(C::kOffQ, P_Q_FULL);
+            ++item_it;
+            for (int k = g.k0; k < g.k1 && ok; ++k, ++it) {
+                const int c0 = (g.r.f + k) * kSpBN;
+                fetch(p.K, p.ks, c0);
+                if (!wwait(P_K_EMPTY, (it & 1) ^ 1)) { ok = false; break; }
+                put(C::kOffK, P_K_FULL);
+                fetch(p.V, p.vs, c0);
+                if (!wwait(P_V_EMPTY, (it & 1) ^ 1)) { ok = false; break; }
+                put(C::kOffV, P_V_FULL);
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else {
+        // ------------------------------------------------------------ softmax / output
+        const int hf = warp >> 2, pair = warp & 3, t = pair * 32 + lane;
+        const uint32_t lane_base = uint32_t(pair * 32) << 16;
+        const uint32_t tO = tmem + lane_base + C::kO + 32u * hf, tP = tmem + lane_base + C::kP;
+        float* xch_s = reinterpret_cast<float*>(smem + C::kOffXch);
+        uint32_t it = 0, x_cnt = 0;
+        auto exchange = [&](float v, float& other) -> bool {
+            float* buf = xch_s + (x_cnt & 1) * 256 + pair * 32;
+            buf[hf * 128 + lane] = v;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(P_XCH + pair));
+            const bool good = wwait(P_XCH + pair, x_cnt & 1);
+            ++x_cnt;
+            if (good) other = buf[(hf ^ 1) * 128 + lane];
+            return good;
+        };
+        while (ok && cur.next(p, g)) {
+            const int n = g.r.n > 0 ? g.k1 - g.k0 : 0;
+            const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * kSpBM;
+            const bool row_valid = r0 + t < R;
+            const int rc = min(r0 + t, R - 1), tok = div_g(p, rc), head = g.hk * p.g + rc - tok * p.g;
+            const int rel = tok + diag;  // rows past the end repeat the last one's masks
+            const int t0 = __shfl_sync(0xffffffffu, tok, 0), t31 = __shfl_sync(0xffffffffu, tok, 31);
+            const float* brow = BIAS ? p.bias + head * 32 : nullptr;
+            const size_t orow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(head);
+            float m = -INFINITY, l = 0.f, o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            // the output of the step before, added and brought to the new maximum
+            auto add_o = [&](float alpha) {
+                uint32_t r[32];
+                tmem_ld32(tO, r);
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = (o[e] + __uint_as_float(r[e])) * alpha;
+            };
+            for (int j = 0; j < n; ++j) {
+                const uint32_t i = it + j, x = i & 1;
+                const int col0 = (g.r.f + g.k0 + j) * kSpBN + 64 * hf;  // this warp's first key
+                int lim = g.s.kv_len - col0;
+                if (p.causal) lim = min(lim, rel + 1 - col0);
+                const int lo = p.window >= 0 ? rel - p.window - col0 : 0;
+                const bool full = __all_sync(0xffffffffu, lim >= 64 && lo <= 0);
+                if (!wwait(P_S_FULL + x, (i >> 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t sr[2][32];
+                tmem_ld32(tmem + lane_base + 128u * x + 64u * hf, sr[0]);
+                tmem_ld32(tmem + lane_base + 128u * x + 64u * hf + 32u, sr[1]);
+                tmem_ld_wait(sr[0]);
+                tmem_ld_wait(sr[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(P_S_EMPTY + x));
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int rk = rel - col0 - 32 * k;
+                    const int far = t31 + diag - col0 - 32 * k, near = t0 + diag - col0 - 32 * k - 31;
+                    const int bk = BIAS ? relpos_bucket(far) : 0;
+                    const bool one = !BIAS || ((near >= 0 || far <= 0) && bk == relpos_bucket(near));
+                    const float b1 = BIAS ? __ldg(brow + bk) * 1.4426950408889634f : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float y = __uint_as_float(sr[k][e]) * p.scale_log2;
+                        if (BIAS) y += one ? b1 : __ldg(brow + relpos_bucket(rk - e)) * 1.4426950408889634f;
+                        if (!full) y = e + 32 * k >= lo && e + 32 * k < lim ? y : -INFINITY;
+                        sr[k][e] = __float_as_uint(y);
+                        mx = fmaxf(mx, y);
+                    }
+                }
+                float mo;
+                if (!exchange(mx, mo)) { ok = false; break; }
+                const float m_new = fmaxf(m, fmaxf(mx, mo)), m_use = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_use);
+                m = m_new;
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float y = ex2_approx(__uint_as_float(sr[k][e]) - m_use);
+                        sr[k][e] = __float_as_uint(y);
+                        sum += y;
+                    }
+                l = fmaf(l, alpha, sum);
+                if (j > 0) {  // P's columns and the output are free once the product before is done
+                    if (!wwait(P_O_DONE, (i - 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    add_o(alpha);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // (eight packed columns at a time: the scores still to come fill the registers)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[3][8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            split2(__uint_as_float(sr[k][16 * h + 2 * e]), __uint_as_float(sr[k][16 * h + 2 * e + 1]), w[0][e],
+                                   w[1][e], w[2][e]);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) tmem_st8(tP + 64u * q + 32u * hf + 16u * k + 8u * h, w[q]);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(P_P_FULL));
+            }
+            if (!ok) break;
+            it += n;
+            float lt = l;
+            if (n > 0) {
+                if (!wwait(P_O_DONE, (it - 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                add_o(1.f);
+                // (the next item's first product waits for its P, which these warps write)
+                tc_fence_before();
+                float other;
+                if (!exchange(l, other)) { ok = false; break; }
+                lt = l + other;
+            }
+            if (g.whole()) {
+                const float inv = lt > 0.f ? 1.f / lt : 0.f;
+                if (32 * hf < D && row_valid) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + 32 * hf);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+                }
+                if (p.lse && hf == 0 && row_valid) p.lse[orow] = lt > 0.f ? (m + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+                continue;
+            }
+            // an item cut between CTAs: this part, and with the first one the merge's record
+            const int first = cache_first_cta(p, start, g), last = cache_last_cta(p, start, g);
+            float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * cache_merge_part(D);
+            if (row_valid) {
+                if (32 * hf < D) {
+                    float4* po = reinterpret_cast<float4*>(part);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        po[(8 * hf + e) * kMergeRows + t] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+                if (hf == 0) {
+                    part[kMergeRows * D + t] = m;
+                    part[kMergeRows * D + kMergeRows + t] = lt;
+                }
+            }
+            if (threadIdx.x < kMergeCtas && g.k0 == 0) {
+                if (threadIdx.x == 0)
+                    p.cuts[first] = CacheCut{g.s.q0, min(kSpBM, R - r0), r0, g.hk * p.g, first, last, {0, 0}};
+                p.cut_flags[first * kMergeCtas + threadIdx.x] = 1u;
+            }
+        }
+        if (!ok && lane == 0) fail();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int D, bool BIAS>
+cudaError_t launch(const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(jfa_cache_split_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SpCfg::kBytes);
+    if (e != cudaSuccess) return e;
+    jfa_cache_split_kernel<D, BIAS><<<num_sms, SpCfg::kThreads, SpCfg::kBytes, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_split_part_bytes(int D, int num_sms) { return size_t(num_sms) * 2 * cache_merge_part(D) * 4; }
+
+cudaError_t launch_cache_split(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    if (D == 32) return p.bias ? launch<32, true>(p, num_sms, st) : launch<32, false>(p, num_sms, st);
+    return p.bias ? launch<64, true>(p, num_sms, st) : launch<64, false>(p, num_sms, st);
+}
+
+}  // namespace jfa
