@@ -19,7 +19,7 @@ struct jfa_cache_t {
     int64_t ks[3], vs[3];
     int device, num_sms;
     int* d_status;
-    CUtensorMap mk, mv;  // bf16: the pages as (D, slot, head, page), boxes of one page's keys (at most 64)
+    CUtensorMap mk, mv;  // the pages as (D, slot, head, page), boxes of one page's keys (at most 64)
 };
 
 namespace {
@@ -38,18 +38,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
     return enc;
 }
 
-// A bf16 tensor of `rank` dimensions (the first dense, strides of the others in elements), its
-// boxes 128 bytes of the first, with 128-byte swizzle.
-jfa_status make_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const int64_t* strides,
+// A tensor of `rank` dimensions (the first dense, strides of the others in elements), its boxes
+// 128 bytes of the first, with 128-byte swizzle.
+jfa_status make_map(CUtensorMap* map, int dtype, const void* base, int rank, const cuuint64_t* dims, const int64_t* strides,
                          const cuuint32_t* box) {
     const auto enc = encode_tiled();
     if (!enc) return JFA_ERR_CUDA;
     cuuint64_t bytes[3];
-    for (int i = 0; i + 1 < rank; ++i) bytes[i] = cuuint64_t(strides[i]) * 2;
+    for (int i = 0; i + 1 < rank; ++i) bytes[i] = cuuint64_t(strides[i]) * elem(dtype);
     const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, bytes, box, one,
+    return enc(map, dtype == JFA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, bytes, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               dims[0] * 2 >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               dims[0] * elem(dtype) >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? JFA_OK
                : JFA_ERR_CUDA;
@@ -59,8 +59,8 @@ jfa_status make_bf16_map(CUtensorMap* map, const void* base, int rank, const cuu
 jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* c, const int64_t* s, int rows) {
     const cuuint64_t dims[4] = {cuuint64_t(c->D), cuuint64_t(1) << c->page_log2, cuuint64_t(c->Hkv), cuuint64_t(c->n_pages)};
     const int64_t strides[3] = {s[1], s[2], s[0]};
-    const cuuint32_t box[4] = {64u, cuuint32_t(rows), 1u, 1u};
-    return make_bf16_map(map, base, 4, dims, strides, box);
+    const cuuint32_t box[4] = {cuuint32_t(128 / elem(c->dtype)), cuuint32_t(rows), 1u, 1u};
+    return make_map(map, c->dtype, base, 4, dims, strides, box);
 }
 
 constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
@@ -130,7 +130,7 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
     }
     c->device = dev;
     c->num_sms = prop.multiProcessorCount;
-    if (dtype == JFA_BF16) {
+    {
         const int rows = std::min(64, page_size);
         if (make_page_map(&c->mk, K, c, c->ks, rows) != JFA_OK || make_page_map(&c->mv, V, c, c->vs, rows) != JFA_OK) {
             delete c;
@@ -307,7 +307,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         if (!bf16) {
             p.item_cost = kChunkItemUnits;
             if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
-            e = launch_cache_split(D, p, n, st);
+            e = launch_cache_split(D, cache->mk, cache->mv, p, n, st);
         } else {
             // the queries as (D, head, token), boxes of one tile's rows
             p.tile_tokens = 128 / p.g;
@@ -319,7 +319,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
             const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
             const int64_t strides[2] = {D, q_stride};
             const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(p.tile_tokens)};
-            const jfa_status ms = make_bf16_map(&mq, Q, 3, dims, strides, box);
+            const jfa_status ms = make_map(&mq, JFA_BF16, Q, 3, dims, strides, box);
             if (ms != JFA_OK) return ms;
             e = launch_cache_chunk(D, mq, cache->mk, cache->mv, p, n, st);
         }

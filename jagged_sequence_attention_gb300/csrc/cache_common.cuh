@@ -494,7 +494,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 }
 
 // fp32, items of 128 packed rows: tensor-core products of operands in three bf16 parts each.
-cudaError_t launch_cache_split(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_cache_split(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                               cudaStream_t st);
 size_t cache_split_part_bytes(int D, int num_sms);
 // fp32, row tiles of 128 (chunk) or 16 packed rows.
 cudaError_t launch_cache_simt(int D, bool chunk, const CacheFwdParams& p, int num_sms, cudaStream_t st);

@@ -16,9 +16,11 @@
 // An item is 128 packed rows of one (sequence, key head); a step is 128 keys.  Head dimension
 // 32 runs as 64 with zeros.  CTA = 13 warps, one CTA per SM:
 //   warps 0-7   softmax: two warps share a row, 64 score columns and 32 output columns each
-//   warps 8-11  load Q, K, V (16-byte loads by page, the next tile's ahead in registers), split
-//               them, and write the parts' swizzled tiles
+//   warps 8-11  split Q (from global memory) and the K and V tiles that TMA left in shared
+//               memory, and write the parts' swizzled tiles
 //   warp 12     tcgen05.mma issuer and TMEM owner
+//   warp 13     TMA loads of K and V, a tile of each ahead (one box per page and 128 bytes of a
+//               row): 64 KB in flight, which loads through registers would not reach
 // TMEM (512 columns): scores twice [0,128), [128,256), so that a tile's scores form during the
 // previous one's softmax; P's parts [256,448); the tile's output [448,512).
 #include "cache_common.cuh"
@@ -34,12 +36,14 @@ struct SpCfg {
     static constexpr int kPlane = 128 * 128;        // one part of a tile: 128 rows of 64 bf16
     static constexpr int kTile = 3 * kPlane;
     static constexpr int kOffQ = 0, kOffK = kTile, kOffV = kOffK + kTile;
-    static constexpr int kOffBar = kOffV + kTile;
+    static constexpr int kStageBlock = 128 * 128;   // fp32 tile as loaded: 128 rows of 32 floats, twice
+    static constexpr int kOffKS = kOffV + kTile, kOffVS = kOffKS + 2 * kStageBlock;
+    static constexpr int kOffBar = kOffVS + 2 * kStageBlock;
     static constexpr int kOffMisc = kOffBar + 32 * 8;
     static constexpr int kOffXch = kOffMisc + 16;   // pair exchanges [2][2][4][32]
     static constexpr int kOffSums = kOffXch + 2 * 2 * 4 * 32 * 4;  // scratch of the work split
     static constexpr int kBytes = kOffSums + kCacheMaxGroups * 4 + 1024;
-    static constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kThreads = 13 * 32;
+    static constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kTmaWarp = 13, kThreads = 14 * 32;
     static constexpr uint32_t kTmemCols = 512, kP = 256, kO = 448;
     static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, 128, 128, false, false);
     static constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, 128, kSpD, false, true);
@@ -58,6 +62,10 @@ enum {
     P_S_FULL,                // +buffer
     P_S_EMPTY = P_S_FULL + 2,
     P_XCH = P_S_EMPTY + 2,   // +pair of warps
+    P_KS_FULL = P_XCH + 4,   // K as loaded
+    P_KS_EMPTY,
+    P_VS_FULL,
+    P_VS_EMPTY,
 };
 
 // The six products of split operands, the small ones first: (part of A, part of B).
@@ -73,7 +81,9 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& p0, uint32_t&
 }
 
 template <int D, bool BIAS>
-__global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(const CacheFwdParams p) {
+__global__ void __launch_bounds__(SpCfg::kThreads, 1)
+    jfa_cache_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                           const CacheFwdParams p) {
     using C = SpCfg;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -93,6 +103,12 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(con
         mbar_init(bar(P_P_FULL), C::kSoftWarps);
         mbar_init(bar(P_O_DONE), 1);
         mbar_init(bar(P_DRAIN), 1);
+        mbar_init(bar(P_KS_FULL), 1);
+        mbar_init(bar(P_KS_EMPTY), C::kLoadWarps);
+        mbar_init(bar(P_VS_FULL), 1);
+        mbar_init(bar(P_VS_EMPTY), C::kLoadWarps);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(P_S_FULL + s), 1);
             mbar_init(bar(P_S_EMPTY + s), C::kSoftWarps);
@@ -101,6 +117,11 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(con
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if (D == 32)  // the parts' upper columns stay zero
+        for (int e = threadIdx.x; e < 9 * 128 * 4; e += C::kThreads) {
+            const int row = e >> 2, c = 4 + (e & 3);
+            st_shared_v4(sbase + uint32_t(row * 128 + ((c ^ (row & 7)) << 4)), 0, 0, 0, 0);
+        }
     if (warp == C::kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
@@ -178,75 +199,114 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(con
         if (!ok && lane == 0) fail();
         commit(P_DRAIN);  // every issued product, before TMEM is released
         mbar_wait_bounded(bar(P_DRAIN), 0, nullptr);
-    } else if (warp >= C::kSoftWarps) {
-        // ------------------------------------------------------------ loads and splits
-        const int tid = threadIdx.x - 32 * C::kSoftWarps;
-        const int c = tid & 7, row0 = tid >> 3;  // eight elements of rows row0 + 16 i
-        uint32_t it = 0, item_it = 0;
-        const int page_mask = (1 << p.page_log2) - 1;
-        float4 a[8], b[8];
-        auto put = [&](int off, int full) {
+    } else if (warp == C::kTmaWarp) {
+        // ------------------------------------------------------------ loads
+        const int rows = min(1 << p.page_log2, 64), per = kSpBN / rows;  // keys of a box, boxes of a column block
+        const int mask = (1 << p.page_log2) - 1;
+        uint32_t it = 0, v_it = 0;
+        while (ok && cur.next(p, g)) {
+            if (g.r.n == 0) continue;
+            for (int k = g.k0; k < g.k1 && ok; ++k, ++it) {
+                // lane: a page of the tile (two column blocks of it)
+                const int j = (g.r.f + k) * kSpBN + lane * rows;
+                int page = -1;
+                if (lane < per && j < g.r.hi && j + rows > g.r.lo) {
+                    page = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                    if (page < 0 || page >= p.n_pages) {
+                        atomicOr(p.status, kStatusBounds);
+                        page = p.n_pages;  // past the cache: read as zeros
+                    }
+                }
+                const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, page >= 0)) * rows * 128 * (D / 32));
+                auto issue = [&](int full, int empty, int stage, const CUtensorMap* map) -> bool {
+                    if (!wwait(empty, (it & 1) ^ 1)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+                    __syncwarp();
+                    if (page >= 0)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = row0 + 16 * i;
-                uint32_t w[3][4];
-                split2(a[i].x, a[i].y, w[0][0], w[1][0], w[2][0]);
-                split2(a[i].z, a[i].w, w[0][1], w[1][1], w[2][1]);
-                split2(b[i].x, b[i].y, w[0][2], w[1][2], w[2][2]);
-                split2(b[i].z, b[i].w, w[0][3], w[1][3], w[2][3]);
-#pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    st_shared_v4(sbase + uint32_t(off + q * C::kPlane + r * 128 + ((c ^ (r & 7)) << 4)), w[q][0], w[q][1],
-                                 w[q][2], w[q][3]);
+                        for (int h = 0; h < D / 32; ++h)
+                            tma_load_4d(sbase + uint32_t(stage + h * C::kStageBlock + lane * rows * 128), map, bar(full), 32 * h,
+                                        j & mask, g.hk, page);
+                    return true;
+                };
+                if (!issue(P_KS_FULL, P_KS_EMPTY, C::kOffKS, &tmK)) { ok = false; break; }
+                if (!issue(P_VS_FULL, P_VS_EMPTY, C::kOffVS, &tmV)) { ok = false; ++it; break; }
+                ++v_it;
             }
+        }
+        if (!ok && lane == 0) fail();
+        drain_ring(bar(P_KS_FULL), it, 1);
+        drain_ring(bar(P_VS_FULL), v_it, 1);
+    } else if (warp >= C::kSoftWarps) {
+        // ------------------------------------------------------------ splits
+        const int tid = threadIdx.x - 32 * C::kSoftWarps;
+        const int c = tid & 7, row0 = tid >> 3;  // elements 4 c .. and 32 + 4 c .. of rows row0 + 16 i
+        uint32_t it = 0, item_it = 0;
+        // four elements of row r, from column 4 c (+ 32) on, to the parts' tiles at `off`
+        auto put4 = [&](int off, int r, int piece, const float4& v) {
+            uint32_t w[3][2];
+            split2(v.x, v.y, w[0][0], w[1][0], w[2][0]);
+            split2(v.z, v.w, w[0][1], w[1][1], w[2][1]);
+            const uint32_t at = sbase + uint32_t(off + r * 128 + (((piece >> 1) ^ (r & 7)) << 4) + (piece & 1) * 8);
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + uint32_t(q * C::kPlane)), "r"(w[q][0]), "r"(w[q][1])
+                             : "memory");
+        };
+        auto arrive = [&](int full) {
             fence_proxy_async_smem();  // before the products read them
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(full));
         };
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        // the tile's rows of K or V from position c0 on; zeros where no row of the item may look
-        auto fetch = [&](const void* base, const int64_t* s, int c0) {
-#pragma unroll
+        // a loaded tile's rows, zeros where no row of the item may look (positions from c0 on)
+        auto convert = [&](int stage, int off, int c0) {
+#pragma unroll 4
             for (int i = 0; i < 8; ++i) {
-                const int j = c0 + row0 + 16 * i;
-                a[i] = b[i] = zero;
-                if (j < g.r.lo || j >= g.r.hi || 8 * c >= D) continue;
-                const int page = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
-                if (page < 0 || page >= p.n_pages) {
-                    if (c == 0) atomicOr(p.status, kStatusBounds);
-                    continue;
+                const int r = row0 + 16 * i, j = c0 + r;
+                const bool in = j >= g.r.lo && j < g.r.hi;
+                const uint32_t at = sbase + uint32_t(stage + r * 128 + ((c ^ (r & 7)) << 4));
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    const uint4 u = ld_shared_v4(at + uint32_t(h * C::kStageBlock));
+                    float4 v = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+                    if (!in) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    put4(off, r, c + 8 * h, v);
                 }
-                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(base) + page * s[0] +
-                                                                    (j & page_mask) * s[1] + g.hk * s[2] + 8 * c);
-                a[i] = src[0];
-                b[i] = src[1];
             }
         };
         while (ok && cur.next(p, g)) {
             if (g.r.n == 0) continue;
             const int R = g.s.q_len * p.g, r0 = g.tile * kSpBM;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = r0 + row0 + 16 * i;
-                a[i] = b[i] = zero;
-                if (r >= R || 8 * c >= D) continue;
-                const int tok = div_g(p, r);
-                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
-                                                                    int64_t(g.hk * p.g + r - tok * p.g) * D + 8 * c);
-                a[i] = src[0];
-                b[i] = src[1];
-            }
             if (!wwait(P_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
-            put(C::kOffQ, P_Q_FULL);
+#pragma unroll 4
+            for (int i = 0; i < 8; ++i) {
+                const int r = row0 + 16 * i;
+                float4 v[D / 32];
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r0 + r < R) {
+                    const int tok = div_g(p, r0 + r);
+                    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
+                                                                        int64_t(g.hk * p.g + r0 + r - tok * p.g) * D);
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h) v[h] = src[c + 8 * h];
+                }
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) put4(C::kOffQ, r, c + 8 * h, v[h]);
+            }
+            arrive(P_Q_FULL);
             ++item_it;
             for (int k = g.k0; k < g.k1 && ok; ++k, ++it) {
                 const int c0 = (g.r.f + k) * kSpBN;
-                fetch(p.K, p.ks, c0);
-                if (!wwait(P_K_EMPTY, (it & 1) ^ 1)) { ok = false; break; }
-                put(C::kOffK, P_K_FULL);
-                fetch(p.V, p.vs, c0);
-                if (!wwait(P_V_EMPTY, (it & 1) ^ 1)) { ok = false; break; }
-                put(C::kOffV, P_V_FULL);
+                const uint32_t ph = it & 1;
+                if (!wwait(P_KS_FULL, ph) || !wwait(P_K_EMPTY, ph ^ 1)) { ok = false; break; }
+                convert(C::kOffKS, C::kOffK, c0);
+                arrive(P_K_FULL);
+                if (lane == 0) mbar_arrive(bar(P_KS_EMPTY));
+                if (!wwait(P_VS_FULL, ph) || !wwait(P_V_EMPTY, ph ^ 1)) { ok = false; break; }
+                convert(C::kOffVS, C::kOffV, c0);
+                arrive(P_V_FULL);
+                if (lane == 0) mbar_arrive(bar(P_VS_EMPTY));
             }
         }
         if (!ok && lane == 0) fail();
@@ -296,65 +356,77 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(con
                 const bool full = __all_sync(0xffffffffu, lim >= 64 && lo <= 0);
                 if (!wwait(P_S_FULL + x, (i >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t sr[2][32];
-                tmem_ld32(tmem + lane_base + 128u * x + 64u * hf, sr[0]);
-                tmem_ld32(tmem + lane_base + 128u * x + 64u * hf + 32u, sr[1]);
-                tmem_ld_wait(sr[0]);
-                tmem_ld_wait(sr[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(P_S_EMPTY + x));
-                float mx = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                const uint32_t tS = tmem + lane_base + 128u * x + 64u * hf;
+                // scaled, biased and masked scores of columns 32 k .. + 32 of this half; read twice
+                // (for the maximum, then for P), so that 32 are held at a time
+                auto scores = [&](int k, uint32_t (&r)[32]) {
+                    tmem_ld32(tS + 32u * k, r);
                     const int rk = rel - col0 - 32 * k;
                     const int far = t31 + diag - col0 - 32 * k, near = t0 + diag - col0 - 32 * k - 31;
                     const int bk = BIAS ? relpos_bucket(far) : 0;
                     const bool one = !BIAS || ((near >= 0 || far <= 0) && bk == relpos_bucket(near));
                     const float b1 = BIAS ? __ldg(brow + bk) * 1.4426950408889634f : 0.f;
+                    tmem_ld_wait(r);
+                    if (one) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float y = __uint_as_float(sr[k][e]) * p.scale_log2;
-                        if (BIAS) y += one ? b1 : __ldg(brow + relpos_bucket(rk - e)) * 1.4426950408889634f;
-                        if (!full) y = e + 32 * k >= lo && e + 32 * k < lim ? y : -INFINITY;
-                        sr[k][e] = __float_as_uint(y);
-                        mx = fmaxf(mx, y);
+                        for (int e = 0; e < 32; ++e)
+                            r[e] = __float_as_uint(BIAS ? fmaf(__uint_as_float(r[e]), p.scale_log2, b1) : __uint_as_float(r[e]) * p.scale_log2);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), p.scale_log2,
+                                                        __ldg(brow + relpos_bucket(rk - e)) * 1.4426950408889634f));
                     }
+                    if (!full) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e + 32 * k < lo || e + 32 * k >= lim) r[e] = __float_as_uint(-INFINITY);
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t r[32];
+                    scores(k, r);
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                    mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                 }
                 float mo;
                 if (!exchange(mx, mo)) { ok = false; break; }
                 const float m_new = fmaxf(m, fmaxf(mx, mo)), m_use = m_new == -INFINITY ? 0.f : m_new;
                 const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_use);
                 m = m_new;
-                float sum = 0.f;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float y = ex2_approx(__uint_as_float(sr[k][e]) - m_use);
-                        sr[k][e] = __float_as_uint(y);
-                        sum += y;
-                    }
-                l = fmaf(l, alpha, sum);
                 if (j > 0) {  // P's columns and the output are free once the product before is done
                     if (!wwait(P_O_DONE, (i - 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     add_o(alpha);
                 }
-#pragma unroll
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
-                    // (eight packed columns at a time: the scores still to come fill the registers)
+                    uint32_t r[32];
+                    scores(k, r);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t w[3][8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            split2(__uint_as_float(sr[k][16 * h + 2 * e]), __uint_as_float(sr[k][16 * h + 2 * e + 1]), w[0][e],
-                                   w[1][e], w[2][e]);
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 y = make_float2(ex2_approx(__uint_as_float(r[16 * h + 2 * e]) - m_use),
+                                                         ex2_approx(__uint_as_float(r[16 * h + 2 * e + 1]) - m_use));
+                            sum = add2(sum, y);
+                            split2(y.x, y.y, w[0][e], w[1][e], w[2][e]);
+                        }
 #pragma unroll
                         for (int q = 0; q < 3; ++q) tmem_st8(tP + 64u * q + 32u * hf + 16u * k + 8u * h, w[q]);
                     }
                 }
+                l = fmaf(l, alpha, sum.x + sum.y);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(P_S_EMPTY + x));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -414,11 +486,11 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1) jfa_cache_split_kernel(con
 }
 
 template <int D, bool BIAS>
-cudaError_t launch(const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(jfa_cache_split_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          SpCfg::kBytes);
     if (e != cudaSuccess) return e;
-    jfa_cache_split_kernel<D, BIAS><<<num_sms, SpCfg::kThreads, SpCfg::kBytes, st>>>(p);
+    jfa_cache_split_kernel<D, BIAS><<<num_sms, SpCfg::kThreads, SpCfg::kBytes, st>>>(mk, mv, p);
     return cudaGetLastError();
 }
 
@@ -426,9 +498,10 @@ cudaError_t launch(const CacheFwdParams& p, int num_sms, cudaStream_t st) {
 
 size_t cache_split_part_bytes(int D, int num_sms) { return size_t(num_sms) * 2 * cache_merge_part(D) * 4; }
 
-cudaError_t launch_cache_split(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    if (D == 32) return p.bias ? launch<32, true>(p, num_sms, st) : launch<32, false>(p, num_sms, st);
-    return p.bias ? launch<64, true>(p, num_sms, st) : launch<64, false>(p, num_sms, st);
+cudaError_t launch_cache_split(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                               cudaStream_t st) {
+    if (D == 32) return p.bias ? launch<32, true>(mk, mv, p, num_sms, st) : launch<32, false>(mk, mv, p, num_sms, st);
+    return p.bias ? launch<64, true>(mk, mv, p, num_sms, st) : launch<64, false>(mk, mv, p, num_sms, st);
 }
 
 }  // namespace jfa
