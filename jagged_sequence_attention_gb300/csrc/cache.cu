@@ -327,14 +327,14 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.row_hi = kDecodeRows;
     }
     const CacheFwdParams pc = p;  // the merge's parameters
-    p.bm = 16;
+    p.bm = bf16 || p.g > 4 ? 16 : 4;
     p.min_units = 1;
     p.item_cost = bf16 ? kDecodeItemUnits : 2;
-    if (!fits(chunks ? 0 : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
+    if (!fits(chunks ? 4 * int64_t(B) * p.bm : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
     if (e == cudaSuccess)
-        e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, false, p, n, st);
+        e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, p, chunks, n, st);
     if (e == cudaSuccess && chunks) e = launch_cache_merge(D, pc, n, st);
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }

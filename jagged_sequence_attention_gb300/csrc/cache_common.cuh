@@ -497,8 +497,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 cudaError_t launch_cache_split(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
                                cudaStream_t st);
 size_t cache_split_part_bytes(int D, int num_sms);
-// fp32, row tiles of 128 (chunk) or 16 packed rows.
-cudaError_t launch_cache_simt(int D, bool chunk, const CacheFwdParams& p, int num_sms, cudaStream_t st);
+// fp32, items of p.bm = 4 or 16 packed rows; early: as launch_cache_decode's.
+cudaError_t launch_cache_simt(int D, const CacheFwdParams& p, bool early, int num_sms, cudaStream_t st);
 size_t cache_simt_part_bytes(int D, int num_sms);
 // bf16, row tiles of 16 packed rows: bound by the stream of K and V.
 // early: start while the chunk kernel before it in the stream still runs (they share no

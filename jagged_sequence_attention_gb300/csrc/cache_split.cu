@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    launch_dependents();  // the kernel for few rows may fill SMs as they come free
     CacheSeg g;
     auto fail = [&]() {
         *abort_flag = 1;
