@@ -878,8 +878,8 @@ __global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdPara
 
 template <int D, bool BIAS>
 cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(jfa_cache_chunk_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         ChkCfg<D>::kSmemBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(jfa_cache_chunk_kernel<D, BIAS>, ChkCfg<D>::kSmemBytes, done);
     if (e != cudaSuccess) return e;
     jfa_cache_chunk_kernel<D, BIAS><<<num_sms, ChkCfg<D>::kThreads, ChkCfg<D>::kSmemBytes, st>>>(mq, mk, mv, p);
     return cudaGetLastError();

@@ -17,6 +17,8 @@
 #include "jfa_internal.h"
 #include "ptx.cuh"
 
+#include <atomic>
+
 namespace jfa {
 
 constexpr int kCacheMaxB = 1 << 13, kCacheMaxGroups = kCacheMaxB / 32;
@@ -491,6 +493,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+// Lets `kernel` use `bytes` of shared memory per CTA, once per device (done: a bit for each).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev) & 1u)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return e;
 }
 
 // fp32, items of 128 packed rows: tensor-core products of operands in three bf16 parts each.

@@ -572,8 +572,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 template <int D, bool BIAS>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early, int num_sms,
                    cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(jfa_cache_decode_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DecCfg<D>::kBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(jfa_cache_decode_kernel<D, BIAS>, DecCfg<D>::kBytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtCtasPerSm) jfa_cache_simt_k
 template <int D, int BM, bool BIAS>
 cudaError_t launch(const CacheFwdParams& p, bool early, int num_sms, cudaStream_t st) {
     using C = SimtCfg<D, BM>;
-    cudaError_t e = cudaFuncSetAttribute(jfa_cache_simt_kernel<D, BM, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(jfa_cache_simt_kernel<D, BM, BIAS>, C::kBytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
 
 template <int D, bool BIAS>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(jfa_cache_split_kernel<D, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SpCfg::kBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(jfa_cache_split_kernel<D, BIAS>, SpCfg::kBytes, done);
     if (e != cudaSuccess) return e;
     jfa_cache_split_kernel<D, BIAS><<<num_sms, SpCfg::kThreads, SpCfg::kBytes, st>>>(mk, mv, p);
     return cudaGetLastError();
