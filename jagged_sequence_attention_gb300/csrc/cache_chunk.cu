@@ -798,9 +798,9 @@ __global__ void __launch_bounds__(608, 1)
                     part[C::kPair * D + C::kPair + prow] = n > 0 ? lt : 0.f;
                 }
             }
-            if (threadIdx.x < kMergeCtas && g.k0 == 0) {
-                if (threadIdx.x == 0)
-                    p.cuts[first] = CacheCut{g.s.q0, min(2 * rt, R - 2 * g.tile * rt), 2 * g.tile * rt, g.hk * p.g, first, last, {0, 0}};
+            const int rows = min(2 * rt, R - 2 * g.tile * rt);
+            if (int(threadIdx.x) * 64 < rows && g.k0 == 0) {
+                if (threadIdx.x == 0) p.cuts[first] = CacheCut{g.s.q0, rows, 2 * g.tile * rt, g.hk * p.g, first, last, {0, 0}};
                 p.cut_flags[first * kMergeCtas + threadIdx.x] = 1u;
             }
         }
@@ -813,23 +813,15 @@ __global__ void __launch_bounds__(608, 1)
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Adds up the parts of the items cut between blocks: CTA (i, j) takes rows 64 j .. 64 j + 63
-// of the item that starts in block i and goes on past it, if there is one (its flag, which
-// the CTA clears for the next call).  A thread takes one row and a quarter of the columns;
-// a warp's loads are whole lines, since parts are stored four columns of all rows at a time.
+// Adds up the parts of the items cut between blocks.  A task is 64 rows of the item that starts
+// in a block and goes on past it; its flag says whether there is one.  The grid is small and a
+// CTA looks at the flags of all its tasks at once, clearing them for the next call: most calls
+// cut few items, and a CTA for each possible task would cost 10 us to find nothing to do.
+// A thread takes one row and a quarter of the columns; a warp's loads are whole lines, since
+// parts are stored four columns of all rows at a time.
 template <int D>
-__global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdParams p) {
+__device__ __forceinline__ void merge_rows(const CacheFwdParams& p, const CacheCut& cut, int row, int quarter) {
     constexpr int kPart = cache_merge_part(D);
-    __shared__ uint32_t there;
-    if (threadIdx.x == 0) {
-        uint32_t* flag = p.cut_flags + blockIdx.x * kMergeCtas + blockIdx.y;
-        there = *flag;
-        if (there) *flag = 0u;
-    }
-    __syncthreads();
-    if (!there) return;
-    const CacheCut cut = p.cuts[blockIdx.x];
-    const int row = 64 * blockIdx.y + (threadIdx.x & 63), quarter = threadIdx.x >> 6;
     if (row >= cut.rows) return;
     const int first = cut.first, last = cut.last;
     const float* pm = p.part + kMergeRows * D + row;
@@ -876,6 +868,27 @@ __global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdPara
     if (p.lse && quarter == 0) p.lse[orow] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
 }
 
+template <int D>
+__global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdParams p, int tasks) {
+    __shared__ uint32_t there;
+    for (int base = blockIdx.x; base < tasks; base += 32 * gridDim.x) {  // 32 tasks of this CTA
+        if (threadIdx.x < 32) {
+            const int i = base + threadIdx.x * gridDim.x;
+            const bool set = i < tasks && p.cut_flags[i] != 0u;
+            if (set) p.cut_flags[i] = 0u;
+            const uint32_t m = __ballot_sync(0xffffffffu, set);
+            if (threadIdx.x == 0) there = m;
+        }
+        __syncthreads();
+        for (uint32_t m = there; m; m &= m - 1) {
+            const int i = base + (__ffs(m) - 1) * gridDim.x;
+            const CacheCut cut = p.cuts[i / kMergeCtas];
+            merge_rows<D>(p, cut, 64 * (i % kMergeCtas) + (threadIdx.x & 63), threadIdx.x >> 6);
+        }
+        __syncthreads();
+    }
+}
+
 template <int D, bool BIAS>
 cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
@@ -896,13 +909,13 @@ cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& 
 }
 
 cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    const dim3 grid(num_sms * kBlocksPerCta, kMergeCtas);
+    const int tasks = num_sms * kBlocksPerCta * kMergeCtas, grid = num_sms * 4;
     if (D == 128)
-        jfa_cache_merge_kernel<128><<<grid, 256, 0, st>>>(p);
+        jfa_cache_merge_kernel<128><<<grid, 256, 0, st>>>(p, tasks);
     else if (D == 32)
-        jfa_cache_merge_kernel<32><<<grid, 256, 0, st>>>(p);
+        jfa_cache_merge_kernel<32><<<grid, 256, 0, st>>>(p, tasks);
     else
-        jfa_cache_merge_kernel<64><<<grid, 256, 0, st>>>(p);
+        jfa_cache_merge_kernel<64><<<grid, 256, 0, st>>>(p, tasks);
     return cudaGetLastError();
 }
 

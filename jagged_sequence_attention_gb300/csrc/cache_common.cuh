@@ -23,7 +23,7 @@ namespace jfa {
 
 constexpr int kCacheMaxB = 1 << 13, kCacheMaxGroups = kCacheMaxB / 32;
 constexpr int kBlocksPerCta = 4;  // chunk kernel: blocks of the last part of the work, per CTA
-constexpr int kMergeCtas = 4;     // CTAs that merge a cut item of it
+constexpr int kMergeCtas = 4;     // merge tasks of a cut item of it, 64 rows each
 constexpr int kMaxSms = 320;
 // Words of the workspace's zeroed part: pieces drawn and CTAs done (chunk kernel), arrivals of
 // split items (the other kernels, at most 3 CTAs an SM), flags of cut items (chunk kernel).

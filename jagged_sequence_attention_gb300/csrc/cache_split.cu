@@ -472,9 +472,9 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
                     part[kMergeRows * D + kMergeRows + t] = lt;
                 }
             }
-            if (threadIdx.x < kMergeCtas && g.k0 == 0) {
-                if (threadIdx.x == 0)
-                    p.cuts[first] = CacheCut{g.s.q0, min(kSpBM, R - r0), r0, g.hk * p.g, first, last, {0, 0}};
+            const int rows = min(kSpBM, R - r0);
+            if (int(threadIdx.x) * 64 < rows && g.k0 == 0) {
+                if (threadIdx.x == 0) p.cuts[first] = CacheCut{g.s.q0, rows, r0, g.hk * p.g, first, last, {0, 0}};
                 p.cut_flags[first * kMergeCtas + threadIdx.x] = 1u;
             }
         }
