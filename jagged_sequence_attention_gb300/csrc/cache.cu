@@ -313,7 +313,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
             p.tile_tokens = 128 / p.g;
             p.bm = 2 * p.tile_tokens * p.g;
             p.item_cost = kChunkItemUnits;
-            p.min_units = kChunkItemUnits + 4;
+            p.min_units = kChunkItemUnits + 1;
             if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
             CUtensorMap mq;
             const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};

@@ -2,6 +2,8 @@
 any CUDA call, the binding refuses what it would misread, and planning without a device
 fails loudly."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -41,6 +43,12 @@ def test_create_without_a_gpu_fails_loudly(jfa):
     if torch.cuda.is_available():
         pytest.skip("checks the behaviour without a GPU")
     assert create(jfa) == (jfa.JFA_ERR_NO_DEVICE, None)
+
+
+def test_binding_constant_matches_the_header(jfa):
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "jfa.h")).read()
+    m = re.search(r"#define\s+JFA_CACHE_ZERO_BYTES\s+\(\(size_t\)(\d+)\)", text)
+    assert m and jfa.JFA_CACHE_ZERO_BYTES == int(m.group(1))
 
 
 def test_null_handles(jfa):

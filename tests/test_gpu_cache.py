@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from cache_cases import Case, np64
+from cache_cases import FP32_SLACK, Case, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -94,12 +94,59 @@ def test_long_history_is_split(jfa):
     c.check(*c.run(jfa))
 
 
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 2), (12, 1)])
+@pytest.mark.parametrize("D", [32, 64])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fp32_products_are_fp32(jfa, H, Hkv, D, causal):
+    # single tokens (CUDA cores), short sets, and chunks (tensor cores on split operands)
+    c = Case([1, 3, 40, 130, 300], [900, 64, 41, 700, 2500], H=H, Hkv=Hkv, D=D, page=16, dtype=F32, causal=causal, seed=30)
+    c.check(*c.run(jfa), slack=FP32_SLACK)
+
+
+@pytest.mark.parametrize("H,Hkv", [(128, 1), (100, 1), (66, 1), (34, 2)])
+def test_many_grouped_heads(jfa, H, Hkv):
+    for lens in (([1, 1], [700, 40]), ([3, 17], [130, 500])):
+        for bias in (False, True):
+            c = Case(*lens, H=H, Hkv=Hkv, D=64, page=32, bias=bias, seed=H)
+            c.check(*c.run(jfa))
+    c = Case([1, 5], [70, 300], H=H, Hkv=Hkv, D=32, page=32, dtype=F32, seed=H)
+    c.check(*c.run(jfa))
+
+
+def test_cache_past_32_bits(jfa):
+    # pages whose elements lie past 2^31 (and bytes past 2^32), in reads and in appends
+    page, Hkv, D = 64, 8, 128
+    n_pages = 2 ** 31 // (page * Hkv * D) + 40
+    q, kv = [1, 70, 1], [200, 300, 900]
+    c = append_case(q, kv, H=16, Hkv=Hkv, D=D, page=page, dtype=BF, R=D, kind="half", seed=31)
+    small_k, small_v, table = c.Kc, c.Vc, c.host_table.copy()
+    far = n_pages - small_k.shape[0]
+    c.Kc = torch.empty(n_pages, page, Hkv, D, dtype=BF, device="cuda")
+    c.Vc = torch.empty(n_pages, page, Hkv, D, dtype=BF, device="cuda")
+    c.Kc[far:], c.Vc[far:] = small_k, small_v
+    c.host_table = np.where(table >= 0, table + far, table).astype(np.int32)
+    c.table = torch.from_numpy(c.host_table).cuda()
+    cache = jfa.jfa_cache_create(c.Kc, c.Vc)
+    c.Q = jfa.jfa_cache_append(cache, c.K, c.V, c.q_off, c.kv_lens, c.table, Q=c.Q, rot=c.rot)
+    O, lse = c.run(jfa, cache)
+    # the same on the small copy
+    near = jfa.jfa_cache_create(small_k, small_v)
+    t0 = torch.from_numpy(table).cuda()
+    jfa.jfa_cache_append(near, c.K, c.V, c.q_off, c.kv_lens, t0, rot=c.rot)
+    O2, lse2 = jfa.jfa_cache_fwd(near, c.Q, c.q_off, c.kv_lens, t0, max_q_len=70)
+    torch.cuda.synchronize()
+    assert torch.equal(c.Kc[far:], small_k) and torch.equal(c.Vc[far:], small_v)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    c.Kc, c.Vc, c.host_table = small_k, small_v, table
+    c.check(O, lse)
+
+
 def test_many_sequences(jfa):
     rs = np.random.RandomState(1)
-    for B in (33, 300, 1500):
+    for B, dtype in ((33, BF), (300, BF), (1500, BF), (1025, F32), (8192, BF)):
         kv = rs.randint(1, 90, B)
-        q = np.minimum(kv, np.where(rs.rand(B) < 0.9, 1, rs.randint(0, 40, B)))
-        c = Case(q, kv, H=4, Hkv=2, D=64, page=16, seed=B)
+        q = np.minimum(kv, np.where(rs.rand(B) < 0.9, 1, rs.randint(0, 80, B)))
+        c = Case(q, kv, H=4, Hkv=2, D=64, page=16, dtype=dtype, seed=B)
         c.check(*c.run(jfa))
 
 
@@ -410,6 +457,44 @@ def test_a_captured_step_is_replayed_on_new_contents(jfa):
     assert jfa.jfa_cache_device_status(cache) == jfa.JFA_OK
 
 
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64)])
+def test_a_captured_mixed_batch_is_replayed_on_new_lengths(jfa, dtype, D):
+    """One graph over every kernel of a mixed batch; between replays the offsets, lengths and
+    page table change, so sequences move between the kernels."""
+    H, Hkv, page, T = 4, 2, 16, 500
+    Q = torch.randn(T, H, D, device="cuda", dtype=F32).to(dtype)
+    Kc = torch.randn(400, page, Hkv, D, device="cuda", dtype=F32).to(dtype)
+    Vc = torch.randn(400, page, Hkv, D, device="cuda", dtype=F32).to(dtype)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    off, kv, table = torch.zeros(6, **i32), torch.zeros(5, **i32), torch.zeros(5, 100, **i32)
+    cache = jfa.jfa_cache_create(Kc, Vc)
+    ws = jfa.jfa_cache_workspace(cache, H)
+    O, lse = torch.empty_like(Q), torch.empty(T, H, device="cuda", dtype=F32)
+
+    def step():
+        jfa.jfa_cache_fwd(cache, Q, off, kv, table, O=O, lse=lse, workspace=ws)  # (no bound on the query lengths)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rs = np.random.RandomState(5)
+    for q, n in (([1, 300, 1, 0, 40], [900, 1300, 30, 77, 640]), ([1] * 5, [100, 1, 1500, 16, 17]),
+                 ([0, 0, 0, 0, 500], [0, 5, 0, 0, 500]), ([90, 10, 300, 20, 80], [1500, 900, 301, 20, 1200])):
+        off.copy_(torch.tensor(np.concatenate([[0], np.cumsum(q)])))
+        kv.copy_(torch.tensor(n))
+        table.copy_(torch.from_numpy(np.stack([rs.permutation(400)[:100] for _ in range(5)])))
+        O.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert jfa.jfa_cache_device_status(cache) == jfa.JFA_OK
+        c = Case(q, n, H=H, Hkv=Hkv, D=D, page=page, dtype=dtype)
+        c.Q, c.Kc, c.Vc, c.table, c.host_table = Q, Kc, Vc, table, table.cpu().numpy()
+        c.check(O, lse)
+        assert bool((O[c.T:] == 3.0).all()) and not bool(ws[:jfa.JFA_CACHE_ZERO_BYTES].any())
+
+
 def test_two_calls_at_once_on_one_handle(jfa):
     c = Case([1, 1, 200], [9000, 17, 5000], H=8, Hkv=2, D=128, page=64, seed=21)
     cache = jfa.jfa_cache_create(c.Kc, c.Vc)
@@ -459,6 +544,10 @@ def test_refusals(jfa):
     assert fwd(workspace=ws[:-256]) == bad and fwd(workspace=ws[16:]) == bad
     assert fwd(bias=torch.zeros(4, 31, device="cuda", dtype=F32)) == bad
     assert fwd(O=torch.empty(6, 4, 64, dtype=torch.float16, device="cuda")) == uns
+    many = torch.zeros(8194, dtype=torch.int32, device="cuda")  # more sequences than a call takes
+    assert fwd(q_offsets=many, kv_lens=many[1:], page_table=many[1:, None].contiguous()) == bad
+    wide = torch.zeros(6, 258, 64, dtype=BF, device="cuda")     # more than 128 heads on one key head
+    assert status_of(jfa, jfa.jfa_cache_fwd, cache, wide, c.q_off, c.kv_lens, c.table) == uns
     assert app(Q=None) == jfa.JFA_OK and app(rot=None) == bad and app(Q=None, rot=None) == jfa.JFA_OK
     assert app(rot=torch.zeros(60, 24, device="cuda", dtype=F32)) == bad and app(rot=torch.zeros(60, 80, device="cuda", dtype=F32)) == bad
     assert app(rot_kind="other") == bad and app(V=c.V[:3]) == bad and app(Q_out=c.Q[:3]) == bad
