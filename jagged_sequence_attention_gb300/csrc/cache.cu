@@ -66,10 +66,10 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
 constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 // What an item's start and end cost the decode kernel, in its stages of 32 KB: about 4 us of a
-// CTA, at its share of the memory's rate.
-// The same for the chunk kernel, in its steps of 128 keys (about 2 us each).
-constexpr int kChunkItemUnits = 3;
+// CTA, at its share of the memory's rate.  And the chunk and split kernels, in their steps of
+// 128 keys (about 2 us each).
 constexpr int kDecodeItemUnits = 3;
+constexpr int kChunkItemUnits = 3;
 
 // Whether the cache's device is the current one.
 bool on_device(jfa_cache c) {
@@ -238,7 +238,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     int32_t max_kv = 0;
     const jfa_status s = check_batch(cache, B, T, q_offsets, kv_lens, page_table, max_pages, &max_kv);
     if (s != JFA_OK) return s;
-    if (H < 1 || H > 65535 || H % cache->Hkv != 0 || T * H > INT32_MAX || max_q_len < 0) return JFA_ERR_INVALID_ARG;
+    if (H < 1 || H > 65535 || H % cache->Hkv != 0 || T * H > INT32_MAX - 256 || max_q_len < 0) return JFA_ERR_INVALID_ARG;
     if (cache->dtype == JFA_BF16 && H / cache->Hkv > 128) return JFA_ERR_UNSUPPORTED;  // a token's rows fill one tile
     if ((causal != 0 && causal != 1) || window < -1 || (window >= 0 && causal != 1)) return JFA_ERR_INVALID_ARG;
     if (bias_kind != JFA_BIAS_NONE && bias_kind != JFA_BIAS_RELPOS32)
@@ -247,7 +247,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     if (!(scale > 0.f && scale < INFINITY)) return JFA_ERR_INVALID_ARG;
     if (o_dtype != JFA_BF16 && o_dtype != JFA_F32) return JFA_ERR_INVALID_ARG;
     if (cache->dtype == JFA_F32 && o_dtype != JFA_F32) return JFA_ERR_UNSUPPORTED;
-    if (T > 0 && (!row_ok(cache, Q, q_stride, H) || !O || !aligned(O, 16) || !aligned(lse, 4))) return JFA_ERR_INVALID_ARG;
+    if (T > 0 && (!row_ok(cache, Q, q_stride, H) || !O || O == Q || !aligned(O, 16) || !aligned(lse, 4))) return JFA_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < jfa_cache_workspace_size(cache, H))
         return JFA_ERR_INVALID_ARG;
     if (!on_device(cache)) return JFA_ERR_PLAN_MISMATCH;
@@ -294,9 +294,10 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const int n = cache->num_sms, D = cache->D;
     const bool bf16 = cache->dtype == JFA_BF16;
     const bool chunks = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g > kDecodeRows;
-    // the kernels count units in 31 bits
-    auto fits = [&](int64_t rows, int bm, int bn) {
-        return double(rows / bm + B) * p.Hkv * (double(max_kv) / bn + 16.0) < double(INT32_MAX);
+    // the kernels count units in 31 bits; the row tiles of `rows` rows are at most
+    auto tiles = [&](int64_t rows) { return rows / p.bm + B; };
+    auto fits = [&](int64_t n_tiles, int bn) {
+        return double(n_tiles) * p.Hkv * (double(max_kv) / bn + 16.0) < double(INT32_MAX) - 65536.0;
     };
     cudaError_t e = cudaSuccess;
     if (chunks) {
@@ -306,7 +307,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.min_units = 1;
         if (!bf16) {
             p.item_cost = kChunkItemUnits;
-            if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
+            if (!fits(tiles(T * p.g), 128)) return JFA_ERR_UNSUPPORTED;
             e = launch_cache_split(D, cache->mk, cache->mv, p, n, st);
         } else {
             // the queries as (D, head, token), boxes of one tile's rows
@@ -314,7 +315,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
             p.bm = 2 * p.tile_tokens * p.g;
             p.item_cost = kChunkItemUnits;
             p.min_units = kChunkItemUnits + 1;
-            if (!fits(T * p.g, p.bm, 128)) return JFA_ERR_UNSUPPORTED;
+            if (!fits(tiles(T * p.g), 128)) return JFA_ERR_UNSUPPORTED;
             CUtensorMap mq;
             const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
             const int64_t strides[2] = {D, q_stride};
@@ -330,7 +331,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.bm = bf16 || p.g > 4 ? 16 : 4;
     p.min_units = 1;
     p.item_cost = bf16 ? kDecodeItemUnits : 2;
-    if (!fits(chunks ? 4 * int64_t(B) * p.bm : T * p.g, p.bm, 64)) return JFA_ERR_UNSUPPORTED;
+    if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g), 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
     if (e == cudaSuccess)

@@ -5,7 +5,7 @@
 // One CTA per token.  Everything is read and written once in 16-byte vectors; a thread
 // takes both vectors of a half-split pair, so a query head may be rotated in place.  The
 // token's sequence is found by a 32-way search of the offsets (one load deep up to 31
-// sequences, two up to 1023), and the token's data loads do not wait for it.
+// sequences, two up to 1023).
 #include "cache_common.cuh"
 
 namespace jfa {

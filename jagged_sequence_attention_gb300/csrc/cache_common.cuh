@@ -18,6 +18,7 @@
 #include "ptx.cuh"
 
 #include <atomic>
+#include <climits>
 
 namespace jfa {
 
@@ -135,6 +136,15 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
     return v;
 }
 
+// Sum over the warp of values below 2^31 that lanes have added up mod 2^32 (w) and in their
+// upper 16 bits (hi); -1 unless it is below 2^31 - 2^16.  One sequence's units fit (cache.cu
+// checks), but offsets that go back and forth make many sequences of the same rows.
+__device__ __forceinline__ int cache_sum(uint32_t w, int hi) {
+    const int s = int(__reduce_add_sync(0xffffffffu, w));
+    return __reduce_add_sync(0xffffffffu, hi) >= 0x7fff || s < 0 ? -1 : s;  // (hi: within 256 of the sum's)
+}
+__device__ __forceinline__ int cache_sum(int v) { return cache_sum(uint32_t(v), v >> 16); }
+
 // Units of one key head of a lane's sequence, by the whole warp: a lane counts the tiles of
 // its own short sequence, and the warp together those of a long one.
 template <int BN>
@@ -212,7 +222,12 @@ __device__ __forceinline__ void cache_locate(const CacheFwdParams& p, int c, con
     }
 }
 
+// total < 0: more units than can be counted, none is worked on.
 __device__ __forceinline__ void cache_cut(const CacheFwdParams& p, int total, CacheStart& st) {
+    if (total < 0) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
+        total = 0;
+    }
     const int want = int((uint32_t(total) + uint32_t(p.min_units) - 1u) / uint32_t(p.min_units));
     const int G = min(int(gridDim.x), max(want, 1)), cta = blockIdx.x;
     st = CacheStart{0, 0, 0, 0, 0, 0, 0, 0};
@@ -235,19 +250,23 @@ __device__ __forceinline__ CacheStart cache_start(const CacheFwdParams& p, int* 
     if (groups <= 1) {
         const CacheSeq s = cache_lane_seq(p, 0, lane, blockIdx.x == 0 && warp == 0);
         const int one = cache_seq_units<BN>(p, s, lane);
-        cache_cut(p, __reduce_add_sync(0xffffffffu, one) * p.Hkv, st);
+        cache_cut(p, cache_sum(one * p.Hkv), st);
         if (st.u < st.u_end) cache_locate<BN>(p, 0, s, one, st.u, lane, st);
         return st;
     }
     for (int c = warp; c < groups; c += warps) {
         const CacheSeq s = cache_lane_seq(p, c, lane, blockIdx.x == 0);
-        const int v = __reduce_add_sync(0xffffffffu, cache_seq_units<BN>(p, s, lane));
-        if (lane == 0) sums[c] = v * p.Hkv;
+        const int v = cache_sum(cache_seq_units<BN>(p, s, lane) * p.Hkv);
+        if (lane == 0) sums[c] = v < 0 ? INT_MAX : v;
     }
     __syncthreads();
-    int total = 0;
-    for (int c = lane; c < groups; c += 32) total += sums[c];
-    cache_cut(p, __reduce_add_sync(0xffffffffu, total), st);
+    uint32_t total = 0;
+    int hi = 0;
+    for (int c = lane; c < groups; c += 32) {
+        total += uint32_t(sums[c]);
+        hi += sums[c] >> 16;
+    }
+    cache_cut(p, cache_sum(total, hi), st);
     if (st.u < st.u_end) {
         int left = st.u, c = 0;
         for (int c0 = 0; c0 < groups; c0 += 32) {
@@ -414,17 +433,17 @@ __device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroup
         if (32 * c + lane < p.B) G->order[32 * c + rank] = uint8_t(lane);
         // a sequence's last item sees the most keys (but for a window's odd tile)
         const int n = __reduce_max_sync(0xffffffffu, tiles > 0 ? cache_units<BN>(p, s, tiles - 1) : 0);
-        const int u = __reduce_add_sync(0xffffffffu, cache_seq_units<BN>(p, s, lane));
+        const int u = cache_sum(cache_seq_units<BN>(p, s, lane) * p.Hkv);
         const int t = __reduce_add_sync(0xffffffffu, tiles);
         if (lane == 0) {
-            G->units[c] = u * p.Hkv;
+            G->units[c] = u < 0 ? INT_MAX : u;
             G->items[c] = t * p.Hkv;
             atomicMax(&G->longest, n);
         }
     }
     __syncthreads();
     if (warp == 0) {
-        int u = 0, items = 0;
+        int u = 0, items = 0, hi = 0;
         for (int c0 = 0; c0 < groups; c0 += 32) {  // sums to exclusive prefixes
             const bool in = c0 + lane < groups;
             const int v = in ? G->units[c0 + lane] : 0, w = in ? G->items[c0 + lane] : 0;
@@ -435,8 +454,13 @@ __device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroup
             }
             u += __shfl_sync(0xffffffffu, vi, 31);
             items += __shfl_sync(0xffffffffu, wi, 31);
+            hi += __reduce_add_sync(0xffffffffu, v >> 16);
         }
         __syncwarp();
+        if (hi >= 0x7fff || u < 0) {  // more units than can be counted: none is worked on
+            if (blockIdx.x == 0 && lane == 0) atomicOr(p.status, kStatusBounds);
+            u = items = 0;
+        }
         const int grid = gridDim.x, longest = G->longest;
         // The last part, cut in blocks, covers the spread with which the CTAs come out of the
         // whole items: half an item each, the last ones being of average length or less.  Where

@@ -499,12 +499,13 @@ def jfa_cache_append(cache: Cache, K, V, q_offsets, kv_lens, page_table, Q=None,
     [rot_len, rot_dim] (cosines, then sines, fp32), applied to the keys and to Q [T, H, D]
     (into Q_out, which may be Q; allocated if None).  Returns Q_out (None without Q)."""
     if Q is not None and Q_out is None:
-        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        with torch.cuda.stream(stream):
+            Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
     try:
         status = _calls.append(cache.info, K, V, q_offsets, kv_lens, page_table, Q, Q_out, rot,
                                ROT_KINDS.get(rot_kind, -1) if isinstance(rot_kind, str) else rot_kind,
                                None if stream is None else stream.cuda_stream)
-    except (ValueError, TypeError) as e:
+    except (ValueError, TypeError, OverflowError) as e:
         raise JFAError(f"jfa_cache_append ({e})", JFA_ERR_INVALID_ARG) from None
     if status != JFA_OK:
         raise JFAError("jfa_cache_append", status)
@@ -531,22 +532,19 @@ def jfa_cache_fwd(cache: Cache, Q, q_offsets, kv_lens, page_table, bias=None, sc
     """Attention of the new tokens Q [T, H, D] over the cache.  Returns (O, lse).  bias: the
     bucket table [H, 32]; max_q_len: an upper bound of the batch's query lengths (it chooses
     the kernel); workspace: jfa_cache_workspace's, kept by the caller (one is made if None)."""
-    if O is None:
-        O = torch.empty(Q.shape, dtype=out_dtype or Q.dtype, device=Q.device)
-    if lse is None:
-        lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
-    if workspace is None:
-        H = Q.shape[1] if Q.dim() == 3 else 0
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                workspace = jfa_cache_workspace(cache, H)
-        else:
-            workspace = jfa_cache_workspace(cache, H)
+    if O is None or lse is None or workspace is None:
+        with torch.cuda.stream(stream):  # what is made here belongs to the stream that writes it
+            if O is None:
+                O = torch.empty(Q.shape, dtype=out_dtype or Q.dtype, device=Q.device)
+            if lse is None:
+                lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
+            if workspace is None:
+                workspace = jfa_cache_workspace(cache, Q.shape[1] if Q.dim() == 3 else 0)
     try:
         status = _calls.fwd(cache.info, Q, q_offsets, kv_lens, page_table, bias,
                             cache.D ** -0.5 if scale is None else scale, causal, window, max_q_len, O, lse, workspace,
                             None if stream is None else stream.cuda_stream)
-    except (ValueError, TypeError) as e:
+    except (ValueError, TypeError, OverflowError) as e:
         raise JFAError(f"jfa_cache_fwd ({e})", JFA_ERR_INVALID_ARG) from None
     if status != JFA_OK:
         raise JFAError("jfa_cache_fwd", status)

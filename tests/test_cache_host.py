@@ -107,6 +107,10 @@ def test_binding_refuses_what_it_would_misread(jfa):
     with pytest.raises(jfa.JFAError) as e:  # the public call, with the binding's own error
         jfa.jfa_cache_append(cache, wide, v, off, kv, table)
     assert e.value.status == bad
+    for kw in (dict(window=2 ** 70), dict(max_q_len=-2 ** 70)):
+        with pytest.raises(jfa.JFAError) as e:
+            jfa.jfa_cache_fwd(cache, q, off, kv, table, O=fgood["O"], lse=fgood["lse"], workspace=fgood["ws"], **kw)
+        assert e.value.status == bad
     cache.handle = cache.info = None        # as after jfa_cache_destroy
     with pytest.raises(jfa.JFAError):
         jfa.jfa_cache_append(cache, k, v, off, kv, table)

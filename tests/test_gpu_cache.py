@@ -590,3 +590,60 @@ def test_empty_calls(jfa):
         assert O.shape == (0, 4, 64) and lse.shape == (0, 4)
     torch.cuda.synchronize()
     assert jfa.jfa_cache_device_status(cache) == jfa.JFA_OK
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 64), (F32, 64)])
+@pytest.mark.parametrize("max_q_len", [None, 1])
+def test_offsets_that_go_back_and_forth(jfa, dtype, D, max_q_len):
+    # every second sequence claims all 512 rows over a million keys: 4096 x 16 row tiles x 8
+    # heads x 8192 key tiles are more than 2^31.  Nothing is computed, and the call says so.
+    B, T, H, kv = 8192, 512, 64, 1 << 20
+    Kc = torch.zeros(1, 1024, 8, D, dtype=dtype, device="cuda")
+    cache = jfa.jfa_cache_create(Kc, Kc.clone())
+    i32 = dict(dtype=torch.int32, device="cuda")
+    off = torch.zeros(B + 1, **i32)
+    off[1::2] = T
+    lens, table = torch.full((B,), kv, **i32), torch.zeros(B, kv // 1024, **i32)
+    Q = torch.zeros(T, H, D, dtype=dtype, device="cuda")
+    O = torch.full_like(Q, 7.0)
+    ws = jfa.jfa_cache_workspace(cache, H)
+    jfa.jfa_cache_fwd(cache, Q, off, lens, table, max_q_len=max_q_len, O=O, workspace=ws)
+    torch.cuda.synchronize()
+    assert jfa.jfa_cache_device_status(cache) == jfa.JFA_ERR_DEVICE_BOUNDS
+    assert torch.all(O == 7.0) and not ws[:jfa.JFA_CACHE_ZERO_BYTES].any()
+    # the same workspace afterwards: zero keys and queries give the mean of zero values
+    off = torch.cat([torch.zeros(1, **i32), torch.full((B,), T, **i32)])
+    lens[0], lens[1:] = 700, 0
+    jfa.jfa_cache_fwd(cache, Q, off, lens, table, max_q_len=max_q_len, O=O, workspace=ws)
+    torch.cuda.synchronize()
+    assert jfa.jfa_cache_device_status(cache) == jfa.JFA_OK and not O.any()
+
+
+def test_outputs_made_by_a_call_belong_to_its_stream(jfa):
+    c = Case(*RAGGED, H=4, Hkv=2, D=64, page=16, seed=8)
+    cache = jfa.jfa_cache_create(c.Kc, c.Vc)
+    want = c.run(jfa, cache)
+    rot = make_table(2048, 64)
+    K, V = torch.randn(2, c.T, 2, 64, device="cuda", dtype=F32).to(BF)
+    full = torch.arange(c.table.numel(), dtype=torch.int32, device="cuda").view_as(c.table)
+    scratch = [jfa.jfa_cache_create(*torch.zeros(2, full.numel(), 16, 2, 64, device="cuda", dtype=BF)) for _ in range(2)]
+    lens = torch.maximum(c.kv_lens, c.q_off[1:] - c.q_off[:-1])
+    want_q = jfa.jfa_cache_append(scratch[0], K, V, c.q_off, lens, full, Q=c.Q, rot=rot)
+    ws = jfa.jfa_cache_workspace(cache, 4)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)  # the current stream is busy for about 50 ms
+    freed = [torch.empty_like(x) for x in (*want, c.Q)]
+    for x in freed:
+        x.fill_(3.0)                # writes still to come to memory that is given back now
+    del freed, x
+    O, lse = jfa.jfa_cache_fwd(cache, c.Q, c.q_off, c.kv_lens, c.table, workspace=ws, max_q_len=200, stream=s)
+    Qo = jfa.jfa_cache_append(scratch[1], K, V, c.q_off, lens, full, Q=c.Q, rot=rot, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(O, want[0]) and torch.equal(lse, want[1]) and torch.equal(Qo, want_q)
+
+
+def test_output_over_the_queries_is_refused(jfa):
+    c = Case([1, 5], [20, 9], H=4, Hkv=2, D=64, page=16, unset=False)
+    cache = jfa.jfa_cache_create(c.Kc, c.Vc)
+    assert status_of(jfa, jfa.jfa_cache_fwd, cache, c.Q, c.q_off, c.kv_lens, c.table, O=c.Q) == jfa.JFA_ERR_INVALID_ARG
