@@ -13,7 +13,8 @@
 //   warps 4-7, 12-15   tile B
 //   warp 16            TMA loads: Q once per item, K and V boxes through rings
 //   warp 17            tcgen05.mma issuer and TMEM owner; clears V rows no query may see
-//   warp 18            draws pieces of work ahead of the others and hands out their items
+//   warp 18            draws pieces of work when the loads near the end of what was drawn, and
+//                      hands out their items
 // TMEM (512 columns): S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P
 // overwrites its own S columns as packed bf16 and is read from TMEM by O += P V.
 // An item with a single row tile runs its steps alternately as tile A and tile B (both on
@@ -56,10 +57,12 @@ struct ChkCfg {
     static constexpr int kStages = D == 128 ? 2 : 5;
     static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + kStages * kKVBytes;
     static constexpr int kOffBar = kOffV + kStages * kKVBytes;
-    static constexpr int kNumBars = 48;
+    static constexpr int kNumBars = 56;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag, merge flag
-    static constexpr int kOffSeg = kOffMisc + 16;             // the part of an item handed out next
-    static constexpr int kOffStarts = kOffSeg + int(sizeof(SegRec));  // first position of each bias bucket
+    static constexpr int kSlots = 4;                          // parts of items handed out and not yet taken by all
+    static constexpr int kAsk = 3;                            // key tiles of a part left to load when the next is asked for
+    static constexpr int kOffSeg = kOffMisc + 16;
+    static constexpr int kOffStarts = kOffSeg + kSlots * int(sizeof(SegRec));  // first position of each bias bucket
     static constexpr int kOffComb = kOffStarts + 32 * 4;      // tile B's m and l of a split item, two buffers
     static constexpr int kOffXch = kOffComb + 2 * 3 * BM * 4; // pair exchanges [2][2][8][32]
     static constexpr int kOffGroups = kOffXch + 2 * 2 * 8 * 32 * 4;
@@ -86,13 +89,14 @@ enum {
     B_O_EMPTY = 8,
     B_DRAIN = 10,
     B_COMBINE = 11,  // split item: tile B's last P V done and its m and l written
-    B_SEG_FULL = 12,   // the next part of an item handed out
-    B_SEG_EMPTY = 13,  // and read by every other warp
+    B_ASK = 12,      // the producer is near the end of its part
     B_XCH = 14,      // +pair of warps
     B_K_FULL = 22,   // +stage (up to 6)
     B_K_EMPTY = 28,
     B_V_FULL = 34,
     B_V_EMPTY = 40,
+    B_SEG_FULL = 46,   // +slot: a part of an item handed out
+    B_SEG_EMPTY = 50,  // +slot: and read by every other warp
 };
 
 // TMEM column (within a tile's S/P columns) of the 16 P values of P V step s.
@@ -160,8 +164,11 @@ __global__ void __launch_bounds__(608, 1)
         mbar_init(bar(B_DRAIN), 1);
         mbar_init(bar(B_COMBINE), 8);
         for (int q = 0; q < 8; ++q) mbar_init(bar(B_XCH + q), 2);
-        mbar_init(bar(B_SEG_FULL), 1);
-        mbar_init(bar(B_SEG_EMPTY), C::kSoftWarps + 2);
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(bar(B_SEG_FULL + s), 1);
+            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + 2);
+        }
+        mbar_init(bar(B_ASK), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -197,10 +204,12 @@ __global__ void __launch_bounds__(608, 1)
     uint32_t seg_no = 0;
     // The next part of an item (false: no more, or the CTA gave up).
     auto next = [&]() -> bool {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_SEG_FULL), seg_no & 1, abort_flag))) return false;
-        const SegRec r = *handed;
+        const uint32_t slot = seg_no % C::kSlots;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_SEG_FULL + slot), (seg_no / C::kSlots) & 1, abort_flag)))
+            return false;
+        const SegRec r = handed[slot];
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_SEG_EMPTY));
+        if (lane == 0) mbar_arrive(bar(B_SEG_EMPTY + slot));
         ++seg_no;
         if (r.b < 0) return false;
         g.b = r.b;
@@ -242,10 +251,15 @@ __global__ void __launch_bounds__(608, 1)
         auto wwait = [&](int b, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag));
         };
+        auto ask = [&]() {
+            if (lane == 0) mbar_arrive(bar(B_ASK));
+        };
         while (ok && next()) {
-            if (g.r.n == 0) continue;
-            if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
-            {
+            if (g.r.n == 0) {
+                ask();
+                continue;
+            }
+            auto load_q = [&]() {
                 // a box per tile and column block; tokens past the sequence's are not stored
                 const int tiles = (2 * g.tile + 1) * p.tile_tokens < g.s.q_len ? 2 : 1;
                 if (lane == 0)
@@ -254,10 +268,20 @@ __global__ void __launch_bounds__(608, 1)
                 if (lane < tiles * C::kCB)
                     tma_load_3d(sQ + (lane / C::kCB) * C::kQBytes + (lane % C::kCB) * C::BM * 128, &tmQ, bar(B_Q_FULL),
                                 (lane % C::kCB) * 64, g.hk * p.g, g.s.q0 + (2 * g.tile + lane / C::kCB) * p.tile_tokens);
-            }
-            ++item_it;
+                ++item_it;
+            };
+            // Q's memory is free when the last part's scores are done; its first key tiles may
+            // be in flight by then
+            bool have_q = __all_sync(0xffffffffu, mbar_try_wait(bar(B_Q_EMPTY), (item_it & 1) ^ 1));
+            if (have_q) load_q();
             int page = page_of(g, g.k0);
             for (int k = g.k0; k < g.k1; ++k, ++kv_it) {
+                if (g.k1 - k == min(C::kAsk, g.k1 - g.k0)) ask();
+                if (!have_q && k - g.k0 == C::kStages / 2) {
+                    if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+                    load_q();
+                    have_q = true;
+                }
                 const uint32_t st = kv_it % C::kStages, ph = (kv_it / C::kStages) & 1;
                 const int at = page, slot = ((g.r.f + k) * C::BN + pg * rows) & ((1 << p.page_log2) - 1);
                 const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, at >= 0)) * rows * 128);
@@ -271,6 +295,10 @@ __global__ void __launch_bounds__(608, 1)
                 __syncwarp();
                 if (at >= 0) tma_load_4d(sV + st * C::kKVBytes + box, &tmV, bar(B_V_FULL + st), cb * 64, slot, g.hk, at);
             }
+            if (ok && !have_q) {
+                if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+                load_q();
+            }
         }
         if (!ok && lane == 0) fail();
         if (item_it > 0) mbar_wait_bounded(bar(B_Q_FULL), (item_it - 1) & 1, nullptr);
@@ -281,19 +309,29 @@ __global__ void __launch_bounds__(608, 1)
         const int ng = (p.B + 31) >> 5, pieces = groups->pieces, whole = groups->whole, blk = groups->blk;
         const int cut = groups->cut;
         bool ok = true;
-        // Waits until the part handed out last has been taken by every warp, so that a CTA
-        // holds one part beside the one it works on, and draws no more than it can work off.
-        auto taken = [&]() {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(B_SEG_EMPTY), (seg_no & 1) ^ 1, abort_flag));
+        uint32_t asked = 0;
+        auto wwait = [&](int b, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag));
+            return ok;
+        };
+        // A CTA draws when the loads of all it was handed are near their end: no more than it
+        // can work off, however long, and as many short parts as keep the loads in flight.
+        // (Waited for before every part handed out, so that the barrier is never two phases
+        // ahead of the wait.)
+        auto wanted = [&]() {
+            for (; asked < seg_no && ok; ++asked) wwait(B_ASK, asked & 1);
             return ok;
         };
         auto hand_out = [&](const SegRec& r) {
+            const uint32_t slot = seg_no % C::kSlots;
+            if (!wanted() || !wwait(B_SEG_EMPTY + int(slot), ((seg_no / C::kSlots) & 1) ^ 1)) return false;
             if (lane == 0) {
-                *handed = r;
-                mbar_arrive(bar(B_SEG_FULL));
+                handed[slot] = r;
+                mbar_arrive(bar(B_SEG_FULL + slot));
             }
             __syncwarp();
             ++seg_no;
+            return true;
         };
         int w = blockIdx.x;
         while (w < pieces) {
@@ -307,7 +345,7 @@ __global__ void __launch_bounds__(608, 1)
                 st.u_end = min(groups->total, u + blk);
             }
             CacheCursor<C::BN> cur(st, groups->order);
-            while (cur.next(p, g) && taken()) {
+            while (ok && cur.next(p, g)) {
                 SegRec r{g.b, g.hk, g.tile, g.k0, g.k1, g.s.q0, g.s.q_len, g.s.kv_len, 0, 0, 0, 0};
                 if (w >= whole) {
                     r.first = int(uint32_t(g.first + p.item_cost - cut) / uint32_t(blk));
@@ -317,11 +355,11 @@ __global__ void __launch_bounds__(608, 1)
                 hand_out(r);
                 if (w < whole) break;
             }
-            if (!taken()) break;
+            if (!wanted()) break;
             if (lane == 0) w = int(gridDim.x + atomicAdd(p.counters + kCtrDrawn, 1u));
             w = __shfl_sync(0xffffffffu, w, 0);
         }
-        if (taken()) hand_out(SegRec{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
+        hand_out(SegRec{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
         if (!ok && lane == 0) fail();
         // the last CTA to have drawn its last piece leaves the counters zero
         if (lane == 0 && atomicAdd(p.counters + kCtrDone, 1u) == gridDim.x - 1) {

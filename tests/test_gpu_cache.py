@@ -647,3 +647,24 @@ def test_output_over_the_queries_is_refused(jfa):
     c = Case([1, 5], [20, 9], H=4, Hkv=2, D=64, page=16, unset=False)
     cache = jfa.jfa_cache_create(c.Kc, c.Vc)
     assert status_of(jfa, jfa.jfa_cache_fwd, cache, c.Q, c.q_off, c.kv_lens, c.table, O=c.Q) == jfa.JFA_ERR_INVALID_ARG
+
+
+# Query sets of at most 64 packed rows at head dimension 64, two key tiles at a time: odd and
+# even numbers of key tiles, a single one, an item cut between CTAs, more rows than keys.
+SETS = ([17, 33, 64, 63, 20, 48, 32, 21, 60], [17, 200, 640, 129, 5000, 257, 0, 20000, 9])
+
+
+@pytest.mark.parametrize("H,Hkv,div", [(3, 3, 1), (4, 2, 2), (5, 1, 5), (3, 1, 3)])
+@pytest.mark.parametrize("causal,window,bias", [(False, None, False), (True, None, True), (True, 300, False), (False, None, True)])
+@pytest.mark.parametrize("page", [8, 128])
+def test_short_query_sets(jfa, H, Hkv, div, causal, window, bias, page):
+    q = [max(1, n // div) for n in SETS[0]]
+    c = Case(q, SETS[1], H=H, Hkv=Hkv, D=64, page=page, causal=causal, window=window, bias=bias, seed=H + page)
+    c.check(*c.run(jfa, out_dtype=F32))
+
+
+def test_short_and_long_query_sets_take_turns(jfa):
+    q = [40, 300, 18, 129, 64, 65, 500, 33] * 40
+    kv = [n + 100 * (i % 7) for i, n in enumerate(q)]
+    c = Case(q, kv, H=2, Hkv=1, D=64, page=32, seed=4)
+    c.check(*c.run(jfa))
