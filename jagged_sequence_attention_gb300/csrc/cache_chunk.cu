@@ -563,19 +563,26 @@ __global__ void __launch_bounds__(608, 1)
                 }
                 if (!wwait(B_S_FULL + x, s_cnt & 1)) { ok = false; break; }
                 tc_fence_after();
-                // With a bias one chunk's scores are held at a time, in rolled loops: the three
-                // ways of its lookup would otherwise be laid out four times, and a short item
-                // pays for every line of code it fetches.
-                constexpr int kLive = BIAS ? 1 : 2;
-                uint32_t sr[kLive][32];
-                if (!BIAS) {
+                // Without a bias both chunks' scores are held at a time, with one they are taken one
+                // by one in rolled loops: the three ways of its lookup would otherwise be laid out
+                // four times, and a short item pays for every line of code it fetches.  (A path for
+                // two plain chunks beside it made steps with a bias slower: 67 -> 73 us for prompts
+                // of 200-800 tokens among single ones.)
+                constexpr bool plain = !BIAS;
+                uint32_t sr[2][32];
+                if (plain) {
                     tmem_ld32(tS, sr[0]);
-                    tmem_ld32(tS + 32u, sr[kLive - 1]);
+                    tmem_ld32(tS + 32u, sr[1]);
                 }
+                auto mask = [&](uint32_t (&r)[32], int kk) {
+                    const int lk = lim - 32 * kk, lok = lo - 32 * kk;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = (e >= lok && e < lk) ? r[e] : __float_as_uint(-INFINITY);
+                };
                 // in place: scaled, biased and masked scores of chunk k, minus `shift`
                 auto to_x = [&](uint32_t (&r)[32], int k, float shift) {
                     const int kk = 2 * hf + k;
-                    if (!BIAS || (hmask & (1u << k))) {
+                    if (hmask & (1u << k)) {
                         const float c1k = k ? cb[1] : cb[0];
                         const float2 sc = make_float2(xs, xs), add = make_float2(c1k - shift, c1k - shift);
 #pragma unroll
@@ -612,34 +619,12 @@ __global__ void __launch_bounds__(608, 1)
                             }
                         }
                     }
-                    if (!full) {
-                        const int lk = lim - 32 * kk, lok = lo - 32 * kk;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = (e >= lok && e < lk) ? r[e] : __float_as_uint(-INFINITY);
-                    }
+                    if (!full) mask(r, kk);
                 };
-                if (!BIAS) {
-                    tmem_ld_wait(sr[0]);
-                    tmem_ld_wait(sr[kLive - 1]);
-                }
-                // pass 1: this half's row maximum, from the raw scores where the bias is one value
-                float mx = -INFINITY;
-#pragma unroll kLive
-                for (int k = 0; k < 2; ++k) {
-                    const int kk = 2 * hf + k;
-                    uint32_t(&r)[32] = sr[BIAS ? 0 : k];
-                    if (BIAS) {
-                        tmem_ld32(tS + 32u * k, r);
-                        tmem_ld_wait(r);
-                    }
+                // raw scores' maximum, of those the row sees
+                auto raw_max = [&](const uint32_t (&r)[32], int kk) {
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    const bool vary = BIAS && !(hmask & (1u << k));
-                    if (vary) {
-                        to_x(r, k, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-                    } else if (full) {
+                    if (full) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
                             m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
@@ -649,8 +634,29 @@ __global__ void __launch_bounds__(608, 1)
                         for (int e = 0; e < 32; ++e)
                             m4[e & 3] = fmaxf(m4[e & 3], (e >= lok && e < lk) ? __uint_as_float(r[e]) : -INFINITY);
                     }
-                    const float mk = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    mx = fmaxf(mx, vary ? mk : fmaf(mk, xs, (k ? cb[1] : cb[0])));
+                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                };
+                // pass 1: this half's row maximum, from the raw scores where the bias is one value
+                float mx = -INFINITY;
+                if (plain) {
+                    tmem_ld_wait(sr[0]);
+                    tmem_ld_wait(sr[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) mx = fmaxf(mx, fmaf(raw_max(sr[k], 2 * hf + k), xs, cb[k]));
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t(&r)[32] = sr[0];
+                        tmem_ld32(tS + 32u * k, r);
+                        tmem_ld_wait(r);
+                        if (hmask & (1u << k)) {
+                            mx = fmaxf(mx, fmaf(raw_max(r, 2 * hf + k), xs, (k ? cb[1] : cb[0])));
+                        } else {
+                            to_x(r, k, 0.f);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                        }
+                    }
                 }
                 float mo;
                 if (!exchange(mx, mo)) { ok = false; break; }
@@ -675,41 +681,41 @@ __global__ void __launch_bounds__(608, 1)
                 }
                 // pass 2: P = exp2(x - m), its sum in fp32, and bf16 P over the scores
                 float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                if (!BIAS) {
-                    tmem_ld32(tS, sr[0]);  // the raw scores again: cheaper than 64 live registers
-                    tmem_ld32(tS + 32u, sr[kLive - 1]);
-                    tmem_ld_wait(sr[0]);
-                    tmem_ld_wait(sr[kLive - 1]);
-                }
-#pragma unroll kLive
-                for (int k = 0; k < 2; ++k) {
-                    const int kk = 2 * hf + k;
-                    uint32_t(&r)[32] = sr[BIAS ? 0 : k];
-                    const float cbk = k ? cb[1] : cb[0];
-                    if (BIAS) {
-                        tmem_ld32(tS + 32u * k, r);
-                        tmem_ld_wait(r);
-                    }
+                auto exps = [&](const uint32_t (&r)[32], int kk) {
                     uint32_t pk[16];
-                    if (full && (!BIAS || (hmask & (1u << k)))) {
-                        const float2 xs2 = make_float2(xs, xs), add = make_float2(cbk - m_use, cbk - m_use);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 t2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), xs2, add);
-                            const float2 e2 = make_float2(ex2_approx(t2.x), ex2_approx(t2.y));
-                            rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], e2);
-                            pk[e >> 1] = pack_bf16x2(e2.x, e2.y);
-                        }
-                    } else {
-                        to_x(r, k, m_use);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 e2 = make_float2(ex2_approx(__uint_as_float(r[e])), ex2_approx(__uint_as_float(r[e + 1])));
-                            rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], e2);
-                            pk[e >> 1] = pack_bf16x2(e2.x, e2.y);
-                        }
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 e2 = make_float2(ex2_approx(__uint_as_float(r[e])), ex2_approx(__uint_as_float(r[e + 1])));
+                        rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], e2);
+                        pk[e >> 1] = pack_bf16x2(e2.x, e2.y);
                     }
                     tmem_st16(tSt + 32u * kk, pk);
+                };
+                if (plain) {
+                    tmem_ld32(tS, sr[0]);  // the raw scores again: cheaper than 64 live registers
+                    tmem_ld32(tS + 32u, sr[1]);
+                    tmem_ld_wait(sr[0]);
+                    tmem_ld_wait(sr[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 xs2 = make_float2(xs, xs), add = make_float2(cb[k] - m_use, cb[k] - m_use);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 t2 = fma2(make_float2(__uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1])), xs2, add);
+                            sr[k][e] = __float_as_uint(t2.x);
+                            sr[k][e + 1] = __float_as_uint(t2.y);
+                        }
+                        if (!full) mask(sr[k], 2 * hf + k);
+                        exps(sr[k], 2 * hf + k);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_ld32(tS + 32u * k, sr[0]);
+                        tmem_ld_wait(sr[0]);
+                        to_x(sr[0], k, m_use);
+                        exps(sr[0], 2 * hf + k);
+                    }
                 }
                 const float2 r01 = add2(rs[0], rs[1]);
                 l = l * alpha + (r01.x + r01.y);
