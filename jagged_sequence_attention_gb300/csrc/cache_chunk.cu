@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(608, 1)
                 st = cache_find_unit<C::BN>(p, *groups, ng, u, lane);
                 st.u_end = min(groups->total, u + blk);
             }
-            CacheCursor<C::BN> cur(st, groups->order);
+            CacheCursor<C::BN> cur(p, st, groups->order);
             while (ok && cur.next(p, g)) {
                 SegRec r{g.b, g.hk, g.tile, g.k0, g.k1, g.s.q0, g.s.q_len, g.s.kv_len, 0, 0, 0, 0};
                 if (w >= whole) {

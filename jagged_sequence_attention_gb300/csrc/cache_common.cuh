@@ -188,6 +188,7 @@ struct CacheStart {
     int b, hk, tile, kt;
     int u, u_end;       // this CTA's units [u, u_end)
     int base, rem;      // units per CTA, the first `rem` CTAs one more
+    CacheSeq s;         // sequence b
 };
 
 // The item of the `left`-th unit of the sequences that a warp's lanes hold (s: a lane's
@@ -201,6 +202,7 @@ __device__ __forceinline__ void cache_locate(const CacheFwdParams& p, int c, con
     const int per = __shfl_sync(0xffffffffu, one, l);
     const CacheSeq q{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
                      __shfl_sync(0xffffffffu, s.kv_len, l)};
+    st.s = q;
     st.b = 32 * c + l;
     st.hk = int(uint32_t(left) / uint32_t(per));
     left -= st.hk * per;
@@ -230,7 +232,7 @@ __device__ __forceinline__ void cache_cut(const CacheFwdParams& p, int total, Ca
     }
     const int want = int((uint32_t(total) + uint32_t(p.min_units) - 1u) / uint32_t(p.min_units));
     const int G = min(int(gridDim.x), max(want, 1)), cta = blockIdx.x;
-    st = CacheStart{0, 0, 0, 0, 0, 0, 0, 0};
+    st = CacheStart{};
     if (cta < G && total > 0) {
         st.base = int(uint32_t(total) / uint32_t(G));
         st.rem = total - st.base * G;
@@ -306,8 +308,8 @@ struct CacheCursor {
     CacheSeq s;
     int nt;
     const uint8_t* order;
-    __device__ explicit CacheCursor(const CacheStart& start, const uint8_t* ord = nullptr)
-        : st(start), s{0, 0, 0}, nt(-1), order(ord) {}
+    __device__ CacheCursor(const CacheFwdParams& p, const CacheStart& start, const uint8_t* ord = nullptr)
+        : st(start), s(start.s), nt(cache_tiles(p, start.s)), order(ord) {}  // (nt = 0: an empty range)
     __device__ bool next(const CacheFwdParams& p, CacheSeg& g) {
         while (st.u < st.u_end) {
             while (nt <= 0) {
@@ -389,7 +391,8 @@ __device__ __forceinline__ int cache_find_group(const int* before, int groups, i
 template <int BN>
 __device__ __forceinline__ CacheStart cache_find_unit(const CacheFwdParams& p, const CacheGroups& G, int groups, int u,
                                                       int lane) {
-    CacheStart st{0, 0, 0, 0, u, u, 0, 0};
+    CacheStart st{};
+    st.u = st.u_end = u;
     const int c = cache_find_group(G.units, groups, u, lane);
     const CacheSeq s = cache_lane_seq(p, c, lane, false, G.order);
     cache_locate<BN>(p, c, s, cache_seq_units<BN>(p, s, lane), u - G.units[c], lane, st);
@@ -399,14 +402,17 @@ __device__ __forceinline__ CacheStart cache_find_unit(const CacheFwdParams& p, c
 // Item i of the batch, by a whole warp.
 __device__ __forceinline__ CacheStart cache_find_item(const CacheFwdParams& p, const CacheGroups& G, int groups, int i,
                                                       int lane) {
-    CacheStart st{0, 0, 0, 0, 0, 0, 0, 0};
+    CacheStart st{};
     const int c = cache_find_group(G.items, groups, i, lane);
-    const int tiles = cache_tiles(p, cache_lane_seq(p, c, lane, false, G.order));
+    const CacheSeq s = cache_lane_seq(p, c, lane, false, G.order);
+    const int tiles = cache_tiles(p, s);
     const int inc = warp_scan(tiles * p.Hkv, lane);
     int left = i - G.items[c];
     const int l = __ffs(__ballot_sync(0xffffffffu, inc > left)) - 1;
     left -= __shfl_sync(0xffffffffu, inc - tiles * p.Hkv, l);
     const int nt = __shfl_sync(0xffffffffu, tiles, l);
+    st.s = CacheSeq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
+                    __shfl_sync(0xffffffffu, s.kv_len, l)};
     st.b = 32 * c + l;
     st.hk = int(uint32_t(left) / uint32_t(nt));
     st.tile = left - st.hk * nt;

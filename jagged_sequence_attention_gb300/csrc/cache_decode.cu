@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         tma_prefetch_desc(&tmV);
     }
     CacheStart* start = reinterpret_cast<CacheStart*>(smem + C::kOffMisc + 16);
-    CacheCursor<BN> cur(cache_start<BN>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
+    CacheCursor<BN> cur(p, cache_start<BN>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
     if (threadIdx.x == 0) *start = cur.st;
     __syncthreads();
     CacheSeg g;

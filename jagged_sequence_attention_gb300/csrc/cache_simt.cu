@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtCtasPerSm) jfa_cache_simt_k
     float* sP = sm + C::kP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const CacheStart start = cache_start<BN>(p, reinterpret_cast<int*>(sm));
-    CacheCursor<BN> cur(start);
+    CacheCursor<BN> cur(p, start);
     CacheSeg g;
     const int page_mask = (1 << p.page_log2) - 1;
     while (cur.next(p, g)) {

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
-    CacheCursor<kSpBN> cur(cache_start<kSpBN>(p, reinterpret_cast<int*>(smem + C::kOffSums)));
+    CacheCursor<kSpBN> cur(p, cache_start<kSpBN>(p, reinterpret_cast<int*>(smem + C::kOffSums)));
     const CacheStart start = cur.st;
     tc_fence_before();
     __syncthreads();
