@@ -29,7 +29,7 @@ struct DecCfg {
     static constexpr int kBlock = BN * 128;                  // one column block of a stage's keys
     static constexpr int kStage = 2 * kCB * kBlock;          // K blocks, then V blocks
     static constexpr int kStages = 98304 / kStage;
-    static constexpr int kOffSlots = kStages * kStage;       // two 16 x 64 fp32 tiles of the merge
+    static constexpr int kOffSlots = kStages * kStage;       // two tiles of 8 fp32 rows of the merge (8 KB kept)
     static constexpr int kOffML = kOffSlots + 2 * 16 * 64 * 4;   // [2 buffers][m, l][warp][row]
     static constexpr int kOffBias = kOffML + 2 * 2 * kDecWarps * 16 * 4;  // [row][32 buckets + 1], log2 units
     static constexpr int kOffBar = kOffBias + 16 * 33 * 4;
@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             if (lane == 0) mbar_arrive(empty(st));
         }
         // ------------------------------------------------------------ end of the item's part
-        // Merge the four warps: m and l of every row, then O, 64 columns at a time, warps 2
-        // and 3 into the slots, warps 0 and 1 onto them, and the two slots' sum out.
+        // Merge the four warps: m and l of every row, then O, 8 rows at a time (most items have
+        // no more), warps 2 and 3 into the slots, warps 0 and 1 onto them, and the two slots'
+        // sum out.
         float* mw = ml + (seg_no & 1) * (2 * kDecWarps * 16);
         float* lw = mw + kDecWarps * 16;
         ++seg_no;
@@ -346,16 +347,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             const float mm = fmaxf(fmaxf(mw[r], mw[16 + r]), fmaxf(mw[32 + r], mw[48 + r]));
             f[i] = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - mm);
         }
-        // this thread's output: row orow, columns 8 (tid & 7) + of each 64
-        const int orow = threadIdx.x >> 3, ocol = threadIdx.x & 7;
-        float om = -INFINITY, ol = 0.f;
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) om = fmaxf(om, mw[16 * w + orow]);
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-            const float mm = mw[16 * w + orow];
-            ol = fmaf(mm == -INFINITY ? 0.f : ex2_approx(mm - om), lw[16 * w + orow], ol);
-        }
         const bool whole = g.whole();
         int first = 0, last = 0;
         if (!whole) {
@@ -363,67 +354,73 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             last = cache_last_cta(p, *start, g);
         }
         float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
-        const int r = r0 + orow, tok = div_g(p, r);
-        const size_t grow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
-        const bool out = orow < nr && ok;
-        const float inv = ol > 0.f ? 1.f / ol : 0.f;
-        auto put = [&](int col, const float (&v)[8], float mul) {
-            if (p.o_f32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + grow * D + col);
-                dst[0] = make_float4(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul);
-                dst[1] = make_float4(v[4] * mul, v[5] * mul, v[6] * mul, v[7] * mul);
-            } else {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + grow * D + col) =
-                    make_uint4(pack_bf16x2(v[0] * mul, v[1] * mul), pack_bf16x2(v[2] * mul, v[3] * mul),
-                               pack_bf16x2(v[4] * mul, v[5] * mul), pack_bf16x2(v[6] * mul, v[7] * mul));
-            }
-        };
-#pragma unroll
-        for (int hc = 0; hc < D / 64; ++hc) {
-            float2* slot = reinterpret_cast<float2*>(slots) + (warp & 1) * 512 + lane;  // [8 n][2 halves][32 lanes]
+        constexpr int CW = D / 16;  // columns of a thread: 16 threads a row
+        const int ocol = CW * (threadIdx.x & 15);
+        float2* slot = reinterpret_cast<float2*>(slots) + (warp & 1) * (4 * D) + lane;  // [D / 8][8 rows][4]
+#pragma unroll 1
+        for (int h = 0; 8 * h < nr; ++h) {
+            if (h) consumer_sync();
+            const float fh = h ? f[1] : f[0];
             if (warp >= 2) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float* v = o[8 * hc + n];
-                    slot[n * 64] = make_float2(v[0] * f[0], v[1] * f[0]);
-                    slot[n * 64 + 32] = make_float2(v[2] * f[1], v[3] * f[1]);
-                }
+                for (int n = 0; n < NT; ++n)
+                    slot[n * 32] = make_float2((h ? o[n][2] : o[n][0]) * fh, (h ? o[n][3] : o[n][1]) * fh);
             }
             consumer_sync();
             if (warp < 2) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float* v = o[8 * hc + n];
-                    const float2 x = slot[n * 64], y = slot[n * 64 + 32];
-                    slot[n * 64] = make_float2(fmaf(v[0], f[0], x.x), fmaf(v[1], f[0], x.y));
-                    slot[n * 64 + 32] = make_float2(fmaf(v[2], f[1], y.x), fmaf(v[3], f[1], y.y));
+                for (int n = 0; n < NT; ++n) {
+                    const float2 x = slot[n * 32];
+                    slot[n * 32] = make_float2(fmaf(h ? o[n][2] : o[n][0], fh, x.x), fmaf(h ? o[n][3] : o[n][1], fh, x.y));
                 }
+            }
+            // this thread's row: its maximum and sum
+            const int orow = 8 * h + (threadIdx.x >> 4);
+            float om = -INFINITY, ol = 0.f;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) om = fmaxf(om, mw[16 * w + orow]);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+                const float mm = mw[16 * w + orow];
+                ol = fmaf(mm == -INFINITY ? 0.f : ex2_approx(mm - om), lw[16 * w + orow], ol);
             }
             consumer_sync();
-            const float4* a = reinterpret_cast<const float4*>(slots) + (ocol * 2 + (orow >> 3)) * 16 + (orow & 7) * 2;
-            const float4 a0 = a[0], a1 = a[1], b0 = a[256], b1 = a[257];
-            const float v[8] = {a0.x + b0.x, a0.y + b0.y, a0.z + b0.z, a0.w + b0.w,
-                                a1.x + b1.x, a1.y + b1.y, a1.z + b1.z, a1.w + b1.w};
-            if (out) {
-                if (whole) {
-                    put(64 * hc + 8 * ocol, v, inv);
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(part + orow * D + 64 * hc + 8 * ocol);
-                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-                }
+            const float* a = slots + (ocol >> 3) * 64 + (orow & 7) * 8 + (ocol & 7);
+            float v[CW];
+#pragma unroll
+            for (int e = 0; e < CW; e += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(a + e), y = *reinterpret_cast<const float4*>(a + 8 * D + e);
+                v[e] = x.x + y.x;
+                v[e + 1] = x.y + y.y;
+                v[e + 2] = x.z + y.z;
+                v[e + 3] = x.w + y.w;
             }
-            if (hc + 1 < D / 64) consumer_sync();
+            if (orow >= nr || !ok) continue;
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < CW; e += 4)
+                    *reinterpret_cast<float4*>(part + orow * D + ocol + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                if (ocol == 0) {
+                    part[BM * D + orow] = om;
+                    part[BM * D + BM + orow] = ol;
+                }
+                continue;
+            }
+            const int r = r0 + orow, tok = div_g(p, r);
+            const size_t grow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(g.hk * p.g + r - tok * p.g);
+            const float inv = ol > 0.f ? 1.f / ol : 0.f;
+#pragma unroll
+            for (int e = 0; e < CW; e += 4) {
+                if (p.o_f32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.O) + grow * D + ocol + e) =
+                        make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + grow * D + ocol + e) =
+                        make_uint2(pack_bf16x2(v[e] * inv, v[e + 1] * inv), pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv));
+            }
+            if (ocol == 0 && p.lse) p.lse[grow] = ol > 0.f ? (om + __log2f(ol)) * 0.6931471805599453f : -INFINITY;
         }
-        if (whole) {
-            if (out && ocol == 0 && p.lse)
-                p.lse[grow] = ol > 0.f ? (om + __log2f(ol)) * 0.6931471805599453f : -INFINITY;
-            continue;
-        }
-        if (out && ocol == 0) {
-            part[BM * D + orow] = om;
-            part[BM * D + BM + orow] = ol;
-        }
+        if (whole) continue;
         __threadfence();
         consumer_sync();
         if (threadIdx.x == 0) {
