@@ -14,12 +14,14 @@
 // the loads bound the kernel, not the products.
 //
 // An item is 128 packed rows of one (sequence, key head); a step is 128 keys.  Head dimension
-// 32 runs as 64 with zeros.  CTA = 13 warps, one CTA per SM:
-//   warps 0-7   softmax: two warps share a row, 64 score columns and 32 output columns each
-//   warps 8-11  split Q (from global memory) and the K and V tiles that TMA left in shared
-//               memory, and write the parts' swizzled tiles
-//   warp 12     tcgen05.mma issuer and TMEM owner
-//   warp 13     TMA loads of K and V, a tile of each ahead (one box per page and 128 bytes of a
+// 32 runs as 64 with zeros.  CTA = 16 warps, one CTA per SM:
+//   warps 0-7    softmax: two warps share a row, 64 score columns and 32 output columns each
+//   warps 8-11   split Q (from global memory) and the V tiles that TMA left in shared memory,
+//                and write the parts' swizzled tiles
+//   warps 12-13  the same for the K tiles: their turn comes a step ahead of V's, and one group
+//                for both would make each wait for the other's product (4.4 us a step)
+//   warp 14      tcgen05.mma issuer and TMEM owner
+//   warp 15      TMA loads of K and V, a tile of each ahead (one box per page and 128 bytes of a
 //               row): 64 KB in flight, which loads through registers would not reach
 // TMEM (512 columns): scores twice [0,128), [128,256), so that a tile's scores form during the
 // previous one's softmax; P's parts [256,448); the tile's output [448,512).
@@ -43,7 +45,8 @@ struct SpCfg {
     static constexpr int kOffXch = kOffMisc + 16;   // pair exchanges [2][2][4][32]
     static constexpr int kOffSums = kOffXch + 2 * 2 * 4 * 32 * 4;  // scratch of the work split
     static constexpr int kBytes = kOffSums + kCacheMaxGroups * 4 + 1024;
-    static constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kTmaWarp = 13, kThreads = 14 * 32;
+    static constexpr int kSoftWarps = 8, kValueWarps = 4, kKeyWarps = 2, kKeyWarp = 12, kMmaWarp = 14, kTmaWarp = 15,
+                         kThreads = 16 * 32;
     static constexpr uint32_t kTmemCols = 512, kP = 256, kO = 448;
     static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, 128, 128, false, false);
     static constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, 128, kSpD, false, true);
@@ -94,19 +97,19 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(P_Q_FULL), C::kLoadWarps);
+        mbar_init(bar(P_Q_FULL), C::kValueWarps);
         mbar_init(bar(P_Q_EMPTY), 1);
-        mbar_init(bar(P_K_FULL), C::kLoadWarps);
+        mbar_init(bar(P_K_FULL), C::kKeyWarps);
         mbar_init(bar(P_K_EMPTY), 1);
-        mbar_init(bar(P_V_FULL), C::kLoadWarps);
+        mbar_init(bar(P_V_FULL), C::kValueWarps);
         mbar_init(bar(P_V_EMPTY), 1);
         mbar_init(bar(P_P_FULL), C::kSoftWarps);
         mbar_init(bar(P_O_DONE), 1);
         mbar_init(bar(P_DRAIN), 1);
         mbar_init(bar(P_KS_FULL), 1);
-        mbar_init(bar(P_KS_EMPTY), C::kLoadWarps);
+        mbar_init(bar(P_KS_EMPTY), C::kKeyWarps);
         mbar_init(bar(P_VS_FULL), 1);
-        mbar_init(bar(P_VS_EMPTY), C::kLoadWarps);
+        mbar_init(bar(P_VS_EMPTY), C::kValueWarps);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         for (int s = 0; s < 2; ++s) {
@@ -240,8 +243,10 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
         drain_ring(bar(P_VS_FULL), v_it, 1);
     } else if (warp >= C::kSoftWarps) {
         // ------------------------------------------------------------ splits
-        const int tid = threadIdx.x - 32 * C::kSoftWarps;
-        const int c = tid & 7, row0 = tid >> 3;  // elements 4 c .. and 32 + 4 c .. of rows row0 + 16 i
+        const bool keys = warp >= C::kKeyWarp;
+        const int tid = threadIdx.x - 32 * (keys ? C::kKeyWarp : C::kSoftWarps);
+        const int step = keys ? 4 * C::kKeyWarps : 4 * C::kValueWarps;
+        const int c = tid & 7, row0 = tid >> 3;  // elements 4 c .. and 32 + 4 c .. of rows row0 + step i
         uint32_t it = 0, item_it = 0;
         // four elements of row r, from column 4 c (+ 32) on, to the parts' tiles at `off`
         auto put4 = [&](int off, int r, int piece, const float4& v) {
@@ -260,54 +265,62 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
             if (lane == 0) mbar_arrive(bar(full));
         };
         // a loaded tile's rows, zeros where no row of the item may look (positions from c0 on)
+        // (four rows' loads at once, ahead of the stores that the compiler keeps them in order with)
         auto convert = [&](int stage, int off, int c0) {
-#pragma unroll 4
-            for (int i = 0; i < 8; ++i) {
-                const int r = row0 + 16 * i, j = c0 + r;
-                const bool in = j >= g.r.lo && j < g.r.hi;
-                const uint32_t at = sbase + uint32_t(stage + r * 128 + ((c ^ (r & 7)) << 4));
+#pragma unroll 1
+            for (int r0 = row0; r0 < 128; r0 += 4 * step) {
+                uint4 u[4][D / 32];
 #pragma unroll
-                for (int h = 0; h < D / 32; ++h) {
-                    const uint4 u = ld_shared_v4(at + uint32_t(h * C::kStageBlock));
-                    float4 v = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
-                    if (!in) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    put4(off, r, c + 8 * h, v);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + i * step;
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h)
+                        u[i][h] = ld_shared_v4(sbase + uint32_t(stage + h * C::kStageBlock + r * 128 + ((c ^ (r & 7)) << 4)));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + i * step, j = c0 + r;
+                    const bool in = j >= g.r.lo && j < g.r.hi;
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h)
+                        put4(off, r, c + 8 * h,
+                             in ? make_float4(__uint_as_float(u[i][h].x), __uint_as_float(u[i][h].y), __uint_as_float(u[i][h].z),
+                                              __uint_as_float(u[i][h].w))
+                                : make_float4(0.f, 0.f, 0.f, 0.f));
                 }
             }
         };
         while (ok && cur.next(p, g)) {
             if (g.r.n == 0) continue;
-            const int R = g.s.q_len * p.g, r0 = g.tile * kSpBM;
-            if (!wwait(P_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+            if (!keys) {
+                const int R = g.s.q_len * p.g, r0 = g.tile * kSpBM;
+                if (!wwait(P_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
 #pragma unroll 4
-            for (int i = 0; i < 8; ++i) {
-                const int r = row0 + 16 * i;
-                float4 v[D / 32];
+                for (int i = 0; i < 8; ++i) {
+                    const int r = row0 + 16 * i;
+                    float4 v[D / 32];
 #pragma unroll
-                for (int h = 0; h < D / 32; ++h) v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r0 + r < R) {
-                    const int tok = div_g(p, r0 + r);
-                    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
-                                                                        int64_t(g.hk * p.g + r0 + r - tok * p.g) * D);
+                    for (int h = 0; h < D / 32; ++h) v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r0 + r < R) {
+                        const int tok = div_g(p, r0 + r);
+                        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
+                                                                            int64_t(g.hk * p.g + r0 + r - tok * p.g) * D);
 #pragma unroll
-                    for (int h = 0; h < D / 32; ++h) v[h] = src[c + 8 * h];
+                        for (int h = 0; h < D / 32; ++h) v[h] = src[c + 8 * h];
+                    }
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h) put4(C::kOffQ, r, c + 8 * h, v[h]);
                 }
-#pragma unroll
-                for (int h = 0; h < D / 32; ++h) put4(C::kOffQ, r, c + 8 * h, v[h]);
+                arrive(P_Q_FULL);
             }
-            arrive(P_Q_FULL);
             ++item_it;
+            const int staged = keys ? P_KS_FULL : P_VS_FULL, full = keys ? P_K_FULL : P_V_FULL;
             for (int k = g.k0; k < g.k1 && ok; ++k, ++it) {
-                const int c0 = (g.r.f + k) * kSpBN;
                 const uint32_t ph = it & 1;
-                if (!wwait(P_KS_FULL, ph) || !wwait(P_K_EMPTY, ph ^ 1)) { ok = false; break; }
-                convert(C::kOffKS, C::kOffK, c0);
-                arrive(P_K_FULL);
-                if (lane == 0) mbar_arrive(bar(P_KS_EMPTY));
-                if (!wwait(P_VS_FULL, ph) || !wwait(P_V_EMPTY, ph ^ 1)) { ok = false; break; }
-                convert(C::kOffVS, C::kOffV, c0);
-                arrive(P_V_FULL);
-                if (lane == 0) mbar_arrive(bar(P_VS_EMPTY));
+                if (!wwait(staged, ph) || !wwait(full + 1, ph ^ 1)) { ok = false; break; }
+                convert(keys ? C::kOffKS : C::kOffVS, keys ? C::kOffK : C::kOffV, (g.r.f + k) * kSpBN);
+                arrive(full);
+                if (lane == 0) mbar_arrive(bar(staged + 1));
             }
         }
         if (!ok && lane == 0) fail();
