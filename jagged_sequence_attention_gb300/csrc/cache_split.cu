@@ -207,40 +207,60 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
         // ------------------------------------------------------------ loads
         const int rows = min(1 << p.page_log2, 64), per = kSpBN / rows;  // keys of a box, boxes of a column block
         const int mask = (1 << p.page_log2) - 1;
-        uint32_t it = 0, v_it = 0;
-        while (ok && cur.next(p, g)) {
-            if (g.r.n == 0) continue;
-            for (int k = g.k0; k < g.k1 && ok; ++k, ++it) {
-                // lane: a page of the tile (two column blocks of it)
-                const int j = (g.r.f + k) * kSpBN + lane * rows;
-                int page = -1;
-                if (lane < per && j < g.r.hi && j + rows > g.r.lo) {
-                    page = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
-                    if (page < 0 || page >= p.n_pages) {
-                        atomicOr(p.status, kStatusBounds);
-                        page = p.n_pages;  // past the cache: read as zeros
-                    }
+        // K and V are loaded in turn, K a step ahead: its tile is split, and its memory free
+        // again, before V's.
+        struct Stream {
+            CacheCursor<kSpBN> cur;
+            CacheSeg g;
+            int k;
+            uint32_t it;
+            bool have;
+        };
+        auto advance = [&](Stream& s) {  // to the next step's key tile
+            if (s.have && ++s.k < s.g.k1) return;
+            do {
+                s.have = s.cur.next(p, s.g);
+            } while (s.have && s.g.r.n == 0);
+            if (s.have) s.k = s.g.k0;
+        };
+        auto issue = [&](Stream& s, int full, int empty, int stage, const CUtensorMap* map) -> bool {
+            // lane: a page of the tile (two column blocks of it)
+            const int j = (s.g.r.f + s.k) * kSpBN + lane * rows;
+            int page = -1;
+            if (lane < per && j < s.g.r.hi && j + rows > s.g.r.lo) {
+                page = p.table[size_t(s.g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                if (page < 0 || page >= p.n_pages) {
+                    atomicOr(p.status, kStatusBounds);
+                    page = p.n_pages;  // past the cache: read as zeros
                 }
-                const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, page >= 0)) * rows * 128 * (D / 32));
-                auto issue = [&](int full, int empty, int stage, const CUtensorMap* map) -> bool {
-                    if (!wwait(empty, (it & 1) ^ 1)) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
-                    __syncwarp();
-                    if (page >= 0)
-#pragma unroll
-                        for (int h = 0; h < D / 32; ++h)
-                            tma_load_4d(sbase + uint32_t(stage + h * C::kStageBlock + lane * rows * 128), map, bar(full), 32 * h,
-                                        j & mask, g.hk, page);
-                    return true;
-                };
-                if (!issue(P_KS_FULL, P_KS_EMPTY, C::kOffKS, &tmK)) { ok = false; break; }
-                if (!issue(P_VS_FULL, P_VS_EMPTY, C::kOffVS, &tmV)) { ok = false; ++it; break; }
-                ++v_it;
             }
+            const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, page >= 0)) * rows * 128 * (D / 32));
+            if (!wwait(empty, (s.it & 1) ^ 1)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+            __syncwarp();
+            if (page >= 0)
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h)
+                    tma_load_4d(sbase + uint32_t(stage + h * C::kStageBlock + lane * rows * 128), map, bar(full), 32 * h, j & mask,
+                                s.g.hk, page);
+            ++s.it;
+            return true;
+        };
+        Stream ks{cur, g, 0, 0, false}, vs{cur, g, 0, 0, false};
+        advance(ks);
+        advance(vs);
+        for (bool first = true; vs.have && ok; first = false) {
+            if (ks.have) {
+                ok = issue(ks, P_KS_FULL, P_KS_EMPTY, C::kOffKS, &tmK);
+                advance(ks);
+                if (first) continue;
+            }
+            if (ok) ok = issue(vs, P_VS_FULL, P_VS_EMPTY, C::kOffVS, &tmV);
+            advance(vs);
         }
         if (!ok && lane == 0) fail();
-        drain_ring(bar(P_KS_FULL), it, 1);
-        drain_ring(bar(P_VS_FULL), v_it, 1);
+        drain_ring(bar(P_KS_FULL), ks.it, 1);
+        drain_ring(bar(P_VS_FULL), vs.it, 1);
     } else if (warp >= C::kSoftWarps) {
         // ------------------------------------------------------------ splits
         const bool keys = warp >= C::kKeyWarp;
