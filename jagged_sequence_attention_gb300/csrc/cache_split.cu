@@ -16,10 +16,10 @@
 // An item is 128 packed rows of one (sequence, key head); a step is 128 keys.  Head dimension
 // 32 runs as 64 with zeros.  CTA = 16 warps, one CTA per SM:
 //   warps 0-7    softmax: two warps share a row, 64 score columns and 32 output columns each
-//   warps 8-11   split Q (from global memory) and the V tiles that TMA left in shared memory,
-//                and write the parts' swizzled tiles
-//   warps 12-13  the same for the K tiles: their turn comes a step ahead of V's, and one group
-//                for both would make each wait for the other's product (4.4 us a step)
+//   warps 8-13   split Q (from global memory) and the K and V tiles that TMA left in shared
+//                memory, and write the parts' swizzled tiles; K a step ahead of V, since each
+//                step's K parts wait for the step before's scores and its V parts for the
+//                step before's output (in the order of the steps: 4.4 us a step)
 //   warp 14      tcgen05.mma issuer and TMEM owner
 //   warp 15      TMA loads of K and V, a tile of each ahead (one box per page and 128 bytes of a
 //               row): 64 KB in flight, which loads through registers would not reach
@@ -45,7 +45,7 @@ struct SpCfg {
     static constexpr int kOffXch = kOffMisc + 16;   // pair exchanges [2][2][4][32]
     static constexpr int kOffSums = kOffXch + 2 * 2 * 4 * 32 * 4;  // scratch of the work split
     static constexpr int kBytes = kOffSums + kCacheMaxGroups * 4 + 1024;
-    static constexpr int kSoftWarps = 8, kValueWarps = 4, kKeyWarps = 2, kKeyWarp = 12, kMmaWarp = 14, kTmaWarp = 15,
+    static constexpr int kSoftWarps = 8, kSplitWarps = 6, kMmaWarp = 14, kTmaWarp = 15,
                          kThreads = 16 * 32;
     static constexpr uint32_t kTmemCols = 512, kP = 256, kO = 448;
     static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, 128, 128, false, false);
@@ -83,6 +83,25 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& p0, uint32_t&
     p2 = pack_bf16x2(rx - __uint_as_float(p1 << 16), ry - __uint_as_float(p1 & 0xffff0000u));
 }
 
+// The steps of a CTA's range, one key tile after the other.
+struct SplitStream {
+    CacheCursor<kSpBN> cur;
+    CacheSeg g;
+    int k;         // the step's key tile of its item
+    uint32_t it;   // steps and items begun before it
+    uint32_t item;
+    bool have;
+    __device__ explicit SplitStream(const CacheCursor<kSpBN>& c) : cur(c), k(0), it(0), item(0), have(false) {}
+    __device__ void advance(const CacheFwdParams& p) {  // to the next step; its number is counted by the caller
+        if (have && ++k < g.k1) return;
+        if (have) ++item;
+        do {
+            have = cur.next(p, g);
+        } while (have && g.r.n == 0);
+        if (have) k = g.k0;
+    }
+};
+
 template <int D, bool BIAS>
 __global__ void __launch_bounds__(SpCfg::kThreads, 1)
     jfa_cache_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -97,19 +116,19 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(P_Q_FULL), C::kValueWarps);
+        mbar_init(bar(P_Q_FULL), C::kSplitWarps);
         mbar_init(bar(P_Q_EMPTY), 1);
-        mbar_init(bar(P_K_FULL), C::kKeyWarps);
+        mbar_init(bar(P_K_FULL), C::kSplitWarps);
         mbar_init(bar(P_K_EMPTY), 1);
-        mbar_init(bar(P_V_FULL), C::kValueWarps);
+        mbar_init(bar(P_V_FULL), C::kSplitWarps);
         mbar_init(bar(P_V_EMPTY), 1);
         mbar_init(bar(P_P_FULL), C::kSoftWarps);
         mbar_init(bar(P_O_DONE), 1);
         mbar_init(bar(P_DRAIN), 1);
         mbar_init(bar(P_KS_FULL), 1);
-        mbar_init(bar(P_KS_EMPTY), C::kKeyWarps);
+        mbar_init(bar(P_KS_EMPTY), C::kSplitWarps);
         mbar_init(bar(P_VS_FULL), 1);
-        mbar_init(bar(P_VS_EMPTY), C::kValueWarps);
+        mbar_init(bar(P_VS_EMPTY), C::kSplitWarps);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         for (int s = 0; s < 2; ++s) {
@@ -209,21 +228,7 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
         const int mask = (1 << p.page_log2) - 1;
         // K and V are loaded in turn, K a step ahead: its tile is split, and its memory free
         // again, before V's.
-        struct Stream {
-            CacheCursor<kSpBN> cur;
-            CacheSeg g;
-            int k;
-            uint32_t it;
-            bool have;
-        };
-        auto advance = [&](Stream& s) {  // to the next step's key tile
-            if (s.have && ++s.k < s.g.k1) return;
-            do {
-                s.have = s.cur.next(p, s.g);
-            } while (s.have && s.g.r.n == 0);
-            if (s.have) s.k = s.g.k0;
-        };
-        auto issue = [&](Stream& s, int full, int empty, int stage, const CUtensorMap* map) -> bool {
+        auto issue = [&](SplitStream& s, int full, int empty, int stage, const CUtensorMap* map) -> bool {
             // lane: a page of the tile (two column blocks of it)
             const int j = (s.g.r.f + s.k) * kSpBN + lane * rows;
             int page = -1;
@@ -246,28 +251,26 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
             ++s.it;
             return true;
         };
-        Stream ks{cur, g, 0, 0, false}, vs{cur, g, 0, 0, false};
-        advance(ks);
-        advance(vs);
+        SplitStream ks{cur}, vs{cur};
+        ks.advance(p);
+        vs.advance(p);
         for (bool first = true; vs.have && ok; first = false) {
             if (ks.have) {
                 ok = issue(ks, P_KS_FULL, P_KS_EMPTY, C::kOffKS, &tmK);
-                advance(ks);
+                ks.advance(p);
                 if (first) continue;
             }
             if (ok) ok = issue(vs, P_VS_FULL, P_VS_EMPTY, C::kOffVS, &tmV);
-            advance(vs);
+            vs.advance(p);
         }
         if (!ok && lane == 0) fail();
         drain_ring(bar(P_KS_FULL), ks.it, 1);
         drain_ring(bar(P_VS_FULL), vs.it, 1);
     } else if (warp >= C::kSoftWarps) {
         // ------------------------------------------------------------ splits
-        const bool keys = warp >= C::kKeyWarp;
-        const int tid = threadIdx.x - 32 * (keys ? C::kKeyWarp : C::kSoftWarps);
-        const int step = keys ? 4 * C::kKeyWarps : 4 * C::kValueWarps;
-        const int c = tid & 7, row0 = tid >> 3;  // elements 4 c .. and 32 + 4 c .. of rows row0 + step i
-        uint32_t it = 0, item_it = 0;
+        const int tid = threadIdx.x - 32 * C::kSoftWarps;
+        constexpr int kStep = 4 * C::kSplitWarps;
+        const int c = tid & 7, row0 = tid >> 3;  // elements 4 c .. and 32 + 4 c .. of rows row0 + kStep i
         // four elements of row r, from column 4 c (+ 32) on, to the parts' tiles at `off`
         auto put4 = [&](int off, int r, int piece, const float4& v) {
             uint32_t w[3][2];
@@ -285,22 +288,24 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
             if (lane == 0) mbar_arrive(bar(full));
         };
         // a loaded tile's rows, zeros where no row of the item may look (positions from c0 on)
-        // (four rows' loads at once, ahead of the stores that the compiler keeps them in order with)
-        auto convert = [&](int stage, int off, int c0) {
+        // (three rows' loads at once, ahead of the stores that the compiler keeps them in order with)
+        auto convert = [&](const SplitStream& s, int stage, int off) {
+            const int c0 = (s.g.r.f + s.k) * kSpBN;
 #pragma unroll 1
-            for (int r0 = row0; r0 < 128; r0 += 4 * step) {
-                uint4 u[4][D / 32];
+            for (int r0 = row0; r0 < 128; r0 += 3 * kStep) {
+                uint4 u[3][D / 32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + i * step;
+                for (int i = 0; i < 3; ++i) {
+                    const int r = min(r0 + i * kStep, 127);
 #pragma unroll
                     for (int h = 0; h < D / 32; ++h)
                         u[i][h] = ld_shared_v4(sbase + uint32_t(stage + h * C::kStageBlock + r * 128 + ((c ^ (r & 7)) << 4)));
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + i * step, j = c0 + r;
-                    const bool in = j >= g.r.lo && j < g.r.hi;
+                for (int i = 0; i < 3; ++i) {
+                    const int r = r0 + i * kStep, j = c0 + r;
+                    if (r >= 128) break;
+                    const bool in = j >= s.g.r.lo && j < s.g.r.hi;
 #pragma unroll
                     for (int h = 0; h < D / 32; ++h)
                         put4(off, r, c + 8 * h,
@@ -310,38 +315,49 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
                 }
             }
         };
-        while (ok && cur.next(p, g)) {
-            if (g.r.n == 0) continue;
-            if (!keys) {
-                const int R = g.s.q_len * p.g, r0 = g.tile * kSpBM;
-                if (!wwait(P_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
-#pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                    const int r = row0 + 16 * i;
-                    float4 v[D / 32];
+        auto split_tile = [&](SplitStream& s, int staged, int full, int stage, int off) {
+            const uint32_t ph = s.it & 1;
+            if (!wwait(staged, ph) || !wwait(full + 1, ph ^ 1)) return false;
+            convert(s, stage, off);
+            arrive(full);
+            if (lane == 0) mbar_arrive(bar(staged + 1));
+            ++s.it;
+            s.advance(p);
+            return true;
+        };
+        auto split_q = [&](const SplitStream& s) {
+            const int R = s.g.s.q_len * p.g, r0 = s.g.tile * kSpBM;
+            if (!wwait(P_Q_EMPTY, (s.item & 1) ^ 1)) return false;
+#pragma unroll 3
+            for (int r = row0; r < 128; r += kStep) {
+                float4 v[D / 32];
 #pragma unroll
-                    for (int h = 0; h < D / 32; ++h) v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (r0 + r < R) {
-                        const int tok = div_g(p, r0 + r);
-                        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (g.s.q0 + tok) * p.q_stride +
-                                                                            int64_t(g.hk * p.g + r0 + r - tok * p.g) * D);
+                for (int h = 0; h < D / 32; ++h) v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r0 + r < R) {
+                    const int tok = div_g(p, r0 + r);
+                    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.Q) + (s.g.s.q0 + tok) * p.q_stride +
+                                                                        int64_t(s.g.hk * p.g + r0 + r - tok * p.g) * D);
 #pragma unroll
-                        for (int h = 0; h < D / 32; ++h) v[h] = src[c + 8 * h];
-                    }
-#pragma unroll
-                    for (int h = 0; h < D / 32; ++h) put4(C::kOffQ, r, c + 8 * h, v[h]);
+                    for (int h = 0; h < D / 32; ++h) v[h] = src[c + 8 * h];
                 }
-                arrive(P_Q_FULL);
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) put4(C::kOffQ, r, c + 8 * h, v[h]);
             }
-            ++item_it;
-            const int staged = keys ? P_KS_FULL : P_VS_FULL, full = keys ? P_K_FULL : P_V_FULL;
-            for (int k = g.k0; k < g.k1 && ok; ++k, ++it) {
-                const uint32_t ph = it & 1;
-                if (!wwait(staged, ph) || !wwait(full + 1, ph ^ 1)) { ok = false; break; }
-                convert(keys ? C::kOffKS : C::kOffVS, keys ? C::kOffK : C::kOffV, (g.r.f + k) * kSpBN);
-                arrive(full);
-                if (lane == 0) mbar_arrive(bar(staged + 1));
+            arrive(P_Q_FULL);
+            return true;
+        };
+        SplitStream ks(cur), vs(cur);
+        ks.advance(p);
+        vs.advance(p);
+        if (vs.have) ok = split_q(vs);
+        for (bool first = true; vs.have && ok; first = false) {
+            if (ks.have) {
+                ok = split_tile(ks, P_KS_FULL, P_K_FULL, C::kOffKS, C::kOffK);
+                if (first) continue;
             }
+            const uint32_t item = vs.item;
+            if (ok) ok = split_tile(vs, P_VS_FULL, P_V_FULL, C::kOffVS, C::kOffV);
+            if (ok && vs.have && vs.item != item) ok = split_q(vs);
         }
         if (!ok && lane == 0) fail();
     } else {
