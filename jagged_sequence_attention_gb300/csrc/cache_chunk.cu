@@ -861,59 +861,72 @@ __global__ void __launch_bounds__(608, 1)
 // in a block and goes on past it; its flag says whether there is one.  The grid is small and a
 // CTA looks at the flags of all its tasks at once, clearing them for the next call: most calls
 // cut few items, and a CTA for each possible task would cost 10 us to find nothing to do.
-// A thread takes one row and a quarter of the columns; a warp's loads are whole lines, since
-// parts are stored four columns of all rows at a time.
+// A thread takes one row and a quarter of the columns, some parts at a time against a running
+// maximum; a warp's loads are whole lines, since parts are stored four columns of all rows at a
+// time.
+constexpr int kMergeThreads = 256;
 template <int D>
-__device__ __forceinline__ void merge_rows(const CacheFwdParams& p, const CacheCut& cut, int row, int quarter) {
-    constexpr int kPart = cache_merge_part(D);
+__device__ __forceinline__ void merge_rows(const CacheFwdParams& p, const CacheCut& cut, int row, int group) {
+    constexpr int kPart = cache_merge_part(D), NV = D / 16, kAtOnce = D == 128 ? 2 : 4;  // NV: float4s of a thread
     if (row >= cut.rows) return;
-    const int first = cut.first, last = cut.last;
-    const float* pm = p.part + kMergeRows * D + row;
-    float mm = -INFINITY;
-#pragma unroll 8
-    for (int c = first; c <= last; ++c) mm = fmaxf(mm, pm[size_t(cache_slot(c, first)) * kPart]);
-    constexpr int NV = D / 16;  // float4s of a thread
-    float ll = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 v[NV];
 #pragma unroll
     for (int e = 0; e < NV; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = first; c <= last; ++c) {
-        const float* q = p.part + size_t(cache_slot(c, first)) * kPart;
-        const float mc = q[kMergeRows * D + row], lc = q[kMergeRows * D + kMergeRows + row];
-        const float w = mc == -INFINITY ? 0.f : ex2_approx(mc - mm);
-        const float4* q4 = reinterpret_cast<const float4*>(q) + quarter * NV * kMergeRows + row;
-        ll = fmaf(lc, w, ll);
+    for (int c = cut.first; c <= cut.last; c += kAtOnce) {
+        float mc[kAtOnce], lc[kAtOnce], top = m;
+        float4 u[kAtOnce][NV];
 #pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            float4 u = q4[e * kMergeRows];
-            if (mc == -INFINITY) u = make_float4(0.f, 0.f, 0.f, 0.f);  // no key of this part: its O is not set
-            v[e].x = fmaf(u.x, w, v[e].x);
-            v[e].y = fmaf(u.y, w, v[e].y);
-            v[e].z = fmaf(u.z, w, v[e].z);
-            v[e].w = fmaf(u.w, w, v[e].w);
+        for (int k = 0; k < kAtOnce; ++k) {
+            mc[k] = -INFINITY;
+            if (c + k > cut.last) continue;
+            const float* q = p.part + size_t(cache_slot(c + k, cut.first)) * kPart;
+            const float4* q4 = reinterpret_cast<const float4*>(q) + group * NV * kMergeRows + row;
+            mc[k] = q[kMergeRows * D + row];
+            lc[k] = q[kMergeRows * D + kMergeRows + row];
+#pragma unroll
+            for (int e = 0; e < NV; ++e) u[k][e] = q4[e * kMergeRows];
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, mc[k]);
+        if (top == -INFINITY) continue;
+        const float keep = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) v[e] = make_float4(v[e].x * keep, v[e].y * keep, v[e].z * keep, v[e].w * keep);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (mc[k] == -INFINITY) continue;  // no key of this part (or no part): its O is not set
+            const float w = ex2_approx(mc[k] - top);
+            l = fmaf(lc[k], w, l);
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                v[e].x = fmaf(u[k][e].x, w, v[e].x);
+                v[e].y = fmaf(u[k][e].y, w, v[e].y);
+                v[e].z = fmaf(u[k][e].z, w, v[e].z);
+                v[e].w = fmaf(u[k][e].w, w, v[e].w);
+            }
         }
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
     const int r = cut.row0 + row, tok = div_g(p, r);
     const size_t orow = size_t(cut.q0 + tok) * size_t(p.H) + size_t(cut.head0 + r - tok * p.g);
-    if (p.o_f32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + quarter * (D / 4));
 #pragma unroll
-        for (int e = 0; e < NV; ++e) dst[e] = make_float4(v[e].x * inv, v[e].y * inv, v[e].z * inv, v[e].w * inv);
-    } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + orow * D + quarter * (D / 4));
-#pragma unroll
-        for (int e = 0; e < NV; e += 2)
-            dst[e / 2] = make_uint4(pack_bf16x2(v[e].x * inv, v[e].y * inv), pack_bf16x2(v[e].z * inv, v[e].w * inv),
-                                    pack_bf16x2(v[e + 1].x * inv, v[e + 1].y * inv),
-                                    pack_bf16x2(v[e + 1].z * inv, v[e + 1].w * inv));
+    for (int e = 0; e < NV; ++e) {
+        const size_t at = orow * D + group * (D / 4) + 4 * e;
+        if (p.o_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) =
+                make_float4(v[e].x * inv, v[e].y * inv, v[e].z * inv, v[e].w * inv);
+        else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + at) =
+                make_uint2(pack_bf16x2(v[e].x * inv, v[e].y * inv), pack_bf16x2(v[e].z * inv, v[e].w * inv));
     }
-    if (p.lse && quarter == 0) p.lse[orow] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && group == 0) p.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) jfa_cache_merge_kernel(const CacheFwdParams p, int tasks) {
+__global__ void __launch_bounds__(kMergeThreads) jfa_cache_merge_kernel(const CacheFwdParams p, int tasks) {
     __shared__ uint32_t there;
     for (int base = blockIdx.x; base < tasks; base += 32 * gridDim.x) {  // 32 tasks of this CTA
         if (threadIdx.x < 32) {
@@ -955,11 +968,11 @@ cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& 
 cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     const int tasks = num_sms * kBlocksPerCta * kMergeCtas, grid = num_sms * 4;
     if (D == 128)
-        jfa_cache_merge_kernel<128><<<grid, 256, 0, st>>>(p, tasks);
+        jfa_cache_merge_kernel<128><<<grid, kMergeThreads, 0, st>>>(p, tasks);
     else if (D == 32)
-        jfa_cache_merge_kernel<32><<<grid, 256, 0, st>>>(p, tasks);
+        jfa_cache_merge_kernel<32><<<grid, kMergeThreads, 0, st>>>(p, tasks);
     else
-        jfa_cache_merge_kernel<64><<<grid, 256, 0, st>>>(p, tasks);
+        jfa_cache_merge_kernel<64><<<grid, kMergeThreads, 0, st>>>(p, tasks);
     return cudaGetLastError();
 }
 
