@@ -26,7 +26,7 @@
  *    aligned DEVICE pointers owned by the caller.  lse is fp32 [T_q, H].
  *  - Element type: JFA_BF16 (bfloat16, head_dim 64 or 128; tensor-core products)
  *    or JFA_F32 (float, head_dim 32 or 64; plain fp32 arithmetic on the CUDA cores,
- *    no TF32 rounding).  Accumulation is fp32.
+ *    no TF32 rounding; jfa_cache_fwd says what it does).  Accumulation is fp32.
  *  - Values must be finite: a key/value row of a neighbouring sequence is read
  *    (and multiplied by an exact zero weight) at jagged tile edges.
  *  - Calls are asynchronous on `stream` (a cudaStream_t, NULL = legacy default
@@ -420,8 +420,8 @@ const char* jfa_status_string(int32_t status);
  *                     position rotation applied to keys and queries on the way;
  *   jfa_cache_fwd     attends from the new tokens to the cached positions.
  * Both take, as int32 DEVICE arrays read when the kernels run (so a captured graph can be
- * replayed on new contents), for B of at most 8192 sequences and T below 2^30 rows:
- * *   q_offsets [B+1]  the new tokens of sequence b are rows q_offsets[b] .. q_offsets[b+1]
+ * replayed on new contents), for B of at most 8192 sequences and T of at most 2^30 rows:
+ *   q_offsets [B+1]  the new tokens of sequence b are rows q_offsets[b] .. q_offsets[b+1]
  *                    of Q, K and V (non-decreasing; rows from q_offsets[B] to T belong to
  *                    no sequence and are left alone);
  *   kv_lens [B]      positions of sequence b in the cache, its new tokens included: they are
@@ -432,7 +432,9 @@ const char* jfa_status_string(int32_t status);
  * [0, max_pages * page_size], or a page outside [0, n_pages) sets the status that
  * jfa_cache_device_status reports as JFA_ERR_DEVICE_BOUNDS.  Nothing outside the arrays is
  * read or written then; a bad sequence's rows stay as they were, and rows that needed a bad
- * page are wrong.
+ * page are wrong.  Offsets that decrease make a bad sequence and let others overlap: rows of
+ * several sequences hold one's result, or, where the overlap asks for more work than can be
+ * counted, nothing is computed.
  */
 typedef struct jfa_cache_t* jfa_cache;
 
@@ -495,10 +497,14 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  * over the keys j < kv_len allowed as in jfa_plan_create_ex: causal (0/1) j <= i', window
  * W >= 0 (with causal) j >= i' - W, -1: none.  A row with no allowed key gets o = 0 and
  * lse = -inf.
- *   Q [T, H, D] in the cache's dtype, tokens q_stride elements apart (a multiple of 16
- *   bytes); O [T, H, D] dense, in o_dtype (JFA_F32, or JFA_BF16 with a bf16 cache);
+ *   Q [T, H, D] in the cache's dtype (T H at most 2^31 - 257), tokens q_stride elements apart (a
+ *   multiple of 16 bytes); O [T, H, D] dense, in o_dtype (JFA_F32, or JFA_BF16 with a bf16 cache);
+ *   O must not overlap Q.
  *   lse fp32 [T, H], or NULL.  bias_kind JFA_BIAS_NONE or JFA_BIAS_RELPOS32 (fp32 [H, 32]).
- *   scale must be finite and positive.
+ *   scale must be finite and positive, and scores finite (so the bias too: it is no mask).
+ *   fp32 is computed at fp32's accuracy, single tokens and short query sets (up to 16 rows of
+ *   grouped heads) on the CUDA cores, longer ones on the tensor cores with each operand as the
+ *   sum of three bf16 values, for magnitudes below 2^127.
  *   max_q_len: an upper bound of the batch's q_len, or 0 if unknown (T is taken).  It only
  *   chooses among kernels: results do not depend on it beyond rounding, and a longer
  *   sequence is still computed in full.
@@ -509,8 +515,11 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  *   JFA_CACHE_ZERO_BYTES must be zero before its first use and are zero again after every
  *   call (zero them again after JFA_ERR_TIMEOUT); the rest needs no initialisation.  Calls
  *   that may overlap on the GPU need a workspace each: order those that share one.
- *   The result is the same bit for bit on every run of the same call.
- * Errors: INVALID_ARG, UNSUPPORTED, PLAN_MISMATCH (another device is current), CUDA.
+ *   The result is the same bit for bit on every run of the same call.  There is no backward
+ *   pass: a cache is for serving (training keys and values go through jfa_fwd and jfa_bwd).
+ * Errors: INVALID_ARG, UNSUPPORTED (a dense bias, bf16 output of an fp32 cache, more than 128
+ *   grouped heads with bf16, or row tiles x key tiles that max_pages and T allow past 2^31),
+ *   PLAN_MISMATCH (another device is current), CUDA.
  */
 #define JFA_CACHE_ZERO_BYTES ((size_t)32768)
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,

@@ -4,14 +4,22 @@
 // at most 16 multiply-adds: the kernel is a stream of K and V at memory speed, and everything
 // else has to hide under it.  Stages of 32 KB (K and V of 64 keys, or of 128 at head_dim 64;
 // one TMA box per page and 128-byte column block) pass through a ring of 96 KB per CTA, two
-// CTAs per SM; one warp issues the loads, four warps take a quarter of each stage's keys.  The products are m16n8k16 tensor-core
-// instructions on operands read by ldmatrix: at 16 rows a 128-row accumulator tile would be
-// seven-eighths padding, and the arithmetic is a small part of the time either way.
+// CTAs per SM; one warp issues the loads, four warps take a quarter of each stage's keys.
+// The products are m16n8k16 tensor-core instructions on operands read by ldmatrix: at 16 rows a
+// 128-row accumulator tile would be seven-eighths padding, and the arithmetic is a small part of
+// the time either way.
 //   S = Q K^T (Q in registers), online softmax per warp with a lazily moved maximum, O += P V.
 // P is rounded to bf16 for the product (its sum is taken before, in fp32).  The warps work on
 // separate keys with separate (m, l, O) and merge at the end of the item, so no step of the
 // stream waits for another warp.  The work split, and the merge of an item split over CTAs,
 // are those of cache_common.cuh.
+// Measured, one token each of 32 query and 8 key heads of 128: 64 sequences of 200-16k keys
+// (1.06 GB) 175 us, 6.07 TB/s, 0.90 of the copy rate; one history of 131k keys (537 MB) 97 us,
+// 0.82; 200 sequences of up to 2k keys, 8 heads, with a bias table (454 MB) 94 us, 0.71; one
+// sequence of 1k keys 10.9 us.  What is not the stream: 3 us until the first keys arrive (launch,
+// offsets, page), 2.5 us an item's end (four warps' results, and its part's way to memory), 3 us
+// for the last CTA's merge of an item's parts, and equal ranges that end up to 10% apart (131k
+// keys: 71 to 85 us, at a mean of 77).
 #include "cache_common.cuh"
 #include "tilemath.cuh"
 

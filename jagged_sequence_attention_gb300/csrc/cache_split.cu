@@ -10,8 +10,12 @@
 // sums at fp32's level: the small terms go first, while the accumulator is small, and leave
 // only the x0 y0 steps (4 for a score, 8 for an output) to the full-size accumulator; and the
 // output of each key tile starts from zero and is added to the running one in registers.
-// Six bf16 products at 16 times and more the rate of the FMA units: the split, the softmax and
-// the loads bound the kernel, not the products.
+// Six bf16 products at 16 times and more the rate of the FMA units.  A step of 128 rows x 128
+// keys takes 2.5 us: 2.1 of products (24 + 48 instructions of M = 128, those of P V at the half
+// rate of N = 64), the rest the chain output -> P -> output of a step, as TMEM holds one P and
+// one output.  Measured: 20 sequences of 200-4000 keys, 5 of them prompts of 100-600 tokens (8
+// query, 4 key heads of 64) 75 us, of which this kernel 47, the single tokens' 20 and the merge
+// 8.
 //
 // An item is 128 packed rows of one (sequence, key head); a step is 128 keys.  Head dimension
 // 32 runs as 64 with zeros.  CTA = 16 warps, one CTA per SM:
