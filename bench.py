@@ -115,10 +115,11 @@ KERNEL_SOURCE = {
 
 def kernel_digest(kernel):
     """Digest of the sources a kernel is built from: its own .cu file and every header in
-    csrc (a measurement stays valid while these are unchanged)."""
+    csrc but the paged cache's own (a measurement stays valid while these are unchanged)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "jagged_sequence_attention_gb300", "csrc")
-    names = [KERNEL_SOURCE[kernel]] + sorted(n for n in os.listdir(csrc) if n.endswith((".h", ".cuh")))
+    names = [KERNEL_SOURCE[kernel]] + sorted(n for n in os.listdir(csrc)
+                                             if n.endswith((".h", ".cuh")) and not n.startswith("cache_"))
     for name in names:
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
