@@ -106,6 +106,50 @@ struct SplitStream {
     }
 };
 
+// Four elements of row r, the piece-th four, to the parts' tiles at `dst`.
+__device__ __forceinline__ void put_parts(uint32_t dst, int r, int piece, const float4& v) {
+    uint32_t w[3][2];
+    split2(v.x, v.y, w[0][0], w[1][0], w[2][0]);
+    split2(v.z, v.w, w[0][1], w[1][1], w[2][1]);
+    const uint32_t at = dst + uint32_t(r * 128 + (((piece >> 1) ^ (r & 7)) << 4) + (piece & 1) * 8);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + uint32_t(q * SpCfg::kPlane)), "r"(w[q][0]), "r"(w[q][1])
+                     : "memory");
+}
+
+// A thread's rows of a loaded tile at `src`, in parts to `dst`; zeros but for rows [lo, hi), as
+// no row of the item may look there.  Three rows' loads at once, ahead of the stores that the
+// compiler keeps them in order with.  (Not inlined: the warps of an SM fetch code from many
+// places at a time.)
+template <int D>
+__device__ __noinline__ void split_rows(uint32_t src, uint32_t dst, int lo, int hi, int row0, int c) {
+    constexpr int kStep = 4 * SpCfg::kSplitWarps;
+#pragma unroll 1
+    for (int r0 = row0; r0 < 128; r0 += 3 * kStep) {
+        uint4 u[3][D / 32];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int r = min(r0 + i * kStep, 127);
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h)
+                u[i][h] = ld_shared_v4(src + uint32_t(h * SpCfg::kStageBlock + r * 128 + ((c ^ (r & 7)) << 4)));
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int r = r0 + i * kStep;
+            if (r >= 128) break;
+            const bool in = r >= lo && r < hi;
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h)
+                put_parts(dst, r, c + 8 * h,
+                          in ? make_float4(__uint_as_float(u[i][h].x), __uint_as_float(u[i][h].y), __uint_as_float(u[i][h].z),
+                                           __uint_as_float(u[i][h].w))
+                             : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+    }
+}
+
 template <int D, bool BIAS>
 __global__ void __launch_bounds__(SpCfg::kThreads, 1)
     jfa_cache_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -275,54 +319,16 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
         const int tid = threadIdx.x - 32 * C::kSoftWarps;
         constexpr int kStep = 4 * C::kSplitWarps;
         const int c = tid & 7, row0 = tid >> 3;  // elements 4 c .. and 32 + 4 c .. of rows row0 + kStep i
-        // four elements of row r, from column 4 c (+ 32) on, to the parts' tiles at `off`
-        auto put4 = [&](int off, int r, int piece, const float4& v) {
-            uint32_t w[3][2];
-            split2(v.x, v.y, w[0][0], w[1][0], w[2][0]);
-            split2(v.z, v.w, w[0][1], w[1][1], w[2][1]);
-            const uint32_t at = sbase + uint32_t(off + r * 128 + (((piece >> 1) ^ (r & 7)) << 4) + (piece & 1) * 8);
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + uint32_t(q * C::kPlane)), "r"(w[q][0]), "r"(w[q][1])
-                             : "memory");
-        };
         auto arrive = [&](int full) {
             fence_proxy_async_smem();  // before the products read them
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(full));
         };
-        // a loaded tile's rows, zeros where no row of the item may look (positions from c0 on)
-        // (three rows' loads at once, ahead of the stores that the compiler keeps them in order with)
-        auto convert = [&](const SplitStream& s, int stage, int off) {
-            const int c0 = (s.g.r.f + s.k) * kSpBN;
-#pragma unroll 1
-            for (int r0 = row0; r0 < 128; r0 += 3 * kStep) {
-                uint4 u[3][D / 32];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int r = min(r0 + i * kStep, 127);
-#pragma unroll
-                    for (int h = 0; h < D / 32; ++h)
-                        u[i][h] = ld_shared_v4(sbase + uint32_t(stage + h * C::kStageBlock + r * 128 + ((c ^ (r & 7)) << 4)));
-                }
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int r = r0 + i * kStep, j = c0 + r;
-                    if (r >= 128) break;
-                    const bool in = j >= s.g.r.lo && j < s.g.r.hi;
-#pragma unroll
-                    for (int h = 0; h < D / 32; ++h)
-                        put4(off, r, c + 8 * h,
-                             in ? make_float4(__uint_as_float(u[i][h].x), __uint_as_float(u[i][h].y), __uint_as_float(u[i][h].z),
-                                              __uint_as_float(u[i][h].w))
-                                : make_float4(0.f, 0.f, 0.f, 0.f));
-                }
-            }
-        };
         auto split_tile = [&](SplitStream& s, int staged, int full, int stage, int off) {
             const uint32_t ph = s.it & 1;
             if (!wwait(staged, ph) || !wwait(full + 1, ph ^ 1)) return false;
-            convert(s, stage, off);
+            const int c0 = (s.g.r.f + s.k) * kSpBN;
+            split_rows<D>(sbase + uint32_t(stage), sbase + uint32_t(off), s.g.r.lo - c0, s.g.r.hi - c0, row0, c);
             arrive(full);
             if (lane == 0) mbar_arrive(bar(staged + 1));
             ++s.it;
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(SpCfg::kThreads, 1)
                     for (int h = 0; h < D / 32; ++h) v[h] = src[c + 8 * h];
                 }
 #pragma unroll
-                for (int h = 0; h < D / 32; ++h) put4(C::kOffQ, r, c + 8 * h, v[h]);
+                for (int h = 0; h < D / 32; ++h) put_parts(sbase + C::kOffQ, r, c + 8 * h, v[h]);
             }
             arrive(P_Q_FULL);
             return true;
