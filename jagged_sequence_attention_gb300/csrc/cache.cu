@@ -66,10 +66,13 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
 constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 // What an item's start and end cost the decode kernel, in its stages of 32 KB: about 4 us of a
-// CTA, at its share of the memory's rate.  And the chunk and split kernels, in their steps of
-// 128 keys (about 2 us each).
-constexpr int kDecodeItemUnits = 3;
+// CTA, at its share of the memory's rate (200 sequences of up to 2k keys: 102 us with 1, 93 with 2,
+// 95 with 3, 98 with 5).  And the chunk and split kernels, in their steps of 128 keys: 1.8-2.6 us
+// (48 sequences, ten of them prompts: 71 us with 2, 66.5 with 3, 70.5 with 5) and 2.5 us (20
+// ragged sequences: 74.4 with 2, 75.6 with 3, 78.4 with 5).
+constexpr int kDecodeItemUnits = 2;
 constexpr int kChunkItemUnits = 3;
+constexpr int kSplitItemUnits = 2;
 
 // Whether the cache's device is the current one.
 bool on_device(jfa_cache c) {
@@ -306,7 +309,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.item_cost = 0;
         p.min_units = 1;
         if (!bf16) {
-            p.item_cost = kChunkItemUnits;
+            p.item_cost = kSplitItemUnits;
             if (!fits(tiles(T * p.g), 128)) return JFA_ERR_UNSUPPORTED;
             e = launch_cache_split(D, cache->mk, cache->mv, p, n, st);
         } else {

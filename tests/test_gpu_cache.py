@@ -668,3 +668,13 @@ def test_short_and_long_query_sets_take_turns(jfa):
     kv = [n + 100 * (i % 7) for i, n in enumerate(q)]
     c = Case(q, kv, H=2, Hkv=1, D=64, page=32, seed=4)
     c.check(*c.run(jfa))
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (BF, 64), (F32, 64)])
+def test_many_short_chunks(jfa, dtype, D):
+    # hundreds of items of one to four key tiles, with some that see no key among them
+    rs = np.random.RandomState(D)
+    q = rs.randint(5, 60, 700)
+    kv = np.where(rs.rand(700) < 0.1, 0, rs.randint(1, 450, 700))
+    c = Case(q, kv, H=8, Hkv=2, D=D, page=16, dtype=dtype, seed=D)
+    c.check(*c.run(jfa))
