@@ -66,11 +66,13 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
 constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
 constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 // What an item's start and end cost the decode kernel, in its stages of 32 KB: about 4 us of a
-// CTA, at its share of the memory's rate (200 sequences of up to 2k keys: 102 us with 1, 93 with 2,
-// 95 with 3, 98 with 5).  And the chunk and split kernels, in their steps of 128 keys: 1.8-2.6 us
-// (48 sequences, ten of them prompts: 71 us with 2, 66.5 with 3, 70.5 with 5) and 2.5 us (20
-// ragged sequences: 74.4 with 2, 75.6 with 3, 78.4 with 5).
-constexpr int kDecodeItemUnits = 2;
+// CTA, at its share of the memory's rate (one history of 131k keys: 100.5 us with 2, 97 with 3, 96
+// with 4; 200 sequences of up to 2k keys: 102 with 1, 93 with 2, 95 with 3, 98 with 5).  Beside
+// the chunk kernel, on SMs that come free at different times, less (256 ragged query sets: 248.5
+// us with 3 and with 5, 244 with 2 and with 1).  And the chunk and split kernels, in their steps
+// of 128 keys: 1.8-2.6 us (48 sequences, ten of them prompts: 71 us with 2, 66.5 with 3, 70.5 with
+// 5) and 2.5 us (20 ragged sequences: 74.4 with 2, 75.6 with 3, 78.4 with 5).
+constexpr int kDecodeItemUnits = 3, kDecodeItemUnitsBeside = 2, kSimtItemUnits = 2;
 constexpr int kChunkItemUnits = 3;
 constexpr int kSplitItemUnits = 2;
 
@@ -333,7 +335,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const CacheFwdParams pc = p;  // the merge's parameters
     p.bm = bf16 || p.g > 4 ? 16 : 4;
     p.min_units = 1;
-    p.item_cost = bf16 ? kDecodeItemUnits : 2;
+    p.item_cost = !bf16 ? kSimtItemUnits : chunks ? kDecodeItemUnitsBeside : kDecodeItemUnits;
     if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g), 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
