@@ -25,11 +25,11 @@
 // adds them up: the last part's CTA alone would read them at one SM's rate (about 2 us a
 // part of 132 KB), and a long history under one chunk has tens of parts.
 // Measured: 8 prompts of 700-1024 tokens (32 query, 8 key heads of 128) over 3k-14k keys, 859
-// GFLOP, 723 us with the merge, 1188 TFLOP/s, 0.63 of the measured matrix-product burst rate.  A
+// GFLOP, 709 us with the merge, 1211 TFLOP/s, 0.64 of the measured matrix-product burst rate.  A
 // step of 256 x 128 scores takes 1.8 us (2.6 with a bias), its products 1.1 and its exponentials
 // as much: what is left is each tile's own chain S -> softmax -> P V -> S, since at head_dim 128
 // TMEM holds no second score tile per row tile.  256 sets of 1-64 rows over 100-8000 keys (8
-// heads of 64, 947 MB) 248 us, 0.56 of the copy rate: long items stream 128 keys in 0.86 us on
+// heads of 64, 947 MB) 243 us, 0.57 of the copy rate: long items stream 128 keys in 0.86 us on
 // each SM (5.7 TB/s in all), an item's end and start cost 3 us more, a single short item 5-8 us
 // from its draw to its stored rows, and the sets of up to 16 rows follow in the decode kernel
 // (53 us).  Slower, and not kept: two key tiles in one score tile for sets of up to 64 rows
@@ -872,8 +872,8 @@ __global__ void __launch_bounds__(608, 1)
 
 // Adds up the parts of the items cut between blocks.  A task is 64 rows of the item that starts
 // in a block and goes on past it; its flag says whether there is one.  Bound by the latency of
-// its few loads for most calls, and by the parts' bytes for long prompts (84 MB for the 8 prompts
-// above, which it reads in about 15 us).  The grid is small and a
+// its few loads for most calls, and by the parts' bytes for long prompts (42 MB for the 8 prompts
+// above: 17 us from DRAM, less from L2).  The grid is small and a
 // CTA looks at the flags of all its tasks at once, clearing them for the next call: most calls
 // cut few items, and a CTA for each possible task would cost 10 us to find nothing to do.
 // A thread takes one row and a quarter of the columns, some parts at a time against a running

@@ -15,7 +15,7 @@
 // are those of cache_common.cuh.
 // Measured, one token each of 32 query and 8 key heads of 128: 64 sequences of 200-16k keys
 // (1.06 GB) 175 us, 6.07 TB/s, 0.90 of the copy rate; one history of 131k keys (537 MB) 97 us,
-// 0.82; 200 sequences of up to 2k keys, 8 heads, with a bias table (454 MB) 94 us, 0.71; one
+// 0.82; 200 sequences of up to 2k keys, 8 heads, with a bias table (454 MB) 95 us, 0.70; one
 // sequence of 1k keys 10.9 us.  What is not the stream: 3 us until the first keys arrive (launch,
 // offsets, page), 2.5 us an item's end (four warps' results, and its part's way to memory), 3 us
 // for the last CTA's merge of an item's parts, and equal ranges that end up to 10% apart (131k
