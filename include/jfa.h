@@ -519,7 +519,8 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  *   pass: a cache is for serving (training keys and values go through jfa_fwd and jfa_bwd).
  * Errors: INVALID_ARG, UNSUPPORTED (a dense bias, bf16 output of an fp32 cache, more than 128
  *   grouped heads with bf16, or row tiles x key tiles that max_pages and T allow past 2^31),
- *   PLAN_MISMATCH (another device is current), CUDA.
+ *   PLAN_MISMATCH (another device is current), CUDA.  A call refused with one of the first
+ *   three launches nothing and writes nothing.
  */
 #define JFA_CACHE_ZERO_BYTES ((size_t)32768)
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,

@@ -300,49 +300,53 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const int n = cache->num_sms, D = cache->D;
     const bool bf16 = cache->dtype == JFA_BF16;
     const bool chunks = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g > kDecodeRows;
-    // the kernels count units in 31 bits; the row tiles of `rows` rows are at most
-    auto tiles = [&](int64_t rows) { return rows / p.bm + B; };
+    // the kernels count units in 31 bits; tiles(): the row tiles of bm rows that `rows` rows have at most
+    auto tiles = [&](int64_t rows, int bm) { return rows / bm + B; };
     auto fits = [&](int64_t n_tiles, int bn) {
         return double(n_tiles) * p.Hkv * (double(max_kv) / bn + 16.0) < double(INT32_MAX) - 65536.0;
     };
-    cudaError_t e = cudaSuccess;
+    // Every check of both kernels comes before the first launch: a refused call does nothing.
+    CacheFwdParams pc = p;  // the chunk kernel's parameters, and the merge's
+    CUtensorMap mq;
     if (chunks) {
-        p.row_lo = kDecodeRows;
-        p.bm = 128;
-        p.item_cost = 0;
-        p.min_units = 1;
-        if (!bf16) {
-            p.item_cost = kSplitItemUnits;
-            if (!fits(tiles(T * p.g), 128)) return JFA_ERR_UNSUPPORTED;
-            e = launch_cache_split(D, cache->mk, cache->mv, p, n, st);
-        } else {
-            // the queries as (D, head, token), boxes of one tile's rows
-            p.tile_tokens = 128 / p.g;
-            p.bm = 2 * p.tile_tokens * p.g;
-            p.item_cost = kChunkItemUnits;
-            p.min_units = kChunkItemUnits + 1;
-            if (!fits(tiles(T * p.g), 128)) return JFA_ERR_UNSUPPORTED;
-            CUtensorMap mq;
-            const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
-            const int64_t strides[2] = {D, q_stride};
-            const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(p.tile_tokens)};
-            const jfa_status ms = make_map(&mq, JFA_BF16, Q, 3, dims, strides, box);
-            if (ms != JFA_OK) return ms;
-            e = launch_cache_chunk(D, mq, cache->mk, cache->mv, p, n, st);
+        pc.row_lo = kDecodeRows;
+        pc.bm = 128;
+        pc.item_cost = kSplitItemUnits;
+        pc.min_units = 1;
+        if (bf16) {
+            pc.tile_tokens = 128 / p.g;
+            pc.bm = 2 * pc.tile_tokens * p.g;
+            pc.item_cost = kChunkItemUnits;
+            pc.min_units = kChunkItemUnits + 1;
         }
-        p.row_lo = 0;
+        if (!fits(tiles(T * p.g, pc.bm), 128)) return JFA_ERR_UNSUPPORTED;
         p.row_hi = kDecodeRows;
     }
-    const CacheFwdParams pc = p;  // the merge's parameters
     p.bm = bf16 || p.g > 4 ? 16 : 4;
     p.min_units = 1;
     p.item_cost = !bf16 ? kSimtItemUnits : chunks ? kDecodeItemUnitsBeside : kDecodeItemUnits;
-    if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g), 64)) return JFA_ERR_UNSUPPORTED;
+    if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g, p.bm), 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
+    if (chunks && bf16) {  // the queries as (D, head, token), boxes of one tile's rows
+        const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
+        const int64_t strides[2] = {D, q_stride};
+        const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(pc.tile_tokens)};
+        const jfa_status ms = make_map(&mq, JFA_BF16, Q, 3, dims, strides, box);
+        if (ms != JFA_OK) return ms;
+    }
+    cudaError_t e = cudaSuccess;
+    if (chunks)
+        e = bf16 ? launch_cache_chunk(D, mq, cache->mk, cache->mv, pc, n, st) : launch_cache_split(D, cache->mk, cache->mv, pc, n, st);
     if (e == cudaSuccess)
         e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, p, chunks, n, st);
-    if (e == cudaSuccess && chunks) e = launch_cache_merge(D, pc, n, st);
+    if (chunks) {
+        // The chunk kernel's flags of cut items are the merge's to clear, so it follows whatever
+        // failed before it; where it fails itself they are cleared here.
+        const cudaError_t em = launch_cache_merge(D, pc, n, st);
+        if (em != cudaSuccess) (void)cudaMemsetAsync(workspace, 0, JFA_CACHE_ZERO_BYTES, st);
+        if (e == cudaSuccess) e = em;
+    }
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 

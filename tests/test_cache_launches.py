@@ -1,0 +1,95 @@
+"""What the paged-cache calls launch, and in which order they check: the library's host code
+against a stand-in for the CUDA runtime and the kernels (fake_cuda.cpp), without a GPU."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from jagged_sequence_attention_gb300 import _build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+WS = 1 << 20  # the workspace's address
+
+
+@pytest.fixture(scope="module")
+def jfa():
+    _build.build()
+    from jagged_sequence_attention_gb300 import jfa as m
+    m.lib()
+    return m
+
+
+@pytest.fixture(scope="module")
+def fake(jfa, tmp_path_factory):
+    path = str(tmp_path_factory.mktemp("fake") / "libcache_fake.so")
+    # (symbols bind within the library: torch has loaded a CUDA runtime of its own)
+    subprocess.run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-Wl,-z,defs",
+                    "-I/usr/local/cuda/include", os.path.join(HERE, "fake_cuda.cpp"),
+                    os.path.join(_build.BUILD, "cache.o"), "-o", path], check=True)
+    L = ctypes.CDLL(path)
+    for name in ("jfa_cache_create", "jfa_cache_destroy", "jfa_cache_append", "jfa_cache_workspace_size", "jfa_cache_fwd"):
+        f = getattr(L, name)
+        f.argtypes, f.restype = getattr(jfa.lib(), name).argtypes, getattr(jfa.lib(), name).restype
+    L.fake_log.argtypes, L.fake_log.restype = [ctypes.c_char_p], ctypes.c_char_p
+    return L
+
+
+class Calls:
+    """A cache of `Hkv` heads of 64 in pages of 1024, and attention over it."""
+
+    def __init__(self, L, dtype, Hkv, g=1):
+        self.L, self.H, self.D = L, Hkv * g, 64
+        s = (ctypes.c_int64 * 3)(1024 * Hkv * 64, Hkv * 64, 64)
+        self.h = ctypes.c_void_p()
+        assert L.jfa_cache_create(dtype, Hkv, 64, 1024, 4, 1 << 16, 1 << 17, s, s, None, ctypes.byref(self.h)) == 0
+        L.fake_log(b"")
+        self.o_dtype = 1
+
+    def fwd(self, B, T, max_q_len, max_kv, fail=""):
+        """(status, what was launched)"""
+        self.L.fake_log(fail.encode())
+        n = self.L.jfa_cache_workspace_size(self.h, self.H)
+        r = self.L.jfa_cache_fwd(self.h, B, T, max_q_len, 4096, 4096, 4096, max_kv // 1024, 1 << 18, self.H * self.D, self.H, 1, -1,
+                                 0, None, 0.125, 1 << 19, self.o_dtype, None, WS, n, None)
+        return r, self.L.fake_log(b"").decode()
+
+
+BF16, F32 = 0, 1
+
+
+@pytest.mark.parametrize("dtype,chunk,few", [(BF16, "chunk", "decode"), (F32, "split", "simt")])
+def test_launches(jfa, fake, dtype, chunk, few):
+    c = Calls(fake, dtype, 4, 2)
+    assert c.fwd(3, 3, 1, 4096) == (jfa.JFA_OK, few)
+    assert c.fwd(3, 100, 8, 4096) == (jfa.JFA_OK, few)
+    assert c.fwd(3, 100, 9, 4096) == (jfa.JFA_OK, f"{chunk} {few} merge")
+    assert c.fwd(3, 100, 0, 4096) == (jfa.JFA_OK, f"{chunk} {few} merge")
+    assert c.fwd(0, 0, 0, 4096) == (jfa.JFA_OK, "")
+
+
+# Batches that the chunk kernel could count and the few-rows kernel, with shorter key tiles and
+# in fp32 four items a sequence, could not; and ones that neither could.
+@pytest.mark.parametrize("dtype,Hkv,max_kv", [(F32, 32, 131072), (F32, 8, 524288), (BF16, 32, 524288), (F32, 64, 1 << 24),
+                                              (BF16, 64, 1 << 24)])
+def test_a_refused_call_launches_nothing(jfa, fake, dtype, Hkv, max_kv):
+    c = Calls(fake, dtype, Hkv)
+    for T, max_q_len in ((64, 64), (8192 * 17, 17), (8192, 0)):
+        assert c.fwd(8192, T, max_q_len, max_kv) == (jfa.JFA_ERR_UNSUPPORTED, "")
+
+
+def test_a_failed_tensor_map_launches_nothing(jfa, fake):
+    c = Calls(fake, BF16, 4, 2)
+    assert c.fwd(3, 100, 0, 4096, fail="encode") == (jfa.JFA_ERR_CUDA, "")
+
+
+@pytest.mark.parametrize("dtype,chunk,few", [(BF16, "chunk", "decode"), (F32, "split", "simt")])
+def test_a_failed_launch_leaves_the_workspace_zero(jfa, fake, dtype, chunk, few):
+    """The chunk kernel sets flags that the merge clears: once its launch was tried, the merge
+    follows, and where that fails, the zeroed part is zeroed on the stream."""
+    c = Calls(fake, dtype, 4, 2)
+    assert c.fwd(3, 100, 0, 4096, fail=chunk) == (jfa.JFA_ERR_CUDA, f"{chunk}! merge")
+    assert c.fwd(3, 100, 0, 4096, fail=few) == (jfa.JFA_ERR_CUDA, f"{chunk} {few}! merge")
+    zeroed = f"memset({WS},0,{jfa.JFA_CACHE_ZERO_BYTES})"
+    assert c.fwd(3, 100, 0, 4096, fail="merge") == (jfa.JFA_ERR_CUDA, f"{chunk} {few} merge! {zeroed}")
+    assert c.fwd(3, 3, 1, 4096, fail=few) == (jfa.JFA_ERR_CUDA, f"{few}!")
