@@ -513,7 +513,9 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  *   such positions may be unset in the table; the other values must be finite.
  *   workspace: at least jfa_cache_workspace_size bytes, 256-byte aligned.  Its first
  *   JFA_CACHE_ZERO_BYTES must be zero before its first use and are zero again after every
- *   call (zero them again after JFA_ERR_TIMEOUT); the rest needs no initialisation.  Calls
+ *   call (zero them again after JFA_ERR_TIMEOUT; what was not zero can spoil results, and sets
+ *   JFA_ERR_DEVICE_BOUNDS where it names rows that the call does not have, which are not
+ *   written); the rest needs no initialisation.  Calls
  *   that may overlap on the GPU need a workspace each: order those that share one.
  *   The result is the same bit for bit on every run of the same call.  There is no backward
  *   pass: a cache is for serving (training keys and values go through jfa_fwd and jfa_bwd).

@@ -343,7 +343,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     if (chunks) {
         // The chunk kernel's flags of cut items are the merge's to clear, so it follows whatever
         // failed before it; where it fails itself they are cleared here.
-        const cudaError_t em = launch_cache_merge(D, pc, n, st);
+        const cudaError_t em = launch_cache_merge(D, pc, bf16 ? n * kBlocksPerCta : n, n, st);
         if (em != cudaSuccess) (void)cudaMemsetAsync(workspace, 0, JFA_CACHE_ZERO_BYTES, st);
         if (e == cudaSuccess) e = em;
     }

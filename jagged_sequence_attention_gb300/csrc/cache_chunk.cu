@@ -940,8 +940,17 @@ __device__ __forceinline__ void merge_rows(const CacheFwdParams& p, const CacheC
     if (p.lse && group == 0) p.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Whether a record is one of this call's: one that an earlier call left (in a workspace that was
+// not zero) may name rows, heads or parts that this call does not have.
+__device__ __forceinline__ bool cut_fits(const CacheFwdParams& p, const CacheCut& c, int blocks) {
+    return c.q0 >= 0 && c.q0 < p.T && c.rows >= 1 && c.rows <= kMergeRows && c.row0 >= 0 && c.row0 <= INT_MAX - kMergeRows &&
+           div_g(p, c.row0 + c.rows - 1) < p.T - c.q0 && c.head0 >= 0 && c.head0 <= p.H - p.g && c.first >= 0 &&
+           c.first <= c.last && c.last < blocks;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) jfa_cache_merge_kernel(const CacheFwdParams p, int tasks) {
+__global__ void __launch_bounds__(kMergeThreads) jfa_cache_merge_kernel(const CacheFwdParams p, int blocks) {
+    const int tasks = blocks * kMergeCtas;
     __shared__ uint32_t there;
     for (int base = blockIdx.x; base < tasks; base += 32 * gridDim.x) {  // 32 tasks of this CTA
         if (threadIdx.x < 32) {
@@ -955,6 +964,10 @@ __global__ void __launch_bounds__(kMergeThreads) jfa_cache_merge_kernel(const Ca
         for (uint32_t m = there; m; m &= m - 1) {
             const int i = base + (__ffs(m) - 1) * gridDim.x;
             const CacheCut cut = p.cuts[i / kMergeCtas];
+            if (!cut_fits(p, cut, blocks)) {
+                if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
+                continue;
+            }
             merge_rows<D>(p, cut, 64 * (i % kMergeCtas) + (threadIdx.x & 63), threadIdx.x >> 6);
         }
         __syncthreads();
@@ -980,14 +993,14 @@ cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& 
     return p.bias ? launch<64, true>(mq, mk, mv, p, num_sms, st) : launch<64, false>(mq, mk, mv, p, num_sms, st);
 }
 
-cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    const int tasks = num_sms * kBlocksPerCta * kMergeCtas, grid = num_sms * 4;
+cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int blocks, int num_sms, cudaStream_t st) {
+    const int grid = num_sms * 4;
     if (D == 128)
-        jfa_cache_merge_kernel<128><<<grid, kMergeThreads, 0, st>>>(p, tasks);
+        jfa_cache_merge_kernel<128><<<grid, kMergeThreads, 0, st>>>(p, blocks);
     else if (D == 32)
-        jfa_cache_merge_kernel<32><<<grid, kMergeThreads, 0, st>>>(p, tasks);
+        jfa_cache_merge_kernel<32><<<grid, kMergeThreads, 0, st>>>(p, blocks);
     else
-        jfa_cache_merge_kernel<64><<<grid, kMergeThreads, 0, st>>>(p, tasks);
+        jfa_cache_merge_kernel<64><<<grid, kMergeThreads, 0, st>>>(p, blocks);
     return cudaGetLastError();
 }
 

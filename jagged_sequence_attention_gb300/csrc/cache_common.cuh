@@ -560,7 +560,9 @@ size_t cache_chunk_part_bytes(int D, int num_sms);
 // time, then the rows' m and l.
 constexpr int kMergeRows = 256;
 __host__ __device__ constexpr int cache_merge_part(int D) { return kMergeRows * (D + 2); }  // floats
-cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
+// blocks: how many the items may be cut between (num_sms of the split kernel, kBlocksPerCta times
+// as many of the chunk kernel).
+cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int blocks, int num_sms, cudaStream_t st);
 
 struct CacheAppendParams {
     const int32_t* q_off;

@@ -47,7 +47,7 @@ cudaError_t launch_cache_chunk(int, const CUtensorMap&, const CUtensorMap&, cons
                                cudaStream_t) {
     return launched("chunk");
 }
-cudaError_t launch_cache_merge(int, const CacheFwdParams&, int, cudaStream_t) { return launched("merge"); }
+cudaError_t launch_cache_merge(int, const CacheFwdParams&, int, int, cudaStream_t) { return launched("merge"); }
 
 }  // namespace jfa
 
