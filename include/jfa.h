@@ -446,7 +446,8 @@ typedef enum { JFA_ROT_HALF = 0, JFA_ROT_PAIRS = 1 } jfa_rot_kind;
  * A handle on a cache whose K and V arrays the caller owns (they must outlive it).
  *   dtype JFA_BF16 (D 64 or 128) or JFA_F32 (D 32 or 64); Hkv >= 1 key/value heads;
  *   page_size a power of two from 8 to 1024; n_pages >= 1.
- *   K, V: DEVICE pointers of the current device, 16-byte aligned; k_strides, v_strides:
+ *   K, V: DEVICE pointers of the current device (device memory of another one is refused with
+ *   INVALID_ARG: the handle's kernels run where it was created), 16-byte aligned; k_strides, v_strides:
  *   host int64[3] (page, slot, head), each at least D and a multiple of 16 bytes.
  *   The handle allocates a status word on the current device (synchronises `stream`).
  *   It keeps no state between calls: calls on one handle may run at once on different

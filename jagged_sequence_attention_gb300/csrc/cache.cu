@@ -120,6 +120,14 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
     if (cudaGetDevice(&dev) != cudaSuccess || cudaGetDeviceProperties(&prop, dev) != cudaSuccess || prop.major != 10 ||
         prop.multiProcessorCount > kMaxSms)
         return JFA_ERR_NO_DEVICE;
+    // (an address that CUDA does not know, or memory of no one device, is the caller's matter)
+    for (const void* a : {K, V}) {
+        cudaPointerAttributes at;
+        if (cudaPointerGetAttributes(&at, a) != cudaSuccess)
+            (void)cudaGetLastError();
+        else if (at.type == cudaMemoryTypeDevice && at.device != dev)
+            return JFA_ERR_INVALID_ARG;
+    }
     jfa_cache_t* c = new (std::nothrow) jfa_cache_t();
     if (!c) return JFA_ERR_CUDA;
     c->dtype = dtype;

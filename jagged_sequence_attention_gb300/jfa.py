@@ -472,6 +472,8 @@ def jfa_cache_create(K: torch.Tensor, V: torch.Tensor, stream=None) -> Cache:
     fn = "jfa_cache_create"
     if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or K.device != V.device or not K.is_cuda:
         _bad(fn, "K and V must be CUDA tensors of one shape [n_pages, page_size, Hkv, D] and type")
+    if K.device.index != torch.cuda.current_device():
+        _bad(fn, f"K and V lie on {K.device}, which is not the current device")
     if K.stride(3) != 1 or V.stride(3) != 1:
         _bad(fn, "the head dimension must be dense")
     n, ps, Hkv, D = K.shape

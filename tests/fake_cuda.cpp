@@ -72,6 +72,15 @@ cudaError_t cudaGetDeviceProperties(cudaDeviceProp* p, int) {
     p->multiProcessorCount = 152;
     return cudaSuccess;
 }
+// addresses from 2^40 on belong to device 1, those from 2^41 on to no device
+cudaError_t cudaPointerGetAttributes(cudaPointerAttributes* a, const void* p) {
+    std::memset(a, 0, sizeof(*a));
+    const uintptr_t v = reinterpret_cast<uintptr_t>(p);
+    a->type = v >> 41 ? cudaMemoryTypeUnregistered : cudaMemoryTypeDevice;
+    a->device = v >> 41 ? -2 : int(v >> 40);
+    return result("attributes");
+}
+cudaError_t cudaGetLastError() { return cudaSuccess; }
 cudaError_t cudaMalloc(void** p, size_t) {
     *p = reinterpret_cast<void*>(uintptr_t(4096));
     return cudaSuccess;

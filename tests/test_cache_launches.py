@@ -5,6 +5,7 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 from jagged_sequence_attention_gb300 import _build
 
@@ -93,3 +94,60 @@ def test_a_failed_launch_leaves_the_workspace_zero(jfa, fake, dtype, chunk, few)
     zeroed = f"memset({WS},0,{jfa.JFA_CACHE_ZERO_BYTES})"
     assert c.fwd(3, 100, 0, 4096, fail="merge") == (jfa.JFA_ERR_CUDA, f"{chunk} {few} merge! {zeroed}")
     assert c.fwd(3, 3, 1, 4096, fail=few) == (jfa.JFA_ERR_CUDA, f"{few}!")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_arrays_of_another_device_are_refused(jfa, fake, dtype):
+    """The handle's device is the current one; keys and values that lie on another would be read
+    there by its kernels."""
+    s = (ctypes.c_int64 * 3)(1024 * 64, 64, 64)
+
+    def create(K, V, fail=""):
+        h = ctypes.c_void_p()
+        fake.fake_log(fail.encode())
+        r = fake.jfa_cache_create(dtype, 1, 64, 1024, 4, K, V, s, s, None, ctypes.byref(h))
+        assert (h.value is not None) == (r == jfa.JFA_OK)
+        fake.jfa_cache_destroy(h)
+        return r
+
+    here, there, host = 1 << 20, 1 << 40, 1 << 41
+    assert create(here, here) == jfa.JFA_OK
+    for K, V in ((there, there), (here, there), (there, here)):
+        assert create(K, V) == jfa.JFA_ERR_INVALID_ARG
+    assert create(host, here) == jfa.JFA_OK             # memory of no device (managed, or the host's) is the caller's matter
+    assert create(here, here, "attributes") == jfa.JFA_OK
+
+
+class OnGpu:
+    """What jfa_cache_create asks of an array, as on a machine with several GPUs."""
+
+    dtype, shape, is_cuda = torch.bfloat16, (4, 16, 2, 64), True
+
+    def __init__(self, device):
+        self.device = torch.device("cuda", device)
+
+    def dim(self):
+        return 4
+
+    def stride(self, i):
+        return (2048, 128, 64, 1)[i]
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_binding_refuses_arrays_of_another_device(jfa, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(jfa, "_stream", lambda s=None: None)
+
+    class Library:
+        jfa_status_string = jfa.lib().jfa_status_string
+
+        def jfa_cache_create(self, *a):
+            pytest.fail("reached the library")
+
+    monkeypatch.setattr(jfa, "lib", lambda: Library())
+    for K, V in ((OnGpu(1), OnGpu(1)), (OnGpu(0), OnGpu(1))):
+        with pytest.raises(jfa.JFAError) as e:
+            jfa.jfa_cache_create(K, V)
+        assert e.value.status == jfa.JFA_ERR_INVALID_ARG
