@@ -477,6 +477,7 @@ jfa_status jfa_cache_device_status(jfa_cache cache, void* stream);
  *   most D.  A position at or past rot_len sets JFA_ERR_DEVICE_BOUNDS and its token is
  *   skipped.
  *   Q may be NULL with a rotation (keys alone); H is then ignored.
+ *   A sequence with fewer positions than new tokens (kv_len < q_len) is bad, as a whole.
  *   Two tokens must not share a slot (pages shared by sequences are for reading).
  * Errors: INVALID_ARG, PLAN_MISMATCH (another device is current), CUDA.
  */

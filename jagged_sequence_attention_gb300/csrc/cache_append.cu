@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kAppendThreads) jfa_cache_append_kernel(const 
     if (b < 0 || b >= p.B) return;  // rows behind the last sequence
     const int q0 = p.q_off[b], q1 = p.q_off[b + 1], kv = p.kv_lens[b];
     const int pos = kv - q1 + t;
-    bool ok = q0 >= 0 && q1 <= p.T && t >= q0 && t < q1 && kv >= 0 && kv <= p.max_kv && pos >= 0;
+    // (at least as many positions as new tokens, so that none lies before the first)
+    bool ok = q0 >= 0 && q1 <= p.T && t >= q0 && t < q1 && kv >= q1 - q0 && kv <= p.max_kv;
     ok = ok && (!p.rot || pos < p.rot_len);
     int page = -1;
     if (ok) page = p.table[size_t(b) * size_t(p.max_pages) + size_t(pos >> p.page_log2)];
