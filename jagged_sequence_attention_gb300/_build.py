@@ -4,8 +4,10 @@ Each translation unit compiles in its own process; the objects link into
 ``jagged_sequence_attention_gb300/libjfa.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU driver (tests that
 only need the host planner) and only needs the driver when a CUDA call runs.  The
-paged cache's compiled Python calls are built beside it (``_cache_calls.so``, host code
-against torch's headers).
+paged cache's compiled Python calls are built beside it (``_cache_calls`` with the
+interpreter's own suffix, host code against torch's headers).  The library needs neither
+torch nor Python's headers: where the calls cannot be compiled, build() warns and the
+library is complete without them.
 """
 from __future__ import annotations
 
@@ -15,6 +17,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libjfa.so")
-CALLS = os.path.join(PKG, "_cache_calls.so")  # compiled Python calls of the paged cache
+# compiled Python calls of the paged cache (the suffix names the interpreter and the machine)
+CALLS = os.path.join(PKG, "_cache_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "plan.cpp", "fwd.cu", "fwd_short.cu", "fwd_pack.cu", "bwd.cu", "bwd_dq.cu", "bwd_fused.cu", "bwd_short.cu", "f32.cu", "static_scratch.cu",
@@ -54,8 +59,6 @@ def _digest(extra) -> str:
 
 def _calls_command(out: str):
     """The compile command of the Python extension (host code only, against torch's headers)."""
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_paths()["include"], INCLUDE, "/usr/local/cuda/include", os.path.join(root, "include"),
@@ -66,23 +69,63 @@ def _calls_command(out: str):
                "-lc10_cuda", "-ltorch_python", "-ltorch_cpu", "-ltorch"])
 
 
-def _build_calls():
+def _build_calls(force: bool):
+    """Compile the Python extension if its sources, its command, torch or the interpreter have
+    changed.  Returns what went wrong, if anything; there is no extension then, as an older one
+    might not fit the library."""
+    stamp = os.path.join(BUILD, "cache_calls.stamp")
     tmp = CALLS + f".tmp{os.getpid()}"
-    r = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"compile failed: cache_calls.cpp\n{r.stdout}\n{r.stderr}")
+    try:
+        import torch
+        cmd = _calls_command(tmp)
+        h = hashlib.sha256(" ".join([*_calls_command(CALLS), torch.__version__, str(torch.version.git_version),
+                                     sys.version]).encode())
+        for path in (os.path.join(CSRC, "cache_calls.cpp"), os.path.join(INCLUDE, "jfa.h")):
+            with open(path, "rb") as f:
+                h.update(f.read())
+        if not force and os.path.exists(CALLS) and _stamped(stamp, h.hexdigest()):
+            return None
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        error = None if r.returncode == 0 else r.stdout + r.stderr
+    except (ImportError, OSError) as e:  # no torch, or no compiler
+        error = str(e)
+    untagged = os.path.join(PKG, "_cache_calls.so")  # builds once left it under this name
+    for old in (untagged, *([CALLS, stamp] if error else [])):
+        if os.path.exists(old):
+            os.remove(old)
+    if error:
+        return error
     os.replace(tmp, CALLS)
+    with open(stamp, "w") as f:
+        f.write(h.hexdigest())
+    return None
+
+
+def _stamped(path: str, digest: str) -> bool:
+    if not os.path.exists(path):
+        return False
+    with open(path) as f:
+        return f.read().strip() == digest
 
 
 def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
-    """Compile (if sources changed) and return the path of libjfa.so."""
+    """Compile (what has changed) and return the path of libjfa.so."""
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_build_calls, force)
+        _build_library(force, extra_flags, verbose)
+        error = calls.result()
+    if error:
+        warnings.warn("the paged cache's compiled Python calls were not built (jfa.jfa_cache_create will refuse):\n"
+                      + error, RuntimeWarning, stacklevel=2)
+    return LIB
+
+
+def _build_library(force: bool, extra_flags, verbose: bool):
     stamp = os.path.join(BUILD, "libjfa.stamp")
-    dig = _digest(extra_flags) + " ".join(_calls_command(CALLS))
-    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == dig:
-                return LIB
+    dig = _digest(extra_flags)
+    if not force and os.path.exists(LIB) and _stamped(stamp, dig):
+        return
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -97,10 +140,8 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
             raise RuntimeError(f"compile failed: {src}\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_build_calls)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        calls.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, err in results:
@@ -114,7 +155,6 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     with open(stamp, "w") as f:
         f.write(dig)
-    return LIB
 
 
 def build_variant(name: str, defines, sources=("fwd.cu",), verbose: bool = False) -> str:

@@ -65,7 +65,10 @@ def _cache_calls():
     global _calls
     if _calls is None:
         L = lib()
-        from . import _cache_calls as m
+        try:
+            from . import _cache_calls as m
+        except ImportError as e:
+            raise RuntimeError(f"the paged cache's compiled calls are not built ({e}); run __graft_entry__.build()") from None
         m.set_calls(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.jfa_cache_append, L.jfa_cache_fwd)))
         _calls = m
     return _calls
