@@ -2,20 +2,22 @@
 // into three bf16 parts each.
 //
 // x = x0 + x1 + x2 with x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1): both
-// differences are exact in fp32, so the parts hold x to 2^-27 of it.  A product of two split
+// differences are exact in fp32, |x1| <= 2^-8 and |x2| <= 2^-17 of x's power of two, and the
+// three parts hold x exactly (8 + 8 + 7 of its 24 bits and the signs).  A product of two split
 // values keeps
 //   x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0),
-// leaving out terms of 2^-26 and less: each product is as exact as fp32's own rounding.  The
-// tensor core accumulates in fp32, but not with rounding to nearest, so two things keep its
-// sums at fp32's level: the small terms go first, while the accumulator is small, and leave
-// only the x0 y0 steps (4 for a score, 8 for an output) to the full-size accumulator; and the
-// output of each key tile starts from zero and is added to the running one in registers.
+// leaving out x1 y2 + x2 y1 + x2 y2, together at most 2^-24 of the product (two terms of 2^-25):
+// each product is as exact as fp32's own rounding.  The tensor core accumulates in fp32, but not
+// with rounding to nearest, so two things keep its sums at fp32's level: the small terms go first,
+// while the accumulator is small, and leave only the x0 y0 steps (4 for a score, 8 for an output)
+// to the full-size accumulator; and the output of each key tile starts from zero and is added to
+// the running one in registers.
 // Six bf16 products at 16 times and more the rate of the FMA units.  A step of 128 rows x 128
 // keys takes 2.5 us: 2.1 of products (24 + 48 instructions of M = 128, those of P V at the half
 // rate of N = 64), the rest the chain output -> P -> output of a step, as TMEM holds one P and
 // one output.  Measured: 20 sequences of 200-4000 keys, 5 of them prompts of 100-600 tokens (8
-// query, 4 key heads of 64) 75 us, of which this kernel 47, the single tokens' 20 and the merge
-// 8.
+// query, 4 key heads of 64) 75 us, of which this kernel 47 (its 1788 steps over 152 CTAs are 29),
+// the single tokens' 20 and the merge 8.
 //
 // An item is 128 packed rows of one (sequence, key head); a step is 128 keys.  Head dimension
 // 32 runs as 64 with zeros.  CTA = 16 warps, one CTA per SM:

@@ -14,10 +14,11 @@ keys in any tree of fp32 additions stay well inside the rest.  The lse is off by
 scores' error: LSE_TOL = 1e-4.
 FP32_SLACK = 2e-5 for N(0,1) inputs and D <= 64: a score's terms sum to 64 * 0.64 / 8 = 5.1 in
 magnitude; a plain fp32 sum of 64 products, or the tensor core's (products of split operands
-exact to 2^-25, at most 8 roundings of a full-size accumulator, each below 2^-23 of it), is off
-by less than 8 * 2^-23 * 5.1 = 4.9e-6 natural units, so p by 4.9e-6 and its normalised weight by
-twice that; the exponential (2^-22), the split of P and V (2^-25 each), 8 roundings of 2^-23 in a
-tile's output and 2^-24 for each of the tiles added add less than 4e-6.
+exact to 2^-24, so 3e-7 in all, and at most 8 roundings of a full-size accumulator, each below
+2^-23 of it), is off by less than 3e-7 + 8 * 2^-23 * 5.1 = 5.2e-6 natural units, so p by 5.2e-6
+and its normalised weight by twice that; the exponential (2^-22), the products of split P and V
+(2^-24), 8 roundings of 2^-23 in a tile's output and 2^-24 for each of the tiles added add less
+than 4e-6.
 """
 from __future__ import annotations
 
