@@ -199,7 +199,7 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
         return JFA_ERR_INVALID_ARG;
     if (T > 0 && Q && (!row_ok(cache, Q, q_stride, H) || !row_ok(cache, Q_out, qo_stride, H)))
         return JFA_ERR_INVALID_ARG;
-    if (T > 0 && Q == Q_out && q_stride != qo_stride) return JFA_ERR_INVALID_ARG;
+    if (T > 0 && Q && Q == Q_out && q_stride != qo_stride) return JFA_ERR_INVALID_ARG;
     if (!on_device(cache)) return JFA_ERR_PLAN_MISMATCH;
     if (B == 0 || T == 0) return JFA_OK;
     CacheAppendParams p;

@@ -151,3 +151,20 @@ def test_binding_refuses_arrays_of_another_device(jfa, monkeypatch):
         with pytest.raises(jfa.JFAError) as e:
             jfa.jfa_cache_create(K, V)
         assert e.value.status == jfa.JFA_ERR_INVALID_ARG
+
+
+def test_appending_keys_alone_ignores_the_queries_arguments(jfa, fake):
+    c = Calls(fake, BF16, 4)
+
+    def append(Q=None, Q_out=None, H=0, q_stride=0, qo_stride=0, rot=1 << 20):
+        r = fake.jfa_cache_append(c.h, 2, 5, 4096, 4096, 4096, 3, 1 << 18, 256, 1 << 19, 256, Q, q_stride, H, Q_out, qo_stride, rot,
+                                  64, 100, 0, None)
+        return r, fake.fake_log(b"").decode()
+
+    ok, bad = (jfa.JFA_OK, "append"), (jfa.JFA_ERR_INVALID_ARG, "")
+    assert append() == ok and append(rot=None) == ok and append(H=-3) == ok
+    assert append(q_stride=512, qo_stride=3) == ok
+    q = 1 << 21
+    assert append(q, q, 8, 512, 512) == ok and append(q, q + (1 << 16), 8, 512, 1024) == ok
+    assert append(q, q, 8, 512, 1024) == bad and append(q, q, 8, 511, 511) == bad and append(q, None, 8, 512) == bad
+    assert append(q, q, 0, 512, 512) == bad and append(q, q, 8, 512, 512, rot=None) == bad
