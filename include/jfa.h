@@ -468,7 +468,8 @@ jfa_status jfa_cache_device_status(jfa_cache cache, void* stream);
  * Appends the new tokens' keys and values, rotating keys (and queries) by their position.
  *   K, V [T, Hkv, D] and, with a rotation, Q, Q_out [T, H, D] in the cache's dtype: heads
  *   dense, tokens *_stride elements apart (at least the row, a multiple of 16 bytes), so that
- *   slices of one fused projection are taken as they are.  Q_out may be Q itself.
+ *   slices of one fused projection are taken as they are.  Q_out may be Q itself, and
+ *   overlaps nothing else.
  *   rot: NULL (keys stored as given, Q and Q_out must be NULL), or an fp32 table
  *   [rot_len, rot_dim], 16-byte aligned, whose row p holds the rot_dim / 2 cosines and then
  *   the sines of position p.  Of each pair of the first rot_dim elements of a head
@@ -476,7 +477,7 @@ jfa_status jfa_cache_device_status(jfa_cache cache, void* stream);
  *   in fp32, rounded once; the other elements are copied.  rot_dim is a multiple of 16, at
  *   most D.  A position at or past rot_len sets JFA_ERR_DEVICE_BOUNDS and its token is
  *   skipped.
- *   Q may be NULL with a rotation (keys alone); H is then ignored.
+ *   Q may be NULL with a rotation (keys alone); H and the two strides are then ignored.
  *   A sequence with fewer positions than new tokens (kv_len < q_len) is bad, as a whole.
  *   Two tokens must not share a slot (pages shared by sequences are for reading).
  * Errors: INVALID_ARG, PLAN_MISMATCH (another device is current), CUDA.
@@ -502,6 +503,9 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  *   Q [T, H, D] in the cache's dtype (T H at most 2^31 - 257), tokens q_stride elements apart (a
  *   multiple of 16 bytes); O [T, H, D] dense, in o_dtype (JFA_F32, or JFA_BF16 with a bf16 cache);
  *   O must not overlap Q.
+ *   With a bf16 cache each weight of the softmax is rounded to bf16 for its product with the
+ *   values, after their sum has been taken in fp32, as in jfa_fwd: at most 2^-8 of sum_j p_j |v_j|.
+ *   Scores, maxima, sums, partial outputs and lse are fp32.
  *   lse fp32 [T, H], or NULL.  bias_kind JFA_BIAS_NONE or JFA_BIAS_RELPOS32 (fp32 [H, 32]).
  *   scale must be finite and positive, and scores finite (so the bias too: it is no mask).
  *   fp32 is computed at fp32's accuracy, single tokens and short query sets (up to 16 rows of
@@ -521,6 +525,7 @@ size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H);
  *   that may overlap on the GPU need a workspace each: order those that share one.
  *   The result is the same bit for bit on every run of the same call.  There is no backward
  *   pass: a cache is for serving (training keys and values go through jfa_fwd and jfa_bwd).
+ *   Over a cache there is the softmax alone: the GDPA activations take packed keys (jfa_fwd).
  * Errors: INVALID_ARG, UNSUPPORTED (a dense bias, bf16 output of an fp32 cache, more than 128
  *   grouped heads with bf16, or row tiles x key tiles that max_pages and T allow past 2^31),
  *   PLAN_MISMATCH (another device is current), CUDA.  A call refused with one of the first

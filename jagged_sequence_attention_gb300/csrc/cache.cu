@@ -70,7 +70,7 @@ constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 // with 4; 200 sequences of up to 2k keys: 102 with 1, 93 with 2, 95 with 3, 98 with 5).  Beside
 // the chunk kernel, on SMs that come free at different times, less (256 ragged query sets: 248.5
 // us with 3 and with 5, 244 with 2 and with 1).  And the chunk and split kernels, in their steps
-// of 128 keys: 1.8-2.6 us (48 sequences, ten of them prompts: 71 us with 2, 66.5 with 3, 70.5 with
+// of 128 keys: 1.8-2.6 us (48 sequences, nine of them prompts: 71 us with 2, 66.5 with 3, 70.5 with
 // 5) and 2.5 us (20 ragged sequences: 74.4 with 2, 75.6 with 3, 78.4 with 5); the simt kernel, in
 // its steps of 64 keys, the same 2 (64 fp32 single tokens: 109-114 us with 1 to 4, 118 with 6).
 constexpr int kDecodeItemUnits = 3, kDecodeItemUnitsBeside = 2, kSimtItemUnits = 2;

@@ -8,8 +8,9 @@
 // place.  The token's sequence is found by a 32-way search of the offsets (one load deep up to 31
 // sequences, two up to 1023).
 // Measured: 24 prompts of up to 2048 tokens (32 query and 2 x 8 cached heads of 128, bf16, 710 MB)
-// 108 us, 6.5 TB/s, 0.97 of the copy rate; 7 fp32 prompts (60 MB) 13.5 us, 0.65, a few waves
-// whose start and end show; 256 single tokens 3.8 us and one token 3.3 us, the launch and the
+// 108 us, 6.5 TB/s, 0.96 of the copy rate; 7 fp32 prompts (60 MB) 13.5 us, 0.65, a few waves
+// whose start and end show, and a thread loads its next vectors only after it has stored the
+// last; 256 single tokens 3.8 us and one token 3.3 us, the launch and the
 // chain of loads.  Loading a token's data before its sequence is found was slower (108 -> 114 us,
 // fp32 13.5 -> 15.9 us: more live registers, fewer CTAs an SM).
 #include "cache_common.cuh"

@@ -25,10 +25,11 @@
 // adds them up: the last part's CTA alone would read them at one SM's rate (about 2 us a
 // part of 132 KB), and a long history under one chunk has tens of parts.
 // Measured: 8 prompts of 700-1024 tokens (32 query, 8 key heads of 128) over 3k-14k keys, 859
-// GFLOP, 709 us with the merge, 1211 TFLOP/s, 0.64 of the measured matrix-product burst rate.  A
-// step of 256 x 128 scores takes 1.8 us (2.6 with a bias), its products 1.1 and its exponentials
-// as much: what is left is each tile's own chain S -> softmax -> P V -> S, since at head_dim 128
-// TMEM holds no second score tile per row tile.  256 sets of 1-64 rows over 100-8000 keys (8
+// GFLOP, 708 us with the merge, 1213 TFLOP/s, 0.64 of the measured matrix-product burst rate (874 us
+// with a bias).  A step of 256 x 128 scores takes 1.8 us, its products 1.1 and its exponentials 0.5
+// (32 a clock): what is left is each tile's own chain S -> softmax -> P V -> S, since at head_dim
+// 128 TMEM holds no second score tile per row tile.  P is rounded to bf16 for its product, as in
+// the packed forward, after its sum is taken in fp32: 2^-8 of each weight, at most.  256 sets of 1-64 rows over 100-8000 keys (8
 // heads of 64, 947 MB) 243 us, 0.57 of the copy rate: long items stream 128 keys in 0.86 us on
 // each SM (5.7 TB/s in all), an item's end and start cost 3 us more, a single short item 5-8 us
 // from its draw to its stored rows, and the sets of up to 16 rows follow in the decode kernel
@@ -579,8 +580,9 @@ __global__ void __launch_bounds__(608, 1)
                 // Without a bias both chunks' scores are held at a time, with one they are taken one
                 // by one in rolled loops: the three ways of its lookup would otherwise be laid out
                 // four times, and a short item pays for every line of code it fetches.  (A path for
-                // two plain chunks beside it made steps with a bias slower: 67 -> 73 us for prompts
-                // of 200-800 tokens among single ones.)
+                // two plain chunks beside it made steps with a bias slower: 67 -> 73 us for nine prompts
+                // of 200-800 tokens among single ones, short items.  It was not measured on long
+                // prompts, which pay 708 -> 874 us for a bias in this form.)
                 constexpr bool plain = !BIAS;
                 uint32_t sr[2][32];
                 if (plain) {

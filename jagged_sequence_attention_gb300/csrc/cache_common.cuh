@@ -471,8 +471,9 @@ __device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroup
         // The last part, cut in blocks, covers the spread with which the CTAs come out of the
         // whole items: a quarter of an item each (half: more parts to merge, 8 prompts 726 us
         // against 709; an eighth: 5 equal prompts 648 us against 575).  Never none, so that the
-        // unit the blocks start at exists.  Where the longest item is over half a CTA's share,
-        // everything is cut.
+        // unit the blocks start at exists: without one the search below would look for unit `u`,
+        // past the last, and find no lane that holds it.  Where the longest item is over half a
+        // CTA's share, everything is cut.
         const int mean = int(uint32_t(u) / uint32_t(max(items, 1)));
         const int rest = (long long)(longest) * 2 * grid > u ? u : min(u, grid * max(1, (mean + 1) / 4));
         int cut = 0, whole = 0;

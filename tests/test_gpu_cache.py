@@ -649,8 +649,9 @@ def test_output_over_the_queries_is_refused(jfa):
     assert status_of(jfa, jfa.jfa_cache_fwd, cache, c.Q, c.q_off, c.kv_lens, c.table, O=c.Q) == jfa.JFA_ERR_INVALID_ARG
 
 
-# Query sets of at most 64 packed rows at head dimension 64, two key tiles at a time: odd and
-# even numbers of key tiles, a single one, an item cut between CTAs, more rows than keys.
+# Query sets of at most 64 packed rows at head dimension 64, items of one row tile, whose key
+# steps take turns as tile A and tile B: odd and even numbers of steps, a single one, an item cut
+# between CTAs, more rows than keys.
 SETS = ([17, 33, 64, 63, 20, 48, 32, 21, 60], [17, 200, 640, 129, 5000, 257, 0, 20000, 9])
 
 
