@@ -254,7 +254,7 @@ def prepare(c, seed):
         from jagged_sequence_attention_gb300 import jfa
         s["jfa"] = jfa
         if c["bits"] == 4:
-            s["cache"] = jfa.jfa_cache_create_4bit(s["kc"], s["vc"], s["ks"], s["vs"], c["factor"], c["factor"])
+            s["cache"] = jfa.jfa_cache_create_quantized(s["kc"], s["vc"], s["ks"], s["vs"], c["factor"], c["factor"])
         else:
             s["cache"] = jfa.jfa_cache_create(s["kc"], s["vc"])
         if c["op"] in ("attend", "blocks"):
