@@ -7,7 +7,7 @@ selection, the attention).
 calls on the same inputs.  A batch holds B sequences; sequence b has q_len[b] new tokens,
 the last of its kv_len[b] positions.  Position p of sequence b lies in page
 page_table[b, p // page], slot p % page.  A 16-bit cache is bf16 [n_pages, page, Hkv, D].  A
-4-bit cache holds e2m1 codes [n_pages, page, Hkv, D / 2], element 2i in the low half of byte
+4-bit cache holds e2m1 codes [n_pages, page, Hkv, D / 2] (head-major), element 2i in the low half of byte
 i, and an e4m3 scale for each 16 elements [n_pages, Hkv, page, D / 16]; a value is
 factor * scale * code, with one factor for all keys and one for all values.
 """
@@ -200,7 +200,7 @@ def prepare(c, seed):
     for name in ("k", "v") if c["op"] != "select" else ("k",):
         x = normal(n_pages, page, Hkv, D)
         if c["bits"] == 4:
-            codes = torch.empty(n_pages, page, Hkv, D // 2, dtype=torch.uint8, device=dev)
+            codes = torch.empty(n_pages, Hkv, page, D // 2, dtype=torch.uint8, device=dev).transpose(1, 2)
             scales = torch.empty(n_pages, Hkv, page, D // 16, dtype=E4M3, device=dev)
             for i in range(0, n_pages, 4096):  # (a long history in parts: less memory)
                 codes[i:i + 4096], part = quantised(x[i:i + 4096].float(), c["factor"])
