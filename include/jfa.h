@@ -458,6 +458,37 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
                             void* K, void* V, const int64_t* k_strides, const int64_t* v_strides,
                             void* stream, jfa_cache* out);
 
+/*
+ * A cache held in 4 bits: a history of 9 bytes for 16 elements, 3.6 times less than bf16 to keep
+ * and to read.  The handle is used like any other: jfa_cache_append quantises the new rows,
+ * jfa_cache_fwd attends over the values that the cache stands for, and workspaces, status and
+ * destruction are the same calls.  Rows (K, V, Q, O of those calls) are as of a bf16 cache.
+ *   A row of D elements of one (page, slot, head) is D / 2 bytes of e2m1 codes (a sign and 0, 0.5, 1,
+ *   1.5, 2, 3, 4 or 6; element 2i in the low half of byte i) and D / 16 e4m3 scales, one for each 16
+ *   elements; an element is  factor * scale * code,  with one factor for all keys (k_factor) and
+ *   one for all values (v_factor), powers of two or not, in [2^-60, 2^60].  1 suits rows whose
+ *   largest magnitudes lie in 0.02 .. 2688.
+ *   K, V: the codes; k_strides, v_strides: host int64[3] (page, slot, head) in bytes, each at least
+ *   D / 2 and a multiple of 16.  K_scales, V_scales: the scales, a head's page_size * D / 16 bytes of
+ *   one page in one piece (slot by slot); ks_strides, vs_strides: host int64[2] (page, head) in
+ *   bytes, each at least that size and a multiple of 16.  All DEVICE pointers of the current
+ *   device, 16-byte aligned, owned by the caller.  Codes with a head's slots of a page in one piece
+ *   ([n_pages, Hkv, page_size, D / 2]) are read fastest.
+ *   D 64 or 128; Hkv, page_size, n_pages as in jfa_cache_create.
+ * Appending: of each 16 elements y of a row (keys after their rotation, which is not rounded in
+ *   between)  scale = e4m3(max|y| / (6 factor)), at most 448, and code = e2m1(y / (factor scale)), at
+ *   most 6 in magnitude (0 where the scale is 0), both to nearest, ties to the even code, as if
+ *   in exact arithmetic.
+ * Attention: scale * code is exact in the products' types.  jfa_cache_fwd's text on bf16 caches
+ *   holds, with each weight of the softmax rounded to fp16 for its product where a sequence has
+ *   at most 16 rows (new tokens x grouped heads), to bf16 elsewhere.  scale * k_factor must lie in [1e-37, 1e37].
+ * Errors: those of jfa_cache_create.
+ */
+jfa_status jfa_cache_create_quantized(int32_t Hkv, int32_t D, int32_t page_size, int64_t n_pages, void* K, void* V,
+                                      const int64_t* k_strides, const int64_t* v_strides, void* K_scales, void* V_scales,
+                                      const int64_t* ks_strides, const int64_t* vs_strides, float k_factor, float v_factor,
+                                      void* stream, jfa_cache* out);
+
 /* Frees the handle (not K and V).  cudaFree synchronises the device.  NULL is accepted. */
 jfa_status jfa_cache_destroy(jfa_cache cache);
 
@@ -488,6 +519,18 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
                             const void* Q, int64_t q_stride, int32_t H, void* Q_out, int64_t qo_stride,
                             const float* rot, int32_t rot_dim, int64_t rot_len, int32_t rot_kind,
                             void* stream);
+
+/*
+ * The rows that jfa_cache_append wrote for the same arrays, as the cache holds them (a cache of any
+ * type): row t of K and V [T, Hkv, D], in the type of the cache's rows, is the position of new token
+ * t.  With kv_lens for lengths of new tokens (q_offsets their sums) these are whole histories.  Of a
+ * 4-bit cache, factor * scale * code is rounded to bf16.  Strides, bad sequences and pages as in
+ * jfa_cache_append (their rows are left alone); K and V overlap neither each other nor the cache.
+ * Errors: INVALID_ARG, PLAN_MISMATCH (another device is current), CUDA.
+ */
+jfa_status jfa_cache_read(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
+                          const int32_t* page_table, int32_t max_pages, void* K, int64_t k_stride, void* V, int64_t v_stride,
+                          void* stream);
 
 /* Bytes of device workspace jfa_cache_fwd needs, for any batch with H query heads (0: bad
  * arguments). */
@@ -537,6 +580,63 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
                          const void* Q, int64_t q_stride, int32_t H, int32_t causal, int32_t window,
                          int32_t bias_kind, const float* bias_table, float scale, void* O, int32_t o_dtype,
                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention over selected blocks: a long history is read in part, and every new token chooses
+ * which part for each key head.  A block is a page (block k of a sequence is its positions
+ * k * page_size on).  A step of a served batch is four calls on the same arrays:
+ *   jfa_cache_append      as before;
+ *   jfa_cache_summarize   brings the bounds of the pages that got new tokens up to date;
+ *   jfa_cache_select      chooses blocks by a score from the bounds alone;
+ *   jfa_cache_fwd_blocks  attends over the chosen blocks.
+ * For bf16 and 4-bit caches with pages of at least 16 positions (UNSUPPORTED otherwise).  Bad sequences,
+ * lengths and pages are reported as in the calls above.  Attention is causal, without a window.
+ *
+ * Bounds: bf16 [n_pages, Hkv, 2, D], 16-byte aligned, the caller's: the least and the largest of each
+ * element over the keys of a page (of a 4-bit cache scale * code, without the factor).  Summarize
+ * takes a page's positions below kv_len, all of them anew, so that a page that was given to another
+ * sequence needs nothing else.  Bounds of other pages are left alone.
+ */
+jfa_status jfa_cache_summarize(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
+                               const int32_t* page_table, int32_t max_pages, void* bounds, void* stream);
+
+/* Bytes of device workspace jfa_cache_select needs (0: bad arguments); it needs no initialisation. */
+size_t jfa_cache_select_workspace_size(jfa_cache cache, int64_t T, int32_t max_pages);
+
+/*
+ * blocks [T, Hkv, n_blocks] int32, for new token i of sequence b at position i' = i + kv_len - q_len
+ * and each key head: n_blocks of the blocks 0 .. c, c = i' / page_size its own, ascending.  If there
+ * are no more than n_blocks, all of them and then -1.  Otherwise the first n_first, the last n_last (c
+ * among them), and of the others those of the highest score
+ *   sum_{h in the key head's group} sum_d max(q_hd lo_d, q_hd hi_d),
+ * an upper bound of what the group's scores with a key of the block can sum to; of equal scores the lower index.
+ * Scores are compared as in 64-bit arithmetic.  Bounds of blocks 0 .. c - 1 are read where they
+ * decide, and must be finite.  Rows that belong to no sequence are left alone.
+ *   Q [T, H, D] as in jfa_cache_fwd (with the rotation); max_q_len: an upper bound of the batch's
+ *   q_len, or 0; it only chooses among kernels.
+ *   n_last >= 1, n_first >= 0, n_first + n_last <= n_blocks, n_blocks * page_size <= 2^30.
+ *   workspace: at least jfa_cache_select_workspace_size bytes, 256-byte aligned; calls that may
+ *   overlap on the GPU need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED (the cache; more than 128 grouped heads), PLAN_MISMATCH, CUDA.
+ */
+jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
+                            const int32_t* kv_lens, const int32_t* page_table, int32_t max_pages, const void* bounds,
+                            const void* Q, int64_t q_stride, int32_t H, int32_t n_blocks, int32_t n_first, int32_t n_last,
+                            int32_t* blocks, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * jfa_cache_fwd (causal) with the keys of row i of key head hk limited to the blocks listed for it in
+ * blocks [T, Hkv, n_blocks]: indices that ascend strictly, then -1.  Listed positions after i' are
+ * not seen, so a list may name the token's own block and later ones.  An entry that does not ascend, or
+ * follows a -1, is left out where it is met, and sets JFA_ERR_DEVICE_BOUNDS.  At most 16 grouped
+ * heads.  Workspace (jfa_cache_workspace_size), outputs, bias, rounding and empty rows are as in
+ * jfa_cache_fwd; the result is the same bit for bit on every run.
+ * Errors: those of jfa_cache_fwd; UNSUPPORTED also for the cache and for more than 16 grouped heads.
+ */
+jfa_status jfa_cache_fwd_blocks(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
+                                const int32_t* page_table, int32_t max_pages, const void* Q, int64_t q_stride, int32_t H,
+                                const int32_t* blocks, int32_t n_blocks, int32_t bias_kind, const float* bias_table, float scale,
+                                void* O, int32_t o_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

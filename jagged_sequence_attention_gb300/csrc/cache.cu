@@ -1,42 +1,12 @@
 // C-ABI of the paged key/value cache: argument checks, the handle, and kernel launches.
 // Semantics of every entry point are documented in include/jfa.h.
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
-#include <algorithm>
-#include <cmath>
-#include <cstdint>
 #include <new>
 
-#include "cache_common.cuh"
+#include "cache_handle.h"
 
 using namespace jfa;
 
-struct jfa_cache_t {
-    int32_t dtype, Hkv, D, page_log2, n_pages;
-    void* K;
-    void* V;
-    int64_t ks[3], vs[3];
-    int device, num_sms;
-    int* d_status;
-    CUtensorMap mk, mv;  // the pages as (D, slot, head, page), boxes of one page's keys (at most 64)
-};
-
 namespace {
-
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline size_t elem(int dtype) { return dtype == JFA_F32 ? 4 : 2; }
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-    static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f
-                                                                                                             : nullptr);
-    }();
-    return enc;
-}
 
 // A tensor of `rank` dimensions (the first dense, strides of the others in elements), its boxes
 // 128 bytes of the first, with 128-byte swizzle.
@@ -63,41 +33,6 @@ jfa_status make_page_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
     return make_map(map, c->dtype, base, 4, dims, strides, box);
 }
 
-constexpr size_t kCutBytes = size_t(kMaxSms) * kBlocksPerCta * sizeof(CacheCut);
-constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
-// What an item's start and end cost the decode kernel, in its stages of 32 KB: about 4 us of a
-// CTA, at its share of the memory's rate (one history of 131k keys: 100.5 us with 2, 97 with 3, 96
-// with 4; 200 sequences of up to 2k keys: 102 with 1, 93 with 2, 95 with 3, 98 with 5).  Beside
-// the chunk kernel, on SMs that come free at different times, less (256 ragged query sets: 248.5
-// us with 3 and with 5, 244 with 2 and with 1).  And the chunk and split kernels, in their steps
-// of 128 keys: 1.8-2.6 us (48 sequences, nine of them prompts: 71 us with 2, 66.5 with 3, 70.5 with
-// 5) and 2.5 us (20 ragged sequences: 74.4 with 2, 75.6 with 3, 78.4 with 5); the simt kernel, in
-// its steps of 64 keys, the same 2 (64 fp32 single tokens: 109-114 us with 1 to 4, 118 with 6).
-constexpr int kDecodeItemUnits = 3, kDecodeItemUnitsBeside = 2, kSimtItemUnits = 2;
-constexpr int kChunkItemUnits = 3;
-constexpr int kSplitItemUnits = 2;
-
-// Whether the cache's device is the current one.
-bool on_device(jfa_cache c) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
-}
-
-// Checks of the arrays both calls take; max_kv: the longest sequence they can address.
-jfa_status check_batch(jfa_cache c, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
-                       const int32_t* page_table, int32_t max_pages, int32_t* max_kv) {
-    if (!c || B < 0 || B > kCacheMaxB || T < 0 || T > (1 << 30) || max_pages < 0) return JFA_ERR_INVALID_ARG;
-    if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4)) return JFA_ERR_INVALID_ARG;
-    if (B > 0 && (!q_offsets || !kv_lens || (max_pages > 0 && !page_table))) return JFA_ERR_INVALID_ARG;
-    *max_kv = int32_t(std::min<int64_t>(int64_t(max_pages) << c->page_log2, INT32_MAX - T - 1024));
-    return JFA_OK;
-}
-
-// [T, heads, D] rows `stride` elements apart.
-bool row_ok(jfa_cache c, const void* p, int64_t stride, int32_t heads) {
-    return p && aligned(p, 16) && stride >= int64_t(heads) * c->D && (size_t(stride) * elem(c->dtype)) % 16 == 0;
-}
-
 }  // namespace
 
 extern "C" {
@@ -115,25 +50,11 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
     for (int i = 0; i < 3; ++i)
         for (const int64_t s : {k_strides[i], v_strides[i]})
             if (s < D || s > (int64_t(1) << 38) || (size_t(s) * elem(dtype)) % 16 != 0) return JFA_ERR_INVALID_ARG;
-    int dev = 0;
-    cudaDeviceProp prop;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaGetDeviceProperties(&prop, dev) != cudaSuccess || prop.major != 10 ||
-        prop.multiProcessorCount > kMaxSms)
-        return JFA_ERR_NO_DEVICE;
-    // (an address that CUDA does not know, or memory of no one device, is the caller's matter)
-    for (const void* a : {K, V}) {
-        cudaPointerAttributes at;
-        if (cudaPointerGetAttributes(&at, a) != cudaSuccess)
-            (void)cudaGetLastError();
-        else if (at.type == cudaMemoryTypeDevice && at.device != dev)
-            return JFA_ERR_INVALID_ARG;
-    }
     jfa_cache_t* c = new (std::nothrow) jfa_cache_t();
     if (!c) return JFA_ERR_CUDA;
     c->dtype = dtype;
     c->Hkv = Hkv;
     c->D = D;
-    c->page_log2 = 0;
     while ((1 << c->page_log2) < page_size) ++c->page_log2;
     c->n_pages = int32_t(n_pages);
     c->K = K;
@@ -142,24 +63,15 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
         c->ks[i] = k_strides[i];
         c->vs[i] = v_strides[i];
     }
-    c->device = dev;
-    c->num_sms = prop.multiProcessorCount;
-    {
-        const int rows = std::min(64, page_size);
-        if (make_page_map(&c->mk, K, c, c->ks, rows) != JFA_OK || make_page_map(&c->mv, V, c, c->vs, rows) != JFA_OK) {
-            delete c;
-            return JFA_ERR_CUDA;
-        }
-    }
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cudaMalloc(reinterpret_cast<void**>(&c->d_status), 256) != cudaSuccess) {
+    const void* arrays[2] = {K, V};
+    jfa_status s = check_new(c, arrays, 2);
+    const int rows = std::min(64, page_size);
+    if (s == JFA_OK) s = make_page_map(&c->mk, K, c, c->ks, rows);
+    if (s == JFA_OK) s = make_page_map(&c->mv, V, c, c->vs, rows);
+    if (s == JFA_OK) s = make_status(c, stream);
+    if (s != JFA_OK) {
         delete c;
-        return JFA_ERR_CUDA;
-    }
-    if (cudaMemsetAsync(c->d_status, 0, 256, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) {
-        cudaFree(c->d_status);
-        delete c;
-        return JFA_ERR_CUDA;
+        return s;
     }
     *out = c;
     return JFA_OK;
@@ -234,14 +146,18 @@ jfa_status jfa_cache_append(jfa_cache cache, int32_t B, int64_t T, const int32_t
     p.rot_len = int(std::min<int64_t>(rot_len, INT32_MAX));
     p.pairs = rot_kind == JFA_ROT_PAIRS;
     p.status = cache->d_status;
-    return launch_cache_append(cache->dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache->ops ? cache->ops->append(cache, p, st) : launch_cache_append(cache->dtype, p, st);
+    return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 size_t jfa_cache_workspace_size(jfa_cache cache, int32_t H) {
     if (!cache || H < 1 || H > 65535 || H % cache->Hkv != 0) return 0;
     const int D = cache->D, n = cache->num_sms;
-    return JFA_CACHE_ZERO_BYTES + kCutBytes + (cache->dtype == JFA_F32 ? cache_simt_part_bytes(D, n) + cache_split_part_bytes(D, n)
-                                                           : cache_decode_part_bytes(D, n) + cache_chunk_part_bytes(D, n));
+    if (cache->dtype == JFA_F32)
+        return JFA_CACHE_ZERO_BYTES + kCutBytes + cache_simt_part_bytes(D, n) + cache_split_part_bytes(D, n);
+    return JFA_CACHE_ZERO_BYTES + kCutBytes + cache_chunk_part_bytes(D, n) +
+           std::max(cache_decode_part_bytes(D, n), cache->ops ? cache->ops->decode_part_bytes(D, n) : 0);
 }
 
 jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
@@ -259,6 +175,8 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         return bias_kind == JFA_BIAS_DENSE ? JFA_ERR_UNSUPPORTED : JFA_ERR_INVALID_ARG;
     if (bias_kind == JFA_BIAS_RELPOS32 && (!bias_table || !aligned(bias_table, 4))) return JFA_ERR_INVALID_ARG;
     if (!(scale > 0.f && scale < INFINITY)) return JFA_ERR_INVALID_ARG;
+    // (the keys' factor goes into the scores' scale, which has to stay a normal number)
+    if (cache->ops && !(scale * cache->k_factor >= 1e-37f && scale * cache->k_factor <= 1e37f)) return JFA_ERR_INVALID_ARG;
     if (o_dtype != JFA_BF16 && o_dtype != JFA_F32) return JFA_ERR_INVALID_ARG;
     if (cache->dtype == JFA_F32 && o_dtype != JFA_F32) return JFA_ERR_UNSUPPORTED;
     if (T > 0 && (!row_ok(cache, Q, q_stride, H) || !O || O == Q || !aligned(O, 16) || !aligned(lse, 4))) return JFA_ERR_INVALID_ARG;
@@ -266,48 +184,16 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         return JFA_ERR_INVALID_ARG;
     if (!on_device(cache)) return JFA_ERR_PLAN_MISMATCH;
     if (B == 0 || T == 0) return JFA_OK;
-    CacheFwdParams p;
-    p.q_off = q_offsets;
-    p.kv_lens = kv_lens;
-    p.table = page_table;
-    p.B = B;
-    p.max_pages = max_pages;
-    p.T = int(T);
-    p.max_kv = max_kv;
-    p.H = H;
-    p.Hkv = cache->Hkv;
-    p.g = H / cache->Hkv;
-    set_div_g(p);
-    p.page_log2 = cache->page_log2;
-    p.n_pages = cache->n_pages;
-    p.causal = causal;
-    p.window = window < max_kv ? window : -1;  // a window of every position is none
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.bias = bias_kind == JFA_BIAS_RELPOS32 ? bias_table : nullptr;
-    p.Q = Q;
-    p.q_stride = q_stride;
-    p.O = O;
-    p.o_f32 = o_dtype == JFA_F32;
-    p.lse = lse;
-    p.K = cache->K;
-    p.V = cache->V;
-    for (int i = 0; i < 3; ++i) {
-        p.ks[i] = cache->ks[i];
-        p.vs[i] = cache->vs[i];
-    }
-    p.counters = static_cast<uint32_t*>(workspace);
-    p.cut_flags = p.counters + kCtrCuts;
-    p.cuts = reinterpret_cast<CacheCut*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + JFA_CACHE_ZERO_BYTES + kCutBytes);
-    p.status = cache->d_status;
-    p.row_lo = 0;
-    p.row_hi = INT32_MAX;
+    CacheFwdParams p{};
+    fwd_params(p, cache, B, T, q_offsets, kv_lens, page_table, max_pages, max_kv, Q, q_stride, H, causal, window,
+               bias_kind == JFA_BIAS_RELPOS32 ? bias_table : nullptr, scale, O, o_dtype, lse, workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Sequences of at most kDecodeRows packed rows run in the decode kernel, the others in the
     // chunk kernel; which there are is known on the device only, beyond max_q_len.
     const int n = cache->num_sms, D = cache->D;
     const bool bf16 = cache->dtype == JFA_BF16;
-    const bool chunks = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g > kDecodeRows;
+    const int64_t most_rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
+    const bool chunks = most_rows > kDecodeRows && (!cache->ops || cache->ops->chunk);
     // the kernels count units in 31 bits; tiles(): the row tiles of bm rows that `rows` rows have at most
     auto tiles = [&](int64_t rows, int bm) { return rows / bm + B; };
     auto fits = [&](int64_t n_tiles, int bn) {
@@ -331,6 +217,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         p.row_hi = kDecodeRows;
     }
     p.bm = bf16 || p.g > 4 ? 16 : 4;
+    if (cache->ops && most_rows <= 8) p.bm = 8;
     p.min_units = 1;
     p.item_cost = !bf16 ? kSimtItemUnits : chunks ? kDecodeItemUnitsBeside : kDecodeItemUnits;
     if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g, p.bm), 64)) return JFA_ERR_UNSUPPORTED;
@@ -344,10 +231,15 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
         if (ms != JFA_OK) return ms;
     }
     cudaError_t e = cudaSuccess;
-    if (chunks)
-        e = bf16 ? launch_cache_chunk(D, mq, cache->mk, cache->mv, pc, n, st) : launch_cache_split(D, cache->mk, cache->mv, pc, n, st);
-    if (e == cudaSuccess)
-        e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, p, chunks, n, st);
+    if (cache->ops) {
+        if (chunks) e = cache->ops->chunk(cache, mq, pc, st);
+        if (e == cudaSuccess) e = cache->ops->decode(cache, p, chunks, st);
+    } else {
+        if (chunks)
+            e = bf16 ? launch_cache_chunk(D, mq, cache->mk, cache->mv, pc, n, st) : launch_cache_split(D, cache->mk, cache->mv, pc, n, st);
+        if (e == cudaSuccess)
+            e = bf16 ? launch_cache_decode(D, cache->mk, cache->mv, p, chunks, n, st) : launch_cache_simt(D, p, chunks, n, st);
+    }
     if (chunks) {
         // The chunk kernel's flags of cut items are the merge's to clear, so it follows whatever
         // failed before it; where it fails itself they are cleared here.

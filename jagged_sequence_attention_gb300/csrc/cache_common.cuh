@@ -68,6 +68,12 @@ struct CacheFwdParams {
     int row_lo, row_hi;      // sequences this launch works on: row_lo < q_len * g <= row_hi
     int bm;                  // packed rows of an item
     int tile_tokens;         // chunk kernel: tokens of one of an item's two tiles
+    float o_mul;             // factor of O (1, or the values' factor of a 4-bit cache)
+    const uint8_t* k_scales; // a 4-bit cache's scales, and their page and head strides in bytes
+    const uint8_t* v_scales;
+    int64_t kss[2], vss[2];
+    const int32_t* lists;    // [T, Hkv, n_list] blocks (pages) of a token and key head, or nullptr
+    int n_list;
 };
 
 struct CacheSeq {
@@ -96,14 +102,23 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheFwdParams& p, int b, bo
 }
 
 // Keys [lo, hi) that some row of the row tile may see, and the key tiles [f, f + n) they lie in.
+// LIST: attention over listed blocks.  A row tile is then a token's rows (p.bm = g), and the keys
+// are the positions of its list's blocks, one block after the other.
 struct CacheRange {
     int lo, hi, f, n;
 };
-template <int BN>
+template <int BN, bool LIST = false>
 __device__ __forceinline__ CacheRange cache_range(const CacheFwdParams& p, const CacheSeq& s, int tile, int bm) {
     const int r0 = tile * bm, r1 = min(s.q_len * p.g, r0 + bm) - 1;
     const int diag = s.kv_len - s.q_len;
     CacheRange k;
+    if constexpr (LIST) {
+        // a token's blocks ascend, so those from its own block's number on lie past it
+        k.lo = k.f = 0;
+        k.hi = min(p.n_list, ((max(tile + diag, -1) + (1 << p.page_log2)) >> p.page_log2)) << p.page_log2;
+        k.n = (k.hi + BN - 1) / BN;
+        return k;
+    }
     k.hi = p.causal ? max(0, min(s.kv_len, div_g(p, r1) + diag + 1)) : s.kv_len;
     k.lo = p.window >= 0 ? max(0, div_g(p, r0) + diag - p.window) : 0;
     k.f = k.lo / BN;
@@ -111,9 +126,9 @@ __device__ __forceinline__ CacheRange cache_range(const CacheFwdParams& p, const
     return k;
 }
 
-template <int BN>
+template <int BN, bool LIST = false>
 __device__ __forceinline__ CacheRange cache_range(const CacheFwdParams& p, const CacheSeq& s, int tile) {
-    return cache_range<BN>(p, s, tile, p.bm);
+    return cache_range<BN, LIST>(p, s, tile, p.bm);
 }
 
 __device__ __forceinline__ int cache_tiles(const CacheFwdParams& p, const CacheSeq& s) {
@@ -122,9 +137,9 @@ __device__ __forceinline__ int cache_tiles(const CacheFwdParams& p, const CacheS
 
 // Units of an item: its key tiles, and p.item_cost more that stand for its start and end, so
 // that equal ranges of units take equal times.  (Unit counts fit 31 bits: cache.cu checks.)
-template <int BN>
+template <int BN, bool LIST = false>
 __device__ __forceinline__ int cache_units(const CacheFwdParams& p, const CacheSeq& s, int tile) {
-    return max(1, cache_range<BN>(p, s, tile).n) + p.item_cost;
+    return max(1, cache_range<BN, LIST>(p, s, tile).n) + p.item_cost;
 }
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
@@ -147,13 +162,13 @@ __device__ __forceinline__ int cache_sum(int v) { return cache_sum(uint32_t(v), 
 
 // Units of one key head of a lane's sequence, by the whole warp: a lane counts the tiles of
 // its own short sequence, and the warp together those of a long one.
-template <int BN>
+template <int BN, bool LIST = false>
 __device__ __forceinline__ int cache_seq_units(const CacheFwdParams& p, const CacheSeq& s, int lane) {
     const int nt = cache_tiles(p, s);
     int u = 0;
     const bool heavy = nt > 32;
     if (!heavy)
-        for (int t = 0; t < nt; ++t) u += cache_units<BN>(p, s, t);
+        for (int t = 0; t < nt; ++t) u += cache_units<BN, LIST>(p, s, t);
     uint32_t todo = __ballot_sync(0xffffffffu, heavy);
     while (todo) {
         const int l = __ffs(todo) - 1;
@@ -161,7 +176,7 @@ __device__ __forceinline__ int cache_seq_units(const CacheFwdParams& p, const Ca
         const CacheSeq h{0, __shfl_sync(0xffffffffu, s.q_len, l), __shfl_sync(0xffffffffu, s.kv_len, l)};
         const int hn = cache_tiles(p, h);
         int v = 0;
-        for (int t = lane; t < hn; t += 32) v += cache_units<BN>(p, h, t);
+        for (int t = lane; t < hn; t += 32) v += cache_units<BN, LIST>(p, h, t);
         v = __reduce_add_sync(0xffffffffu, v);
         if (lane == l) u = v;
     }
@@ -183,6 +198,20 @@ __device__ __forceinline__ CacheSeq cache_lane_seq(const CacheFwdParams& p, int 
     return s;
 }
 
+// Entry e of a token's list: its block, -1 if there is none to read.  Entries ascend and end with
+// -1 (each is compared with the one before it alone); blocks past the token's own hold no key
+// that it may see.
+__device__ __forceinline__ int cache_list_block(const int32_t* list, int e, int own_block, int* status) {
+    const int block = list[e], before = e > 0 ? list[e - 1] : -1;
+    if (block < 0) return -1;
+    if (e > 0 && (before < 0 || block <= before)) {
+        atomicOr(status, kStatusBounds);
+        return -1;
+    }
+    return block <= own_block ? block : -1;
+}
+constexpr int kNoBlock = 1 << 30;  // the position of keys of no block, past every row's
+
 // Where a CTA's range of units starts, and how the ranges are cut.
 struct CacheStart {
     int b, hk, tile, kt;
@@ -193,7 +222,7 @@ struct CacheStart {
 
 // The item of the `left`-th unit (one that they have) of the sequences that a warp's lanes hold
 // (s: a lane's sequence 32 c + lane, one: its units per key head), into b, hk, tile and kt of `st`.
-template <int BN>
+template <int BN, bool LIST = false>
 __device__ __forceinline__ void cache_locate(const CacheFwdParams& p, int c, const CacheSeq& s, int one, int left, int lane,
                                              CacheStart& st) {
     const int inc = warp_scan(one * p.Hkv, lane);
@@ -211,7 +240,7 @@ __device__ __forceinline__ void cache_locate(const CacheFwdParams& p, int c, con
     st.kt = left;
     if (nt == 1) return;
     for (int t0 = 0; t0 < nt; t0 += 32) {
-        const int n = t0 + lane < nt ? cache_units<BN>(p, q, t0 + lane) : 0;
+        const int n = t0 + lane < nt ? cache_units<BN, LIST>(p, q, t0 + lane) : 0;
         const int in = warp_scan(n, lane);
         const uint32_t m = __ballot_sync(0xffffffffu, in > left);
         if (m) {
@@ -244,21 +273,21 @@ __device__ __forceinline__ void cache_cut(const CacheFwdParams& p, int total, Ca
 // This CTA's range, by every thread of the CTA; each warp gets it in registers.  sums: shared
 // scratch of ceil(B / 32) values (unused up to 32 sequences, which every warp looks over
 // itself); the caller synchronises before it is used for anything else.
-template <int BN>
+template <int BN, bool LIST = false>
 __device__ __forceinline__ CacheStart cache_start(const CacheFwdParams& p, int* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int groups = (p.B + 31) >> 5;
     CacheStart st;
     if (groups <= 1) {
         const CacheSeq s = cache_lane_seq(p, 0, lane, blockIdx.x == 0 && warp == 0);
-        const int one = cache_seq_units<BN>(p, s, lane);
+        const int one = cache_seq_units<BN, LIST>(p, s, lane);
         cache_cut(p, cache_sum(one * p.Hkv), st);
-        if (st.u < st.u_end) cache_locate<BN>(p, 0, s, one, st.u, lane, st);
+        if (st.u < st.u_end) cache_locate<BN, LIST>(p, 0, s, one, st.u, lane, st);
         return st;
     }
     for (int c = warp; c < groups; c += warps) {
         const CacheSeq s = cache_lane_seq(p, c, lane, blockIdx.x == 0);
-        const int v = cache_sum(cache_seq_units<BN>(p, s, lane) * p.Hkv);
+        const int v = cache_sum(cache_seq_units<BN, LIST>(p, s, lane) * p.Hkv);
         if (lane == 0) sums[c] = v < 0 ? INT_MAX : v;
     }
     __syncthreads();
@@ -284,7 +313,7 @@ __device__ __forceinline__ CacheStart cache_start(const CacheFwdParams& p, int* 
             left -= __shfl_sync(0xffffffffu, inc, 31);
         }
         const CacheSeq s = cache_lane_seq(p, c, lane, false);
-        cache_locate<BN>(p, c, s, cache_seq_units<BN>(p, s, lane), left, lane, st);
+        cache_locate<BN, LIST>(p, c, s, cache_seq_units<BN, LIST>(p, s, lane), left, lane, st);
     }
     return st;
 }
@@ -302,7 +331,7 @@ struct CacheSeg {
 
 // Walks a range of units, sequences in the batch's order or a given one (st.b then counts
 // places in that order).  Every role of a CTA walks its own copy.
-template <int BN>
+template <int BN, bool LIST = false>
 struct CacheCursor {
     CacheStart st;
     CacheSeq s;
@@ -323,7 +352,7 @@ struct CacheCursor {
             g.hk = st.hk;
             g.tile = st.tile;
             g.s = s;
-            g.r = cache_range<BN>(p, s, st.tile);
+            g.r = cache_range<BN, LIST>(p, s, st.tile);
             g.n = max(1, g.r.n);
             // the units before the first key tile are the item's cost
             const int v1 = min(g.n + p.item_cost, st.kt + (st.u_end - st.u));
@@ -552,6 +581,9 @@ size_t cache_simt_part_bytes(int D, int num_sms);
 cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early,
                                 int num_sms, cudaStream_t st);
 size_t cache_decode_part_bytes(int D, int num_sms);
+// The same over the blocks of p.lists, a token (p.bm = g rows) at a time.
+cudaError_t launch_cache_decode_lists(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                                      cudaStream_t st);
 // bf16, items of 256 packed rows: bound by the tensor cores and the exponentials.
 // mq: the queries as (D, head, token), boxes of 128 bytes x g heads x tile_tokens.
 cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,

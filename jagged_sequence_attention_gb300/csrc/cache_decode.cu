@@ -42,7 +42,9 @@ struct DecCfg {
     static constexpr int kOffBias = kOffML + 2 * 2 * kDecWarps * 16 * 4;  // [row][32 buckets + 1], log2 units
     static constexpr int kOffBar = kOffBias + 16 * 33 * 4;
     static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
-    static constexpr int kBytes = kOffMisc + 16 + int(sizeof(CacheStart)) + 1024;
+    static constexpr int kOffBase = (kOffMisc + 16 + int(sizeof(CacheStart)) + 15) / 16 * 16;  // lists: position of each box
+    static constexpr int kBoxes = BN / 16;
+    static constexpr int kBytes = kOffBase + kStages * kBoxes * 4 + 1024;
     static_assert(kDecCtasPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
     static constexpr int kPart = kDecBM * (D + 2);           // floats of a partial result: O, m, l
 };
@@ -68,7 +70,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecWarps) : "memory"); }
 
-template <int D, bool BIAS>
+template <int D, bool BIAS, bool LIST>
 __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     jfa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const CacheFwdParams p) {
@@ -94,10 +96,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         tma_prefetch_desc(&tmV);
     }
     CacheStart* start = reinterpret_cast<CacheStart*>(smem + C::kOffMisc + 16);
-    CacheCursor<BN> cur(p, cache_start<BN>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
+    CacheCursor<BN, LIST> cur(p, cache_start<BN, LIST>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
     if (threadIdx.x == 0) *start = cur.st;
     __syncthreads();
     CacheSeg g;
+    int* bases = reinterpret_cast<int*>(smem + C::kOffBase);  // [stage][box]
 
     if (warp == kDecWarps) {
         // ---------------------------------------------------------------- producer
@@ -114,10 +117,22 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         int kt = g.k0;
         // A stage's page: -1 outside the item's keys (not loaded); past the cache (read as
         // zeros) for a bad entry.
+        int base = 0;  // lists: the position of the stage's first key in this lane's box
         auto page_of = [&](const CacheSeg& s, int k) -> int {
             const int j = (s.r.f + k) * BN + pg * rows;
+            int block = j >> p.page_log2;
+            if constexpr (LIST) {
+                base = kNoBlock;
+                if (!mine || j >= s.r.hi) return -1;
+                const int at = s.s.kv_len - s.s.q_len + s.tile;  // the token's position
+                block = cache_list_block(p.lists + (size_t(s.s.q0 + s.tile) * size_t(p.Hkv) + size_t(s.hk)) * size_t(p.n_list), block,
+                                         at >> p.page_log2, p.status);
+                if (block < 0) return -1;
+                base = (block << p.page_log2) + (j & ((1 << p.page_log2) - 1));
+                if (base > at) return -1;
+            }
             if (!mine || j >= s.r.hi || j + rows <= s.r.lo) return -1;
-            const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+            const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(block)];
             if (page >= 0 && page < p.n_pages) return page;
             atomicOr(p.status, kStatusBounds);
             return p.n_pages;
@@ -125,7 +140,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         while (have && (g.r.n == 0)) have = cur.next(p, g), kt = g.k0;
         int page = have ? page_of(g, kt) : -1;
         while (have) {
-            const int at = page, j0 = (g.r.f + kt) * BN + pg * rows, hk = g.hk;
+            const int at = page, j0 = (g.r.f + kt) * BN + pg * rows, hk = g.hk, base0 = base;
             if (++kt >= g.k1) {
                 do {
                     have = cur.next(p, g);
@@ -139,6 +154,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 break;
             }
             const int n = __popc(__ballot_sync(0xffffffffu, at >= 0));
+            if constexpr (LIST) {
+                if (lane < per) bases[st * C::kBoxes + pg] = at >= 0 ? base0 : kNoBlock;
+                __syncwarp();
+            }
             if (lane == 0) mbar_arrive_expect_tx(full(st), uint32_t(n * rows * 128));
             __syncwarp();
             if (at >= 0)
@@ -165,8 +184,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     const int krow = 16 * KG * warp + (lane & 7) + ((lane >> 4) << 3), kpc = (lane >> 3) & 1;
     const int vrow = 16 * KG * warp + (lane & 7) + (((lane >> 3) & 1) << 3), vpc = lane >> 4;
     while (cur.next(p, g)) {
-        const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * BM;
-        const int nr = min(BM, R - r0);
+        const int bm = LIST ? p.bm : BM;
+        const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * bm;
+        const int nr = min(bm, R - r0);
         const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.Q);
         // this lane's rows qrow and qrow + 8: queries, limits, heads
         uint32_t qa[D / 16][4];
@@ -218,8 +238,34 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             const int w0 = (g.r.f + kt) * BN + 16 * KG * warp;  // this warp's keys [w0, w0 + 16 KG)
             const uint32_t sK = sbase + st * C::kStage, sV = sK + C::kCB * C::kBlock;
             // Values that no row may see are undefined, and 0 * NaN is not 0: clear them.
-            const bool edge = w0 < g.r.lo || w0 + 16 * KG > g.r.hi;
-            if (edge) {
+            bool edge = w0 < g.r.lo || w0 + 16 * KG > g.r.hi;
+            int at16[KG];  // lists: the positions of each 16 keys
+            if constexpr (LIST) {
+                const int brows = min(1 << p.page_log2, 64);
+                edge = false;
+                bool none = true;
+#pragma unroll
+                for (int q = 0; q < KG; ++q) {
+                    const int c = 16 * (KG * warp + q);
+                    at16[q] = bases[st * C::kBoxes + c / brows] + (c & (brows - 1));
+                    edge = edge || at16[q] + 16 > all_hi;
+                    none = none && at16[q] >= all_hi;
+                }
+                if (none) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty(st));
+                    continue;
+                }
+                if (edge) {
+                    for (int e = lane; e < 16 * KG * C::kCB * 8; e += 32) {
+                        const int row = e / (C::kCB * 8), c = e % (C::kCB * 8);
+                        if (at16[KG == 2 ? row >> 4 : 0] + (row & 15) >= all_hi)
+                            st_shared_v4(sV + uint32_t((c >> 3) * C::kBlock + (16 * KG * warp + row) * 128 + (c & 7) * 16), 0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!LIST && edge) {
                 for (int e = lane; e < 16 * KG * C::kCB * 8; e += 32) {
                     const int row = e / (C::kCB * 8), c = e % (C::kCB * 8), j = w0 + row;
                     if (j < g.r.lo || j >= g.r.hi)
@@ -242,7 +288,24 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                     mma16816(s[2 * q + 1], qa[k], b[2], b[3]);
                 }
             // scores of rows qrow (i = 0) and qrow + 8 (i = 1) at keys w0 + 8 n + 2 quad + e
-            if (BIAS) {
+            if constexpr (LIST) {
+#pragma unroll
+                for (int q = 0; q < KG; ++q) {
+                    const int far = rel[0] - at16[q];  // (the rows are one token's)
+                    const int bk = relpos_bucket(far);
+                    const bool one = far >= 15 && bk == relpos_bucket(far - 15);
+#pragma unroll
+                    for (int n = 2 * q; n < 2 * q + 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = 8 * (n & 1) + 2 * quad + (i & 1);  // key of the 16
+                            float b = 0.f;
+                            if (BIAS) b = brow[i >> 1][one ? bk : relpos_bucket(far - j)];
+                            s[n][i] = BIAS ? fmaf(s[n][i], p.scale_log2, b) : s[n][i] * p.scale_log2;
+                            if (j > far) s[n][i] = -INFINITY;
+                        }
+                }
+            } else if (BIAS) {
                 const int far = t_last + diag - w0, near = t_first + diag - (w0 + 16 * KG - 1);
                 const int bk = relpos_bucket(far);
                 if ((near >= 0 || far <= 0) && bk == relpos_bucket(near)) {
@@ -270,7 +333,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
             }
-            if (w0 < all_lo || w0 + 16 * KG > all_hi) {
+            if (!LIST && (w0 < all_lo || w0 + 16 * KG > all_hi)) {
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -574,11 +637,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     }
 }
 
-template <int D, bool BIAS>
+template <int D, bool BIAS, bool LIST = false>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early, int num_sms,
                    cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(jfa_cache_decode_kernel<D, BIAS>, DecCfg<D>::kBytes, done);
+    cudaError_t e = allow_smem(jfa_cache_decode_kernel<D, BIAS, LIST>, DecCfg<D>::kBytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -590,7 +653,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdP
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, jfa_cache_decode_kernel<D, BIAS>, mk, mv, p);
+    return cudaLaunchKernelEx(&cfg, jfa_cache_decode_kernel<D, BIAS, LIST>, mk, mv, p);
 }
 
 }  // namespace
@@ -604,6 +667,13 @@ cudaError_t launch_cache_decode(int D, const CUtensorMap& mk, const CUtensorMap&
     if (D == 128)
         return p.bias ? launch<128, true>(mk, mv, p, early, num_sms, st) : launch<128, false>(mk, mv, p, early, num_sms, st);
     return p.bias ? launch<64, true>(mk, mv, p, early, num_sms, st) : launch<64, false>(mk, mv, p, early, num_sms, st);
+}
+
+cudaError_t launch_cache_decode_lists(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                                      cudaStream_t st) {
+    if (D == 128)
+        return p.bias ? launch<128, true, true>(mk, mv, p, false, num_sms, st) : launch<128, false, true>(mk, mv, p, false, num_sms, st);
+    return p.bias ? launch<64, true, true>(mk, mv, p, false, num_sms, st) : launch<64, false, true>(mk, mv, p, false, num_sms, st);
 }
 
 }  // namespace jfa

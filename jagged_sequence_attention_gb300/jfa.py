@@ -37,7 +37,8 @@ EXPORTED = ["jfa_plan_create", "jfa_plan_create_ex", "jfa_plan_destroy", "jfa_pl
             "jfa_partition_sequences", "jfa_bwd_ex_workspace_size", "jfa_bwd_ex", "jfa_plan_create_shared_kv",
             "jfa_partition_users", "jfa_plan_set_deterministic", "jfa_plan_set_work_item",
             "jfa_cache_create", "jfa_cache_destroy", "jfa_cache_device_status", "jfa_cache_append",
-            "jfa_cache_workspace_size", "jfa_cache_fwd"]
+            "jfa_cache_workspace_size", "jfa_cache_fwd", "jfa_cache_create_quantized", "jfa_cache_read",
+            "jfa_cache_summarize", "jfa_cache_select_workspace_size", "jfa_cache_select", "jfa_cache_fwd_blocks"]
 
 
 class JFAError(RuntimeError):
@@ -69,7 +70,9 @@ def _cache_calls():
             from . import _cache_calls as m
         except ImportError as e:
             raise RuntimeError(f"the paged cache's compiled calls are not built ({e}); run __graft_entry__.build()") from None
-        m.set_calls(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.jfa_cache_append, L.jfa_cache_fwd)))
+        m.set_calls(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (L.jfa_cache_append, L.jfa_cache_fwd, L.jfa_cache_read, L.jfa_cache_summarize,
+                                L.jfa_cache_select, L.jfa_cache_fwd_blocks)))
         _calls = m
     return _calls
 
@@ -111,6 +114,15 @@ def load_library(path):
     L.jfa_cache_workspace_size.restype = sz
     L.jfa_cache_fwd.argtypes = [vp, i32, i64, i32, vp, vp, vp, i32, vp, i64, i32, i32, i32, i32, vp, f32, vp, i32, vp,
                                 vp, sz, vp]
+    L.jfa_cache_create_quantized.argtypes = [i32, i32, i32, i64, vp, vp, P(i64), P(i64), vp, vp, P(i64), P(i64), f32, f32,
+                                             vp, P(vp)]
+    L.jfa_cache_read.argtypes = [vp, i32, i64, vp, vp, vp, i32, vp, i64, vp, i64, vp]
+    L.jfa_cache_summarize.argtypes = [vp, i32, i64, vp, vp, vp, i32, vp, vp]
+    L.jfa_cache_select_workspace_size.argtypes = [vp, i64, i32]
+    L.jfa_cache_select_workspace_size.restype = sz
+    L.jfa_cache_select.argtypes = [vp, i32, i64, i32, vp, vp, vp, i32, vp, vp, i64, i32, i32, i32, i32, vp, vp, sz, vp]
+    L.jfa_cache_fwd_blocks.argtypes = [vp, i32, i64, vp, vp, vp, i32, vp, i64, i32, vp, i32, i32, vp, f32, vp, i32, vp,
+                                       vp, sz, vp]
     L.jfa_status_string.argtypes = [i32]
     L.jfa_status_string.restype = ctypes.c_char_p
     for name in ("jfa_plan_create", "jfa_plan_create_ex", "jfa_plan_destroy", "jfa_plan_info", "jfa_fwd", "jfa_bwd",
@@ -118,7 +130,8 @@ def load_library(path):
                  "jfa_plan_kernel_times", "jfa_bwd_static_scratch", "jfa_partition_sequences", "jfa_bwd_ex",
                  "jfa_plan_create_shared_kv", "jfa_partition_users", "jfa_plan_set_deterministic",
                  "jfa_plan_set_work_item", "jfa_cache_create", "jfa_cache_destroy", "jfa_cache_device_status",
-                 "jfa_cache_append", "jfa_cache_fwd"):
+                 "jfa_cache_append", "jfa_cache_fwd", "jfa_cache_create_quantized", "jfa_cache_read",
+                 "jfa_cache_summarize", "jfa_cache_select", "jfa_cache_fwd_blocks"):
         getattr(L, name).restype = i32
     return L
 
@@ -448,13 +461,17 @@ def jfa_worklist_build(q_offsets, kv_offsets, H: int, causal: bool, pass_: int, 
 
 
 class Cache:
-    """Owns a jfa_cache handle and keeps the cache's arrays alive."""
+    """Owns a jfa_cache handle and keeps the cache's arrays alive.  dtype: of the rows that are
+    appended and attended with."""
 
-    def __init__(self, handle, K, V):
-        self.handle, self.K, self.V = handle, K, V
+    def __init__(self, handle, K, V, scales=None):
+        self.handle, self.K, self.V, self.scales = handle, K, V, scales
         self.n_pages, self.page_size, self.Hkv, self.D = K.shape
         self.dtype, self.device = K.dtype, K.device
-        self.info = _cache_calls().describe(handle.value or 0, K)  # what the compiled calls check against
+        if scales is not None:  # 4 bits: two codes in a byte
+            self.D, self.dtype = 2 * self.D, torch.bfloat16
+        # what the compiled calls check against
+        self.info = _cache_calls().describe(handle.value or 0, K, scales is not None)
 
     def __del__(self):
         try:
@@ -486,6 +503,41 @@ def jfa_cache_create(K: torch.Tensor, V: torch.Tensor, stream=None) -> Cache:
     _check(fn, lib().jfa_cache_create(_dtype_code(K), Hkv, D, ps, n, K.data_ptr(), V.data_ptr(), ks, vs,
                                       _stream(stream), ctypes.byref(h)))
     return Cache(h, K, V)
+
+
+def jfa_cache_create_quantized(K: torch.Tensor, V: torch.Tensor, K_scales: torch.Tensor, V_scales: torch.Tensor,
+                               k_factor: float = 1.0, v_factor: float = 1.0, stream=None) -> Cache:
+    """A handle on a cache held in 4 bits: codes K, V uint8 [n_pages, page_size, Hkv, D / 2] (any
+    strides that are multiples of 16 bytes with a dense last dimension; head-major pages, given
+    as a permuted view, are read fastest) and scales uint8 or float8_e4m3fn
+    [n_pages, Hkv, page_size, D / 16] (the last two dimensions dense), on the current CUDA
+    device.  It is used like jfa_cache_create's, with bf16 rows."""
+    fn = "jfa_cache_create_quantized"
+    if (K.dim() != 4 or K.shape != V.shape or K.dtype != torch.uint8 or V.dtype != torch.uint8 or not K.is_cuda
+            or K.device != V.device):
+        _bad(fn, "K and V must be uint8 CUDA tensors of one shape [n_pages, page_size, Hkv, D / 2]")
+    if K.device.index != torch.cuda.current_device():
+        _bad(fn, f"K and V lie on {K.device}, which is not the current device")
+    n, ps, Hkv, half = K.shape
+    for s in (K_scales, V_scales):
+        if (s.shape != (n, Hkv, ps, half // 8) or half % 8 or s.dtype not in (torch.uint8, torch.float8_e4m3fn)
+                or s.device != K.device):
+            _bad(fn, "scales must be e4m3 tensors [n_pages, Hkv, page_size, D / 16] on the codes' device")
+        if s.stride(3) != 1 or (ps > 1 and s.stride(2) != half // 8):
+            _bad(fn, "a head's scales of one page must lie in one piece")
+    if K.stride(3) != 1 or V.stride(3) != 1:
+        _bad(fn, "the head dimension must be dense")
+    # (a dimension of one element leaves its stride free)
+    ks, vs = ((ctypes.c_int64 * 3)(*[t.stride(i) if t.shape[i] > 1 else -(-half // 16) * 16 for i in range(3)])
+              for t in (K, V))
+    piece = -(-ps * (half // 8) // 16) * 16
+    kss, vss = ((ctypes.c_int64 * 2)(*[t.stride(i) if t.shape[i] > 1 else piece for i in range(2)])
+                for t in (K_scales, V_scales))
+    h = ctypes.c_void_p()
+    _check(fn, lib().jfa_cache_create_quantized(Hkv, 2 * half, ps, n, K.data_ptr(), V.data_ptr(), ks, vs,
+                                                K_scales.data_ptr(), V_scales.data_ptr(), kss, vss, float(k_factor),
+                                                float(v_factor), _stream(stream), ctypes.byref(h)))
+    return Cache(h, K, V, (K_scales, V_scales))
 
 
 def jfa_cache_destroy(cache: Cache):
@@ -553,6 +605,84 @@ def jfa_cache_fwd(cache: Cache, Q, q_offsets, kv_lens, page_table, bias=None, sc
         raise JFAError(f"jfa_cache_fwd ({e})", JFA_ERR_INVALID_ARG) from None
     if status != JFA_OK:
         raise JFAError("jfa_cache_fwd", status)
+    return O, lse
+
+
+def _compiled(fn, call, *args):
+    """A compiled call whose failed checks become this binding's error."""
+    try:
+        status = call(*args)
+    except (ValueError, TypeError, OverflowError) as e:
+        raise JFAError(f"{fn} ({e})", JFA_ERR_INVALID_ARG) from None
+    if status != JFA_OK:
+        raise JFAError(fn, status)
+
+
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
+
+
+def jfa_cache_read(cache: Cache, T: int, q_offsets, kv_lens, page_table, K=None, V=None, stream=None):
+    """The rows of the T new tokens as the cache holds them, K and V [T, Hkv, D] (allocated if
+    None), which are returned."""
+    if K is None or V is None:
+        with torch.cuda.stream(stream):
+            K = torch.empty(T, cache.Hkv, cache.D, dtype=cache.dtype, device=cache.device) if K is None else K
+            V = torch.empty(T, cache.Hkv, cache.D, dtype=cache.dtype, device=cache.device) if V is None else V
+    _compiled("jfa_cache_read", _calls.read, cache.info, T, q_offsets, kv_lens, page_table, K, V, _raw(stream))
+    return K, V
+
+
+def jfa_cache_summarize(cache: Cache, bounds, T: int, q_offsets, kv_lens, page_table, stream=None):
+    """Brings bounds (bf16 [n_pages, Hkv, 2, D]: least and largest keys of each page) up to date
+    for the pages of the T new tokens.  Returns bounds."""
+    _compiled("jfa_cache_summarize", _calls.summarize, cache.info, cache.n_pages, bounds, T, q_offsets, kv_lens,
+              page_table, _raw(stream))
+    return bounds
+
+
+def jfa_cache_select_workspace_size(cache: Cache, T: int, max_pages: int) -> int:
+    return int(lib().jfa_cache_select_workspace_size(cache.handle, int(T), int(max_pages)))
+
+
+def jfa_cache_select_workspace(cache: Cache, T: int, max_pages: int) -> torch.Tensor:
+    """A workspace for jfa_cache_select on up to T new tokens.  Calls that may overlap need one
+    each."""
+    n = jfa_cache_select_workspace_size(cache, T, max_pages)
+    if n == 0:
+        _bad("jfa_cache_select_workspace", "T and max_pages must not be negative")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def jfa_cache_select(cache: Cache, bounds, Q, q_offsets, kv_lens, page_table, n_blocks: int, n_first: int = 1,
+                     n_last: int = 1, max_q_len=None, blocks=None, workspace=None, stream=None):
+    """The blocks (pages) that each new token attends to, by the score of their bounds: blocks
+    [T, Hkv, n_blocks] int32, ascending, then -1 (allocated if None), which is returned."""
+    if blocks is None or workspace is None:
+        with torch.cuda.stream(stream):
+            if blocks is None:
+                blocks = torch.empty(Q.shape[0], cache.Hkv, max(int(n_blocks), 0), dtype=torch.int32, device=Q.device)
+            if workspace is None:
+                workspace = jfa_cache_select_workspace(cache, Q.shape[0], page_table.shape[-1])
+    _compiled("jfa_cache_select", _calls.select, cache.info, cache.n_pages, bounds, Q, q_offsets, kv_lens, page_table,
+              n_blocks, n_first, n_last, max_q_len, blocks, workspace, _raw(stream))
+    return blocks
+
+
+def jfa_cache_fwd_blocks(cache: Cache, Q, q_offsets, kv_lens, page_table, blocks, bias=None, scale=None, O=None,
+                         lse=None, out_dtype=None, workspace=None, stream=None):
+    """Causal attention of the new tokens Q [T, H, D] over the blocks [T, Hkv, n] listed for
+    them.  Returns (O, lse).  The other arguments are jfa_cache_fwd's."""
+    if O is None or lse is None or workspace is None:
+        with torch.cuda.stream(stream):
+            if O is None:
+                O = torch.empty(Q.shape, dtype=out_dtype or Q.dtype, device=Q.device)
+            if lse is None:
+                lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
+            if workspace is None:
+                workspace = jfa_cache_workspace(cache, Q.shape[1] if Q.dim() == 3 else 0)
+    _compiled("jfa_cache_fwd_blocks", _calls.fwd_blocks, cache.info, Q, q_offsets, kv_lens, page_table, blocks, bias,
+              cache.D ** -0.5 if scale is None else scale, O, lse, workspace, _raw(stream))
     return O, lse
 
 
