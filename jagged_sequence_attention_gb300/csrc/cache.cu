@@ -193,7 +193,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     const int n = cache->num_sms, D = cache->D;
     const bool bf16 = cache->dtype == JFA_BF16;
     const int64_t most_rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * p.g;
-    const bool chunks = most_rows > kDecodeRows && (!cache->ops || cache->ops->chunk);
+    const bool chunks = most_rows > kDecodeRows;
     // the kernels count units in 31 bits; tiles(): the row tiles of bm rows that `rows` rows have at most
     auto tiles = [&](int64_t rows, int bm) { return rows / bm + B; };
     auto fits = [&](int64_t n_tiles, int bn) {
@@ -223,7 +223,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g, p.bm), 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
-    if (chunks && bf16) {  // the queries as (D, head, token), boxes of one tile's rows
+    if (chunks && bf16 && !cache->ops) {  // the queries as (D, head, token), boxes of one tile's rows
         const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
         const int64_t strides[2] = {D, q_stride};
         const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(pc.tile_tokens)};
@@ -232,7 +232,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     }
     cudaError_t e = cudaSuccess;
     if (cache->ops) {
-        if (chunks) e = cache->ops->chunk(cache, mq, pc, st);
+        if (chunks) e = cache->ops->chunk(cache, pc, st);
         if (e == cudaSuccess) e = cache->ops->decode(cache, p, chunks, st);
     } else {
         if (chunks)

@@ -38,6 +38,7 @@
 // 266 us), drawing an item ahead of time (738 -> 796 us for the prompts, whose last items then
 // wait in CTAs that are busy).
 #include "cache_common.cuh"
+#include "quant.cuh"
 #include "tilemath.cuh"
 
 #include <limits.h>
@@ -61,7 +62,7 @@ struct alignas(16) SegRec {
 // rows over the banks.
 constexpr int kThreeBuckets = 62, kNear = 96, kNearStride = 100, kNearHeads = 32;
 
-template <int D>
+template <int D, bool Q4>
 struct ChkCfg {
     static constexpr int BM = 128, BN = 128, kPair = kMergeRows;
     static constexpr int kCB = D / 64;
@@ -72,7 +73,7 @@ struct ChkCfg {
     static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + kStages * kKVBytes;
     static constexpr int kOffBar = kOffV + kStages * kKVBytes;
     static constexpr int kNumBars = 56;
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag, merge flag
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag
     static constexpr int kSlots = 4;                          // parts of items handed out and not yet taken by all
     static constexpr int kAsk = 3;                            // key tiles of a part left to load when the next is asked for
     static constexpr int kOffSeg = kOffMisc + 16;
@@ -82,13 +83,17 @@ struct ChkCfg {
     static constexpr int kOffGroups = kOffXch + 2 * 2 * 8 * 32 * 4;
     // bias by relative position |r| < kNear, log2 units, of the first kNearHeads heads
     static constexpr int kOffNear = kOffGroups + (int(sizeof(CacheGroups)) + 15) / 16 * 16;
-    static constexpr int kSmemNeed = kOffNear + kNearHeads * kNearStride * 4 + 1024;
+    // 4 bits: what takes a row's scores back to its queries' size
+    static constexpr int kOffDown = kOffNear + kNearHeads * kNearStride * 4;
+    static constexpr int kSmemNeed = kOffDown + (Q4 ? 2 * BM * 4 : 0) + 1024;
     // at least 120 KB: one CTA per SM, as the CTA allocates all 512 TMEM columns
     static constexpr int kSmemBytes = kSmemNeed > 120 * 1024 ? kSmemNeed : 120 * 1024;
-    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 17, kDrawWarp = 18, kThreads = 19 * 32;
+    static constexpr int kProdWarps = Q4 ? 4 : 1;  // 4 bits: they unpack
+    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 16 + kProdWarps, kDrawWarp = kMmaWarp + 1,
+                         kThreads = (kDrawWarp + 1) * 32;
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, BM, BN, false, false);
-    static constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, BM, D, false, true);
+    static constexpr uint32_t kIdescQK = make_idesc(Q4 ? kFmtF16 : kFmtBF16, BM, BN, false, false);
+    static constexpr uint32_t kIdescPV = make_idesc(Q4 ? kFmtF16 : kFmtBF16, BM, D, false, true);
     static constexpr int kPart = cache_merge_part(D);  // floats of a partial result: O (four columns of all rows at a time), m, l
     __host__ __device__ static constexpr uint32_t tmem_s(int x) { return x ? 128u : 0u; }
     __host__ __device__ static constexpr uint32_t tmem_o(int x) { return x ? 384u : 256u; }
@@ -143,10 +148,10 @@ __device__ __forceinline__ Steps steps_of(const CacheFwdParams& p, const CacheSe
     return s;
 }
 
-template <int D, bool BIAS>
-__global__ void __launch_bounds__(608, 1)
+template <int D, bool BIAS, bool Q4>
+__global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
     jfa_cache_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const CacheFwdParams p) {
-    using C = ChkCfg<D>;
+    using C = ChkCfg<D, Q4>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -161,12 +166,12 @@ __global__ void __launch_bounds__(608, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(B_Q_FULL), 1);
-        mbar_init(bar(B_Q_EMPTY), 1);
+        mbar_init(bar(B_Q_FULL), C::kProdWarps);
+        mbar_init(bar(B_Q_EMPTY), Q4 ? 1 + C::kSoftWarps : 1);
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(B_K_FULL + s), 1);
+            mbar_init(bar(B_K_FULL + s), C::kProdWarps);
             mbar_init(bar(B_K_EMPTY + s), 1);
-            mbar_init(bar(B_V_FULL + s), 1);
+            mbar_init(bar(B_V_FULL + s), C::kProdWarps);
             mbar_init(bar(B_V_EMPTY + s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -180,13 +185,13 @@ __global__ void __launch_bounds__(608, 1)
         for (int q = 0; q < 8; ++q) mbar_init(bar(B_XCH + q), 2);
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(bar(B_SEG_FULL + s), 1);
-            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + 2);
+            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + C::kProdWarps + 1);
         }
         mbar_init(bar(B_ASK), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == C::kProdWarp && lane == 0) {
+    if (!Q4 && warp == C::kProdWarp && lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
@@ -245,7 +250,154 @@ __global__ void __launch_bounds__(608, 1)
         atomicOr(p.status, kStatusTimeout);
     };
 
-    if (warp == C::kProdWarp) {
+    if (Q4 && warp >= C::kProdWarp && warp < C::kMmaWarp) {
+        if constexpr (Q4) {
+            // -------------------------------------------------------- loads, unpacked
+            // A thread takes 32 neighbouring elements of a row at a time, in `kPer` lanes a row:
+            // queries from bf16 with a power of two of their row that brings their largest
+            // magnitude to 2^14, keys and values from 16 bytes of codes and two scales.  What it
+            // writes are four of the eight 16-byte pieces of a 128-byte row of the tile; the lanes of
+            // a row's second half write theirs in another order, so that eight lanes meet all banks.
+            constexpr int kPer = D / 32, kRows = 128 / kPer, NP = 128 / kRows;
+            const int tid = threadIdx.x - 32 * C::kProdWarp, quarter = tid % kPer, row0 = tid / kPer;
+            const int turn = D == 128 ? 2 * (quarter >> 1) : 0;  // its order: pieces c ^ turn
+            float* down_s = reinterpret_cast<float*>(smem + C::kOffDown);
+            auto piece = [&](uint32_t tile, int row, int c) -> uint32_t {
+                return tile + uint32_t((quarter >> 1) * C::BM * 128 + row * 128 + (((4 * (quarter & 1) + (c ^ turn)) ^ (row & 7)) << 4));
+            };
+            auto wwait = [&](int b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag));
+            };
+            auto publish = [&](int b) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(b));
+            };
+            uint32_t kv_it = 0, item_it = 0;
+            bool ok = true;
+            const uint8_t *kc = static_cast<const uint8_t*>(p.K) + 16 * quarter, *vc = static_cast<const uint8_t*>(p.V) + 16 * quarter;
+            const uint8_t *ksc = p.k_scales + 2 * quarter, *vsc = p.v_scales + 2 * quarter;
+            // The pages of this thread's rows of key tile k: -1 for keys outside the item's (they
+            // read as zeros) and for bad entries.
+            auto pages_of = [&](int k, int (&pg)[NP]) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int j = (g.r.f + k) * C::BN + kRows * i + row0;
+                    pg[i] = -1;
+                    if (j < g.r.lo || j >= g.r.hi) continue;
+                    pg[i] = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                    if (pg[i] < 0 || pg[i] >= p.n_pages) {
+                        atomicOr(p.status, kStatusBounds);
+                        pg[i] = -1;
+                    }
+                }
+            };
+            auto fetch = [&](const uint8_t* codes, const uint8_t* scales, const int64_t* st, const int64_t* ss, int k, const int (&pg)[NP],
+                             uint4 (&w)[NP], uint32_t (&sc)[NP]) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int slot = ((g.r.f + k) * C::BN + kRows * i + row0) & ((1 << p.page_log2) - 1);
+                    w[i] = make_uint4(0u, 0u, 0u, 0u);
+                    sc[i] = 0u;
+                    if (pg[i] < 0) continue;
+                    w[i] = __ldg(reinterpret_cast<const uint4*>(codes + pg[i] * st[0] + slot * st[1] + g.hk * st[2]));
+                    sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + pg[i] * ss[0] + g.hk * ss[1] + slot * (D / 16)));
+                }
+            };
+            auto unpack = [&](uint32_t tile, const uint4 (&w)[NP], const uint32_t (&sc)[NP]) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const uint32_t two = e4m3_to_f16(sc[i]), s01 = __byte_perm(two, 0u, 0x1010), s23 = __byte_perm(two, 0u, 0x3232);
+                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t h[4];
+                        e2m1_to_f16(turn ? x[c ^ 2] : x[c], h);
+                        const uint32_t s = (c < 2) == (turn == 0) ? s01 : s23;
+                        st_shared_v4(piece(tile, kRows * i + row0, c), f16_mul2(h[0], s), f16_mul2(h[1], s), f16_mul2(h[2], s), f16_mul2(h[3], s));
+                    }
+                }
+            };
+            auto load_q = [&]() {
+                const int rt = p.tile_tokens * p.g, R = g.s.q_len * p.g;
+                const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.Q);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    if (x && (2 * g.tile + 1) * rt >= R) break;
+#pragma unroll 1
+                    for (int i = 0; i < NP; ++i) {
+                        const int t = kRows * i + row0, r = (2 * g.tile + x) * rt + t;
+                        uint4 q[4];
+                        const bool in = t < rt && r < R;
+                        const int tok = div_g(p, in ? r : 0);
+                        const uint4* src = reinterpret_cast<const uint4*>(Q + (g.s.q0 + tok) * p.q_stride +
+                                                                          int64_t(g.hk * p.g + (in ? r : 0) - tok * p.g) * D + 32 * quarter);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) q[c] = in ? __ldg(src + (c ^ turn)) : make_uint4(0u, 0u, 0u, 0u);
+                        float top = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t v[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                top = fmax3(top, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u)));
+                        }
+#pragma unroll
+                        for (int d = 1; d < kPer; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
+                        const float up = __uint_as_float((268u - e) << 23);
+                        if (quarter == 0) down_s[x * C::BM + t] = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t v[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+                            uint32_t h[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                h[k] = pack_f16x2(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+                            st_shared_v4(piece(sQ + x * C::kQBytes, t, c), h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+            };
+            auto ask = [&]() {
+                if (tid == 0) mbar_arrive(bar(B_ASK));
+            };
+            while (ok && next()) {
+                if (g.r.n == 0) {
+                    ask();
+                    continue;
+                }
+                int pg[NP], pn[NP];
+                uint4 wk[NP], wv[NP];
+                uint32_t sk[NP], sv[NP];
+                pages_of(g.k0, pg);
+                if (g.k0 + 1 < g.k1) pages_of(g.k0 + 1, pn);
+                fetch(kc, ksc, p.ks, p.kss, g.k0, pg, wk, sk);
+                if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+                load_q();
+                publish(B_Q_FULL);
+                ++item_it;
+                for (int k = g.k0; k < g.k1; ++k, ++kv_it) {
+                    if (g.k1 - k == min(C::kAsk, g.k1 - g.k0)) ask();
+                    const uint32_t st = kv_it % C::kStages, ph = (kv_it / C::kStages) & 1;
+                    fetch(vc, vsc, p.vs, p.vss, k, pg, wv, sv);
+                    if (!wwait(B_K_EMPTY + st, ph ^ 1)) { ok = false; break; }
+                    unpack(sK + st * C::kKVBytes, wk, sk);
+                    publish(B_K_FULL + st);
+                    if (k + 1 < g.k1) {
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) pg[i] = pn[i];
+                        fetch(kc, ksc, p.ks, p.kss, k + 1, pg, wk, sk);
+                        if (k + 2 < g.k1) pages_of(k + 2, pn);
+                    }
+                    if (!wwait(B_V_EMPTY + st, ph ^ 1)) { ok = false; break; }
+                    unpack(sV + st * C::kKVBytes, wv, sv);
+                    publish(B_V_FULL + st);
+                }
+            }
+            if (!ok && lane == 0) fail();
+        }
+    } else if (!Q4 && warp == C::kProdWarp) {
         // ------------------------------------------------------------ loads
         // One box of K and one of V per lane and tile: column block, page (or 64 keys of one).
         const int rows = min(1 << p.page_log2, 64), per = C::BN / rows;
@@ -462,7 +614,7 @@ __global__ void __launch_bounds__(608, 1)
                     const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
                     const uint32_t t1 = t + 1, st1 = t1 % C::kStages, ph1 = (t1 / C::kStages) & 1;
                     if (!wwait(B_V_FULL + st, ph)) { ok = false; break; }
-                    clear_v(st, j);
+                    if (!Q4) clear_v(st, j);
                     if (act(0, j) && !issue_pv(0, st, j == s.a[0])) { ok = false; break; }
                     if (i + 1 < n && !wwait(B_K_FULL + st1, ph1)) { ok = false; break; }
                     if (act(0, j + 1) && !issue_s(0, st1, 0)) { ok = false; break; }
@@ -487,7 +639,7 @@ __global__ void __launch_bounds__(608, 1)
                     const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
                     const uint32_t t2 = t + 2, st2 = t2 % C::kStages, ph2 = (t2 / C::kStages) & 1;
                     if (!wwait(B_V_FULL + st, ph)) { ok = false; break; }
-                    clear_v(st, s.k0 + i);
+                    if (!Q4) clear_v(st, s.k0 + i);
                     if (!issue_pv(x, st, i < 2)) { ok = false; break; }
                     commit(B_V_EMPTY + st);
                     if (i + 2 < n) {
@@ -505,7 +657,7 @@ __global__ void __launch_bounds__(608, 1)
         if (!ok && lane == 0) fail();
         commit(B_DRAIN);  // every issued product, before TMEM is released
         mbar_wait_bounded(bar(B_DRAIN), 0, nullptr);
-    } else {
+    } else if (warp < C::kSoftWarps) {
         // ------------------------------------------------------------ softmax / epilogue
         const int x = (warp >> 2) & 1, hf = warp >> 3, pair = warp & 7;
         const int t = (warp & 3) * 32 + lane;  // row in the tile == TMEM lane
@@ -537,7 +689,10 @@ __global__ void __launch_bounds__(608, 1)
             if (good) other = buf[(hf ^ 1) * 256 + lane];
             return good;
         };
-        const float xs = p.scale_log2;
+        float xs = p.scale_log2;
+        // 4 bits: P = 2^6 times the weights, in fp16, where small ones keep more of their bits
+        constexpr float kLift = Q4 ? 6.f : 0.f;
+        uint32_t item_it = 0;
         bool ok = true;
         while (ok && next()) {
             const Steps sp = steps_of(p, g);
@@ -553,6 +708,13 @@ __global__ void __launch_bounds__(608, 1)
             const float* brow = BIAS ? p.bias + head * 32 : nullptr;
             const size_t orow = size_t(g.s.q0 + tok) * size_t(p.H) + size_t(head);
             float m = -INFINITY, l = 0.f;
+            if (Q4 && g.r.n > 0) {
+                if (!wwait(B_Q_FULL, item_it & 1)) { ok = false; break; }
+                xs = p.scale_log2 * reinterpret_cast<const float*>(smem + C::kOffDown)[(sp.split ? 0 : x) * C::BM + t];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_Q_EMPTY));
+                ++item_it;
+            }
             for (int i = 0; i < n; ++i) {
                 const int col0 = (g.r.f + first_k + i * stride_k) * C::BN;
                 int lim = g.s.kv_len - col0;
@@ -583,7 +745,7 @@ __global__ void __launch_bounds__(608, 1)
                 // two plain chunks beside it made steps with a bias slower: 67 -> 73 us for nine prompts
                 // of 200-800 tokens among single ones, short items.  It was not measured on long
                 // prompts, which pay 708 -> 874 us for a bias in this form.)
-                constexpr bool plain = !BIAS;
+                constexpr bool plain = !BIAS && !Q4;
                 uint32_t sr[2][32];
                 if (plain) {
                     tmem_ld32(tS, sr[0]);
@@ -702,7 +864,7 @@ __global__ void __launch_bounds__(608, 1)
                     for (int e = 0; e < 32; e += 2) {
                         const float2 e2 = make_float2(ex2_approx(__uint_as_float(r[e])), ex2_approx(__uint_as_float(r[e + 1])));
                         rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], e2);
-                        pk[e >> 1] = pack_bf16x2(e2.x, e2.y);
+                        pk[e >> 1] = Q4 ? pack_f16x2(e2.x, e2.y) : pack_bf16x2(e2.x, e2.y);
                     }
                     tmem_st16(tSt + 32u * kk, pk);
                 };
@@ -713,7 +875,7 @@ __global__ void __launch_bounds__(608, 1)
                     tmem_ld_wait(sr[1]);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float2 xs2 = make_float2(xs, xs), add = make_float2(cb[k] - m_use, cb[k] - m_use);
+                        const float2 xs2 = make_float2(xs, xs), add = make_float2(cb[k] - m_use + kLift, cb[k] - m_use + kLift);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const float2 t2 = fma2(make_float2(__uint_as_float(sr[k][e]), __uint_as_float(sr[k][e + 1])), xs2, add);
@@ -728,7 +890,7 @@ __global__ void __launch_bounds__(608, 1)
                     for (int k = 0; k < 2; ++k) {
                         tmem_ld32(tS + 32u * k, sr[0]);
                         tmem_ld_wait(sr[0]);
-                        to_x(sr[0], k, m_use);
+                        to_x(sr[0], k, m_use - kLift);
                         exps(sr[0], 2 * hf + k);
                     }
                 }
@@ -741,6 +903,7 @@ __global__ void __launch_bounds__(608, 1)
                 ++s_cnt;
             }
             if (!ok) break;
+            m -= kLift;
             const bool whole = g.whole();
             if (n > 0) {
                 if (!wwait(B_O_DONE + x, (s_cnt - 1) & 1)) { ok = false; break; }
@@ -820,7 +983,7 @@ __global__ void __launch_bounds__(608, 1)
             };
             if (whole) {
                 if (!owner) continue;
-                const float inv = lt > 0.f ? 1.f / lt : 0.f;
+                const float inv = lt > 0.f ? (Q4 ? p.o_mul : 1.f) / lt : 0.f;
 #pragma unroll
                 for (int c = 0; c < OC / 32; ++c) {
                     float v[32];
@@ -926,7 +1089,7 @@ __device__ __forceinline__ void merge_rows(const CacheFwdParams& p, const CacheC
             }
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? p.o_mul / l : 0.f;
     const int r = cut.row0 + row, tok = div_g(p, r);
     const size_t orow = size_t(cut.q0 + tok) * size_t(p.H) + size_t(cut.head0 + r - tok * p.g);
 #pragma unroll
@@ -976,12 +1139,13 @@ __global__ void __launch_bounds__(kMergeThreads) jfa_cache_merge_kernel(const Ca
     }
 }
 
-template <int D, bool BIAS>
+template <int D, bool BIAS, bool Q4>
 cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(jfa_cache_chunk_kernel<D, BIAS>, ChkCfg<D>::kSmemBytes, done);
+    using C = ChkCfg<D, Q4>;
+    cudaError_t e = allow_smem(jfa_cache_chunk_kernel<D, BIAS, Q4>, C::kSmemBytes, done);
     if (e != cudaSuccess) return e;
-    jfa_cache_chunk_kernel<D, BIAS><<<num_sms, ChkCfg<D>::kThreads, ChkCfg<D>::kSmemBytes, st>>>(mq, mk, mv, p);
+    jfa_cache_chunk_kernel<D, BIAS, Q4><<<num_sms, C::kThreads, C::kSmemBytes, st>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 
@@ -991,8 +1155,16 @@ size_t cache_chunk_part_bytes(int D, int num_sms) { return size_t(num_sms) * kBl
 
 cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    if (D == 128) return p.bias ? launch<128, true>(mq, mk, mv, p, num_sms, st) : launch<128, false>(mq, mk, mv, p, num_sms, st);
-    return p.bias ? launch<64, true>(mq, mk, mv, p, num_sms, st) : launch<64, false>(mq, mk, mv, p, num_sms, st);
+    if (D == 128)
+        return p.bias ? launch<128, true, false>(mq, mk, mv, p, num_sms, st) : launch<128, false, false>(mq, mk, mv, p, num_sms, st);
+    return p.bias ? launch<64, true, false>(mq, mk, mv, p, num_sms, st) : launch<64, false, false>(mq, mk, mv, p, num_sms, st);
+}
+
+cudaError_t launch_cache_chunk4(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
+    const CUtensorMap none{};  // (everything is loaded by address)
+    if (D == 128)
+        return p.bias ? launch<128, true, true>(none, none, none, p, num_sms, st) : launch<128, false, true>(none, none, none, p, num_sms, st);
+    return p.bias ? launch<64, true, true>(none, none, none, p, num_sms, st) : launch<64, false, true>(none, none, none, p, num_sms, st);
 }
 
 cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int blocks, int num_sms, cudaStream_t st) {

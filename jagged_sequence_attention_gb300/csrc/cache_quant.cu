@@ -28,6 +28,8 @@ namespace jfa {
 cudaError_t launch_cache_decode4(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early,
                                  int num_sms, cudaStream_t st);
 size_t cache_decode4_part_bytes(int D, int num_sms);
+// Items of 256 packed rows.
+cudaError_t launch_cache_chunk4(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st);
 
 namespace {
 
@@ -272,7 +274,11 @@ cudaError_t decode4(jfa_cache c, const CacheFwdParams& p, bool early, cudaStream
     return launch_cache_decode4(c->D, c->mk, c->mv, p, early, c->num_sms, st);
 }
 
-const CacheOps kQuantOps = {append4, nullptr, decode4, cache_decode4_part_bytes};
+cudaError_t chunk4(jfa_cache c, const CacheFwdParams& p, cudaStream_t st) {
+    return launch_cache_chunk4(c->D, p, c->num_sms, st);
+}
+
+const CacheOps kQuantOps = {append4, chunk4, decode4, cache_decode4_part_bytes};
 
 // Pages of codes as bytes (D/2, slot, head, page), boxes of one page's rows (at most 64).  Rows of
 // 64 bytes are swizzled, which spreads a column of eight of them over all banks.
