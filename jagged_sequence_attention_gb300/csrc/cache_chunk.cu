@@ -69,9 +69,12 @@ struct ChkCfg {
     static constexpr int kQBytes = BM * D * 2, kKVBytes = BN * D * 2;
     // K and V rings: what shared memory holds (a short item's keys come from DRAM, and two
     // stages of 16 KB in flight would not keep up with it)
-    static constexpr int kStages = D == 128 ? 2 : 5;
-    static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + kStages * kKVBytes;
-    static constexpr int kOffBar = kOffV + kStages * kKVBytes;
+    // 4 bits: one ring of unpacked tiles, K and V in turn, and one of packed ones
+    static constexpr int kStages = D == 128 ? 2 : 5, kRing = D == 128 ? 3 : 6, kRaw = D == 128 ? 3 : 6;
+    static constexpr int kRawCodes = BN * D / 2, kRawBytes = kRawCodes + BN * D / 16;
+    static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + (Q4 ? 0 : kStages * kKVBytes);
+    static constexpr int kOffRaw = kOffK + kRing * kKVBytes;
+    static constexpr int kOffBar = Q4 ? kOffRaw + kRaw * kRawBytes : kOffV + kStages * kKVBytes;
     static constexpr int kNumBars = 56;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag
     static constexpr int kSlots = 4;                          // parts of items handed out and not yet taken by all
@@ -88,9 +91,9 @@ struct ChkCfg {
     static constexpr int kSmemNeed = kOffDown + (Q4 ? 2 * BM * 4 : 0) + 1024;
     // at least 120 KB: one CTA per SM, as the CTA allocates all 512 TMEM columns
     static constexpr int kSmemBytes = kSmemNeed > 120 * 1024 ? kSmemNeed : 120 * 1024;
-    static constexpr int kProdWarps = Q4 ? 4 : 1;  // 4 bits: they unpack
-    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 16 + kProdWarps, kDrawWarp = kMmaWarp + 1,
-                         kThreads = (kDrawWarp + 1) * 32;
+    static constexpr int kUnpackWarps = Q4 ? 4 : 0, kWriters = Q4 ? kUnpackWarps : 1;  // writers: of the products' tiles
+    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 17, kDrawWarp = 18, kUnpackWarp = 19,
+                         kThreads = (kUnpackWarp + kUnpackWarps) * 32;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdescQK = make_idesc(Q4 ? kFmtF16 : kFmtBF16, BM, BN, false, false);
     static constexpr uint32_t kIdescPV = make_idesc(Q4 ? kFmtF16 : kFmtBF16, BM, D, false, true);
@@ -166,12 +169,22 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(B_Q_FULL), C::kProdWarps);
+        mbar_init(bar(B_Q_FULL), C::kWriters);
         mbar_init(bar(B_Q_EMPTY), Q4 ? 1 + C::kSoftWarps : 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(B_K_FULL + s), C::kProdWarps);
+        if (Q4) {  // K_*: the ring of unpacked tiles; V_*: of packed ones
+            for (int s = 0; s < C::kRing; ++s) {
+                mbar_init(bar(B_K_FULL + s), C::kWriters);
+                mbar_init(bar(B_K_EMPTY + s), 1);
+            }
+            for (int s = 0; s < C::kRaw; ++s) {
+                mbar_init(bar(B_V_FULL + s), 1);
+                mbar_init(bar(B_V_EMPTY + s), C::kUnpackWarps);
+            }
+        }
+        for (int s = 0; !Q4 && s < C::kStages; ++s) {
+            mbar_init(bar(B_K_FULL + s), 1);
             mbar_init(bar(B_K_EMPTY + s), 1);
-            mbar_init(bar(B_V_FULL + s), C::kProdWarps);
+            mbar_init(bar(B_V_FULL + s), 1);
             mbar_init(bar(B_V_EMPTY + s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -185,14 +198,14 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
         for (int q = 0; q < 8; ++q) mbar_init(bar(B_XCH + q), 2);
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(bar(B_SEG_FULL + s), 1);
-            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + C::kProdWarps + 1);
+            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + 2 + C::kUnpackWarps);
         }
         mbar_init(bar(B_ASK), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (!Q4 && warp == C::kProdWarp && lane == 0) {
-        tma_prefetch_desc(&tmQ);
+    if (warp == C::kProdWarp && lane == 0) {
+        if (!Q4) tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
@@ -250,16 +263,17 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
         atomicOr(p.status, kStatusTimeout);
     };
 
-    if (Q4 && warp >= C::kProdWarp && warp < C::kMmaWarp) {
+    if (Q4 && warp >= C::kUnpackWarp) {
         if constexpr (Q4) {
-            // -------------------------------------------------------- loads, unpacked
+            // -------------------------------------------------------- unpacking
             // A thread takes 32 neighbouring elements of a row at a time, in `kPer` lanes a row:
             // queries from bf16 with a power of two of their row that brings their largest
-            // magnitude to 2^14, keys and values from 16 bytes of codes and two scales.  What it
+            // magnitude to 2^14, keys and values from 16 bytes of codes and two scales in shared memory
+            // (loaded by address a tile ahead, they came too late: 1478 us instead of @).  What it
             // writes are four of the eight 16-byte pieces of a 128-byte row of the tile; the lanes of
             // a row's second half write theirs in another order, so that eight lanes meet all banks.
             constexpr int kPer = D / 32, kRows = 128 / kPer, NP = 128 / kRows;
-            const int tid = threadIdx.x - 32 * C::kProdWarp, quarter = tid % kPer, row0 = tid / kPer;
+            const int tid = threadIdx.x - 32 * C::kUnpackWarp, quarter = tid % kPer, row0 = tid / kPer;
             const int turn = D == 128 ? 2 * (quarter >> 1) : 0;  // its order: pieces c ^ turn
             float* down_s = reinterpret_cast<float*>(smem + C::kOffDown);
             auto piece = [&](uint32_t tile, int row, int c) -> uint32_t {
@@ -275,36 +289,31 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
             };
             uint32_t kv_it = 0, item_it = 0;
             bool ok = true;
-            const uint8_t *kc = static_cast<const uint8_t*>(p.K) + 16 * quarter, *vc = static_cast<const uint8_t*>(p.V) + 16 * quarter;
-            const uint8_t *ksc = p.k_scales + 2 * quarter, *vsc = p.v_scales + 2 * quarter;
-            // The pages of this thread's rows of key tile k: -1 for keys outside the item's (they
-            // read as zeros) and for bad entries.
-            auto pages_of = [&](int k, int (&pg)[NP]) {
+            // Tile number j of the rings, key tile k; keys outside the item's become zeros (what lies
+            // there is undefined, and 0 * NaN is not 0).
+            auto unpack = [&](uint32_t j, int k) -> bool {
+                const uint32_t rs = j % C::kRaw, st = j % C::kRing;
+                const uint32_t raw = sbase + C::kOffRaw + rs * C::kRawBytes, tile = sK + st * C::kKVBytes;
+                if (!wwait(B_V_FULL + int(rs), (j / C::kRaw) & 1)) return false;
+                uint4 w[NP];
+                uint32_t sc[NP];
+                const int c0 = (g.r.f + k) * C::BN, lo = g.r.lo - c0, hi = g.r.hi - c0;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const int j = (g.r.f + k) * C::BN + kRows * i + row0;
-                    pg[i] = -1;
-                    if (j < g.r.lo || j >= g.r.hi) continue;
-                    pg[i] = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
-                    if (pg[i] < 0 || pg[i] >= p.n_pages) {
-                        atomicOr(p.status, kStatusBounds);
-                        pg[i] = -1;
-                    }
+                    const int row = kRows * i + row0;
+                    w[i] = ld_shared_v4(raw + uint32_t(row * (D / 2) + ((D == 128 ? quarter ^ ((row >> 1) & 3) : quarter) << 4)));
+                    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+                                 : "=r"(sc[i])
+                                 : "r"(raw + uint32_t(C::kRawCodes + row * (D / 16) + 2 * quarter)));
                 }
-            };
-            auto fetch = [&](const uint8_t* codes, const uint8_t* scales, const int64_t* st, const int64_t* ss, int k, const int (&pg)[NP],
-                             uint4 (&w)[NP], uint32_t (&sc)[NP]) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_V_EMPTY + int(rs)));
+                if (lo > 0 || hi < C::BN) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int slot = ((g.r.f + k) * C::BN + kRows * i + row0) & ((1 << p.page_log2) - 1);
-                    w[i] = make_uint4(0u, 0u, 0u, 0u);
-                    sc[i] = 0u;
-                    if (pg[i] < 0) continue;
-                    w[i] = __ldg(reinterpret_cast<const uint4*>(codes + pg[i] * st[0] + slot * st[1] + g.hk * st[2]));
-                    sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + pg[i] * ss[0] + g.hk * ss[1] + slot * (D / 16)));
+                    for (int i = 0; i < NP; ++i)
+                        if (kRows * i + row0 < lo || kRows * i + row0 >= hi) sc[i] = 0u;
                 }
-            };
-            auto unpack = [&](uint32_t tile, const uint4 (&w)[NP], const uint32_t (&sc)[NP]) {
+                if (!wwait(B_K_EMPTY + int(st), ((j / C::kRing) & 1) ^ 1)) return false;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const uint32_t two = e4m3_to_f16(sc[i]), s01 = __byte_perm(two, 0u, 0x1010), s23 = __byte_perm(two, 0u, 0x3232);
@@ -317,6 +326,8 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                         st_shared_v4(piece(tile, kRows * i + row0, c), f16_mul2(h[0], s), f16_mul2(h[1], s), f16_mul2(h[2], s), f16_mul2(h[3], s));
                     }
                 }
+                publish(B_K_FULL + int(st));
+                return true;
             };
             auto load_q = [&]() {
                 const int rt = p.tile_tokens * p.g, R = g.s.q_len * p.g;
@@ -359,43 +370,69 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                     }
                 }
             };
+            while (ok && next()) {
+                if (g.r.n == 0) continue;
+                if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+                load_q();
+                publish(B_Q_FULL);
+                ++item_it;
+                for (int k = g.k0; k < g.k1 && ok; ++k, ++kv_it) ok = unpack(2 * kv_it, k) && unpack(2 * kv_it + 1, k);
+            }
+            if (!ok && lane == 0) fail();
+        }
+    } else if (Q4 && warp == C::kProdWarp) {
+        if constexpr (Q4) {
+            // -------------------------------------------------------- loads of packed tiles
+            // A lane loads one box of each tile, the codes of a page (or of 64 keys of one), and its scales.
+            const int rows = min(1 << p.page_log2, 64), per = C::BN / rows;
+            const int pg = lane;
+            const bool mine = lane < per;
+            const uint32_t box = uint32_t(pg * rows * (D / 2)), sbox = uint32_t(C::kRawCodes + pg * rows * (D / 16));
+            uint32_t it = 0;
+            bool ok = true;
+            auto page_of = [&](const CacheSeg& s, int k) -> int {
+                const int j = (s.r.f + k) * C::BN + pg * rows;
+                if (!mine || j >= s.r.hi || j + rows <= s.r.lo) return -1;
+                const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                if (page >= 0 && page < p.n_pages) return page;
+                atomicOr(p.status, kStatusBounds);
+                return p.n_pages;  // past the cache: codes read as zeros (with any scales)
+            };
             auto ask = [&]() {
-                if (tid == 0) mbar_arrive(bar(B_ASK));
+                if (lane == 0) mbar_arrive(bar(B_ASK));
             };
             while (ok && next()) {
                 if (g.r.n == 0) {
                     ask();
                     continue;
                 }
-                int pg[NP], pn[NP];
-                uint4 wk[NP], wv[NP];
-                uint32_t sk[NP], sv[NP];
-                pages_of(g.k0, pg);
-                if (g.k0 + 1 < g.k1) pages_of(g.k0 + 1, pn);
-                fetch(kc, ksc, p.ks, p.kss, g.k0, pg, wk, sk);
-                if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
-                load_q();
-                publish(B_Q_FULL);
-                ++item_it;
-                for (int k = g.k0; k < g.k1; ++k, ++kv_it) {
+                int page = page_of(g, g.k0);
+                for (int k = g.k0; k < g.k1 && ok; ++k) {
                     if (g.k1 - k == min(C::kAsk, g.k1 - g.k0)) ask();
-                    const uint32_t st = kv_it % C::kStages, ph = (kv_it / C::kStages) & 1;
-                    fetch(vc, vsc, p.vs, p.vss, k, pg, wv, sv);
-                    if (!wwait(B_K_EMPTY + st, ph ^ 1)) { ok = false; break; }
-                    unpack(sK + st * C::kKVBytes, wk, sk);
-                    publish(B_K_FULL + st);
-                    if (k + 1 < g.k1) {
+                    const int at = page, slot = ((g.r.f + k) * C::BN + pg * rows) & ((1 << p.page_log2) - 1);
+                    const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, at >= 0)) * rows * (D / 2 + D / 16));
+                    if (k + 1 < g.k1) page = page_of(g, k + 1);
 #pragma unroll
-                        for (int i = 0; i < NP; ++i) pg[i] = pn[i];
-                        fetch(kc, ksc, p.ks, p.kss, k + 1, pg, wk, sk);
-                        if (k + 2 < g.k1) pages_of(k + 2, pn);
+                    for (int v = 0; v < 2; ++v) {
+                        const uint32_t st = it % C::kRaw, dst = sbase + C::kOffRaw + st * C::kRawBytes;
+                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_V_EMPTY + int(st)), ((it / C::kRaw) & 1) ^ 1, abort_flag))) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(bar(B_V_FULL + int(st)), bytes);
+                        __syncwarp();
+                        if (at >= 0) {
+                            const uint8_t* scales = v ? p.v_scales : p.k_scales;
+                            const int64_t from = (at < p.n_pages ? at : 0) * (v ? p.vss[0] : p.kss[0]) + g.hk * (v ? p.vss[1] : p.kss[1]) + slot * (D / 16);
+                            tma_load_4d(dst + box, v ? &tmV : &tmK, bar(B_V_FULL + int(st)), 0, slot, g.hk, at);
+                            bulk_load(dst + sbox, scales + from, uint32_t(rows * (D / 16)), bar(B_V_FULL + int(st)));
+                        }
+                        ++it;
                     }
-                    if (!wwait(B_V_EMPTY + st, ph ^ 1)) { ok = false; break; }
-                    unpack(sV + st * C::kKVBytes, wv, sv);
-                    publish(B_V_FULL + st);
                 }
             }
             if (!ok && lane == 0) fail();
+            drain_ring(bar(B_V_FULL), it, C::kRaw);
         }
     } else if (!Q4 && warp == C::kProdWarp) {
         // ------------------------------------------------------------ loads
@@ -541,6 +578,12 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
         bool ok = true;
         const SDesc dQ0 = sdesc_sw128(sQ, 16, 1024), dQ1 = sdesc_sw128(sQ + C::kQBytes, 16, 1024);
         const SDesc dK0 = sdesc_sw128(sK, 16, 1024), dV0 = sdesc_sw128(sV, C::BN * 128, 1024);
+        // stage and phase of key tile t's K and V: rings of their own, or one ring in turn
+        constexpr int kVFull = Q4 ? B_K_FULL : B_V_FULL, kVEmpty = Q4 ? B_K_EMPTY : B_V_EMPTY;
+        auto k_stage = [](uint32_t t) { return Q4 ? (2 * t) % C::kRing : t % C::kStages; };
+        auto k_phase = [](uint32_t t) { return (Q4 ? (2 * t) / C::kRing : t / C::kStages) & 1; };
+        auto v_stage = [](uint32_t t) { return Q4 ? (2 * t + 1) % C::kRing : t % C::kStages; };
+        auto v_phase = [](uint32_t t) { return (Q4 ? (2 * t + 1) / C::kRing : t / C::kStages) & 1; };
         auto stage = [&](const SDesc& d, uint32_t st) { return SDesc{d.lo + st * (C::kKVBytes >> 4), d.hi}; };
         // S_x = Q K^T, after the tile's previous P V product, which reads P from those columns
         auto issue_s = [&](int x, uint32_t st, int qx) -> bool {
@@ -602,7 +645,7 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
             if (!s.split) {
                 auto act = [&](int x, int j) { return j >= s.a[x] && j < s.b[x]; };
                 {
-                    const uint32_t st = kv_it % C::kStages, ph = (kv_it / C::kStages) & 1;
+                    const uint32_t st = k_stage(kv_it), ph = k_phase(kv_it);
                     if (!wwait(B_K_FULL + st, ph)) { ok = false; break; }
                     if (act(0, s.k0) && !issue_s(0, st, 0)) { ok = false; break; }
                     if (act(1, s.k0) && !issue_s(1, st, 1)) { ok = false; break; }
@@ -611,15 +654,15 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                 }
                 for (int i = 0; i < n && ok; ++i) {
                     const int j = s.k0 + i;
-                    const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
-                    const uint32_t t1 = t + 1, st1 = t1 % C::kStages, ph1 = (t1 / C::kStages) & 1;
-                    if (!wwait(B_V_FULL + st, ph)) { ok = false; break; }
+                    const uint32_t t = kv_it + i, st = v_stage(t), ph = v_phase(t);
+                    const uint32_t t1 = t + 1, st1 = k_stage(t1), ph1 = k_phase(t1);
+                    if (!wwait(kVFull + st, ph)) { ok = false; break; }
                     if (!Q4) clear_v(st, j);
                     if (act(0, j) && !issue_pv(0, st, j == s.a[0])) { ok = false; break; }
                     if (i + 1 < n && !wwait(B_K_FULL + st1, ph1)) { ok = false; break; }
                     if (act(0, j + 1) && !issue_s(0, st1, 0)) { ok = false; break; }
                     if (act(1, j) && !issue_pv(1, st, j == s.a[1])) { ok = false; break; }
-                    commit(B_V_EMPTY + st);
+                    commit(kVEmpty + st);
                     if (act(1, j + 1) && !issue_s(1, st1, 1)) { ok = false; break; }
                     if (i + 1 < n) {
                         commit(B_K_EMPTY + st1);
@@ -629,19 +672,19 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
             } else {
                 // step i: tile x = i & 1 computes P V of step i, then S of step i + 2
                 for (int i = 0; i < 2 && i < n && ok; ++i) {
-                    const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
+                    const uint32_t t = kv_it + i, st = k_stage(t), ph = k_phase(t);
                     if (!wwait(B_K_FULL + st, ph) || !issue_s(i, st, 0)) { ok = false; break; }
                     commit(B_K_EMPTY + st);
                     if (i + 1 == n) commit(B_Q_EMPTY);
                 }
                 for (int i = 0; i < n && ok; ++i) {
                     const int x = i & 1;
-                    const uint32_t t = kv_it + i, st = t % C::kStages, ph = (t / C::kStages) & 1;
-                    const uint32_t t2 = t + 2, st2 = t2 % C::kStages, ph2 = (t2 / C::kStages) & 1;
-                    if (!wwait(B_V_FULL + st, ph)) { ok = false; break; }
+                    const uint32_t t = kv_it + i, st = v_stage(t), ph = v_phase(t);
+                    const uint32_t t2 = t + 2, st2 = k_stage(t2), ph2 = k_phase(t2);
+                    if (!wwait(kVFull + st, ph)) { ok = false; break; }
                     if (!Q4) clear_v(st, s.k0 + i);
                     if (!issue_pv(x, st, i < 2)) { ok = false; break; }
-                    commit(B_V_EMPTY + st);
+                    commit(kVEmpty + st);
                     if (i + 2 < n) {
                         if (!wwait(B_K_FULL + st2, ph2) || !issue_s(x, st2, 0)) { ok = false; break; }
                         commit(B_K_EMPTY + st2);
@@ -1160,11 +1203,12 @@ cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& 
     return p.bias ? launch<64, true, false>(mq, mk, mv, p, num_sms, st) : launch<64, false, false>(mq, mk, mv, p, num_sms, st);
 }
 
-cudaError_t launch_cache_chunk4(int D, const CacheFwdParams& p, int num_sms, cudaStream_t st) {
-    const CUtensorMap none{};  // (everything is loaded by address)
+cudaError_t launch_cache_chunk4(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
+                                cudaStream_t st) {
+    const CUtensorMap none{};  // (queries are loaded by address)
     if (D == 128)
-        return p.bias ? launch<128, true, true>(none, none, none, p, num_sms, st) : launch<128, false, true>(none, none, none, p, num_sms, st);
-    return p.bias ? launch<64, true, true>(none, none, none, p, num_sms, st) : launch<64, false, true>(none, none, none, p, num_sms, st);
+        return p.bias ? launch<128, true, true>(none, mk, mv, p, num_sms, st) : launch<128, false, true>(none, mk, mv, p, num_sms, st);
+    return p.bias ? launch<64, true, true>(none, mk, mv, p, num_sms, st) : launch<64, false, true>(none, mk, mv, p, num_sms, st);
 }
 
 cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int blocks, int num_sms, cudaStream_t st) {

@@ -557,6 +557,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// `bytes` contiguous bytes into shared memory (addresses and size in 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // Lets `kernel` use `bytes` of shared memory per CTA, once per device (done: a bit for each).
 template <typename Kernel>
 cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& done) {
