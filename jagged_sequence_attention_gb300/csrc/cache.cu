@@ -223,7 +223,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g, p.bm), 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);
-    if (chunks && bf16 && !cache->ops) {  // the queries as (D, head, token), boxes of one tile's rows
+    if (chunks && bf16) {  // the queries as (D, head, token), boxes of one tile's rows
         const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
         const int64_t strides[2] = {D, q_stride};
         const cuuint32_t box[3] = {64u, cuuint32_t(p.g), cuuint32_t(pc.tile_tokens)};
@@ -232,7 +232,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     }
     cudaError_t e = cudaSuccess;
     if (cache->ops) {
-        if (chunks) e = cache->ops->chunk(cache, pc, st);
+        if (chunks) e = cache->ops->chunk(cache, mq, pc, st);
         if (e == cudaSuccess) e = cache->ops->decode(cache, p, chunks, st);
     } else {
         if (chunks)

@@ -69,13 +69,13 @@ struct ChkCfg {
     static constexpr int kQBytes = BM * D * 2, kKVBytes = BN * D * 2;
     // K and V rings: what shared memory holds (a short item's keys come from DRAM, and two
     // stages of 16 KB in flight would not keep up with it)
-    // 4 bits: one ring of unpacked tiles, K and V in turn, and one of packed ones
-    static constexpr int kStages = D == 128 ? 2 : 5, kRing = D == 128 ? 3 : 6, kRaw = D == 128 ? 3 : 6;
+    // 4 bits: one ring of unpacked tiles, K and V in turn, and of packed ones a ring each
+    static constexpr int kStages = D == 128 ? 2 : 5, kRing = D == 128 ? 3 : 6, kRaw = 2;
     static constexpr int kRawCodes = BN * D / 2, kRawBytes = kRawCodes + BN * D / 16;
     static constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kQBytes, kOffV = kOffK + (Q4 ? 0 : kStages * kKVBytes);
     static constexpr int kOffRaw = kOffK + kRing * kKVBytes;
-    static constexpr int kOffBar = Q4 ? kOffRaw + kRaw * kRawBytes : kOffV + kStages * kKVBytes;
-    static constexpr int kNumBars = 56;
+    static constexpr int kOffBar = Q4 ? kOffRaw + 2 * kRaw * kRawBytes : kOffV + kStages * kKVBytes;
+    static constexpr int kNumBars = 60;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem slot, abort flag
     static constexpr int kSlots = 4;                          // parts of items handed out and not yet taken by all
     static constexpr int kAsk = 3;                            // key tiles of a part left to load when the next is asked for
@@ -86,14 +86,17 @@ struct ChkCfg {
     static constexpr int kOffGroups = kOffXch + 2 * 2 * 8 * 32 * 4;
     // bias by relative position |r| < kNear, log2 units, of the first kNearHeads heads
     static constexpr int kOffNear = kOffGroups + (int(sizeof(CacheGroups)) + 15) / 16 * 16;
-    // 4 bits: what takes a row's scores back to its queries' size
-    static constexpr int kOffDown = kOffNear + kNearHeads * kNearStride * 4;
-    static constexpr int kSmemNeed = kOffDown + (Q4 ? 2 * BM * 4 : 0) + 1024;
+    static constexpr int kStride = Q4 ? kNear + 1 : kNearStride;  // (shared memory is short by 400 bytes)
+    // 4 bits: what takes a row's scores back to its queries' size [2 BM], behind the m and l in use
+    static constexpr int kOffDown = kOffComb + 2 * 2 * BM * 4;
+    static constexpr int kSmemNeed = kOffNear + kNearHeads * kStride * 4 + 1024;
     // at least 120 KB: one CTA per SM, as the CTA allocates all 512 TMEM columns
     static constexpr int kSmemBytes = kSmemNeed > 120 * 1024 ? kSmemNeed : 120 * 1024;
-    static constexpr int kUnpackWarps = Q4 ? 4 : 0, kWriters = Q4 ? kUnpackWarps : 1;  // writers: of the products' tiles
-    static constexpr int kSoftWarps = 16, kProdWarp = 16, kMmaWarp = 17, kDrawWarp = 18, kUnpackWarp = 19,
-                         kThreads = (kUnpackWarp + kUnpackWarps) * 32;
+    // 4 bits: two warps unpack K's tiles and two V's, half of the rows each, and the first of each two
+    // loads.  One warp each left a thread 96 registers instead of 80, but took longer than a step
+    // (8 prompts 841 us instead of 788); four warps on each tile in turn and a loading one 815.
+    static constexpr int kShare = 2, kWriters = Q4 ? 2 * kShare : 1;
+    static constexpr int kSoftWarps = 16, kMmaWarp = 16, kDrawWarp = 17, kProdWarp = 18, kThreads = (kProdWarp + kWriters) * 32;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdescQK = make_idesc(Q4 ? kFmtF16 : kFmtBF16, BM, BN, false, false);
     static constexpr uint32_t kIdescPV = make_idesc(Q4 ? kFmtF16 : kFmtBF16, BM, D, false, true);
@@ -119,6 +122,8 @@ enum {
     B_V_EMPTY = 40,
     B_SEG_FULL = 46,   // +slot: a part of an item handed out
     B_SEG_EMPTY = 50,  // +slot: and read by every other warp
+    B_Q_RAW = 54,      // 4 bits: queries as they are given
+    B_RAW_EMPTY = 55,  // +stage: packed tiles read, K's, then V's
 };
 
 // TMEM column (within a tile's S/P columns) of the 16 P values of P V step s.
@@ -171,15 +176,17 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
     if (threadIdx.x == 0) {
         mbar_init(bar(B_Q_FULL), C::kWriters);
         mbar_init(bar(B_Q_EMPTY), Q4 ? 1 + C::kSoftWarps : 1);
-        if (Q4) {  // K_*: the ring of unpacked tiles; V_*: of packed ones
+        if (Q4) {  // K_*: the ring of unpacked tiles; V_FULL: of packed ones, K's, then V's
             for (int s = 0; s < C::kRing; ++s) {
-                mbar_init(bar(B_K_FULL + s), C::kWriters);
+                mbar_init(bar(B_K_FULL + s), C::kShare);
                 mbar_init(bar(B_K_EMPTY + s), 1);
             }
-            for (int s = 0; s < C::kRaw; ++s) {
+            for (int s = 0; s < 2 * C::kRaw; ++s) {
                 mbar_init(bar(B_V_FULL + s), 1);
-                mbar_init(bar(B_V_EMPTY + s), C::kUnpackWarps);
+                mbar_init(bar(B_RAW_EMPTY + s), C::kShare);
             }
+            for (int s = 0; s < 3; ++s) mbar_init(bar(B_V_EMPTY + s), 1);  // every third V read
+            mbar_init(bar(B_Q_RAW), 1);
         }
         for (int s = 0; !Q4 && s < C::kStages; ++s) {
             mbar_init(bar(B_K_FULL + s), 1);
@@ -198,14 +205,14 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
         for (int q = 0; q < 8; ++q) mbar_init(bar(B_XCH + q), 2);
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(bar(B_SEG_FULL + s), 1);
-            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + 2 + C::kUnpackWarps);
+            mbar_init(bar(B_SEG_EMPTY + s), C::kSoftWarps + 1 + C::kWriters);
         }
         mbar_init(bar(B_ASK), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == C::kProdWarp && lane == 0) {
-        if (!Q4) tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
     const bool near_ok = BIAS && p.H <= kNearHeads;
     if (near_ok)
         for (int e = threadIdx.x; e < p.H * kNear; e += C::kThreads)
-            near_tab[(e / kNear) * kNearStride + e % kNear] = p.bias[(e / kNear) * 32 + relpos_bucket(e % kNear)] * 1.4426950408889634f;
+            near_tab[(e / kNear) * C::kStride + e % kNear] = p.bias[(e / kNear) * 32 + relpos_bucket(e % kNear)] * 1.4426950408889634f;
     cache_pieces<C::BN>(p, groups);
     tc_fence_before();
     __syncthreads();
@@ -263,22 +270,25 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
         atomicOr(p.status, kStatusTimeout);
     };
 
-    if (Q4 && warp >= C::kUnpackWarp) {
+    if (Q4 && warp >= C::kProdWarp) {
         if constexpr (Q4) {
-            // -------------------------------------------------------- unpacking
-            // A thread takes 32 neighbouring elements of a row at a time, in `kPer` lanes a row:
-            // queries from bf16 with a power of two of their row that brings their largest
-            // magnitude to 2^14, keys and values from 16 bytes of codes and two scales in shared memory
-            // (loaded by address a tile ahead, they came too late: 1478 us instead of @).  What it
-            // writes are four of the eight 16-byte pieces of a 128-byte row of the tile; the lanes of
-            // a row's second half write theirs in another order, so that eight lanes meet all banks.
-            constexpr int kPer = D / 32, kRows = 128 / kPer, NP = 128 / kRows;
-            const int tid = threadIdx.x - 32 * C::kUnpackWarp, quarter = tid % kPer, row0 = tid / kPer;
+            // -------------------------------------------------------- loads and unpacking
+            // Two warps each for K and V; the queries are taken to fp16 by all.  A thread takes 32
+            // neighbouring elements of a row at a time, `kPer` lanes a row: queries from bf16, in
+            // place, with a power of two of their row that brings their largest magnitude to
+            // 2^14, keys and values from 16 bytes of codes and two scales.  What it writes are four
+            // of the eight 16-byte pieces of a 128-byte row of the tile; the lanes of a row's second
+            // half write theirs in another order, so that eight lanes meet all banks.  (Codes
+            // loaded by address, a tile ahead, came too late: 1478 us for the 8 prompts.)
+            constexpr int kPer = D / 32, kRows = 32 / kPer, NP = 4, kGroups = C::BN / (NP * kRows);
+            const int v = (warp - C::kProdWarp) & 1, share = (warp - C::kProdWarp) >> 1, quarter = lane % kPer, row0 = lane / kPer;
             const int turn = D == 128 ? 2 * (quarter >> 1) : 0;  // its order: pieces c ^ turn
             float* down_s = reinterpret_cast<float*>(smem + C::kOffDown);
-            auto piece = [&](uint32_t tile, int row, int c) -> uint32_t {
-                return tile + uint32_t((quarter >> 1) * C::BM * 128 + row * 128 + (((4 * (quarter & 1) + (c ^ turn)) ^ (row & 7)) << 4));
-            };
+            // (rows of a thread are 8 or 16 apart: their pieces lie alike)
+            uint32_t piece[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                piece[c] = uint32_t((quarter >> 1) * C::BM * 128 + row0 * 128 + (((4 * (quarter & 1) + (c ^ turn)) ^ (row0 & 7)) << 4));
             auto wwait = [&](int b, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag));
             };
@@ -287,152 +297,161 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(b));
             };
-            uint32_t kv_it = 0, item_it = 0;
+            uint32_t done = 0, item_it = 0;  // tiles unpacked, items
             bool ok = true;
-            // Tile number j of the rings, key tile k; keys outside the item's become zeros (what lies
-            // there is undefined, and 0 * NaN is not 0).
-            auto unpack = [&](uint32_t j, int k) -> bool {
-                const uint32_t rs = j % C::kRaw, st = j % C::kRing;
-                const uint32_t raw = sbase + C::kOffRaw + rs * C::kRawBytes, tile = sK + st * C::kKVBytes;
-                if (!wwait(B_V_FULL + int(rs), (j / C::kRaw) & 1)) return false;
-                uint4 w[NP];
-                uint32_t sc[NP];
-                const int c0 = (g.r.f + k) * C::BN, lo = g.r.lo - c0, hi = g.r.hi - c0;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int row = kRows * i + row0;
-                    w[i] = ld_shared_v4(raw + uint32_t(row * (D / 2) + ((D == 128 ? quarter ^ ((row >> 1) & 3) : quarter) << 4)));
-                    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
-                                 : "=r"(sc[i])
-                                 : "r"(raw + uint32_t(C::kRawCodes + row * (D / 16) + 2 * quarter)));
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_V_EMPTY + int(rs)));
-                if (lo > 0 || hi < C::BN) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i)
-                        if (kRows * i + row0 < lo || kRows * i + row0 >= hi) sc[i] = 0u;
-                }
-                if (!wwait(B_K_EMPTY + int(st), ((j / C::kRing) & 1) ^ 1)) return false;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const uint32_t two = e4m3_to_f16(sc[i]), s01 = __byte_perm(two, 0u, 0x1010), s23 = __byte_perm(two, 0u, 0x3232);
-                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t h[4];
-                        e2m1_to_f16(turn ? x[c ^ 2] : x[c], h);
-                        const uint32_t s = (c < 2) == (turn == 0) ? s01 : s23;
-                        st_shared_v4(piece(tile, kRows * i + row0, c), f16_mul2(h[0], s), f16_mul2(h[1], s), f16_mul2(h[2], s), f16_mul2(h[3], s));
-                    }
-                }
-                publish(B_K_FULL + int(st));
-                return true;
-            };
-            auto load_q = [&]() {
-                const int rt = p.tile_tokens * p.g, R = g.s.q_len * p.g;
-                const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.Q);
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
-                    if (x && (2 * g.tile + 1) * rt >= R) break;
-#pragma unroll 1
-                    for (int i = 0; i < NP; ++i) {
-                        const int t = kRows * i + row0, r = (2 * g.tile + x) * rt + t;
-                        uint4 q[4];
-                        const bool in = t < rt && r < R;
-                        const int tok = div_g(p, in ? r : 0);
-                        const uint4* src = reinterpret_cast<const uint4*>(Q + (g.s.q0 + tok) * p.q_stride +
-                                                                          int64_t(g.hk * p.g + (in ? r : 0) - tok * p.g) * D + 32 * quarter);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) q[c] = in ? __ldg(src + (c ^ turn)) : make_uint4(0u, 0u, 0u, 0u);
-                        float top = 0.f;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t v[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                top = fmax3(top, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u)));
-                        }
-#pragma unroll
-                        for (int d = 1; d < kPer; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
-                        const float up = __uint_as_float((268u - e) << 23);
-                        if (quarter == 0) down_s[x * C::BM + t] = __uint_as_float((e - 14u) << 23);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t v[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-                            uint32_t h[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                h[k] = pack_f16x2(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
-                            st_shared_v4(piece(sQ + x * C::kQBytes, t, c), h[0], h[1], h[2], h[3]);
-                        }
-                    }
-                }
-            };
-            while (ok && next()) {
-                if (g.r.n == 0) continue;
-                if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
-                load_q();
-                publish(B_Q_FULL);
-                ++item_it;
-                for (int k = g.k0; k < g.k1 && ok; ++k, ++kv_it) ok = unpack(2 * kv_it, k) && unpack(2 * kv_it + 1, k);
-            }
-            if (!ok && lane == 0) fail();
-        }
-    } else if (Q4 && warp == C::kProdWarp) {
-        if constexpr (Q4) {
-            // -------------------------------------------------------- loads of packed tiles
-            // A lane loads one box of each tile, the codes of a page (or of 64 keys of one), and its scales.
+            // Loads: a lane takes one box of each tile, the codes of a page (or of 64 keys of one), and
+            // its scales.
+            const CUtensorMap* map = v ? &tmV : &tmK;
+            const uint8_t* scales = v ? p.v_scales : p.k_scales;
+            const int64_t s_page = v ? p.vss[0] : p.kss[0], s_head = v ? p.vss[1] : p.kss[1];
             const int rows = min(1 << p.page_log2, 64), per = C::BN / rows;
-            const int pg = lane;
-            const bool mine = lane < per;
-            const uint32_t box = uint32_t(pg * rows * (D / 2)), sbox = uint32_t(C::kRawCodes + pg * rows * (D / 16));
-            uint32_t it = 0;
-            bool ok = true;
-            auto page_of = [&](const CacheSeg& s, int k) -> int {
-                const int j = (s.r.f + k) * C::BN + pg * rows;
-                if (!mine || j >= s.r.hi || j + rows <= s.r.lo) return -1;
-                const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
-                if (page >= 0 && page < p.n_pages) return page;
+            const uint32_t raw0 = sbase + C::kOffRaw + v * C::kRaw * C::kRawBytes;
+            uint32_t issued = 0;
+            int lk = 0, page = -1;           // the next key tile to load, and its page
+            auto page_of = [&](int k) -> int {
+                const int j = (g.r.f + k) * C::BN + lane * rows;
+                if (lane >= per || k >= g.k1 || j >= g.r.hi || j + rows <= g.r.lo) return -1;
+                const int at = p.table[size_t(g.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
+                if (at >= 0 && at < p.n_pages) return at;
                 atomicOr(p.status, kStatusBounds);
                 return p.n_pages;  // past the cache: codes read as zeros (with any scales)
             };
-            auto ask = [&]() {
-                if (lane == 0) mbar_arrive(bar(B_ASK));
+            // The next tile into its place, which this warp has read.
+            auto load_tile = [&]() {
+                if (share || lk >= g.k1) return;
+                const uint32_t st = issued % C::kRaw, dst = raw0 + st * C::kRawBytes;
+                const uint32_t full_b = bar(B_V_FULL + v * C::kRaw + int(st));
+                if (!v && g.k1 - lk == min(C::kAsk, g.k1 - g.k0) && lane == 0) mbar_arrive(bar(B_ASK));
+                if (!wwait(B_RAW_EMPTY + v * C::kRaw + int(st), ((issued / C::kRaw) & 1) ^ 1)) { ok = false; return; }
+                const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, page >= 0)) * rows * (D / 2 + D / 16));
+                if (lane == 0) mbar_arrive_expect_tx(full_b, bytes);
+                __syncwarp();
+                if (page >= 0) {
+                    const int slot = ((g.r.f + lk) * C::BN + lane * rows) & ((1 << p.page_log2) - 1);
+                    tma_load_4d(dst + lane * rows * (D / 2), map, full_b, 0, slot, g.hk, page);
+                    bulk_load(dst + C::kRawCodes + lane * rows * (D / 16),
+                              scales + (page < p.n_pages ? page : 0) * s_page + g.hk * s_head + slot * (D / 16), uint32_t(rows * (D / 16)), full_b);
+                }
+                ++issued;
+                page = page_of(++lk);
+            };
+            // The next tile, of key tile k; keys outside the item's become zeros (what lies there is
+            // undefined, and 0 * NaN is not 0).
+            auto unpack = [&](int k) -> bool {
+                const uint32_t rs = done % C::kRaw, at = 2 * done + v, st = at % C::kRing;
+                const uint32_t raw = raw0 + rs * C::kRawBytes, tile = sK + st * C::kKVBytes;
+                const int c0 = (g.r.f + k) * C::BN, lo = g.r.lo - c0, hi = g.r.hi - c0;
+                const bool edge = lo > 0 || hi < C::BN;
+                uint4 w[2][NP];
+                uint32_t sc[2][NP];
+                auto fetch = [&](int n) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const int row = kRows * (NP * (C::kShare * n + share) + i) + row0;
+                        w[n & 1][i] = ld_shared_v4(raw + uint32_t(row * (D / 2) + ((D == 128 ? quarter ^ ((row >> 1) & 3) : quarter) << 4)));
+                        uint16_t two;
+                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(raw + uint32_t(C::kRawCodes + row * (D / 16) + 2 * quarter)));
+                        sc[n & 1][i] = two;
+                        if (edge && (row < lo || row >= hi)) sc[n & 1][i] = 0u;
+                    }
+                };
+                if (!wwait(B_V_FULL + v * C::kRaw + int(rs), (done / C::kRaw) & 1)) return false;
+                fetch(0);
+                // (A place's barrier tells its last use from the one before by parity alone, and V may
+                // run ahead of K by two: a split item's keys are read up to two tiles before its
+                // values.  So V's third last tile, which had this place two uses ago, is seen read first.)
+                if (v && done >= 3 && !wwait(B_V_EMPTY + int(done % 3), (done / 3 - 1) & 1)) return false;
+                if (!wwait(B_K_EMPTY + int(st), ((at / C::kRing) & 1) ^ 1)) return false;
+#pragma unroll
+                for (int n = 0; n < kGroups / C::kShare; ++n) {
+                    if (n + 1 < kGroups / C::kShare) {
+                        fetch(n + 1);
+                    } else {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_RAW_EMPTY + v * C::kRaw + int(rs)));
+                    }
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const uint32_t two = e4m3_to_f16(sc[n & 1][i]);
+                        const uint32_t s0 = __byte_perm(two, 0u, turn ? 0x3232 : 0x1010), s1 = __byte_perm(two, 0u, turn ? 0x1010 : 0x3232);
+                        const uint4 u = w[n & 1][i];
+                        const uint32_t x[4] = {turn ? u.z : u.x, turn ? u.w : u.y, turn ? u.x : u.z, turn ? u.y : u.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t h[4];
+                            e2m1_to_f16(x[c], h);
+                            const uint32_t s = c < 2 ? s0 : s1;
+                            st_shared_v4(tile + piece[c] + uint32_t(kRows * (NP * (C::kShare * n + share) + i) * 128), f16_mul2(h[0], s), f16_mul2(h[1], s),
+                                         f16_mul2(h[2], s), f16_mul2(h[3], s));
+                        }
+                    }
+                }
+                publish(B_K_FULL + int(st));
+                ++done;
+                return true;
+            };
+            auto convert_q = [&](int tiles) {
+#pragma unroll 1
+                for (int r0 = kRows * (warp - C::kProdWarp); r0 < tiles * C::BM; r0 += C::kWriters * kRows) {
+                    const uint32_t tile = sQ + uint32_t((r0 >= C::BM ? C::kQBytes : 0) + (r0 & (C::BM - 1)) * 128);
+                    uint4 q[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) q[c] = ld_shared_v4(tile + piece[c]);
+                    float top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t v[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            top = fmax3(top, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u)));
+                    }
+#pragma unroll
+                    for (int d = 1; d < kPer; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const uint32_t e = min(max(__float_as_uint(top) >> 23, 15u), 254u);  // (rows past the tile's hold anything)
+                    const float up = __uint_as_float((268u - e) << 23);
+                    if (quarter == 0) down_s[r0 + row0] = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t v[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            h[k] = pack_f16x2(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+                        st_shared_v4(tile + piece[c], h[0], h[1], h[2], h[3]);
+                    }
+                }
             };
             while (ok && next()) {
                 if (g.r.n == 0) {
-                    ask();
+                    if (warp == C::kProdWarp && lane == 0) mbar_arrive(bar(B_ASK));
                     continue;
                 }
-                int page = page_of(g, g.k0);
+                lk = g.k0;
+                page = share ? -1 : page_of(lk);
+#pragma unroll 1
+                for (int i = 0; i < C::kRaw; ++i) load_tile();
+                if (!wwait(B_Q_EMPTY, (item_it & 1) ^ 1)) { ok = false; break; }
+                const int tiles = (2 * g.tile + 1) * p.tile_tokens < g.s.q_len ? 2 : 1;
+                if (warp == C::kProdWarp) {  // a box per tile and column block; tokens past the sequence's are not stored
+                    if (lane == 0) mbar_arrive_expect_tx(bar(B_Q_RAW), uint32_t(tiles * C::kCB * p.tile_tokens * p.g * 128));
+                    __syncwarp();
+                    if (lane < tiles * C::kCB)
+                        tma_load_3d(sQ + (lane / C::kCB) * C::kQBytes + (lane % C::kCB) * C::BM * 128, &tmQ, bar(B_Q_RAW),
+                                    (lane % C::kCB) * 64, g.hk * p.g, g.s.q0 + (2 * g.tile + lane / C::kCB) * p.tile_tokens);
+                }
+                ++item_it;
+                if (!wwait(B_Q_RAW, (item_it - 1) & 1)) { ok = false; break; }
+                convert_q(tiles);
+                publish(B_Q_FULL);
+#pragma unroll 1
                 for (int k = g.k0; k < g.k1 && ok; ++k) {
-                    if (g.k1 - k == min(C::kAsk, g.k1 - g.k0)) ask();
-                    const int at = page, slot = ((g.r.f + k) * C::BN + pg * rows) & ((1 << p.page_log2) - 1);
-                    const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, at >= 0)) * rows * (D / 2 + D / 16));
-                    if (k + 1 < g.k1) page = page_of(g, k + 1);
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const uint32_t st = it % C::kRaw, dst = sbase + C::kOffRaw + st * C::kRawBytes;
-                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_V_EMPTY + int(st)), ((it / C::kRaw) & 1) ^ 1, abort_flag))) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(bar(B_V_FULL + int(st)), bytes);
-                        __syncwarp();
-                        if (at >= 0) {
-                            const uint8_t* scales = v ? p.v_scales : p.k_scales;
-                            const int64_t from = (at < p.n_pages ? at : 0) * (v ? p.vss[0] : p.kss[0]) + g.hk * (v ? p.vss[1] : p.kss[1]) + slot * (D / 16);
-                            tma_load_4d(dst + box, v ? &tmV : &tmK, bar(B_V_FULL + int(st)), 0, slot, g.hk, at);
-                            bulk_load(dst + sbox, scales + from, uint32_t(rows * (D / 16)), bar(B_V_FULL + int(st)));
-                        }
-                        ++it;
-                    }
+                    ok = unpack(k);
+                    if (ok) load_tile();
                 }
             }
             if (!ok && lane == 0) fail();
-            drain_ring(bar(B_V_FULL), it, C::kRaw);
+            if (warp == C::kProdWarp && item_it > 0) mbar_wait_bounded(bar(B_Q_RAW), (item_it - 1) & 1, nullptr);
+            drain_ring(bar(B_V_FULL + v * C::kRaw), issued, C::kRaw);
         }
     } else if (!Q4 && warp == C::kProdWarp) {
         // ------------------------------------------------------------ loads
@@ -663,6 +682,7 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                     if (act(0, j + 1) && !issue_s(0, st1, 0)) { ok = false; break; }
                     if (act(1, j) && !issue_pv(1, st, j == s.a[1])) { ok = false; break; }
                     commit(kVEmpty + st);
+                    if (Q4) commit(B_V_EMPTY + t % 3);
                     if (act(1, j + 1) && !issue_s(1, st1, 1)) { ok = false; break; }
                     if (i + 1 < n) {
                         commit(B_K_EMPTY + st1);
@@ -685,6 +705,7 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                     if (!Q4) clear_v(st, s.k0 + i);
                     if (!issue_pv(x, st, i < 2)) { ok = false; break; }
                     commit(kVEmpty + st);
+                    if (Q4) commit(B_V_EMPTY + t % 3);
                     if (i + 2 < n) {
                         if (!wwait(B_K_FULL + st2, ph2) || !issue_s(x, st2, 0)) { ok = false; break; }
                         commit(B_K_EMPTY + st2);
@@ -782,7 +803,8 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                 }
                 if (!wwait(B_S_FULL + x, s_cnt & 1)) { ok = false; break; }
                 tc_fence_after();
-                // Without a bias both chunks' scores are held at a time, with one they are taken one
+                // Without a bias both chunks' scores are held at a time, with one (and over 4 bits, where a
+                // thread has 80 registers: 916 -> 788 us for the prompts) they are taken one
                 // by one in rolled loops: the three ways of its lookup would otherwise be laid out
                 // four times, and a short item pays for every line of code it fetches.  (A path for
                 // two plain chunks beside it made steps with a bias slower: 67 -> 73 us for nine prompts
@@ -827,7 +849,7 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
                             for (int e = 0; e < 32; ++e)
                                 r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), xs, e < e1 ? v0 : e < e2 ? v1 : v2));
                         } else if (near_ok) {
-                            const float* tab = near_tab + head * kNearStride;
+                            const float* tab = near_tab + head * C::kStride;
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), xs, tab[abs(rk - e)] - shift));
@@ -1203,12 +1225,11 @@ cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& 
     return p.bias ? launch<64, true, false>(mq, mk, mv, p, num_sms, st) : launch<64, false, false>(mq, mk, mv, p, num_sms, st);
 }
 
-cudaError_t launch_cache_chunk4(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
-                                cudaStream_t st) {
-    const CUtensorMap none{};  // (queries are loaded by address)
+cudaError_t launch_cache_chunk4(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p,
+                                int num_sms, cudaStream_t st) {
     if (D == 128)
-        return p.bias ? launch<128, true, true>(none, mk, mv, p, num_sms, st) : launch<128, false, true>(none, mk, mv, p, num_sms, st);
-    return p.bias ? launch<64, true, true>(none, mk, mv, p, num_sms, st) : launch<64, false, true>(none, mk, mv, p, num_sms, st);
+        return p.bias ? launch<128, true, true>(mq, mk, mv, p, num_sms, st) : launch<128, false, true>(mq, mk, mv, p, num_sms, st);
+    return p.bias ? launch<64, true, true>(mq, mk, mv, p, num_sms, st) : launch<64, false, true>(mq, mk, mv, p, num_sms, st);
 }
 
 cudaError_t launch_cache_merge(int D, const CacheFwdParams& p, int blocks, int num_sms, cudaStream_t st) {

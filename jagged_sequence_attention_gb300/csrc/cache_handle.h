@@ -15,7 +15,7 @@ namespace jfa {
 // What a cache held in 4 bits does in place of the 16- and 32-bit kernels.
 struct CacheOps {
     cudaError_t (*append)(jfa_cache c, CacheAppendParams p, cudaStream_t st);
-    cudaError_t (*chunk)(jfa_cache c, const CacheFwdParams& p, cudaStream_t st);
+    cudaError_t (*chunk)(jfa_cache c, const CUtensorMap& mq, const CacheFwdParams& p, cudaStream_t st);
     cudaError_t (*decode)(jfa_cache c, const CacheFwdParams& p, bool early, cudaStream_t st);
     size_t (*decode_part_bytes)(int D, int num_sms);
 };

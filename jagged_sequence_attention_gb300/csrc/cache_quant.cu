@@ -29,8 +29,8 @@ cudaError_t launch_cache_decode4(int D, const CUtensorMap& mk, const CUtensorMap
                                  int num_sms, cudaStream_t st);
 size_t cache_decode4_part_bytes(int D, int num_sms);
 // Items of 256 packed rows.
-cudaError_t launch_cache_chunk4(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
-                                cudaStream_t st);
+cudaError_t launch_cache_chunk4(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p,
+                                int num_sms, cudaStream_t st);
 
 namespace {
 
@@ -275,8 +275,8 @@ cudaError_t decode4(jfa_cache c, const CacheFwdParams& p, bool early, cudaStream
     return launch_cache_decode4(c->D, c->mk, c->mv, p, early, c->num_sms, st);
 }
 
-cudaError_t chunk4(jfa_cache c, const CacheFwdParams& p, cudaStream_t st) {
-    return launch_cache_chunk4(c->D, c->mk, c->mv, p, c->num_sms, st);
+cudaError_t chunk4(jfa_cache c, const CUtensorMap& mq, const CacheFwdParams& p, cudaStream_t st) {
+    return launch_cache_chunk4(c->D, mq, c->mk, c->mv, p, c->num_sms, st);
 }
 
 const CacheOps kQuantOps = {append4, chunk4, decode4, cache_decode4_part_bytes};
