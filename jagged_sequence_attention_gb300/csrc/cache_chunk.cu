@@ -348,7 +348,7 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
                         const int row = kRows * (NP * (C::kShare * n + share) + i) + row0;
-                        w[n & 1][i] = ld_shared_v4(raw + uint32_t(row * (D / 2) + ((D == 128 ? quarter ^ ((row >> 1) & 3) : quarter) << 4)));
+                        w[n & 1][i] = ld_shared_v4(raw + uint32_t(row * (D / 2) + 16 * quarter));
                         uint16_t two;
                         asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(raw + uint32_t(C::kRawCodes + row * (D / 16) + 2 * quarter)));
                         sc[n & 1][i] = two;

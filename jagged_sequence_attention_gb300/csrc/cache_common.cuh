@@ -72,6 +72,7 @@ struct CacheFwdParams {
     const uint8_t* k_scales; // a 4-bit cache's scales, and their page and head strides in bytes
     const uint8_t* v_scales;
     int64_t kss[2], vss[2];
+    int dense;               // a head's codes of one page lie in one piece
     const int32_t* lists;    // [T, Hkv, n_list] blocks (pages) of a token and key head, or nullptr
     int n_list;
 };
@@ -198,13 +199,13 @@ __device__ __forceinline__ CacheSeq cache_lane_seq(const CacheFwdParams& p, int 
     return s;
 }
 
-// Entry e of a token's list: its block, -1 if there is none to read.  Entries ascend and end with
-// -1 (each is compared with the one before it alone); blocks past the token's own hold no key
-// that it may see.
-__device__ __forceinline__ int cache_list_block(const int32_t* list, int e, int own_block, int* status) {
-    const int block = list[e], before = e > 0 ? list[e - 1] : -1;
+// A list's entry, `before` the one before it (kNoEntry: there is none): its block, or -1 if there
+// is none to read.  Entries ascend and end with -1 (each is compared with the one before it
+// alone); blocks past the token's own hold no key that it may see.
+constexpr int kNoEntry = INT_MIN;
+__device__ __forceinline__ int cache_list_block(int block, int before, int own_block, int* status) {
     if (block < 0) return -1;
-    if (e > 0 && (before < 0 || block <= before)) {
+    if (before != kNoEntry && (before < 0 || block <= before)) {
         atomicOr(status, kStatusBounds);
         return -1;
     }

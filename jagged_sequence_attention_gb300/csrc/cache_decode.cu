@@ -117,30 +117,90 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         int kt = g.k0;
         // A stage's page: -1 outside the item's keys (not loaded); past the cache (read as
         // zeros) for a bad entry.
-        int base = 0;  // lists: the position of the stage's first key in this lane's box
         auto page_of = [&](const CacheSeg& s, int k) -> int {
             const int j = (s.r.f + k) * BN + pg * rows;
-            int block = j >> p.page_log2;
-            if constexpr (LIST) {
-                base = kNoBlock;
-                if (!mine || j >= s.r.hi) return -1;
-                const int at = s.s.kv_len - s.s.q_len + s.tile;  // the token's position
-                block = cache_list_block(p.lists + (size_t(s.s.q0 + s.tile) * size_t(p.Hkv) + size_t(s.hk)) * size_t(p.n_list), block,
-                                         at >> p.page_log2, p.status);
-                if (block < 0) return -1;
-                base = (block << p.page_log2) + (j & ((1 << p.page_log2) - 1));
-                if (base > at) return -1;
-            }
             if (!mine || j >= s.r.hi || j + rows <= s.r.lo) return -1;
-            const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(block)];
+            const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(j >> p.page_log2)];
             if (page >= 0 && page < p.n_pages) return page;
             atomicOr(p.status, kStatusBounds);
             return p.n_pages;
         };
+        // Lists: a stage, as this lane sees it (its block, -1: nothing to load; that block's page, the
+        // slot and the position of the first key).  Its entry is asked for two stages before it is loaded,
+        // its page one stage, so that the stream waits for neither.
+        struct Stage {
+            bool have, head;
+            int hk, block, before, slot, base, page, at;
+            size_t row;  // of the page table
+        };
+        auto step = [&](Stage& s) {
+            while (have && (g.r.n == 0 || kt >= g.k1)) {
+                have = cur.next(p, g);
+                kt = g.k0;
+            }
+            s.have = have;
+            s.block = -1;
+            s.base = kNoBlock;
+            if (!have) return;
+            const int j = kt++ * BN + pg * rows;
+            s.hk = g.hk;
+            s.slot = j & ((1 << p.page_log2) - 1);
+            s.row = size_t(g.b) * size_t(p.max_pages);
+            if (!mine || j >= g.r.hi) return;
+            const int e = j >> p.page_log2;
+            const int32_t* list = p.lists + (size_t(g.s.q0 + g.tile) * size_t(p.Hkv) + size_t(g.hk)) * size_t(p.n_list);
+            s.at = g.s.kv_len - g.s.q_len + g.tile;  // the token's position
+            s.block = list[e];
+            s.before = list[max(e - 1, 0)];
+            s.head = e == 0;
+        };
+        auto look = [&](Stage& s) {
+            if (s.block >= 0) {
+                s.block = cache_list_block(s.block, s.head ? kNoEntry : max(s.before, -1), s.at >> p.page_log2, p.status);
+                s.base = (s.block << p.page_log2) + s.slot;
+                if (s.base > s.at) s.block = -1;
+            }
+            s.page = s.block >= 0 ? p.table[s.row + size_t(s.block)] : -1;
+        };
+        if constexpr (LIST) {
+            Stage now, next;
+            step(now);
+            look(now);
+            step(next);
+            while (now.have) {
+                const Stage s = now;
+                now = next;
+                if (now.have) {
+                    look(now);
+                    step(next);
+                }
+                const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(st), ph ^ 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const bool in = s.block >= 0;
+                const int n = __popc(__ballot_sync(0xffffffffu, in));
+                if (lane < per) bases[st * C::kBoxes + pg] = in ? s.base : kNoBlock;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(full(st), uint32_t(n * rows * 128));
+                __syncwarp();
+                if (in) {
+                    int page = s.page;
+                    if (page < 0 || page >= p.n_pages) {
+                        atomicOr(p.status, kStatusBounds);
+                        page = p.n_pages;  // past the cache: read as zeros
+                    }
+                    tma_load_4d(sbase + st * C::kStage + box, map, full(st), cb * 64, s.slot, s.hk, page);
+                }
+                ++it;
+            }
+            have = false;
+        }
         while (have && (g.r.n == 0)) have = cur.next(p, g), kt = g.k0;
         int page = have ? page_of(g, kt) : -1;
         while (have) {
-            const int at = page, j0 = (g.r.f + kt) * BN + pg * rows, hk = g.hk, base0 = base;
+            const int at = page, j0 = (g.r.f + kt) * BN + pg * rows, hk = g.hk;
             if (++kt >= g.k1) {
                 do {
                     have = cur.next(p, g);
@@ -154,10 +214,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 break;
             }
             const int n = __popc(__ballot_sync(0xffffffffu, at >= 0));
-            if constexpr (LIST) {
-                if (lane < per) bases[st * C::kBoxes + pg] = at >= 0 ? base0 : kNoBlock;
-                __syncwarp();
-            }
             if (lane == 0) mbar_arrive_expect_tx(full(st), uint32_t(n * rows * 128));
             __syncwarp();
             if (at >= 0)

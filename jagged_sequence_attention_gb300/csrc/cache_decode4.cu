@@ -20,8 +20,8 @@
 // 2^14: they keep all of their bits down to 2^-28 of it (2^-39 of it is lost at most).
 // P = 2^6 softmax weights against a maximum that moves lazily (at most 2^14), in fp16: 2^-11 of each
 // weight, and 2^-31 of the largest.  Sums are taken in fp32 before.
-// Stages of 128 keys pass through a ring of 54 KB per CTA; one warp issues the loads (a box of codes
-// and a row of scales for each page), four warps take a quarter of each stage's keys.
+// Stages pass through a ring of 72 KB per CTA; one warp issues the loads (a box of codes and a row of
+// scales for each page), eight (or four) warps take 32 keys of each stage.
 #include "cache_common.cuh"
 #include "quant.cuh"
 #include "tilemath.cuh"
@@ -34,12 +34,15 @@ size_t cache_decode4_part_bytes(int D, int num_sms);
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);
 constexpr float kLift = 6.f;  // log2 of the weights' factor
 
 template <int D, int NT>
 struct Cfg {
-    static constexpr int BN = 128, BM = 8 * NT, kCtas = NT == 1 ? 3 : 2;
+    // (eight consumer warps a CTA, two CTAs an SM, at 96 registers: 64 histories of 4-bit keys 84 us
+    // instead of 75)
+    static constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1), kCtas = NT == 1 ? 3 : 2;
+    static constexpr int BN = 32 * kWarps, BM = 8 * NT;
+    static constexpr int kSlotsN = kWarps / 2;               // tiles of 8 rows in the merge of the warps
     static constexpr int kRow = D / 2, kScales = D / 16;     // bytes of a key's codes and scales
     static constexpr int kCodes = BN * kRow;
     static constexpr int kOffKS = 2 * kCodes, kOffVS = kOffKS + BN * kScales;
@@ -48,7 +51,7 @@ struct Cfg {
     static constexpr int kPitch = D + 4;                     // floats of a row in the merge's slots
     static constexpr int kSlot = 8 * kPitch;
     static constexpr int kOffSlots = kStages * kStage;
-    static constexpr int kSlots = 2 * kSlot * 4 > 8192 ? 2 * kSlot * 4 : 8192;
+    static constexpr int kSlots = kSlotsN * kSlot * 4 > 8192 ? kSlotsN * kSlot * 4 : 8192;
     static constexpr int kOffML = kOffSlots + kSlots;        // [2 buffers][m, l][warp][row]
     static constexpr int kOffBias = kOffML + 2 * 2 * kWarps * 16 * 4;
     static constexpr int kOffBar = kOffBias + 16 * 33 * 4;
@@ -91,20 +94,22 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <int WARPS>
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
+}
 
 // Key of 16 that is row i of the product.
-template <int D>
 __device__ __forceinline__ int key_of(int i) {
-    return D == 128 ? (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1) : (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3);
+    return (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3);
 }
 
 template <int D, bool BIAS, bool LIST, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
+__global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
     jfa_cache_decode4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const CacheFwdParams p) {
     using C = Cfg<D, NT>;
-    constexpr int BM = C::BM, BN = C::BN, KG = 2, MT = D / 16, KS = D / 16, NR = 2 * NT;
+    constexpr int kWarps = C::kWarps, BM = C::BM, BN = C::BN, KG = 2, MT = D / 16, KS = D / 16, NR = 2 * NT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -133,71 +138,97 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 
     if (warp == kWarps) {
         // ---------------------------------------------------------------- producer
-        // A lane loads one box of each stage, K or V of a page, and its scales.
+        // A lane loads a page's (or 64 keys' of one) part of each stage: K and V, codes and scales.
         fence_proxy_async_smem();  // the scratch's writes before the first loads into it
         const int rows = min(1 << p.page_log2, 64);          // keys of a box
         const int per = BN / rows;                           // pages (or parts of one) in a stage
-        const bool mine = lane < 2 * per;
-        const int pg = lane % per, isv = lane / per;
-        const uint32_t box = uint32_t(isv * C::kCodes + pg * rows * C::kRow);
-        const uint32_t sbox = uint32_t((isv ? C::kOffVS : C::kOffKS) + pg * rows * C::kScales);
-        const CUtensorMap* map = isv ? &tmV : &tmK;
-        const uint8_t* scales = isv ? p.v_scales : p.k_scales;
-        const int64_t s_page = isv ? p.vss[0] : p.kss[0], s_head = isv ? p.vss[1] : p.kss[1];
+        const int pg = lane;
+        const bool mine = lane < per;
+        const uint32_t box = uint32_t(pg * rows * C::kRow), sbox = uint32_t(C::kOffKS + pg * rows * C::kScales);
         uint32_t it = 0;
-        bool ok = true, have = cur.next(p, g);
+        bool ok = true, more = cur.next(p, g);
         int kt = g.k0;
-        int base = 0;  // lists: the position of the stage's first key in this lane's box
-        // A stage's page: -1 outside the item's keys (not loaded); past the cache (codes read as
-        // zeros) for a bad entry.
-        auto page_of = [&](const CacheSeg& s, int k) -> int {
-            const int j = (s.r.f + k) * BN + pg * rows;
-            int block = j >> p.page_log2;
-            if constexpr (LIST) {
-                base = kNoBlock;
-                if (!mine || j >= s.r.hi) return -1;
-                const int at = s.s.kv_len - s.s.q_len + s.tile;  // the token's position
-                block = cache_list_block(p.lists + (size_t(s.s.q0 + s.tile) * size_t(p.Hkv) + size_t(s.hk)) * size_t(p.n_list), block,
-                                         at >> p.page_log2, p.status);
-                if (block < 0) return -1;
-                base = (block << p.page_log2) + (j & ((1 << p.page_log2) - 1));
-                if (base > at) return -1;
-            }
-            if (!mine || j >= s.r.hi || j + rows <= s.r.lo) return -1;
-            const int page = p.table[size_t(s.b) * size_t(p.max_pages) + size_t(block)];
-            if (page >= 0 && page < p.n_pages) return page;
-            atomicOr(p.status, kStatusBounds);
-            return p.n_pages;
+        // A stage, as this lane sees it: its block of the sequence (-1: nothing to load), that block's page,
+        // the slot and the position of the first key.  Its list entry is asked for two stages before it
+        // is loaded, its page one stage, so that the stream waits for neither.
+        struct Stage {
+            bool have, head;
+            int hk, block, before, slot, base, page, at;
+            size_t row;  // of the page table
         };
-        while (have && (g.r.n == 0)) have = cur.next(p, g), kt = g.k0;
-        int page = have ? page_of(g, kt) : -1;
-        while (have) {
-            const int at = page, j0 = (g.r.f + kt) * BN + pg * rows, hk = g.hk, base0 = base;
-            if (++kt >= g.k1) {
-                do {
-                    have = cur.next(p, g);
-                    kt = g.k0;
-                } while (have && g.r.n == 0);
+        auto step = [&](Stage& s) {
+            while (more && (g.r.n == 0 || kt >= g.k1)) {
+                more = cur.next(p, g);
+                kt = g.k0;
             }
-            if (have) page = page_of(g, kt);
+            s.have = more;
+            s.block = -1;
+            s.base = kNoBlock;
+            if (!more) return;
+            const int j = (g.r.f + kt++) * BN + pg * rows;
+            s.hk = g.hk;
+            s.slot = j & ((1 << p.page_log2) - 1);
+            s.row = size_t(g.b) * size_t(p.max_pages);
+            if (!mine || j >= g.r.hi || (!LIST && j + rows <= g.r.lo)) return;
+            const int e = j >> p.page_log2;
+            s.block = e;
+            if constexpr (LIST) {
+                const int32_t* list = p.lists + (size_t(g.s.q0 + g.tile) * size_t(p.Hkv) + size_t(g.hk)) * size_t(p.n_list);
+                s.at = g.s.kv_len - g.s.q_len + g.tile;  // the token's position
+                s.block = list[e];
+                s.before = list[max(e - 1, 0)];
+                s.head = e == 0;
+            }
+        };
+        auto look = [&](Stage& s) {
+            if (LIST && s.block >= 0) {
+                s.block = cache_list_block(s.block, s.head ? kNoEntry : max(s.before, -1), s.at >> p.page_log2, p.status);
+                s.base = (s.block << p.page_log2) + s.slot;
+                if (s.base > s.at) s.block = -1;
+            }
+            s.page = s.block >= 0 ? p.table[s.row + size_t(s.block)] : -1;
+        };
+        Stage now, next;
+        step(now);
+        look(now);
+        step(next);
+        while (now.have) {
+            const Stage s = now;
+            now = next;
+            if (now.have) {
+                look(now);
+                step(next);
+            }
             const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(st), ph ^ 1, abort_flag))) {
                 ok = false;
                 break;
             }
-            const int n = __popc(__ballot_sync(0xffffffffu, at >= 0));
+            const bool in = s.block >= 0;
+            const int n = __popc(__ballot_sync(0xffffffffu, in));
             if constexpr (LIST) {
-                if (lane < per) bases[st * C::kBoxes + pg] = at >= 0 ? base0 : kNoBlock;
+                if (mine) bases[st * C::kBoxes + pg] = in ? s.base : kNoBlock;
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive_expect_tx(full(st), uint32_t(n * rows * (C::kRow + C::kScales)));
+            if (lane == 0) mbar_arrive_expect_tx(full(st), uint32_t(n * rows * 2 * (C::kRow + C::kScales)));
             __syncwarp();
-            if (at >= 0) {
-                const int slot = j0 & ((1 << p.page_log2) - 1);
-                tma_load_4d(sbase + st * C::kStage + box, map, full(st), 0, slot, hk, at);
-                // (any scales will do for codes that read as zeros)
-                bulk_load(sbase + st * C::kStage + sbox, scales + (at < p.n_pages ? at : 0) * s_page + hk * s_head + slot * C::kScales,
-                          uint32_t(rows * C::kScales), full(st));
+            if (in) {
+                const uint32_t dst = sbase + st * C::kStage, bytes = uint32_t(rows * C::kScales), codes = uint32_t(rows * C::kRow);
+                // (a bad entry is reported; any page will do for it)
+                const bool bad = s.page < 0 || s.page >= p.n_pages;
+                if (bad) atomicOr(p.status, kStatusBounds);
+                const int page = bad ? 0 : s.page;
+                if (p.dense) {
+                    bulk_load(dst + box, static_cast<const uint8_t*>(p.K) + page * p.ks[0] + s.hk * p.ks[2] + s.slot * C::kRow, codes, full(st));
+                    bulk_load(dst + C::kCodes + box, static_cast<const uint8_t*>(p.V) + page * p.vs[0] + s.hk * p.vs[2] + s.slot * C::kRow, codes,
+                              full(st));
+                } else {
+                    tma_load_4d(dst + box, &tmK, full(st), 0, s.slot, s.hk, page);
+                    tma_load_4d(dst + C::kCodes + box, &tmV, full(st), 0, s.slot, s.hk, page);
+                }
+                bulk_load(dst + sbox, p.k_scales + page * p.kss[0] + s.hk * p.kss[1] + s.slot * C::kScales, bytes, full(st));
+                bulk_load(dst + (C::kOffVS - C::kOffKS) + sbox, p.v_scales + page * p.vss[0] + s.hk * p.vss[1] + s.slot * C::kScales, bytes,
+                          full(st));
             }
             ++it;
         }
@@ -217,10 +248,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     const int quad = lane & 3, qrow = lane >> 2;
     uint32_t it = 0, seg_no = 0;
     bool ok = true;
-    const int kkey = key_of<D>(qrow);                        // this lane's key of a fragment's first 8 (and 8 on)
+    const int kkey = key_of(qrow);                        // this lane's key of a fragment's first 8 (and 8 on)
     int vkey[4];                                             // its four keys of V^T
 #pragma unroll
-    for (int c = 0; c < 4; ++c) vkey[c] = key_of<D>(2 * quad + (c & 1) + 8 * (c >> 1));
+    for (int c = 0; c < 4; ++c) vkey[c] = key_of(2 * quad + (c & 1) + 8 * (c >> 1));
+    // where they lie in 16 keys: K's row, V's of vkey[0] and vkey[1]
+    constexpr int kR = C::kRow, kSc = C::kScales;
+    const uint32_t k_at = uint32_t(kkey * kR + (D == 128 ? 16 : 8) * quad);
+    const uint32_t ks_at = uint32_t(kkey * kSc + (D == 128 ? 2 * quad : quad));
+    uint32_t v_at[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        v_at[c] = uint32_t(vkey[c] * kR + (D == 128 ? 8 : 4) * qrow);
+    const uint32_t vs_at = uint32_t(  // (vkey[1] is 4 keys on)
+        vkey[0] * kSc + (D == 128 ? qrow : qrow >> 1));
     while (cur.next(p, g)) {
         const int R = g.s.q_len * p.g, diag = g.s.kv_len - g.s.q_len, r0 = g.tile * p.bm;
         const int nr = min(LIST ? p.bm : BM, R - r0);
@@ -262,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             for (int v = 0; v < D / 8; ++v)
                 qb[x][v >> 1][v & 1] = pack_f16x2(__uint_as_float(raw[v] << 16) * up, __uint_as_float(raw[v] & 0xffff0000u) * up);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) rs[2 * x + i] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 4 * (2 * quad + i));
+            for (int i = 0; i < 2; ++i)  // (not 0, which would not leave a masked score at -inf; scores are below 2^33)
+                rs[2 * x + i] = fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, down, 4 * (2 * quad + i)), 1e-37f);
         }
         // the rows of this lane's scores
         int lim[NR], low[NR], rel[NR];
@@ -275,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             low[i] = p.window >= 0 ? rel[i] - p.window : 0;
             brow[i] = btab + (rr < nr ? rr : 0) * 33;
         }
-        if (BIAS) consumer_sync();
+        if (BIAS) consumer_sync<kWarps>();
         // keys that every row of the tile sees: no mask in [all_lo, all_hi)
         const int t_first = div_g(p, r0), t_last = div_g(p, r0 + nr - 1);
         const int all_hi = p.causal ? min(g.s.kv_len, t_first + diag + 1) : g.s.kv_len;
@@ -335,21 +377,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 uint32_t w[2][D / 32], sc[2][D / 64];  // codes and scales of keys kkey, kkey + 8
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int key = 16 * q + 8 * i + kkey;
+                    const uint32_t row = uint32_t((16 * q + 8 * i) * kR), srow = uint32_t((16 * q + 8 * i) * kSc);
                     if constexpr (D == 128) {
-                        const uint4 u = ld_shared_v4(sK + uint32_t(key * 64 + ((quad ^ ((key >> 1) & 3)) << 4)));
+                        const uint4 u = ld_shared_v4(sK + k_at + row);
                         w[i][0] = u.x;
                         w[i][1] = u.y;
                         w[i][2] = u.z;
                         w[i][3] = u.w;
-                        const uint32_t two = e4m3_to_f16(lds16(sKS + uint32_t(key * 8 + 2 * quad)));
+                        const uint32_t two = e4m3_to_f16(lds16(sKS + ks_at + srow));
                         sc[i][0] = __byte_perm(two, 0u, 0x1010);
                         sc[i][1] = __byte_perm(two, 0u, 0x3232);
                     } else {
-                        const uint2 u = lds64(sK + uint32_t(key * 32 + 8 * quad));
+                        const uint2 u = lds64(sK + k_at + row);
                         w[i][0] = u.x;
                         w[i][1] = u.y;
-                        sc[i][0] = e4m3_to_f16(lds8(sKS + uint32_t(key * 4 + quad)) * 0x101u);
+                        sc[i][0] = e4m3_to_f16(lds8(sKS + ks_at + srow) * 0x101u);
                     }
                 }
 #pragma unroll
@@ -382,11 +424,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                             const int b = one ? bk : relpos_bucket(rel[ri] - (a16 + kkey + 8 * (i >> 1)));
                             s[q][x][i] = fmaf(s[q][x][i], rs[ri], brow[ri][b]);
                         }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < NT; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[q][x][i] *= rs[2 * x + (i & 1)];
                 }
                 if (a16 < all_lo || a16 + 16 > all_hi) {
 #pragma unroll
@@ -406,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             for (int i = 0; i < NR; ++i) {
                 const int x = i >> 1, e = i & 1;
                 mx[i] = fmaxf(fmaxf(s[0][x][e], s[0][x][e + 2]), fmaxf(s[1][x][e], s[1][x][e + 2]));
+                if (!BIAS) mx[i] *= rs[i];  // (with a bias the scores are in log2 units already)
                 grow = grow || mx[i] > m[i] + 8.f;
             }
             if (__any_sync(0xffffffffu, grow)) {
@@ -432,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 for (int q = 0; q < KG; ++q)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float e0 = ex2_approx(s[q][x][2 * h] - u0), e1 = ex2_approx(s[q][x][2 * h + 1] - u1);
+                        const float e0 = ex2_approx(BIAS ? s[q][x][2 * h] - u0 : fmaf(s[q][x][2 * h], rs[2 * x], -u0));
+                        const float e1 = ex2_approx(BIAS ? s[q][x][2 * h + 1] - u1 : fmaf(s[q][x][2 * h + 1], rs[2 * x + 1], -u1));
                         l[2 * x] += e0;
                         l[2 * x + 1] += e1;
                         pb[q][x][h] = transposed(pack_f16x2(e0, e1));
@@ -443,16 +482,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 uint32_t w[4][D / 64], sb[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int key = 16 * q + vkey[c];
+                    const uint32_t row = uint32_t((16 * q + 8 * (c >> 1)) * kR), srow = uint32_t((16 * q + 8 * (c >> 1)) * kSc);
                     if constexpr (D == 128) {
-                        const uint2 u = lds64(sV + uint32_t(key * 64 + (((qrow >> 1) ^ ((key >> 1) & 3)) << 4) + 8 * (qrow & 1)));
+                        const uint2 u = lds64(sV + v_at[c & 1] + row);
                         w[c][0] = u.x;
                         w[c][1] = u.y;
-                        sb[c] = lds8(sVS + uint32_t(key * 8 + qrow));
                     } else {
-                        w[c][0] = lds32(sV + uint32_t(key * 32 + 4 * qrow));
-                        sb[c] = lds8(sVS + uint32_t(key * 4 + (qrow >> 1)));
+                        w[c][0] = lds32(sV + v_at[c & 1] + row);
                     }
+                    sb[c] = lds8(sVS + vs_at + (c & 1 ? uint32_t(4 * kSc) : 0u) + srow);
                 }
                 // Scales of keys that no row may see are undefined, and 0 * NaN is not 0.
                 if (at16[q] < lo || at16[q] + 16 > hi) {
@@ -484,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             if (lane == 0) mbar_arrive(empty(st));
         }
         // ------------------------------------------------------------ end of the item's part
-        // Merge the four warps: m and l of every row, then O, 8 rows at a time, warps 2 and 3
-        // into the slots, warps 0 and 1 onto them, and the two slots' sum out.
+        // Merge the warps: m and l of every row, then O, 8 rows at a time: the second half of the
+        // warps into slots, the first onto them, and the slots' sum out.
         float* mw = ml + (seg_no & 1) * (2 * kWarps * 16);
         float* lw = mw + kWarps * 16;
         ++seg_no;
@@ -498,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 lw[warp * 16 + 8 * (i >> 1) + 2 * quad + (i & 1)] = l[i];
             }
         }
-        consumer_sync();
+        consumer_sync<kWarps>();
         const bool whole = g.whole();
         int first = 0, last = 0;
         if (!whole) {
@@ -508,16 +546,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         float* part = p.part + size_t(cache_slot(blockIdx.x, first)) * C::kPart;
         constexpr int CW = D / 16;  // columns of a thread: 16 threads a row
         const int ocol = CW * (threadIdx.x & 15);
-        float* slot = slots + (warp & 1) * C::kSlot + (D / 8) * qrow;
+        float* slot = slots + (warp % C::kSlotsN) * C::kSlot + (D / 8) * qrow;
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
             if (8 * h >= nr) break;
-            if (h) consumer_sync();
+            if (h) consumer_sync<kWarps>();
             float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * h + 2 * quad + e;
-                const float mm = fmaxf(fmaxf(mw[r], mw[16 + r]), fmaxf(mw[32 + r], mw[48 + r]));
+                float mm = mw[r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, mw[16 * w + r]);
                 f[e] = m[2 * h + e] == -INFINITY ? 0.f : ex2_approx(m[2 * h + e] - kLift - mm);
             }
             auto put = [&](bool add) {
@@ -534,11 +574,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                         *dst = x;
                     }
             };
-            if (warp >= 2) put(false);
-            consumer_sync();
-            if (warp < 2) put(true);
+            if (warp >= C::kSlotsN) put(false);
+            consumer_sync<kWarps>();
+            if (warp < C::kSlotsN) put(true);
             // this thread's row: its maximum and sum
-            const int orow = 8 * h + (threadIdx.x >> 4);
+            const int orow = 8 * h + ((threadIdx.x & 127) >> 4);
             float om = -INFINITY, ol = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) om = fmaxf(om, mw[16 * w + orow]);
@@ -547,18 +587,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 const float mm = mw[16 * w + orow];
                 ol = fmaf(mm == -INFINITY ? 0.f : ex2_approx(mm - om), lw[16 * w + orow], ol);
             }
-            consumer_sync();
+            consumer_sync<kWarps>();
             const float* a = slots + (orow & 7) * C::kPitch + ocol;
             float v[CW];
 #pragma unroll
             for (int e = 0; e < CW; e += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(a + e), y = *reinterpret_cast<const float4*>(a + C::kSlot + e);
-                v[e] = x.x + y.x;
-                v[e + 1] = x.y + y.y;
-                v[e + 2] = x.z + y.z;
-                v[e + 3] = x.w + y.w;
+                float4 x = *reinterpret_cast<const float4*>(a + e);
+#pragma unroll
+                for (int k = 1; k < C::kSlotsN; ++k) {
+                    const float4 y = *reinterpret_cast<const float4*>(a + k * C::kSlot + e);
+                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                }
+                v[e] = x.x;
+                v[e + 1] = x.y;
+                v[e + 2] = x.z;
+                v[e + 3] = x.w;
             }
-            if (orow >= nr || !ok) continue;
+            if (threadIdx.x >= 128 || orow >= nr || !ok) continue;
             if (!whole) {
 #pragma unroll
                 for (int e = 0; e < CW; e += 4)
@@ -585,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         }
         if (whole) continue;
         __threadfence();
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (threadIdx.x == 0) {
             int done = 0;
             if (ok) {
@@ -595,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             }
             *last_flag = done;
         }
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (!*last_flag) continue;
         // The last part to arrive adds them all up, in the order of the keys: weights first (a
         // warp takes a row's maxima and sums, its lanes the parts), then a thread takes four
@@ -610,14 +655,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         // columns: up to kCols per thread, or as many threads per column as fit
         const int share = cols > 64 ? 1 : 32 * kWarps / cols, who = share > 1 ? threadIdx.x / cols : 0;
         const int col0 = share > 1 ? threadIdx.x % cols : threadIdx.x;
-        for (int rr = warp; rr < nr; rr += kWarps) {
-            float mm = -INFINITY, ll = 0.f;
-            for (int c = lane; c < parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 16 * D + rr));
+        constexpr int kAhead = 8;           // parts of the first column asked for before the weights are known
+        float4 ahead[kAhead];
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-            for (int c = lane; c < parts; c += 32) {
-                const float mc = __ldcg(part_of(c) + 16 * D + rr);
-                ll = fmaf(mc == -INFINITY ? 0.f : ex2_approx(mc - mm), __ldcg(part_of(c) + 16 * D + 16 + rr), ll);
+        for (int k = 0; k < kAhead; ++k)
+            if (who + k * share < parts && col0 < cols && who < share)
+                ahead[k] = __ldcg(reinterpret_cast<const float4*>(part_of(who + k * share)) + col0);
+        const bool few = parts <= 64;        // a row's m and l in two registers of a lane
+        for (int rr = warp; rr < nr; rr += kWarps) {
+            float mm, ll = 0.f;
+            if (few) {
+                float mc[2], lc[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int c = lane + 32 * k;
+                    mc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + rr) : -INFINITY;
+                    lc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + 16 + rr) : 0.f;
+                }
+                mm = fmaxf(mc[0], mc[1]);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float f = mc[k] == -INFINITY ? 0.f : ex2_approx(mc[k] - mm);
+                    ll = fmaf(f, lc[k], ll);
+                    if (lane + 32 * k < parts) wts[(lane + 32 * k) * 16 + rr] = f;
+                }
+            } else {
+                mm = -INFINITY;
+                for (int c = lane; c < parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 16 * D + rr));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                for (int c = lane; c < parts; c += 32) {
+                    const float mc = __ldcg(part_of(c) + 16 * D + rr);
+                    ll = fmaf(mc == -INFINITY ? 0.f : ex2_approx(mc - mm), __ldcg(part_of(c) + 16 * D + 16 + rr), ll);
+                }
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
@@ -626,40 +698,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 row_l[rr] = ll;
             }
         }
-        consumer_sync();
+        consumer_sync<kWarps>();
         float4 acc[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c0 = 0; c0 < parts; c0 += kBatch) {
             const int n = min(kBatch, parts - c0);
-            for (int e = threadIdx.x; e < n * 16; e += 32 * kWarps) {
+            for (int e = threadIdx.x; !few && e < n * 16; e += 32 * kWarps) {
                 const int rr = e & 15;
                 const float mc = rr < nr ? __ldcg(part_of(c0 + (e >> 4)) + 16 * D + rr) : -INFINITY;
                 wts[e] = mc == -INFINITY ? 0.f : ex2_approx(mc - row_m[rr]);
             }
-            consumer_sync();
+            if (!few) consumer_sync<kWarps>();
             if (who < share) {
 #pragma unroll
                 for (int k = 0; k < kCols; ++k) {
                     const int col = col0 + k * 32 * kWarps, rr = col / (D / 4);
                     if (col >= cols) break;
-#pragma unroll 8
-                    for (int c = who; c < n; c += share) {
-                        const float4 u = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c)) + col);
+                    auto add = [&](const float4 u, int c) {
                         const float f0 = wts[c * 16 + rr];
                         acc[k].x = fmaf(u.x, f0, acc[k].x);
                         acc[k].y = fmaf(u.y, f0, acc[k].y);
                         acc[k].z = fmaf(u.z, f0, acc[k].z);
                         acc[k].w = fmaf(u.w, f0, acc[k].w);
+                    };
+                    int c = who;
+                    if (k == 0 && c0 == 0) {
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+                            if (who + i * share < n) add(ahead[i], who + i * share);
+                        c = who + kAhead * share;
                     }
+#pragma unroll 8
+                    for (; c < n; c += share) add(__ldcg(reinterpret_cast<const float4*>(part_of(c0 + c)) + col), c);
                 }
             }
-            consumer_sync();
+            consumer_sync<kWarps>();
         }
         if (share > 1) {  // the threads of a column, added in their order
             float4* sums = reinterpret_cast<float4*>(slots);  // (over the weights, read by now; row_l lies behind)
             if (who < share) sums[threadIdx.x] = acc[0];
-            consumer_sync();
+            consumer_sync<kWarps>();
             if (who == 0)
                 for (int k = 1; k < share; ++k) {
                     const float4 u = sums[k * cols + col0];
@@ -686,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 if (p.lse && c == 0) p.lse[at] = ll > 0.f ? (row_m[rr] + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
             }
         }
-        consumer_sync();  // (the weights' memory is the next item's slots)
+        consumer_sync<kWarps>();  // (the weights' memory is the next item's slots)
     }
 }
 
@@ -702,7 +781,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdP
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms * C::kCtas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kBytes;
     cfg.stream = st;
     cfg.attrs = &attr;

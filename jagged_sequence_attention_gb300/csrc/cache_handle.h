@@ -156,6 +156,7 @@ inline void fwd_params(CacheFwdParams& p, jfa_cache cache, int32_t B, int64_t T,
         p.o_mul = cache->v_factor;
         p.k_scales = cache->k_scales;
         p.v_scales = cache->v_scales;
+        p.dense = cache->ks[1] == cache->D / 2 && cache->vs[1] == cache->D / 2;
         for (int i = 0; i < 2; ++i) {
             p.kss[i] = cache->kss[i];
             p.vss[i] = cache->vss[i];

@@ -281,8 +281,7 @@ cudaError_t chunk4(jfa_cache c, const CUtensorMap& mq, const CacheFwdParams& p, 
 
 const CacheOps kQuantOps = {append4, chunk4, decode4, cache_decode4_part_bytes};
 
-// Pages of codes as bytes (D/2, slot, head, page), boxes of one page's rows (at most 64).  Rows of
-// 64 bytes are swizzled, which spreads a column of eight of them over all banks.
+// Pages of codes as bytes (D/2, slot, head, page), boxes of one page's rows (at most 64).
 jfa_status make_code_map(CUtensorMap* map, const void* base, const jfa_cache_t* c, const int64_t* s) {
     const auto enc = encode_tiled();
     if (!enc) return JFA_ERR_CUDA;
@@ -291,7 +290,7 @@ jfa_status make_code_map(CUtensorMap* map, const void* base, const jfa_cache_t* 
     const cuuint32_t box[4] = {cuuint32_t(c->D / 2), cuuint32_t(std::min(64, 1 << c->page_log2)), 1u, 1u};
     const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               c->D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? JFA_OK
                : JFA_ERR_CUDA;
