@@ -32,7 +32,7 @@ CALLS = os.path.join(PKG, "_cache_calls" + sysconfig.get_config_var("EXT_SUFFIX"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "plan.cpp", "fwd.cu", "fwd_short.cu", "fwd_pack.cu", "bwd.cu", "bwd_dq.cu", "bwd_fused.cu", "bwd_short.cu", "f32.cu", "static_scratch.cu",
            "cache.cu", "cache_append.cu", "cache_simt.cu", "cache_decode.cu", "cache_chunk.cu", "cache_split.cu",
-           "cache_quant.cu", "cache_decode4.cu", "cache_blocks.cu"]
+           "cache_quant.cu", "cache_decode4.cu", "cache_blocks.cu", "cache_join.cu"]
 
 
 def _nvcc() -> str:

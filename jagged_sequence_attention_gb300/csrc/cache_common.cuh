@@ -536,6 +536,9 @@ __device__ __forceinline__ void cache_pieces(const CacheFwdParams& p, CacheGroup
 // first part in slot 1 of `first`, the others in slot 0.
 __device__ __forceinline__ int cache_slot(int cta, int first_cta) { return 2 * cta + (cta == first_cta ? 1 : 0); }
 
+// What a CTA leaves for the join kernel: the item that starts in it and goes on past it (rows 0: none).
+__device__ __forceinline__ CacheCut cache_no_cut() { return CacheCut{0, 0, 0, 0, 0, -1, {0, 0}}; }
+
 // Programmatic launch: let the next kernel of the stream start (when it was launched so), and
 // wait for the previous one to have finished.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -592,6 +595,8 @@ size_t cache_decode_part_bytes(int D, int num_sms);
 // The same over the blocks of p.lists, a token (p.bm = g rows) at a time.
 cudaError_t launch_cache_decode_lists(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, int num_sms,
                                       cudaStream_t st);
+// Adds up the parts that the `ctas` CTAs of the kernel launched before left by p.cuts.
+cudaError_t launch_cache_join(int D, const CacheFwdParams& p, int ctas, cudaStream_t st);
 // bf16, items of 256 packed rows: bound by the tensor cores and the exponentials.
 // mq: the queries as (D, head, token), boxes of 128 bytes x g heads x tile_tokens.
 cudaError_t launch_cache_chunk(int D, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,

@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     CacheCursor<BN, LIST> cur(p, cache_start<BN, LIST>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
     if (threadIdx.x == 0) *start = cur.st;
     __syncthreads();
+    if (LIST) launch_dependents();  // (the join kernel waits for this one to end)
     CacheSeg g;
     int* bases = reinterpret_cast<int*>(smem + C::kOffBase);  // [stage][box]
 
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     const int quad = lane & 3, qrow = lane >> 2;
     uint32_t it = 0, seg_no = 0;
     bool ok = true;
+    CacheCut cut = cache_no_cut();  // lists: parts are added up by the join kernel
     // ldmatrix source: row of this warp's 16 keys and 16-byte piece, for K and (transposed) V
     const int krow = 16 * KG * warp + (lane & 7) + ((lane >> 4) << 3), kpc = (lane >> 3) & 1;
     const int vrow = 16 * KG * warp + (lane & 7) + (((lane >> 3) & 1) << 3), vpc = lane >> 4;
@@ -547,7 +549,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             }
             if (ocol == 0 && p.lse) p.lse[grow] = ol > 0.f ? (om + __log2f(ol)) * 0.6931471805599453f : -INFINITY;
         }
-        if (whole) continue;
+        if (LIST && !whole && g.k0 == 0 && ok) cut = CacheCut{g.s.q0, nr, r0, g.hk * p.g, first, last, {0, 0}};
+        if (LIST || whole) continue;
         __threadfence();
         consumer_sync();
         if (threadIdx.x == 0) {
@@ -691,6 +694,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             }
         }
     }
+    if (LIST && threadIdx.x == 0) p.cuts[blockIdx.x] = ok ? cut : cache_no_cut();
 }
 
 template <int D, bool BIAS, bool LIST = false>
@@ -709,7 +713,8 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdP
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, jfa_cache_decode_kernel<D, BIAS, LIST>, mk, mv, p);
+    e = cudaLaunchKernelEx(&cfg, jfa_cache_decode_kernel<D, BIAS, LIST>, mk, mv, p);
+    return e == cudaSuccess && LIST ? launch_cache_join(D, p, num_sms * kDecCtasPerSm, st) : e;
 }
 
 }  // namespace

@@ -116,7 +116,6 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
     auto full = [&](uint32_t s) -> uint32_t { return sbase + C::kOffBar + 8u * s; };
     auto empty = [&](uint32_t s) -> uint32_t { return sbase + C::kOffBar + 8u * (C::kStages + s); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
-    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     int* bases = reinterpret_cast<int*>(smem + C::kOffBase);  // [stage][box]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -134,6 +133,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
     CacheCursor<BN, LIST> cur(p, cache_start<BN, LIST>(p, reinterpret_cast<int*>(smem)));  // (the ring's memory as scratch)
     if (threadIdx.x == 0) *start = cur.st;
     __syncthreads();
+    launch_dependents();  // (the join kernel waits for this one to end)
     CacheSeg g;
 
     if (warp == kWarps) {
@@ -248,6 +248,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
     const int quad = lane & 3, qrow = lane >> 2;
     uint32_t it = 0, seg_no = 0;
     bool ok = true;
+    CacheCut cut = cache_no_cut();
     const int kkey = key_of(qrow);                        // this lane's key of a fragment's first 8 (and 8 on)
     int vkey[4];                                             // its four keys of V^T
 #pragma unroll
@@ -628,145 +629,10 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
             }
             if (ocol == 0 && p.lse) p.lse[at] = ol > 0.f ? (om + __log2f(ol)) * 0.6931471805599453f : -INFINITY;
         }
-        if (whole) continue;
-        __threadfence();
-        consumer_sync<kWarps>();
-        if (threadIdx.x == 0) {
-            int done = 0;
-            if (ok) {
-                done = atomicAdd(p.counters + kCtrSplit + first, 1u) == uint32_t(last - first);
-                if (done) p.counters[kCtrSplit + first] = 0u;  // every part has arrived: ready for the next call
-                __threadfence();
-            }
-            *last_flag = done;
-        }
-        consumer_sync<kWarps>();
-        if (!*last_flag) continue;
-        // The last part to arrive adds them all up, in the order of the keys: weights first (a
-        // warp takes a row's maxima and sums, its lanes the parts), then a thread takes four
-        // columns of a row over the parts.
-        const int parts = last - first + 1, cols = nr * (D / 4);
-        constexpr int kBatch = 96;           // parts x 16 rows of weights: 6 of the slots' 8 KB
-        constexpr int kCols = (BM * (D / 4) + 32 * kWarps - 1) / (32 * kWarps);
-        float* wts = slots;                  // [part][16]
-        float* row_m = slots + kBatch * 16;  // [16], and the sums [16]
-        float* row_l = row_m + 16;
-        auto part_of = [&](int c) { return p.part + size_t(cache_slot(first + c, first)) * C::kPart; };
-        // columns: up to kCols per thread, or as many threads per column as fit
-        const int share = cols > 64 ? 1 : 32 * kWarps / cols, who = share > 1 ? threadIdx.x / cols : 0;
-        const int col0 = share > 1 ? threadIdx.x % cols : threadIdx.x;
-        constexpr int kAhead = 8;           // parts of the first column asked for before the weights are known
-        float4 ahead[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (who + k * share < parts && col0 < cols && who < share)
-                ahead[k] = __ldcg(reinterpret_cast<const float4*>(part_of(who + k * share)) + col0);
-        const bool few = parts <= 64;        // a row's m and l in two registers of a lane
-        for (int rr = warp; rr < nr; rr += kWarps) {
-            float mm, ll = 0.f;
-            if (few) {
-                float mc[2], lc[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int c = lane + 32 * k;
-                    mc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + rr) : -INFINITY;
-                    lc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + 16 + rr) : 0.f;
-                }
-                mm = fmaxf(mc[0], mc[1]);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float f = mc[k] == -INFINITY ? 0.f : ex2_approx(mc[k] - mm);
-                    ll = fmaf(f, lc[k], ll);
-                    if (lane + 32 * k < parts) wts[(lane + 32 * k) * 16 + rr] = f;
-                }
-            } else {
-                mm = -INFINITY;
-                for (int c = lane; c < parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 16 * D + rr));
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-                for (int c = lane; c < parts; c += 32) {
-                    const float mc = __ldcg(part_of(c) + 16 * D + rr);
-                    ll = fmaf(mc == -INFINITY ? 0.f : ex2_approx(mc - mm), __ldcg(part_of(c) + 16 * D + 16 + rr), ll);
-                }
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-            if (lane == 0) {
-                row_m[rr] = mm;
-                row_l[rr] = ll;
-            }
-        }
-        consumer_sync<kWarps>();
-        float4 acc[kCols];
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < parts; c0 += kBatch) {
-            const int n = min(kBatch, parts - c0);
-            for (int e = threadIdx.x; !few && e < n * 16; e += 32 * kWarps) {
-                const int rr = e & 15;
-                const float mc = rr < nr ? __ldcg(part_of(c0 + (e >> 4)) + 16 * D + rr) : -INFINITY;
-                wts[e] = mc == -INFINITY ? 0.f : ex2_approx(mc - row_m[rr]);
-            }
-            if (!few) consumer_sync<kWarps>();
-            if (who < share) {
-#pragma unroll
-                for (int k = 0; k < kCols; ++k) {
-                    const int col = col0 + k * 32 * kWarps, rr = col / (D / 4);
-                    if (col >= cols) break;
-                    auto add = [&](const float4 u, int c) {
-                        const float f0 = wts[c * 16 + rr];
-                        acc[k].x = fmaf(u.x, f0, acc[k].x);
-                        acc[k].y = fmaf(u.y, f0, acc[k].y);
-                        acc[k].z = fmaf(u.z, f0, acc[k].z);
-                        acc[k].w = fmaf(u.w, f0, acc[k].w);
-                    };
-                    int c = who;
-                    if (k == 0 && c0 == 0) {
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i)
-                            if (who + i * share < n) add(ahead[i], who + i * share);
-                        c = who + kAhead * share;
-                    }
-#pragma unroll 8
-                    for (; c < n; c += share) add(__ldcg(reinterpret_cast<const float4*>(part_of(c0 + c)) + col), c);
-                }
-            }
-            consumer_sync<kWarps>();
-        }
-        if (share > 1) {  // the threads of a column, added in their order
-            float4* sums = reinterpret_cast<float4*>(slots);  // (over the weights, read by now; row_l lies behind)
-            if (who < share) sums[threadIdx.x] = acc[0];
-            consumer_sync<kWarps>();
-            if (who == 0)
-                for (int k = 1; k < share; ++k) {
-                    const float4 u = sums[k * cols + col0];
-                    acc[0].x += u.x;
-                    acc[0].y += u.y;
-                    acc[0].z += u.z;
-                    acc[0].w += u.w;
-                }
-        }
-        if (who == 0) {
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-                const int col = col0 + k * 32 * kWarps, rr = col / (D / 4), c = 4 * (col % (D / 4));
-                if (col >= cols) break;
-                const int r2 = r0 + rr, t2 = div_g(p, r2);
-                const size_t at = size_t(g.s.q0 + t2) * size_t(p.H) + size_t(g.hk * p.g + r2 - t2 * p.g);
-                const float ll = row_l[rr], li = ll > 0.f ? p.o_mul / ll : 0.f;
-                if (p.o_f32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at * D + c) =
-                        make_float4(acc[k].x * li, acc[k].y * li, acc[k].z * li, acc[k].w * li);
-                else
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + at * D + c) =
-                        make_uint2(pack_bf16x2(acc[k].x * li, acc[k].y * li), pack_bf16x2(acc[k].z * li, acc[k].w * li));
-                if (p.lse && c == 0) p.lse[at] = ll > 0.f ? (row_m[rr] + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
-            }
-        }
-        consumer_sync<kWarps>();  // (the weights' memory is the next item's slots)
+        // (an item cut between CTAs: the first part's CTA leaves the record)
+        if (!whole && g.k0 == 0 && ok) cut = CacheCut{g.s.q0, nr, r0, g.hk * p.g, first, last, {0, 0}};
     }
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = ok ? cut : cache_no_cut();
 }
 
 template <int D, bool BIAS, bool LIST, int NT>
@@ -786,7 +652,8 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdP
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, jfa_cache_decode4_kernel<D, BIAS, LIST, NT>, mk, mv, p);
+    e = cudaLaunchKernelEx(&cfg, jfa_cache_decode4_kernel<D, BIAS, LIST, NT>, mk, mv, p);
+    return e == cudaSuccess ? launch_cache_join(D, p, num_sms * C::kCtas, st) : e;
 }
 
 template <int D, bool LIST>
@@ -799,10 +666,16 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdP
 
 }  // namespace
 
-size_t cache_decode4_part_bytes(int D, int num_sms) { return size_t(num_sms) * 3 * 2 * 16 * size_t(D + 2) * 4; }
+// The records, then the parts.
+constexpr size_t kRecordBytes = size_t(3) * kMaxSms * sizeof(CacheCut);
 
-cudaError_t launch_cache_decode4(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& p, bool early,
+size_t cache_decode4_part_bytes(int D, int num_sms) { return kRecordBytes + size_t(num_sms) * 3 * 2 * 16 * size_t(D + 2) * 4; }
+
+cudaError_t launch_cache_decode4(int D, const CUtensorMap& mk, const CUtensorMap& mv, const CacheFwdParams& call, bool early,
                                  int num_sms, cudaStream_t st) {
+    CacheFwdParams p = call;  // (the chunk kernel, which may run at the same time, has records of its own)
+    p.cuts = reinterpret_cast<CacheCut*>(p.part);
+    p.part += kRecordBytes / sizeof(float);
     if (p.lists)
         return D == 128 ? launch<128, true>(mk, mv, p, early, num_sms, st) : launch<64, true>(mk, mv, p, early, num_sms, st);
     return D == 128 ? launch<128, false>(mk, mv, p, early, num_sms, st) : launch<64, false>(mk, mv, p, early, num_sms, st);
