@@ -3,8 +3,8 @@
 //
 // Every CTA of those kernels leaves a record: the item that starts in it and goes on past it, or
 // none.  A CTA here takes a record's row: its four warps deal the parts among them, a lane takes four
-// (or two) columns, all loads of up to 64 parts are in flight at once, and the warps' sums are
-// added in order, so the result does not depend on timing.
+// (or two) columns, the loads of 64 parts are in flight at once, and the warps' sums are added
+// in order, so the result does not depend on timing.
 // Bound by latency: a record, its maxima and its parts, about 2.5 us.  The last CTA of an item used to add
 // its parts itself, which took 9 us for one history of 131k keys (57 parts for each of 8 heads: 43.5 -> @ us
 // in all) and 2 us for one of 1k.
@@ -26,22 +26,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) jfa_cache_join_kernel(const C
     const int parts = cut.last - cut.first + 1;
     for (int row = blockIdx.y; row < cut.rows; row += kJoinRows) {
         auto part_of = [&](int c) { return p.part + size_t(cache_slot(cut.first + c, cut.first)) * kPart; };
-        float m = -INFINITY, l = 0.f, mine[2];
-        for (int c = lane; c < parts; c += 32) m = fmaxf(m, __ldcg(part_of(c) + 16 * D + row));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        float acc[V];
+        float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.f;
         for (int c0 = 0; c0 < parts; c0 += 64) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {  // the weights of 64 parts
-                const int c = c0 + lane + 32 * k;
-                const float mc = c < parts ? __ldcg(part_of(c) + 16 * D + row) : -INFINITY;
-                mine[k] = mc == -INFINITY ? 0.f : ex2_approx(mc - m);
-                if (c < parts) l = fmaf(mine[k], __ldcg(part_of(c) + 16 * D + 16 + row), l);
-            }
-            float x[kAtOnce][V];
+            float x[kAtOnce][V], mc[2], lc[2];
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const int c = c0 + kJoinWarps * k + warp;
@@ -60,9 +49,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) jfa_cache_join_kernel(const C
                 }
             }
 #pragma unroll
+            for (int k = 0; k < 2; ++k) {  // 64 parts' maxima and sums
+                const int c = c0 + lane + 32 * k;
+                mc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + row) : -INFINITY;
+                lc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + 16 + row) : 0.f;
+            }
+            float top = fmaxf(m, fmaxf(mc[0], mc[1]));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (top == -INFINITY) continue;  // (no key yet: O is 0 in all of them)
+            const float keep = ex2_approx(m - top);
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] *= keep;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mc[k] = ex2_approx(mc[k] - top);
+                l = fmaf(mc[k], lc[k], l);
+            }
+#pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const int at = kJoinWarps * k + warp;
-                const float f = __shfl_sync(0xffffffffu, mine[k / 8], at & 31);
+                const float f = __shfl_sync(0xffffffffu, mc[kJoinWarps * k / 32], at & 31);
                 if (c0 + at >= parts) continue;
 #pragma unroll
                 for (int v = 0; v < V; ++v) acc[v] = fmaf(x[k][v], f, acc[v]);
