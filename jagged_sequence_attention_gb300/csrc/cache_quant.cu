@@ -5,13 +5,14 @@
 //   s = e4m3(max|y| / (6 c)),  code_i = e2m1(y_i / (c s)),  c the array's factor,
 // each to nearest even, as if in exact arithmetic.  In fp32 the rotated y and the quotients are a
 // little off, which matters only next to the middle between two codes (or scales): both ends of
-// the interval that y can lie in are rounded, and where they differ (about one group in
-// thousands) the 16 elements are done again in 64 bits.  So a cache's contents do not depend on
-// how the rotation was computed.  Elements taken as they are, with a factor that is a power
-// of two, need no interval: their quotients are rounded correctly in fp32, and a bf16 value that
-// is not at a middle is 2^-9 of it away or more.
-// A thread takes the 16 elements of a group; a rotated group's partners (the other halves of its
-// pairs, eight or sixteen elements on) are read again by it instead of handed over.
+// the interval that a quotient can lie in are rounded, and where they differ (one element in 10^5) the
+// element is compared with the middle in 64 bits.  So a cache's contents do not depend on how
+// the rotation was computed.  Elements taken as they are, with a factor that is a power of two,
+// need no interval: their quotients are rounded correctly in fp32, and a bf16 value that is not
+// at a middle is 2^-9 of it away or more.
+// A thread takes 8 elements, two threads a group, so that a warp's loads and stores lie side by
+// side; a rotated row's other halves are read again (from L1) instead of handed over.
+// Measured: @
 #include <cuda_bf16.h>
 
 #include <new>
@@ -42,17 +43,18 @@ struct QuantParams {
     float factor[2];
 };
 
-// One group of a row: 16 elements from d0 on of src, with its pairs' angles (R: rotated elements).
-struct Group {
+// Half a group of a row: 8 elements from d on of src (the group's from d & ~15 on), with its pairs'
+// angles (R: rotated elements).
+struct Half {
     const __nv_bfloat16* src;
     const float* row;
-    int d0, R;
+    int d, R;
     bool pairs;
 };
 
-// Element i of a rotated group in 64 bits (the products are exact there).
-__device__ __forceinline__ double exact_element(const Group& g, int i) {
-    const int d = g.d0 + i, half = g.R / 2;
+// Element d of a rotated row in 64 bits (the products are exact there).
+__device__ __forceinline__ double exact_element(const Half& g, int d) {
+    const int half = g.R / 2;
     const double x = double(__bfloat162float(g.src[d]));
     if (d >= g.R) return x;
     const bool first = g.pairs ? (d & 1) == 0 : d < half;
@@ -61,112 +63,155 @@ __device__ __forceinline__ double exact_element(const Group& g, int i) {
     return first ? x * c - y * s : x * c + y * s;
 }
 
-// A group in 64 bits: its codes, and the nearer one of two neighbouring scales lo <= hi.
-__device__ __noinline__ uint2 exact_group(const Group& g, float factor, uint32_t lo, uint32_t hi, uint32_t& scale) {
+__device__ __forceinline__ float scale_value(uint32_t byte) { return f16_to_float(e4m3_to_f16(byte)).x; }
+
+// The nearer one of neighbouring scales lo <= hi.  (The middle of two has five bits: the comparison
+// is exact.)
+__device__ __noinline__ uint32_t exact_scale(const Half& g, float factor, uint32_t lo, uint32_t hi) {
     double top = 0.0;
-    for (int i = 0; i < 16; ++i) top = fmax(top, fabs(exact_element(g, i)));
-    auto value = [](uint32_t b) { return double(f16_to_float(e4m3_to_f16(b)).x); };
-    const double c = double(factor);
-    while (lo < hi) {  // (the middle of two scales has five bits: the comparison is exact)
-        const double mid = 0.5 * (value(lo) + value(lo + 1)) * (6.0 * c);
+    for (int i = 0; i < 16; ++i) top = fmax(top, fabs(exact_element(g, (g.d & ~15) + i)));
+    for (; lo < hi; ++lo) {
+        const double mid = 0.5 * (double(scale_value(lo)) + double(scale_value(lo + 1))) * (6.0 * double(factor));
         if (!(top > mid || (top == mid && (lo & 1u)))) break;
-        ++lo;
     }
-    scale = lo;
-    const double step = c * value(lo);
-    uint32_t w[2] = {0u, 0u};
-    for (int i = 0; i < 16; ++i) {
-        const double y = exact_element(g, i), a = fabs(y);
-        uint32_t code = 0u;
-        const double mids[7] = {0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0};
-        if (step > 0.0)
-            for (int k = 0; k < 7; ++k) code += (a > mids[k] * step || ((k & 1) && a == mids[k] * step)) ? 1u : 0u;
-        if (y < 0.0) code |= 8u;
-        w[i >> 3] |= code << (4 * (i & 7));
-    }
-    return make_uint2(w[0], w[1]);
+    return lo;
 }
 
-// The group's codes and scale.  exact: a row as it is and a factor that is a power of two.
-__device__ __forceinline__ uint2 quantise(const Group& g, float factor, bool exact, uint32_t& scale) {
-    float y[16], slack = 0.f;
+// The nearer one of codes lo .. hi of element i, for a step of factor * scale, and its sign.
+__device__ __noinline__ uint32_t exact_code(const Half& g, double step, int i, uint32_t lo, uint32_t hi) {
+    const double x = exact_element(g, g.d + i), y = fabs(x);
+    for (; lo < hi; ++lo) {
+        const double mid = lo < 4u ? 0.25 + 0.5 * lo : lo == 4u ? 2.5 : lo == 5u ? 3.5 : 5.0;
+        if (!(y > mid * step || (y == mid * step && (lo & 1u)))) break;
+    }
+    return lo | (x < 0.0 ? 8u : 0u);
+}
+
+// A half's elements, and those of the other half of its head that a rotation pairs them with.
+struct Raw {
+    uint4 own, other;
+};
+__device__ __forceinline__ Raw load_raw(const Half& g) {
+    Raw r;
+    r.own = *reinterpret_cast<const uint4*>(g.src + g.d);
     const int half = g.R / 2;
+    if (g.d < g.R && !g.pairs) r.other = *reinterpret_cast<const uint4*>(g.src + (g.d < half ? g.d + half : g.d - half));
+    return r;
+}
+
+// Eight codes and the group's scale, by the two lanes (an even one and the next) that have its halves;
+// the whole warp comes here.  exact: a row as it is and a factor that is a power of two.
+__device__ __forceinline__ uint32_t quantise(const Half& g, const Raw& raw, float factor, bool exact, uint32_t& scale) {
+    float y[8], slack = 0.f;
+    const int half = g.R / 2;
+    Vec<__nv_bfloat16> a;
+    a.set(raw.own);
+    if (g.d < g.R) {
+        if (g.pairs) {
+            float cs[4], sn[4];
+            load_floats<4>(g.row + g.d / 2, cs);
+            load_floats<4>(g.row + half + g.d / 2, sn);
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-        const int d = g.d0 + 8 * v;
-        Vec<__nv_bfloat16> a;
-        a.load(g.src + d);
-        if (d < g.R) {
-            if (g.pairs) {
+            for (int i = 0; i < 8; i += 2) {
+                const float c = cs[i / 2], s = sn[i / 2], x = a.v[i], z = a.v[i + 1];
+                a.v[i] = x * c - z * s;
+                a.v[i + 1] = z * c + x * s;
+                slack = fmaxf(slack, (fabsf(x) + fabsf(z)) * fmaxf(fabsf(c), fabsf(s)));
+            }
+        } else {
+            const bool first = g.d < half;
+            const int k = first ? g.d : g.d - half;
+            Vec<__nv_bfloat16> b;
+            b.set(raw.other);
+            float cs[8], sn[8];
+            load_floats<8>(g.row + k, cs);
+            load_floats<8>(g.row + half + k, sn);
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float c = g.row[(d + i) / 2], s = g.row[half + (d + i) / 2], x = a.v[i], z = a.v[i + 1];
-                    a.v[i] = x * c - z * s;
-                    a.v[i + 1] = z * c + x * s;
-                    slack = fmaxf(slack, (fabsf(x) + fabsf(z)) * fmaxf(fabsf(c), fabsf(s)));
-                }
-            } else {
-                const bool first = d < half;
-                const int k = first ? d : d - half;
-                Vec<__nv_bfloat16> b;
-                b.load(g.src + (first ? d + half : d - half));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float c = g.row[k + i], s = g.row[half + k + i], x = a.v[i], z = first ? -b.v[i] : b.v[i];
-                    a.v[i] = x * c + z * s;
-                    slack = fmaxf(slack, fabsf(x * c) + fabsf(z * s));
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float u = a.v[i] * cs[i], w = (first ? -b.v[i] : b.v[i]) * sn[i];
+                a.v[i] = u + w;
+                slack = fmaxf(slack, fabsf(u) + fabsf(w));
             }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[8 * v + i] = a.v[i];
     }
-    // a sum of two products is off by less than 2^-22 of their magnitudes
-    slack *= 0x1p-22f;
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
-    const float six = 6.f * factor;
+    for (int i = 0; i < 8; ++i) {
+        y[i] = a.v[i];
+        top = fmaxf(top, fabsf(y[i]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    // a sum of two products is off by less than 2^-22 of their magnitudes
+    slack = 0x1p-22f * fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, 1));
+    const float six = 6.f * factor, over = __fdiv_rn(top, six);
     uint32_t lo, hi;
     if (exact) {
-        lo = hi = to_e4m3(__fdiv_rn(top, six), 0.f) & 255u;
+        lo = hi = to_e4m3(over, 0.f) & 255u;
     } else {
-        const float q = __fdiv_rn(top, six), e = __fdividef(slack, six);
-        const uint32_t both = to_e4m3(fmaxf(fmaf(q, -0x1p-22f, q - e), 0.f), fmaf(q, 0x1p-22f, q + e));
+        const float e = __fdividef(slack, six);
+        const uint32_t both = to_e4m3(fmaxf(fmaf(over, -0x1p-22f, over - e), 0.f), fmaf(over, 0x1p-22f, over + e));
         lo = both & 255u;
         hi = both >> 8;
     }
+    if (lo != hi) lo = exact_scale(g, factor, lo, hi);
     scale = lo;
-    bool sure = lo == hi;
-    uint32_t w[2] = {0u, 0u};
-    if (sure && lo != 0u) {
-        const float step = factor * f16_to_float(e4m3_to_f16(lo)).x;
-        if (exact) {
+    if (lo == 0u) return 0u;
+    const float step = factor * scale_value(lo), inv = __fdiv_rn(1.f, step);
+    if (lo == 0x7eu) {  // the largest scale: what is over 6 steps becomes 6
 #pragma unroll
-            for (int i = 0; i < 16; i += 2)
-                w[i >> 3] |= to_e2m1(__fdiv_rn(y[i], step), __fdiv_rn(y[i + 1], step)) << (4 * (i & 7));
-        } else {
-            const float inv = __fdiv_rn(1.f, step), e = slack * inv * 1.0001f;
-            uint32_t above[2] = {0u, 0u};
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float a = fabsf(y[i] * inv), b = fabsf(y[i + 1] * inv);
-                w[i >> 3] |= to_e2m1(copysignf(fmaxf(fmaf(a, -0x1p-21f, a - e), 0.f), y[i]),
-                                     copysignf(fmaxf(fmaf(b, -0x1p-21f, b - e), 0.f), y[i + 1]))
-                             << (4 * (i & 7));
-                above[i >> 3] |= to_e2m1(copysignf(fmaf(a, 0x1p-21f, a + e), y[i]), copysignf(fmaf(b, 0x1p-21f, b + e), y[i + 1]))
-                                 << (4 * (i & 7));
-            }
-            sure = w[0] == above[0] && w[1] == above[1];
-        }
+        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -8.f * step), 8.f * step);
     }
-    if (!sure) return exact_group(g, factor, lo, hi, scale);
-    return make_uint2(w[0], w[1]);
+    if (exact) {
+        // Quotients rounded correctly: with the reciprocal so rounded, one step on the remainder makes
+        // them so (Markstein, IBM J. Res. Dev. 34, 1990).
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = y[i] * inv;
+            y[i] = fmaf(fmaf(-t, step, y[i]), inv, t);
+        }
+        return to_e2m1(y);
+    }
+    // (quotients of at most 8 are off by less than 2^-19 besides)
+    const float e = fmaf(slack, inv * 1.0001f, 0x1p-19f);
+    float above[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        above[i] = fmaf(y[i], inv, e);
+        y[i] = fmaf(y[i], inv, -e);
+    }
+    uint32_t w = to_e2m1(y);
+    const uint32_t x = to_e2m1(above);
+    // elements next to a middle: other magnitudes, or other signs of one that is not 0
+    const uint32_t other = w ^ x, some = ((w | x) & 0x77777777u) + 0x77777777u;
+    for (uint32_t differ = (other & 0x77777777u) | (other & some & 0x88888888u); differ;) {
+        const int at = (__ffs(differ) - 1) & 28;
+        differ &= ~(15u << at);
+        const uint32_t p = (w >> at) & 7u, q = (x >> at) & 7u;
+        const bool across = (other >> at) & 8u;
+        const uint32_t code = exact_code(g, double(factor) * double(scale_value(lo)), at / 4, across ? 0u : min(p, q), max(p, q));
+        w = (w & ~(15u << at)) | (code << at);
+    }
+    return w;
 }
 
 __global__ void __launch_bounds__(kThreads) jfa_cache_append4_kernel(const CacheAppendParams p, const QuantParams z) {
     using T = __nv_bfloat16;
     const int t = blockIdx.x, lane = threadIdx.x & 31;
+    const int vl = p.D == 128 ? 4 : 3, vecs = 1 << vl, nk = p.Hkv << vl;  // vectors of a head, of all key heads
+    const int R = p.rot ? p.rot_dim : 0;
+    // the vector of a thread in the loops over key heads (past the end: one of the warp's own, again)
+    auto vec = [&](int i0) { return i0 + lane < nk ? i0 + lane : i0 + (lane & 1); };
+    auto half_of = [&](int i, bool v, const float* row) {
+        const T* src = v ? static_cast<const T*>(p.V) + t * p.v_stride : static_cast<const T*>(p.K) + t * p.k_stride;
+        return Half{src + (i >> vl) * p.D, row, 8 * (i & (vecs - 1)), v ? 0 : R, p.pairs != 0};
+    };
+    // rows lie where the token's number says: the first ones are on their way while its place is found
+    const int first = threadIdx.x - lane;
+    Raw rk{}, rv{};
+    if (first < nk) {
+        rk = load_raw(half_of(vec(first), false, nullptr));
+        rv = load_raw(half_of(vec(first), true, nullptr));
+    }
     const CachePlace at = cache_place(p, t, lane);
     if (at.b < 0) return;  // rows behind the last sequence
     if (at.page < 0) {
@@ -175,40 +220,56 @@ __global__ void __launch_bounds__(kThreads) jfa_cache_append4_kernel(const Cache
     }
     const int slot = at.pos & ((1 << p.page_log2) - 1);
     const float* row = p.rot ? p.rot + size_t(at.pos) * size_t(p.rot_dim) : nullptr;
-    const int R = p.rot ? p.rot_dim : 0;
-    const int ng = p.D / 16, units = p.pairs ? p.D / 8 : p.D / 8 - R / 16;
-    const int nk = p.Hkv * ng, nq = p.H * units;
-    for (int i = threadIdx.x; i < 2 * nk + nq; i += kThreads) {
-        if (i >= 2 * nk) {  // a query head's vectors, as in a 16-bit cache
-            const int j = i - 2 * nk, h = j / units, u = j - h * units;
-            rotate_unit<T>(static_cast<const T*>(p.Q) + t * p.q_stride + h * p.D, static_cast<T*>(p.Q_out) + t * p.qo_stride + h * p.D,
-                           u, row, R, p.pairs);
-            continue;
+    // query heads' vectors, as beside a 16-bit cache, two at a time
+    const int units = p.pairs ? vecs : vecs - R / 16, nq = p.H * units;
+    for (int i = threadIdx.x; i < nq; i += 2 * kThreads) {
+        const T* src[2];
+        T* dst[2];
+        int u[2];
+        Raw r[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int j = i + k * kThreads, h = j / units;
+            u[k] = j - h * units;
+            src[k] = static_cast<const T*>(p.Q) + t * p.q_stride + h * p.D;
+            dst[k] = static_cast<T*>(p.Q_out) + t * p.qo_stride + h * p.D;
+            if (j < nq) {
+                const bool copied = !p.pairs && 16 * u[k] >= R;
+                r[k].own = *reinterpret_cast<const uint4*>(src[k] + 8 * u[k] + (copied ? R / 2 : 0));
+                if (!p.pairs && !copied) r[k].other = *reinterpret_cast<const uint4*>(src[k] + 8 * u[k] + R / 2);
+            }
         }
-        const bool v = i >= nk;
-        const int j = v ? i - nk : i, h = j / ng, gi = j - h * ng;
-        Group g;
-        g.src = (v ? static_cast<const T*>(p.V) + t * p.v_stride : static_cast<const T*>(p.K) + t * p.k_stride) + h * p.D;
-        g.row = row;
-        g.d0 = 16 * gi;
-        g.R = v ? 0 : R;
-        g.pairs = p.pairs;
-        const float factor = z.factor[v ? 1 : 0];
-        const bool exact = g.d0 >= g.R && (__float_as_uint(factor) & 0x7fffffu) == 0u;
-        uint32_t s;
-        const uint2 w = quantise(g, factor, exact, s);
-        const int64_t* st = v ? p.vs : p.ks;
-        const int64_t* ss = v ? z.vss : z.kss;
-        uint8_t* codes = static_cast<uint8_t*>(v ? p.Vc : p.Kc) + at.page * st[0] + slot * st[1] + h * st[2] + 8 * gi;
-        *reinterpret_cast<uint2*>(codes) = w;
-        (v ? z.v_scales : z.k_scales)[at.page * ss[0] + h * ss[1] + slot * ng + gi] = uint8_t(s);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (i + k * kThreads < nq) rotate_unit<T>(r[k].own, r[k].other, dst[k], u[k], row, R, p.pairs);
+    }
+    auto whole = [](float f) { return (__float_as_uint(f) & 0x7fffffu) == 0u; };  // a power of two
+    for (int i0 = first; i0 < nk; i0 += kThreads) {
+        const int i = vec(i0), h = i >> vl, u = i & (vecs - 1);
+        const Half gk = half_of(i, false, row), gv = half_of(i, true, nullptr);
+        if (i0 != first) {
+            rk = load_raw(gk);
+            rv = load_raw(gv);
+        }
+        uint32_t sk, sv;
+        const uint32_t wk = quantise(gk, rk, z.factor[0], gk.d >= R && whole(z.factor[0]), sk);
+        if (i0 + lane < nk) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.Kc) + at.page * p.ks[0] + slot * p.ks[1] + h * p.ks[2] + 4 * u) = wk;
+            if (!(u & 1)) z.k_scales[at.page * z.kss[0] + h * z.kss[1] + ((slot << vl) + u) / 2] = uint8_t(sk);
+        }
+        const uint32_t wv = quantise(gv, rv, z.factor[1], whole(z.factor[1]), sv);
+        if (i0 + lane < nk) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.Vc) + at.page * p.vs[0] + slot * p.vs[1] + h * p.vs[2] + 4 * u) = wv;
+            if (!(u & 1)) z.v_scales[at.page * z.vss[0] + h * z.vss[1] + ((slot << vl) + u) / 2] = uint8_t(sv);
+        }
     }
 }
 
-// Rows out of a cache of any type: a thread takes 16 elements of a row.  p.K and p.V are the
-// outputs (not const here).  Bound by its bytes.
+// Rows out of a cache of any type: a thread takes 16 bytes of an output row.  p.K and p.V are the outputs
+// (not const here).
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) jfa_cache_read_kernel(const CacheAppendParams p, const QuantParams z) {
+    constexpr int ES = BITS == 32 ? 4 : 2, N = 16 / ES;  // bytes of an output element, elements of a vector
     const int t = blockIdx.x, lane = threadIdx.x & 31;
     const CachePlace at = cache_place(p, t, lane);
     if (at.b < 0) return;
@@ -216,40 +277,39 @@ __global__ void __launch_bounds__(kThreads) jfa_cache_read_kernel(const CacheApp
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
         return;
     }
-    const int slot = at.pos & ((1 << p.page_log2) - 1);
-    constexpr int ES = BITS == 32 ? 4 : 2;  // bytes of an output element
-    const int ng = p.D / 16, n = p.Hkv * ng;
-    for (int i = threadIdx.x; i < 2 * n; i += kThreads) {
-        const bool v = i >= n;
-        const int j = v ? i - n : i, h = j / ng, gi = j - h * ng;
-        const int64_t* st = v ? p.vs : p.ks;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(const_cast<void*>(v ? p.V : p.K)) +
-                                              (t * (v ? p.v_stride : p.k_stride) + h * p.D + 16 * gi) * ES);
-        const int64_t from = at.page * st[0] + slot * st[1] + h * st[2];
+    const int slot = at.pos & ((1 << p.page_log2) - 1), vl = 31 - __clz(p.D / N), vecs = 1 << vl, n = p.Hkv << vl;
+    for (int i = threadIdx.x; i < n; i += kThreads) {  // a vector of K and the same of V
+        const int h = i >> vl, u = i & (vecs - 1);
+        const int64_t from[2] = {at.page * p.ks[0] + slot * p.ks[1] + h * p.ks[2], at.page * p.vs[0] + slot * p.vs[1] + h * p.vs[2]};
+        const int64_t to[2] = {(t * p.k_stride + h * p.D) * ES + 16 * u, (t * p.v_stride + h * p.D) * ES + 16 * u};
+        uint4 x[2];
         if constexpr (BITS == 4) {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(v ? p.Vc : p.Kc) + from + 8 * gi);
-            const int64_t* ss = v ? z.vss : z.kss;
-            const uint32_t s = (v ? z.v_scales : z.k_scales)[at.page * ss[0] + h * ss[1] + slot * ng + gi];
-            const float f = z.factor[v ? 1 : 0], sc = f16_to_float(e4m3_to_f16(s)).x;
+            uint32_t w[2], s[2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int v = 0; v < 2; ++v) {
+                const int64_t* ss = v ? z.vss : z.kss;
+                w[v] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(v ? p.Vc : p.Kc) + from[v] + 4 * u);
+                s[v] = (v ? z.v_scales : z.k_scales)[at.page * ss[0] + h * ss[1] + ((slot << vl) + u) / 2];
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float f = z.factor[v], sc = scale_value(s[v]);
                 uint32_t e[4], o[4];
-                e2m1_to_f16(q ? w.y : w.x, e);
+                e2m1_to_f16(w[v], e);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x = f16_to_float(e[k]);
-                    o[k] = pack_bf16x2(x.x * sc * f, x.y * sc * f);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = f16_to_float(e[j]);
+                    o[j] = pack_bf16x2(y.x * sc * f, y.y * sc * f);
                 }
-                dst[q] = make_uint4(o[0], o[1], o[2], o[3]);
+                x[v] = make_uint4(o[0], o[1], o[2], o[3]);
             }
         } else {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(v ? p.Vc : p.Kc) + (from + 16 * gi) * ES);
-            uint4 x[ES];
 #pragma unroll
-            for (int k = 0; k < ES; ++k) x[k] = src[k];
-#pragma unroll
-            for (int k = 0; k < ES; ++k) dst[k] = x[k];
+            for (int v = 0; v < 2; ++v)
+                x[v] = *reinterpret_cast<const uint4*>(static_cast<const char*>(v ? p.Vc : p.Kc) + from[v] * ES + 16 * u);
         }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) *reinterpret_cast<uint4*>(static_cast<char*>(const_cast<void*>(v ? p.V : p.K)) + to[v]) = x[v];
     }
 }
 

@@ -26,8 +26,8 @@ template <typename T>
 struct Vec {  // 16 bytes of T as floats
     static constexpr int N = 16 / sizeof(T);
     float v[N];
-    __device__ __forceinline__ void load(const T* src) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src);
+    __device__ __forceinline__ void load(const T* src) { set(*reinterpret_cast<const uint4*>(src)); }
+    __device__ __forceinline__ void set(const uint4 u) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -51,18 +51,42 @@ struct Vec {  // 16 bytes of T as floats
     }
 };
 
-// Vectors [d, d + N) (and, for a half-split pair, [d + R/2, + N)) of one head, from src to dst.
+// COUNT neighbouring floats (their address a multiple of COUNT floats).
+template <int COUNT>
+__device__ __forceinline__ void load_floats(const float* src, float (&v)[COUNT]) {
+    static_assert(COUNT == 2 || COUNT % 4 == 0, "one or more vectors");
+    if constexpr (COUNT == 2) {
+        const float2 u = *reinterpret_cast<const float2*>(src);
+        v[0] = u.x;
+        v[1] = u.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < COUNT; i += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(src + i);
+            v[i] = u.x;
+            v[i + 1] = u.y;
+            v[i + 2] = u.z;
+            v[i + 3] = u.w;
+        }
+    }
+}
+
+// Unit `unit` of one head: vectors [d, d + N) (and, for a half-split pair, [d + R/2, + N)), given as
+// they are, to dst.  (The table's rows start on 16 bytes, and R is a multiple of 16.)
 template <typename T>
-__device__ __forceinline__ void rotate_unit(const T* src, T* dst, int unit, const float* row, int R, bool pairs) {
+__device__ __forceinline__ void rotate_unit(const uint4 own, const uint4 other, T* dst, int unit, const float* row, int R, bool pairs) {
     constexpr int N = Vec<T>::N;
     Vec<T> a;
     if (pairs) {
         const int d = unit * N;
-        a.load(src + d);
+        a.set(own);
         if (d < R) {
+            float cs[N / 2], sn[N / 2];
+            load_floats<N / 2>(row + d / 2, cs);
+            load_floats<N / 2>(row + R / 2 + d / 2, sn);
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                const float c = row[(d + i) / 2], s = row[R / 2 + (d + i) / 2];
+                const float c = cs[i / 2], s = sn[i / 2];
                 const float x = a.v[i], y = a.v[i + 1];
                 a.v[i] = x * c - y * s;
                 a.v[i + 1] = y * c + x * s;
@@ -73,23 +97,33 @@ __device__ __forceinline__ void rotate_unit(const T* src, T* dst, int unit, cons
     }
     const int half = R / 2;
     if (unit * N >= half) {  // the elements past R, copied
-        const int d = unit * N + half;
-        *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
+        *reinterpret_cast<uint4*>(dst + unit * N + half) = own;
         return;
     }
     const int d = unit * N;
     Vec<T> b;
-    a.load(src + d);
-    b.load(src + d + half);
+    a.set(own);
+    b.set(other);
+    float cs[N], sn[N];
+    load_floats<N>(row + d, cs);
+    load_floats<N>(row + half + d, sn);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float c = row[d + i], s = row[half + d + i];
+        const float c = cs[i], s = sn[i];
         const float x = a.v[i], y = b.v[i];
         a.v[i] = x * c - y * s;
         b.v[i] = y * c + x * s;
     }
     a.store(dst + d);
     b.store(dst + d + half);
+}
+template <typename T>
+__device__ __forceinline__ void rotate_unit(const T* src, T* dst, int unit, const float* row, int R, bool pairs) {
+    constexpr int N = Vec<T>::N;
+    const int d = unit * N + (!pairs && 2 * unit * N >= R ? R / 2 : 0);
+    uint4 other = make_uint4(0u, 0u, 0u, 0u);
+    if (!pairs && 2 * unit * N < R) other = *reinterpret_cast<const uint4*>(src + d + R / 2);
+    rotate_unit<T>(*reinterpret_cast<const uint4*>(src + d), other, dst, unit, row, R, pairs);
 }
 
 // Where new token t lies: its sequence's number, position and page, or b < 0 (it belongs to none)

@@ -35,13 +35,18 @@ __device__ __forceinline__ uint32_t to_e4m3(float a, float b) {
     return two;
 }
 
-// The e2m1 codes nearest to a (low half of the byte) and b, ties to even, at most 6.
-__device__ __forceinline__ uint32_t to_e2m1(float a, float b) {
-    uint32_t two;
-    asm("{\n\t.reg .b8 x;\n\t.reg .b16 y;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\tmov.b16 y, {x, 0};\n\tcvt.u32.u16 %0, y;\n\t}"
-        : "=r"(two)
-        : "f"(a), "f"(b));
-    return two;
+// The e2m1 codes nearest to eight values, ties to even, at most 6.
+__device__ __forceinline__ uint32_t to_e2m1(const float* v) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
 }
 
 __device__ __forceinline__ uint32_t f16_mul2(uint32_t a, uint32_t b) {
