@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) jfa_cache_append4_kernel(const Cache
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            if (i + k * kThreads < nq) rotate_unit<T>(r[k].own, r[k].other, dst[k], u[k], row, R, p.pairs);
+            if (i + k * kThreads < nq) rotate_vectors<T>(r[k].own, r[k].other, dst[k], u[k], row, R, p.pairs);
     }
     auto whole = [](float f) { return (__float_as_uint(f) & 0x7fffffu) == 0u; };  // a power of two
     for (int i0 = first; i0 < nk; i0 += kThreads) {

@@ -51,6 +51,47 @@ struct Vec {  // 16 bytes of T as floats
     }
 };
 
+// Vectors [d, d + N) (and, for a half-split pair, [d + R/2, + N)) of one head, from src to dst.
+template <typename T>
+__device__ __forceinline__ void rotate_unit(const T* src, T* dst, int unit, const float* row, int R, bool pairs) {
+    constexpr int N = Vec<T>::N;
+    Vec<T> a;
+    if (pairs) {
+        const int d = unit * N;
+        a.load(src + d);
+        if (d < R) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float c = row[(d + i) / 2], s = row[R / 2 + (d + i) / 2];
+                const float x = a.v[i], y = a.v[i + 1];
+                a.v[i] = x * c - y * s;
+                a.v[i + 1] = y * c + x * s;
+            }
+        }
+        a.store(dst + d);
+        return;
+    }
+    const int half = R / 2;
+    if (unit * N >= half) {  // the elements past R, copied
+        const int d = unit * N + half;
+        *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
+        return;
+    }
+    const int d = unit * N;
+    Vec<T> b;
+    a.load(src + d);
+    b.load(src + d + half);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float c = row[d + i], s = row[half + d + i];
+        const float x = a.v[i], y = b.v[i];
+        a.v[i] = x * c - y * s;
+        b.v[i] = y * c + x * s;
+    }
+    a.store(dst + d);
+    b.store(dst + d + half);
+}
+
 // COUNT neighbouring floats (their address a multiple of COUNT floats).
 template <int COUNT>
 __device__ __forceinline__ void load_floats(const float* src, float (&v)[COUNT]) {
@@ -71,10 +112,11 @@ __device__ __forceinline__ void load_floats(const float* src, float (&v)[COUNT])
     }
 }
 
-// Unit `unit` of one head: vectors [d, d + N) (and, for a half-split pair, [d + R/2, + N)), given as
-// they are, to dst.  (The table's rows start on 16 bytes, and R is a multiple of 16.)
+// rotate_unit of vectors that are loaded, with the angles in vectors as well (the table's rows start on
+// 16 bytes, and R is a multiple of 16).  It takes more registers: in the append kernel of 16- and 32-bit
+// caches, which lives on many CTAs an SM, 24 prompts took 114 us with it instead of 107.
 template <typename T>
-__device__ __forceinline__ void rotate_unit(const uint4 own, const uint4 other, T* dst, int unit, const float* row, int R, bool pairs) {
+__device__ __forceinline__ void rotate_vectors(const uint4 own, const uint4 other, T* dst, int unit, const float* row, int R, bool pairs) {
     constexpr int N = Vec<T>::N;
     Vec<T> a;
     if (pairs) {
@@ -117,15 +159,6 @@ __device__ __forceinline__ void rotate_unit(const uint4 own, const uint4 other, 
     a.store(dst + d);
     b.store(dst + d + half);
 }
-template <typename T>
-__device__ __forceinline__ void rotate_unit(const T* src, T* dst, int unit, const float* row, int R, bool pairs) {
-    constexpr int N = Vec<T>::N;
-    const int d = unit * N + (!pairs && 2 * unit * N >= R ? R / 2 : 0);
-    uint4 other = make_uint4(0u, 0u, 0u, 0u);
-    if (!pairs && 2 * unit * N < R) other = *reinterpret_cast<const uint4*>(src + d + R / 2);
-    rotate_unit<T>(*reinterpret_cast<const uint4*>(src + d), other, dst, unit, row, R, pairs);
-}
-
 // Where new token t lies: its sequence's number, position and page, or b < 0 (it belongs to none)
 // or page < 0 (a bad sequence or page).  By a whole warp.
 struct CachePlace {
