@@ -7,9 +7,9 @@
 // with lo and hi the block's least and largest elements, so the group costs what one head does.
 //
 // The selection is that of exact arithmetic.  Scores are taken in fp32: u and w are sums of g values of
-// one sign, and a dot product adds at most 128 products (the even or odd ones, or a lane's 32) and
-// joins the sums in up to 3 steps, so a score is off by less than
-//   slack = (g + 132) 2^-24 max|lo, hi| sum_d (u_d - w_d).
+// one sign, and a dot product adds n products one after the other (a lane's D / 4, or the D even or
+// odd ones of a tile) and joins the sums in up to 3 steps, so a score is off by less than
+//   slack = (g + n + 4) 2^-24 max|lo, hi| sum_d (u_d - w_d).
 // With t the k-th largest fp32 score, the exact k-th largest lies within slack of t: a block above
 // t + 2 slack is in, one below t - 2 slack is out, and those between, mostly one, are scored
 // again in 64 bits and taken in order, of equal ones the lower index.
@@ -31,9 +31,7 @@ namespace {
 constexpr int kChunk = 64;          // blocks that a CTA scores
 constexpr int kSumThreads = 512, kScoreThreads = 256, kTileThreads = 128;
 constexpr int kTileTokens = 32;     // tokens that a CTA scores, where a sequence has many
-constexpr int kWarpItems = 4, kWarpRegs = 16, kWarpHeld = 32 * kWarpRegs;    // choosing by warps: up to 512 scores
-constexpr int kSelThreads = 512, kSelRegs = 16, kHeld = kSelThreads * kSelRegs;  // and by CTAs: so many in registers
-constexpr int kExact = 1024;        // candidates whose 64-bit scores a CTA keeps
+constexpr int kSelWarps = 32;       // warps that choose for one item, where more than 512 blocks may compete
 
 struct BlockParams {
     CacheAppendParams a;            // the batch and the cache
@@ -105,7 +103,7 @@ __global__ void __launch_bounds__(kSumThreads) jfa_cache_summarize_kernel(const 
                 if constexpr (FOUR) {
                     const uint8_t* codes = static_cast<const uint8_t*>(p.Kc) + page * p.ks[0] + h * p.ks[2] + 4 * u;
                     const uint8_t* scales = z.k_scales + page * z.kss[0] + h * z.kss[1] + (u >> 1);
-#pragma unroll 4
+#pragma unroll 8
                     for (int j = in ? who : n; j < n; j += share) {
                         const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + j * p.ks[1]);
                         const float s = f16_to_float(e4m3_to_f16(scales[j << (vl - 1)])).x;
@@ -181,8 +179,8 @@ __device__ __forceinline__ void query_sums(const BlockParams& z, int t, int hk, 
 
 // What an fp32 score may be off by: m the largest magnitude among the bounds, norm the sums' norm
 // (which is itself a sum of 2 D values, hence the 1.01).
-__device__ __forceinline__ float slack_of(const BlockParams& z, float m, float norm) {
-    return float(z.g + 132) * (1.01f * 0x1p-24f) * m * norm;
+__device__ __forceinline__ float slack_of(const BlockParams& z, int steps, float m, float norm) {
+    return float(z.g + steps) * (1.01f * 0x1p-24f) * m * norm;
 }
 
 // Page of block k of sequence b, or -1.
@@ -199,6 +197,7 @@ __global__ void __launch_bounds__(kScoreThreads) jfa_cache_score_kernel(const Bl
     const CacheAppendParams& p = z.a;
     constexpr int kLanes = 8, kAt = kScoreThreads / kLanes, kTimes = kChunk / kAt, NV = D / 32;  // vectors of a lane: 2 D / 64
     const int t = blockIdx.x, hk = blockIdx.z, lane = threadIdx.x & 31;
+    launch_dependents();  // (the choice waits for this kernel to end)
     const Chooser c = chooser(p, t, lane);
     const int first = z.n_first, end = c.own + 1 - z.n_last, k0 = blockIdx.y * kChunk;  // the blocks that compete
     if (c.b < 0 || c.own + 1 <= z.n_blocks || k0 >= end) return;
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kScoreThreads) jfa_cache_score_kernel(const Bl
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int w = 1; w < kScoreThreads / 32; ++w) m = fmaxf(m, red[w]);
-        z.slack[(size_t(t) * p.Hkv + hk) * size_t(z.chunks) + blockIdx.y] = slack_of(z, m, norm);
+        z.slack[(size_t(t) * p.Hkv + hk) * size_t(z.chunks) + blockIdx.y] = slack_of(z, 8 * NV + 4, m, norm);
     }
 }
 
@@ -276,6 +275,7 @@ __global__ void __launch_bounds__(kTileThreads) jfa_cache_score_tile_kernel(cons
     const int lane = threadIdx.x & 31, hk = blockIdx.z, t0 = blockIdx.x * kTileTokens, t1 = min(t0 + kTileTokens, p.T), k0 = blockIdx.y * kChunk;
     // tokens 4 tg .. and blocks bg + 16 i of a thread: a warp has two token groups
     const int tg = threadIdx.x >> 4, bg = threadIdx.x & 15;
+    launch_dependents();  // (the choice waits for this kernel to end)
     int b = find_sequence(p.q_off, p.B, t0, lane);
     if (b < 0) b = 0;
     bool have_sums = false;
@@ -291,31 +291,42 @@ __global__ void __launch_bounds__(kTileThreads) jfa_cache_score_tile_kernel(cons
         const int last = kv - q1 + tb - 1;                              // the last token's position
         const int most = last >= 0 ? (last >> p.page_log2) + 1 : 0;
         if (most <= z.n_blocks || k0 >= most - z.n_last) continue;
-        const bool fresh = !have_sums;
-        if (fresh) {
+        if (!have_sums) {
             have_sums = true;
-            for (int e = threadIdx.x; e < kTileTokens * D; e += kTileThreads) {
-                const int i = e / D, d = e % D;
-                float u = 0.f, w = 0.f;
+            // eight columns of a token a thread, the lanes of a token side by side
+            constexpr int kVecs = D / 8;
+            for (int e = threadIdx.x; e < kTileTokens * kVecs; e += kTileThreads) {
+                const int i = e / kVecs, v = e % kVecs;
+                float u[8], w[8], n = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = w[j] = 0.f;
                 if (t0 + i < t1) {
-                    const __nv_bfloat16* q = z.Q + (t0 + i) * z.q_stride + hk * z.g * D + d;
+                    const __nv_bfloat16* q = z.Q + (t0 + i) * z.q_stride + hk * z.g * D + 8 * v;
+#pragma unroll 4
                     for (int h = 0; h < z.g; ++h) {
-                        const float x = __bfloat162float(q[h * D]);
-                        u += fmaxf(x, 0.f);
-                        w += fminf(x, 0.f);
+                        Vec<__nv_bfloat16> x;
+                        x.load(q + h * D);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            u[j] += fmaxf(x.v[j], 0.f);
+                            w[j] += fminf(x.v[j], 0.f);
+                        }
                     }
                 }
-                sums[i * kPitch + d] = w;
-                sums[i * kPitch + D + d] = u;
+                float4* to = reinterpret_cast<float4*>(sums + i * kPitch + 8 * v);
+                to[0] = make_float4(w[0], w[1], w[2], w[3]);
+                to[1] = make_float4(w[4], w[5], w[6], w[7]);
+                to[D / 4] = make_float4(u[0], u[1], u[2], u[3]);
+                to[D / 4 + 1] = make_float4(u[4], u[5], u[6], u[7]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) n += u[j] - w[j];
+#pragma unroll
+                for (int d = 1; d < kVecs; d <<= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+                if (v == 0) norms[i] = n;
             }
         }
         if (threadIdx.x == 0) top = 0u;
         __syncthreads();
-        if (fresh && threadIdx.x < kTileTokens) {
-            float n = 0.f;
-            for (int d = 0; d < kRow; ++d) n += fabsf(sums[threadIdx.x * kPitch + d]);
-            norms[threadIdx.x] = n;
-        }
         uint32_t m = 0u;
         for (int e = threadIdx.x; e < kChunk * (kRow / 8); e += kTileThreads) {
             const int i = e / (kRow / 8), v = e % (kRow / 8), k = k0 + i;
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kTileThreads) jfa_cache_score_tile_kernel(cons
                 if (k >= z.n_first && k < n - z.n_last) out[k] = acc[i][j].x + acc[i][j].y;
             }
             if (bg == 0)
-                z.slack[(size_t(t) * p.Hkv + hk) * size_t(z.chunks) + blockIdx.y] = slack_of(z, __uint_as_float(top << 16), norms[4 * tg + i]);
+                z.slack[(size_t(t) * p.Hkv + hk) * size_t(z.chunks) + blockIdx.y] = slack_of(z, D + 2, __uint_as_float(top << 16), norms[4 * tg + i]);
         }
         __syncthreads();
     }
@@ -405,23 +416,264 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
     return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-// The k-th largest (k >= 1) of the scores that a group of threads holds, NR a thread (-inf where there
-// is none; at least k are finite): the border between `count(c) >= k` and `< k`, count(c) the
-// number of scores of at least c, which is the same in all threads.  Halves the values between
-// the smallest and the largest, and after that their bit patterns, until a border has k scores above.
-template <int NR, typename Count, typename Least>
-__device__ __forceinline__ float kth_largest(const float (&v)[NR], float smallest, float largest, int k, Count&& count, Least&& least) {
-    uint32_t lo = ordered(smallest), hi = ordered(largest) + 1u;  // count(lo) >= k > count(hi)
-    for (int step = 0; hi - lo > 1u; ++step) {
+// The threads that choose for one token and key head: a warp of a CTA, or the CTA.  Their kernels run
+// alone and cold, so what they cost beside latencies is the code they fetch: scores lie in shared
+// memory and loops stay rolled (kept in registers, with every pass laid out: 37 us for one long
+// history instead of @, most of it instruction fetches), and what few items need is a call.
+template <int WARPS>
+struct Choosers {
+    static constexpr int kThreads = 32 * WARPS, kItems = WARPS == 1 ? 4 : 1;
+    static constexpr int kHeld = WARPS == 1 ? 512 : 8192, kCands = WARPS == 1 ? 512 : 1024;
+    struct Smem {
+        float held[kHeld];
+        unsigned long long keys[kCands];
+        double sums[2 * 128];
+        int cand[kCands];
+        unsigned long long prefix;
+        float ends[3][WARPS > 2 ? WARPS : 2];
+        int hist[256];
+        int parts[2][WARPS];
+        int left, found;
+    };
+    Smem* m;
+    int thread, lane, warp, turn;
+
+    __device__ void sync() const {
+        if (WARPS == 1)
+            __syncwarp();
+        else
+            __syncthreads();
+    }
+    __device__ int total(int a) {  // (two buffers: one synchronisation a sum)
+        a = __reduce_add_sync(0xffffffffu, a);
+        if (WARPS == 1) return a;
+        turn ^= 1;
+        if (lane == 0) m->parts[turn][warp] = a;
+        __syncthreads();
+        return __reduce_add_sync(0xffffffffu, lane < WARPS ? m->parts[turn][lane] : 0);
+    }
+    // a's sum over the threads before this one, and over all of them
+    __device__ int before(bool a, int& all) {
+        const uint32_t votes = __ballot_sync(0xffffffffu, a);
+        const int mine = __popc(votes & ((1u << lane) - 1u));
+        all = __popc(votes);
+        if (WARPS == 1) return mine;
+        turn ^= 1;
+        if (lane == 0) m->parts[turn][warp] = all;
+        __syncthreads();
+        const int p = lane < WARPS ? m->parts[turn][lane] : 0;
+        all = __reduce_add_sync(0xffffffffu, p);
+        return __reduce_add_sync(0xffffffffu, lane < warp ? p : 0) + mine;
+    }
+};
+
+// Settles the candidates, scores in [low, above], of which the best `need` are chosen: their scores become
+// +inf or -inf.  In 64 bits, on arithmetic units that are few here, so only what settle_pairs leaves.
+template <int WARPS>
+__device__ __noinline__ void settle_exactly(Choosers<WARPS>& g, const BlockParams& z, const int t, const int b, const int hk, const int first,
+                                            float* sc, const int n, const float low, const float above, const int need, const int nc) {
+    using C = Choosers<WARPS>;
+    auto is_cand = [&](int i) { return i < n && sc[i] >= low && sc[i] <= above; };
+    query_sums<double>(z, t, hk, g.m->sums, g.thread, C::kThreads);
+    if (g.thread == 0) g.m->found = 0;
+    g.sync();
+    if (nc <= C::kCands) {
+        for (int i = g.thread; i < n; i += C::kThreads)
+            if (is_cand(i)) g.m->cand[atomicAdd(&g.m->found, 1)] = i;
+        g.sync();
+        for (int i = g.warp; i < nc; i += WARPS) {
+            const double s = exact_score(z, b, hk, first + g.m->cand[i], g.m->sums, g.lane);
+            if (g.lane == 0) g.m->keys[i] = ordered64(s);
+        }
+        g.sync();
+        for (int i = g.thread; i < nc; i += C::kThreads) {
+            const unsigned long long mine = g.m->keys[i];
+            const int at = g.m->cand[i];
+            int rank = 0;
+            for (int j = 0; j < nc; ++j) rank += g.m->keys[j] > mine || (g.m->keys[j] == mine && g.m->cand[j] < at);
+            sc[at] = rank < need ? INFINITY : -INFINITY;
+        }
+        g.sync();
+        return;
+    }
+    // Very many nearly equal scores (a CTA's): the need-th largest exact score, eight bits at a time, each
+    // pass scoring all candidates again; then equal ones by their index.
+    if constexpr (WARPS > 1) {
+        if (g.thread == 0) {
+            g.m->prefix = 0ull;
+            g.m->left = need;
+        }
+        auto key_of = [&](int i) { return ordered64(exact_score(z, b, hk, first + i, g.m->sums, g.lane)); };
+        for (int shift = 56; shift >= 0; shift -= 8) {
+            if (g.thread < 256) g.m->hist[g.thread] = 0;
+            __syncthreads();
+            const unsigned long long mask = shift == 56 ? 0ull : ~0ull << (shift + 8), want = g.m->prefix;
+            for (int i = g.warp; i < n; i += WARPS) {
+                if (!is_cand(i)) continue;
+                const unsigned long long key = key_of(i);
+                if (g.lane == 0 && (key & mask) == want) atomicAdd(&g.m->hist[int((key >> shift) & 255u)], 1);
+            }
+            __syncthreads();
+            if (g.thread == 0) {
+                int higher = 0, d = 255;
+                while (d > 0 && higher + g.m->hist[d] < g.m->left) higher += g.m->hist[d--];
+                g.m->left -= higher;
+                g.m->prefix |= (unsigned long long)(d) << shift;
+            }
+            __syncthreads();
+        }
+        const unsigned long long border = g.m->prefix;
+        int equal = g.m->left;  // of those at the border, the first so many
+        for (int i0 = 0; i0 < n; i0 += WARPS) {
+            const int i = i0 + g.warp;
+            const bool is = is_cand(i);
+            const unsigned long long key = is ? key_of(i) : 0ull;
+            int all;
+            // (one vote a warp: thread 0 of each)
+            const int at = g.before(g.lane == 0 && is && key == border, all);
+            if (g.lane == 0 && is) sc[i] = key > border || (key == border && at < equal) ? INFINITY : -INFINITY;
+            equal -= all;
+        }
+        __syncthreads();
+    }
+}
+
+// a + b = s + e exactly (Knuth).
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+    s = __fadd_rn(a, b);
+    const float v = __fsub_rn(s, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v));
+}
+
+// The same in pairs of floats: sums and products with their rounding errors carried along (Ogita, Rump
+// and Oishi, SIAM J. Sci. Comput. 26, 2005).  A lane's 8 terms and 5 steps between lanes leave an error below
+// 2^-40 of the products' magnitudes, less than slack / 2^20.  What even that leaves open goes on
+// to settle_exactly.  slack 0: all bounds or all queries are zero, the candidates' scores exact and equal.
+template <int WARPS>
+__device__ __noinline__ void settle(Choosers<WARPS>& g, const BlockParams& z, const int t, const int b, const int hk, const int first, float* sc,
+                                    const int n, const float low, const float above, const float slack, const int need, const int nc) {
+    using C = Choosers<WARPS>;
+    const CacheAppendParams& p = z.a;
+    auto is_cand = [&](int i) { return i < n && sc[i] >= low && sc[i] <= above; };
+    if (slack == 0.f) {
+        int seen = 0, all;
+        for (int i0 = 0; i0 < n; i0 += C::kThreads) {
+            const int i = i0 + g.thread;
+            const bool is = is_cand(i);
+            const int at = seen + g.before(is, all);
+            if (is) sc[i] = at < need ? INFINITY : -INFINITY;
+            seen += all;
+        }
+        g.sync();
+        return;
+    }
+    if (nc > C::kCands) {
+        settle_exactly<WARPS>(g, z, t, b, hk, first, sc, n, low, above, need, nc);
+        return;
+    }
+    float2* pairs = reinterpret_cast<float2*>(g.m->keys);
+    // A lane has 8 (or 4) of a block's 2 D bounds, lo's in the first half of the lanes, and their queries' sums.
+    const int per = p.D / 16, d0 = (g.lane & 15) * per;
+    float hi8[8], lo8[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hi8[j] = lo8[j] = 0.f;
+    const __nv_bfloat16* q = z.Q + t * z.q_stride + hk * z.g * p.D + d0;
+    auto eight = [&](const __nv_bfloat16* src, float (&v)[8]) {
+        const uint2 a = *reinterpret_cast<const uint2*>(src), b = per == 8 ? *reinterpret_cast<const uint2*>(src + 4) : make_uint2(0u, 0u);
+        Vec<__nv_bfloat16> x;
+        x.set(make_uint4(a.x, a.y, b.x, b.y));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = x.v[j];
+    };
+#pragma unroll(WARPS == 1 ? 4 : 1)
+    for (int h = 0; h < z.g; ++h) {
+        float x[8], e;
+        eight(q + h * p.D, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            two_sum(hi8[j], g.lane < 16 ? fminf(x[j], 0.f) : fmaxf(x[j], 0.f), hi8[j], e);
+            lo8[j] += e;
+        }
+    }
+    if (g.thread == 0) g.m->found = 0;
+    g.sync();
+    for (int i = g.thread; i < n; i += C::kThreads)
+        if (is_cand(i)) g.m->cand[atomicAdd(&g.m->found, 1)] = i;
+    g.sync();
+    constexpr int kAtOnce = WARPS == 1 ? 4 : 1;  // candidates whose pages and bounds a warp asks for together
+    for (int i0 = g.warp * kAtOnce; i0 < nc; i0 += WARPS * kAtOnce) {
+        int page[kAtOnce];
+        float x[kAtOnce][8];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) page[k] = i0 + k < nc ? block_page(p, b, first + g.m->cand[i0 + k]) : -1;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (page[k] >= 0) eight(z.bounds + (size_t(page[k]) * p.Hkv + hk) * 2 * p.D + per * g.lane, x[k]);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (i0 + k >= nc) break;
+            float s = 0.f, c = 0.f, e;
+            if (page[k] >= 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float m = __fmul_rn(x[k][j], hi8[j]), r = __fmaf_rn(x[k][j], hi8[j], -m);
+                    two_sum(s, m, s, e);
+                    c += e + (r + x[k][j] * lo8[j]);
+                }
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                const float other = __shfl_xor_sync(0xffffffffu, s, d);
+                c += __shfl_xor_sync(0xffffffffu, c, d);
+                two_sum(s, other, s, e);
+                c += e;
+            }
+            two_sum(s, c, s, e);
+            if (g.lane == 0) pairs[i0 + k] = make_float2(s, e);
+        }
+    }
+    g.sync();
+    // the need-th and the next, by pairs
+    float2* border = reinterpret_cast<float2*>(g.m->ends);
+    uint8_t* chosen = reinterpret_cast<uint8_t*>(g.m->sums);
+    static_assert(C::kCands <= sizeof(g.m->sums));
+    for (int i = g.thread; i < nc; i += C::kThreads) {
+        const float2 mine = pairs[i];
+        const int at = g.m->cand[i];
+        int rank = 0;
+        for (int j = 0; j < nc; ++j) {
+            const float2 o = pairs[j];
+            rank += o.x > mine.x || (o.x == mine.x && (o.y > mine.y || (o.y == mine.y && g.m->cand[j] < at)));
+        }
+        if (rank == need - 1 || rank == need) border[rank - need + 1] = mine;
+        chosen[i] = rank < need;
+    }
+    g.sync();
+    const bool open = (border[0].x - border[1].x) + (border[0].y - border[1].y) <= 0x1p-14f * slack;
+    g.sync();
+    if (open) {
+        settle_exactly<WARPS>(g, z, t, b, hk, first, sc, n, low, above, need, nc);
+        return;
+    }
+    for (int i = g.thread; i < nc; i += C::kThreads) sc[g.m->cand[i]] = chosen[i] ? INFINITY : -INFINITY;
+    g.sync();
+}
+
+// The k-th largest score where very many are nearly equal (or all are): halves the values between the least and
+// the largest, after 16 steps their bit patterns.
+template <int WARPS>
+__device__ __noinline__ float search(Choosers<WARPS>& g, const float* sc, const int n, const int k, const float small, const float large) {
+    uint32_t lo = ordered(small), hi = ordered(large) + 1u;  // k scores or more are at least lo, fewer at least hi
+    for (int step = 0; hi - lo > 1u && step < 64; ++step) {
         uint32_t mid = lo + (hi - lo) / 2u;
         if (step < 16) {
-            const uint32_t c = ordered(0.5f * unordered(lo) + 0.5f * unordered(hi - 1u));
-            if (c > lo && c < hi) mid = c;
+            const uint32_t m = ordered(0.5f * unordered(lo) + 0.5f * unordered(hi - 1u));
+            if (m > lo && m < hi) mid = m;
         }
         const float c = unordered(mid);
-        const int n = count(c);
-        if (n == k) return least(c);  // the smallest of those k
-        if (n > k)
+        int a = 0;
+        for (int i = g.thread; i < n; i += Choosers<WARPS>::kThreads) a += sc[i] >= c;
+        if (g.total(a) >= k)
             lo = mid;
         else
             hi = mid;
@@ -429,347 +681,166 @@ __device__ __forceinline__ float kth_largest(const float (&v)[NR], float smalles
     return unordered(lo);
 }
 
-// The chosen blocks of one token and key head by one warp, its scores in registers: up to 512 blocks
-// that compete.  Bound by latency: the sequence, the scores, about 12 steps of a search.
-__global__ void __launch_bounds__(32 * kWarpItems) jfa_cache_choose_warp_kernel(const BlockParams z) {
+// The chosen blocks of one token and key head, from its scores.
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems) jfa_cache_choose_kernel(const BlockParams z) {
+    using C = Choosers<WARPS>;
     const CacheAppendParams& p = z.a;
-    __shared__ unsigned long long keys[kWarpItems][kWarpHeld];
-    __shared__ uint16_t cand[kWarpItems][kWarpHeld];
-    __shared__ double sums[kWarpItems][2 * 128];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, item = blockIdx.x * kWarpItems + warp;
-    const int t = item / p.Hkv, hk = item - t * p.Hkv;
+    extern __shared__ __align__(16) uint8_t choose_smem[];
+    const int item = blockIdx.x * C::kItems + threadIdx.x / C::kThreads, t = item / p.Hkv, hk = item - t * p.Hkv;
+    C g{reinterpret_cast<typename C::Smem*>(choose_smem) + threadIdx.x / C::kThreads, int(threadIdx.x % C::kThreads), int(threadIdx.x & 31),
+        int(threadIdx.x % C::kThreads) >> 5, 0};
     if (t >= p.T) return;
-    const Chooser c = chooser(p, t, lane, lane == 0);
+    const Chooser c = chooser(p, t, g.lane, g.thread == 0);
     if (c.b < 0) return;
     int32_t* out = z.blocks + (size_t(t) * p.Hkv + hk) * size_t(z.n_blocks);
-    const int n = c.own + 1;
-    if (n <= z.n_blocks) {  // all that there are
-        for (int i = lane; i < z.n_blocks; i += 32) out[i] = i < n ? i : -1;
-        return;
+    const int all = c.own + 1, first = z.n_first, k = z.n_blocks - z.n_first - z.n_last, n = all - z.n_last - first;  // n compete for k places
+    const bool few = all <= z.n_blocks;
+    // the blocks that are chosen in any case, or all that there are
+#pragma unroll 1
+    for (int i = g.thread; i < z.n_blocks; i += C::kThreads) {
+        if (few)
+            out[i] = i < all ? i : -1;
+        else if (i < first || i >= first + k)
+            out[i] = i < first ? i : all - z.n_blocks + i;
     }
-    const int first = z.n_first, end = n - z.n_last, m = end - first, k = z.n_blocks - z.n_first - z.n_last;  // m > k
-    for (int i = lane; i < z.n_first; i += 32) out[i] = i;
-    for (int i = lane; i < z.n_last; i += 32) out[z.n_first + k + i] = end + i;
-    if (k == 0) return;
-    const float* sc = z.scores + (size_t(t) * p.Hkv + hk) * size_t(p.max_pages) + first;
-    const float* sl = z.slack + (size_t(t) * p.Hkv + hk) * size_t(z.chunks);
-    float v[kWarpRegs], small = INFINITY, large = -INFINITY, slack = 0.f;
-#pragma unroll
-    for (int r = 0; r < kWarpRegs; ++r) {
-        const int i = 32 * r + lane;
-        v[r] = -INFINITY;
-        if (i < m) {
-            v[r] = sc[i] + 0.f;  // (-0 is 0)
-            small = fminf(small, v[r]);
-            large = fmaxf(large, v[r]);
-        }
-    }
-    for (int i = first / kChunk + lane; i <= (end - 1) / kChunk; i += 32) slack = fmaxf(slack, sl[i]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        small = fminf(small, __shfl_xor_sync(0xffffffffu, small, d));
-        large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, d));
-        slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, d));
-    }
-    auto count = [&](float c) {
-        int a = 0;
-#pragma unroll
-        for (int r = 0; r < kWarpRegs; ++r) a += v[r] >= c;
-        return __reduce_add_sync(0xffffffffu, a);
-    };
-    auto least = [&](float c) {
-        float a = INFINITY;
-#pragma unroll
-        for (int r = 0; r < kWarpRegs; ++r)
-            if (v[r] >= c) a = fminf(a, v[r]);
-        return unordered(__reduce_min_sync(0xffffffffu, ordered(a)));
-    };
-    const float kth = kth_largest(v, small, large, k, count, least);
-    // (rounding the limits outwards only moves a block to the candidates)
-    const float above = __fadd_ru(kth, 2.f * slack), low = __fadd_rd(kth, -2.f * slack);
-    uint32_t is_in = 0u, is_cand = 0u;  // a bit for each register
-#pragma unroll
-    for (int r = 0; r < kWarpRegs; ++r) {
-        if (v[r] > above)
-            is_in |= 1u << r;
-        else if (v[r] >= low && 32 * r + lane < m)
-            is_cand |= 1u << r;
-    }
-    const int need = k - __reduce_add_sync(0xffffffffu, __popc(is_in)), nc = __reduce_add_sync(0xffffffffu, __popc(is_cand));
-    if (nc == need) {
-        is_in |= is_cand;
-    } else if (slack == 0.f) {
-        // bounds or queries of zeros: the scores are exact, and the candidates' equal: by index
-        int before = 0;
-#pragma unroll
-        for (int r = 0; r < kWarpRegs; ++r) {
-            const uint32_t votes = __ballot_sync(0xffffffffu, (is_cand >> r) & 1u);
-            if (((is_cand >> r) & 1u) && before + __popc(votes & ((1u << lane) - 1u)) < need) is_in |= 1u << r;
-            before += __popc(votes);
-        }
-    } else {
-        query_sums<double>(z, t, hk, sums[warp], lane, 32);
-        int at = 0;
-#pragma unroll
-        for (int r = 0; r < kWarpRegs; ++r) {  // the candidates, by index
-            const uint32_t votes = __ballot_sync(0xffffffffu, (is_cand >> r) & 1u);
-            if ((is_cand >> r) & 1u) cand[warp][at + __popc(votes & ((1u << lane) - 1u))] = uint16_t(32 * r + lane);
-            at += __popc(votes);
-        }
-        __syncwarp();
-        for (int i = 0; i < nc; ++i) {
-            const double s = exact_score(z, c.b, hk, first + cand[warp][i], sums[warp], lane);
-            if (lane == 0) keys[warp][i] = ordered64(s);
-        }
-        __syncwarp();
-        // a candidate's rank among them, noted in the place of its number
-        for (int i = lane; i < nc; i += 32) {
-            const unsigned long long mine = keys[warp][i];
-            int rank = 0;
-            for (int j = 0; j < nc; ++j) {
-                const unsigned long long other = keys[warp][j];
-                rank += other > mine || (other == mine && j < i);
-            }
-            if (rank >= need) cand[warp][i] = 0xffffu;
-        }
-        __syncwarp();
-        at = 0;
-#pragma unroll
-        for (int r = 0; r < kWarpRegs; ++r) {
-            const uint32_t votes = __ballot_sync(0xffffffffu, (is_cand >> r) & 1u);
-            if (((is_cand >> r) & 1u) && cand[warp][at + __popc(votes & ((1u << lane) - 1u))] != 0xffffu) is_in |= 1u << r;
-            at += __popc(votes);
-        }
-    }
-    int done = z.n_first;  // the chosen ones, ascending
-#pragma unroll
-    for (int r = 0; r < kWarpRegs; ++r) {
-        const bool in = (is_in >> r) & 1u;
-        const uint32_t votes = __ballot_sync(0xffffffffu, in);
-        const int to = done + __popc(votes & ((1u << lane) - 1u));
-        if (in && to < z.n_first + k) out[to] = first + 32 * r + lane;
-        done += __popc(votes);
-    }
-}
-
-// The same by a CTA: scores in registers up to 8192 blocks, from memory beyond.
-__global__ void __launch_bounds__(kSelThreads) jfa_cache_choose_kernel(const BlockParams z) {
-    const CacheAppendParams& p = z.a;
-    constexpr int kWarps = kSelThreads / 32;
-    __shared__ int hist[256];
-    __shared__ int cand[kExact];
-    __shared__ unsigned long long keys[kExact];
-    __shared__ double sums[2 * 128];
-    __shared__ float ends[3][kWarps];
-    __shared__ int parts[2][kWarps];
-    __shared__ int found, left;
-    __shared__ unsigned long long prefix;
-    const int t = blockIdx.x, hk = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Chooser c = chooser(p, t, lane, threadIdx.x == 0);
-    if (c.b < 0) return;
-    int32_t* out = z.blocks + (size_t(t) * p.Hkv + hk) * size_t(z.n_blocks);
-    const int n = c.own + 1;
-    if (n <= z.n_blocks) {  // all that there are
-        for (int i = threadIdx.x; i < z.n_blocks; i += kSelThreads) out[i] = i < n ? i : -1;
-        return;
-    }
-    const int first = z.n_first, end = n - z.n_last, m = end - first, k = z.n_blocks - z.n_first - z.n_last;  // m > k
-    for (int i = threadIdx.x; i < z.n_first; i += kSelThreads) out[i] = i;
-    for (int i = threadIdx.x; i < z.n_last; i += kSelThreads) out[z.n_first + k + i] = end + i;
-    if (k == 0) return;
+    if (few || k == 0) return;
+    wait_previous();  // for the scores
     float* sc = z.scores + (size_t(t) * p.Hkv + hk) * size_t(p.max_pages) + first;
     const float* sl = z.slack + (size_t(t) * p.Hkv + hk) * size_t(z.chunks);
-    // Warps hold neighbouring scores: warp w those from w * per on, `per` a multiple of 32.
-    const bool held = m <= kHeld;
-    const int per = (m + kSelThreads - 1) / kSelThreads * 32, from = warp * per, to = min(m, from + per);
-    float v[kSelRegs], small = INFINITY, large = -INFINITY, slack = 0.f;
-#pragma unroll
-    for (int r = 0; r < kSelRegs; ++r) {
-        const int i = from + 32 * r + lane;
-        v[r] = -INFINITY;
-        if (held && i < to) v[r] = sc[i] + 0.f;
+    float small = INFINITY, large = -INFINITY, slack = 0.f;
+    const bool held = n <= C::kHeld;
+#pragma unroll 4
+    for (int i = g.thread; i < n; i += C::kThreads) {
+        const float x = sc[i] + 0.f;  // (-0 is 0)
+        small = fminf(small, x);
+        large = fmaxf(large, x);
+        if (held) g.m->held[i] = x;
     }
-    // f(score, its number) for this thread's scores, in whole warps
-    auto each = [&](auto&& f) {
-        if (held) {
-#pragma unroll
-            for (int r = 0; r < kSelRegs; ++r)
-                if (32 * r < per) f(v[r], from + 32 * r + lane);
-        } else {
-            for (int i0 = from; i0 < from + per; i0 += 32) f(i0 + lane < to ? sc[i0 + lane] + 0.f : -INFINITY, i0 + lane);
-        }
-    };
-    each([&](float x, int i) {
-        if (i < to) {
-            small = fminf(small, x);
-            large = fmaxf(large, x);
-        }
-    });
-    for (int i = first / kChunk + threadIdx.x; i <= (end - 1) / kChunk; i += kSelThreads) slack = fmaxf(slack, sl[i]);
+    if (held) sc = g.m->held;
+#pragma unroll 1
+    for (int i = first / kChunk + g.thread; i <= (first + n - 1) / kChunk; i += C::kThreads) slack = fmaxf(slack, sl[i]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         small = fminf(small, __shfl_xor_sync(0xffffffffu, small, d));
         large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, d));
         slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, d));
     }
-    if (lane == 0) {
-        ends[0][warp] = small;
-        ends[1][warp] = large;
-        ends[2][warp] = slack;
-    }
-    if (threadIdx.x == 0) found = 0;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-        small = fminf(small, ends[0][w]);
-        large = fmaxf(large, ends[1][w]);
-        slack = fmaxf(slack, ends[2][w]);
-    }
-    int turn = 0;
-    auto total = [&](int a) {  // over the CTA (two buffers: one synchronisation a sum)
-        a = __reduce_add_sync(0xffffffffu, a);
-        turn ^= 1;
-        if (lane == 0) parts[turn][warp] = a;
-        __syncthreads();
-        return __reduce_add_sync(0xffffffffu, lane < kWarps ? parts[turn][lane] : 0);
-    };
-    auto count = [&](float x0) {
-        int a = 0;
-        each([&](float x, int) { a += x >= x0; });
-        return total(a);
-    };
-    auto least = [&](float x0) {
-        float a = INFINITY;
-        each([&](float x, int) {
-            if (x >= x0) a = fminf(a, x);
-        });
-        const uint32_t o = __reduce_min_sync(0xffffffffu, ordered(a));
-        __syncthreads();
-        if (lane == 0) ends[0][warp] = unordered(o);
-        __syncthreads();
-        a = ends[0][0];
-        for (int w = 1; w < kWarps; ++w) a = fminf(a, ends[0][w]);
-        return a;
-    };
-    const float kth = kth_largest(v, small, large, k, count, least);
-    const float above = __fadd_ru(kth, 2.f * slack), low = __fadd_rd(kth, -2.f * slack);
-    int sure = 0, maybe = 0;
-    each([&](float x, int i) {
-        if (x > above)
-            ++sure;
-        else if (x >= low && i < to)
-            ++maybe;
-    });
-    const int need = k - total(sure), nc = total(maybe);
-    // border: exact keys above it are in, and of equal ones those of lower numbers
-    unsigned long long border = 0ull;
-    int equal = 0;
-    const bool all = nc == need, exact = !all && slack != 0.f, keep = exact && nc <= kExact;
-    if (exact) {
-        query_sums<double>(z, t, hk, sums, threadIdx.x, kSelThreads);
-        __syncthreads();
-    }
-    auto is_cand = [&](float x, int i) { return i < to && x <= above && x >= low; };
-    if (keep) {
-        each([&](float x, int i) {
-            if (is_cand(x, i)) cand[atomicAdd(&found, 1)] = i;
-        });
-        __syncthreads();
-        for (int i = warp; i < nc; i += kWarps) {
-            const double s = exact_score(z, c.b, hk, first + cand[i], sums, lane);
-            if (lane == 0) keys[i] = ordered64(s);
+    if (WARPS > 1) {
+        if (g.lane == 0) {
+            g.m->ends[0][g.warp] = small;
+            g.m->ends[1][g.warp] = large;
+            g.m->ends[2][g.warp] = slack;
         }
         __syncthreads();
-        // the need-th of them: its key and number
-        for (int i = threadIdx.x; i < nc; i += kSelThreads) {
-            int rank = 0;
-            for (int j = 0; j < nc; ++j) rank += keys[j] > keys[i] || (keys[j] == keys[i] && cand[j] < cand[i]);
-            if (rank == need - 1) {
-                prefix = keys[i];
-                left = cand[i];
+#pragma unroll 1
+        for (int w = 0; w < WARPS; ++w) {
+            small = fminf(small, g.m->ends[0][w]);
+            large = fmaxf(large, g.m->ends[1][w]);
+            slack = fmaxf(slack, g.m->ends[2][w]);
+        }
+    } else {
+        __syncwarp();
+    }
+    // The k-th largest score, `up`, and the next, `down`: the scores by 256 steps of their range, then
+    // those of the step that holds the k-th by their rank.
+    float up, down = -INFINITY, kth;
+    bool found = large > small;
+    if (found) {
+        const float per = 255.f / (large - small);
+        auto step_of = [&](float x) { return max(0, min(int((x - small) * per), 255)); };
+#pragma unroll 1
+        for (int i = g.thread; i < 256; i += C::kThreads) g.m->hist[i] = 0;
+        if (g.thread == 0) {
+            g.m->found = g.m->left = 0;
+            g.m->prefix = 0ull;
+        }
+        g.sync();
+#pragma unroll 4
+        for (int i = g.thread; i < n; i += C::kThreads) atomicAdd(&g.m->hist[step_of(sc[i])], 1);
+        g.sync();
+        if (g.warp == 0) {  // a lane eight steps, from the top
+            int mine = 0;
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) mine += g.m->hist[255 - (8 * g.lane + j)];
+            int higher = warp_scan(mine, g.lane) - mine;
+            if (higher < k && higher + mine >= k) {
+                int j = 255 - 8 * g.lane;
+                while (higher + g.m->hist[j] < k) higher += g.m->hist[j--];
+                g.m->left = j;
+                g.m->prefix = higher;
             }
         }
-        __syncthreads();
-        border = prefix;
-        equal = left;
-        for (int i = threadIdx.x; i < nc; i += kSelThreads)  // the chosen ones' numbers stay
-            if (keys[i] < border || (keys[i] == border && cand[i] > equal)) cand[i] = -1;
-        __syncthreads();
-    } else if (exact) {
-        // Very many nearly equal scores: the need-th largest exact score, eight bits at a time, each
-        // pass scoring all candidates again.
-        if (threadIdx.x == 0) {
-            prefix = 0ull;
-            left = need;
-        }
-        for (int shift = 56; shift >= 0; shift -= 8) {
-            if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-            __syncthreads();
-            const unsigned long long mask = shift == 56 ? 0ull : ~0ull << (shift + 8), want = prefix;
-            each([&](float x, int i) {
-                for (uint32_t todo = __ballot_sync(0xffffffffu, is_cand(x, i)); todo; todo &= todo - 1) {
-                    const unsigned long long key = ordered64(exact_score(z, c.b, hk, first + i - lane + __ffs(todo) - 1, sums, lane));
-                    if (lane == 0 && (key & mask) == want) atomicAdd(&hist[int((key >> shift) & 255u)], 1);
+        g.sync();
+        const int step = g.m->left, rank = k - 1 - int(g.m->prefix), here = g.m->hist[step];
+        float* list = reinterpret_cast<float*>(g.m->keys);
+        found = here <= C::kCands;
+        if (found) {
+#pragma unroll 4
+            for (int i = g.thread; i < n; i += C::kThreads) {
+                const float x = sc[i];
+                const int at = step_of(x);
+                if (at == step)
+                    list[atomicAdd(&g.m->found, 1)] = x;
+                else if (at < step)
+                    down = fmaxf(down, x);
+            }
+            g.sync();
+#pragma unroll 1
+            for (int i = g.thread; i < here; i += C::kThreads) {
+                const float x = list[i];
+                int r = 0;
+#pragma unroll 4
+                for (int j = 0; j < here; ++j) r += list[j] > x || (list[j] == x && j < i);
+                if (r == rank) g.m->ends[0][0] = x;
+                if (r == rank + 1) g.m->ends[0][1] = x;
+            }
+            g.sync();
+            up = g.m->ends[0][0];
+            if (rank + 1 < here) {
+                down = g.m->ends[0][1];
+            } else {  // the largest of the lower steps
+                down = unordered(__reduce_max_sync(0xffffffffu, ordered(down)));
+                if (WARPS > 1) {
+                    if (g.lane == 0) g.m->ends[1][g.warp] = down;
+                    __syncthreads();
+#pragma unroll 1
+                    for (int w = 0; w < WARPS; ++w) down = fmaxf(down, g.m->ends[1][w]);
                 }
-            });
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                int higher = 0, d = 255;
-                while (d > 0 && higher + hist[d] < left) higher += hist[d--];
-                left -= higher;
-                prefix |= (unsigned long long)(d) << shift;
             }
-            __syncthreads();
         }
-        border = prefix;
-        equal = left;
-    } else if (!all) {
-        equal = need;  // (exact and equal: the first so many)
     }
-    // The chosen ones, ascending: a warp's numbers come after those of the warps before it.
-    // pass 0 counts, pass 1 writes; of candidates at the border (or equal ones) the first come first.
-    const bool by_count = !all && !keep;  // `equal` counts candidates, over the warps in order
-    int eq_before = 0, base = z.n_first;
-    for (int pass = 0; pass < 3; ++pass) {
-        // pass 0 (by_count only): candidates at the border before this warp
-        if (pass == 0 && !by_count) continue;
-        int mine = 0, eq = eq_before, at = base;
-        each([&](float x, int i) {
-            bool in = x > above, tie = false;
-            const bool cd = is_cand(x, i);
-            if (all) {
-                in = in || cd;
-            } else if (keep) {
-                if (cd)
-                    for (int j = 0; j < nc; ++j) in = in || cand[j] == i;
-            } else if (exact) {
-                for (uint32_t todo = __ballot_sync(0xffffffffu, cd); todo; todo &= todo - 1) {
-                    const int l = __ffs(todo) - 1;
-                    const unsigned long long key = ordered64(exact_score(z, c.b, hk, first + i - lane + l, sums, lane));
-                    if (l == lane) {
-                        in = key > border;
-                        tie = key == border;
-                    }
-                }
-            } else {
-                tie = cd;
-            }
-            const uint32_t ties = __ballot_sync(0xffffffffu, tie);
-            if (tie && pass > 0) in = eq + __popc(ties & ((1u << lane) - 1u)) < equal;
-            eq += __popc(ties);
-            if (pass == 0) return;
-            const uint32_t votes = __ballot_sync(0xffffffffu, in);
-            const int to_at = at + __popc(votes & ((1u << lane) - 1u));
-            if (pass == 2 && in && to_at < z.n_first + k) out[to_at] = first + i;
-            at += __popc(votes);
-            mine += __popc(votes);
-        });
-        __syncthreads();
-        turn ^= 1;
-        if (lane == 0) parts[turn][warp] = pass == 0 ? eq : mine;
-        __syncthreads();
-        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? parts[turn][lane] : 0);
-        if (pass == 0) eq_before = before;
-        if (pass == 1) base = z.n_first + before;
+    if (!found) up = down = search<WARPS>(g, sc, n, k, small, large);
+    kth = up;
+    float cut = kth;  // chosen: scores of at least this
+    // Scores further apart than twice the slack are in the order of the exact ones: then the k largest
+    // are the chosen ones.
+    if (up - down <= 2.01f * slack) {
+        const float above = __fadd_ru(kth, 2.f * slack), low = __fadd_rd(kth, -2.f * slack);
+        int sure = 0, maybe = 0;
+#pragma unroll 1
+        for (int i = g.thread; i < n; i += C::kThreads) {
+            sure += sc[i] > above;
+            maybe += sc[i] >= low && sc[i] <= above;
+        }
+        sure = g.total(sure);
+        maybe = g.total(maybe);
+        cut = low;
+        if (sure + maybe != k) {
+            settle<WARPS>(g, z, t, c.b, hk, first, sc, n, low, above, slack, k - sure, maybe);
+            // (chosen candidates are +inf now, the others -inf)
+            cut = above;
+        }
+    }
+    int done = 0;  // the chosen ones, ascending
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += C::kThreads) {
+        const int i = i0 + g.thread;
+        const bool in = i < n && sc[i] >= cut;
+        int here;
+        const int to = done + g.before(in, here);
+        if (in && to < k) out[first + to] = first + i;
+        done += here;
     }
 }
 
@@ -891,11 +962,31 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
         }
         if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return JFA_ERR_CUDA;
     }
-    if (max_pages <= kWarpHeld)
-        jfa_cache_choose_warp_kernel<<<int((T * cache->Hkv + kWarpItems - 1) / kWarpItems), 32 * kWarpItems, 0, st>>>(z);
-    else
-        jfa_cache_choose_kernel<<<dim3(z.a.T, cache->Hkv), kSelThreads, 0, st>>>(z);
-    return cudaGetLastError() == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+    // (started while the scores are still computed, whose end it waits for)
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = max_pages > n_blocks ? 1 : 0;
+    cudaError_t e;
+    if (max_pages <= Choosers<1>::kHeld) {
+        using C = Choosers<1>;
+        cfg.gridDim = dim3(int((T * cache->Hkv + C::kItems - 1) / C::kItems));
+        cfg.blockDim = dim3(C::kThreads * C::kItems);
+        cfg.dynamicSmemBytes = sizeof(C::Smem) * C::kItems;
+        e = cudaLaunchKernelEx(&cfg, jfa_cache_choose_kernel<1>, z);
+    } else {
+        using C = Choosers<kSelWarps>;
+        static std::atomic<uint64_t> done{0};
+        e = allow_smem(jfa_cache_choose_kernel<kSelWarps>, int(sizeof(C::Smem)), done);
+        cfg.gridDim = dim3(int(T * cache->Hkv));
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = sizeof(C::Smem);
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, jfa_cache_choose_kernel<kSelWarps>, z);
+    }
+    return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 jfa_status jfa_cache_fwd_blocks(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
