@@ -480,8 +480,8 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
  *   most 6 in magnitude (0 where the scale is 0), both to nearest, ties to the even code, as if
  *   in exact arithmetic.
  * Attention: scale * code is exact in the products' types.  jfa_cache_fwd's text on bf16 caches
- *   holds, with each weight of the softmax rounded to fp16 for its product where a sequence has
- *   at most 16 rows (new tokens x grouped heads), to bf16 elsewhere.  scale * k_factor must lie in [1e-37, 1e37].
+ *   holds, with each weight of the softmax rounded to fp16 for its product: off by 2^-11 of itself, or
+ *   by 2^-31 of the row's largest where that is more.  scale * k_factor must lie in [1e-37, 1e37].
  * Errors: those of jfa_cache_create.
  */
 jfa_status jfa_cache_create_quantized(int32_t Hkv, int32_t D, int32_t page_size, int64_t n_pages, void* K, void* V,

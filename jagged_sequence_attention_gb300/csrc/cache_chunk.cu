@@ -774,7 +774,8 @@ __global__ void __launch_bounds__((ChkCfg<D, Q4>::kThreads), 1)
             float m = -INFINITY, l = 0.f;
             if (Q4 && g.r.n > 0) {
                 if (!wwait(B_Q_FULL, item_it & 1)) { ok = false; break; }
-                xs = p.scale_log2 * reinterpret_cast<const float*>(smem + C::kOffDown)[(sp.split ? 0 : x) * C::BM + t];
+                // (not 0, which would not leave a masked score at -inf; scores are below 2^33)
+                xs = fmaxf(p.scale_log2 * reinterpret_cast<const float*>(smem + C::kOffDown)[(sp.split ? 0 : x) * C::BM + t], 1e-37f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_Q_EMPTY));
                 ++item_it;

@@ -1,10 +1,9 @@
 """Helpers for the tests of 4-bit caches: the format in plain 64-bit torch, and batches over a
 cache in it, whose attention the CPU oracle computes on the values that the cache stands for.
 
-Tolerances on top of cache_cases': a weight is rounded to fp16 where a sequence has at most 16 packed
-rows, to bf16 elsewhere (2^-8).  In fp16 that is 2^-11 of it, and of a weight below fp16's normal numbers
-half of their step of 2^-24: weights are held times 2^6 relative to a maximum that is at most the
-row's true one, so its largest is 2^6 or more, and a small one is off by 2^-25 / 2^6 = 2^-31 of that.
+Tolerances on top of cache_cases': a weight is rounded to fp16: off by 2^-11 of it, and a weight below
+fp16's normal numbers by half of their step of 2^-24: weights are held times 2^6 relative to a maximum that is
+at most the row's true one, so its largest is 2^6 or more, and a small one is off by 2^-25 / 2^6 = 2^-31 of that.
 A sum over n keys is off by n 2^-31 max|v| more (tiny(), which shows only where the keys of large
 weights hold zeros).  Queries are taken to fp16 with 2^-39 of the row's largest element
 lost at most.  Keys and values are exact in the products.
@@ -88,8 +87,7 @@ class QCase(Case):
     def check(self, O, lse, ref=None, slack=SLACK):
         ro, rl, A = ref or self.reference()
         o, l = np64(O)[:self.T], np64(lse)[:self.T]
-        few = np.repeat(self.q * (self.H // self.Hkv) <= 16, self.q)[:, None, None]
-        tol = slack * A + np.where(few, 2.0 ** -11, 2.0 ** -8) * A + np.where(few, self.tiny(), 0.0) + 1e-30
+        tol = slack * A + 2.0 ** -11 * A + self.tiny() + 1e-30
         if O.dtype == BF:
             tol = tol + 2.0 ** -8 * np.abs(ro)
         assert np.all(np.isfinite(o)), "non-finite output"

@@ -240,6 +240,16 @@ def test_queries_of_any_size(jfa):
         c.check(*c.run(jfa))
 
 
+@pytest.mark.parametrize("lens", [SINGLE, CHUNKS, EMPTY_ROWS], ids=["single", "chunks", "empty"])
+def test_masks_hold_where_scores_vanish(jfa, lens):
+    # queries and a scale whose product is below fp32's numbers: all scores are 0, masked ones still -inf
+    c = QCase(*lens, H=4, Hkv=2, D=64, page=16, seed=12)
+    c.Q = torch.full_like(c.Q, 1e-37)
+    O, lse = c.run(jfa, scale=1e-36)
+    c.Q = torch.zeros_like(c.Q)
+    c.check(O, lse)
+
+
 def test_large_scores(jfa):
     c = QCase(*CHUNKS, H=4, Hkv=2, D=128, page=16, seed=9, std=6.0)
     O, lse = c.run(jfa)
