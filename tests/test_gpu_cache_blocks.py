@@ -387,6 +387,76 @@ def test_served_steps(jfa, bits):
     assert jfa.jfa_cache_device_status(cache) == jfa.JFA_OK
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+def test_steps_at_once_on_two_streams(jfa, bits):
+    """Selections and attention over them, each stream with workspaces of its own, and then two
+    graphs that share one, replayed in turn."""
+    cases = [make(bits, *lens, H=8, Hkv=2, D=128, page=16, seed=21) for lens in (SETS, ([1, 40, 2], [5000, 700, 1900]))]
+    runs = []
+    for c in cases:
+        cache, bounds = cache_of(jfa, c), torch.nan_to_num(bounds_for(c, 21))
+        lists, O, lse = torch.empty(c.T, 2, 7, dtype=torch.int32, device="cuda"), torch.empty_like(c.Q), torch.empty(c.T, 8, device="cuda")
+        ws, sel = jfa.jfa_cache_workspace(cache, 8), jfa.jfa_cache_select_workspace(cache, 200, 1024)
+
+        def run(c=c, cache=cache, bounds=bounds, lists=lists, O=O, lse=lse, ws=ws, sel=sel, **kw):
+            jfa.jfa_cache_select(cache, bounds, c.Q, c.q_off, c.kv_lens, c.table, 7, blocks=lists, workspace=sel, **kw)
+            jfa.jfa_cache_fwd_blocks(cache, c.Q, c.q_off, c.kv_lens, c.table, lists, O=O, lse=lse, workspace=ws, **kw)
+            return lists, O, lse
+
+        assert np.array_equal(run()[0].cpu().numpy(), expected_blocks(c, bounds, 7, 1, 1))
+        runs.append((run, [x.clone() for x in run()], ws, sel))
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, (run, *_) in zip(streams, runs):
+            run(stream=s)
+    torch.cuda.synchronize()
+    for run, want, *_ in runs:
+        assert all(torch.equal(x, y) for x, y in zip(run(), want))
+    ws, sel = runs[0][2:]
+    graphs = []
+    for run, *_ in runs:
+        run(ws=ws, sel=sel)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            out = run(ws=ws, sel=sel)
+        for x in out:
+            x.zero_()
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for run, want, *_ in runs:
+        got = [x.clone() for x in run.__defaults__[3:6]]
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_the_query_bound_changes_no_selection(jfa):
+    for lens in (SINGLE, SETS, ([64, 200, 1], [3000, 4100, 2000])):
+        c = Case(*lens, H=8, Hkv=2, D=128, page=16, seed=22)
+        bounds = bounds_for(c, 22)
+        want = expected_blocks(c, bounds, 12, 1, 1)
+        for n in (None, 1, 4, 5, 10 ** 6):
+            assert np.array_equal(choose(jfa, c, bounds, 12, max_q_len=n), want)
+
+
+def test_no_tokens_and_no_pages(jfa):
+    c = Case([0, 0], [40, 0], H=4, Hkv=2, D=64, page=16, seed=23)
+    cache, bounds = cache_of(jfa, c), torch.zeros(c.n_pages, 2, 2, 64, dtype=BF, device="cuda")
+    a = (c.q_off, c.kv_lens, c.table)
+    jfa.jfa_cache_summarize(cache, bounds, 0, *a)
+    lists = jfa.jfa_cache_select(cache, bounds, c.Q[:0], *a, 3)
+    O, lse = jfa.jfa_cache_fwd_blocks(cache, c.Q[:0], *a, lists)
+    assert lists.shape == (0, 2, 3) and O.shape == (0, 4, 64) and lse.shape == (0, 4)
+    # rows with no position: no block is theirs
+    c = Case([3, 2], [1, 0], H=4, Hkv=2, D=64, page=16, seed=23)
+    got = choose(jfa, c, torch.zeros(c.n_pages, 2, 2, 64, dtype=BF, device="cuda"), 2)
+    assert np.array_equal(got, np.repeat([[[-1, -1]], [[-1, -1]], [[0, -1]], [[-1, -1]], [[-1, -1]]], 2, axis=1))
+    torch.cuda.synchronize()
+    assert jfa.jfa_cache_device_status(cache) == jfa.JFA_OK
+
+
 def test_refusals(jfa):
     def status(fn, *a, **k):
         try:
