@@ -7,9 +7,10 @@
 // with lo and hi the block's least and largest elements, so the group costs what one head does.
 //
 // The selection is that of exact arithmetic.  Scores are taken in fp32: u and w are sums of g values of
-// one sign, and a dot product adds n products one after the other (a lane's D / 4, or the D even or
-// odd ones of a tile) and joins the sums in up to 3 steps, so a score is off by less than
-//   slack = (g + n + 4) 2^-24 max|lo, hi| sum_d (u_d - w_d).
+// one sign, and a dot product adds n products one after the other (a lane's D / 4, joined in 3 steps; of
+// a tile, see there), so a score is off by less than
+//   slack = (g + n + 4) 2^-24 max|lo, hi| sum_d (u_d - w_d),
+// and 2^-116 times as much as these for what falls below fp32's (or bf16's) numbers.
 // With t the k-th largest fp32 score, the exact k-th largest lies within slack of t: a block above
 // t + 2 slack is in, one below t - 2 slack is out, and those between, mostly one, are scored
 // again in 64 bits and taken in order, of equal ones the lower index.
@@ -29,7 +30,7 @@ cudaError_t launch_cache_decode4(int D, const CUtensorMap& mk, const CUtensorMap
 namespace {
 
 constexpr int kChunk = 64;          // blocks that a CTA scores
-constexpr int kSumThreads = 512, kScoreThreads = 256, kTileThreads = 128;
+constexpr int kSumThreads = 512, kScoreThreads = 256, kTileThreads = 256;
 constexpr int kTileTokens = 32;     // tokens that a CTA scores, where a sequence has many
 constexpr int kSelWarps = 32;       // warps that choose for one item, where more than 512 blocks may compete
 
@@ -45,7 +46,7 @@ struct BlockParams {
     float* scores;                  // [T, Hkv, max_pages]
     float* slack;                   // [T, Hkv, chunks]
     int chunks;
-    int tile;                       // summarize: tokens that a CTA looks over
+    int tile;                       // summarize: tokens that a CTA looks over; tiles' scores: chunks of a CTA
 };
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
@@ -178,9 +179,11 @@ __device__ __forceinline__ void query_sums(const BlockParams& z, int t, int hk, 
 }
 
 // What an fp32 score may be off by: m the largest magnitude among the bounds, norm the sums' norm
-// (which is itself a sum of 2 D values, hence the 1.01).
+// (which is itself a sum of 2 D values, hence the 1.01).  An operand below 2^-126 may count as 0, and a
+// product or sum may lose 2^-126: 2 D and a few times that is below 2^-116.
 __device__ __forceinline__ float slack_of(const BlockParams& z, int steps, float m, float norm) {
-    return float(z.g + steps) * (1.01f * 0x1p-24f) * m * norm;
+    if (!(m > 0.f && norm > 0.f)) return 0.f;  // all scores are 0
+    return fmaf(float(z.g + steps) * (1.01f * 0x1p-24f) * m, norm, 0x1p-116f * (m + norm) + 0x1p-116f);
 }
 
 // Page of block k of sequence b, or -1.
@@ -259,26 +262,45 @@ __global__ void __launch_bounds__(kScoreThreads) jfa_cache_score_kernel(const Bl
     }
 }
 
-// Scores of kChunk blocks for kTileTokens tokens and one key head: a matrix product in fp32 on the CUDA
-// cores, bounds and sums in shared memory, four tokens by four blocks a thread, even and odd
-// products in the halves of paired sums.  (A tensor core would need the sums in three parts.)  The
-// tile's sequences come one after the other: it is taken where they are long.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const __nv_bfloat16* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Scores for kTileTokens tokens and one key head, kChunk blocks at a time: a matrix product on the tensor
+// cores, the sums as three bf16 parts each.  16 of the 2 D products are added at a time, the small
+// parts' first, by instructions that add to no less than fp32's precision, and the 16s' sums in
+// fp32: in all within 35 + D / 8 + 1 steps of 2^-24 of the products' magnitudes.  A warp has 16 tokens by 16 blocks.
+// Bound by the chain page table -> bounds -> products of each chunk, the next one's loads under way
+// meanwhile; chunks are dealt to as many CTAs as there is room for.  The product on the CUDA cores in fp32,
+// a CTA a chunk with the sums anew, took 41 us for four prompts of 100-500 tokens over up to 20k
+// keys, of @ in all.  The tile's sequences come one after the other: it is taken where they are long.
 template <int D>
-__global__ void __launch_bounds__(kTileThreads) jfa_cache_score_tile_kernel(const BlockParams z) {
+__global__ void __launch_bounds__(kTileThreads, 2) jfa_cache_score_tile_kernel(const BlockParams z) {
     const CacheAppendParams& p = z.a;
-    constexpr int kRow = 2 * D, kPitch = kRow + 4, kBPitch = kRow + 8;  // floats; bf16 (rows of both end 16 bytes apart in the banks)
+    constexpr int kRow = 2 * D, kPitch = kRow + 8;  // (rows end 16 bytes apart in the banks)
+    constexpr int kVecs = kRow / 8, kLoads = kChunk * kVecs / kTileThreads;
     extern __shared__ __align__(16) uint8_t tile_smem[];
-    float* sums = reinterpret_cast<float*>(tile_smem);                  // [kTileTokens][kPitch]
-    __nv_bfloat16* bounds = reinterpret_cast<__nv_bfloat16*>(sums + kTileTokens * kPitch);  // [kChunk][kBPitch]
+    __nv_bfloat16* sums = reinterpret_cast<__nv_bfloat16*>(tile_smem);  // [3][kTileTokens][kPitch]
+    __nv_bfloat16* bounds = sums + 3 * kTileTokens * kPitch;            // [kChunk][kPitch]
     __shared__ float norms[kTileTokens];
-    __shared__ uint32_t top;
-    const int lane = threadIdx.x & 31, hk = blockIdx.z, t0 = blockIdx.x * kTileTokens, t1 = min(t0 + kTileTokens, p.T), k0 = blockIdx.y * kChunk;
-    // tokens 4 tg .. and blocks bg + 16 i of a thread: a warp has two token groups
-    const int tg = threadIdx.x >> 4, bg = threadIdx.x & 15;
+    __shared__ uint32_t top[2];  // this chunk's largest magnitude, and the next one's
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hk = blockIdx.z;
+    const int t0 = blockIdx.x * kTileTokens, t1 = min(t0 + kTileTokens, p.T);
+    const int m0 = 16 * (warp & 1), n0 = 16 * (warp >> 1);  // this warp's tokens and blocks
     launch_dependents();  // (the choice waits for this kernel to end)
     int b = find_sequence(p.q_off, p.B, t0, lane);
     if (b < 0) b = 0;
     bool have_sums = false;
+    uint32_t odd = 0u;
     for (; b < p.B; ++b) {
         const int q0 = p.q_off[b], q1 = p.q_off[b + 1], kv = p.kv_lens[b];
         if (q0 >= t1) break;
@@ -288,104 +310,132 @@ __global__ void __launch_bounds__(kTileThreads) jfa_cache_score_tile_kernel(cons
             if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
             continue;
         }
-        const int last = kv - q1 + tb - 1;                              // the last token's position
-        const int most = last >= 0 ? (last >> p.page_log2) + 1 : 0;
-        if (most <= z.n_blocks || k0 >= most - z.n_last) continue;
+        const int last = kv - q1 + tb - 1;  // the last token's position
+        const int most = last >= 0 ? (last >> p.page_log2) + 1 : 0, end = most - z.n_last;
+        if (most <= z.n_blocks) continue;
+        int ch = max(int(blockIdx.y) * z.tile, z.n_first / kChunk);
+        const int ch_end = min((int(blockIdx.y) + 1) * z.tile, (end + kChunk - 1) / kChunk);
+        if (ch >= ch_end) continue;
+        uint4 x[kLoads];
+        auto load = [&](int chunk) {
+            int page[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int k = chunk * kChunk + (threadIdx.x + kTileThreads * i) / kVecs;
+                page[i] = -1;
+                if (k >= z.n_first && k < end) {
+                    page[i] = block_page(p, b, k);
+                    if (page[i] < 0) atomicOr(p.status, kStatusBounds);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                x[i] = page[i] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                   : *reinterpret_cast<const uint4*>(z.bounds + (size_t(page[i]) * p.Hkv + hk) * kRow + 8 * (threadIdx.x % kVecs));
+        };
+        load(ch);
         if (!have_sums) {
             have_sums = true;
+            if (threadIdx.x < 2) top[threadIdx.x] = 0u;
             // eight columns of a token a thread, the lanes of a token side by side
-            constexpr int kVecs = D / 8;
-            for (int e = threadIdx.x; e < kTileTokens * kVecs; e += kTileThreads) {
-                const int i = e / kVecs, v = e % kVecs;
-                float u[8], w[8], n = 0.f;
+            for (int e = threadIdx.x; e < kTileTokens * D / 8; e += kTileThreads) {
+                const int i = e / (D / 8), v = e % (D / 8);
+                float u[2][8], n = 0.f;  // w, u
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = w[j] = 0.f;
+                for (int j = 0; j < 8; ++j) u[0][j] = u[1][j] = 0.f;
                 if (t0 + i < t1) {
                     const __nv_bfloat16* q = z.Q + (t0 + i) * z.q_stride + hk * z.g * D + 8 * v;
 #pragma unroll 4
                     for (int h = 0; h < z.g; ++h) {
-                        Vec<__nv_bfloat16> x;
-                        x.load(q + h * D);
+                        Vec<__nv_bfloat16> q8;
+                        q8.load(q + h * D);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            u[j] += fmaxf(x.v[j], 0.f);
-                            w[j] += fminf(x.v[j], 0.f);
+                            u[0][j] += fminf(q8.v[j], 0.f);
+                            u[1][j] += fmaxf(q8.v[j], 0.f);
                         }
                     }
                 }
-                float4* to = reinterpret_cast<float4*>(sums + i * kPitch + 8 * v);
-                to[0] = make_float4(w[0], w[1], w[2], w[3]);
-                to[1] = make_float4(w[4], w[5], w[6], w[7]);
-                to[D / 4] = make_float4(u[0], u[1], u[2], u[3]);
-                to[D / 4 + 1] = make_float4(u[4], u[5], u[6], u[7]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n += u[j] - w[j];
+                for (int j = 0; j < 8; ++j) n += u[1][j] - u[0][j];
 #pragma unroll
-                for (int d = 1; d < kVecs; d <<= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+                for (int d = 1; d < D / 8; d <<= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
                 if (v == 0) norms[i] = n;
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int side = 0; side < 2; ++side) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float &a = u[side][2 * j], &c = u[side][2 * j + 1];
+                            r[j] = pack_bf16x2(a, c);
+                            a -= __uint_as_float(r[j] << 16);
+                            c -= __uint_as_float(r[j] & 0xffff0000u);
+                        }
+                        *reinterpret_cast<uint4*>(sums + (part * kTileTokens + i) * kPitch + side * D + 8 * v) = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
             }
         }
-        if (threadIdx.x == 0) top = 0u;
-        __syncthreads();
-        uint32_t m = 0u;
-        for (int e = threadIdx.x; e < kChunk * (kRow / 8); e += kTileThreads) {
-            const int i = e / (kRow / 8), v = e % (kRow / 8), k = k0 + i;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (k >= z.n_first && k < most - z.n_last) {
-                const int page = block_page(p, b, k);
-                if (page >= 0)
-                    x = *reinterpret_cast<const uint4*>(z.bounds + (size_t(page) * p.Hkv + hk) * kRow + 8 * v);
-                else
-                    atomicOr(p.status, kStatusBounds);
+        for (; ch < ch_end; ++ch, odd ^= 1u) {
+            __syncthreads();  // (the last chunk's products are done)
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                m = max_bf16x2(max_bf16x2(m, x[i].x & 0x7fff7fffu), x[i].y & 0x7fff7fffu);
+                m = max_bf16x2(max_bf16x2(m, x[i].z & 0x7fff7fffu), x[i].w & 0x7fff7fffu);
+                const int e = threadIdx.x + kTileThreads * i;
+                *reinterpret_cast<uint4*>(bounds + (e / kVecs) * kPitch + 8 * (e % kVecs)) = x[i];
             }
-            m = max_bf16x2(max_bf16x2(m, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
-            m = max_bf16x2(max_bf16x2(m, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
-            *reinterpret_cast<uint4*>(bounds + i * kBPitch + 8 * v) = x;
-        }
-        m = max(m & 0xffffu, m >> 16);  // (magnitudes compare like whole numbers)
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(&top, m);
-        __syncthreads();
-        float2 acc[4][4];
+            m = max(m & 0xffffu, m >> 16);  // (magnitudes compare like whole numbers)
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0) atomicMax(&top[odd], m);
+            __syncthreads();
+            if (threadIdx.x == 0) top[odd ^ 1u] = 0u;
+            if (ch + 1 < ch_end) load(ch + 1);
+            float acc[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+            // ldmatrix sources: rows of this warp's tokens and blocks, and 16-byte pieces
+            const __nv_bfloat16* pa = sums + (m0 + (lane & 15)) * kPitch + 8 * (lane >> 4);
+            const __nv_bfloat16* pb = bounds + (n0 + (lane & 7) + 8 * (lane >> 4)) * kPitch + 8 * ((lane >> 3) & 1);
 #pragma unroll 4
-        for (int d = 0; d < kRow; d += 4) {
-            float4 u[4];
-            uint2 x[4];
+            for (int d = 0; d < kRow; d += 16) {
+                uint32_t bb[4];
+                ldmatrix4(bb, pb + d);
+                float c[2][4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(sums + (4 * tg + i) * kPitch + d);
+                for (int part = 2; part >= 0; --part) {
+                    uint32_t a[4];
+                    ldmatrix4(a, pa + part * kTileTokens * kPitch + d);
+                    mma_bf16(c[0], a, bb[0], bb[1]);
+                    mma_bf16(c[1], a, bb[2], bb[3]);
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint2*>(bounds + (bg + 16 * j) * kBPitch + d);
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 lo = make_float2(__uint_as_float(x[j].x << 16), __uint_as_float(x[j].x & 0xffff0000u));
-                const float2 hi = make_float2(__uint_as_float(x[j].y << 16), __uint_as_float(x[j].y & 0xffff0000u));
+                    for (int i = 0; i < 4; ++i) acc[j][i] += c[j][i];
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[i][j] = fma2(make_float2(u[i].x, u[i].y), lo, acc[i][j]);
-                    acc[i][j] = fma2(make_float2(u[i].z, u[i].w), hi, acc[i][j]);
+            for (int r = 0; r < 2; ++r) {
+                const int t = t0 + m0 + (lane >> 2) + 8 * r, pos = kv - q1 + t, n = (pos >> p.page_log2) + 1;
+                if (t < ta || t >= tb || pos < 0 || n <= z.n_blocks) continue;
+                float* out = z.scores + (size_t(t) * p.Hkv + hk) * size_t(p.max_pages);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = ch * kChunk + n0 + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+                    if (k >= z.n_first && k < n - z.n_last) out[k] = acc[j >> 1][2 * r + (j & 1)];
                 }
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 4 * tg + i, pos = kv - q1 + t;
-            if (t < ta || t >= tb || pos < 0) continue;
-            const int n = (pos >> p.page_log2) + 1;
-            if (n <= z.n_blocks) continue;
-            float* out = z.scores + (size_t(t) * p.Hkv + hk) * size_t(p.max_pages);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + bg + 16 * j;
-                if (k >= z.n_first && k < n - z.n_last) out[k] = acc[i][j].x + acc[i][j].y;
+            if (threadIdx.x < kTileTokens) {
+                const int t = t0 + int(threadIdx.x), pos = kv - q1 + t;
+                if (t >= ta && t < tb && pos >= 0 && (pos >> p.page_log2) + 1 > z.n_blocks)
+                    z.slack[(size_t(t) * p.Hkv + hk) * size_t(z.chunks) + ch] =
+                        slack_of(z, 35 + D / 8 + 1, __uint_as_float(top[odd] << 16), norms[threadIdx.x]);
             }
-            if (bg == 0)
-                z.slack[(size_t(t) * p.Hkv + hk) * size_t(z.chunks) + blockIdx.y] = slack_of(z, D + 2, __uint_as_float(top << 16), norms[4 * tg + i]);
         }
-        __syncthreads();
     }
 }
 
@@ -947,8 +997,11 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
         const bool tiles = (max_q_len == 0 || max_q_len > 4) && T >= 8 * int64_t(B);
         cudaError_t e = cudaSuccess;
         if (tiles) {
-            const dim3 grid((z.a.T + kTileTokens - 1) / kTileTokens, z.chunks, cache->Hkv);
-            const int D = cache->D, bytes = kTileTokens * (2 * D + 4) * 4 + kChunk * (2 * D + 8) * 2;
+            const int D = cache->D, bytes = (3 * kTileTokens + kChunk) * (2 * D + 8) * 2, tiles_of_tokens = (z.a.T + kTileTokens - 1) / kTileTokens;
+            // as many CTAs as run at a time, where the chunks allow
+            const int64_t ctas = int64_t(tiles_of_tokens) * cache->Hkv, parts = std::max<int64_t>(1, std::min<int64_t>(z.chunks, (2 * cache->num_sms + ctas - 1) / ctas));
+            z.tile = int((z.chunks + parts - 1) / parts);
+            const dim3 grid(tiles_of_tokens, (z.chunks + z.tile - 1) / z.tile, cache->Hkv);
             static std::atomic<uint64_t> done[2];
             e = D == 128 ? allow_smem(jfa_cache_score_tile_kernel<128>, bytes, done[0]) : allow_smem(jfa_cache_score_tile_kernel<64>, bytes, done[1]);
             if (e == cudaSuccess) {
