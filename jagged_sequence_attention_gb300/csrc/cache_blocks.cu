@@ -281,8 +281,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // fp32: in all within 35 + D / 8 + 1 steps of 2^-24 of the products' magnitudes.  A warp has 16 tokens by 16 blocks.
 // Bound by the chain page table -> bounds -> products of each chunk, the next one's loads under way
 // meanwhile; chunks are dealt to as many CTAs as there is room for.  The product on the CUDA cores in fp32,
-// a CTA a chunk with the sums anew, took 41 us for four prompts of 100-500 tokens over up to 20k
-// keys, of @ in all.  The tile's sequences come one after the other: it is taken where they are long.
+// a CTA a chunk with the sums anew, took 41 us of 82 for four prompts of 100-500 tokens over up to 20k
+// keys; this one about 18 of 58.  The tile's sequences come one after the other: it is taken where they are long.
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 2) jfa_cache_score_tile_kernel(const BlockParams z) {
     const CacheAppendParams& p = z.a;
@@ -473,7 +473,7 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
 template <int WARPS>
 struct Choosers {
     static constexpr int kThreads = 32 * WARPS, kItems = WARPS == 1 ? 4 : 1;
-    static constexpr int kHeld = WARPS == 1 ? 512 : 8192, kCands = WARPS == 1 ? 512 : 1024;
+    static constexpr int kHeld = WARPS == 1 ? 512 : 8192, kCands = WARPS == 1 ? 128 : 1024;
     struct Smem {
         float held[kHeld];
         unsigned long long keys[kCands];
@@ -546,46 +546,44 @@ __device__ __noinline__ void settle_exactly(Choosers<WARPS>& g, const BlockParam
         g.sync();
         return;
     }
-    // Very many nearly equal scores (a CTA's): the need-th largest exact score, eight bits at a time, each
+    // Very many nearly equal scores: the need-th largest exact score, eight bits at a time, each
     // pass scoring all candidates again; then equal ones by their index.
-    if constexpr (WARPS > 1) {
-        if (g.thread == 0) {
-            g.m->prefix = 0ull;
-            g.m->left = need;
-        }
-        auto key_of = [&](int i) { return ordered64(exact_score(z, b, hk, first + i, g.m->sums, g.lane)); };
-        for (int shift = 56; shift >= 0; shift -= 8) {
-            if (g.thread < 256) g.m->hist[g.thread] = 0;
-            __syncthreads();
-            const unsigned long long mask = shift == 56 ? 0ull : ~0ull << (shift + 8), want = g.m->prefix;
-            for (int i = g.warp; i < n; i += WARPS) {
-                if (!is_cand(i)) continue;
-                const unsigned long long key = key_of(i);
-                if (g.lane == 0 && (key & mask) == want) atomicAdd(&g.m->hist[int((key >> shift) & 255u)], 1);
-            }
-            __syncthreads();
-            if (g.thread == 0) {
-                int higher = 0, d = 255;
-                while (d > 0 && higher + g.m->hist[d] < g.m->left) higher += g.m->hist[d--];
-                g.m->left -= higher;
-                g.m->prefix |= (unsigned long long)(d) << shift;
-            }
-            __syncthreads();
-        }
-        const unsigned long long border = g.m->prefix;
-        int equal = g.m->left;  // of those at the border, the first so many
-        for (int i0 = 0; i0 < n; i0 += WARPS) {
-            const int i = i0 + g.warp;
-            const bool is = is_cand(i);
-            const unsigned long long key = is ? key_of(i) : 0ull;
-            int all;
-            // (one vote a warp: thread 0 of each)
-            const int at = g.before(g.lane == 0 && is && key == border, all);
-            if (g.lane == 0 && is) sc[i] = key > border || (key == border && at < equal) ? INFINITY : -INFINITY;
-            equal -= all;
-        }
-        __syncthreads();
+    if (g.thread == 0) {
+        g.m->prefix = 0ull;
+        g.m->left = need;
     }
+    auto key_of = [&](int i) { return ordered64(exact_score(z, b, hk, first + i, g.m->sums, g.lane)); };
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        for (int i = g.thread; i < 256; i += C::kThreads) g.m->hist[i] = 0;
+        g.sync();
+        const unsigned long long mask = shift == 56 ? 0ull : ~0ull << (shift + 8), want = g.m->prefix;
+        for (int i = g.warp; i < n; i += WARPS) {
+            if (!is_cand(i)) continue;
+            const unsigned long long key = key_of(i);
+            if (g.lane == 0 && (key & mask) == want) atomicAdd(&g.m->hist[int((key >> shift) & 255u)], 1);
+        }
+        g.sync();
+        if (g.thread == 0) {
+            int higher = 0, d = 255;
+            while (d > 0 && higher + g.m->hist[d] < g.m->left) higher += g.m->hist[d--];
+            g.m->left -= higher;
+            g.m->prefix |= (unsigned long long)(d) << shift;
+        }
+        g.sync();
+    }
+    const unsigned long long border = g.m->prefix;
+    int equal = g.m->left;  // of those at the border, the first so many
+    for (int i0 = 0; i0 < n; i0 += WARPS) {
+        const int i = i0 + g.warp;
+        const bool is = is_cand(i);
+        const unsigned long long key = is ? key_of(i) : 0ull;
+        int all;
+        // (one vote a warp: thread 0 of each)
+        const int at = g.before(g.lane == 0 && is && key == border, all);
+        if (g.lane == 0 && is) sc[i] = key > border || (key == border && at < equal) ? INFINITY : -INFINITY;
+        equal -= all;
+    }
+    g.sync();
 }
 
 // a + b = s + e exactly (Knuth).
@@ -733,7 +731,7 @@ __device__ __noinline__ float search(Choosers<WARPS>& g, const float* sc, const 
 
 // The chosen blocks of one token and key head, from its scores.
 template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems) jfa_cache_choose_kernel(const BlockParams z) {
+__global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems, WARPS == 1 ? 5 : 1) jfa_cache_choose_kernel(const BlockParams z) {
     using C = Choosers<WARPS>;
     const CacheAppendParams& p = z.a;
     extern __shared__ __align__(16) uint8_t choose_smem[];
@@ -998,8 +996,9 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
         cudaError_t e = cudaSuccess;
         if (tiles) {
             const int D = cache->D, bytes = (3 * kTileTokens + kChunk) * (2 * D + 8) * 2, tiles_of_tokens = (z.a.T + kTileTokens - 1) / kTileTokens;
-            // as many CTAs as run at a time, where the chunks allow
-            const int64_t ctas = int64_t(tiles_of_tokens) * cache->Hkv, parts = std::max<int64_t>(1, std::min<int64_t>(z.chunks, (2 * cache->num_sms + ctas - 1) / ctas));
+            // four times as many CTAs as run at a time, where the chunks allow: 58 us for the prompts of the kernel's
+            // comment, against 61 for twice as many, 63 for as many (with a few of them in a second wave)
+            const int64_t ctas = int64_t(tiles_of_tokens) * cache->Hkv, parts = std::max<int64_t>(1, std::min<int64_t>(z.chunks, (8 * cache->num_sms + ctas - 1) / ctas));
             z.tile = int((z.chunks + parts - 1) / parts);
             const dim3 grid(tiles_of_tokens, (z.chunks + z.tile - 1) / z.tile, cache->Hkv);
             static std::atomic<uint64_t> done[2];
