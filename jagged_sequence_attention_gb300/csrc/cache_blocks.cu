@@ -942,8 +942,10 @@ jfa_status jfa_cache_summarize(jfa_cache cache, int32_t B, int64_t T, const int3
     z.k_scales = cache->k_scales;
     for (int i = 0; i < 2; ++i) z.kss[i] = cache->kss[i];
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // a CTA for each token, or where there are many for a page's worth of them
-    z.tile = T > 2048 || T >= 8 * int64_t(B) ? 1 << cache->page_log2 : 1;
+    // A CTA for as many tokens as a sequence has on average, at most a page's: about a page each.  (A page's
+    // worth always: 16 x 8 tokens on pages of 32 9.0 us instead of 3.5, 512 single ones 61 instead of 7.4; a CTA
+    // for each token: 16 x 64 tokens 5.9 instead of 3.6, 512 of one sequence 4.3 instead of 3.5.)
+    for (z.tile = 1; z.tile < 1 << cache->page_log2 && 2 * int64_t(z.tile) * B <= T;) z.tile *= 2;
     const int grid = int((T + z.tile - 1) / z.tile);
     if (cache->ops)
         jfa_cache_summarize_kernel<true><<<grid, kSumThreads, 0, st>>>(z);
@@ -991,8 +993,10 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
     z.slack = z.scores + size_t(T) * size_t(cache->Hkv) * size_t(max_pages);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (max_pages > n_blocks) {
-        // many tokens a sequence (as far as the host knows): 32 of them share the bounds' reads
-        const bool tiles = (max_q_len == 0 || max_q_len > 4) && T >= 8 * int64_t(B);
+        // Many tokens a sequence (as far as the host knows): 32 of them share the bounds' reads.  On 8 key
+        // heads of 128 over 250 blocks, token by token against in tiles: 4 x 8 tokens 18.6 and 28.7 us, 16 x 8
+        // 32.4 and 30.8, 64 x 8 (125 blocks) 55.5 and 39.1, 1 x 16 15.4 and 17.6, 16 x 16 49.9 and 25.7, 1 x 512 87.8 and 34.3.
+        const bool tiles = (max_q_len == 0 || max_q_len > 4) && T >= 8 * int64_t(B) && T >= 128;
         cudaError_t e = cudaSuccess;
         if (tiles) {
             const int D = cache->D, bytes = (3 * kTileTokens + kChunk) * (2 * D + 8) * 2, tiles_of_tokens = (z.a.T + kTileTokens - 1) / kTileTokens;
@@ -1027,7 +1031,10 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
     cfg.attrs = &attr;
     cfg.numAttrs = max_pages > n_blocks ? 1 : 0;
     cudaError_t e;
-    if (max_pages <= Choosers<1>::kHeld) {
+    // A warp an item where that holds all scores that there can be and there are more items than SMs.  (With
+    // a CTA an item, 8 heads, 250 blocks: 8 tokens 9.5 us instead of 14.8, 16 13.6 instead of 15.4, 32 23 instead of
+    // 18.6, 64 36 instead of 25, 512 203 instead of 41.)
+    if (max_pages <= Choosers<1>::kHeld && T * cache->Hkv > cache->num_sms) {
         using C = Choosers<1>;
         cfg.gridDim = dim3(int((T * cache->Hkv + C::kItems - 1) / C::kItems));
         cfg.blockDim = dim3(C::kThreads * C::kItems);

@@ -6,15 +6,22 @@
 // tiles of 128 positions are gathered by TMA, one box per page and 128-byte column block; a box
 // of a short page lands at its rows of the tile, whose swizzle repeats every 8 rows (the
 // smallest page).
-// CTA = 19 warps, one CTA per SM; the CTAs draw their work from a counter (cache_common.cuh).
+// A cache held in 4 bits: codes and scales come through rings of their own, and warps 18-21 load and
+// unpack them to fp16 tiles in the layout that TMA would have written; queries are taken to fp16
+// with a power of two per row, and P is 2^6 times the weights in fp16 (as in
+// cache_decode4.cu).  Measured, the prompts below over 4 bits: 786 us, 1093 TFLOP/s, 0.56 of the burst
+// rate: the unpacking hides beside the products, but leaves the softmax warps 80 registers and
+// one chunk of scores at a time.  (Unpacking by one warp each for K and V 855 us, by four from
+// global memory one tile ahead 1478, the few-rows kernel for all 4099.)
+// CTA = 19 warps (22 over 4 bits), one CTA per SM; the CTAs draw their work from a counter (cache_common.cuh).
 // Two warps share each row (thread = row = TMEM lane): one takes score columns [0, 64) and O
 // columns [0, D/2), the other the rest; they exchange row maxima and sums through shared
 // memory.
 //   warps 0-3, 8-11    tile A, columns [0, 64) and [64, 128): softmax, rescaling, epilogue
 //   warps 4-7, 12-15   tile B
-//   warp 16            TMA loads: Q once per item, K and V boxes through rings
-//   warp 17            tcgen05.mma issuer and TMEM owner; clears V rows no query may see
-//   warp 18            draws pieces of work when the loads near the end of what was drawn, and
+//   warp 18            TMA loads: Q once per item, K and V boxes through rings
+//   warp 16            tcgen05.mma issuer and TMEM owner; clears V rows no query may see
+//   warp 17            draws pieces of work when the loads near the end of what was drawn, and
 //                      hands out their items
 // TMEM (512 columns): S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P
 // overwrites its own S columns as packed bf16 and is read from TMEM by O += P V.

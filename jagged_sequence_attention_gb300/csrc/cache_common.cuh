@@ -27,7 +27,7 @@ constexpr int kBlocksPerCta = 4;  // chunk kernel: blocks of the last part of th
 constexpr int kMergeCtas = 4;     // merge tasks of a cut item of it, 64 rows each
 constexpr int kMaxSms = 320;
 // Words of the workspace's zeroed part: pieces drawn and CTAs done (chunk kernel), arrivals of
-// split items (the other kernels, at most 3 CTAs an SM), flags of cut items (chunk kernel).
+// split items (the kernels that add up parts themselves, at most 3 CTAs an SM), flags of cut items (chunk kernel).
 constexpr int kCtrDrawn = 0, kCtrDone = 1, kCtrSplit = 64, kCtrCuts = kCtrSplit + 3 * kMaxSms,
               kCtrEnd = kCtrCuts + kMaxSms * kBlocksPerCta * kMergeCtas;
 static_assert(kCtrEnd * 4 <= JFA_CACHE_ZERO_BYTES, "counters fit the zeroed part");

@@ -5,9 +5,9 @@
 // none.  A CTA here takes a record's row: its four warps deal the parts among them, a lane takes four
 // (or two) columns, the loads of 64 parts are in flight at once, and the warps' sums are added
 // in order, so the result does not depend on timing.
-// Bound by latency: a record, its maxima and its parts, about 2.5 us.  The last CTA of an item used to add
-// its parts itself, which took 9 us for one history of 131k keys (57 parts for each of 8 heads: 43.5 -> @ us
-// in all) and 2 us for one of 1k.
+// Bound by latency: a record, its maxima and its parts, about 2.5 us.  With an item's last CTA adding its parts
+// itself, one 4-bit history of 131k keys (57 parts for each of 8 heads) took 43.5 us instead of 37.5, 64
+// histories 75 instead of 68.6, 128 listed blocks of 64 keys 14.5 instead of 10.6.
 #include "cache_common.cuh"
 
 namespace jfa {

@@ -12,7 +12,11 @@
 // at a middle is 2^-9 of it away or more.
 // A thread takes 8 elements, two threads a group, so that a warp's loads and stores lie side by
 // side; a rotated row's other halves are read again (from L1) instead of handed over.
-// Measured: @
+// Bound by its arithmetic beside the stream: 24 prompts of 1-2048 tokens (32 query and 8 key heads of 128, keys
+// and queries rotated) append in about 120 us, where their 612 MB take 92 at the copy rate, at 0.72 of the issue
+// slots; with their rows read back 152 us, 0.76 of the copy rate.  256 single tokens with
+// their reading take 7.6 us: two launches, and the chain offsets -> page -> slot in each.  (16 elements a thread,
+// and whole groups compared in 64 bits where one element needed it: 182 us, 27 us.)
 #include <cuda_bf16.h>
 
 #include <new>
