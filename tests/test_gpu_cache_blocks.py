@@ -298,6 +298,20 @@ def test_equal_scores_go_by_index(jfa, kinds):
     assert np.array_equal(choose(jfa, c, zero, 40), expected_blocks(c, zero, 40, 1, 1))
 
 
+@pytest.mark.parametrize("kinds", [1, 3])
+def test_equal_scores_of_many_tokens(jfa, kinds):
+    # (items of a warp each, more candidates than it keeps, and few)
+    c = Case([90, 2], [16 * 400, 16 * 350], H=4, Hkv=2, D=128, page=16, seed=kinds)
+    base = torch.nan_to_num(bounds_for(c, kinds))
+    bounds = base[torch.randint(0, kinds, (c.n_pages,), device="cuda")].contiguous()
+    for n in (5, 60, 200, 340):
+        for m in (None, 1):
+            assert np.array_equal(choose(jfa, c, bounds, n, max_q_len=m), expected_blocks(c, bounds, n, 1, 1))
+    some = torch.rand(c.n_pages, device="cuda") < 0.1
+    bounds[some] = base[some]
+    assert np.array_equal(choose(jfa, c, bounds, 60), expected_blocks(c, bounds, 60, 1, 1))
+
+
 def test_nearly_equal_scores(jfa):
     """Scores that fp32 sums cannot tell apart: large parts that cancel, and differences in the
     last bits."""
