@@ -219,7 +219,7 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
     p.bm = bf16 || p.g > 4 ? 16 : 4;
     if (cache->ops && most_rows <= 8) p.bm = 8;
     p.min_units = 1;
-    p.item_cost = !bf16 ? kSimtItemUnits : chunks ? kDecodeItemUnitsBeside : kDecodeItemUnits;
+    p.item_cost = !bf16 ? kSimtItemUnits : cache->ops ? kDecode4ItemUnits : chunks ? kDecodeItemUnitsBeside : kDecodeItemUnits;
     if (!fits(chunks ? int64_t(B) * (kDecodeRows / p.bm) : tiles(T * p.g, p.bm), 64)) return JFA_ERR_UNSUPPORTED;
     // (the two kernels may run at once, and the merge comes last)
     p.part += (bf16 ? cache_chunk_part_bytes(D, n) : cache_split_part_bytes(D, n)) / sizeof(float);

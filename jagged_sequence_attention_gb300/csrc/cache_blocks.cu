@@ -1085,7 +1085,7 @@ jfa_status jfa_cache_fwd_blocks(jfa_cache cache, int32_t B, int64_t T, const int
     p.n_list = n_blocks;
     p.bm = p.g;
     p.min_units = 1;
-    p.item_cost = kDecodeItemUnits;
+    p.item_cost = cache->ops ? kDecode4ItemUnits : kDecodeItemUnits;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = cache->ops ? launch_cache_decode4(cache->D, cache->mk, cache->mv, p, false, cache->num_sms, st)
                                      : launch_cache_decode_lists(cache->D, cache->mk, cache->mv, p, cache->num_sms, st);

@@ -113,7 +113,9 @@ constexpr int kDecodeRows = 16;  // one row tile of the decode kernel
 // of 128 keys: 1.8-2.6 us (48 sequences, nine of them prompts: 71 us with 2, 66.5 with 3, 70.5 with
 // 5) and 2.5 us (20 ragged sequences: 74.4 with 2, 75.6 with 3, 78.4 with 5); the simt kernel, in
 // its steps of 64 keys, the same 2 (64 fp32 single tokens: 109-114 us with 1 to 4, 118 with 6).
-constexpr int kDecodeItemUnits = 3, kDecodeItemUnitsBeside = 2, kSimtItemUnits = 2;
+// The 4-bit kernel, in its stages of 128 keys (1.7 us): 64 histories 68.6 us with 1, 67.4 with 2, 68.7 with 3, 73.5
+// with 6; 64 lists of blocks 36.4, 36.7, 38.7 and 38.8.
+constexpr int kDecodeItemUnits = 3, kDecodeItemUnitsBeside = 2, kSimtItemUnits = 2, kDecode4ItemUnits = 2;
 constexpr int kChunkItemUnits = 3;
 constexpr int kSplitItemUnits = 2;
 

@@ -93,7 +93,7 @@ def test_binding_refuses_what_it_would_misread(jfa):
     good = dict(Q=wide, **batch, blocks=lists, bias=None, scale=0.1, O=O, lse=lse, ws=ws, stream=0)
     refused(calls.fwd_blocks, good,
             (*batches, dict(Q=wide.double()), dict(Q=wide[0]), dict(blocks=lists[:6]), dict(blocks=lists.float()), dict(blocks=lists[..., ::2]),
-             dict(bias=torch.zeros(8, 31)), dict(bias=torch.zeros(7, 32)), dict(scale=None), dict(O=O[:, :4]), dict(O=O.transpose(0, 1)),
+             dict(bias=torch.zeros(8, 31, dtype=F32)), dict(bias=torch.zeros(7, 32, dtype=F32)), dict(scale=None), dict(O=O[:, :4]), dict(O=O.transpose(0, 1)),
              dict(lse=lse.double()), dict(lse=lse.view(-1)), dict(ws=None)))
     assert calls.fwd_blocks(cache.info, *dict(good, O=O.half()).values()) == jfa.JFA_ERR_UNSUPPORTED
 
@@ -103,7 +103,7 @@ def test_public_calls_have_the_binding_s_error(jfa):
     cache = jfa.Cache(ctypes.c_void_p(), codes, codes, (scales, scales))
     off, kv, table = torch.zeros(3, dtype=I32), torch.zeros(2, dtype=I32), torch.zeros(2, 5, dtype=I32)
     Q, bounds, lists, ws = torch.zeros(7, 8, 64, dtype=BF), torch.zeros(4, 2, 2, 64, dtype=BF), torch.zeros(7, 2, 3, dtype=I32), torch.zeros(512, dtype=U8)
-    O, lse = torch.zeros(7, 8, 64, dtype=F32), torch.zeros(7, 8)
+    O, lse = torch.zeros(7, 8, 64, dtype=F32), torch.zeros(7, 8, dtype=F32)
     for call in (lambda: jfa.jfa_cache_read(cache, 7, off, kv, table, K=Q, V=Q),
                  lambda: jfa.jfa_cache_summarize(cache, bounds[:1], 7, off, kv, table),
                  lambda: jfa.jfa_cache_select(cache, bounds, Q, off, kv, table, 4, blocks=lists, workspace=ws),

@@ -409,7 +409,7 @@ def test_steps_at_once_on_two_streams(jfa, bits):
     runs = []
     for c in cases:
         cache, bounds = cache_of(jfa, c), torch.nan_to_num(bounds_for(c, 21))
-        lists, O, lse = torch.empty(c.T, 2, 7, dtype=torch.int32, device="cuda"), torch.empty_like(c.Q), torch.empty(c.T, 8, device="cuda")
+        lists, O, lse = torch.empty(c.T, 2, 7, dtype=torch.int32, device="cuda"), torch.empty_like(c.Q), torch.empty(c.T, 8, device="cuda", dtype=F32)
         ws, sel = jfa.jfa_cache_workspace(cache, 8), jfa.jfa_cache_select_workspace(cache, 200, 1024)
 
         def run(c=c, cache=cache, bounds=bounds, lists=lists, O=O, lse=lse, ws=ws, sel=sel, **kw):
