@@ -198,6 +198,8 @@ __device__ __forceinline__ uint32_t quantise(const Half& g, const Raw& raw, floa
     return w;
 }
 
+__device__ __forceinline__ bool power_of_two(float f) { return (__float_as_uint(f) & 0x7fffffu) == 0u; }
+
 __global__ void __launch_bounds__(kThreads) jfa_cache_append4_kernel(const CacheAppendParams p, const QuantParams z) {
     using T = __nv_bfloat16;
     const int t = blockIdx.x, lane = threadIdx.x & 31;
@@ -247,7 +249,6 @@ __global__ void __launch_bounds__(kThreads) jfa_cache_append4_kernel(const Cache
         for (int k = 0; k < 2; ++k)
             if (i + k * kThreads < nq) rotate_vectors<T>(r[k].own, r[k].other, dst[k], u[k], row, R, p.pairs);
     }
-    auto whole = [](float f) { return (__float_as_uint(f) & 0x7fffffu) == 0u; };  // a power of two
     for (int i0 = first; i0 < nk; i0 += kThreads) {
         const int i = vec(i0), h = i >> vl, u = i & (vecs - 1);
         const Half gk = half_of(i, false, row), gv = half_of(i, true, nullptr);
@@ -256,17 +257,24 @@ __global__ void __launch_bounds__(kThreads) jfa_cache_append4_kernel(const Cache
             rv = load_raw(gv);
         }
         uint32_t sk, sv;
-        const uint32_t wk = quantise(gk, rk, z.factor[0], gk.d >= R && whole(z.factor[0]), sk);
+        const uint32_t wk = quantise(gk, rk, z.factor[0], gk.d >= R && power_of_two(z.factor[0]), sk);
         if (i0 + lane < nk) {
             *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.Kc) + at.page * p.ks[0] + slot * p.ks[1] + h * p.ks[2] + 4 * u) = wk;
             if (!(u & 1)) z.k_scales[at.page * z.kss[0] + h * z.kss[1] + ((slot << vl) + u) / 2] = uint8_t(sk);
         }
-        const uint32_t wv = quantise(gv, rv, z.factor[1], whole(z.factor[1]), sv);
+        const uint32_t wv = quantise(gv, rv, z.factor[1], power_of_two(z.factor[1]), sv);
         if (i0 + lane < nk) {
             *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.Vc) + at.page * p.vs[0] + slot * p.vs[1] + h * p.vs[2] + 4 * u) = wv;
             if (!(u & 1)) z.v_scales[at.page * z.vss[0] + h * z.vss[1] + ((slot << vl) + u) / 2] = uint8_t(sv);
         }
     }
+}
+
+// a f, cut to 24 bits with the last one set where something was cut off: it rounds to bf16 as the
+// product itself would.
+__device__ __forceinline__ float odd_product(float a, float f) {
+    const float x = __fmul_rz(a, f);
+    return __fmaf_rn(a, f, -x) != 0.f ? __uint_as_float(__float_as_uint(x) | 1u) : x;
 }
 
 // Rows out of a cache of any type: a thread takes 16 bytes of an output row.  p.K and p.V are the outputs
@@ -298,12 +306,13 @@ __global__ void __launch_bounds__(kThreads) jfa_cache_read_kernel(const CacheApp
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const float f = z.factor[v], sc = scale_value(s[v]);
+                const bool exact = power_of_two(f);
                 uint32_t e[4], o[4];
                 e2m1_to_f16(w[v], e);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 y = f16_to_float(e[j]);
-                    o[j] = pack_bf16x2(y.x * sc * f, y.y * sc * f);
+                    o[j] = exact ? pack_bf16x2(y.x * sc * f, y.y * sc * f) : pack_bf16x2(odd_product(y.x * sc, f), odd_product(y.y * sc, f));
                 }
                 x[v] = make_uint4(o[0], o[1], o[2], o[3]);
             }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from cache_cases import Case, np64
-from quant_cases import BF, E4M3, F32, F64, QCase, arrays, quantise, values
+from quant_cases import BF, CODES, E4M3, F32, F64, QCase, arrays, quantise, values
 
 pytestmark = pytest.mark.gpu
 
@@ -187,6 +187,37 @@ def test_read_gives_whole_histories(jfa, bits, D):
     torch.cuda.synchronize()
     assert np.array_equal(np64(K)[:n], b.c.gathered(b.c.Kc)) and np.array_equal(np64(V)[:n], b.c.gathered(b.c.Vc))
     assert bool((wide[n:] == 9).all()) and bool((wide[:, 0] == 9).all()) and bool((wide[:, 4] == 9).all())
+
+
+def test_read_rounds_once(jfa):
+    """Factors whose products with a value lie next to the middle of two bf16 numbers, on the
+    side that a product rounded to fp32 before would lose."""
+    grid = torch.arange(127, dtype=torch.uint8).view(E4M3).double().numpy()
+    held = np.unique(np.outer([0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], grid[1:]).ravel())
+    mids = (2 * np.arange(128, 256) + 1) / 512.0                     # middles of bf16 numbers in [0.5, 1)
+    a = held[:, None] / 2.0 ** np.floor(np.log2(held))[:, None]
+    f = (mids[None] / a).astype(np.float32)
+    x = a * f.astype(np.float64)                                     # exact: 6 bits by 24
+    near = (x != mids) & (x.astype(np.float32).astype(np.float64) == mids)
+    below, above = near & (x < mids), near & (x > mids)
+    assert below.sum() > 20 and above.sum() > 20
+    for side in (below, above):
+        for i, j in np.argwhere(side)[::max(1, side.sum() // 8)][:8]:
+            factor = float(f[i, j])
+            for bits in range(126, 0, -1):
+                codes = [c for c in range(1, 8) if np.isclose(CODES[c] * grid[bits], held[i], rtol=0, atol=0)]
+                if codes:
+                    break
+            k, ks = arrays(2, 16, 1, 64, "heads")
+            k[1, 3, 0], ks[1, 0, 3] = codes[0] | ((codes[0] | 8) << 4), bits
+            cache = jfa.jfa_cache_create_quantized(k, k.clone(), ks, ks.clone(), factor, factor)
+            one = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+            K, V = jfa.jfa_cache_read(cache, 4, one(0, 4), one(20), one(0, 1).view(1, 2))
+            value = held[i] * factor
+            unit = 2.0 ** (np.floor(np.log2(value)) - 7)
+            want = np.round(value / unit) * unit                     # (not a middle: no tie)
+            got = np64(K)[3, 0]
+            assert np.all(got[0::2] == want) and np.all(got[1::2] == -want) and torch.equal(K, V)
 
 
 # ------------------------------------------------------------------ attention
