@@ -3,34 +3,39 @@
 //
 // Every CTA of those kernels leaves a record: the item that starts in it and goes on past it, or
 // none.  A CTA here takes a record's row: its four warps deal the parts among them, a lane takes four
-// (or two) columns, the loads of 64 parts are in flight at once, and the warps' sums are added
+// (or two) columns, the loads of 32 parts are in flight at once, and the warps' sums are added
 // in order, so the result does not depend on timing.
 // Bound by latency: a record, its maxima and its parts, about 2.5 us.  With an item's last CTA adding its parts
 // itself, one 4-bit history of 131k keys (57 parts for each of 8 heads) took 43.5 us instead of 37.5, 64
-// histories 75 instead of 68.6, 128 listed blocks of 64 keys 14.5 instead of 10.6.
+// histories 75 instead of 68.6, 128 listed blocks of 64 keys 14.5 instead of 10.6.  Then with 32 parts in
+// flight instead of 64, and twice the CTAs an SM for it: one user 9.6 -> 9.1, 64 histories 67.4 -> 66.0, 64 lists
+// of blocks 36.8 -> 35.2 (16 parts: the long history 39.1).
+#include <algorithm>
+
 #include "cache_common.cuh"
 
 namespace jfa {
 
 namespace {
 
-constexpr int kJoinWarps = 4, kJoinRows = 4, kAtOnce = 16;
+constexpr int kJoinWarps = 4, kJoinRows = 4, kAtOnce = 8;
+static_assert(kJoinWarps * kAtOnce == 32, "a lane has a part's maximum and sum");
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) jfa_cache_join_kernel(const CacheFwdParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 8) jfa_cache_join_kernel(const CacheFwdParams p) {
     constexpr int V = D / 32, kPart = 16 * (D + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ float sums[kJoinWarps][D];
     wait_previous();
     const CacheCut cut = p.cuts[blockIdx.x];
     const int parts = cut.last - cut.first + 1;
-    for (int row = blockIdx.y; row < cut.rows; row += kJoinRows) {
+    for (int row = blockIdx.y; row < cut.rows; row += int(gridDim.y)) {
         auto part_of = [&](int c) { return p.part + size_t(cache_slot(cut.first + c, cut.first)) * kPart; };
         float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.f;
-        for (int c0 = 0; c0 < parts; c0 += 64) {
-            float x[kAtOnce][V], mc[2], lc[2];
+        for (int c0 = 0; c0 < parts; c0 += 32) {
+            float x[kAtOnce][V], mc, lc;
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const int c = c0 + kJoinWarps * k + warp;
@@ -48,13 +53,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) jfa_cache_join_kernel(const C
                     x[k][1] = u.y;
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {  // 64 parts' maxima and sums
-                const int c = c0 + lane + 32 * k;
-                mc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + row) : -INFINITY;
-                lc[k] = c < parts ? __ldcg(part_of(c) + 16 * D + 16 + row) : 0.f;
-            }
-            float top = fmaxf(m, fmaxf(mc[0], mc[1]));
+            const int mine = c0 + lane;  // 32 parts' maxima and sums
+            mc = mine < parts ? __ldcg(part_of(mine) + 16 * D + row) : -INFINITY;
+            lc = mine < parts ? __ldcg(part_of(mine) + 16 * D + 16 + row) : 0.f;
+            float top = fmaxf(m, mc);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             if (top == -INFINITY) continue;  // (no key yet: O is 0 in all of them)
@@ -63,15 +65,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) jfa_cache_join_kernel(const C
             l *= keep;
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[v] *= keep;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                mc[k] = ex2_approx(mc[k] - top);
-                l = fmaf(mc[k], lc[k], l);
-            }
+            mc = ex2_approx(mc - top);
+            l = fmaf(mc, lc, l);
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const int at = kJoinWarps * k + warp;
-                const float f = __shfl_sync(0xffffffffu, mc[kJoinWarps * k / 32], at & 31);
+                const float f = __shfl_sync(0xffffffffu, mc, at);
                 if (c0 + at >= parts) continue;
 #pragma unroll
                 for (int v = 0; v < V; ++v) acc[v] = fmaf(x[k][v], f, acc[v]);
@@ -108,7 +107,7 @@ cudaError_t launch(const CacheFwdParams& p, int ctas, cudaStream_t st) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, kJoinRows);
+    cfg.gridDim = dim3(ctas, std::min(kJoinRows, p.bm));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cfg.attrs = &attr;
