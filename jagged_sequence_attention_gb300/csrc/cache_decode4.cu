@@ -25,12 +25,12 @@
 // piece, else by tensor maps), four warps take 32 keys of each stage.  The warps merge at the end of an item;
 // the parts of an item cut between CTAs are added by a kernel of their own (cache_join.cu).
 // Measured, one token each of 32 query and 8 key heads of 128: 64 sequences of 200-16k keys (300 MB)
-// 68.6 us, 4.4 TB/s, 0.66 of the copy rate; one history of 131k keys (151 MB) 37.5 us, 0.60; 64 lists of 64
-// blocks of 32 keys (104 MB) 38.3 us, 0.41; one sequence of 1k keys 9.6 us.  The same stream with no
-// arithmetic takes 52 us of the 68.6: the rest is instructions, 620 a warp for 32 keys (128 conversions and as many
+// 66 us, 4.5 TB/s, 0.68 of the copy rate; one history of 131k keys (151 MB) 37.6 us, 0.60; 64 lists of 64
+// blocks of 32 keys (104 MB) 35.2 us, 0.44; one sequence of 1k keys 9.1 us.  The same stream with no
+// arithmetic takes 52 us of the 66: the rest is instructions, 620 a warp for 32 keys (128 conversions and as many
 // multiplications by scales among them), which fill half the issue slots; the warps wait for their own
 // chains and, a fifth of the time, for code.  More warps do not help: four CTAs an SM at 96
-// registers (which spill) 86 us, two CTAs 73, 16 keys at a time in half the code 73.
+// registers (which spill) 86 us instead of 69 then, two CTAs 73, 16 keys at a time in half the code 73.
 #include "cache_common.cuh"
 #include "quant.cuh"
 #include "tilemath.cuh"
