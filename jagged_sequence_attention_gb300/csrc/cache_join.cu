@@ -7,7 +7,7 @@
 // in order, so the result does not depend on timing.
 // Bound by latency: a record, its maxima and its parts, about 2.5 us.  With an item's last CTA adding its parts
 // itself, one 4-bit history of 131k keys (57 parts for each of 8 heads) took 43.5 us instead of 37.5, 64
-// histories 75 instead of 68.6, 128 listed blocks of 64 keys 14.5 instead of 10.6.  Then with 32 parts in
+// histories 75 instead of 68.6, 128 listed blocks of 16 keys 14.5 instead of 10.6.  Then with 32 parts in
 // flight instead of 64, and twice the CTAs an SM for it: one user 9.6 -> 9.1, 64 histories 67.4 -> 66.0, 64 lists
 // of blocks 36.8 -> 35.2 (16 parts: the long history 39.1).
 #include <algorithm>
