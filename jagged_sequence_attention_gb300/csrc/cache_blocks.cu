@@ -32,7 +32,7 @@ namespace {
 constexpr int kChunk = 64;          // blocks that a CTA scores
 constexpr int kSumThreads = 512, kScoreThreads = 256, kTileThreads = 256;
 constexpr int kTileTokens = 32;     // tokens that a CTA scores, where a sequence has many
-constexpr int kSelWarps = 32;       // warps that choose for one item, where more than 512 blocks may compete
+constexpr int kSelWarps = 32;       // warps that choose for one item, where more than 1024 blocks may compete
 
 struct BlockParams {
     CacheAppendParams a;            // the batch and the cache
@@ -466,14 +466,14 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
     return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-// The threads that choose for one token and key head: a warp of a CTA, or the CTA.  Their kernels run
+// The threads that choose for one token and key head: a warp of a CTA, or a CTA (of 4 or 32 warps).  Their kernels run
 // alone and cold, so what they cost beside latencies is the code they fetch: scores lie in shared
 // memory and loops stay rolled, and what few items need is a call (scores in registers, every pass laid
 // out: 37.7 us for a step over one history of 131k keys instead of 27.1).
 template <int WARPS>
 struct Choosers {
     static constexpr int kThreads = 32 * WARPS, kItems = WARPS == 1 ? 4 : 1;
-    static constexpr int kHeld = WARPS == 1 ? 512 : 8192, kCands = WARPS == 1 ? 128 : 1024;
+    static constexpr int kHeld = WARPS == 1 ? 512 : WARPS <= 4 ? 1024 : 8192, kCands = WARPS <= 4 ? 128 : 1024;
     struct Smem {
         float held[kHeld];
         unsigned long long keys[kCands];
@@ -731,7 +731,7 @@ __device__ __noinline__ float search(Choosers<WARPS>& g, const float* sc, const 
 
 // The chosen blocks of one token and key head, from its scores.
 template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems, WARPS == 1 ? 5 : 1) jfa_cache_choose_kernel(const BlockParams z) {
+__global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems, WARPS <= 4 ? 5 : 1) jfa_cache_choose_kernel(const BlockParams z) {
     using C = Choosers<WARPS>;
     const CacheAppendParams& p = z.a;
     extern __shared__ __align__(16) uint8_t choose_smem[];
@@ -919,6 +919,26 @@ void batch_params(CacheAppendParams& p, jfa_cache c, int32_t B, int64_t T, const
     p.status = c->d_status;
 }
 
+// Started while the scores are still computed, whose end it waits for.
+template <int WARPS>
+cudaError_t launch_choice(const BlockParams& z, int64_t items, cudaStream_t st) {
+    using C = Choosers<WARPS>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(jfa_cache_choose_kernel<WARPS>, int(sizeof(typename C::Smem)) * C::kItems, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((items + C::kItems - 1) / C::kItems));
+    cfg.blockDim = dim3(C::kThreads * C::kItems);
+    cfg.dynamicSmemBytes = sizeof(typename C::Smem) * C::kItems;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = z.a.max_pages > z.n_blocks ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, jfa_cache_choose_kernel<WARPS>, z);
+}
+
 // Blocks are those of bf16 and 4-bit caches with pages of at least 16 positions.
 jfa_status check_blocks(jfa_cache c) { return c->dtype == JFA_BF16 && c->page_log2 >= 4 ? JFA_OK : JFA_ERR_UNSUPPORTED; }
 
@@ -1022,33 +1042,18 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
         }
         if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return JFA_ERR_CUDA;
     }
-    // (started while the scores are still computed, whose end it waits for)
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = max_pages > n_blocks ? 1 : 0;
+    // As many warps an item as hold its scores and fill the SMs: one where there are many items, four, or a
+    // CTA's 32.  On 8 heads, 250 blocks, with one, four and 32: 8 items 8.6, 6.4 and 8.5 us, 64 14.8, 9.9 and
+    // 9.5, 128 15.4, 8.4 and 10.7, 512 24.4, 20.0 and 36, 1024 30.7, 29.5 and 63, 2048 25.9, 28.6 and 94 (in tiles),
+    // 4096 (125 blocks) 42, 53 and 203.
+    const int64_t items = T * cache->Hkv;
     cudaError_t e;
-    // A warp an item where that holds all scores that there can be and there are more items than SMs.  (With
-    // a CTA an item, 8 heads, 250 blocks: 8 tokens 9.5 us instead of 14.8, 16 13.6 instead of 15.4, 32 23 instead of
-    // 18.6, 64 36 instead of 25, 512 203 instead of 41.)
-    if (max_pages <= Choosers<1>::kHeld && T * cache->Hkv > cache->num_sms) {
-        using C = Choosers<1>;
-        cfg.gridDim = dim3(int((T * cache->Hkv + C::kItems - 1) / C::kItems));
-        cfg.blockDim = dim3(C::kThreads * C::kItems);
-        cfg.dynamicSmemBytes = sizeof(C::Smem) * C::kItems;
-        e = cudaLaunchKernelEx(&cfg, jfa_cache_choose_kernel<1>, z);
-    } else {
-        using C = Choosers<kSelWarps>;
-        static std::atomic<uint64_t> done{0};
-        e = allow_smem(jfa_cache_choose_kernel<kSelWarps>, int(sizeof(C::Smem)), done);
-        cfg.gridDim = dim3(int(T * cache->Hkv));
-        cfg.blockDim = dim3(C::kThreads);
-        cfg.dynamicSmemBytes = sizeof(C::Smem);
-        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, jfa_cache_choose_kernel<kSelWarps>, z);
-    }
+    if (max_pages <= Choosers<1>::kHeld && items > 8 * cache->num_sms)
+        e = launch_choice<1>(z, items, st);
+    else if (max_pages <= Choosers<4>::kHeld)
+        e = launch_choice<4>(z, items, st);
+    else
+        e = launch_choice<kSelWarps>(z, items, st);
     return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 

@@ -312,6 +312,17 @@ def test_equal_scores_of_many_tokens(jfa, kinds):
     assert np.array_equal(choose(jfa, c, bounds, 60), expected_blocks(c, bounds, 60, 1, 1))
 
 
+@pytest.mark.parametrize("pages,tokens", [(400, 420), (400, 60), (900, 420), (900, 5), (1200, 20)])
+def test_numbers_of_items_and_pages(jfa, pages, tokens):
+    # (a warp, four or 32 an item, by both numbers)
+    c = Case([tokens, 1], [16 * pages, 16 * pages - 3], H=3, Hkv=3, D=64, page=16, seed=pages + tokens)
+    random = torch.nan_to_num(bounds_for(c, tokens))
+    few = random[torch.randint(0, 3, (c.n_pages,), device="cuda")].contiguous()
+    for bounds in (random, few):
+        for n in (4, 300):
+            assert np.array_equal(choose(jfa, c, bounds, n), expected_blocks(c, bounds, n, 1, 1))
+
+
 def test_nearly_equal_scores(jfa):
     """Scores that fp32 sums cannot tell apart: large parts that cancel, and differences in the
     last bits."""
