@@ -178,11 +178,12 @@ __device__ __forceinline__ void query_sums(const BlockParams& z, int t, int hk, 
     }
 }
 
-// What an fp32 score may be off by: m the largest magnitude among the bounds, norm the sums' norm
-// (which is itself a sum of 2 D values, hence the 1.01).  An operand below 2^-126 may count as 0, and a
-// product or sum may lose 2^-126: 2 D and a few times that is below 2^-116.
+// What an fp32 score may be off by (infinite where it may be no number at all): m the largest magnitude
+// among the bounds, norm the sums' norm (which is itself a sum of 2 D values, hence the 1.01).  An operand
+// below 2^-126 may count as 0, and a product or sum may lose 2^-126: 2 D and a few times that is below 2^-116.
 __device__ __forceinline__ float slack_of(const BlockParams& z, int steps, float m, float norm) {
-    if (!(m > 0.f && norm > 0.f)) return 0.f;  // all scores are 0
+    if (!(m * norm < 3e38f)) return INFINITY;  // a sum may leave fp32's range
+    if (m == 0.f || norm == 0.f) return 0.f;   // all scores are 0
     return fmaf(float(z.g + steps) * (1.01f * 0x1p-24f) * m, norm, 0x1p-116f * (m + norm) + 0x1p-116f);
 }
 
@@ -797,7 +798,15 @@ __global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems, WARPS <=
     // The k-th largest score, `up`, and the next, `down`: the scores by 256 steps of their range, then
     // those of the step that holds the k-th by their rank.
     float up, down = -INFINITY, kth;
-    bool found = large > small;
+    const bool wild = slack == INFINITY;  // (the scores are of no use: all are taken again in 64 bits)
+    if (wild) {
+#pragma unroll 1
+        for (int i = g.thread; i < n; i += C::kThreads) sc[i] = 0.f;
+        g.sync();
+        settle_exactly<WARPS>(g, z, t, c.b, hk, first, sc, n, -INFINITY, INFINITY, k, n);
+        up = INFINITY;
+    }
+    bool found = !wild && large > small;
     if (found) {
         const float per = 255.f / (large - small);
         auto step_of = [&](float x) { return max(0, min(int((x - small) * per), 255)); };
@@ -862,12 +871,12 @@ __global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems, WARPS <=
             }
         }
     }
-    if (!found) up = down = search<WARPS>(g, sc, n, k, small, large);
+    if (!found && !wild) up = down = search<WARPS>(g, sc, n, k, small, large);
     kth = up;
     float cut = kth;  // chosen: scores of at least this
     // Scores further apart than twice the slack are in the order of the exact ones: then the k largest
     // are the chosen ones.
-    if (up - down <= 2.01f * slack) {
+    if (!wild && up - down <= 2.01f * slack) {
         const float above = __fadd_ru(kth, 2.f * slack), low = __fadd_rd(kth, -2.f * slack);
         int sure = 0, maybe = 0;
 #pragma unroll 1

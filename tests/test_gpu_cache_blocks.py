@@ -323,6 +323,18 @@ def test_numbers_of_items_and_pages(jfa, pages, tokens):
             assert np.array_equal(choose(jfa, c, bounds, n), expected_blocks(c, bounds, n, 1, 1))
 
 
+@pytest.mark.parametrize("pages,tokens", [(68, 1), (400, 420), (400, 60), (1200, 2)])
+def test_scores_past_fp32(jfa, pages, tokens):
+    """Finite bounds and queries whose products are not finite in fp32, or only just."""
+    c = Case([tokens, 1], [16 * pages, 16 * pages - 3], H=12, Hkv=3, D=128, page=16, seed=pages + tokens)
+    Q = c.Q.float()
+    for big in (1e14, 1e16, 1e18):
+        bounds = torch.nan_to_num(bounds_for(c, tokens, std=1e20))
+        c.Q = (Q * big).to(BF)
+        for n, m in ((4, None), (60, 1)):
+            assert np.array_equal(choose(jfa, c, bounds, n, max_q_len=m), expected_blocks(c, bounds, n, 1, 1))
+
+
 def test_nearly_equal_scores(jfa):
     """Scores that fp32 sums cannot tell apart: large parts that cancel, and differences in the
     last bits."""
