@@ -179,10 +179,12 @@ __device__ __forceinline__ void query_sums(const BlockParams& z, int t, int hk, 
 }
 
 // What an fp32 score may be off by (infinite where it may be no number at all): m the largest magnitude
-// among the bounds, norm the sums' norm (which is itself a sum of 2 D values, hence the 1.01).  An operand
+// among the bounds, norm the sums' norm (which is itself a sum of 2 D values, hence the 1.01).  A product or sum
+// may leave fp32's range, and so may a sum of queries by itself: from 2^128 - 2^119 on its first bf16 part is
+// infinite, whatever the bounds.  An operand
 // below 2^-126 may count as 0, and a product or sum may lose 2^-126: 2 D and a few times that is below 2^-116.
 __device__ __forceinline__ float slack_of(const BlockParams& z, int steps, float m, float norm) {
-    if (!(m * norm < 3e38f)) return INFINITY;  // a sum may leave fp32's range
+    if (!(m * norm < 3e38f && norm < 3e38f)) return INFINITY;
     if (m == 0.f || norm == 0.f) return 0.f;   // all scores are 0
     return fmaf(float(z.g + steps) * (1.01f * 0x1p-24f) * m, norm, 0x1p-116f * (m + norm) + 0x1p-116f);
 }
