@@ -211,7 +211,10 @@ __device__ __forceinline__ int cache_list_block(int block, int before, int own_b
     }
     return block <= own_block ? block : -1;
 }
-constexpr int kNoBlock = 1 << 30;  // the position of keys of no block, past every row's
+// Positions are below INT_MAX - kPositionRoom (check_batch): a tile's keys may be counted on past them.
+// kNoBlock, the position of keys of no block, is past every row's, and so are those counted on from it.
+constexpr int kPositionRoom = 1024, kNoBlock = INT_MAX - kPositionRoom;
+static_assert(kPositionRoom >= 256, "a tile of 128 keys from any position on, and from kNoBlock on");
 
 // Where a CTA's range of units starts, and how the ranges are cut.
 struct CacheStart {

@@ -65,7 +65,7 @@ inline jfa_status check_batch(jfa_cache c, int32_t B, int64_t T, const int32_t* 
     if (!c || B < 0 || B > kCacheMaxB || T < 0 || T > (1 << 30) || max_pages < 0) return JFA_ERR_INVALID_ARG;
     if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4)) return JFA_ERR_INVALID_ARG;
     if (B > 0 && (!q_offsets || !kv_lens || (max_pages > 0 && !page_table))) return JFA_ERR_INVALID_ARG;
-    *max_kv = int32_t(std::min<int64_t>(int64_t(max_pages) << c->page_log2, INT32_MAX - T - 1024));
+    *max_kv = int32_t(std::min<int64_t>(int64_t(max_pages) << c->page_log2, INT32_MAX - T - kPositionRoom));
     return JFA_OK;
 }
 

@@ -1,12 +1,12 @@
 """The 4-bit cache and attention over selected blocks on a GPU, at the ends of what their calls take:
-sums next to fp32's largest number."""
+sums next to fp32's largest number, positions past 2^30."""
 import numpy as np
 import pytest
 import torch
 
-from cache_cases import Case
-from quant_cases import BF
-from test_gpu_cache_blocks import bounds_for, choose, expected_blocks, tokens
+from cache_cases import Case, np64
+from quant_cases import BF, F32
+from test_gpu_cache_blocks import attend, bounds_for, check, choose, expected_blocks, make, reference, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,57 @@ def test_selection_by_sums_past_bf16(jfa, pages, tokens, D):
     for b in (bounds, flat, torch.zeros_like(bounds)):
         for n, m in ((4, None), (60, None), (60, 1)):
             assert np.array_equal(choose(jfa, c, b, n, max_q_len=m), expected_blocks(c, b, n, 1, 1))
+
+
+# ------------------------------------------------------------------ positions past 2^30
+
+class Histories:
+    """Rows of histories that are longer than their pages: position j of sequence b by the page table."""
+
+    def __init__(self, c, which):
+        self.c, self.which, self.off = c, np64(which), np.concatenate([[0], np.cumsum(c.kv)])
+
+    def __getitem__(self, at):
+        i, h = at
+        b = np.searchsorted(self.off, i, "right") - 1
+        j = i - self.off[b]
+        return self.which[self.c.host_table[b, j // self.c.page], j % self.c.page, h]
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bias", [False, True])
+def test_lists_of_a_history_past_2_30(jfa, bits, D, bias):
+    """A list's end, and its blocks past the token, hold no key whatever the token's position."""
+    page = 1024
+    c = make(bits, [2, 1], [40 * page, 3000], H=4, Hkv=2, D=D, page=page, bias=bias, unset=False, seed=D + bits)
+    for kv in (2 ** 30 + 5000, (2 ** 31 - 1 - c.T - 1024) // page * page):  # (the second: the longest there is in whole pages)
+        width = -(-kv // page)
+        table = np.full((2, width), -1, np.int32)
+        table[0] = c.host_table[0, np.arange(width) % 40]
+        table[1, :3] = c.host_table[1, :3]
+        c.kv, at = np.array([kv, 3000]), c.host_table
+        c.kv_lens = torch.tensor(c.kv, dtype=torch.int32, device="cuda")
+        c.host_table, c.table = table, torch.from_numpy(table).cuda()
+        c.gathered = lambda which: Histories(c, which)
+        own = (kv - 1) // page
+        lists = np.full((3, 2, 11), -1, np.int32)
+        lists[0, 0, :3], lists[0, 1, :5] = [0, 7, own], [2, 3, own - 1, own, own + 1]
+        lists[1, 0, :1], lists[1, 1] = own, own - 10 + np.arange(11)
+        lists[2, 0, :2], lists[2, 1, :1] = [0, 2], 1
+        ref = reference(c, lists)
+        check(c, *attend(jfa, c, lists), ref)
+        check(c, *attend(jfa, c, lists, out_dtype=F32), ref)
+        c.host_table = at
+
+
+def test_selection_from_a_history_past_2_30(jfa):
+    page, kinds = 1024, 40
+    c = Case([2], [kinds * page], H=2, Hkv=1, D=64, page=page, unset=False, seed=2)
+    c.kv = np.array([2 ** 30 + 5000])
+    width = -(-int(c.kv[0]) // page)
+    c.host_table = np.ascontiguousarray(c.host_table[:, np.arange(width) % kinds])
+    c.table, c.kv_lens = torch.from_numpy(c.host_table).cuda(), torch.tensor(c.kv, dtype=torch.int32, device="cuda")
+    bounds = torch.nan_to_num(bounds_for(c, 2))
+    for n in (3, 50, 40000):
+        assert np.array_equal(choose(jfa, c, bounds, n, 1, 2), expected_blocks(c, bounds, n, 1, 2))
