@@ -199,18 +199,77 @@ __device__ __forceinline__ CacheSeq cache_lane_seq(const CacheFwdParams& p, int 
     return s;
 }
 
-// A list's entry, `before` the one before it (kNoEntry: there is none): its block, or -1 if there
-// is none to read.  Entries ascend and end with -1 (each is compared with the one before it
-// alone); blocks past the token's own hold no key that it may see.
-constexpr int kNoEntry = INT_MIN;
-__device__ __forceinline__ int cache_list_block(int block, int before, int own_block, int* status) {
-    if (block < 0) return -1;
-    if (before != kNoEntry && (before < 0 || block <= before)) {
-        atomicOr(status, kStatusBounds);
-        return -1;
+// A warp's way along lists.  An entry counts that is above all before it, a -1 among them being above every block: so
+// entries ascend and end with -1.  One that does not count is left out where it is met, and reported.
+// As long as each entry is above its neighbour, it is above all before it, and nothing else is looked at (with the largest
+// entry so far kept up at every stage, 64 lists of blocks took 37.2 us instead of 35.5).  From the first that is not on,
+// the largest is kept.  A CTA whose part of an item starts inside its list looks over the entries before it (128
+// blocks of one history: 9.9 -> 10.4 us).
+struct CacheListScan {
+    bool broken = false;   // an entry of this list was not above its neighbour
+    uint32_t before = 0u;  // then: the largest entry before the stage's first one
+    // Entries compare by their block plus 1, a -1 as 2^32 - 1, none as 0.
+    static __device__ __forceinline__ uint32_t key(int block) { return block < 0 ? ~0u : uint32_t(block) + 1u; }
+    static __device__ __forceinline__ bool falls(int block, uint32_t last) { return block >= 0 && key(block) <= last; }
+    // A list from its entry n on.
+    __device__ __forceinline__ void start(const int32_t* list, int n, int lane) {
+        bool bad = false;
+#pragma unroll 1
+        for (int i0 = 1; i0 < n; i0 += 128) {  // (128 entries' loads in flight)
+            int block[4], last[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + 32 * k + lane;
+                block[k] = i < n ? list[i] : -1;
+                last[k] = i < n ? list[i - 1] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bad |= falls(block[k], key(last[k]));
+        }
+        broken = __any_sync(0xffffffffu, bad);
+        if (broken) {
+            uint32_t top = 0u;
+            for (int i = lane; i < n; i += 32) top = max(top, key(list[i]));
+            before = __reduce_max_sync(0xffffffffu, top);
+        }
     }
-    return block <= own_block ? block : -1;
-}
+    // The largest entry before a lane's, and before the next stage's first one.  (Lists are in order: a call, whose code is not
+    // fetched for them.)
+    static __device__ __noinline__ uint2 largest(uint32_t mine, uint32_t before, bool single, bool ends, int per, int at) {
+        uint32_t above = before;
+        if (single) {
+            uint32_t top = mine;  // of the boxes up to this one
+            for (int d = 1; d < per; d <<= 1) {
+                const uint32_t other = __shfl_up_sync(0xffffffffu, top, d, per);
+                if (at >= d) top = max(top, other);
+            }
+            const uint32_t left = __shfl_up_sync(0xffffffffu, top, 1, per);
+            if (at > 0) above = max(above, left);
+        }
+        return make_uint2(above, ends ? max(before, __reduce_max_sync(0xffffffffu, mine)) : before);
+    }
+    // Whether a lane's entry counts, by the whole warp: lane `at` of each `per` side by side has a box's, and all groups of
+    // `per` lanes the same; met: there is one; last: the key of the entry before it.  single: a box is a block (else
+    // a stage is of one entry, and ends: it is the last of that entry).
+    __device__ __forceinline__ bool counts(int block, bool met, uint32_t last, bool single, bool ends, int per, int at, int* status) {
+        const bool bad = met && falls(block, last);
+        if (!broken && __any_sync(0xffffffffu, bad)) {
+            broken = true;
+            before = __shfl_sync(0xffffffffu, last, 0);  // (all before ascend)
+        }
+        bool in = met && block >= 0;
+        if (broken) {
+            const uint32_t mine = met ? key(block) : 0u;
+            const uint2 tops = largest(mine, before, single, single || ends, per, at);
+            before = tops.y;
+            if (in && mine <= tops.x) {
+                atomicOr(status, kStatusBounds);
+                in = false;
+            }
+        }
+        return in;
+    }
+};
 // Positions are below INT_MAX - kPositionRoom (check_batch): a tile's keys may be counted on past them.
 // kNoBlock, the position of keys of no block, is past every row's, and so are those counted on from it.
 constexpr int kPositionRoom = 1024, kNoBlock = INT_MAX - kPositionRoom;

@@ -126,47 +126,56 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             atomicOr(p.status, kStatusBounds);
             return p.n_pages;
         };
-        // Lists: a stage, as this lane sees it (its block, -1: nothing to load; that block's page, the
+        // Lists: a stage, as this lane sees it (its block; whether to load it; that block's page, the
         // slot and the position of the first key).  Its entry is asked for two stages before it is loaded,
-        // its page one stage, so that the stream waits for neither.
+        // its page one stage, so that the stream waits for neither; whether the entry counts is seen when it is loaded, the
+        // first time while its page is on the way.
         struct Stage {
-            bool have, head;
-            int hk, block, before, slot, base, page, at;
-            size_t row;  // of the page table
+            bool have, read, met, head, starts, ends;  // an entry, the first, a new list, an entry's last stage
+            int hk, block, last, slot, base, page, at;  // last: the entry before
+            size_t row;                                // of the page table
+        };
+        CacheListScan scan;
+        bool starts = false;
+        auto list_of = [&](const CacheSeg& s) {
+            return p.lists + (size_t(s.s.q0 + s.tile) * size_t(p.Hkv) + size_t(s.hk)) * size_t(p.n_list);
         };
         auto step = [&](Stage& s) {
             while (have && (g.r.n == 0 || kt >= g.k1)) {
                 have = cur.next(p, g);
                 kt = g.k0;
+                starts = true;
             }
             s.have = have;
             s.block = -1;
-            s.base = kNoBlock;
             if (!have) return;
-            const int j = kt++ * BN + pg * rows;
+            const int j0 = kt++ * BN, j = j0 + pg * rows, e = j >> p.page_log2;
             s.hk = g.hk;
             s.slot = j & ((1 << p.page_log2) - 1);
             s.row = size_t(g.b) * size_t(p.max_pages);
-            if (!mine || j >= g.r.hi) return;
-            const int e = j >> p.page_log2;
-            const int32_t* list = p.lists + (size_t(g.s.q0 + g.tile) * size_t(p.Hkv) + size_t(g.hk)) * size_t(p.n_list);
             s.at = g.s.kv_len - g.s.q_len + g.tile;  // the token's position
-            s.block = list[e];
-            s.before = list[max(e - 1, 0)];
+            s.met = j < g.r.hi;
             s.head = e == 0;
-        };
-        auto look = [&](Stage& s) {
-            if (s.block >= 0) {
-                s.block = cache_list_block(s.block, s.head ? kNoEntry : max(s.before, -1), s.at >> p.page_log2, p.status);
-                s.base = (s.block << p.page_log2) + s.slot;
-                if (s.base > s.at) s.block = -1;
+            if (s.met) {
+                s.block = list_of(g)[e];
+                s.last = list_of(g)[max(e - 1, 0)];
             }
-            s.page = s.block >= 0 ? p.table[s.row + size_t(s.block)] : -1;
+            s.ends = ((j0 + BN) & ((1 << p.page_log2) - 1)) == 0;
+            s.starts = starts;
+            starts = false;
+        };
+        auto look = [&](Stage& s) {  // (blocks past the token's own hold no key that it may see)
+            s.base = int(uint32_t(s.block) << p.page_log2) + s.slot;
+            s.read = mine && s.block >= 0 && s.block <= s.at >> p.page_log2 && s.base <= s.at;
+            s.page = s.read ? p.table[s.row + size_t(s.block)] : -1;
         };
         if constexpr (LIST) {
             Stage now, next;
             step(now);
-            look(now);
+            if (now.have) {
+                look(now);
+                scan.start(list_of(g), (g.k0 * BN) >> p.page_log2, lane);
+            }
             step(next);
             while (now.have) {
                 const Stage s = now;
@@ -175,12 +184,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                     look(now);
                     step(next);
                 }
+                if (s.starts) scan = CacheListScan();
+                const bool counts = scan.counts(s.block, s.met, s.head ? 0u : CacheListScan::key(s.last), p.page_log2 <= 6, s.ends, per, pg, p.status);
+                const bool in = s.read && counts;
                 const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1;
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(st), ph ^ 1, abort_flag))) {
                     ok = false;
                     break;
                 }
-                const bool in = s.block >= 0;
                 const int n = __popc(__ballot_sync(0xffffffffu, in));
                 if (lane < per) bases[st * C::kBoxes + pg] = in ? s.base : kNoBlock;
                 __syncwarp();

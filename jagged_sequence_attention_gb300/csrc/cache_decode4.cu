@@ -151,7 +151,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
         fence_proxy_async_smem();  // the scratch's writes before the first loads into it
         const int rows = min(1 << p.page_log2, 64);          // keys of a box
         const int per = BN / rows;                           // pages (or parts of one) in a stage
-        const int pg = lane;
+        const int pg = LIST ? lane & (per - 1) : lane;
         const bool mine = lane < per;
         const uint32_t box = uint32_t(pg * rows * C::kRow), sbox = uint32_t(C::kOffKS + pg * rows * C::kScales);
         uint32_t it = 0;
@@ -159,47 +159,64 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
         int kt = g.k0;
         // A stage, as this lane sees it: its block of the sequence (-1: nothing to load), that block's page,
         // the slot and the position of the first key.  Its list entry is asked for two stages before it
-        // is loaded, its page one stage, so that the stream waits for neither.
+        // is loaded, its page one stage, so that the stream waits for neither; whether the entry counts is seen when it
+        // is loaded, the first time while its page is on the way.
         struct Stage {
-            bool have, head;
-            int hk, block, before, slot, base, page, at;
-            size_t row;  // of the page table
+            bool have, read, met, head, starts, ends;  // read: a page; lists: an entry, the first, a new list, an entry's last stage
+            int hk, block, last, slot, base, page, at;  // last: the entry before
+            size_t row;                                // of the page table
+        };
+        CacheListScan scan;
+        bool starts = false;
+        auto list_of = [&](const CacheSeg& s) {
+            return p.lists + (size_t(s.s.q0 + s.tile) * size_t(p.Hkv) + size_t(s.hk)) * size_t(p.n_list);
         };
         auto step = [&](Stage& s) {
             while (more && (g.r.n == 0 || kt >= g.k1)) {
                 more = cur.next(p, g);
                 kt = g.k0;
+                starts = true;
             }
             s.have = more;
             s.block = -1;
             s.base = kNoBlock;
             if (!more) return;
-            const int j = (g.r.f + kt++) * BN + pg * rows;
+            const int j0 = (g.r.f + kt++) * BN, j = j0 + pg * rows;
             s.hk = g.hk;
             s.slot = j & ((1 << p.page_log2) - 1);
             s.row = size_t(g.b) * size_t(p.max_pages);
-            if (!mine || j >= g.r.hi || (!LIST && j + rows <= g.r.lo)) return;
-            const int e = j >> p.page_log2;
-            s.block = e;
             if constexpr (LIST) {
-                const int32_t* list = p.lists + (size_t(g.s.q0 + g.tile) * size_t(p.Hkv) + size_t(g.hk)) * size_t(p.n_list);
+                const int e = j >> p.page_log2;
                 s.at = g.s.kv_len - g.s.q_len + g.tile;  // the token's position
-                s.block = list[e];
-                s.before = list[max(e - 1, 0)];
+                s.met = j < g.r.hi;
                 s.head = e == 0;
+                if (s.met) {
+                    s.block = list_of(g)[e];
+                    s.last = list_of(g)[max(e - 1, 0)];
+                }
+                s.ends = ((j0 + BN) & ((1 << p.page_log2) - 1)) == 0;
+                s.starts = starts;
+                starts = false;
+            } else if (mine && j < g.r.hi && j + rows > g.r.lo) {
+                s.block = j >> p.page_log2;
             }
         };
         auto look = [&](Stage& s) {
-            if (LIST && s.block >= 0) {
-                s.block = cache_list_block(s.block, s.head ? kNoEntry : max(s.before, -1), s.at >> p.page_log2, p.status);
-                s.base = (s.block << p.page_log2) + s.slot;
-                if (s.base > s.at) s.block = -1;
+            bool in = s.block >= 0;
+            if constexpr (LIST) {  // (blocks past the token's own hold no key that it may see)
+                in = in && mine && s.block <= s.at >> p.page_log2;
+                s.base = int(uint32_t(s.block) << p.page_log2) + s.slot;
+                in = in && s.base <= s.at;
             }
-            s.page = s.block >= 0 ? p.table[s.row + size_t(s.block)] : -1;
+            s.page = in ? p.table[s.row + size_t(s.block)] : -1;
+            s.read = in;
         };
         Stage now, next;
         step(now);
-        look(now);
+        if (now.have) {
+            look(now);
+            if constexpr (LIST) scan.start(list_of(g), (g.k0 * BN) >> p.page_log2, lane);
+        }
         step(next);
         while (now.have) {
             const Stage s = now;
@@ -208,12 +225,17 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), (Cfg<D, NT>::kCtas))
                 look(now);
                 step(next);
             }
+            bool in = s.read;
+            if constexpr (LIST) {
+                if (s.starts) scan = CacheListScan();
+                const bool counts = scan.counts(s.block, s.met, s.head ? 0u : CacheListScan::key(s.last), p.page_log2 <= 6, s.ends, per, pg, p.status);
+                in = in && counts;
+            }
             const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(st), ph ^ 1, abort_flag))) {
                 ok = false;
                 break;
             }
-            const bool in = s.block >= 0;
             const int n = __popc(__ballot_sync(0xffffffffu, in));
             if constexpr (LIST) {
                 if (mine) bases[st * C::kBoxes + pg] = in ? s.base : kNoBlock;

@@ -1,12 +1,12 @@
 """The 4-bit cache and attention over selected blocks on a GPU, at the ends of what their calls take:
-sums next to fp32's largest number, positions past 2^30."""
+sums next to fp32's largest number, positions past 2^30, lists out of order."""
 import numpy as np
 import pytest
 import torch
 
 from cache_cases import Case, np64
 from quant_cases import BF, F32
-from test_gpu_cache_blocks import attend, bounds_for, check, choose, expected_blocks, make, reference, tokens
+from test_gpu_cache_blocks import attend, bounds_for, check, choose, expected_blocks, make, random_lists, reference, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,62 @@ def test_selection_from_a_history_past_2_30(jfa):
     bounds = torch.nan_to_num(bounds_for(c, 2))
     for n in (3, 50, 40000):
         assert np.array_equal(choose(jfa, c, bounds, n, 1, 2), expected_blocks(c, bounds, n, 1, 2))
+
+
+# ------------------------------------------------------------------ lists out of order
+
+def in_order(lists):
+    """The entries that ascend over all before them and follow no -1, as a list; whether others were left out (of each list:
+    up to which entry there is none)."""
+    kept, wrong = np.full_like(lists, -1), np.full(lists.shape[:-1], lists.shape[-1])
+    for at in np.ndindex(lists.shape[:-1]):
+        top, n = -1, 0
+        for e, x in enumerate(lists[at]):
+            if x < 0:
+                top = np.iinfo(np.int64).max
+            elif x > top:
+                kept[at][n] = top = x
+                n += 1
+            else:
+                wrong[at] = min(wrong[at], e)
+    return kept, wrong
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_entries_out_of_order_are_left_out(jfa, bits):
+    c = make(bits, [1], [300], H=4, Hkv=1, D=64, page=16, seed=6)
+    for bad, same in (([0, -1, 2, 3], [0]), ([5, 3, 5], [5]), ([-1, 0, 1, 2], []), ([7, 1, 6, 2, 7, 8], [7, 8]), ([4, -1, -1, 9], [4])):
+        assert [x for x in in_order(np.array([bad]))[0][0] if x >= 0] == same
+        lists = np.array([[bad]], np.int32)
+        kept = np.full_like(lists, -1)
+        kept[0, 0, :len(same)] = same
+        check(c, *attend(jfa, c, lists, status=jfa.JFA_ERR_DEVICE_BOUNDS), reference(c, kept))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 1024])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_lists_out_of_order(jfa, bits, page, D):
+    """Lists that are cut between CTAs: what comes before a CTA's part decides about it too."""
+    blocks = min(700, 120000 // page)
+    c = make(bits, [1, 3, 1], [blocks * page, blocks * page // 2, blocks * page - 5], H=4, Hkv=2, D=D, page=page, seed=page + D)
+    good = random_lists(c, blocks, 1, 0.9)
+    rs = np.random.RandomState(page + D + bits)
+    looked = np.minimum(blocks, tokens(c)[1] // page + 1)  # entries that a token looks at
+    for change in range(5):
+        lists = good.copy()
+        if change == 0:
+            lists[0, 0, 0] = blocks - 2          # nearly all lie before it
+            lists[1, 1, 2] = -1
+        elif change == 1:
+            lists[0, 0, blocks // 3] = blocks - 1
+            lists[4, 1, blocks // 2] = -5
+        elif change == 2:
+            lists[:, :, 1:] = rs.randint(0, blocks, lists[:, :, 1:].shape)
+        elif change == 3:
+            lists[:, 0] = blocks - 1 - np.arange(blocks)
+        kept, wrong = in_order(lists)
+        reported = bool((wrong < looked[:, None]).any())
+        assert reported == (change < 4)
+        O, lse = attend(jfa, c, lists, status=jfa.JFA_ERR_DEVICE_BOUNDS if reported else None)
+        check(c, O, lse, reference(c, kept))
