@@ -139,7 +139,8 @@ inline void fwd_params(CacheFwdParams& p, jfa_cache cache, int32_t B, int64_t T,
     p.n_pages = cache->n_pages;
     p.causal = causal;
     p.window = window < max_kv ? window : -1;  // a window of every position is none
-    p.scale_log2 = scale * 1.4426950408889634f;
+    // (the factor first: it is the product that the calls check to be a normal number)
+    p.scale_log2 = (cache->ops ? scale * cache->k_factor : scale) * 1.4426950408889634f;
     p.bias = bias;
     p.Q = Q;
     p.q_stride = q_stride;
@@ -154,7 +155,6 @@ inline void fwd_params(CacheFwdParams& p, jfa_cache cache, int32_t B, int64_t T,
         p.vs[i] = cache->vs[i];
     }
     if (cache->ops) {
-        p.scale_log2 *= cache->k_factor;
         p.o_mul = cache->v_factor;
         p.k_scales = cache->k_scales;
         p.v_scales = cache->v_scales;

@@ -1,12 +1,13 @@
 """The 4-bit cache and attention over selected blocks on a GPU, at the ends of what their calls take:
-sums next to fp32's largest number, positions past 2^30, lists out of order."""
+sums next to fp32's largest number, positions past 2^30, lists out of order, scales that only
+their product with the cache's factor brings into range."""
 import numpy as np
 import pytest
 import torch
 
 from cache_cases import Case, np64
-from quant_cases import BF, F32
-from test_gpu_cache_blocks import attend, bounds_for, check, choose, expected_blocks, make, random_lists, reference, tokens
+from quant_cases import BF, F32, QCase
+from test_gpu_cache_blocks import SETS, attend, bounds_for, check, choose, expected_blocks, make, random_lists, reference, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +155,30 @@ def test_long_lists_out_of_order(jfa, bits, page, D):
         assert reported == (change < 4)
         O, lse = attend(jfa, c, lists, status=jfa.JFA_ERR_DEVICE_BOUNDS if reported else None)
         check(c, O, lse, reference(c, kept))
+
+
+# ------------------------------------------------------------------ scales
+
+@pytest.mark.parametrize("factor,scale", [(2.0 ** -60, 3e38), (2.0 ** -60, 2.5e38), (2.0 ** 60, 1e-45), (2.0 ** 60, 7e-45), (1e18, 3e-44), (1e-3, 3e38)])
+def test_scales_that_the_factor_brings_into_range(jfa, factor, scale):
+    """scale * k_factor lies in the documented range; scale * log2(e) alone would not be a number, or lose its bits."""
+    factor, scale = float(np.float32(factor)), float(np.float32(scale))
+    for lens in (([1, 2, 1], [70, 1000, 33]), ([40, 1, 300], [900, 65, 301])):
+        c = QCase(*lens, H=8, Hkv=2, D=64, page=16, factors=(factor, 1.0), seed=3)
+        c.Q = (c.Q.double() / (scale * factor * 8)).to(BF)  # scores of the usual size
+        assert bool(torch.isfinite(c.Q).all())
+        lists = np.tile(np.arange(70, dtype=np.int32), (c.T, 2, 1))
+        dense, listed = c.run(jfa, scale=scale, out_dtype=F32), attend(jfa, c, lists, scale=scale, out_dtype=F32)
+        c.Q = c.Q.double() * (scale * 8)  # (the reference's scale is 1 / 8)
+        ref = c.reference()
+        c.check(*dense, ref)
+        c.check(*listed, ref)
+
+
+def test_scales_out_of_range_are_refused(jfa):
+    for factor, scale in ((2.0 ** -60, 1e-20), (2.0 ** 60, 1e20), (1.0, 1e-45), (1.0, 3e38)):
+        c = QCase(*SETS, H=4, Hkv=2, D=64, page=16, factors=(factor, 1.0), seed=4)
+        for call in (lambda: c.run(jfa, scale=scale), lambda: attend(jfa, c, np.zeros((c.T, 2, 3), np.int32), scale=scale)):
+            with pytest.raises(jfa.JFAError) as e:
+                call()
+            assert e.value.status == jfa.JFA_ERR_INVALID_ARG
