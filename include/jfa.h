@@ -600,7 +600,8 @@ jfa_status jfa_cache_fwd(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_le
 jfa_status jfa_cache_summarize(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
                                const int32_t* page_table, int32_t max_pages, void* bounds, void* stream);
 
-/* Bytes of device workspace jfa_cache_select needs (0: bad arguments); it needs no initialisation. */
+/* Bytes of device workspace jfa_cache_select needs (0: bad arguments, or more than it takes); it needs no
+ * initialisation.  About 4 T Hkv max_pages. */
 size_t jfa_cache_select_workspace_size(jfa_cache cache, int64_t T, int32_t max_pages);
 
 /*
@@ -617,7 +618,7 @@ size_t jfa_cache_select_workspace_size(jfa_cache cache, int64_t T, int32_t max_p
  *   n_last >= 1, n_first >= 0, n_first + n_last <= n_blocks, n_blocks * page_size <= 2^30.
  *   workspace: at least jfa_cache_select_workspace_size bytes, 256-byte aligned; calls that may
  *   overlap on the GPU need one each.
- * Errors: INVALID_ARG, UNSUPPORTED (the cache; more than 128 grouped heads), PLAN_MISMATCH, CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (the cache; more than 128 grouped heads; max_pages over 65535 * 64), PLAN_MISMATCH, CUDA.
  */
 jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
                             const int32_t* kv_lens, const int32_t* page_table, int32_t max_pages, const void* bounds,

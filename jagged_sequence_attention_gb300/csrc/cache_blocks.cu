@@ -907,7 +907,8 @@ __global__ void __launch_bounds__(32 * WARPS * Choosers<WARPS>::kItems, WARPS <=
     }
 }
 
-int chunks_of(int32_t max_pages) { return std::max(1, (max_pages + kChunk - 1) / kChunk); }
+constexpr int kMaxChunks = 65535;  // of a grid's second dimension
+int chunks_of(int32_t max_pages) { return max_pages > 0 ? (max_pages - 1) / kChunk + 1 : 1; }
 
 void batch_params(CacheAppendParams& p, jfa_cache c, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,
                   const int32_t* page_table, int32_t max_pages) {
@@ -986,7 +987,8 @@ jfa_status jfa_cache_summarize(jfa_cache cache, int32_t B, int64_t T, const int3
 }
 
 size_t jfa_cache_select_workspace_size(jfa_cache cache, int64_t T, int32_t max_pages) {
-    if (!cache || T < 0 || T > (1 << 30) || max_pages < 0) return 0;
+    // (sizes that jfa_cache_select refuses have no workspace: it would not always fit 64 bits)
+    if (!cache || T < 0 || T > (1 << 30) || max_pages < 0 || T * cache->Hkv > INT32_MAX || chunks_of(max_pages) > kMaxChunks) return 0;
     return 256 + size_t(T) * size_t(cache->Hkv) * (size_t(max_pages) + size_t(chunks_of(max_pages))) * 4;
 }
 
@@ -999,7 +1001,7 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
     if (s == JFA_OK) s = check_blocks(cache);
     if (s != JFA_OK) return s;
     if (H < 1 || H > 65535 || H % cache->Hkv != 0 || T * H > INT32_MAX - 256 || max_q_len < 0) return JFA_ERR_INVALID_ARG;
-    if (H / cache->Hkv > 128) return JFA_ERR_UNSUPPORTED;
+    if (H / cache->Hkv > 128 || chunks_of(max_pages) > kMaxChunks) return JFA_ERR_UNSUPPORTED;
     if (n_first < 0 || n_last < 1 || n_blocks < 1 || n_first > n_blocks - n_last ||
         (int64_t(n_blocks) << cache->page_log2) > (1 << 30))
         return JFA_ERR_INVALID_ARG;
@@ -1007,7 +1009,6 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
         return JFA_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < jfa_cache_select_workspace_size(cache, T, max_pages))
         return JFA_ERR_INVALID_ARG;
-    if (chunks_of(max_pages) > 65535) return JFA_ERR_UNSUPPORTED;
     if (!on_device(cache)) return JFA_ERR_PLAN_MISMATCH;
     if (B == 0 || T == 0) return JFA_OK;
     batch_params(z.a, cache, B, T, q_offsets, kv_lens, page_table, max_pages);

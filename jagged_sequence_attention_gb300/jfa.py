@@ -650,7 +650,7 @@ def jfa_cache_select_workspace(cache: Cache, T: int, max_pages: int) -> torch.Te
     each."""
     n = jfa_cache_select_workspace_size(cache, T, max_pages)
     if n == 0:
-        _bad("jfa_cache_select_workspace", "T and max_pages must not be negative")
+        _bad("jfa_cache_select_workspace", "T and max_pages must not be negative, nor more than jfa_cache_select takes")
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 

@@ -178,6 +178,18 @@ def test_selection(jfa, fake, bits):
         assert call(Calls(fake, 32)) == call(Calls(fake, bits, page=8)) == (jfa.JFA_ERR_UNSUPPORTED, "")
 
 
+def test_select_workspace_of_sizes_past_its_limits(jfa, fake):
+    size = fake.jfa_cache_select_workspace_size
+    c = Calls(fake, 16, 8, 1)
+    for T, pages in ((0, 0), (1, 1), (1, 64), (1, 65), (2 ** 28 - 1, 65535 * 64)):
+        assert size(c.h, T, pages) == 256 + 4 * T * 8 * (pages + max(1, -(-pages // 64)))
+    # what the call refuses, past 64 bits or not
+    for T, pages in ((1, 65535 * 64 + 1), (1, 2 ** 31 - 1), (2 ** 28, 1), (2 ** 30, 2 ** 30), (-1, 1), (1, -1)):
+        assert size(c.h, T, pages) == 0
+    assert c.select(3, 2 ** 28, 1, 200, 5) == (jfa.JFA_ERR_INVALID_ARG, "")
+    assert c.select(3, 3, 1, 2 ** 31 - 1, 5) == (jfa.JFA_ERR_UNSUPPORTED, "")
+
+
 @pytest.mark.parametrize("bits,append,read", [(4, "append4", "read4"), (16, "append", "read16"), (32, "append", "read32")])
 def test_rows_and_bounds(jfa, fake, bits, append, read):
     c = Calls(fake, bits)
