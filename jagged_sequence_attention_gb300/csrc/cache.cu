@@ -6,6 +6,17 @@
 
 using namespace jfa;
 
+PFN_cuTensorMapEncodeTiled_v12000 jfa::encode_tiled() {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f
+                                                                                                             : nullptr);
+    }();
+    return enc;
+}
+
 namespace {
 
 // A tensor of `rank` dimensions (the first dense, strides of the others in elements), its boxes

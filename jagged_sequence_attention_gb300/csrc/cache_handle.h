@@ -42,16 +42,9 @@ namespace jfa {
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t elem(int dtype) { return dtype == JFA_F32 ? 4 : 2; }
 
-inline PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-    static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f
-                                                                                                             : nullptr);
-    }();
-    return enc;
-}
+// The driver's encoder of tensor maps, or nullptr.  (Not inline: a static variable of an inline function is one for all
+// libraries of a process, such as this one and a stand-in for its runtime.)
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled();
 
 // Whether the cache's device is the current one.
 inline bool on_device(jfa_cache c) {

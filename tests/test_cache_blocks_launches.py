@@ -2,6 +2,7 @@
 code against a stand-in for the CUDA runtime and the kernels (fake_cuda_blocks.cpp), without a GPU."""
 import ctypes
 import os
+import shutil
 import subprocess
 
 import numpy as np
@@ -32,12 +33,17 @@ def fake(jfa, tmp_path_factory):
                     "-Xlinker", "-Bsymbolic", "-Xlinker", "-z", "-Xlinker", "defs", "-I", _build.CSRC, "-I", _build.INCLUDE,
                     os.path.join(HERE, "fake_cuda_blocks.cpp"), os.path.join(HERE, "fake_cuda_blocks.cu"),
                     *(os.path.join(_build.BUILD, f"cache{x}.o") for x in ("", "_quant", "_blocks")), "-o", path], check=True)
+    return load(jfa, path)
+
+
+def load(jfa, path):
     lib = ctypes.CDLL(path)
     for name in CALLS:
         f = getattr(lib, name)
         f.argtypes, f.restype = getattr(jfa.lib(), name).argtypes, getattr(jfa.lib(), name).restype
     lib.fake_log.argtypes, lib.fake_log.restype = [ctypes.c_char_p], ctypes.c_char_p
     lib.fake_scale_log2.restype = ctypes.c_float
+    lib.path = path
     return lib
 
 
@@ -211,3 +217,16 @@ def test_arrays_of_another_device_are_refused(jfa, fake):
                                             1.0, None, ctypes.byref(h))
         assert r == (jfa.JFA_OK if at == 4 else jfa.JFA_ERR_INVALID_ARG) and (h.value is not None) == (at == 4)
         fake.jfa_cache_destroy(h)
+
+
+def test_libraries_of_a_process_share_nothing(jfa, fake, tmp_path):
+    """Tensor maps are encoded by what each library has found itself: the library that runs on a GPU must not use
+    what a stand-in in the same process has."""
+    assert Calls(fake, 4).fwd(3, 100, 0, 4096) == (jfa.JFA_OK, "chunk4:256 decode4:16:early merge")
+    other = load(jfa, shutil.copy(fake.path, tmp_path / "libother.so"))
+    c = Calls(other, 4)
+    assert c.fwd(3, 100, 0, 4096, fail="encode") == (jfa.JFA_ERR_CUDA, "")
+    # (a call that fails in the first is none of the second's)
+    fake.fake_log(b"encode")
+    assert c.fwd(3, 100, 0, 4096) == (jfa.JFA_OK, "chunk4:256 decode4:16:early merge")
+    fake.fake_log(b"")
