@@ -175,7 +175,8 @@ __device__ __forceinline__ uint32_t quantise(const Half& g, const Raw& raw, floa
         }
         return to_e2m1(y);
     }
-    // (quotients of at most 8 are off by less than 2^-19 besides)
+    // Quotients are below 9 (the smallest scale stands for up to 1.5 times itself, the others for less), and off
+    // by less than 2^-19 besides: the step's and its reciprocal's roundings, 2^-24 of them each, and one of 2^-21.
     const float e = fmaf(slack, inv * 1.0001f, 0x1p-19f);
     float above[8];
 #pragma unroll

@@ -1,6 +1,6 @@
 """The 4-bit cache and attention over selected blocks on a GPU, at the ends of what their calls take:
 sums next to fp32's largest number, positions past 2^30, lists out of order, scales that only
-their product with the cache's factor brings into range."""
+their product with the cache's factor brings into range, rows at the smallest of the cache's scales."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +8,7 @@ import torch
 from cache_cases import Case, np64
 from quant_cases import BF, F32, QCase
 from test_gpu_cache_blocks import SETS, attend, bounds_for, check, choose, expected_blocks, make, random_lists, reference, tokens
+from test_gpu_cache_quantized import Batch, check_append
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +183,27 @@ def test_scales_out_of_range_are_refused(jfa):
             with pytest.raises(jfa.JFAError) as e:
                 call()
             assert e.value.status == jfa.JFA_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ the smallest scale
+
+@pytest.mark.parametrize("factors", [(1.0, 1.0), (0.3, 1.7), (2.0 ** -20, 0.7)])
+@pytest.mark.parametrize("R", [0, 32, 128])
+def test_append_at_the_smallest_scale(jfa, factors, R):
+    """Groups whose largest magnitude is 0.4 to 1.6 times 6 steps of the smallest scale, 2^-9: it rounds to that scale, to 0
+    or to the next one, and quotients reach 9."""
+    factors = tuple(float(np.float32(f)) for f in factors)
+    b = Batch([300, 1], [300, 7], D=128, R=R, factors=factors, seed=R)
+    g = torch.Generator(device="cuda").manual_seed(R)
+    rows = []
+    for f in factors:
+        x = torch.rand(b.c.T, 2, 8, 16, generator=g, device="cuda") * 2 - 1
+        x[..., 3] = 1.0
+        size = torch.rand(b.c.T, 2, 8, 1, generator=g, device="cuda") * 1.2 + 0.4
+        size[::2] = size[::2].clamp(1.3, 1.5)
+        rows.append((x * size * (6 * f * 2.0 ** -9)).flatten(-2).to(BF))
+    b.K, b.V = rows
+    if R:
+        b.rot[5::7, :R // 2], b.rot[5::7, R // 2:] = 1.0, 0.0  # (as they are)
+    check_append(jfa, b)
+    assert bool((b.vs == 1).any() and (b.vs == 0).any() and (b.vs == 2).any())
