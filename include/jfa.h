@@ -481,7 +481,9 @@ jfa_status jfa_cache_create(int32_t dtype, int32_t Hkv, int32_t D, int32_t page_
  *   in exact arithmetic.
  * Attention: scale * code is exact in the products' types.  jfa_cache_fwd's text on bf16 caches
  *   holds, with each weight of the softmax rounded to fp16 for its product: off by 2^-11 of itself, or
- *   by 2^-31 of the row's largest where that is more.  scale * k_factor must lie in [1e-37, 1e37].
+ *   by 2^-31 of the row's largest where that is more, and queries taken to fp16 by a power of two for
+ *   each row: exact but for elements below 2^-28 of its largest, which lose 2^-39 of that at
+ *   most.  scale * k_factor must lie in [1e-37, 1e37].
  * Errors: those of jfa_cache_create.
  */
 jfa_status jfa_cache_create_quantized(int32_t Hkv, int32_t D, int32_t page_size, int64_t n_pages, void* K, void* V,
@@ -618,6 +620,11 @@ size_t jfa_cache_select_workspace_size(jfa_cache cache, int64_t T, int32_t max_p
  *   n_last >= 1, n_first >= 0, n_first + n_last <= n_blocks, n_blocks * page_size <= 2^30.
  *   workspace: at least jfa_cache_select_workspace_size bytes, 256-byte aligned; calls that may
  *   overlap on the GPU need one each.
+ *   The kernels are chosen, and the workspace sized, by max_pages, whatever the histories' lengths: a page
+ *   table of no more columns than they need is fastest (64 tokens over up to 499 pages, 8 key heads of 128:
+ *   25 us with 499 columns, 29 with 1024, 51 with 2048, 100 with 8192; four prompts of 1,312
+ *   tokens over up to 313 pages: 64 us with 313, 105 with 1024, 448 with 2048 and more).
+ *   (Lists for more than 16 grouped heads can be had here; jfa_cache_fwd_blocks does not take them.)
  * Errors: INVALID_ARG, UNSUPPORTED (the cache; more than 128 grouped heads; max_pages over 65535 * 64), PLAN_MISMATCH, CUDA.
  */
 jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q_len, const int32_t* q_offsets,
@@ -629,9 +636,15 @@ jfa_status jfa_cache_select(jfa_cache cache, int32_t B, int64_t T, int32_t max_q
  * jfa_cache_fwd (causal) with the keys of row i of key head hk limited to the blocks listed for it in
  * blocks [T, Hkv, n_blocks]: indices that ascend strictly, then -1.  Listed positions after i' are
  * not seen, so a list may name the token's own block and later ones.  An entry that does not ascend, or
- * follows a -1, is left out where it is met, and sets JFA_ERR_DEVICE_BOUNDS.  At most 16 grouped
+ * follows a -1, is left out where it is met, and sets JFA_ERR_DEVICE_BOUNDS (ascends: over all entries before
+ * it, left out or not; as many entries are looked at as the token has blocks).  At most 16 grouped
  * heads.  Workspace (jfa_cache_workspace_size), outputs, bias, rounding and empty rows are as in
  * jfa_cache_fwd; the result is the same bit for bit on every run.
+ *   Every token reads its blocks for itself, so this is a call for single tokens and drafts.  For prompts
+ *   jfa_cache_fwd over everything is faster until histories are long.  With 2,048 listed keys, 32 query
+ *   and 8 key heads of 128: one sequence over 20k keys, from about 64 tokens on (4 bits: 256); 16
+ *   over 12k, from 8 each on (4 bits: past 16); four prompts of 1,312 tokens over 5k-20k 882 us against
+ *   296 (4 bits: 601, 331).  One sequence over 100k: this call, up to 512 tokens at least.
  * Errors: those of jfa_cache_fwd; UNSUPPORTED also for the cache and for more than 16 grouped heads.
  */
 jfa_status jfa_cache_fwd_blocks(jfa_cache cache, int32_t B, int64_t T, const int32_t* q_offsets, const int32_t* kv_lens,

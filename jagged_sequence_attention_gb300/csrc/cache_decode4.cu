@@ -26,7 +26,7 @@
 // the parts of an item cut between CTAs are added by a kernel of their own (cache_join.cu).
 // Measured, one token each of 32 query and 8 key heads of 128: 64 sequences of 200-16k keys (300 MB)
 // 66 us, 4.5 TB/s, 0.68 of the copy rate; one history of 131k keys (151 MB) 37.6 us, 0.60; 64 lists of 64
-// blocks of 32 keys (104 MB) 35.2 us, 0.44; one sequence of 1k keys 9.1 us.  The same stream with no
+// blocks of 32 keys (104 MB) 35.4 us, 0.44; one sequence of 1k keys 9.1 us.  The same stream with no
 // arithmetic takes 52 us of the 66: the rest is instructions, 620 a warp for 32 keys (128 conversions and as many
 // multiplications by scales among them), which fill half the issue slots; the warps wait for their own
 // chains and, a fifth of the time, for code.  More warps do not help: four CTAs an SM at 96
